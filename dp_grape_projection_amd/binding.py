@@ -35,6 +35,9 @@ EXPORTED = (
     "dpg_clip_workspace_size", "dpg_clip_sum_noise",
     "dpg_step_workspace_size", "dpg_private_step", "dpg_private_step_static",
     "dpg_static_scratch_bytes", "dpg_rc_norms_workspace_size", "dpg_rc_norms",
+    "dpg_embed", "dpg_embed_workspace_size", "dpg_embed_norms", "dpg_embed_grad",
+    "dpg_vocab_loss_workspace_size", "dpg_vocab_loss", "dpg_vocab_loss_grad",
+    "dpg_distill_loss_workspace_size", "dpg_distill_loss", "dpg_distill_loss_grad",
     "dpg_status_string", "dpg_last_error", "dpg_version",
     "dpg_timing_enable", "dpg_timing_read", "dpg_kernel_name",
 )
@@ -121,6 +124,21 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.dpg_clip_sum_noise.argtypes = [
         ctypes.POINTER(LayerHat), i32, i64, i32, f64, f64, u64, u64, vp, vp, vp,
         sz, vp]
+    psz = ctypes.POINTER(sz)
+    lib.dpg_embed.argtypes = [vp, i64, vp, i64, i64, i32, f64, i32, vp, vp]
+    lib.dpg_embed_workspace_size.argtypes = [i64, i64, i64, i64, psz]
+    lib.dpg_embed_norms.argtypes = [vp, vp, i64, i64, i64, i64, i32, f64, vp, vp, sz, vp]
+    lib.dpg_embed_grad.argtypes = [vp, vp, i64, i64, i64, i64, i32, f64, vp, i32, i32, vp,
+                                   vp, sz, vp]
+    lib.dpg_vocab_loss_workspace_size.argtypes = [i64, i64, i64, i32, i32, psz]
+    lib.dpg_vocab_loss.argtypes = [vp, vp, vp, i64, i64, i64, i32, f64, vp, vp, vp, sz, vp]
+    lib.dpg_vocab_loss_grad.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i32, f64, vp, vp,
+                                        vp, sz, vp]
+    lib.dpg_distill_loss_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32, psz]
+    lib.dpg_distill_loss.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, i32, f64, f64, vp,
+                                     vp, vp, sz, vp]
+    lib.dpg_distill_loss_grad.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32,
+                                          f64, f64, vp, vp, vp, sz, vp]
     for name in EXPORTED:
         getattr(lib, name).restype = ctypes.c_int
     lib.dpg_static_scratch_bytes.restype = ctypes.c_size_t
@@ -532,6 +550,267 @@ def dpg_philox_normals(seed: int, layer_id: int, step_word: int, tag: int,
                                        int(tag), int(start), int(n), _ptr(z),
                                        _ptr(w), _stream_handle(stream)))
     return (z, w) if words else z
+
+
+def _ids(t, name: str, shape=None):
+    _require(t, name, torch.int64, shape)
+    return t
+
+
+def _same_device(ref: torch.Tensor, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
+
+
+@_on_stream
+def dpg_embed(ids: torch.Tensor, E: torch.Tensor, scale: float = 1.0,
+              dtype: Optional[torch.dtype] = None, Y: Optional[torch.Tensor] = None,
+              stream=None):
+    """Token lookup with scaling (libdpg): Y = scale * E[ids], zero where an
+    id lies outside [0, V).
+
+    ids: int64 of any shape; E: [V, d] fp32 or bf16; dtype (default E's) is
+    Y's: an fp32 table is looked up in fp32 or bf16, a bf16 table in bf16.
+    Returns Y of shape ids.shape + (d,)."""
+    lib = load_library()
+    _require(E, "E")
+    if E.dim() != 2:
+        raise ValueError("E must be [V, d]")
+    V, d = int(E.shape[0]), int(E.shape[1])
+    _ids(ids, "ids")
+    dtype = E.dtype if dtype is None else dtype
+    table = _dtype_code(E.dtype)
+    code = _dtype_code(dtype)
+    if Y is None:
+        Y = torch.empty((*ids.shape, d), dtype=dtype, device=E.device)
+    _require(Y, "Y", dtype, (*ids.shape, d))
+    _same_device(E, ids=ids, Y=Y)
+    if ids.numel() == 0:
+        return Y
+    _check(lib, lib.dpg_embed(_ptr(ids), ids.numel(), _ptr(E), V, d, table, float(scale),
+                              code, _ptr(Y), _stream_handle(stream)))
+    return Y
+
+
+def _embed_args(ids, dY, V):
+    """Checked (B, T, d) of a [B, T] batch of ids and its [B, T, d] gradient."""
+    _ids(ids, "ids")
+    _require(dY, "dY")
+    if ids.dim() != 2 or dY.dim() != 3 or tuple(dY.shape[:2]) != tuple(ids.shape):
+        raise ValueError("ids must be [B, T] and dY [B, T, d]")
+    _same_device(dY, ids=ids)
+    return int(ids.shape[0]), int(ids.shape[1]), int(dY.shape[2])
+
+
+def _embed_workspace(lib, B, T, V, d, device, workspace):
+    need = ctypes.c_size_t(0)
+    _check(lib, lib.dpg_embed_workspace_size(B, T, int(V), d, ctypes.byref(need)))
+    return _workspace(need.value, device, workspace)
+
+
+@_on_stream
+def dpg_embed_norms(ids: torch.Tensor, dY: torch.Tensor, V: int, norm_sq: torch.Tensor,
+                    scale: float = 1.0, workspace: Optional[torch.Tensor] = None,
+                    stream=None):
+    """Each sample's squared gradient norm of the table, added to norm_sq
+    (libdpg): norm_sq[i] += sum_v ||scale sum_{t: ids[i, t] = v} dY[i, t]||^2.
+    ids: [B, T] int64, dY: [B, T, d] (bf16 or fp32), norm_sq: [B] fp32, the
+    buffer dpg_project_layer adds to. Returns norm_sq."""
+    lib = load_library()
+    B, T, d = _embed_args(ids, dY, V)
+    _require(norm_sq, "norm_sq", torch.float32, (B,))
+    _same_device(dY, norm_sq=norm_sq)
+    code = _dtype_code(dY.dtype)
+    ws, ws_bytes = _embed_workspace(lib, B, T, V, d, dY.device, workspace)
+    _check(lib, lib.dpg_embed_norms(_ptr(ids), _ptr(dY), B, T, int(V), d, code, float(scale),
+                                    _ptr(norm_sq), ws.data_ptr(), ws_bytes,
+                                    _stream_handle(stream)))
+    return norm_sq
+
+
+@_on_stream
+def dpg_embed_grad(ids: torch.Tensor, dY: torch.Tensor, V: int, scale: float = 1.0,
+                   sample_scales: Optional[torch.Tensor] = None,
+                   table_dtype: Optional[torch.dtype] = None,
+                   dE: Optional[torch.Tensor] = None, accumulate: bool = False,
+                   workspace: Optional[torch.Tensor] = None, stream=None):
+    """The table's gradient (libdpg): dE[v] = scale sum_i s_i
+    sum_{t: ids[i, t] = v} dY[i, t], s_i = sample_scales[i] ([B] fp32 clip
+    factors; 1 when None). table_dtype (default dE's, else fp32) is dE's type:
+    fp32, or bf16 for a bf16 dY. With accumulate the rows of tokens that occur
+    are added to (dE must be given), otherwise every row is written."""
+    lib = load_library()
+    B, T, d = _embed_args(ids, dY, V)
+    if dE is None:
+        if accumulate:
+            raise ValueError("accumulate needs dE")
+        dE = torch.empty((int(V), d), dtype=table_dtype or torch.float32, device=dY.device)
+    _require(dE, "dE", table_dtype, (int(V), d))
+    if sample_scales is not None:
+        _require(sample_scales, "sample_scales", torch.float32, (B,))
+    _same_device(dY, dE=dE, sample_scales=sample_scales)
+    code, table = _dtype_code(dY.dtype), _dtype_code(dE.dtype)
+    ws, ws_bytes = _embed_workspace(lib, B, T, V, d, dY.device, workspace)
+    _check(lib, lib.dpg_embed_grad(_ptr(ids), _ptr(dY), B, T, int(V), d, code, float(scale),
+                                   _ptr(sample_scales), table, 1 if accumulate else 0,
+                                   _ptr(dE), ws.data_ptr(), ws_bytes,
+                                   _stream_handle(stream)))
+    return dE
+
+
+def _loss_args(X, E, ids, name, k_shape=()):
+    """Checked (N, d, V, dtype code) of X [..., d], E [V, d] and ids [..., *k_shape]."""
+    _require(X, "X")
+    _require(E, "E", X.dtype)
+    if X.dim() < 1 or E.dim() != 2 or int(X.shape[-1]) != int(E.shape[1]):
+        raise ValueError("X must be [..., d] and E [V, d]")
+    _ids(ids, name, (*X.shape[:-1], *k_shape))
+    _same_device(X, E=E, **{name: ids})
+    d = int(X.shape[-1])
+    return X.numel() // max(d, 1), d, int(E.shape[0]), _dtype_code(X.dtype)
+
+
+def _loss_outputs(X, loss, lse):
+    rows = tuple(X.shape[:-1])
+    loss = torch.empty(rows, dtype=torch.float32, device=X.device) if loss is None else loss
+    lse = torch.empty(rows, dtype=torch.float32, device=X.device) if lse is None else lse
+    _require(loss, "loss", torch.float32, rows)
+    _require(lse, "lse", torch.float32, rows)
+    _same_device(X, loss=loss, lse=lse)
+    return loss, lse
+
+
+def _loss_grads(X, E, lse, dloss, need_dX, need_dE, dX, dE):
+    rows = tuple(X.shape[:-1])
+    _require(lse, "lse", torch.float32, rows)
+    _require(dloss, "dloss", torch.float32, rows)
+    if need_dX and dX is None:
+        dX = torch.empty_like(X)
+    if need_dE and dE is None:
+        dE = torch.empty_like(E)
+    if not (need_dX or need_dE):
+        raise ValueError("need_dX or need_dE must be set")
+    dX, dE = (dX if need_dX else None), (dE if need_dE else None)
+    if dX is not None:
+        _require(dX, "dX", X.dtype, X.shape)
+    if dE is not None:
+        _require(dE, "dE", E.dtype, E.shape)
+    _same_device(X, lse=lse, dloss=dloss, dX=dX, dE=dE)
+    return dX, dE
+
+
+def _vocab_workspace(lib, N, d, V, k, code, grad, device, workspace):
+    need = ctypes.c_size_t(0)
+    if k is None:
+        st = lib.dpg_vocab_loss_workspace_size(N, d, V, code, grad, ctypes.byref(need))
+    else:
+        st = lib.dpg_distill_loss_workspace_size(N, d, V, k, code, grad, ctypes.byref(need))
+    _check(lib, st)
+    return _workspace(need.value, device, workspace)
+
+
+@_on_stream
+def dpg_vocab_loss(X: torch.Tensor, E: torch.Tensor, targets: torch.Tensor,
+                   scale: float = 1.0, loss: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None):
+    """Softmax cross entropy against a [V, d] table without an array of
+    logits (libdpg): z = scale X E^T, lse = ln sum_v exp z_v,
+    loss = lse - z_target; both 0 where the target lies outside [0, V).
+    X: [..., d] and E in the same type (bf16 or fp32), targets: [...] int64.
+    Returns (loss, lse), fp32 of X's leading shape."""
+    lib = load_library()
+    N, d, V, code = _loss_args(X, E, targets, "targets")
+    loss, lse = _loss_outputs(X, loss, lse)
+    if N == 0:
+        return loss, lse
+    ws, ws_bytes = _vocab_workspace(lib, N, d, V, None, code, 0, X.device, workspace)
+    _check(lib, lib.dpg_vocab_loss(_ptr(X), _ptr(E), _ptr(targets), N, d, V, code,
+                                   float(scale), _ptr(loss), _ptr(lse), ws.data_ptr(),
+                                   ws_bytes, _stream_handle(stream)))
+    return loss, lse
+
+
+@_on_stream
+def dpg_vocab_loss_grad(X: torch.Tensor, E: torch.Tensor, targets: torch.Tensor,
+                        lse: torch.Tensor, dloss: torch.Tensor, scale: float = 1.0,
+                        need_dX: bool = True, need_dE: bool = True,
+                        dX: Optional[torch.Tensor] = None,
+                        dE: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of sum_n dloss_n loss_n of dpg_vocab_loss (libdpg), with the
+    lse it returned. dloss: fp32 of X's leading shape. Returns (dX, dE) in X's
+    type; None for the one not needed."""
+    lib = load_library()
+    N, d, V, code = _loss_args(X, E, targets, "targets")
+    dX, dE = _loss_grads(X, E, lse, dloss, need_dX, need_dE, dX, dE)
+    if N == 0:
+        return dX, None if dE is None else dE.zero_()
+    ws, ws_bytes = _vocab_workspace(lib, N, d, V, None, code, 1, X.device, workspace)
+    _check(lib, lib.dpg_vocab_loss_grad(_ptr(X), _ptr(E), _ptr(targets), _ptr(lse),
+                                        _ptr(dloss), N, d, V, code, float(scale), _ptr(dX),
+                                        _ptr(dE), ws.data_ptr(), ws_bytes,
+                                        _stream_handle(stream)))
+    return dX, dE
+
+
+def _top_args(X, E, top_ids, top_logits):
+    if not isinstance(top_ids, torch.Tensor) or top_ids.dim() < 1:
+        raise TypeError("top_ids must be a [..., k] torch.Tensor")
+    k = int(top_ids.shape[-1])
+    N, d, V, code = _loss_args(X, E, top_ids, "top_ids", (k,))
+    _require(top_logits, "top_logits", torch.float32, top_ids.shape)
+    _same_device(X, top_logits=top_logits)
+    return N, d, V, k, code
+
+
+@_on_stream
+def dpg_distill_loss(X: torch.Tensor, E: torch.Tensor, top_ids: torch.Tensor,
+                     top_logits: torch.Tensor, temperature: float = 1.0,
+                     scale: float = 1.0, loss: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Distillation from a teacher's top k logits per row (libdpg):
+    loss = tau^2 sum_j q_j (ln q_j - ln p_id(j)), q = softmax of
+    top_logits / tau over the entries whose id lies in [0, V), p = softmax of
+    scale X E^T / tau over the vocabulary. Rows without any weight get 0.
+    top_ids: [..., k] int64, top_logits: [..., k] fp32.
+    Returns (loss, lse), lse = ln sum_v exp(z_v / tau)."""
+    lib = load_library()
+    N, d, V, k, code = _top_args(X, E, top_ids, top_logits)
+    loss, lse = _loss_outputs(X, loss, lse)
+    if N == 0:
+        return loss, lse
+    ws, ws_bytes = _vocab_workspace(lib, N, d, V, k, code, 0, X.device, workspace)
+    _check(lib, lib.dpg_distill_loss(_ptr(X), _ptr(E), _ptr(top_ids), _ptr(top_logits), N, d,
+                                     V, k, code, float(scale), float(temperature),
+                                     _ptr(loss), _ptr(lse), ws.data_ptr(), ws_bytes,
+                                     _stream_handle(stream)))
+    return loss, lse
+
+
+@_on_stream
+def dpg_distill_loss_grad(X: torch.Tensor, E: torch.Tensor, top_ids: torch.Tensor,
+                          top_logits: torch.Tensor, lse: torch.Tensor, dloss: torch.Tensor,
+                          temperature: float = 1.0, scale: float = 1.0,
+                          need_dX: bool = True, need_dE: bool = True,
+                          dX: Optional[torch.Tensor] = None,
+                          dE: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of sum_n dloss_n loss_n of dpg_distill_loss (libdpg), with
+    the lse it returned. Returns (dX, dE); None for the one not needed."""
+    lib = load_library()
+    N, d, V, k, code = _top_args(X, E, top_ids, top_logits)
+    dX, dE = _loss_grads(X, E, lse, dloss, need_dX, need_dE, dX, dE)
+    if N == 0:
+        return dX, None if dE is None else dE.zero_()
+    ws, ws_bytes = _vocab_workspace(lib, N, d, V, k, code, 1, X.device, workspace)
+    _check(lib, lib.dpg_distill_loss_grad(
+        _ptr(X), _ptr(E), _ptr(top_ids), _ptr(top_logits), _ptr(lse), _ptr(dloss), N, d, V, k,
+        code, float(scale), float(temperature), _ptr(dX), _ptr(dE), ws.data_ptr(), ws_bytes,
+        _stream_handle(stream)))
+    return dX, dE
 
 
 class PreparedStep:

@@ -270,6 +270,14 @@ struct Acc {
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[a][b][i] *= s;
   }
+  __device__ __forceinline__ void add(const Acc& o) {
+#pragma unroll
+    for (int a = 0; a < MB; ++a)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[a][b][i] += o.v[a][b][i];
+  }
   __device__ __forceinline__ float sum_sq() const {
     float s = 0.0f;
 #pragma unroll
@@ -658,6 +666,97 @@ __device__ __forceinline__ void run_steps(LA& la, LB& lb, T* smem,
 __device__ __forceinline__ int xcd_logical_block() {
   const int per = gridDim.x >> 3;
   return (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+}
+
+// ------------------------------------------------------- wave and LDS --
+
+// Caller pointers are only element aligned; vector accesses to them are
+// taken when the pointer allows them (the test is uniform per layer).
+__device__ __forceinline__ bool is_aligned(const void* p, unsigned bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
+// Sum over the 64 lanes of a wave (butterfly, deterministic).
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) x += __shfl_xor(x, off, 64);
+  return x;
+}
+
+// ------------------------------------------- direct copies, LDS reads --
+
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+// vmcnt(n) (n < 64) with the other counters left alone.
+__device__ __forceinline__ void wait_vm(int n) {
+  switch (n) {  // the encoding must be an immediate
+    case 0: __builtin_amdgcn_s_waitcnt(0x0F70); break;
+    case 4: __builtin_amdgcn_s_waitcnt(0x0F74); break;
+    case 8: __builtin_amdgcn_s_waitcnt(0x0F78); break;
+    case 12: __builtin_amdgcn_s_waitcnt(0x0F7C); break;
+    default: __builtin_amdgcn_s_waitcnt(0x0F70); break;  // (stricter: wait for all)
+  }
+}
+// lgkmcnt(0) with the other counters left alone.
+__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// One direct global-to-LDS copy of 16 bytes per lane through a buffer
+// resource: lane offset `voff` (kept in a register across a loop) plus the
+// block-uniform `soff`; the 1 KiB a wave copies lands at `lds` (uniform).
+__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t voff,
+                                            uint32_t soff, char* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)lds, 16, voff,
+                                           __builtin_amdgcn_readfirstlane(soff), 0, 0);
+}
+
+// 16-byte LDS read of a matrix-core fragment through a restrict-qualified
+// pointer: the alias-scope information lets the compiler keep the read clear
+// of the direct global-to-LDS copies in flight (without it, it may wait for
+// all of them first; the kernels order copies and reads themselves).
+__device__ __forceinline__ bf16x8 lds_read_b128(const char* __restrict__ p) {
+  return *reinterpret_cast<const bf16x8*>(p);
+}
+__device__ __forceinline__ float lds_read_f32(const float* __restrict__ p) { return *p; }
+
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
+
+// Slot of 16-byte chunk c in row k of a k-major LDS tile with 512-byte rows.
+__device__ __forceinline__ int kmajor_slot(int k, int c) { return c ^ (4 * (k & 3)); }
+
+// Transposing LDS read of four 16-bit values. The restrict-qualified pointer
+// gives the read alias-scope information; without it the compiler makes the
+// read wait for every direct global-to-LDS copy in flight (the kernels order
+// those copies against their reads with explicit waits and barriers).
+__device__ __forceinline__ v4i16 lds_read_tr(const char* __restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)p);
+}
+
+// Matrix-core operand of a 32x32x16 product from a k-major LDS tile (rows of
+// ROW bytes, 256 or 512, kmajor_slot swizzle): lane l receives rows k0 + 8
+// (l / 32) .. + 7 of column c0 + l % 32. In each group of 16 lanes, lane q
+// addresses four consecutive columns of row k0 + 8 (l / 32) + 4 h + q / 4;
+// the transposing read hands lane j element j % 4 of the values lanes j / 4,
+// 4 + j / 4, ... addressed, which is four consecutive rows of one column.
+// The 32 lanes of a half-wave read four rows of 64 bytes; the swizzle puts
+// them in 16 different 16-byte bank groups for either row length.
+template <int ROW = 512>
+__device__ __forceinline__ bf16x8 frag_kmajor(const char* tile, int k0, int c0, int lane) {
+  static_assert(ROW == 256 || ROW == 512, "rows of 16 or 32 chunks");
+  const int q16 = lane & 15, nh = (lane >> 4) & 1, kh = lane >> 5;
+  const int n = c0 + 16 * nh + 4 * (q16 & 3);
+  v4i16 h[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = k0 + 8 * kh + 4 * i + (q16 >> 2);
+    h[i] = lds_read_tr(tile + t * ROW + kmajor_slot(t, n >> 3) * 16 + (n & 7) * 2);
+  }
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 }  // namespace dpg

@@ -321,6 +321,119 @@ int dpg_rc_norms(const dpg_layer_grad* layers, int32_t n_layers, int64_t B,
                  uint64_t seed, uint64_t step, float* norms, float* scales,
                  void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Token operators: the two ends of a language model whose linear layers
+ * take the private step. A table E has shape [V][d] (row-major, one row per
+ * token of the vocabulary); the same table may serve the lookup and the
+ * losses. Token ids are int64. An id outside [0, V) marks a position that
+ * takes no part (padding, a prompt without loss): nothing is read through it.
+ */
+
+/*
+ * dpg_embed: Y[i] = scale * E[ids[i]] for i in [0, n); a row whose id lies
+ * outside [0, V) is zero. table_dtype is E's type, dtype Y's: fp32 tables
+ * are looked up in fp32 or bf16, bf16 tables in bf16 (one rounding).
+ * Limits: n and V in [1, 2^23], d in [1, 2^20]. No workspace.
+ */
+int dpg_embed(const int64_t* ids, int64_t n, const void* E, int64_t V, int64_t d,
+              int32_t table_dtype, double scale, int32_t dtype, void* Y, void* stream);
+
+/* dpg_embed_workspace_size: bytes of device workspace (written to *bytes)
+ * that dpg_embed_norms and dpg_embed_grad need for B samples of T tokens. */
+int dpg_embed_workspace_size(int64_t B, int64_t T, int64_t V, int64_t d, size_t* bytes);
+
+/*
+ * dpg_embed_norms: each sample's squared gradient norm of the table,
+ *     norm_sq[i] += sum_v || scale * sum_{t: ids[i][t] = v} dY[i][t] ||^2
+ * for the clip across all of a model's trained tensors: it adds to the
+ * buffer that dpg_project_layer adds to (same ordering rule).
+ *   ids       device [B][T] int64
+ *   dY        device [B][T][d], dtype: gradient of the lookup's output
+ *   norm_sq   device in/out [B] fp32
+ *   workspace device scratch of dpg_embed_workspace_size bytes, 256-byte aligned
+ */
+int dpg_embed_norms(const int64_t* ids, const void* dY, int64_t B, int64_t T, int64_t V,
+                    int64_t d, int32_t dtype, double scale, float* norm_sq, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
+ * dpg_embed_grad: the table's gradient,
+ *     dE[v] = scale * sum_i s_i sum_{t: ids[i][t] = v} dY[i][t]   [V][d]
+ * with s_i = sample_scales[i] (clip factors, device [B] fp32), or 1 when
+ * sample_scales is NULL. Every row is written (zero for tokens that do not
+ * occur); with accumulate != 0 the sum is added to the rows that occur and
+ * the others are left alone. table_dtype is dE's type (a bf16 dE takes a
+ * bf16 dY). Sums run in fp32 over each token's positions in ascending order
+ * and are rounded once: results do not vary from run to run.
+ */
+int dpg_embed_grad(const int64_t* ids, const void* dY, int64_t B, int64_t T, int64_t V,
+                   int64_t d, int32_t dtype, double scale, const float* sample_scales,
+                   int32_t table_dtype, int32_t accumulate, void* dE, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
+ * dpg_vocab_loss: softmax cross entropy of every row against the table,
+ *     z_nv = scale * x_n . e_v;  lse_n = ln sum_v exp(z_nv)
+ *     loss_n = lse_n - z_n,target(n)
+ * without an array of logits: they are computed in tiles, of which each
+ * row's maximum and sum are kept. Rows whose target lies outside [0, V) get
+ * loss = lse = 0, whatever X holds there.
+ *   X          device [N][d], dtype    E      device [V][d], dtype
+ *   targets    device [N] int64        loss, lse   device out [N] fp32
+ *   workspace  dpg_vocab_loss_workspace_size(..., grad = 0) bytes, 256-byte
+ *              aligned
+ * Limits: N and V in [1, 2^22], d in [1, 2^16].
+ */
+int dpg_vocab_loss_workspace_size(int64_t N, int64_t d, int64_t V, int32_t dtype,
+                                  int32_t grad, size_t* bytes);
+int dpg_vocab_loss(const void* X, const void* E, const int64_t* targets, int64_t N, int64_t d,
+                   int64_t V, int32_t dtype, double scale, float* loss, float* lse,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dpg_vocab_loss_grad: gradients of sum_n dloss_n loss_n,
+ *     D_nv = scale * dloss_n (exp(z_nv - lse_n) - [v = target(n)])
+ *     dX = D E  [N][d],   dE = D^T X  [V][d]        (both in dtype)
+ * with lse as dpg_vocab_loss wrote it. The logits are recomputed in pieces
+ * of the vocabulary, and one piece of D is kept at a time (at most 512 MiB,
+ * but at least 256 columns, in dtype: bf16 D is D rounded once, the products
+ * accumulate in fp32). dX or dE may be NULL (not computed); rows without a
+ * target get a zero dX. dloss_n may carry a sample's mean and clip factor:
+ * the gradient of each row's loss involves no other row of X.
+ *   workspace  dpg_vocab_loss_workspace_size(..., grad = 1) bytes
+ */
+int dpg_vocab_loss_grad(const void* X, const void* E, const int64_t* targets, const float* lse,
+                        const float* dloss, int64_t N, int64_t d, int64_t V, int32_t dtype,
+                        double scale, void* dX, void* dE, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * dpg_distill_loss / dpg_distill_loss_grad: distillation from a teacher's top
+ * k logits per row at a temperature tau,
+ *     q_nj = softmax over j of top_logits[n][j] / tau   (entries whose
+ *            top_ids[n][j] lies in [0, V); the others have no weight)
+ *     p_n  = softmax over the vocabulary of z_n / tau, z_nv = scale * x_n . e_v
+ *     lse_n = ln sum_v exp(z_nv / tau)
+ *     loss_n = tau^2 sum_j q_nj (ln q_nj - ln p_n,id(j))
+ *     D_nv = scale * tau * dloss_n (p_nv - sum_{j: id(j) = v} q_nj)
+ *     dX = D E,   dE = D^T X
+ * A row without any weight (no id in range, or every such logit -inf) gets
+ * loss = lse = 0 and no gradient. Arguments and limits otherwise as above;
+ * top_ids device [N][k] int64, top_logits device [N][k] fp32, 1 <= k <= 1024,
+ * temperature positive and finite.
+ */
+int dpg_distill_loss_workspace_size(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype,
+                                    int32_t grad, size_t* bytes);
+int dpg_distill_loss(const void* X, const void* E, const int64_t* top_ids,
+                     const float* top_logits, int64_t N, int64_t d, int64_t V, int32_t k,
+                     int32_t dtype, double scale, double temperature, float* loss, float* lse,
+                     void* workspace, size_t workspace_bytes, void* stream);
+int dpg_distill_loss_grad(const void* X, const void* E, const int64_t* top_ids,
+                          const float* top_logits, const float* lse, const float* dloss,
+                          int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype,
+                          double scale, double temperature, void* dX, void* dE,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * dpg_philox_normals: the random stream both calls draw from, exposed so it
  * can be checked on its own. For e in [start, start + n):
