@@ -187,6 +187,9 @@ __device__ __forceinline__ void normals_at(const StreamKey& key,
 template <typename T> struct Vec16;
 template <> struct Vec16<bf16> { typedef bf16x8 type; static constexpr int N = 8; };
 template <> struct Vec16<float> { typedef f32x4 type; static constexpr int N = 4; };
+template <typename T> struct Vec4;
+template <> struct Vec4<bf16> { typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 type; };
+template <> struct Vec4<float> { typedef f32x4 type; };
 
 __device__ __forceinline__ float to_float(bf16 x) { return static_cast<float>(x); }
 __device__ __forceinline__ float to_float(float x) { return x; }
@@ -269,14 +272,6 @@ struct Acc {
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[a][b][i] *= s;
-  }
-  __device__ __forceinline__ void add(const Acc& o) {
-#pragma unroll
-    for (int a = 0; a < MB; ++a)
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[a][b][i] += o.v[a][b][i];
   }
   __device__ __forceinline__ float sum_sq() const {
     float s = 0.0f;

@@ -28,10 +28,6 @@ namespace dpg {
 template <typename T> struct StepK { static constexpr int v = sizeof(T) == 2 ? kStepBf16 : kStepF32; };
 template <typename T> using MainTile = Tile<T, kTileM, kTileN, StepK<T>::v, 4, 1>;
 
-template <typename T> struct Vec4;
-template <> struct Vec4<bf16> { typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 type; };
-template <> struct Vec4<float> { typedef f32x4 type; };
-
 // The layer of block b among n: the last one whose first block is <= b
 // (first blocks are non-decreasing, the unused entries INT32_MAX). The array
 // is read with wide scalar loads in flight together (its first 16 entries

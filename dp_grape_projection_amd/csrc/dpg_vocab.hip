@@ -27,10 +27,39 @@ namespace dpg {
 namespace {
 
 constexpr int kRowThreads = 1024;
-constexpr int kRun = 256;  // terms of one run of an fp32 product's sum
+constexpr int kPad = 256;     // packed rows and pieces are padded to whole tiles
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-template <typename T> struct VocabStep { static constexpr int v = sizeof(T) == 2 ? kStepBf16 : kStepF32; };
-template <typename T> using VocabTile = Tile<T, kTileM, kTileN, VocabStep<T>::v, 4, 1>;
+// fp32 operands are split exactly into three bf16 parts (8 + 8 + 8 bits of
+// the significand, each part truncated), x = h + m + l, and a product is six
+// bf16 products: every pair of parts but m l, l m and l l, which lie below
+// 2^-24 of it. The matrix cores run bf16 16 times as fast as fp32, so this is
+// 2.6 times as fast as their fp32 instructions at fp32's accuracy. Small
+// products are added first, so that the sum is rounded at its full size only
+// in the last pass over K.
+template <int PARTS> struct Combos;  // PARTS: bf16 parts of an operand
+template <> struct Combos<1> {
+  static constexpr int n = 1;
+  __device__ __forceinline__ static int a(int) { return 0; }
+  __device__ __forceinline__ static int b(int) { return 0; }
+};
+template <> struct Combos<3> {
+  static constexpr int n = 6;  // (l,h) (h,l) (m,m) (m,h) (h,m) (h,h)
+  __device__ __forceinline__ static int a(int c) { return (0x001102 >> (4 * c)) & 15; }
+  __device__ __forceinline__ static int b(int c) { return (0x010120 >> (4 * c)) & 15; }
+};
+template <typename T> constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+
+// The parts of x; the second and third are zero for infinities and NaN.
+__device__ __forceinline__ void split3(float x, bf16 (&p)[3]) {
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    p[q] = __builtin_bit_cast(bf16, static_cast<unsigned short>(u >> 16));
+    const float h = __builtin_bit_cast(float, u & 0xFFFF0000u);
+    x = (u & 0x7F800000u) == 0x7F800000u ? 0.0f : x - h;
+  }
+}
 
 // Per-call tables in the workspace. Row i of the packed arrays is the i-th
 // row that has a target.
@@ -41,7 +70,9 @@ struct VocabArgs {
   const float* t;       // [N][k] teacher logits, or null (cross entropy)
   const float* dloss;   // [N]
   int64_t N;
-  int32_t V, d, k, ldx; // ldx: row stride of Xp
+  int32_t V, d, k;
+  int32_t ldx;          // row stride of Xp, Ep and dXacc: d rounded up to 64
+  int32_t np;           // rows of Xp, D and dXacc: N rounded up to kPad
   float zscale;         // c / tau
   float dscale;         // c tau
   float tau;
@@ -55,12 +86,14 @@ struct VocabArgs {
   float* q;             // [N][k] target weights (distillation)
   float* ent;           // [N] sum q ln q (distillation)
   float* zt;            // [N][k] packed: target logits
-  void* Xp;             // [N][ldx] packed rows of X
-  float2* part;         // [col tiles][N] packed: tile maximum and sum
-  void* D;              // [N][ldd] packed: one piece of D
-  float* dXacc;         // [N][d] packed
-  int32_t ldd;
-  int32_t v0, vn;       // the piece: columns v0 .. v0 + vn - 1
+  bf16* Xp;             // [parts][np][ldx] packed rows of X
+  bf16* Ep;             // [parts][piece][ldx] the piece's rows of E, or null
+  float2* part;         // [col tiles][np] packed: tile maximum and sum, base 2
+  bf16* D;              // [parts][np][ldd] packed: one piece of D
+  float* dXacc;         // [splits][np][ldx] packed
+  int32_t ldd;          // columns of a piece (a multiple of kPad)
+  int32_t v0, vn;       // the piece: vocabulary rows v0 .. v0 + vn - 1
+  int32_t splits;       // parts of the vocabulary piece dX is summed in
 };
 
 // ------------------------------------------------------------------- rows --
@@ -139,106 +172,525 @@ __global__ __launch_bounds__(kRowThreads) void rows_kernel(const VocabArgs a) {
   if (tid == 0) a.count[0] = base;
 }
 
-// Xp[i] = X[row[i]], zero beyond d; one block per packed row.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a) {
-  const int i = blockIdx.x;
-  if (i >= a.count[0]) return;
-  const T* src = static_cast<const T*>(a.X) + static_cast<int64_t>(a.row[i]) * a.d;
-  T* dst = static_cast<T*>(a.Xp) + static_cast<int64_t>(i) * a.ldx;
-  for (int c = threadIdx.x; c < a.ldx; c += kThreads) dst[c] = c < a.d ? src[c] : zero_val<T>();
-}
-
-// All of a tile's steps. fp32: the products of every kRun columns are added
-// by themselves first, so that a long sum rounds like a short one (at d =
-// 4096 one chain leaves D off by 1.3e-5 of its value, runs of 256 by 4e-6).
-template <typename T, class Tl, class LA, class LB, class LoadStep>
-__device__ __forceinline__ void run_tile(LA& la, LB& lb, T* smem, Acc<Tl::MB, Tl::NB>& acc, int K,
-                                         int tid, LoadStep load_step) {
-  const int n_steps = (K + Tl::BK - 1) / Tl::BK;
-  acc.zero();
-  if constexpr (sizeof(T) == 4) {
-    Acc<Tl::MB, Tl::NB> part;
-    part.zero();
-    run_steps<T, Tl>(la, lb, smem, part, n_steps, tid, load_step, [&](int s) {
-      if ((s + 1) % (kRun / Tl::BK) == 0 || s + 1 == n_steps) {
-        acc.add(part);
-        part.zero();
-      }
-    });
+// One value as PARTS bf16 parts, `stride` elements apart.
+template <int PARTS>
+__device__ __forceinline__ void store_parts(bf16* dst, int64_t stride, float x) {
+  if constexpr (PARTS == 1) {
+    dst[0] = from_float<bf16>(x);
   } else {
-    run_steps<T, Tl>(la, lb, smem, acc, n_steps, tid, load_step, [](int) {});
+    bf16 p[3];
+    split3(x, p);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) dst[q * stride] = p[q];
   }
 }
 
-// ----------------------------------------------------------------- logits --
+// Xp[i] = X[row[i]], in parts, zero beyond d and from the last packed row to
+// the next multiple of kPad; one block per row of Xp.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void pack_rows_kernel(const VocabArgs a) {
+  const int i = blockIdx.x, rows = a.count[0];
+  if (i >= (rows + kPad - 1) / kPad * kPad) return;
+  const T* src = static_cast<const T*>(a.X) + static_cast<int64_t>(i < rows ? a.row[i] : 0) * a.d;
+  bf16* dst = a.Xp + static_cast<int64_t>(i) * a.ldx;
+  for (int c = threadIdx.x; c < a.ldx; c += kThreads)
+    store_parts<kParts<T>>(dst + c, static_cast<int64_t>(a.np) * a.ldx,
+                           i < rows && c < a.d ? to_float(src[c]) : 0.0f);
+}
 
-// One 128 x 128 tile of z (rows of Xp, columns of the vocabulary piece), on
-// the matrix cores. GRAD = false: the tile's maximum and sum of exponentials
-// of each row, and cross entropy's target logit. GRAD = true: the tile of D.
-template <typename T, bool VEC, bool GRAD>
-__global__ __launch_bounds__(kThreads, 2) void logits_kernel(const VocabArgs a) {
-  typedef VocabTile<T> Tl;
-  __shared__ __attribute__((aligned(16))) T smem[Tl::kLdsElems];
-  const int rows = a.count[0];
-  const int m0 = blockIdx.y * Tl::BM, c0 = blockIdx.x * Tl::BN;
-  if (m0 >= rows) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  RowsLoader<T, Tl::BM, Tl::BK, true, IdentityRows> la;
-  la.ld = a.ldx;
-  la.nrows = rows - m0;
-  la.K = a.ldx;
-  RowsLoader<T, Tl::BN, Tl::BK, VEC, BOperandRows<Tl>> lb;
-  lb.ld = a.d;
-  lb.nrows = a.vn - c0;
-  lb.K = a.d;
-  const T* pa = static_cast<const T*>(a.Xp) + static_cast<int64_t>(m0) * a.ldx;
-  const T* pb = static_cast<const T*>(a.E) + (static_cast<int64_t>(a.v0) + c0) * a.d;
-  Acc<Tl::MB, Tl::NB> acc;
-  run_tile<T, Tl>(la, lb, smem, acc, a.d, tid, [&](int s) {
-    la.load(pa, s * Tl::BK, tid, false);
-    lb.load(pb, s * Tl::BK, tid, false);
-  });
-  const int wm = Tl::wave_m(wave), wn = Tl::wave_n(wave);
+// Ep = the piece's rows of E, in parts, padded with zeros; one block per row.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void pack_table_kernel(const VocabArgs a) {
+  const int i = blockIdx.x;
+  const T* src = static_cast<const T*>(a.E) + (static_cast<int64_t>(a.v0) + i) * a.d;
+  bf16* dst = a.Ep + static_cast<int64_t>(i) * a.ldx;
+  for (int c = threadIdx.x; c < a.ldx; c += kThreads)
+    store_parts<kParts<T>>(dst + c, static_cast<int64_t>(a.ldd) * a.ldx,
+                           i < a.vn && c < a.d ? to_float(src[c]) : 0.0f);
+}
+
+// --------------------------------------------------------------- products --
+//
+// One kernel template computes the three products in 256 x 256 tiles, one
+// 16-wave block per CU, each wave 64 x 64 with 32x32x16 matrix instructions:
+//   logits   M = vocabulary rows (E), N = packed rows (Xp), K = d
+//   dX       M = packed rows (D), N = columns (E), K = the vocabulary piece
+//   dE       M = columns (Xp), N = vocabulary rows (D), K = packed rows
+// An operand whose K runs along its rows in memory ("rows") is copied as 256
+// rows of 128 bytes, chunk c of row R in slot c ^ (R / 2 mod 8), and read with
+// 16-byte LDS loads; one whose K runs down its columns ("k-major") as 64 rows
+// of 512 bytes, read with the transposing LDS load. The direct copies of A
+// run two K steps ahead of their use (three stages), those of B one (two
+// stages): 160 KiB of LDS. A lane's accumulator holds, per 32 x 32 block, one
+// N and four runs of four consecutive M; the roles above make that a row of
+// logits whose maximum and sum stay within the lane, and runs of four columns
+// of D and dE.
+//
+// Copies never leave their arrays: Xp, Ep and D are padded to whole tiles;
+// rows and chunks of E beyond its end are clamped to the last ones, and meet
+// zeros of the other operand.
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// vmcnt(N) with the other counters left alone.
+template <int N> __device__ __forceinline__ void wait_vm_n() {
+  static_assert(N < 16, "low four bits of the count");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | N);
+}
+
+constexpr int kTile = 256, kStepK = 64;
+constexpr int kTileBytes = kTile * kStepK * 2;
+
+struct Operand {
+  const bf16* base;     // first row of the tile (rows) or of K (k-major)
+  int64_t ld;           // row stride, elements
+  int64_t part_stride;  // elements between the bf16 parts
+  int rows;             // rows: rows there are from base; k-major: rows of K
+  int cols;             // rows: elements of K in a row; k-major: columns from base
+};
+
+// The direct copies of one operand: two of 1 KiB a wave and step.
+template <bool KMAJOR>
+struct Copier {
+  const char* base;
+  uint32_t ldb;       // row stride, bytes
+  uint32_t off[2];    // rows: row offset; k-major: K row of the lane
+  uint32_t chunk[2];  // byte offset of the lane's 16 bytes within the row
+  uint32_t last;      // rows: last chunk of a row; k-major: last K row
+  int64_t part_bytes;
+
+  __device__ __forceinline__ void init(const Operand& o, int lane, int wave) {
+    base = reinterpret_cast<const char*>(o.base);
+    ldb = static_cast<uint32_t>(o.ld) * 2u;
+    part_bytes = o.part_stride * 2;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = m0 + Tl::acc_row(wm, 0, i, lane);
+    for (int q = 0; q < 2; ++q) {
+      const int g = q * 16 + wave;
+      if constexpr (!KMAJOR) {
+        const int r = g * 8 + (lane >> 3);
+        off[q] = static_cast<uint32_t>(min(r, o.rows - 1)) * ldb;
+        chunk[q] = static_cast<uint32_t>((lane & 7) ^ ((r >> 1) & 7)) * 16u;
+      } else {
+        const int k = g * 2 + (lane >> 5);
+        off[q] = static_cast<uint32_t>(k);
+        chunk[q] = static_cast<uint32_t>(min((lane & 31) ^ (4 * (k & 3)), o.cols / 8 - 1)) * 16u;
+      }
+    }
+    last = KMAJOR ? static_cast<uint32_t>(o.rows - 1) : static_cast<uint32_t>(o.cols) * 2u - 16u;
+  }
+  // step ks of K (kStepK columns or rows from ks * kStepK) of part `part`
+  __device__ __forceinline__ void issue(int part, int ks, char* stage, int wave) const {
+    const char* p = base + part * part_bytes;
+    if constexpr (!KMAJOR) {
+      const uint32_t kb = static_cast<uint32_t>(ks) * (kStepK * 2);
+      const __amdgpu_buffer_rsrc_t rs = tile_rsrc(p);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        copy_to_lds(rs, off[q] + min(kb + chunk[q], last), 0, stage + (q * 16 + wave) * 1024);
+    } else {
+      const __amdgpu_buffer_rsrc_t rs = tile_rsrc(p + static_cast<int64_t>(ks) * kStepK * ldb);
+      const uint32_t lim = last - static_cast<uint32_t>(ks) * kStepK;
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        copy_to_lds(rs, min(off[q], lim) * ldb + chunk[q], 0, stage + (q * 16 + wave) * 1024);
+    }
+  }
+};
+
+// Matrix-core operand of sub-step kk: rows (columns) c0 .. c0 + 31 of the tile.
+template <bool KMAJOR>
+__device__ __forceinline__ bf16x8 tile_frag(const char* tile, int kk, int c0, int lane) {
+  if constexpr (KMAJOR) {
+    return frag_kmajor(tile, 16 * kk, c0, lane);
+  } else {
+    const int r = c0 + (lane & 31), c = 2 * kk + (lane >> 5);
+    return lds_read_b128(tile + r * (kStepK * 2) + (c ^ ((r >> 1) & 7)) * 16);
+  }
+}
+
+// acc = A B^T over K steps [0, n_k) of every combination of parts.
+template <int PARTS, bool KA, bool KB>
+__device__ __forceinline__ void tile_product(const Operand& oa, const Operand& ob, int n_k,
+                                             char* smem, Acc<2, 2>& acc) {
+  typedef Combos<PARTS> C;
+  constexpr int KK = kStepK / 16;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave & 3, wn = wave >> 2;
+  Copier<KA> ca;
+  Copier<KB> cb;
+  ca.init(oa, lane, wave);
+  cb.init(ob, lane, wave);
+  const int n_steps = n_k * C::n;
+  char* const sA = smem;
+  char* const sB = smem + 3 * kTileBytes;
+  auto issue_a = [&](int s, int stage) {
+    const int c = PARTS == 1 ? 0 : s / n_k;
+    ca.issue(C::a(c), s - c * n_k, sA + stage * kTileBytes, wave);
+  };
+  auto issue_b = [&](int s, int stage) {
+    const int c = PARTS == 1 ? 0 : s / n_k;
+    cb.issue(C::b(c), s - c * n_k, sB + stage * kTileBytes, wave);
+  };
+  bf16x8 fa[2][2], fb[2][2];
+  auto read_frags = [&](int sta, int stb, int kk, int to) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+      fa[to][m] = tile_frag<KA>(sA + sta * kTileBytes, kk, 64 * wm + 32 * m, lane);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+      fb[to][n] = tile_frag<KB>(sB + stb * kTileBytes, kk, 64 * wn + 32 * n, lane);
+  };
+  auto mma = [&](int f, int q0, int q1) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q >= q0 && q < q1)
+        acc.v[q >> 1][q & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            fa[f][q >> 1], fb[f][q & 1], acc.v[q >> 1][q & 1], 0, 0, 0);
+  };
+  acc.zero();
+  if (n_steps <= 0) return;
+  // Copies in issue order: A and B of step 0; B of step 1, A of steps 1 and
+  // 2; then at the barrier ending step s, B of step s + 2 and A of step s + 3.
+  // Before that barrier step s + 1's copies are complete once at most the
+  // two of A's step s + 2 are in flight: loads return in order.
+  issue_a(0, 0);
+  issue_b(0, 0);
+  wait_vm_n<0>();
+  lds_barrier();
+  if (n_steps > 1) {
+    issue_b(1, 1);
+    issue_a(1, 1);
+  }
+  if (n_steps > 2) issue_a(2, 2);
+  read_frags(0, 0, 0, 0);
+  int sta = 0;
+  for (int s = 0; s < n_steps; ++s) {
+    const int next = sta == 2 ? 0 : sta + 1;
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      const int cur = kk & 1, nxt = cur ^ 1;
+      const int first = kk + 1 < KK ? 1 : 2;
+      __builtin_amdgcn_sched_barrier(0);
+      mma(cur, 0, first);
+      __builtin_amdgcn_sched_barrier(0);
+      if (kk + 1 < KK) {
+        read_frags(sta, s & 1, kk + 1, nxt);
+      } else if (s + 1 < n_steps) {
+        wait_lgkm0();  // this wave's reads of step s are complete
+        if (s + 2 < n_steps) wait_vm_n<2>();
+        else wait_vm_n<0>();
+        lds_barrier();
+        if (s + 2 < n_steps) issue_b(s + 2, s & 1);
+        if (s + 3 < n_steps) issue_a(s + 3, sta);
+        read_frags(next, (s + 1) & 1, 0, nxt);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      mma(cur, first, 4);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    sta = next;
+  }
+}
+
+// The tile (m, n) of block blockIdx.x among mt x nt: each XCD takes a
+// contiguous run of them, in bands of eight m, so that the blocks an XCD runs
+// together share eight A and four B tiles in its L2. False past the last.
+__device__ __forceinline__ bool tile_of_block(int mt, int nt, int& m, int& n) {
+  const int total = mt * nt;
+  const int per = (total + 7) >> 3;
+  const int at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (static_cast<int>(blockIdx.x >> 3) >= per || at >= total) return false;
+  const int band = at / (8 * nt), in = at - band * 8 * nt;
+  const int h = min(8, mt - band * 8);
+  m = band * 8 + in % h;
+  n = in / h;
+  return true;
+}
+
+__device__ __forceinline__ int row_tiles(const VocabArgs& a) { return (a.count[0] + kTile - 1) / kTile; }
+
+// E as an operand of the current piece: packed, or the caller's own.
+__device__ __forceinline__ Operand table_operand(const VocabArgs& a, bool kmajor, int row0, int col0) {
+  Operand o;
+  if (a.Ep) {
+    o.base = a.Ep;
+    o.ld = a.ldx;
+    o.rows = a.ldd - row0;
+    o.cols = a.ldx;
+  } else {
+    o.base = static_cast<const bf16*>(a.E) + static_cast<int64_t>(a.v0) * a.d;
+    o.ld = a.d;
+    o.rows = a.vn - row0;
+    o.cols = a.d;
+  }
+  o.base += static_cast<int64_t>(row0) * o.ld + col0;
+  if (kmajor) o.cols -= col0;
+  o.part_stride = static_cast<int64_t>(a.ldd) * a.ldx;
+  return o;
+}
+__device__ __forceinline__ Operand rows_operand(const bf16* base, int64_t ld, int64_t part_stride,
+                                                int rows, int cols) {
+  Operand o;
+  o.base = base;
+  o.ld = ld;
+  o.part_stride = part_stride;
+  o.rows = rows;
+  o.cols = cols;
+  return o;
+}
+
+// Each row's maximum and sum of exponentials over a 256-column tile, and
+// cross entropy's target logit. Works in base 2: z log2(e).
+template <int PARTS>
+__global__ __launch_bounds__(4 * kThreads, 1) void stats_kernel(const VocabArgs a, int tile0) {
+  __shared__ __attribute__((aligned(1024))) char smem[5 * kTileBytes];
+  int mt, nt;
+  if (!tile_of_block((a.vn + kTile - 1) / kTile, row_tiles(a), mt, nt)) return;
+  const int c0 = mt * kTile, r0 = nt * kTile, rows = a.count[0];
+  Acc<2, 2> acc;
+  tile_product<PARTS, false, false>(
+      table_operand(a, false, c0, 0),
+      rows_operand(a.Xp + static_cast<int64_t>(r0) * a.ldx, a.ldx,
+                   static_cast<int64_t>(a.np) * a.ldx, kTile, a.ldx),
+      a.ldx / kStepK, smem, acc);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave & 3, wn = wave >> 2, r32 = lane & 31, kh = lane >> 5;
+  const int left = a.vn - c0 - 64 * wm - 4 * kh;  // columns from the lane's first
+  const float z2 = a.zscale * kLog2e;
+  float m[2], s[2];
+#pragma unroll
+  for (int nb = 0; nb < 2; ++nb) {
+    m[nb] = -INFINITY;
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float z = acc.v[mb][nb][i] * z2;
+        acc.v[mb][nb][i] = z;
+        if (32 * mb + 8 * (i >> 2) + (i & 3) < left) m[nb] = fmaxf(m[nb], z);
+      }
+    m[nb] = fmaxf(m[nb], __shfl_xor(m[nb], 32, 64));
+    s[nb] = 0.0f;
+    // (a wave whose columns all lie past the end has no maximum)
+    const float ref = m[nb] == -INFINITY ? 0.0f : m[nb];
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (32 * mb + 8 * (i >> 2) + (i & 3) < left) s[nb] += exp2_(acc.v[mb][nb][i] - ref);
+    s[nb] += __shfl_xor(s[nb], 32, 64);
+  }
+  if (!a.t) {
+#pragma unroll
+    for (int nb = 0; nb < 2; ++nb) {
+      const int r = r0 + 64 * wn + 32 * nb + r32;
+      const int64_t at = r < rows ? a.ids[a.row[r]] - a.v0 - c0 - 64 * wm - 4 * kh : -1;
+      if (at >= 0 && at < 64) {
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (at == 32 * mb + 8 * (i >> 2) + (i & 3)) a.zt[r] = acc.v[mb][nb][i] * kLn2;
+      }
+    }
+  }
+  // the four waves that share a row
+  float2* red = reinterpret_cast<float2*>(smem);
+  __syncthreads();
+  if (kh == 0)
+#pragma unroll
+    for (int nb = 0; nb < 2; ++nb)
+      red[wm * kTile + 64 * wn + 32 * nb + r32] = make_float2(m[nb], s[nb]);
+  __syncthreads();
+  if (tid < kTile) {
+    float2 p[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) p[w] = red[w * kTile + tid];
+    const float mm = fmaxf(fmaxf(p[0].x, p[1].x), fmaxf(p[2].x, p[3].x));
+    const float ref = mm == -INFINITY ? 0.0f : mm;
+    float ss = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) ss = fmaf(p[w].y, exp2_(p[w].x - ref), ss);
+    a.part[static_cast<int64_t>(tile0 + mt) * a.np + r0 + tid] = make_float2(mm, ss);
+  }
+}
+
+// A 256 x 256 tile of bf16 values, staged in LDS and written in rows of 512
+// bytes: value(nb, mb, i) of the accumulator layout goes to row 64 wn + 32 nb
+// + r32, column 64 wm + 32 mb + 8 (i / 4) + 4 kh + i % 4. Rows >= n_rows and
+// columns >= n_cols are not written (n_cols a multiple of eight, or VEC
+// false: element by element). 16-byte chunk c of row R sits in slot
+// c ^ (R mod 32).
+template <class F>
+__device__ __forceinline__ void write_tile(char* smem, bf16* dst, int64_t ld, int n_rows, int n_cols,
+                                           bool vec, F value) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave & 3, wn = wave >> 2, r32 = lane & 31, kh = lane >> 5;
+  __syncthreads();
+#pragma unroll
+  for (int nb = 0; nb < 2; ++nb) {
+    const int r = 64 * wn + 32 * nb + r32;
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        Vec4<bf16>::type v;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = value(nb, mb, 4 * j + q);
+        const int c = 8 * wm + 4 * mb + j;
+        *reinterpret_cast<Vec4<bf16>::type*>(smem + r * 512 + (c ^ r32) * 16 + kh * 8) = v;
+      }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int it = 0; it < 8; ++it) {
+    const int r = it * 32 + wave * 2 + kh, c = r32;
+    const bf16x8 v = lds_read_b128(smem + r * 512 + (c ^ (r & 31)) * 16);
+    if (r < n_rows && c * 8 < n_cols) {
+      bf16* p = dst + static_cast<int64_t>(r) * ld + c * 8;
+      if (vec) {
+        *reinterpret_cast<bf16x8*>(p) = v;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (c * 8 + q < n_cols) p[q] = v[q];
+      }
+    }
+  }
+}
+
+// One tile of D for the piece: dloss_n c tau (exp(z - lse_n) - [target]),
+// zero beyond the piece and the packed rows. (Distillation subtracts its
+// target weights afterwards.) One rounding to bf16: D enters two products
+// whose other operand is bf16; with fp32 D is kept in three parts.
+template <int PARTS>
+__global__ __launch_bounds__(4 * kThreads, 1) void grad_logits_kernel(const VocabArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[5 * kTileBytes];
+  int mt, nt;
+  if (!tile_of_block((a.vn + kTile - 1) / kTile, row_tiles(a), mt, nt)) return;
+  const int c0 = mt * kTile, r0 = nt * kTile, rows = a.count[0];
+  Acc<2, 2> acc;
+  tile_product<PARTS, false, false>(
+      table_operand(a, false, c0, 0),
+      rows_operand(a.Xp + static_cast<int64_t>(r0) * a.ldx, a.ldx,
+                   static_cast<int64_t>(a.np) * a.ldx, kTile, a.ldx),
+      a.ldx / kStepK, smem, acc);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave & 3, wn = wave >> 2, r32 = lane & 31, kh = lane >> 5;
+  const int left = a.vn - c0 - 64 * wm - 4 * kh;
+  const float z2 = a.zscale * kLog2e;
+#pragma unroll
+  for (int nb = 0; nb < 2; ++nb) {
+    const int r = r0 + 64 * wn + 32 * nb + r32;
     const bool in = r < rows;
     const int n = in ? a.row[r] : 0;
-    const int64_t target = in && !a.t ? a.ids[n] : -1;
-    if constexpr (!GRAD) {
-      float m = -INFINITY;
+    const float g = in ? a.dloss[n] * a.dscale : 0.0f;
+    const float lse2 = in ? a.lse[n] * kLog2e : 0.0f;
+    const int64_t at = in && !a.t ? a.ids[n] - a.v0 - c0 - 64 * wm - 4 * kh : -1;
 #pragma unroll
-      for (int nb = 0; nb < Tl::NB; ++nb) {
-        const int c = c0 + Tl::acc_col(wn, nb, lane);
-        const float z = acc.v[0][nb][i] * a.zscale;
-        if (c < a.vn) m = fmaxf(m, z);
-        if (c < a.vn && in && target == a.v0 + c) a.zt[r] = z;
+    for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int c = 32 * mb + 8 * (i >> 2) + (i & 3);
+        float p = exp2_(fmaf(acc.v[mb][nb][i], z2, -lse2));
+        if (at == c) p -= 1.0f;
+        acc.v[mb][nb][i] = in && c < left ? g * p : 0.0f;
       }
+  }
+  bf16* dst = a.D + static_cast<int64_t>(r0) * a.ldd + c0;
+  if constexpr (PARTS == 1) {
+    write_tile(smem, dst, a.ldd, kTile, kTile, true,
+               [&](int nb, int mb, int i) { return from_float<bf16>(acc.v[mb][nb][i]); });
+  } else {
 #pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-      float s = 0.0f;
+    for (int q = 0; q < 3; ++q)
+      write_tile(smem, dst + static_cast<int64_t>(q) * a.np * a.ldd, a.ldd, kTile, kTile, true,
+                 [&](int nb, int mb, int i) {
+                   bf16 p[3];
+                   split3(acc.v[mb][nb][i], p);
+                   return p[q];
+                 });
+  }
+}
+
+// dXacc[split] (+)= D E over the split's part of the piece.
+template <int PARTS>
+__global__ __launch_bounds__(4 * kThreads, 1) void dx_kernel(const VocabArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[5 * kTileBytes];
+  int mt, nt;
+  const int ct = (a.ldx + kTile - 1) / kTile;
+  if (!tile_of_block(row_tiles(a), ct * a.splits, mt, nt)) return;
+  const int split = nt / ct;
+  const int c0 = (nt - split * ct) * kTile, r0 = mt * kTile;
+  const int steps = (a.vn + kStepK - 1) / kStepK, per = (steps + a.splits - 1) / a.splits;
+  const int k0 = min(steps, split * per), k1 = min(steps, k0 + per);
+  Acc<2, 2> acc;
+  tile_product<PARTS, false, true>(
+      rows_operand(a.D + static_cast<int64_t>(r0) * a.ldd + k0 * kStepK, a.ldd,
+                   static_cast<int64_t>(a.np) * a.ldd, kTile, a.ldd - k0 * kStepK),
+      table_operand(a, true, k0 * kStepK, c0), k1 - k0, smem, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave & 3, wn = wave >> 2, r32 = lane & 31, kh = lane >> 5;
+  float* dst = a.dXacc + (static_cast<int64_t>(split) * a.np + r0 + 64 * wm + 4 * kh) * a.ldx + c0 +
+               64 * wn + r32;
 #pragma unroll
-      for (int nb = 0; nb < Tl::NB; ++nb) {
-        const int c = c0 + Tl::acc_col(wn, nb, lane);
-        const float z = acc.v[0][nb][i] * a.zscale;
-        if (c < a.vn) s += expf(z - m);
+  for (int nb = 0; nb < 2; ++nb) {
+    if (c0 + 64 * wn + 32 * nb >= a.ldx) continue;
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float* p = dst + static_cast<int64_t>(32 * mb + 8 * (i >> 2) + (i & 3)) * a.ldx + 32 * nb;
+        *p = a.v0 == 0 ? acc.v[mb][nb][i] : *p + acc.v[mb][nb][i];
       }
+  }
+}
+
+// The piece's rows of dE = D^T Xp, rounded once.
+template <typename T>
+__global__ __launch_bounds__(4 * kThreads, 1) void de_kernel(const VocabArgs a, T* dE) {
+  constexpr int PARTS = kParts<T>;
+  __shared__ __attribute__((aligned(1024))) char smem[5 * kTileBytes];
+  int mt, nt;
+  const int ct = (a.ldx + kTile - 1) / kTile;
+  // (bands of eight run over the vocabulary, the longer side)
+  if (!tile_of_block((a.vn + kTile - 1) / kTile, ct, nt, mt)) return;
+  const int c0 = mt * kTile, w0 = nt * kTile, rows = a.count[0];
+  Acc<2, 2> acc;
+  tile_product<PARTS, true, true>(
+      rows_operand(a.Xp + c0, a.ldx, static_cast<int64_t>(a.np) * a.ldx, a.np, a.ldx - c0),
+      rows_operand(a.D + w0, a.ldd, static_cast<int64_t>(a.np) * a.ldd, a.np, kTile),
+      (rows + kStepK - 1) / kStepK, smem, acc);
+  T* dst = dE + (static_cast<int64_t>(a.v0) + w0) * a.d + c0;
+  const int n_rows = a.vn - w0, n_cols = a.d - c0;
+  if constexpr (PARTS == 1) {
+    write_tile(smem, dst, a.d, n_rows, n_cols, a.d % 8 == 0 && is_aligned(dE, 16),
+               [&](int nb, int mb, int i) { return from_float<bf16>(acc.v[mb][nb][i]); });
+  } else {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = wave & 3, wn = wave >> 2, r32 = lane & 31, kh = lane >> 5;
+    const bool vec = a.d % 4 == 0 && is_aligned(dE, 16);
 #pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor(s, off, 64);
-      if (in && (lane & 31) == 0)
-        a.part[static_cast<int64_t>(blockIdx.x) * a.N + r] = make_float2(m, s);
-    } else if (in) {
-      const float g = a.dloss[n] * a.dscale, lse = a.lse[n];
-      T* dst = static_cast<T*>(a.D) + static_cast<int64_t>(r) * a.ldd;
+    for (int nb = 0; nb < 2; ++nb) {
+      const int r = 64 * wn + 32 * nb + r32;
+      if (r >= n_rows) continue;
 #pragma unroll
-      for (int nb = 0; nb < Tl::NB; ++nb) {
-        const int c = c0 + Tl::acc_col(wn, nb, lane);
-        const float z = acc.v[0][nb][i] * a.zscale;
-        float p = expf(z - lse);
-        if (target == a.v0 + c) p -= 1.0f;
-        if (c < a.ldd) dst[c] = c < a.vn ? from_float<T>(g * p) : zero_val<T>();
-      }
+      for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = 64 * wm + 32 * mb + 8 * j + 4 * kh;
+          T* p = dst + static_cast<int64_t>(r) * a.d + c;
+          f32x4 v;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = acc.v[mb][nb][4 * j + q];
+          if (vec && c + 4 <= n_cols) {
+            *reinterpret_cast<f32x4*>(p) = v;
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (c + q < n_cols) p[q] = v[q];
+          }
+        }
     }
   }
 }
@@ -250,7 +702,7 @@ __global__ __launch_bounds__(kThreads) void target_logits_kernel(const VocabArgs
   if (i >= a.count[0]) return;
   const int lane = threadIdx.x & 63;
   const int64_t n = a.row[i];
-  const T* x = static_cast<const T*>(a.Xp) + static_cast<int64_t>(i) * a.ldx;
+  const T* x = static_cast<const T*>(a.X) + n * a.d;
   for (int j = threadIdx.x >> 6; j < a.k; j += 4) {
     const int64_t id = a.ids[n * a.k + j];
     if (id < 0 || id >= a.V) continue;
@@ -273,16 +725,16 @@ __global__ __launch_bounds__(kThreads) void lse_kernel(const VocabArgs a, int ti
     return;
   }
   float m = -INFINITY;
-  for (int t = lane; t < tiles; t += 64) m = fmaxf(m, a.part[static_cast<int64_t>(t) * a.N + i].x);
+  for (int t = lane; t < tiles; t += 64) m = fmaxf(m, a.part[static_cast<int64_t>(t) * a.np + i].x);
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
   float s = 0.0f;
   for (int t = lane; t < tiles; t += 64) {
-    const float2 p = a.part[static_cast<int64_t>(t) * a.N + i];
-    s = fmaf(p.y, expf(p.x - m), s);
+    const float2 p = a.part[static_cast<int64_t>(t) * a.np + i];
+    s = fmaf(p.y, exp2_(p.x - m), s);
   }
   s = wave_sum(s);
-  const float lse = m + logf(s);
+  const float lse = kLn2 * m + logf(s);
   float qz = 0.0f;
   if (a.t) {
     for (int j = lane; j < a.k; j += 64) {
@@ -314,92 +766,21 @@ __global__ __launch_bounds__(kThreads) void teacher_entries_kernel(const VocabAr
   for (int j = 0; j < a.k; ++j)
     if (ids[j] == id) q += a.q[n * a.k + j];
   const float p = expf(a.zt[at] - a.lse[n]);
-  static_cast<T*>(a.D)[i * a.ldd + (id - a.v0)] = from_float<T>(a.dloss[n] * a.dscale * (p - q));
+  store_parts<kParts<T>>(a.D + i * a.ldd + (id - a.v0), static_cast<int64_t>(a.np) * a.ldd,
+                         a.dloss[n] * a.dscale * (p - q));
 }
 
-// --------------------------------------------------------------- products --
-
-// dXacc (+)= D E over one piece: 128 x 128 tiles over (packed rows, d).
-template <typename T, bool PAIR>
-__global__ __launch_bounds__(kThreads, 2) void dx_kernel(const VocabArgs a) {
-  typedef VocabTile<T> Tl;
-  __shared__ __attribute__((aligned(16))) T smem[Tl::kLdsElems];
-  const int rows = a.count[0];
-  const int m0 = blockIdx.y * Tl::BM, c0 = blockIdx.x * Tl::BN;
-  if (m0 >= rows) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  RowsLoader<T, Tl::BM, Tl::BK, true, IdentityRows> la;
-  la.ld = a.ldd;
-  la.nrows = rows - m0;
-  la.K = a.vn;
-  ColsLoader<T, Tl::BN, Tl::BK, PAIR, BOperandRows<Tl>> lb;
-  lb.ld = a.d;
-  lb.ncols = a.d - c0;
-  lb.K = a.vn;
-  const T* pa = static_cast<const T*>(a.D) + static_cast<int64_t>(m0) * a.ldd;
-  const T* pb = static_cast<const T*>(a.E) + static_cast<int64_t>(a.v0) * a.d + c0;
-  Acc<Tl::MB, Tl::NB> acc;
-  run_tile<T, Tl>(la, lb, smem, acc, a.vn, tid, [&](int s) {
-    la.load(pa, s * Tl::BK, tid, false);
-    lb.load(pb, s * Tl::BK, tid, false);
-  });
-  const int wm = Tl::wave_m(wave), wn = Tl::wave_n(wave);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = m0 + Tl::acc_row(wm, 0, i, lane);
-    if (r >= rows) continue;
-    float* dst = a.dXacc + static_cast<int64_t>(r) * a.d;
-#pragma unroll
-    for (int nb = 0; nb < Tl::NB; ++nb) {
-      const int c = c0 + Tl::acc_col(wn, nb, lane);
-      if (c < a.d) dst[c] = a.v0 == 0 ? acc.v[0][nb][i] : dst[c] + acc.v[0][nb][i];
-    }
-  }
-}
-
-// dX[n] = the row's accumulated gradient rounded once; zero without target.
+// dX[n] = the row's sums over the splits, rounded once; zero without target.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void dx_out_kernel(const VocabArgs a, T* dX) {
   const int64_t n = blockIdx.x;
   const int i = a.inv[n];
-  for (int c = threadIdx.x; c < a.d; c += kThreads)
-    dX[n * a.d + c] = i < 0 ? zero_val<T>() : from_float<T>(a.dXacc[static_cast<int64_t>(i) * a.d + c]);
-}
-
-// dE rows of one piece = D^T Xp: 128 x 128 tiles over (piece, d).
-template <typename T>
-__global__ __launch_bounds__(kThreads, 2) void de_kernel(const VocabArgs a, T* dE) {
-  typedef VocabTile<T> Tl;
-  __shared__ __attribute__((aligned(16))) T smem[Tl::kLdsElems];
-  const int rows = a.count[0];
-  const int m0 = blockIdx.y * Tl::BM, c0 = blockIdx.x * Tl::BN;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  ColsLoader<T, Tl::BM, Tl::BK, true, IdentityRows> la;
-  la.ld = a.ldd;
-  la.ncols = a.vn - m0;
-  la.K = rows;
-  ColsLoader<T, Tl::BN, Tl::BK, true, BOperandRows<Tl>> lb;
-  lb.ld = a.ldx;
-  lb.ncols = a.ldx - c0;
-  lb.K = rows;
-  const T* pa = static_cast<const T*>(a.D) + m0;
-  const T* pb = static_cast<const T*>(a.Xp) + c0;
-  Acc<Tl::MB, Tl::NB> acc;
-  run_tile<T, Tl>(la, lb, smem, acc, rows, tid, [&](int s) {
-    la.load(pa, s * Tl::BK, tid, false);
-    lb.load(pb, s * Tl::BK, tid, false);
-  });
-  const int wm = Tl::wave_m(wave), wn = Tl::wave_n(wave);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = m0 + Tl::acc_row(wm, 0, i, lane);
-    if (r >= a.vn) continue;
-    T* dst = dE + (static_cast<int64_t>(a.v0) + r) * a.d;
-#pragma unroll
-    for (int nb = 0; nb < Tl::NB; ++nb) {
-      const int c = c0 + Tl::acc_col(wn, nb, lane);
-      if (c < a.d) dst[c] = from_float<T>(acc.v[0][nb][i]);
-    }
+  for (int c = threadIdx.x; c < a.d; c += kThreads) {
+    float x = 0.0f;
+    if (i >= 0)
+      for (int s = 0; s < a.splits; ++s)
+        x += a.dXacc[(static_cast<int64_t>(s) * a.np + i) * a.ldx + c];
+    dX[n * a.d + c] = from_float<T>(x);
   }
 }
 
@@ -444,19 +825,32 @@ int check_call(const VocabCall& c, bool distill) {
   return DPG_OK;
 }
 
-// Bytes of D kept at a time.
+// Bytes of D, and of the packed table, kept at a time.
 constexpr int64_t kPieceBytes = 512ll << 20;
 
 struct VocabPlan {
-  int64_t ldx = 0, piece = 0;
-  size_t off_flag, off_count, off_row, off_inv, off_q, off_ent, off_zt, off_Xp, off_part, off_D,
-      off_dX, total;
+  int64_t ldx = 0, np = 0, piece = 0;
+  int32_t splits = 1;
+  size_t off_flag, off_count, off_row, off_inv, off_q, off_ent, off_zt, off_Xp, off_Ep, off_part,
+      off_D, off_dX, total;
 };
 
 VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, bool distill, bool grad) {
   VocabPlan p;
-  const int64_t es = dtype == DPG_BF16 ? 2 : 4;
-  p.ldx = round_up(d, 64);
+  const int64_t parts = dtype == DPG_BF16 ? 1 : 3;
+  p.ldx = round_up(d, kStepK);
+  p.np = round_up(N, kPad);
+  // one piece of the vocabulary: its D, and its packed table where one may be
+  // needed (fp32, rows that are not whole 16 bytes, or an unaligned table)
+  p.piece = kPieceBytes / (p.ldx * 2 * parts);
+  if (grad) p.piece = std::min(p.piece, kPieceBytes / (p.np * 2 * parts));
+  p.piece = std::min(round_up(V, kPad), std::max<int64_t>(kPad, p.piece / kPad * kPad));
+  // dX has few tiles when rows are few: the sum over the vocabulary is then
+  // split so that the blocks fill the chip's 256 CUs, each with at least
+  // eight K steps
+  const int64_t tiles = p.np / kTile * ceil_div(p.ldx, kTile);
+  p.splits = static_cast<int32_t>(
+      std::max<int64_t>(1, std::min<int64_t>(256 / tiles, p.piece / kStepK / 8)));
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -470,11 +864,11 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   p.off_q = take(distill ? N * k * 4 : 0);
   p.off_ent = take(distill ? N * 4 : 0);
   p.off_zt = take(N * k * 4);
-  p.off_Xp = take(N * p.ldx * es);
-  p.off_part = take(grad ? 0 : ceil_div(V, kTileN) * N * 8);
-  p.piece = std::min(round_up(V, 256), std::max<int64_t>(256, kPieceBytes / (N * es) / 256 * 256));
-  p.off_D = take(grad ? N * p.piece * es : 0);
-  p.off_dX = take(grad ? N * d * 4 : 0);
+  p.off_Xp = take(parts * p.np * p.ldx * 2);
+  p.off_Ep = take(parts * p.piece * p.ldx * 2);
+  p.off_part = take(grad ? 0 : ceil_div(V, kTile) * p.np * 8);
+  p.off_D = take(grad ? parts * p.np * p.piece * 2 : 0);
+  p.off_dX = take(grad ? p.splits * p.np * p.ldx * 4 : 0);
   p.total = off;
   return p;
 }
@@ -490,6 +884,7 @@ VocabArgs make_args(const VocabCall& c, const VocabPlan& p, char* ws) {
   a.d = static_cast<int32_t>(c.d);
   a.k = c.k;
   a.ldx = static_cast<int32_t>(p.ldx);
+  a.np = static_cast<int32_t>(p.np);
   a.zscale = static_cast<float>(c.scale / c.tau);
   a.dscale = static_cast<float>(c.scale * c.tau);
   a.tau = static_cast<float>(c.tau);
@@ -500,17 +895,20 @@ VocabArgs make_args(const VocabCall& c, const VocabPlan& p, char* ws) {
   a.q = reinterpret_cast<float*>(ws + p.off_q);
   a.ent = reinterpret_cast<float*>(ws + p.off_ent);
   a.zt = reinterpret_cast<float*>(ws + p.off_zt);
-  a.Xp = ws + p.off_Xp;
+  a.Xp = reinterpret_cast<bf16*>(ws + p.off_Xp);
+  a.Ep = c.dtype == DPG_FP32 || c.d % 8 != 0 || !aligned(c.E, 16)
+             ? reinterpret_cast<bf16*>(ws + p.off_Ep) : nullptr;
   a.part = reinterpret_cast<float2*>(ws + p.off_part);
-  a.D = ws + p.off_D;
+  a.D = reinterpret_cast<bf16*>(ws + p.off_D);
   a.dXacc = reinterpret_cast<float*>(ws + p.off_dX);
   a.ldd = static_cast<int32_t>(p.piece);
-  a.v0 = 0;
-  a.vn = a.V;
+  a.splits = p.splits;
   return a;
 }
 
 unsigned blocks_of(int64_t n, int64_t per) { return static_cast<unsigned>(ceil_div(n, per)); }
+// grid of tile_of_block for mt x nt tiles
+dim3 tile_grid(int64_t mt, int64_t nt) { return dim3(static_cast<unsigned>(round_up(mt * nt, 8))); }
 
 // Target weights, the packed rows and their X; with distillation also the
 // logits of the teacher's entries.
@@ -520,49 +918,53 @@ int prepare_rows(const VocabArgs& a, hipStream_t s) {
   if (a.t) hipLaunchKernelGGL(teacher_kernel, dim3(blocks_of(a.N, 4)), b, 0, s, a);
   else hipLaunchKernelGGL(ce_flag_kernel, dim3(blocks_of(a.N, kThreads)), b, 0, s, a);
   hipLaunchKernelGGL(rows_kernel, dim3(1), dim3(kRowThreads), 0, s, a);
-  hipLaunchKernelGGL(pack_kernel<T>, dim3(static_cast<unsigned>(a.N)), b, 0, s, a);
+  hipLaunchKernelGGL(pack_rows_kernel<T>, dim3(static_cast<unsigned>(a.np)), b, 0, s, a);
   if (a.t) hipLaunchKernelGGL(target_logits_kernel<T>, dim3(static_cast<unsigned>(a.N)), b, 0, s, a);
   return check_launch("vocab rows");
 }
 
-template <typename T, bool GRAD>
-void launch_logits(const VocabArgs& a, hipStream_t s) {
-  const dim3 g(blocks_of(GRAD ? a.ldd : a.vn, kTileN), blocks_of(a.N, kTileM)), b(kThreads);
-  const bool vec = a.d % (16 / sizeof(T)) == 0 && aligned(a.E, 16);
-  if (vec) hipLaunchKernelGGL((logits_kernel<T, true, GRAD>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((logits_kernel<T, false, GRAD>), g, b, 0, s, a);
+// fn for every piece of the vocabulary, its table packed first where needed.
+template <typename T, class F>
+void for_pieces(VocabArgs& a, hipStream_t s, F fn) {
+  for (int64_t v0 = 0; v0 < a.V; v0 += a.ldd) {
+    a.v0 = static_cast<int32_t>(v0);
+    a.vn = static_cast<int32_t>(std::min<int64_t>(a.ldd, a.V - v0));
+    if (a.Ep)
+      hipLaunchKernelGGL(pack_table_kernel<T>, dim3(static_cast<unsigned>(round_up(a.vn, kPad))),
+                         dim3(kThreads), 0, s, a);
+    fn();
+  }
 }
 
 template <typename T>
-int run_loss(const VocabArgs& a, hipStream_t s) {
+int run_loss(VocabArgs a, hipStream_t s) {
   if (const int st = prepare_rows<T>(a, s)) return st;
-  launch_logits<T, false>(a, s);
+  for_pieces<T>(a, s, [&] {
+    hipLaunchKernelGGL(stats_kernel<kParts<T>>, tile_grid(ceil_div(a.vn, kTile), a.np / kTile),
+                       dim3(4 * kThreads), 0, s, a, a.v0 / kTile);
+  });
   hipLaunchKernelGGL(lse_kernel, dim3(blocks_of(a.N, 4)), dim3(kThreads), 0, s, a,
-                     static_cast<int>(blocks_of(a.vn, kTileN)));
+                     static_cast<int>(ceil_div(a.V, kTile)));
   return check_launch("vocab loss");
 }
 
 template <typename T>
 int run_grad(VocabArgs a, void* dX, void* dE, hipStream_t s) {
   if (const int st = prepare_rows<T>(a, s)) return st;
-  const dim3 b(kThreads);
-  const unsigned dt = blocks_of(a.d, kTileN);
-  for (int64_t v0 = 0; v0 < a.V; v0 += a.ldd) {
-    a.v0 = static_cast<int32_t>(v0);
-    a.vn = static_cast<int32_t>(std::min<int64_t>(a.ldd, a.V - v0));
-    launch_logits<T, true>(a, s);
+  const dim3 b(4 * kThreads);
+  const int64_t rt = a.np / kTile, ct = ceil_div(a.ldx, kTile);
+  for_pieces<T>(a, s, [&] {
+    const int64_t vt = ceil_div(a.vn, kTile);
+    hipLaunchKernelGGL(grad_logits_kernel<kParts<T>>, tile_grid(vt, rt), b, 0, s, a);
     if (a.t)
-      hipLaunchKernelGGL(teacher_entries_kernel<T>, dim3(blocks_of(a.N * a.k, kThreads)), b, 0, s, a);
-    if (dX) {
-      const dim3 g(dt, blocks_of(a.N, kTileM));
-      if (a.d % 2 == 0 && aligned(a.E, 4)) hipLaunchKernelGGL((dx_kernel<T, true>), g, b, 0, s, a);
-      else hipLaunchKernelGGL((dx_kernel<T, false>), g, b, 0, s, a);
-    }
-    if (dE)
-      hipLaunchKernelGGL(de_kernel<T>, dim3(dt, blocks_of(a.vn, kTileM)), b, 0, s, a, static_cast<T*>(dE));
-  }
+      hipLaunchKernelGGL(teacher_entries_kernel<T>, dim3(blocks_of(a.N * a.k, kThreads)),
+                         dim3(kThreads), 0, s, a);
+    if (dX) hipLaunchKernelGGL(dx_kernel<kParts<T>>, tile_grid(rt, ct * a.splits), b, 0, s, a);
+    if (dE) hipLaunchKernelGGL(de_kernel<T>, tile_grid(vt, ct), b, 0, s, a, static_cast<T*>(dE));
+  });
   if (dX)
-    hipLaunchKernelGGL(dx_out_kernel<T>, dim3(static_cast<unsigned>(a.N)), b, 0, s, a, static_cast<T*>(dX));
+    hipLaunchKernelGGL(dx_out_kernel<T>, dim3(static_cast<unsigned>(a.N)), dim3(kThreads), 0, s, a,
+                       static_cast<T*>(dX));
   return check_launch("vocab gradient");
 }
 
