@@ -200,11 +200,11 @@ def _on_stream(fn):
     to the stream the library's kernels are enqueued on: the caching
     allocator then does not hand their memory to other work while those
     kernels may still use it."""
-    sig = inspect.signature(fn)
+    at = list(inspect.signature(fn).parameters).index("stream")
 
     @functools.wraps(fn)
     def wrapper(*args, **kw):
-        stream = sig.bind(*args, **kw).arguments.get("stream")
+        stream = args[at] if len(args) > at else kw.get("stream")
         if stream is None:
             return fn(*args, **kw)
         with torch.cuda.stream(stream):
