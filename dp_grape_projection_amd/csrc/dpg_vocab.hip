@@ -85,7 +85,13 @@ struct VocabArgs {
   int32_t* inv;         // [N] row -> packed, -1
   float* q;             // [N][k] target weights (distillation)
   float* ent;           // [N] sum q ln q (distillation)
-  float* zt;            // [N][k] packed: target logits
+  float* zt;            // [N][k] packed: logits of the target, or of the
+                        // teacher's distinct ids in ascending order
+  float* qu;            // [N][k] packed: weights of those ids
+  int32_t* nu;          // [N] packed: how many of them the pieces so far held
+  uint64_t* bits;       // [N][ldd / 64] packed: the piece's columns that are
+                        // teacher ids
+  uint16_t* before;     // [N][ldd / 64] packed: index in qu of a word's first
   bf16* Xp;             // [parts][np][ldx] packed rows of X
   bf16* Ep;             // [parts][piece][ldx] the piece's rows of E, or null
   float2* part;         // [col tiles][np] packed: tile maximum and sum, base 2
@@ -207,6 +213,81 @@ __global__ __launch_bounds__(kThreads) void pack_table_kernel(const VocabArgs a)
   for (int c = threadIdx.x; c < a.ldx; c += kThreads)
     store_parts<kParts<T>>(dst + c, static_cast<int64_t>(a.ldd) * a.ldx,
                            i < a.vn && c < a.d ? to_float(src[c]) : 0.0f);
+}
+
+// Distillation: where a packed row's teacher ids lie in the piece, as one bit
+// per column, so that the tiles' epilogues find them; one block per row. The
+// row's distinct ids get consecutive places in qu, in ascending order; an id
+// named more than once gets its weights' sum, in the order they are named.
+constexpr int kMaxWords = 4096;  // 64-column words of a piece
+__global__ __launch_bounds__(kThreads) void teacher_ids_kernel(const VocabArgs a) {
+  __shared__ uint32_t half[2 * kMaxWords];
+  __shared__ uint16_t first[kMaxWords];
+  __shared__ int wave_cnt[4];
+  const int i = blockIdx.x;
+  if (i >= a.count[0]) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int words = a.ldd / 64;
+  const int64_t n = a.row[i];
+  const int64_t* ids = a.ids + n * a.k;
+  const float* q = a.q + n * a.k;
+  for (int w = tid; w < 2 * words; w += kThreads) half[w] = 0;
+  __syncthreads();
+  auto col = [&](int j) {  // column of entry j in the piece, or -1
+    const int64_t c = ids[j] - a.v0;
+    return c >= 0 && c < a.vn && q[j] != 0.0f ? static_cast<int>(c) : -1;
+  };
+  for (int j = tid; j < a.k; j += kThreads) {
+    const int c = col(j);
+    if (c >= 0) atomicOr(&half[c >> 5], 1u << (c & 31));
+  }
+  __syncthreads();
+  auto word = [&](int w) {
+    return static_cast<uint64_t>(half[2 * w + 1]) << 32 | half[2 * w];
+  };
+  int base = a.v0 == 0 ? 0 : a.nu[i];
+  const int per = (words + kThreads - 1) / kThreads, w0 = min(words, tid * per),
+            w1 = min(words, w0 + per);
+  int c = 0;
+  for (int w = w0; w < w1; ++w) c += __popcll(word(w));
+  int x = c;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int y = __shfl_up(x, off, 64);
+    if (lane >= off) x += y;
+  }
+  if (lane == 63) wave_cnt[wave] = x;
+  __syncthreads();
+  int at = base + x - c, all = 0;
+  for (int w = 0; w < 4; ++w) {
+    if (w < wave) at += wave_cnt[w];
+    all += wave_cnt[w];
+  }
+  for (int w = w0; w < w1; ++w) {
+    first[w] = static_cast<uint16_t>(at);
+    at += __popcll(word(w));
+  }
+  __syncthreads();
+  if (tid == 0) a.nu[i] = base + all;
+  const int64_t out = static_cast<int64_t>(i) * words;
+  for (int w = tid; w < words; w += kThreads) {
+    a.bits[out + w] = word(w);
+    a.before[out + w] = first[w];
+  }
+  for (int j = tid; j < a.k; j += kThreads) {
+    const int c = col(j);
+    if (c < 0) continue;
+    bool again = false;
+    float sum = 0.0f;
+    for (int l = 0; l < a.k; ++l) {
+      if (ids[l] != ids[j]) continue;
+      again |= l < j;
+      sum += q[l];
+    }
+    if (!again)
+      a.qu[static_cast<int64_t>(i) * a.k + first[c >> 6] +
+           __popcll(word(c >> 6) & ((1ull << (c & 63)) - 1))] = sum;
+  }
 }
 
 // --------------------------------------------------------------- products --
@@ -439,22 +520,51 @@ __device__ __forceinline__ Operand rows_operand(const bf16* base, int64_t ld, in
   return o;
 }
 
+// The teacher's ids among the columns of a lane's accumulator for one packed
+// row: columns 64 wm .. of the tile that begins at column c0 of the piece, in
+// the lane's half (4 kh .. 4 kh + 3 of every eight).
+struct LaneIds {
+  uint64_t word, mine;
+  int64_t at;  // the word's index
+  __device__ __forceinline__ void load(const VocabArgs& a, int r, int rows, int c0, int wm, int kh) {
+    at = static_cast<int64_t>(r) * (a.ldd / 64) + c0 / 64 + wm;
+    word = r < rows ? a.bits[at] : 0;
+    mine = word & (0x0F0F0F0F0F0F0F0Full << (4 * kh));
+  }
+  // fn(column - 4 kh in the accumulator's order, place in qu) for each of them
+  template <class F>
+  __device__ __forceinline__ void each(const VocabArgs& a, int r, int kh, F fn) {
+    if (!mine) return;
+    const int64_t base = static_cast<int64_t>(r) * a.k + a.before[at];
+    while (mine) {
+      const int b = __ffsll(static_cast<unsigned long long>(mine)) - 1;
+      mine &= mine - 1;
+      fn(b - 4 * kh, base + __popcll(word & ((1ull << b) - 1)));
+    }
+  }
+};
+
 // Each row's maximum and sum of exponentials over a 256-column tile, and
 // cross entropy's target logit. Works in base 2: z log2(e).
-template <int PARTS>
+template <int PARTS, bool TEACHER>
 __global__ __launch_bounds__(4 * kThreads, 1) void stats_kernel(const VocabArgs a, int tile0) {
   __shared__ __attribute__((aligned(1024))) char smem[5 * kTileBytes];
   int mt, nt;
   if (!tile_of_block((a.vn + kTile - 1) / kTile, row_tiles(a), mt, nt)) return;
   const int c0 = mt * kTile, r0 = nt * kTile, rows = a.count[0];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave & 3, wn = wave >> 2, r32 = lane & 31, kh = lane >> 5;
+  LaneIds ids[2];
+  if constexpr (TEACHER) {
+#pragma unroll
+    for (int nb = 0; nb < 2; ++nb) ids[nb].load(a, r0 + 64 * wn + 32 * nb + r32, rows, c0, wm, kh);
+  }
   Acc<2, 2> acc;
   tile_product<PARTS, false, false>(
       table_operand(a, false, c0, 0),
       rows_operand(a.Xp + static_cast<int64_t>(r0) * a.ldx, a.ldx,
                    static_cast<int64_t>(a.np) * a.ldx, kTile, a.ldx),
       a.ldx / kStepK, smem, acc);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave & 3, wn = wave >> 2, r32 = lane & 31, kh = lane >> 5;
   const int left = a.vn - c0 - 64 * wm - 4 * kh;  // columns from the lane's first
   const float z2 = a.zscale * kLog2e;
   float m[2], s[2];
@@ -480,18 +590,21 @@ __global__ __launch_bounds__(4 * kThreads, 1) void stats_kernel(const VocabArgs 
         if (32 * mb + 8 * (i >> 2) + (i & 3) < left) s[nb] += exp2_(acc.v[mb][nb][i] - ref);
     s[nb] += __shfl_xor(s[nb], 32, 64);
   }
-  if (!a.t) {
 #pragma unroll
-    for (int nb = 0; nb < 2; ++nb) {
-      const int r = r0 + 64 * wn + 32 * nb + r32;
+  for (int nb = 0; nb < 2; ++nb) {
+    const int r = r0 + 64 * wn + 32 * nb + r32;
+    auto logit = [&](int at, float* to) {
+#pragma unroll
+      for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (at == 32 * mb + 8 * (i >> 2) + (i & 3)) *to = acc.v[mb][nb][i] * kLn2;
+    };
+    if constexpr (TEACHER) {
+      ids[nb].each(a, r, kh, [&](int at, int64_t place) { logit(at, a.zt + place); });
+    } else {
       const int64_t at = r < rows ? a.ids[a.row[r]] - a.v0 - c0 - 64 * wm - 4 * kh : -1;
-      if (at >= 0 && at < 64) {
-#pragma unroll
-        for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (at == 32 * mb + 8 * (i >> 2) + (i & 3)) a.zt[r] = acc.v[mb][nb][i] * kLn2;
-      }
+      if (at >= 0 && at < 64) logit(static_cast<int>(at), a.zt + r);
     }
   }
   // the four waves that share a row
@@ -559,24 +672,29 @@ __device__ __forceinline__ void write_tile(char* smem, bf16* dst, int64_t ld, in
   }
 }
 
-// One tile of D for the piece: dloss_n c tau (exp(z - lse_n) - [target]),
-// zero beyond the piece and the packed rows. (Distillation subtracts its
-// target weights afterwards.) One rounding to bf16: D enters two products
-// whose other operand is bf16; with fp32 D is kept in three parts.
-template <int PARTS>
+// One tile of D for the piece: dloss_n c tau (exp(z - lse_n) - q), zero beyond
+// the piece and the packed rows. One rounding to bf16, after the target's
+// weight is subtracted: D enters two products whose other operand is bf16;
+// with fp32 D is kept in three parts.
+template <int PARTS, bool TEACHER>
 __global__ __launch_bounds__(4 * kThreads, 1) void grad_logits_kernel(const VocabArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[5 * kTileBytes];
   int mt, nt;
   if (!tile_of_block((a.vn + kTile - 1) / kTile, row_tiles(a), mt, nt)) return;
   const int c0 = mt * kTile, r0 = nt * kTile, rows = a.count[0];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave & 3, wn = wave >> 2, r32 = lane & 31, kh = lane >> 5;
+  LaneIds ids[2];
+  if constexpr (TEACHER) {
+#pragma unroll
+    for (int nb = 0; nb < 2; ++nb) ids[nb].load(a, r0 + 64 * wn + 32 * nb + r32, rows, c0, wm, kh);
+  }
   Acc<2, 2> acc;
   tile_product<PARTS, false, false>(
       table_operand(a, false, c0, 0),
       rows_operand(a.Xp + static_cast<int64_t>(r0) * a.ldx, a.ldx,
                    static_cast<int64_t>(a.np) * a.ldx, kTile, a.ldx),
       a.ldx / kStepK, smem, acc);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave & 3, wn = wave >> 2, r32 = lane & 31, kh = lane >> 5;
   const int left = a.vn - c0 - 64 * wm - 4 * kh;
   const float z2 = a.zscale * kLog2e;
 #pragma unroll
@@ -586,16 +704,25 @@ __global__ __launch_bounds__(4 * kThreads, 1) void grad_logits_kernel(const Voca
     const int n = in ? a.row[r] : 0;
     const float g = in ? a.dloss[n] * a.dscale : 0.0f;
     const float lse2 = in ? a.lse[n] * kLog2e : 0.0f;
-    const int64_t at = in && !a.t ? a.ids[n] - a.v0 - c0 - 64 * wm - 4 * kh : -1;
+    const int64_t at = in && !TEACHER ? a.ids[n] - a.v0 - c0 - 64 * wm - 4 * kh : -1;
 #pragma unroll
     for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int c = 32 * mb + 8 * (i >> 2) + (i & 3);
         float p = exp2_(fmaf(acc.v[mb][nb][i], z2, -lse2));
-        if (at == c) p -= 1.0f;
+        if (!TEACHER && at == c) p -= 1.0f;
         acc.v[mb][nb][i] = in && c < left ? g * p : 0.0f;
       }
+    if constexpr (TEACHER)
+      ids[nb].each(a, r, kh, [&](int at, int64_t place) {
+        const float gq = g * a.qu[place];
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (at == 32 * mb + 8 * (i >> 2) + (i & 3)) acc.v[mb][nb][i] -= gq;
+      });
   }
   bf16* dst = a.D + static_cast<int64_t>(r0) * a.ldd + c0;
   if constexpr (PARTS == 1) {
@@ -695,25 +822,6 @@ __global__ __launch_bounds__(4 * kThreads, 1) void de_kernel(const VocabArgs a, 
   }
 }
 
-// Distillation: logits of the teacher's entries, one wave per packed row.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void target_logits_kernel(const VocabArgs a) {
-  const int i = blockIdx.x;
-  if (i >= a.count[0]) return;
-  const int lane = threadIdx.x & 63;
-  const int64_t n = a.row[i];
-  const T* x = static_cast<const T*>(a.X) + n * a.d;
-  for (int j = threadIdx.x >> 6; j < a.k; j += 4) {
-    const int64_t id = a.ids[n * a.k + j];
-    if (id < 0 || id >= a.V) continue;
-    const T* e = static_cast<const T*>(a.E) + id * a.d;
-    float z = 0.0f;
-    for (int c = lane; c < a.d; c += 64) z = fmaf(to_float(x[c]), to_float(e[c]), z);
-    z = wave_sum(z);
-    if (lane == 0) a.zt[static_cast<int64_t>(i) * a.k + j] = z * a.zscale;
-  }
-}
-
 // lse and loss of every row from its tile partials: one wave per row.
 __global__ __launch_bounds__(kThreads) void lse_kernel(const VocabArgs a, int tiles) {
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
@@ -737,37 +845,14 @@ __global__ __launch_bounds__(kThreads) void lse_kernel(const VocabArgs a, int ti
   const float lse = kLn2 * m + logf(s);
   float qz = 0.0f;
   if (a.t) {
-    for (int j = lane; j < a.k; j += 64) {
-      const float q = a.q[n * a.k + j];
-      const int64_t id = a.ids[n * a.k + j];
-      if (id >= 0 && id < a.V && q != 0.0f) qz = fmaf(q, a.zt[static_cast<int64_t>(i) * a.k + j] - lse, qz);
-    }
+    const int64_t at = static_cast<int64_t>(i) * a.k;
+    for (int j = lane; j < a.nu[i]; j += 64) qz = fmaf(a.qu[at + j], a.zt[at + j] - lse, qz);
     qz = wave_sum(qz);
   }
   if (lane == 0) {
     a.lse[n] = lse;
     a.loss[n] = a.t ? a.tau * a.tau * (a.ent[n] - qz) : lse - a.zt[i];
   }
-}
-
-// Distillation: the entries of D in the teacher's columns, from their logits
-// in fp32: g (p - sum of q over the row's entries with this id). Entries that
-// name the same id write the same value.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void teacher_entries_kernel(const VocabArgs a) {
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t i = at / a.k;
-  if (i >= a.count[0]) return;
-  const int64_t n = a.row[i];
-  const int64_t* ids = a.ids + n * a.k;
-  const int64_t id = ids[at - i * a.k];
-  if (id < a.v0 || id >= a.v0 + a.vn) return;
-  float q = 0.0f;
-  for (int j = 0; j < a.k; ++j)
-    if (ids[j] == id) q += a.q[n * a.k + j];
-  const float p = expf(a.zt[at] - a.lse[n]);
-  store_parts<kParts<T>>(a.D + i * a.ldd + (id - a.v0), static_cast<int64_t>(a.np) * a.ldd,
-                         a.dloss[n] * a.dscale * (p - q));
 }
 
 // dX[n] = the row's sums over the splits, rounded once; zero without target.
@@ -831,8 +916,8 @@ constexpr int64_t kPieceBytes = 512ll << 20;
 struct VocabPlan {
   int64_t ldx = 0, np = 0, piece = 0;
   int32_t splits = 1;
-  size_t off_flag, off_count, off_row, off_inv, off_q, off_ent, off_zt, off_Xp, off_Ep, off_part,
-      off_D, off_dX, total;
+  size_t off_flag, off_count, off_row, off_inv, off_q, off_ent, off_zt, off_qu, off_nu, off_bits,
+      off_before, off_Xp, off_Ep, off_part, off_D, off_dX, total;
 };
 
 VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, bool distill, bool grad) {
@@ -844,6 +929,7 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   // needed (fp32, rows that are not whole 16 bytes, or an unaligned table)
   p.piece = kPieceBytes / (p.ldx * 2 * parts);
   if (grad) p.piece = std::min(p.piece, kPieceBytes / (p.np * 2 * parts));
+  if (distill) p.piece = std::min<int64_t>({p.piece, kPieceBytes / (N * 10) * 64, 64 * kMaxWords});
   p.piece = std::min(round_up(V, kPad), std::max<int64_t>(kPad, p.piece / kPad * kPad));
   // dX has few tiles when rows are few: the sum over the vocabulary is then
   // split so that the blocks fill the chip's 256 CUs, each with at least
@@ -864,6 +950,10 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   p.off_q = take(distill ? N * k * 4 : 0);
   p.off_ent = take(distill ? N * 4 : 0);
   p.off_zt = take(N * k * 4);
+  p.off_qu = take(distill ? N * k * 4 : 0);
+  p.off_nu = take(distill ? N * 4 : 0);
+  p.off_bits = take(distill ? N * (p.piece / 64) * 8 : 0);
+  p.off_before = take(distill ? N * (p.piece / 64) * 2 : 0);
   p.off_Xp = take(parts * p.np * p.ldx * 2);
   p.off_Ep = take(parts * p.piece * p.ldx * 2);
   p.off_part = take(grad ? 0 : ceil_div(V, kTile) * p.np * 8);
@@ -895,6 +985,10 @@ VocabArgs make_args(const VocabCall& c, const VocabPlan& p, char* ws) {
   a.q = reinterpret_cast<float*>(ws + p.off_q);
   a.ent = reinterpret_cast<float*>(ws + p.off_ent);
   a.zt = reinterpret_cast<float*>(ws + p.off_zt);
+  a.qu = reinterpret_cast<float*>(ws + p.off_qu);
+  a.nu = reinterpret_cast<int32_t*>(ws + p.off_nu);
+  a.bits = reinterpret_cast<uint64_t*>(ws + p.off_bits);
+  a.before = reinterpret_cast<uint16_t*>(ws + p.off_before);
   a.Xp = reinterpret_cast<bf16*>(ws + p.off_Xp);
   a.Ep = c.dtype == DPG_FP32 || c.d % 8 != 0 || !aligned(c.E, 16)
              ? reinterpret_cast<bf16*>(ws + p.off_Ep) : nullptr;
@@ -910,8 +1004,7 @@ unsigned blocks_of(int64_t n, int64_t per) { return static_cast<unsigned>(ceil_d
 // grid of tile_of_block for mt x nt tiles
 dim3 tile_grid(int64_t mt, int64_t nt) { return dim3(static_cast<unsigned>(round_up(mt * nt, 8))); }
 
-// Target weights, the packed rows and their X; with distillation also the
-// logits of the teacher's entries.
+// Target weights, the packed rows and their X.
 template <typename T>
 int prepare_rows(const VocabArgs& a, hipStream_t s) {
   const dim3 b(kThreads);
@@ -919,11 +1012,11 @@ int prepare_rows(const VocabArgs& a, hipStream_t s) {
   else hipLaunchKernelGGL(ce_flag_kernel, dim3(blocks_of(a.N, kThreads)), b, 0, s, a);
   hipLaunchKernelGGL(rows_kernel, dim3(1), dim3(kRowThreads), 0, s, a);
   hipLaunchKernelGGL(pack_rows_kernel<T>, dim3(static_cast<unsigned>(a.np)), b, 0, s, a);
-  if (a.t) hipLaunchKernelGGL(target_logits_kernel<T>, dim3(static_cast<unsigned>(a.N)), b, 0, s, a);
   return check_launch("vocab rows");
 }
 
-// fn for every piece of the vocabulary, its table packed first where needed.
+// fn for every piece of the vocabulary, its table packed first where needed,
+// its teacher ids found.
 template <typename T, class F>
 void for_pieces(VocabArgs& a, hipStream_t s, F fn) {
   for (int64_t v0 = 0; v0 < a.V; v0 += a.ldd) {
@@ -932,6 +1025,8 @@ void for_pieces(VocabArgs& a, hipStream_t s, F fn) {
     if (a.Ep)
       hipLaunchKernelGGL(pack_table_kernel<T>, dim3(static_cast<unsigned>(round_up(a.vn, kPad))),
                          dim3(kThreads), 0, s, a);
+    if (a.t)
+      hipLaunchKernelGGL(teacher_ids_kernel, dim3(static_cast<unsigned>(a.N)), dim3(kThreads), 0, s, a);
     fn();
   }
 }
@@ -940,8 +1035,10 @@ template <typename T>
 int run_loss(VocabArgs a, hipStream_t s) {
   if (const int st = prepare_rows<T>(a, s)) return st;
   for_pieces<T>(a, s, [&] {
-    hipLaunchKernelGGL(stats_kernel<kParts<T>>, tile_grid(ceil_div(a.vn, kTile), a.np / kTile),
-                       dim3(4 * kThreads), 0, s, a, a.v0 / kTile);
+    const dim3 g = tile_grid(ceil_div(a.vn, kTile), a.np / kTile), b(4 * kThreads);
+    const int tile0 = a.v0 / kTile;
+    if (a.t) hipLaunchKernelGGL((stats_kernel<kParts<T>, true>), g, b, 0, s, a, tile0);
+    else hipLaunchKernelGGL((stats_kernel<kParts<T>, false>), g, b, 0, s, a, tile0);
   });
   hipLaunchKernelGGL(lse_kernel, dim3(blocks_of(a.N, 4)), dim3(kThreads), 0, s, a,
                      static_cast<int>(ceil_div(a.V, kTile)));
@@ -955,10 +1052,8 @@ int run_grad(VocabArgs a, void* dX, void* dE, hipStream_t s) {
   const int64_t rt = a.np / kTile, ct = ceil_div(a.ldx, kTile);
   for_pieces<T>(a, s, [&] {
     const int64_t vt = ceil_div(a.vn, kTile);
-    hipLaunchKernelGGL(grad_logits_kernel<kParts<T>>, tile_grid(vt, rt), b, 0, s, a);
-    if (a.t)
-      hipLaunchKernelGGL(teacher_entries_kernel<T>, dim3(blocks_of(a.N * a.k, kThreads)),
-                         dim3(kThreads), 0, s, a);
+    if (a.t) hipLaunchKernelGGL((grad_logits_kernel<kParts<T>, true>), tile_grid(vt, rt), b, 0, s, a);
+    else hipLaunchKernelGGL((grad_logits_kernel<kParts<T>, false>), tile_grid(vt, rt), b, 0, s, a);
     if (dX) hipLaunchKernelGGL(dx_kernel<kParts<T>>, tile_grid(rt, ct * a.splits), b, 0, s, a);
     if (dE) hipLaunchKernelGGL(de_kernel<T>, tile_grid(vt, ct), b, 0, s, a, static_cast<T*>(dE));
   });
