@@ -321,6 +321,13 @@ template <int N> __device__ __forceinline__ void wait_vm_n() {
 
 constexpr int kTile = 256, kStepK = 64;
 constexpr int kTileBytes = kTile * kStepK * 2;
+// Blocks of 32 x 32 in a wave's part of the tile, and the waves' layout.
+constexpr int kMB = 4, kNB = 2;
+constexpr int kWaveM = 32 * kMB, kWaveN = 32 * kNB;
+constexpr int kWavesM = kTile / kWaveM, kWavesN = kTile / kWaveN, kWaves = kWavesM * kWavesN;
+constexpr int kTileThreads = 64 * kWaves;
+constexpr int kCopies = kTileBytes / 1024 / kWaves;  // a wave's, per step and operand
+typedef Acc<kMB, kNB> TileAcc;
 
 struct Operand {
   const bf16* base;     // first row of the tile (rows) or of K (k-major)
@@ -330,50 +337,51 @@ struct Operand {
   int cols;             // rows: elements of K in a row; k-major: columns from base
 };
 
-// The direct copies of one operand: two of 1 KiB a wave and step.
+// The direct copies of one operand: kCopies of 1 KiB a wave and step.
 template <bool KMAJOR>
 struct Copier {
   const char* base;
-  uint32_t ldb;       // row stride, bytes
-  uint32_t off[2];    // rows: row offset; k-major: K row of the lane
-  uint32_t chunk[2];  // byte offset of the lane's 16 bytes within the row
-  uint32_t last;      // rows: last chunk of a row; k-major: last K row
+  uint32_t ldb;           // row stride, bytes
+  uint32_t off[kCopies];  // rows: row offset; k-major: K row of the lane
+  uint32_t chunk;         // byte offset of the lane's 16 bytes within the row
+  uint32_t last;          // rows: last chunk of a row; k-major: last K row
   int64_t part_bytes;
 
   __device__ __forceinline__ void init(const Operand& o, int lane, int wave) {
+    static_assert(kWaves % 2 == 0, "a wave's copies start at rows of one parity");
     base = reinterpret_cast<const char*>(o.base);
     ldb = static_cast<uint32_t>(o.ld) * 2u;
     part_bytes = o.part_stride * 2;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int g = q * 16 + wave;
-      if constexpr (!KMAJOR) {
-        const int r = g * 8 + (lane >> 3);
-        off[q] = static_cast<uint32_t>(min(r, o.rows - 1)) * ldb;
-        chunk[q] = static_cast<uint32_t>((lane & 7) ^ ((r >> 1) & 7)) * 16u;
-      } else {
-        const int k = g * 2 + (lane >> 5);
-        off[q] = static_cast<uint32_t>(k);
-        chunk[q] = static_cast<uint32_t>(min((lane & 31) ^ (4 * (k & 3)), o.cols / 8 - 1)) * 16u;
-      }
+    for (int q = 0; q < kCopies; ++q) {
+      const int g = q * kWaves + wave;
+      if constexpr (!KMAJOR) off[q] = static_cast<uint32_t>(min(g * 8 + (lane >> 3), o.rows - 1)) * ldb;
+      else off[q] = static_cast<uint32_t>(g * 2 + (lane >> 5));
     }
+    if constexpr (!KMAJOR)
+      chunk = static_cast<uint32_t>((lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7)) * 16u;
+    else
+      chunk = static_cast<uint32_t>(
+          min((lane & 31) ^ (4 * ((2 * (wave & 1) + (lane >> 5)) & 3)), o.cols / 8 - 1)) * 16u;
     last = KMAJOR ? static_cast<uint32_t>(o.rows - 1) : static_cast<uint32_t>(o.cols) * 2u - 16u;
   }
-  // step ks of K (kStepK columns or rows from ks * kStepK) of part `part`
-  __device__ __forceinline__ void issue(int part, int ks, char* stage, int wave) const {
+  // copies q0 .. q1 - 1 of step ks of K (kStepK columns or rows) of part `part`
+  __device__ __forceinline__ void issue(int part, int ks, char* stage, int wave, int q0, int q1) const {
     const char* p = base + part * part_bytes;
     if constexpr (!KMAJOR) {
       const uint32_t kb = static_cast<uint32_t>(ks) * (kStepK * 2);
       const __amdgpu_buffer_rsrc_t rs = tile_rsrc(p);
+      const uint32_t c = min(kb + chunk, last);
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-        copy_to_lds(rs, off[q] + min(kb + chunk[q], last), 0, stage + (q * 16 + wave) * 1024);
+      for (int q = 0; q < kCopies; ++q)
+        if (q >= q0 && q < q1) copy_to_lds(rs, off[q] + c, 0, stage + (q * kWaves + wave) * 1024);
     } else {
       const __amdgpu_buffer_rsrc_t rs = tile_rsrc(p + static_cast<int64_t>(ks) * kStepK * ldb);
       const uint32_t lim = last - static_cast<uint32_t>(ks) * kStepK;
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-        copy_to_lds(rs, min(off[q], lim) * ldb + chunk[q], 0, stage + (q * 16 + wave) * 1024);
+      for (int q = 0; q < kCopies; ++q)
+        if (q >= q0 && q < q1)
+          copy_to_lds(rs, min(off[q], lim) * ldb + chunk, 0, stage + (q * kWaves + wave) * 1024);
     }
   }
 };
@@ -392,11 +400,12 @@ __device__ __forceinline__ bf16x8 tile_frag(const char* tile, int kk, int c0, in
 // acc = A B^T over K steps [0, n_k) of every combination of parts.
 template <int PARTS, bool KA, bool KB>
 __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& ob, int n_k,
-                                             char* smem, Acc<2, 2>& acc) {
+                                             char* smem, TileAcc& acc) {
   typedef Combos<PARTS> C;
-  constexpr int KK = kStepK / 16;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave & 3, wn = wave >> 2;
+  constexpr int KK = kStepK / 16, M = kMB * kNB, F = kMB + kNB;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave % kWavesM, wn = wave / kWavesM;
   Copier<KA> ca;
   Copier<KB> cb;
   ca.init(oa, lane, wave);
@@ -404,71 +413,91 @@ __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& o
   const int n_steps = n_k * C::n;
   char* const sA = smem;
   char* const sB = smem + 3 * kTileBytes;
-  auto issue_a = [&](int s, int stage) {
+  auto issue_a = [&](int s, int stage, int q0, int q1) {
     const int c = PARTS == 1 ? 0 : s / n_k;
-    ca.issue(C::a(c), s - c * n_k, sA + stage * kTileBytes, wave);
+    ca.issue(C::a(c), s - c * n_k, sA + stage * kTileBytes, wave, q0, q1);
   };
-  auto issue_b = [&](int s, int stage) {
+  auto issue_b = [&](int s, int stage, int q0, int q1) {
     const int c = PARTS == 1 ? 0 : s / n_k;
-    cb.issue(C::b(c), s - c * n_k, sB + stage * kTileBytes, wave);
+    cb.issue(C::b(c), s - c * n_k, sB + stage * kTileBytes, wave, q0, q1);
   };
-  bf16x8 fa[2][2], fb[2][2];
-  auto read_frags = [&](int sta, int stb, int kk, int to) {
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-      fa[to][m] = tile_frag<KA>(sA + sta * kTileBytes, kk, 64 * wm + 32 * m, lane);
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-      fb[to][n] = tile_frag<KB>(sB + stb * kTileBytes, kk, 64 * wn + 32 * n, lane);
+  bf16x8 fa[2][kMB], fb[2][kNB];
+  // fragment f (A's first, then B's) of sub-step kk
+  auto read_frag = [&](int f, int sta, int stb, int kk, int to) {
+    if (f < kMB)
+      fa[to][f] = tile_frag<KA>(sA + sta * kTileBytes, kk, kWaveM * wm + 32 * f, lane);
+    else
+      fb[to][f - kMB] = tile_frag<KB>(sB + stb * kTileBytes, kk, kWaveN * wn + 32 * (f - kMB), lane);
   };
-  auto mma = [&](int f, int q0, int q1) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (q >= q0 && q < q1)
-        acc.v[q >> 1][q & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            fa[f][q >> 1], fb[f][q & 1], acc.v[q >> 1][q & 1], 0, 0, 0);
+  auto mma = [&](int f, int q) {
+    acc.v[q / kNB][q % kNB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+        fa[f][q / kNB], fb[f][q % kNB], acc.v[q / kNB][q % kNB], 0, 0, 0);
   };
   acc.zero();
   if (n_steps <= 0) return;
   // Copies in issue order: A and B of step 0; B of step 1, A of steps 1 and
-  // 2; then at the barrier ending step s, B of step s + 2 and A of step s + 3.
-  // Before that barrier step s + 1's copies are complete once at most the
-  // two of A's step s + 2 are in flight: loads return in order.
-  issue_a(0, 0);
-  issue_b(0, 0);
+  // 2; then after the barrier in the last sub-step of step s, B of step s + 2
+  // and A of step s + 3, spread over that sub-step and the next three. Before
+  // that barrier step s + 1's copies are complete once at most those of A's
+  // step s + 2 are in flight: loads return in order.
+  issue_a(0, 0, 0, kCopies);
+  issue_b(0, 0, 0, kCopies);
   wait_vm_n<0>();
   lds_barrier();
   if (n_steps > 1) {
-    issue_b(1, 1);
-    issue_a(1, 1);
+    issue_b(1, 1, 0, kCopies);
+    issue_a(1, 1, 0, kCopies);
   }
-  if (n_steps > 2) issue_a(2, 2);
-  read_frags(0, 0, 0, 0);
+  if (n_steps > 2) issue_a(2, 2, 0, kCopies);
+#pragma unroll
+  for (int f = 0; f < F; ++f) read_frag(f, 0, 0, 0, 0);
   int sta = 0;
+  // copies of sub-step kk (counted from the one with the barrier) of `s`
+  constexpr int kPer = kCopies;
+  auto refill = [&](int s, int sta_s, int slot, int i) {
+    const int q = slot * kPer + i;  // of 2 kCopies: B's, then A's
+    if (q < kCopies) {
+      if (s + 2 < n_steps) issue_b(s + 2, s & 1, q, q + 1);
+    } else {
+      if (s + 3 < n_steps) issue_a(s + 3, sta_s, q - kCopies, q - kCopies + 1);
+    }
+  };
+  int prev_sta = 0;
   for (int s = 0; s < n_steps; ++s) {
     const int next = sta == 2 ? 0 : sta + 1;
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
       const int cur = kk & 1, nxt = cur ^ 1;
-      const int first = kk + 1 < KK ? 1 : 2;
-      __builtin_amdgcn_sched_barrier(0);
-      mma(cur, 0, first);
-      __builtin_amdgcn_sched_barrier(0);
-      if (kk + 1 < KK) {
-        read_frags(sta, s & 1, kk + 1, nxt);
-      } else if (s + 1 < n_steps) {
-        wait_lgkm0();  // this wave's reads of step s are complete
-        if (s + 2 < n_steps) wait_vm_n<2>();
-        else wait_vm_n<0>();
-        lds_barrier();
-        if (s + 2 < n_steps) issue_b(s + 2, s & 1);
-        if (s + 3 < n_steps) issue_a(s + 3, sta);
-        read_frags(next, (s + 1) & 1, 0, nxt);
+      const bool last = kk + 1 == KK;
+#pragma unroll
+      for (int q = 0; q < M; ++q) {
+        __builtin_amdgcn_sched_barrier(0);
+        mma(cur, q);
+        __builtin_amdgcn_sched_barrier(0);
+        if (last && q == 0) {
+          if (s + 1 < n_steps) {
+            wait_lgkm0();  // this wave's reads of step s are complete
+            if (s + 2 < n_steps) wait_vm_n<kCopies>();
+            else wait_vm_n<0>();
+            lds_barrier();
+          }
+        }
+        // the next sub-step's fragments, F over the M products
+        if (!last || s + 1 < n_steps) {
+#pragma unroll
+          for (int f = q * F / M; f < (q + 1) * F / M; ++f)
+            if (last) read_frag(f, next, (s + 1) & 1, 0, nxt);
+            else read_frag(f, sta, s & 1, kk + 1, nxt);
+        }
+        // the refills
+#pragma unroll
+        for (int i = q * kPer / M; i < (q + 1) * kPer / M; ++i) {
+          if (last) refill(s, sta, 0, i);
+          else if (s > 0 && (kk + 1) * kPer < 2 * kCopies) refill(s - 1, prev_sta, kk + 1, i);
+        }
       }
-      __builtin_amdgcn_sched_barrier(0);
-      mma(cur, first, 4);
-      __builtin_amdgcn_sched_barrier(0);
     }
+    prev_sta = sta;
     sta = next;
   }
 }
@@ -521,13 +550,13 @@ __device__ __forceinline__ Operand rows_operand(const bf16* base, int64_t ld, in
 }
 
 // The teacher's ids among the columns of a lane's accumulator for one packed
-// row: columns 64 wm .. of the tile that begins at column c0 of the piece, in
-// the lane's half (4 kh .. 4 kh + 3 of every eight).
+// row: the 64 columns from column c0 of the piece, of them the lane's half (4 kh
+// .. 4 kh + 3 of every eight).
 struct LaneIds {
   uint64_t word, mine;
   int64_t at;  // the word's index
-  __device__ __forceinline__ void load(const VocabArgs& a, int r, int rows, int c0, int wm, int kh) {
-    at = static_cast<int64_t>(r) * (a.ldd / 64) + c0 / 64 + wm;
+  __device__ __forceinline__ void load(const VocabArgs& a, int r, int rows, int c0, int kh) {
+    at = static_cast<int64_t>(r) * (a.ldd / 64) + c0 / 64;
     word = r < rows ? a.bits[at] : 0;
     mine = word & (0x0F0F0F0F0F0F0F0Full << (4 * kh));
   }
@@ -547,32 +576,35 @@ struct LaneIds {
 // Each row's maximum and sum of exponentials over a 256-column tile, and
 // cross entropy's target logit. Works in base 2: z log2(e).
 template <int PARTS, bool TEACHER>
-__global__ __launch_bounds__(4 * kThreads, 1) void stats_kernel(const VocabArgs a, int tile0) {
+__global__ __launch_bounds__(kTileThreads, 1) void stats_kernel(const VocabArgs a, int tile0) {
   __shared__ __attribute__((aligned(1024))) char smem[5 * kTileBytes];
   int mt, nt;
   if (!tile_of_block((a.vn + kTile - 1) / kTile, row_tiles(a), mt, nt)) return;
   const int c0 = mt * kTile, r0 = nt * kTile, rows = a.count[0];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave & 3, wn = wave >> 2, r32 = lane & 31, kh = lane >> 5;
-  LaneIds ids[2];
+  const int wm = wave % kWavesM, wn = wave / kWavesM, r32 = lane & 31, kh = lane >> 5;
+  LaneIds ids[kNB][kMB / 2];
   if constexpr (TEACHER) {
 #pragma unroll
-    for (int nb = 0; nb < 2; ++nb) ids[nb].load(a, r0 + 64 * wn + 32 * nb + r32, rows, c0, wm, kh);
+    for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+      for (int h = 0; h < kMB / 2; ++h)
+        ids[nb][h].load(a, r0 + kWaveN * wn + 32 * nb + r32, rows, c0 + kWaveM * wm + 64 * h, kh);
   }
-  Acc<2, 2> acc;
+  TileAcc acc;
   tile_product<PARTS, false, false>(
       table_operand(a, false, c0, 0),
       rows_operand(a.Xp + static_cast<int64_t>(r0) * a.ldx, a.ldx,
                    static_cast<int64_t>(a.np) * a.ldx, kTile, a.ldx),
       a.ldx / kStepK, smem, acc);
-  const int left = a.vn - c0 - 64 * wm - 4 * kh;  // columns from the lane's first
+  const int left = a.vn - c0 - kWaveM * wm - 4 * kh;  // columns from the lane's first
   const float z2 = a.zscale * kLog2e;
-  float m[2], s[2];
+  float m[kNB], s[kNB];
 #pragma unroll
-  for (int nb = 0; nb < 2; ++nb) {
+  for (int nb = 0; nb < kNB; ++nb) {
     m[nb] = -INFINITY;
 #pragma unroll
-    for (int mb = 0; mb < 2; ++mb)
+    for (int mb = 0; mb < kMB; ++mb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float z = acc.v[mb][nb][i] * z2;
@@ -584,46 +616,51 @@ __global__ __launch_bounds__(4 * kThreads, 1) void stats_kernel(const VocabArgs 
     // (a wave whose columns all lie past the end has no maximum)
     const float ref = m[nb] == -INFINITY ? 0.0f : m[nb];
 #pragma unroll
-    for (int mb = 0; mb < 2; ++mb)
+    for (int mb = 0; mb < kMB; ++mb)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         if (32 * mb + 8 * (i >> 2) + (i & 3) < left) s[nb] += exp2_(acc.v[mb][nb][i] - ref);
     s[nb] += __shfl_xor(s[nb], 32, 64);
   }
 #pragma unroll
-  for (int nb = 0; nb < 2; ++nb) {
-    const int r = r0 + 64 * wn + 32 * nb + r32;
+  for (int nb = 0; nb < kNB; ++nb) {
+    const int r = r0 + kWaveN * wn + 32 * nb + r32;
     auto logit = [&](int at, float* to) {
 #pragma unroll
-      for (int mb = 0; mb < 2; ++mb)
+      for (int mb = 0; mb < kMB; ++mb)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (at == 32 * mb + 8 * (i >> 2) + (i & 3)) *to = acc.v[mb][nb][i] * kLn2;
     };
     if constexpr (TEACHER) {
-      ids[nb].each(a, r, kh, [&](int at, int64_t place) { logit(at, a.zt + place); });
+#pragma unroll
+      for (int h = 0; h < kMB / 2; ++h)
+        ids[nb][h].each(a, r, kh, [&](int at, int64_t place) { logit(64 * h + at, a.zt + place); });
     } else {
-      const int64_t at = r < rows ? a.ids[a.row[r]] - a.v0 - c0 - 64 * wm - 4 * kh : -1;
-      if (at >= 0 && at < 64) logit(static_cast<int>(at), a.zt + r);
+      const int64_t at = r < rows ? a.ids[a.row[r]] - a.v0 - c0 - kWaveM * wm - 4 * kh : -1;
+      if (at >= 0 && at < kWaveM) logit(static_cast<int>(at), a.zt + r);
     }
   }
-  // the four waves that share a row
+  // the waves that share a row
   float2* red = reinterpret_cast<float2*>(smem);
   __syncthreads();
   if (kh == 0)
 #pragma unroll
-    for (int nb = 0; nb < 2; ++nb)
-      red[wm * kTile + 64 * wn + 32 * nb + r32] = make_float2(m[nb], s[nb]);
+    for (int nb = 0; nb < kNB; ++nb)
+      red[wm * kTile + kWaveN * wn + 32 * nb + r32] = make_float2(m[nb], s[nb]);
   __syncthreads();
   if (tid < kTile) {
-    float2 p[4];
+    float2 p[kWavesM];
+    float mm = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) p[w] = red[w * kTile + tid];
-    const float mm = fmaxf(fmaxf(p[0].x, p[1].x), fmaxf(p[2].x, p[3].x));
+    for (int w = 0; w < kWavesM; ++w) {
+      p[w] = red[w * kTile + tid];
+      mm = fmaxf(mm, p[w].x);
+    }
     const float ref = mm == -INFINITY ? 0.0f : mm;
     float ss = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) ss = fmaf(p[w].y, exp2_(p[w].x - ref), ss);
+    for (int w = 0; w < kWavesM; ++w) ss = fmaf(p[w].y, exp2_(p[w].x - ref), ss);
     a.part[static_cast<int64_t>(tile0 + mt) * a.np + r0 + tid] = make_float2(mm, ss);
   }
 }
@@ -638,26 +675,26 @@ template <class F>
 __device__ __forceinline__ void write_tile(char* smem, bf16* dst, int64_t ld, int n_rows, int n_cols,
                                            bool vec, F value) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave & 3, wn = wave >> 2, r32 = lane & 31, kh = lane >> 5;
+  const int wm = wave % kWavesM, wn = wave / kWavesM, r32 = lane & 31, kh = lane >> 5;
   __syncthreads();
 #pragma unroll
-  for (int nb = 0; nb < 2; ++nb) {
-    const int r = 64 * wn + 32 * nb + r32;
+  for (int nb = 0; nb < kNB; ++nb) {
+    const int r = kWaveN * wn + 32 * nb + r32;
 #pragma unroll
-    for (int mb = 0; mb < 2; ++mb)
+    for (int mb = 0; mb < kMB; ++mb)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         Vec4<bf16>::type v;
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] = value(nb, mb, 4 * j + q);
-        const int c = 8 * wm + 4 * mb + j;
+        const int c = kWaveM / 8 * wm + 4 * mb + j;
         *reinterpret_cast<Vec4<bf16>::type*>(smem + r * 512 + (c ^ r32) * 16 + kh * 8) = v;
       }
   }
   __syncthreads();
 #pragma unroll
-  for (int it = 0; it < 8; ++it) {
-    const int r = it * 32 + wave * 2 + kh, c = r32;
+  for (int it = 0; it < kTile / (2 * kWaves); ++it) {
+    const int r = (it * kWaves + wave) * 2 + kh, c = r32;
     const bf16x8 v = lds_read_b128(smem + r * 512 + (c ^ (r & 31)) * 16);
     if (r < n_rows && c * 8 < n_cols) {
       bf16* p = dst + static_cast<int64_t>(r) * ld + c * 8;
@@ -677,36 +714,39 @@ __device__ __forceinline__ void write_tile(char* smem, bf16* dst, int64_t ld, in
 // weight is subtracted: D enters two products whose other operand is bf16;
 // with fp32 D is kept in three parts.
 template <int PARTS, bool TEACHER>
-__global__ __launch_bounds__(4 * kThreads, 1) void grad_logits_kernel(const VocabArgs a) {
+__global__ __launch_bounds__(kTileThreads, 1) void grad_logits_kernel(const VocabArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[5 * kTileBytes];
   int mt, nt;
   if (!tile_of_block((a.vn + kTile - 1) / kTile, row_tiles(a), mt, nt)) return;
   const int c0 = mt * kTile, r0 = nt * kTile, rows = a.count[0];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave & 3, wn = wave >> 2, r32 = lane & 31, kh = lane >> 5;
-  LaneIds ids[2];
+  const int wm = wave % kWavesM, wn = wave / kWavesM, r32 = lane & 31, kh = lane >> 5;
+  LaneIds ids[kNB][kMB / 2];
   if constexpr (TEACHER) {
 #pragma unroll
-    for (int nb = 0; nb < 2; ++nb) ids[nb].load(a, r0 + 64 * wn + 32 * nb + r32, rows, c0, wm, kh);
+    for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+      for (int h = 0; h < kMB / 2; ++h)
+        ids[nb][h].load(a, r0 + kWaveN * wn + 32 * nb + r32, rows, c0 + kWaveM * wm + 64 * h, kh);
   }
-  Acc<2, 2> acc;
+  TileAcc acc;
   tile_product<PARTS, false, false>(
       table_operand(a, false, c0, 0),
       rows_operand(a.Xp + static_cast<int64_t>(r0) * a.ldx, a.ldx,
                    static_cast<int64_t>(a.np) * a.ldx, kTile, a.ldx),
       a.ldx / kStepK, smem, acc);
-  const int left = a.vn - c0 - 64 * wm - 4 * kh;
+  const int left = a.vn - c0 - kWaveM * wm - 4 * kh;
   const float z2 = a.zscale * kLog2e;
 #pragma unroll
-  for (int nb = 0; nb < 2; ++nb) {
-    const int r = r0 + 64 * wn + 32 * nb + r32;
+  for (int nb = 0; nb < kNB; ++nb) {
+    const int r = r0 + kWaveN * wn + 32 * nb + r32;
     const bool in = r < rows;
     const int n = in ? a.row[r] : 0;
     const float g = in ? a.dloss[n] * a.dscale : 0.0f;
     const float lse2 = in ? a.lse[n] * kLog2e : 0.0f;
-    const int64_t at = in && !TEACHER ? a.ids[n] - a.v0 - c0 - 64 * wm - 4 * kh : -1;
+    const int64_t at = in && !TEACHER ? a.ids[n] - a.v0 - c0 - kWaveM * wm - 4 * kh : -1;
 #pragma unroll
-    for (int mb = 0; mb < 2; ++mb)
+    for (int mb = 0; mb < kMB; ++mb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int c = 32 * mb + 8 * (i >> 2) + (i & 3);
@@ -714,15 +754,18 @@ __global__ __launch_bounds__(4 * kThreads, 1) void grad_logits_kernel(const Voca
         if (!TEACHER && at == c) p -= 1.0f;
         acc.v[mb][nb][i] = in && c < left ? g * p : 0.0f;
       }
-    if constexpr (TEACHER)
-      ids[nb].each(a, r, kh, [&](int at, int64_t place) {
-        const float gq = g * a.qu[place];
+    if constexpr (TEACHER) {
 #pragma unroll
-        for (int mb = 0; mb < 2; ++mb)
+      for (int h = 0; h < kMB / 2; ++h)
+        ids[nb][h].each(a, r, kh, [&](int at, int64_t place) {
+          const float gq = g * a.qu[place];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (at == 32 * mb + 8 * (i >> 2) + (i & 3)) acc.v[mb][nb][i] -= gq;
-      });
+          for (int mb = 2 * h; mb < 2 * h + 2; ++mb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (64 * h + at == 32 * mb + 8 * (i >> 2) + (i & 3)) acc.v[mb][nb][i] -= gq;
+        });
+    }
   }
   bf16* dst = a.D + static_cast<int64_t>(r0) * a.ldd + c0;
   if constexpr (PARTS == 1) {
@@ -742,7 +785,7 @@ __global__ __launch_bounds__(4 * kThreads, 1) void grad_logits_kernel(const Voca
 
 // dXacc[split] (+)= D E over the split's part of the piece.
 template <int PARTS>
-__global__ __launch_bounds__(4 * kThreads, 1) void dx_kernel(const VocabArgs a) {
+__global__ __launch_bounds__(kTileThreads, 1) void dx_kernel(const VocabArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[5 * kTileBytes];
   int mt, nt;
   const int ct = (a.ldx + kTile - 1) / kTile;
@@ -751,20 +794,20 @@ __global__ __launch_bounds__(4 * kThreads, 1) void dx_kernel(const VocabArgs a) 
   const int c0 = (nt - split * ct) * kTile, r0 = mt * kTile;
   const int steps = (a.vn + kStepK - 1) / kStepK, per = (steps + a.splits - 1) / a.splits;
   const int k0 = min(steps, split * per), k1 = min(steps, k0 + per);
-  Acc<2, 2> acc;
+  TileAcc acc;
   tile_product<PARTS, false, true>(
       rows_operand(a.D + static_cast<int64_t>(r0) * a.ldd + k0 * kStepK, a.ldd,
                    static_cast<int64_t>(a.np) * a.ldd, kTile, a.ldd - k0 * kStepK),
       table_operand(a, true, k0 * kStepK, c0), k1 - k0, smem, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave & 3, wn = wave >> 2, r32 = lane & 31, kh = lane >> 5;
-  float* dst = a.dXacc + (static_cast<int64_t>(split) * a.np + r0 + 64 * wm + 4 * kh) * a.ldx + c0 +
-               64 * wn + r32;
+  const int wm = wave % kWavesM, wn = wave / kWavesM, r32 = lane & 31, kh = lane >> 5;
+  float* dst = a.dXacc + (static_cast<int64_t>(split) * a.np + r0 + kWaveM * wm + 4 * kh) * a.ldx + c0 +
+               kWaveN * wn + r32;
 #pragma unroll
-  for (int nb = 0; nb < 2; ++nb) {
-    if (c0 + 64 * wn + 32 * nb >= a.ldx) continue;
+  for (int nb = 0; nb < kNB; ++nb) {
+    if (c0 + kWaveN * wn + 32 * nb >= a.ldx) continue;
 #pragma unroll
-    for (int mb = 0; mb < 2; ++mb)
+    for (int mb = 0; mb < kMB; ++mb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float* p = dst + static_cast<int64_t>(32 * mb + 8 * (i >> 2) + (i & 3)) * a.ldx + 32 * nb;
@@ -775,7 +818,7 @@ __global__ __launch_bounds__(4 * kThreads, 1) void dx_kernel(const VocabArgs a) 
 
 // The piece's rows of dE = D^T Xp, rounded once.
 template <typename T>
-__global__ __launch_bounds__(4 * kThreads, 1) void de_kernel(const VocabArgs a, T* dE) {
+__global__ __launch_bounds__(kTileThreads, 1) void de_kernel(const VocabArgs a, T* dE) {
   constexpr int PARTS = kParts<T>;
   __shared__ __attribute__((aligned(1024))) char smem[5 * kTileBytes];
   int mt, nt;
@@ -783,7 +826,7 @@ __global__ __launch_bounds__(4 * kThreads, 1) void de_kernel(const VocabArgs a, 
   // (bands of eight run over the vocabulary, the longer side)
   if (!tile_of_block((a.vn + kTile - 1) / kTile, ct, nt, mt)) return;
   const int c0 = mt * kTile, w0 = nt * kTile, rows = a.count[0];
-  Acc<2, 2> acc;
+  TileAcc acc;
   tile_product<PARTS, true, true>(
       rows_operand(a.Xp + c0, a.ldx, static_cast<int64_t>(a.np) * a.ldx, a.np, a.ldx - c0),
       rows_operand(a.D + w0, a.ldd, static_cast<int64_t>(a.np) * a.ldd, a.np, kTile),
@@ -795,17 +838,17 @@ __global__ __launch_bounds__(4 * kThreads, 1) void de_kernel(const VocabArgs a, 
                [&](int nb, int mb, int i) { return from_float<bf16>(acc.v[mb][nb][i]); });
   } else {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = wave & 3, wn = wave >> 2, r32 = lane & 31, kh = lane >> 5;
+    const int wm = wave % kWavesM, wn = wave / kWavesM, r32 = lane & 31, kh = lane >> 5;
     const bool vec = a.d % 4 == 0 && is_aligned(dE, 16);
 #pragma unroll
-    for (int nb = 0; nb < 2; ++nb) {
-      const int r = 64 * wn + 32 * nb + r32;
+    for (int nb = 0; nb < kNB; ++nb) {
+      const int r = kWaveN * wn + 32 * nb + r32;
       if (r >= n_rows) continue;
 #pragma unroll
-      for (int mb = 0; mb < 2; ++mb)
+      for (int mb = 0; mb < kMB; ++mb)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int c = 64 * wm + 32 * mb + 8 * j + 4 * kh;
+          const int c = kWaveM * wm + 32 * mb + 8 * j + 4 * kh;
           T* p = dst + static_cast<int64_t>(r) * a.d + c;
           f32x4 v;
 #pragma unroll
@@ -1035,7 +1078,7 @@ template <typename T>
 int run_loss(VocabArgs a, hipStream_t s) {
   if (const int st = prepare_rows<T>(a, s)) return st;
   for_pieces<T>(a, s, [&] {
-    const dim3 g = tile_grid(ceil_div(a.vn, kTile), a.np / kTile), b(4 * kThreads);
+    const dim3 g = tile_grid(ceil_div(a.vn, kTile), a.np / kTile), b(kTileThreads);
     const int tile0 = a.v0 / kTile;
     if (a.t) hipLaunchKernelGGL((stats_kernel<kParts<T>, true>), g, b, 0, s, a, tile0);
     else hipLaunchKernelGGL((stats_kernel<kParts<T>, false>), g, b, 0, s, a, tile0);
@@ -1048,7 +1091,7 @@ int run_loss(VocabArgs a, hipStream_t s) {
 template <typename T>
 int run_grad(VocabArgs a, void* dX, void* dE, hipStream_t s) {
   if (const int st = prepare_rows<T>(a, s)) return st;
-  const dim3 b(4 * kThreads);
+  const dim3 b(kTileThreads);
   const int64_t rt = a.np / kTile, ct = ceil_div(a.ldx, kTile);
   for_pieces<T>(a, s, [&] {
     const int64_t vt = ceil_div(a.vn, kTile);
