@@ -321,13 +321,23 @@ template <int N> __device__ __forceinline__ void wait_vm_n() {
 
 constexpr int kTile = 256, kStepK = 64;
 constexpr int kTileBytes = kTile * kStepK * 2;
-// Blocks of 32 x 32 in a wave's part of the tile, and the waves' layout.
-constexpr int kMB = 4, kNB = 2;
-constexpr int kWaveM = 32 * kMB, kWaveN = 32 * kNB;
+// Blocks of 16 x 16 in a wave's part of the tile, and the waves' layout.
+constexpr int kMB = 8, kNB = 4;
+constexpr int kWaveM = 16 * kMB, kWaveN = 16 * kNB;
 constexpr int kWavesM = kTile / kWaveM, kWavesN = kTile / kWaveN, kWaves = kWavesM * kWavesN;
 constexpr int kTileThreads = 64 * kWaves;
 constexpr int kCopies = kTileBytes / 1024 / kWaves;  // a wave's, per step and operand
-typedef Acc<kMB, kNB> TileAcc;
+// Lane l, register i of block (mb, nb): M = 16 mb + 4 (l / 16) + i, N = 16 nb +
+// l % 16 of the wave's part.
+struct TileAcc {
+  f32x4 v[kMB][kNB];
+};
+
+// Slot of 16-byte chunk c in row k of a k-major tile (512-byte rows). Of the
+// transposing read, 16 lanes take 32 bytes from each of four rows, and the
+// next 16 the same eight rows further on: the slots of these eight pieces
+// differ in their 64 banks.
+__device__ __forceinline__ int kslot(int k, int c) { return c ^ (4 * (k & 3)) ^ (2 * ((k >> 3) & 1)); }
 
 struct Operand {
   const bf16* base;     // first row of the tile (rows) or of K (k-major)
@@ -348,7 +358,7 @@ struct Copier {
   int64_t part_bytes;
 
   __device__ __forceinline__ void init(const Operand& o, int lane, int wave) {
-    static_assert(kWaves % 2 == 0, "a wave's copies start at rows of one parity");
+    static_assert(kWaves == 8, "a wave's copies are 64 or 16 rows apart: one swizzle for all");
     base = reinterpret_cast<const char*>(o.base);
     ldb = static_cast<uint32_t>(o.ld) * 2u;
     part_bytes = o.part_stride * 2;
@@ -362,7 +372,7 @@ struct Copier {
       chunk = static_cast<uint32_t>((lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7)) * 16u;
     else
       chunk = static_cast<uint32_t>(
-          min((lane & 31) ^ (4 * ((2 * (wave & 1) + (lane >> 5)) & 3)), o.cols / 8 - 1)) * 16u;
+          min(kslot(2 * wave + (lane >> 5), lane & 31), o.cols / 8 - 1)) * 16u;
     last = KMAJOR ? static_cast<uint32_t>(o.rows - 1) : static_cast<uint32_t>(o.cols) * 2u - 16u;
   }
   // copies q0 .. q1 - 1 of step ks of K (kStepK columns or rows) of part `part`
@@ -386,13 +396,24 @@ struct Copier {
   }
 };
 
-// Matrix-core operand of sub-step kk: rows (columns) c0 .. c0 + 31 of the tile.
+// Matrix-core operand of a 16 x 16 x 32 product: lane l receives K 32 kk + 8
+// (l / 16) .. + 7 of row (k-major: column) c0 + l % 16 of the tile.
 template <bool KMAJOR>
 __device__ __forceinline__ bf16x8 tile_frag(const char* tile, int kk, int c0, int lane) {
+  const int q16 = lane & 15, kq = lane >> 4;
   if constexpr (KMAJOR) {
-    return frag_kmajor(tile, 16 * kk, c0, lane);
+    // in each group of 16 lanes, lane q addresses four consecutive columns of
+    // one row, and the transposing read hands it four rows of one column
+    const int n = c0 + 4 * (q16 & 3);
+    v4i16 h[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int k = 32 * kk + 8 * kq + 4 * i + (q16 >> 2);
+      h[i] = lds_read_tr(tile + k * 512 + kslot(k, n >> 3) * 16 + (n & 7) * 2);
+    }
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
   } else {
-    const int r = c0 + (lane & 31), c = 2 * kk + (lane >> 5);
+    const int r = c0 + q16, c = 4 * kk + kq;
     return lds_read_b128(tile + r * (kStepK * 2) + (c ^ ((r >> 1) & 7)) * 16);
   }
 }
@@ -402,7 +423,7 @@ template <int PARTS, bool KA, bool KB>
 __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& ob, int n_k,
                                              char* smem, TileAcc& acc) {
   typedef Combos<PARTS> C;
-  constexpr int KK = kStepK / 16, M = kMB * kNB, F = kMB + kNB;
+  constexpr int KK = kStepK / 32;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % kWavesM, wn = wave / kWavesM;
@@ -421,19 +442,19 @@ __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& o
     const int c = PARTS == 1 ? 0 : s / n_k;
     cb.issue(C::b(c), s - c * n_k, sB + stage * kTileBytes, wave, q0, q1);
   };
-  bf16x8 fa[2][kMB], fb[2][kNB];
-  // fragment f (A's first, then B's) of sub-step kk
-  auto read_frag = [&](int f, int sta, int stb, int kk, int to) {
-    if (f < kMB)
-      fa[to][f] = tile_frag<KA>(sA + sta * kTileBytes, kk, kWaveM * wm + 32 * f, lane);
-    else
-      fb[to][f - kMB] = tile_frag<KB>(sB + stb * kTileBytes, kk, kWaveN * wn + 32 * (f - kMB), lane);
+  // B's fragments of this sub-step and the next; A's of this one, each
+  // replaced by the next sub-step's once its products are issued
+  bf16x8 fa[kMB], fb[2][kNB];
+  auto read_a = [&](int m, int sta, int kk) {
+    fa[m] = tile_frag<KA>(sA + sta * kTileBytes, kk, kWaveM * wm + 16 * m, lane);
   };
-  auto mma = [&](int f, int q) {
-    acc.v[q / kNB][q % kNB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-        fa[f][q / kNB], fb[f][q % kNB], acc.v[q / kNB][q % kNB], 0, 0, 0);
+  auto read_b = [&](int n, int stb, int kk, int to) {
+    fb[to][n] = tile_frag<KB>(sB + stb * kTileBytes, kk, kWaveN * wn + 16 * n, lane);
   };
-  acc.zero();
+#pragma unroll
+  for (int m = 0; m < kMB; ++m)
+#pragma unroll
+    for (int n = 0; n < kNB; ++n) acc.v[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (n_steps <= 0) return;
   // Copies in issue order: A and B of step 0; B of step 1, A of steps 1 and
   // 2; then after the barrier in the last sub-step of step s, B of step s + 2
@@ -450,10 +471,13 @@ __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& o
   }
   if (n_steps > 2) issue_a(2, 2, 0, kCopies);
 #pragma unroll
-  for (int f = 0; f < F; ++f) read_frag(f, 0, 0, 0, 0);
+  for (int n = 0; n < kNB; ++n) read_b(n, 0, 0, 0);
+#pragma unroll
+  for (int m = 0; m < kMB; ++m) read_a(m, 0, 0);
   int sta = 0;
   // copies of sub-step kk (counted from the one with the barrier) of `s`
   constexpr int kPer = kCopies;
+  static_assert(KK == 2 && kPer <= kMB, "B's copies in the last sub-step, A's in the next first");
   auto refill = [&](int s, int sta_s, int slot, int i) {
     const int q = slot * kPer + i;  // of 2 kCopies: B's, then A's
     if (q < kCopies) {
@@ -470,11 +494,13 @@ __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& o
       const int cur = kk & 1, nxt = cur ^ 1;
       const bool last = kk + 1 == KK;
 #pragma unroll
-      for (int q = 0; q < M; ++q) {
+      for (int m = 0; m < kMB; ++m) {
         __builtin_amdgcn_sched_barrier(0);
-        mma(cur, q);
+#pragma unroll
+        for (int n = 0; n < kNB; ++n)
+          acc.v[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[m], fb[cur][n], acc.v[m][n], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
-        if (last && q == 0) {
+        if (last && m == 0) {
           if (s + 1 < n_steps) {
             wait_lgkm0();  // this wave's reads of step s are complete
             if (s + 2 < n_steps) wait_vm_n<kCopies>();
@@ -482,18 +508,18 @@ __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& o
             lds_barrier();
           }
         }
-        // the next sub-step's fragments, F over the M products
-        if (!last || s + 1 < n_steps) {
-#pragma unroll
-          for (int f = q * F / M; f < (q + 1) * F / M; ++f)
-            if (last) read_frag(f, next, (s + 1) & 1, 0, nxt);
-            else read_frag(f, sta, s & 1, kk + 1, nxt);
+        // the next sub-step's fragments
+        if (!last) {
+          read_a(m, sta, kk + 1);
+          if (m < kNB) read_b(m, s & 1, kk + 1, nxt);
+        } else if (s + 1 < n_steps) {
+          read_a(m, next, 0);
+          if (m < kNB) read_b(m, (s + 1) & 1, 0, nxt);
         }
         // the refills
-#pragma unroll
-        for (int i = q * kPer / M; i < (q + 1) * kPer / M; ++i) {
-          if (last) refill(s, sta, 0, i);
-          else if (s > 0 && (kk + 1) * kPer < 2 * kCopies) refill(s - 1, prev_sta, kk + 1, i);
+        if (m < kPer) {
+          if (last) refill(s, sta, 0, m);
+          else if (s > 0) refill(s - 1, prev_sta, 1, m);
         }
       }
     }
@@ -550,25 +576,25 @@ __device__ __forceinline__ Operand rows_operand(const bf16* base, int64_t ld, in
 }
 
 // The teacher's ids among the columns of a lane's accumulator for one packed
-// row: the 64 columns from column c0 of the piece, of them the lane's half (4 kh
-// .. 4 kh + 3 of every eight).
+// row: the 64 columns from column c0 of the piece, of them the lane's quarter
+// (4 kq .. 4 kq + 3 of every 16).
 struct LaneIds {
   uint64_t word, mine;
   int64_t at;  // the word's index
-  __device__ __forceinline__ void load(const VocabArgs& a, int r, int rows, int c0, int kh) {
+  __device__ __forceinline__ void load(const VocabArgs& a, int r, int rows, int c0, int kq) {
     at = static_cast<int64_t>(r) * (a.ldd / 64) + c0 / 64;
     word = r < rows ? a.bits[at] : 0;
-    mine = word & (0x0F0F0F0F0F0F0F0Full << (4 * kh));
+    mine = word & (0x000F000F000F000Full << (4 * kq));
   }
-  // fn(column - 4 kh in the accumulator's order, place in qu) for each of them
+  // fn(column - 4 kq in the accumulator's order, place in qu) for each of them
   template <class F>
-  __device__ __forceinline__ void each(const VocabArgs& a, int r, int kh, F fn) {
+  __device__ __forceinline__ void each(const VocabArgs& a, int r, int kq, F fn) {
     if (!mine) return;
     const int64_t base = static_cast<int64_t>(r) * a.k + a.before[at];
     while (mine) {
       const int b = __ffsll(static_cast<unsigned long long>(mine)) - 1;
       mine &= mine - 1;
-      fn(b - 4 * kh, base + __popcll(word & ((1ull << b) - 1)));
+      fn(b - 4 * kq, base + __popcll(word & ((1ull << b) - 1)));
     }
   }
 };
@@ -582,14 +608,14 @@ __global__ __launch_bounds__(kTileThreads, 1) void stats_kernel(const VocabArgs 
   if (!tile_of_block((a.vn + kTile - 1) / kTile, row_tiles(a), mt, nt)) return;
   const int c0 = mt * kTile, r0 = nt * kTile, rows = a.count[0];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave % kWavesM, wn = wave / kWavesM, r32 = lane & 31, kh = lane >> 5;
-  LaneIds ids[kNB][kMB / 2];
+  const int wm = wave % kWavesM, wn = wave / kWavesM, r16 = lane & 15, kq = lane >> 4;
+  LaneIds ids[kNB][kWaveM / 64];
   if constexpr (TEACHER) {
 #pragma unroll
     for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
-      for (int h = 0; h < kMB / 2; ++h)
-        ids[nb][h].load(a, r0 + kWaveN * wn + 32 * nb + r32, rows, c0 + kWaveM * wm + 64 * h, kh);
+      for (int h = 0; h < kWaveM / 64; ++h)
+        ids[nb][h].load(a, r0 + kWaveN * wn + 16 * nb + r16, rows, c0 + kWaveM * wm + 64 * h, kq);
   }
   TileAcc acc;
   tile_product<PARTS, false, false>(
@@ -597,7 +623,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void stats_kernel(const VocabArgs 
       rows_operand(a.Xp + static_cast<int64_t>(r0) * a.ldx, a.ldx,
                    static_cast<int64_t>(a.np) * a.ldx, kTile, a.ldx),
       a.ldx / kStepK, smem, acc);
-  const int left = a.vn - c0 - kWaveM * wm - 4 * kh;  // columns from the lane's first
+  const int left = a.vn - c0 - kWaveM * wm - 4 * kq;  // columns from the lane's first
   const float z2 = a.zscale * kLog2e;
   float m[kNB], s[kNB];
 #pragma unroll
@@ -606,11 +632,12 @@ __global__ __launch_bounds__(kTileThreads, 1) void stats_kernel(const VocabArgs 
 #pragma unroll
     for (int mb = 0; mb < kMB; ++mb)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const float z = acc.v[mb][nb][i] * z2;
         acc.v[mb][nb][i] = z;
-        if (32 * mb + 8 * (i >> 2) + (i & 3) < left) m[nb] = fmaxf(m[nb], z);
+        if (16 * mb + i < left) m[nb] = fmaxf(m[nb], z);
       }
+    m[nb] = fmaxf(m[nb], __shfl_xor(m[nb], 16, 64));
     m[nb] = fmaxf(m[nb], __shfl_xor(m[nb], 32, 64));
     s[nb] = 0.0f;
     // (a wave whose columns all lie past the end has no maximum)
@@ -618,36 +645,37 @@ __global__ __launch_bounds__(kTileThreads, 1) void stats_kernel(const VocabArgs 
 #pragma unroll
     for (int mb = 0; mb < kMB; ++mb)
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (32 * mb + 8 * (i >> 2) + (i & 3) < left) s[nb] += exp2_(acc.v[mb][nb][i] - ref);
+      for (int i = 0; i < 4; ++i)
+        if (16 * mb + i < left) s[nb] += exp2_(acc.v[mb][nb][i] - ref);
+    s[nb] += __shfl_xor(s[nb], 16, 64);
     s[nb] += __shfl_xor(s[nb], 32, 64);
   }
 #pragma unroll
   for (int nb = 0; nb < kNB; ++nb) {
-    const int r = r0 + kWaveN * wn + 32 * nb + r32;
+    const int r = r0 + kWaveN * wn + 16 * nb + r16;
     auto logit = [&](int at, float* to) {
 #pragma unroll
       for (int mb = 0; mb < kMB; ++mb)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (at == 32 * mb + 8 * (i >> 2) + (i & 3)) *to = acc.v[mb][nb][i] * kLn2;
+        for (int i = 0; i < 4; ++i)
+          if (at == 16 * mb + i) *to = acc.v[mb][nb][i] * kLn2;
     };
     if constexpr (TEACHER) {
 #pragma unroll
-      for (int h = 0; h < kMB / 2; ++h)
-        ids[nb][h].each(a, r, kh, [&](int at, int64_t place) { logit(64 * h + at, a.zt + place); });
+      for (int h = 0; h < kWaveM / 64; ++h)
+        ids[nb][h].each(a, r, kq, [&](int at, int64_t place) { logit(64 * h + at, a.zt + place); });
     } else {
-      const int64_t at = r < rows ? a.ids[a.row[r]] - a.v0 - c0 - kWaveM * wm - 4 * kh : -1;
+      const int64_t at = r < rows ? a.ids[a.row[r]] - a.v0 - c0 - kWaveM * wm - 4 * kq : -1;
       if (at >= 0 && at < kWaveM) logit(static_cast<int>(at), a.zt + r);
     }
   }
   // the waves that share a row
   float2* red = reinterpret_cast<float2*>(smem);
   __syncthreads();
-  if (kh == 0)
+  if (kq == 0)
 #pragma unroll
     for (int nb = 0; nb < kNB; ++nb)
-      red[wm * kTile + kWaveN * wn + 32 * nb + r32] = make_float2(m[nb], s[nb]);
+      red[wm * kTile + kWaveN * wn + 16 * nb + r16] = make_float2(m[nb], s[nb]);
   __syncthreads();
   if (tid < kTile) {
     float2 p[kWavesM];
@@ -666,35 +694,32 @@ __global__ __launch_bounds__(kTileThreads, 1) void stats_kernel(const VocabArgs 
 }
 
 // A 256 x 256 tile of bf16 values, staged in LDS and written in rows of 512
-// bytes: value(nb, mb, i) of the accumulator layout goes to row 64 wn + 32 nb
-// + r32, column 64 wm + 32 mb + 8 (i / 4) + 4 kh + i % 4. Rows >= n_rows and
-// columns >= n_cols are not written (n_cols a multiple of eight, or VEC
+// bytes: an accumulator value's N is its row, its M its column. Rows >= n_rows
+// and columns >= n_cols are not written (n_cols a multiple of eight, or vec
 // false: element by element). 16-byte chunk c of row R sits in slot
 // c ^ (R mod 32).
 template <class F>
 __device__ __forceinline__ void write_tile(char* smem, bf16* dst, int64_t ld, int n_rows, int n_cols,
                                            bool vec, F value) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave % kWavesM, wn = wave / kWavesM, r32 = lane & 31, kh = lane >> 5;
+  const int wm = wave % kWavesM, wn = wave / kWavesM, r16 = lane & 15, kq = lane >> 4;
   __syncthreads();
 #pragma unroll
   for (int nb = 0; nb < kNB; ++nb) {
-    const int r = kWaveN * wn + 32 * nb + r32;
+    const int r = kWaveN * wn + 16 * nb + r16;
 #pragma unroll
-    for (int mb = 0; mb < kMB; ++mb)
+    for (int mb = 0; mb < kMB; ++mb) {
+      Vec4<bf16>::type v;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        Vec4<bf16>::type v;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = value(nb, mb, 4 * j + q);
-        const int c = kWaveM / 8 * wm + 4 * mb + j;
-        *reinterpret_cast<Vec4<bf16>::type*>(smem + r * 512 + (c ^ r32) * 16 + kh * 8) = v;
-      }
+      for (int q = 0; q < 4; ++q) v[q] = value(nb, mb, q);
+      const int c = kWaveM / 8 * wm + 2 * mb + (kq >> 1);
+      *reinterpret_cast<Vec4<bf16>::type*>(smem + r * 512 + (c ^ (r & 31)) * 16 + (kq & 1) * 8) = v;
+    }
   }
   __syncthreads();
 #pragma unroll
   for (int it = 0; it < kTile / (2 * kWaves); ++it) {
-    const int r = (it * kWaves + wave) * 2 + kh, c = r32;
+    const int r = (it * kWaves + wave) * 2 + (lane >> 5), c = lane & 31;
     const bf16x8 v = lds_read_b128(smem + r * 512 + (c ^ (r & 31)) * 16);
     if (r < n_rows && c * 8 < n_cols) {
       bf16* p = dst + static_cast<int64_t>(r) * ld + c * 8;
@@ -720,14 +745,14 @@ __global__ __launch_bounds__(kTileThreads, 1) void grad_logits_kernel(const Voca
   if (!tile_of_block((a.vn + kTile - 1) / kTile, row_tiles(a), mt, nt)) return;
   const int c0 = mt * kTile, r0 = nt * kTile, rows = a.count[0];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave % kWavesM, wn = wave / kWavesM, r32 = lane & 31, kh = lane >> 5;
-  LaneIds ids[kNB][kMB / 2];
+  const int wm = wave % kWavesM, wn = wave / kWavesM, r16 = lane & 15, kq = lane >> 4;
+  LaneIds ids[kNB][kWaveM / 64];
   if constexpr (TEACHER) {
 #pragma unroll
     for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
-      for (int h = 0; h < kMB / 2; ++h)
-        ids[nb][h].load(a, r0 + kWaveN * wn + 32 * nb + r32, rows, c0 + kWaveM * wm + 64 * h, kh);
+      for (int h = 0; h < kWaveM / 64; ++h)
+        ids[nb][h].load(a, r0 + kWaveN * wn + 16 * nb + r16, rows, c0 + kWaveM * wm + 64 * h, kq);
   }
   TileAcc acc;
   tile_product<PARTS, false, false>(
@@ -735,35 +760,35 @@ __global__ __launch_bounds__(kTileThreads, 1) void grad_logits_kernel(const Voca
       rows_operand(a.Xp + static_cast<int64_t>(r0) * a.ldx, a.ldx,
                    static_cast<int64_t>(a.np) * a.ldx, kTile, a.ldx),
       a.ldx / kStepK, smem, acc);
-  const int left = a.vn - c0 - kWaveM * wm - 4 * kh;
+  const int left = a.vn - c0 - kWaveM * wm - 4 * kq;
   const float z2 = a.zscale * kLog2e;
 #pragma unroll
   for (int nb = 0; nb < kNB; ++nb) {
-    const int r = r0 + kWaveN * wn + 32 * nb + r32;
+    const int r = r0 + kWaveN * wn + 16 * nb + r16;
     const bool in = r < rows;
     const int n = in ? a.row[r] : 0;
     const float g = in ? a.dloss[n] * a.dscale : 0.0f;
     const float lse2 = in ? a.lse[n] * kLog2e : 0.0f;
-    const int64_t at = in && !TEACHER ? a.ids[n] - a.v0 - c0 - kWaveM * wm - 4 * kh : -1;
+    const int64_t at = in && !TEACHER ? a.ids[n] - a.v0 - c0 - kWaveM * wm - 4 * kq : -1;
 #pragma unroll
     for (int mb = 0; mb < kMB; ++mb)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int c = 32 * mb + 8 * (i >> 2) + (i & 3);
+      for (int i = 0; i < 4; ++i) {
+        const int c = 16 * mb + i;
         float p = exp2_(fmaf(acc.v[mb][nb][i], z2, -lse2));
         if (!TEACHER && at == c) p -= 1.0f;
         acc.v[mb][nb][i] = in && c < left ? g * p : 0.0f;
       }
     if constexpr (TEACHER) {
 #pragma unroll
-      for (int h = 0; h < kMB / 2; ++h)
-        ids[nb][h].each(a, r, kh, [&](int at, int64_t place) {
+      for (int h = 0; h < kWaveM / 64; ++h)
+        ids[nb][h].each(a, r, kq, [&](int at, int64_t place) {
           const float gq = g * a.qu[place];
 #pragma unroll
-          for (int mb = 2 * h; mb < 2 * h + 2; ++mb)
+          for (int mb = 4 * h; mb < 4 * h + 4; ++mb)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (64 * h + at == 32 * mb + 8 * (i >> 2) + (i & 3)) acc.v[mb][nb][i] -= gq;
+            for (int i = 0; i < 4; ++i)
+              if (64 * h + at == 16 * mb + i) acc.v[mb][nb][i] -= gq;
         });
     }
   }
@@ -795,24 +820,29 @@ __global__ __launch_bounds__(kTileThreads, 1) void dx_kernel(const VocabArgs a) 
   const int steps = (a.vn + kStepK - 1) / kStepK, per = (steps + a.splits - 1) / a.splits;
   const int k0 = min(steps, split * per), k1 = min(steps, k0 + per);
   TileAcc acc;
-  tile_product<PARTS, false, true>(
+  tile_product<PARTS, true, false>(
+      table_operand(a, true, k0 * kStepK, c0),
       rows_operand(a.D + static_cast<int64_t>(r0) * a.ldd + k0 * kStepK, a.ldd,
                    static_cast<int64_t>(a.np) * a.ldd, kTile, a.ldd - k0 * kStepK),
-      table_operand(a, true, k0 * kStepK, c0), k1 - k0, smem, acc);
+      k1 - k0, smem, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave % kWavesM, wn = wave / kWavesM, r32 = lane & 31, kh = lane >> 5;
-  float* dst = a.dXacc + (static_cast<int64_t>(split) * a.np + r0 + kWaveM * wm + 4 * kh) * a.ldx + c0 +
-               kWaveN * wn + r32;
+  const int wm = wave % kWavesM, wn = wave / kWavesM, r16 = lane & 15, kq = lane >> 4;
+  float* dst = a.dXacc + (static_cast<int64_t>(split) * a.np + r0 + kWaveN * wn + r16) * a.ldx + c0 +
+               kWaveM * wm + 4 * kq;
 #pragma unroll
-  for (int nb = 0; nb < kNB; ++nb) {
-    if (c0 + kWaveN * wn + 32 * nb >= a.ldx) continue;
+  for (int mb = 0; mb < kMB; ++mb) {
+    if (c0 + kWaveM * wm + 16 * mb >= a.ldx) continue;
 #pragma unroll
-    for (int mb = 0; mb < kMB; ++mb)
+    for (int nb = 0; nb < kNB; ++nb) {
+      f32x4* p = reinterpret_cast<f32x4*>(dst + static_cast<int64_t>(16 * nb) * a.ldx + 16 * mb);
+      f32x4 x = acc.v[mb][nb];
+      if (a.v0 != 0) {
+        const f32x4 y = *p;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float* p = dst + static_cast<int64_t>(32 * mb + 8 * (i >> 2) + (i & 3)) * a.ldx + 32 * nb;
-        *p = a.v0 == 0 ? acc.v[mb][nb][i] : *p + acc.v[mb][nb][i];
+        for (int i = 0; i < 4; ++i) x[i] += y[i];
       }
+      *p = x;
+    }
   }
 }
 
@@ -838,29 +868,24 @@ __global__ __launch_bounds__(kTileThreads, 1) void de_kernel(const VocabArgs a, 
                [&](int nb, int mb, int i) { return from_float<bf16>(acc.v[mb][nb][i]); });
   } else {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = wave % kWavesM, wn = wave / kWavesM, r32 = lane & 31, kh = lane >> 5;
+    const int wm = wave % kWavesM, wn = wave / kWavesM, r16 = lane & 15, kq = lane >> 4;
     const bool vec = a.d % 4 == 0 && is_aligned(dE, 16);
 #pragma unroll
     for (int nb = 0; nb < kNB; ++nb) {
-      const int r = kWaveN * wn + 32 * nb + r32;
+      const int r = kWaveN * wn + 16 * nb + r16;
       if (r >= n_rows) continue;
 #pragma unroll
-      for (int mb = 0; mb < kMB; ++mb)
+      for (int mb = 0; mb < kMB; ++mb) {
+        const int c = kWaveM * wm + 16 * mb + 4 * kq;
+        T* p = dst + static_cast<int64_t>(r) * a.d + c;
+        if (vec && c + 4 <= n_cols) {
+          *reinterpret_cast<f32x4*>(p) = acc.v[mb][nb];
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = kWaveM * wm + 32 * mb + 8 * j + 4 * kh;
-          T* p = dst + static_cast<int64_t>(r) * a.d + c;
-          f32x4 v;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = acc.v[mb][nb][4 * j + q];
-          if (vec && c + 4 <= n_cols) {
-            *reinterpret_cast<f32x4*>(p) = v;
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (c + q < n_cols) p[q] = v[q];
-          }
+          for (int q = 0; q < 4; ++q)
+            if (c + q < n_cols) p[q] = acc.v[mb][nb][q];
         }
+      }
     }
   }
 }
