@@ -201,6 +201,17 @@ template <> __device__ __forceinline__ float from_float<float>(float x) { return
 
 template <typename T> __device__ __forceinline__ T zero_val() { return from_float<T>(0.0f); }
 
+// Four values of T at dst (dst 4-element aligned).
+template <typename T>
+__device__ __forceinline__ void store4(T* dst, float a, float b, float c, float d) {
+  typename Vec4<T>::type v;
+  v[0] = from_float<T>(a);
+  v[1] = from_float<T>(b);
+  v[2] = from_float<T>(c);
+  v[3] = from_float<T>(d);
+  *reinterpret_cast<typename Vec4<T>::type*>(dst) = v;
+}
+
 // ----------------------------------------------------------- tile engine --
 //
 // A block of 4 waves computes C[BM x BN] = sum_k Aop[m][k] * Bop[n][k] with

@@ -56,17 +56,6 @@ __device__ __forceinline__ float block_sum(float x, float* red4) {
   return t;  // valid in thread 0 only
 }
 
-// Four values of T at dst (dst 4-element aligned).
-template <typename T>
-__device__ __forceinline__ void store4(T* dst, float a, float b, float c, float d) {
-  typename Vec4<T>::type v;
-  v[0] = from_float<T>(a);
-  v[1] = from_float<T>(b);
-  v[2] = from_float<T>(c);
-  v[3] = from_float<T>(d);
-  *reinterpret_cast<typename Vec4<T>::type*>(dst) = v;
-}
-
 // ------------------------------------------------------------------ gen_p --
 
 // One thread per Philox counter c of one layer: elements e = 4c .. 4c+3 of

@@ -26,7 +26,6 @@
 namespace dpg {
 namespace {
 
-constexpr int kRowThreads = 1024;
 constexpr int kPad = 256;     // packed rows and pieces are padded to whole tiles
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -50,15 +49,22 @@ template <> struct Combos<3> {
 };
 template <typename T> constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
 
-// The parts of x; the second and third are zero for infinities and NaN.
+// Takes the leading part off a value: x becomes the rest (zero for infinities
+// and NaN, whose other parts are zero).
+__device__ __forceinline__ bf16 take_part(float& x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  x = (u & 0x7F800000u) == 0x7F800000u ? 0.0f : x - __builtin_bit_cast(float, u & 0xFFFF0000u);
+  return __builtin_bit_cast(bf16, static_cast<unsigned short>(u >> 16));
+}
+__device__ __forceinline__ bf16 take_part(f32x4& v, int i) {
+  float x = v[i];
+  const bf16 p = take_part(x);
+  v[i] = x;
+  return p;
+}
 __device__ __forceinline__ void split3(float x, bf16 (&p)[3]) {
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, x);
-    p[q] = __builtin_bit_cast(bf16, static_cast<unsigned short>(u >> 16));
-    const float h = __builtin_bit_cast(float, u & 0xFFFF0000u);
-    x = (u & 0x7F800000u) == 0x7F800000u ? 0.0f : x - h;
-  }
+  for (int q = 0; q < 3; ++q) p[q] = take_part(x);
 }
 
 // Per-call tables in the workspace. Row i of the packed arrays is the i-th
@@ -104,12 +110,6 @@ struct VocabArgs {
 
 // ------------------------------------------------------------------- rows --
 
-// Cross entropy: a row has a target when its id lies in [0, V).
-__global__ __launch_bounds__(kThreads) void ce_flag_kernel(const VocabArgs a) {
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (n < a.N) a.flag[n] = a.ids[n] >= 0 && a.ids[n] < a.V;
-}
-
 // Distillation: one wave per row. q_j = exp(t_j / tau - m) / sum over the
 // entries whose id lies in [0, V); entries outside get q = 0, and a row
 // without any weight (no id, or every logit -inf) has no target.
@@ -152,32 +152,6 @@ __global__ __launch_bounds__(kThreads) void teacher_kernel(const VocabArgs a) {
   }
 }
 
-// Packed index of every row, in order; one block.
-__global__ __launch_bounds__(kRowThreads) void rows_kernel(const VocabArgs a) {
-  __shared__ int wave_cnt[kRowThreads / 64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int base = 0;
-  for (int64_t n0 = 0; n0 < a.N; n0 += kRowThreads) {
-    const int64_t n = n0 + tid;
-    const bool on = n < a.N && a.flag[n];
-    const uint64_t b = __ballot(on);
-    if (lane == 0) wave_cnt[wave] = __popcll(b);
-    __syncthreads();
-    int before = base, all = 0;
-    for (int w = 0; w < kRowThreads / 64; ++w) {
-      const int c = wave_cnt[w];
-      if (w < wave) before += c;
-      all += c;
-    }
-    const int at = before + __popcll(b & ((1ull << lane) - 1));
-    if (on) a.row[at] = static_cast<int32_t>(n);
-    if (n < a.N) a.inv[n] = on ? at : -1;
-    base += all;
-    __syncthreads();
-  }
-  if (tid == 0) a.count[0] = base;
-}
-
 // One value as PARTS bf16 parts, `stride` elements apart.
 template <int PARTS>
 __device__ __forceinline__ void store_parts(bf16* dst, int64_t stride, float x) {
@@ -191,28 +165,110 @@ __device__ __forceinline__ void store_parts(bf16* dst, int64_t stride, float x) 
   }
 }
 
-// Xp[i] = X[row[i]], in parts, zero beyond d and from the last packed row to
-// the next multiple of kPad; one block per row of Xp.
+// One row of d values as parts, zero beyond d, by 64 lanes.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void pack_rows_kernel(const VocabArgs a) {
-  const int i = blockIdx.x, rows = a.count[0];
-  if (i >= (rows + kPad - 1) / kPad * kPad) return;
-  const T* src = static_cast<const T*>(a.X) + static_cast<int64_t>(i < rows ? a.row[i] : 0) * a.d;
-  bf16* dst = a.Xp + static_cast<int64_t>(i) * a.ldx;
-  for (int c = threadIdx.x; c < a.ldx; c += kThreads)
-    store_parts<kParts<T>>(dst + c, static_cast<int64_t>(a.np) * a.ldx,
-                           i < rows && c < a.d ? to_float(src[c]) : 0.0f);
+__device__ __forceinline__ void pack_row(const T* src, bf16* dst, int d, int ldx, int64_t part_stride,
+                                         bool vec, int lane) {
+  constexpr int VN = Vec16<T>::N;
+  if (vec) {  // d a multiple of VN, src 16-byte aligned
+    for (int c = lane * VN; c < ldx; c += 64 * VN) {
+      typename Vec16<T>::type x;
+#pragma unroll
+      for (int q = 0; q < VN; ++q) x[q] = zero_val<T>();
+      if (c < d) x = *reinterpret_cast<const typename Vec16<T>::type*>(src + c);
+      if constexpr (kParts<T> == 1) {
+        *reinterpret_cast<bf16x8*>(dst + c) = x;
+      } else {
+        Vec4<bf16>::type y[3];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          bf16 p[3];
+          split3(x[q], p);
+#pragma unroll
+          for (int j = 0; j < 3; ++j) y[j][q] = p[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          *reinterpret_cast<Vec4<bf16>::type*>(dst + j * part_stride + c) = y[j];
+      }
+    }
+  } else {
+    for (int c = lane; c < ldx; c += 64)
+      store_parts<kParts<T>>(dst + c, part_stride, c < d ? to_float(src[c]) : 0.0f);
+  }
 }
 
-// Ep = the piece's rows of E, in parts, padded with zeros; one block per row.
+// Packs rows and table in one launch. Blocks [0, row_blocks - kPadBlocks):
+// kPackRows rows of X each. A row's packed index is the number of rows before it that have a
+// target, which each block counts for itself (8 bytes of L2 reads for every
+// earlier row, instead of a launch that counts and one that waits for it). The
+// kPad / kPackRows blocks after them zero Xp up to the next multiple of kPad.
+// The rest: rows of the first piece of the table, where it is packed.
+constexpr int kPackRows = 16, kPadBlocks = kPad / kPackRows;
 template <typename T>
-__global__ __launch_bounds__(kThreads) void pack_table_kernel(const VocabArgs a) {
-  const int i = blockIdx.x;
-  const T* src = static_cast<const T*>(a.E) + (static_cast<int64_t>(a.v0) + i) * a.d;
-  bf16* dst = a.Ep + static_cast<int64_t>(i) * a.ldx;
-  for (int c = threadIdx.x; c < a.ldx; c += kThreads)
-    store_parts<kParts<T>>(dst + c, static_cast<int64_t>(a.ldd) * a.ldx,
-                           i < a.vn && c < a.d ? to_float(src[c]) : 0.0f);
+__global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int row_blocks) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int VN = Vec16<T>::N;
+  const int block = static_cast<int>(blockIdx.x);
+  if (block >= row_blocks) {
+    const bool vec = a.d % VN == 0 && is_aligned(a.E, 16);
+    const int i = (block - row_blocks) * 4 + wave;
+    pack_row(static_cast<const T*>(a.E) + (static_cast<int64_t>(a.v0) + i) * a.d,
+             a.Ep + static_cast<int64_t>(i) * a.ldx, i < a.vn ? a.d : 0, a.ldx,
+             static_cast<int64_t>(a.ldd) * a.ldx, vec, lane);
+    return;
+  }
+  __shared__ int wave_cnt[4];
+  const int n0 = min(block * kPackRows, static_cast<int>(a.N));
+  const int64_t* ids = a.ids;
+  auto on = [&](int n) {
+    if (a.t) return a.flag[n] != 0;
+    const int64_t id = ids[n];
+    return id >= 0 && id < a.V;
+  };
+  int c = 0;
+  for (int j0 = tid; j0 < n0; j0 += 8 * kThreads) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int j = j0 + u * kThreads;
+      c += on(min(j, n0 - 1)) && j < n0;
+    }
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) c += __shfl_xor(c, off, 64);
+  if (lane == 0) wave_cnt[wave] = c;
+  __syncthreads();
+  const int before = (wave_cnt[0] + wave_cnt[1]) + (wave_cnt[2] + wave_cnt[3]);
+  const int64_t part_stride = static_cast<int64_t>(a.np) * a.ldx;
+  const int pad = block - (row_blocks - kPadBlocks);
+  if (pad >= 0) {
+    if (tid == 0 && pad == 0) a.count[0] = before;
+    const int end = (before + kPad - 1) / kPad * kPad;
+    for (int q = 0; q < kPackRows / 4; ++q) {
+      const int i = before + pad * kPackRows + q * 4 + wave;
+      if (i < end)
+        pack_row(static_cast<const T*>(a.X), a.Xp + static_cast<int64_t>(i) * a.ldx, 0, a.ldx,
+                 part_stride, true, lane);
+    }
+    return;
+  }
+  const int mine = n0 + lane;
+  const bool mine_on = lane < kPackRows && mine < a.N && on(mine);
+  const uint64_t b = __ballot(mine_on);
+  if (wave == 0 && lane < kPackRows && mine < a.N) {
+    const int at = before + __popcll(b & ((1ull << lane) - 1));
+    if (mine_on) a.row[at] = mine;
+    a.inv[mine] = mine_on ? at : -1;
+  }
+  const bool vec = a.d % VN == 0 && is_aligned(a.X, 16);
+#pragma unroll
+  for (int q = 0; q < kPackRows / 4; ++q) {
+    const int r = q * 4 + wave;
+    if (!((b >> r) & 1)) continue;
+    const int at = before + __popcll(b & ((1ull << r) - 1));
+    pack_row(static_cast<const T*>(a.X) + static_cast<int64_t>(n0 + r) * a.d,
+             a.Xp + static_cast<int64_t>(at) * a.ldx, a.d, a.ldx, part_stride, vec, lane);
+  }
 }
 
 // Distillation: where a packed row's teacher ids lie in the piece, as one bit
@@ -220,26 +276,31 @@ __global__ __launch_bounds__(kThreads) void pack_table_kernel(const VocabArgs a)
 // row's distinct ids get consecutive places in qu, in ascending order; an id
 // named more than once gets its weights' sum, in the order they are named.
 constexpr int kMaxWords = 4096;  // 64-column words of a piece
+constexpr int kMaxTop = 1024;    // entries of a teacher's row
 __global__ __launch_bounds__(kThreads) void teacher_ids_kernel(const VocabArgs a) {
   __shared__ uint32_t half[2 * kMaxWords];
   __shared__ uint16_t first[kMaxWords];
-  __shared__ int wave_cnt[4];
+  __shared__ int col[kMaxTop];  // column of entry j in the piece, or -1
+  __shared__ float weight[kMaxTop];
+  __shared__ int wave_cnt[4], named;
   const int i = blockIdx.x;
   if (i >= a.count[0]) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int words = a.ldd / 64;
   const int64_t n = a.row[i];
-  const int64_t* ids = a.ids + n * a.k;
-  const float* q = a.q + n * a.k;
   for (int w = tid; w < 2 * words; w += kThreads) half[w] = 0;
+  if (tid == 0) named = 0;
   __syncthreads();
-  auto col = [&](int j) {  // column of entry j in the piece, or -1
-    const int64_t c = ids[j] - a.v0;
-    return c >= 0 && c < a.vn && q[j] != 0.0f ? static_cast<int>(c) : -1;
-  };
   for (int j = tid; j < a.k; j += kThreads) {
-    const int c = col(j);
-    if (c >= 0) atomicOr(&half[c >> 5], 1u << (c & 31));
+    const float q = a.q[n * a.k + j];
+    const int64_t at = a.ids[n * a.k + j] - a.v0;
+    const int c = at >= 0 && at < a.vn && q != 0.0f ? static_cast<int>(at) : -1;
+    col[j] = c;
+    weight[j] = q;
+    if (c >= 0) {
+      atomicOr(&half[c >> 5], 1u << (c & 31));
+      atomicAdd(&named, 1);
+    }
   }
   __syncthreads();
   auto word = [&](int w) {
@@ -275,14 +336,17 @@ __global__ __launch_bounds__(kThreads) void teacher_ids_kernel(const VocabArgs a
     a.before[out + w] = first[w];
   }
   for (int j = tid; j < a.k; j += kThreads) {
-    const int c = col(j);
+    const int c = col[j];
     if (c < 0) continue;
     bool again = false;
-    float sum = 0.0f;
-    for (int l = 0; l < a.k; ++l) {
-      if (ids[l] != ids[j]) continue;
-      again |= l < j;
-      sum += q[l];
+    float sum = weight[j];
+    if (all < named) {  // some id is named twice
+      sum = 0.0f;
+      for (int l = 0; l < a.k; ++l) {
+        if (col[l] != c) continue;
+        again |= l < j;
+        sum += weight[l];
+      }
     }
     if (!again)
       a.qu[static_cast<int64_t>(i) * a.k + first[c >> 6] +
@@ -292,20 +356,20 @@ __global__ __launch_bounds__(kThreads) void teacher_ids_kernel(const VocabArgs a
 
 // --------------------------------------------------------------- products --
 //
-// One kernel template computes the three products in 256 x 256 tiles, one
-// 16-wave block per CU, each wave 64 x 64 with 32x32x16 matrix instructions:
+// One device function computes the three products in tiles of 256 x 256 (8
+// waves of 128 x 64, one block per CU) or, where those would not fill the 256
+// CUs, 128 x 128 (4 waves of 64 x 64, two blocks per CU), with 16x16x32 matrix
+// instructions:
 //   logits   M = vocabulary rows (E), N = packed rows (Xp), K = d
-//   dX       M = packed rows (D), N = columns (E), K = the vocabulary piece
+//   dX       M = columns (E), N = packed rows (D), K = the vocabulary piece
 //   dE       M = columns (Xp), N = vocabulary rows (D), K = packed rows
-// An operand whose K runs along its rows in memory ("rows") is copied as 256
-// rows of 128 bytes, chunk c of row R in slot c ^ (R / 2 mod 8), and read with
-// 16-byte LDS loads; one whose K runs down its columns ("k-major") as 64 rows
-// of 512 bytes, read with the transposing LDS load. The direct copies of A
-// run two K steps ahead of their use (three stages), those of B one (two
-// stages): 160 KiB of LDS. A lane's accumulator holds, per 32 x 32 block, one
-// N and four runs of four consecutive M; the roles above make that a row of
-// logits whose maximum and sum stay within the lane, and runs of four columns
-// of D and dE.
+// so that a row of logits has its maximum and sum within four lanes, and a
+// lane holds runs of four columns of D, dX and dE. An operand whose K runs
+// along its rows in memory ("rows") is copied as rows of 128 bytes, chunk c of
+// row R in slot c ^ (R / 2 mod 8), and read with 16-byte LDS loads; one whose K
+// runs down its columns ("k-major") as 64 rows of the tile's width, read with
+// the transposing LDS load. The direct copies of A run two K steps ahead of
+// their use (three stages), those of B one (two stages): 160 KiB of LDS a CU.
 //
 // Copies never leave their arrays: Xp, Ep and D are padded to whole tiles;
 // rows and chunks of E beyond its end are clamped to the last ones, and meet
@@ -319,21 +383,28 @@ template <int N> __device__ __forceinline__ void wait_vm_n() {
   __builtin_amdgcn_s_waitcnt(0x0F70 | N);
 }
 
-constexpr int kTile = 256, kStepK = 64;
-constexpr int kTileBytes = kTile * kStepK * 2;
-// Blocks of 16 x 16 in a wave's part of the tile, and the waves' layout.
-constexpr int kMB = 8, kNB = 4;
-constexpr int kWaveM = 16 * kMB, kWaveN = 16 * kNB;
-constexpr int kWavesM = kTile / kWaveM, kWavesN = kTile / kWaveN, kWaves = kWavesM * kWavesN;
-constexpr int kTileThreads = 64 * kWaves;
-constexpr int kCopies = kTileBytes / 1024 / kWaves;  // a wave's, per step and operand
-// Lane l, register i of block (mb, nb): M = 16 mb + 4 (l / 16) + i, N = 16 nb +
-// l % 16 of the wave's part.
-struct TileAcc {
-  f32x4 v[kMB][kNB];
+constexpr int kStepK = 64;
+// A block's tile, and the blocks of 16 x 16 in a wave's part of it. In a
+// wave's accumulator, lane l, register i of block (mb, nb) holds M = 16 mb + 4
+// (l / 16) + i, N = 16 nb + l % 16.
+template <int TILE, int MB, int NB>
+struct Geometry {
+  static constexpr int kTile = TILE, kMB = MB, kNB = NB;
+  static constexpr int kWaveM = 16 * MB, kWaveN = 16 * NB;
+  static constexpr int kWavesM = TILE / kWaveM, kWavesN = TILE / kWaveN;
+  static constexpr int kWaves = kWavesM * kWavesN, kThreads = 64 * kWaves;
+  static constexpr int kTileBytes = TILE * kStepK * 2;
+  static constexpr int kCopies = kTileBytes / 1024 / kWaves;  // a wave's, per step and operand
+  static constexpr int kLds = 5 * kTileBytes;
+  static constexpr int kBlocks = TILE == 256 ? 1 : 2;  // resident on a CU
+  struct Acc {
+    f32x4 v[MB][NB];
+  };
 };
+typedef Geometry<256, 8, 4> BigTile;
+typedef Geometry<128, 4, 4> SmallTile;
 
-// Slot of 16-byte chunk c in row k of a k-major tile (512-byte rows). Of the
+// Slot of 16-byte chunk c in row k of a k-major tile. Of the
 // transposing read, 16 lanes take 32 bytes from each of four rows, and the
 // next 16 the same eight rows further on: the slots of these eight pieces
 // differ in their 64 banks.
@@ -347,58 +418,69 @@ struct Operand {
   int cols;             // rows: elements of K in a row; k-major: columns from base
 };
 
-// The direct copies of one operand: kCopies of 1 KiB a wave and step.
-template <bool KMAJOR>
+// The direct copies of one operand: G::kCopies of 1 KiB a wave and step.
+template <class G, bool KMAJOR>
 struct Copier {
-  const char* base;
+  static constexpr int kChunks = G::kTile / 8;        // k-major: of a row
+  static constexpr int kRowsPerCopy = 64 / kChunks;  // k-major
+  const char* base;       // of the part
+  const char* at;         // k-major: of the K step to copy
+  uint32_t kb;            // rows: byte offset of that step; k-major: its K row
   uint32_t ldb;           // row stride, bytes
-  uint32_t off[kCopies];  // rows: row offset; k-major: K row of the lane
+  uint32_t off[G::kCopies];  // rows: row offset; k-major: K row of the lane
   uint32_t chunk;         // byte offset of the lane's 16 bytes within the row
   uint32_t last;          // rows: last chunk of a row; k-major: last K row
   int64_t part_bytes;
 
   __device__ __forceinline__ void init(const Operand& o, int lane, int wave) {
-    static_assert(kWaves == 8, "a wave's copies are 64 or 16 rows apart: one swizzle for all");
-    base = reinterpret_cast<const char*>(o.base);
+    // a wave's copies are 64 (32) rows or 16 K rows apart: one swizzle for all
+    static_assert(G::kWaves % 2 == 0 && G::kWaves * kRowsPerCopy % 16 == 0, "copy layout");
+    base = at = reinterpret_cast<const char*>(o.base);
+    kb = 0;
     ldb = static_cast<uint32_t>(o.ld) * 2u;
     part_bytes = o.part_stride * 2;
 #pragma unroll
-    for (int q = 0; q < kCopies; ++q) {
-      const int g = q * kWaves + wave;
+    for (int q = 0; q < G::kCopies; ++q) {
+      const int g = q * G::kWaves + wave;
       if constexpr (!KMAJOR) off[q] = static_cast<uint32_t>(min(g * 8 + (lane >> 3), o.rows - 1)) * ldb;
-      else off[q] = static_cast<uint32_t>(g * 2 + (lane >> 5));
+      else off[q] = static_cast<uint32_t>(g * kRowsPerCopy + lane / kChunks);
     }
     if constexpr (!KMAJOR)
       chunk = static_cast<uint32_t>((lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7)) * 16u;
     else
       chunk = static_cast<uint32_t>(
-          min(kslot(2 * wave + (lane >> 5), lane & 31), o.cols / 8 - 1)) * 16u;
+          min(kslot(kRowsPerCopy * wave + lane / kChunks, lane % kChunks), o.cols / 8 - 1)) * 16u;
     last = KMAJOR ? static_cast<uint32_t>(o.rows - 1) : static_cast<uint32_t>(o.cols) * 2u - 16u;
   }
-  // copies q0 .. q1 - 1 of step ks of K (kStepK columns or rows) of part `part`
-  __device__ __forceinline__ void issue(int part, int ks, char* stage, int wave, int q0, int q1) const {
-    const char* p = base + part * part_bytes;
-    if constexpr (!KMAJOR) {
-      const uint32_t kb = static_cast<uint32_t>(ks) * (kStepK * 2);
-      const __amdgpu_buffer_rsrc_t rs = tile_rsrc(p);
-      const uint32_t c = min(kb + chunk, last);
+  // copies q0 .. q1 - 1 of the current K step (kStepK columns or rows)
+  __device__ __forceinline__ void issue(char* stage, int wave, int q0, int q1) const {
+    const __amdgpu_buffer_rsrc_t rs = tile_rsrc(KMAJOR ? at : base);
+    const uint32_t c = min(kb + chunk, last), lim = last - kb;
 #pragma unroll
-      for (int q = 0; q < kCopies; ++q)
-        if (q >= q0 && q < q1) copy_to_lds(rs, off[q] + c, 0, stage + (q * kWaves + wave) * 1024);
+    for (int q = 0; q < G::kCopies; ++q)
+      if (q >= q0 && q < q1)
+        copy_to_lds(rs, KMAJOR ? min(off[q], lim) * ldb + chunk : off[q] + c, 0,
+                    stage + (q * G::kWaves + wave) * 1024);
+  }
+  __device__ __forceinline__ void next_step() {
+    if constexpr (KMAJOR) {
+      at += static_cast<uint64_t>(ldb) * kStepK;
+      kb += kStepK;
     } else {
-      const __amdgpu_buffer_rsrc_t rs = tile_rsrc(p + static_cast<int64_t>(ks) * kStepK * ldb);
-      const uint32_t lim = last - static_cast<uint32_t>(ks) * kStepK;
-#pragma unroll
-      for (int q = 0; q < kCopies; ++q)
-        if (q >= q0 && q < q1)
-          copy_to_lds(rs, min(off[q], lim) * ldb + chunk, 0, stage + (q * kWaves + wave) * 1024);
+      kb += kStepK * 2;
     }
+  }
+  // the first step of the part `parts` parts further on (or back)
+  __device__ __forceinline__ void next_part(int parts) {
+    base += parts * part_bytes;
+    at = base;
+    kb = 0;
   }
 };
 
 // Matrix-core operand of a 16 x 16 x 32 product: lane l receives K 32 kk + 8
 // (l / 16) .. + 7 of row (k-major: column) c0 + l % 16 of the tile.
-template <bool KMAJOR>
+template <class G, bool KMAJOR>
 __device__ __forceinline__ bf16x8 tile_frag(const char* tile, int kk, int c0, int lane) {
   const int q16 = lane & 15, kq = lane >> 4;
   if constexpr (KMAJOR) {
@@ -409,7 +491,7 @@ __device__ __forceinline__ bf16x8 tile_frag(const char* tile, int kk, int c0, in
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int k = 32 * kk + 8 * kq + 4 * i + (q16 >> 2);
-      h[i] = lds_read_tr(tile + k * 512 + kslot(k, n >> 3) * 16 + (n & 7) * 2);
+      h[i] = lds_read_tr(tile + k * (2 * G::kTile) + kslot(k, n >> 3) * 16 + (n & 7) * 2);
     }
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
   } else {
@@ -419,71 +501,79 @@ __device__ __forceinline__ bf16x8 tile_frag(const char* tile, int kk, int c0, in
 }
 
 // acc = A B^T over K steps [0, n_k) of every combination of parts.
-template <int PARTS, bool KA, bool KB>
+template <class G, int PARTS, bool KA, bool KB>
 __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& ob, int n_k,
-                                             char* smem, TileAcc& acc) {
+                                             char* smem, typename G::Acc& acc) {
   typedef Combos<PARTS> C;
   constexpr int KK = kStepK / 32;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave % kWavesM, wn = wave / kWavesM;
-  Copier<KA> ca;
-  Copier<KB> cb;
+  const int wm = wave % G::kWavesM, wn = wave / G::kWavesM;
+  Copier<G, KA> ca;
+  Copier<G, KB> cb;
   ca.init(oa, lane, wave);
   cb.init(ob, lane, wave);
   const int n_steps = n_k * C::n;
   char* const sA = smem;
-  char* const sB = smem + 3 * kTileBytes;
-  auto issue_a = [&](int s, int stage, int q0, int q1) {
-    const int c = PARTS == 1 ? 0 : s / n_k;
-    ca.issue(C::a(c), s - c * n_k, sA + stage * kTileBytes, wave, q0, q1);
+  char* const sB = smem + 3 * G::kTileBytes;
+  // after the last copy of a step: the next step, or with several parts the
+  // next combination's first
+  int ka = 0, ia = 0, kb = 0, ib = 0;
+  if (PARTS > 1) ca.next_part(C::a(0)), cb.next_part(C::b(0));
+  auto issue_a = [&](int stage, int q0, int q1) {
+    ca.issue(sA + stage * G::kTileBytes, wave, q0, q1);
+    if (q1 < G::kCopies) return;
+    if (PARTS > 1 && ++ka == n_k) ka = 0, ca.next_part(C::a(ia + 1) - C::a(ia)), ++ia;
+    else ca.next_step();
   };
-  auto issue_b = [&](int s, int stage, int q0, int q1) {
-    const int c = PARTS == 1 ? 0 : s / n_k;
-    cb.issue(C::b(c), s - c * n_k, sB + stage * kTileBytes, wave, q0, q1);
+  auto issue_b = [&](int stage, int q0, int q1) {
+    cb.issue(sB + stage * G::kTileBytes, wave, q0, q1);
+    if (q1 < G::kCopies) return;
+    if (PARTS > 1 && ++kb == n_k) kb = 0, cb.next_part(C::b(ib + 1) - C::b(ib)), ++ib;
+    else cb.next_step();
   };
   // B's fragments of this sub-step and the next; A's of this one, each
   // replaced by the next sub-step's once its products are issued
-  bf16x8 fa[kMB], fb[2][kNB];
+  bf16x8 fa[G::kMB], fb[2][G::kNB];
   auto read_a = [&](int m, int sta, int kk) {
-    fa[m] = tile_frag<KA>(sA + sta * kTileBytes, kk, kWaveM * wm + 16 * m, lane);
+    fa[m] = tile_frag<G, KA>(sA + sta * G::kTileBytes, kk, G::kWaveM * wm + 16 * m, lane);
   };
   auto read_b = [&](int n, int stb, int kk, int to) {
-    fb[to][n] = tile_frag<KB>(sB + stb * kTileBytes, kk, kWaveN * wn + 16 * n, lane);
+    fb[to][n] = tile_frag<G, KB>(sB + stb * G::kTileBytes, kk, G::kWaveN * wn + 16 * n, lane);
   };
 #pragma unroll
-  for (int m = 0; m < kMB; ++m)
+  for (int m = 0; m < G::kMB; ++m)
 #pragma unroll
-    for (int n = 0; n < kNB; ++n) acc.v[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < G::kNB; ++n) acc.v[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (n_steps <= 0) return;
   // Copies in issue order: A and B of step 0; B of step 1, A of steps 1 and
   // 2; then after the barrier in the last sub-step of step s, B of step s + 2
   // and A of step s + 3, spread over that sub-step and the next three. Before
   // that barrier step s + 1's copies are complete once at most those of A's
   // step s + 2 are in flight: loads return in order.
-  issue_a(0, 0, 0, kCopies);
-  issue_b(0, 0, 0, kCopies);
+  issue_a(0, 0, G::kCopies);
+  issue_b(0, 0, G::kCopies);
   wait_vm_n<0>();
   lds_barrier();
   if (n_steps > 1) {
-    issue_b(1, 1, 0, kCopies);
-    issue_a(1, 1, 0, kCopies);
+    issue_b(1, 0, G::kCopies);
+    issue_a(1, 0, G::kCopies);
   }
-  if (n_steps > 2) issue_a(2, 2, 0, kCopies);
+  if (n_steps > 2) issue_a(2, 0, G::kCopies);
 #pragma unroll
-  for (int n = 0; n < kNB; ++n) read_b(n, 0, 0, 0);
+  for (int n = 0; n < G::kNB; ++n) read_b(n, 0, 0, 0);
 #pragma unroll
-  for (int m = 0; m < kMB; ++m) read_a(m, 0, 0);
+  for (int m = 0; m < G::kMB; ++m) read_a(m, 0, 0);
   int sta = 0;
   // copies of sub-step kk (counted from the one with the barrier) of `s`
-  constexpr int kPer = kCopies;
-  static_assert(KK == 2 && kPer <= kMB, "B's copies in the last sub-step, A's in the next first");
+  constexpr int kPer = G::kCopies;
+  static_assert(KK == 2 && kPer <= G::kMB && G::kNB <= G::kMB, "B's copies in the last sub-step, A's in the next first");
   auto refill = [&](int s, int sta_s, int slot, int i) {
-    const int q = slot * kPer + i;  // of 2 kCopies: B's, then A's
-    if (q < kCopies) {
-      if (s + 2 < n_steps) issue_b(s + 2, s & 1, q, q + 1);
+    const int q = slot * kPer + i;  // of 2 G::kCopies: B's, then A's
+    if (q < G::kCopies) {
+      if (s + 2 < n_steps) issue_b(s & 1, q, q + 1);
     } else {
-      if (s + 3 < n_steps) issue_a(s + 3, sta_s, q - kCopies, q - kCopies + 1);
+      if (s + 3 < n_steps) issue_a(sta_s, q - G::kCopies, q - G::kCopies + 1);
     }
   };
   int prev_sta = 0;
@@ -494,16 +584,16 @@ __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& o
       const int cur = kk & 1, nxt = cur ^ 1;
       const bool last = kk + 1 == KK;
 #pragma unroll
-      for (int m = 0; m < kMB; ++m) {
+      for (int m = 0; m < G::kMB; ++m) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int n = 0; n < kNB; ++n)
+        for (int n = 0; n < G::kNB; ++n)
           acc.v[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[m], fb[cur][n], acc.v[m][n], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
         if (last && m == 0) {
           if (s + 1 < n_steps) {
             wait_lgkm0();  // this wave's reads of step s are complete
-            if (s + 2 < n_steps) wait_vm_n<kCopies>();
+            if (s + 2 < n_steps) wait_vm_n<G::kCopies>();
             else wait_vm_n<0>();
             lds_barrier();
           }
@@ -511,10 +601,10 @@ __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& o
         // the next sub-step's fragments
         if (!last) {
           read_a(m, sta, kk + 1);
-          if (m < kNB) read_b(m, s & 1, kk + 1, nxt);
+          if (m < G::kNB) read_b(m, s & 1, kk + 1, nxt);
         } else if (s + 1 < n_steps) {
           read_a(m, next, 0);
-          if (m < kNB) read_b(m, (s + 1) & 1, 0, nxt);
+          if (m < G::kNB) read_b(m, (s + 1) & 1, 0, nxt);
         }
         // the refills
         if (m < kPer) {
@@ -528,14 +618,14 @@ __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& o
   }
 }
 
-// The tile (m, n) of block blockIdx.x among mt x nt: each XCD takes a
+// The tile (m, n) of a block among mt x nt: each XCD takes a
 // contiguous run of them, in bands of eight m, so that the blocks an XCD runs
 // together share eight A and four B tiles in its L2. False past the last.
-__device__ __forceinline__ bool tile_of_block(int mt, int nt, int& m, int& n) {
+__device__ __forceinline__ bool tile_of_block(int block, int mt, int nt, int& m, int& n) {
   const int total = mt * nt;
   const int per = (total + 7) >> 3;
-  const int at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if (static_cast<int>(blockIdx.x >> 3) >= per || at >= total) return false;
+  const int at = (block & 7) * per + (block >> 3);
+  if ((block >> 3) >= per || at >= total) return false;
   const int band = at / (8 * nt), in = at - band * 8 * nt;
   const int h = min(8, mt - band * 8);
   m = band * 8 + in % h;
@@ -543,7 +633,10 @@ __device__ __forceinline__ bool tile_of_block(int mt, int nt, int& m, int& n) {
   return true;
 }
 
-__device__ __forceinline__ int row_tiles(const VocabArgs& a) { return (a.count[0] + kTile - 1) / kTile; }
+template <class G>
+__device__ __forceinline__ int row_tiles(const VocabArgs& a) {
+  return (a.count[0] + G::kTile - 1) / G::kTile;
+}
 
 // E as an operand of the current piece: packed, or the caller's own.
 __device__ __forceinline__ Operand table_operand(const VocabArgs& a, bool kmajor, int row0, int col0) {
@@ -601,36 +694,36 @@ struct LaneIds {
 
 // Each row's maximum and sum of exponentials over a 256-column tile, and
 // cross entropy's target logit. Works in base 2: z log2(e).
-template <int PARTS, bool TEACHER>
-__global__ __launch_bounds__(kTileThreads, 1) void stats_kernel(const VocabArgs a, int tile0) {
-  __shared__ __attribute__((aligned(1024))) char smem[5 * kTileBytes];
+template <class G, int PARTS, bool TEACHER>
+__global__ __launch_bounds__(G::kThreads, G::kBlocks) void stats_kernel(const VocabArgs a, int tile0) {
+  __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
   int mt, nt;
-  if (!tile_of_block((a.vn + kTile - 1) / kTile, row_tiles(a), mt, nt)) return;
-  const int c0 = mt * kTile, r0 = nt * kTile, rows = a.count[0];
+  if (!tile_of_block(blockIdx.x, (a.vn + G::kTile - 1) / G::kTile, row_tiles<G>(a), mt, nt)) return;
+  const int c0 = mt * G::kTile, r0 = nt * G::kTile, rows = a.count[0];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave % kWavesM, wn = wave / kWavesM, r16 = lane & 15, kq = lane >> 4;
-  LaneIds ids[kNB][kWaveM / 64];
+  const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
+  LaneIds ids[G::kNB][G::kWaveM / 64];
   if constexpr (TEACHER) {
 #pragma unroll
-    for (int nb = 0; nb < kNB; ++nb)
+    for (int nb = 0; nb < G::kNB; ++nb)
 #pragma unroll
-      for (int h = 0; h < kWaveM / 64; ++h)
-        ids[nb][h].load(a, r0 + kWaveN * wn + 16 * nb + r16, rows, c0 + kWaveM * wm + 64 * h, kq);
+      for (int h = 0; h < G::kWaveM / 64; ++h)
+        ids[nb][h].load(a, r0 + G::kWaveN * wn + 16 * nb + r16, rows, c0 + G::kWaveM * wm + 64 * h, kq);
   }
-  TileAcc acc;
-  tile_product<PARTS, false, false>(
+  typename G::Acc acc;
+  tile_product<G, PARTS, false, false>(
       table_operand(a, false, c0, 0),
       rows_operand(a.Xp + static_cast<int64_t>(r0) * a.ldx, a.ldx,
-                   static_cast<int64_t>(a.np) * a.ldx, kTile, a.ldx),
+                   static_cast<int64_t>(a.np) * a.ldx, G::kTile, a.ldx),
       a.ldx / kStepK, smem, acc);
-  const int left = a.vn - c0 - kWaveM * wm - 4 * kq;  // columns from the lane's first
+  const int left = a.vn - c0 - G::kWaveM * wm - 4 * kq;  // columns from the lane's first
   const float z2 = a.zscale * kLog2e;
-  float m[kNB], s[kNB];
+  float m[G::kNB], s[G::kNB];
 #pragma unroll
-  for (int nb = 0; nb < kNB; ++nb) {
+  for (int nb = 0; nb < G::kNB; ++nb) {
     m[nb] = -INFINITY;
 #pragma unroll
-    for (int mb = 0; mb < kMB; ++mb)
+    for (int mb = 0; mb < G::kMB; ++mb)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float z = acc.v[mb][nb][i] * z2;
@@ -643,7 +736,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void stats_kernel(const VocabArgs 
     // (a wave whose columns all lie past the end has no maximum)
     const float ref = m[nb] == -INFINITY ? 0.0f : m[nb];
 #pragma unroll
-    for (int mb = 0; mb < kMB; ++mb)
+    for (int mb = 0; mb < G::kMB; ++mb)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (16 * mb + i < left) s[nb] += exp2_(acc.v[mb][nb][i] - ref);
@@ -651,22 +744,22 @@ __global__ __launch_bounds__(kTileThreads, 1) void stats_kernel(const VocabArgs 
     s[nb] += __shfl_xor(s[nb], 32, 64);
   }
 #pragma unroll
-  for (int nb = 0; nb < kNB; ++nb) {
-    const int r = r0 + kWaveN * wn + 16 * nb + r16;
+  for (int nb = 0; nb < G::kNB; ++nb) {
+    const int r = r0 + G::kWaveN * wn + 16 * nb + r16;
     auto logit = [&](int at, float* to) {
 #pragma unroll
-      for (int mb = 0; mb < kMB; ++mb)
+      for (int mb = 0; mb < G::kMB; ++mb)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (at == 16 * mb + i) *to = acc.v[mb][nb][i] * kLn2;
     };
     if constexpr (TEACHER) {
 #pragma unroll
-      for (int h = 0; h < kWaveM / 64; ++h)
+      for (int h = 0; h < G::kWaveM / 64; ++h)
         ids[nb][h].each(a, r, kq, [&](int at, int64_t place) { logit(64 * h + at, a.zt + place); });
     } else {
-      const int64_t at = r < rows ? a.ids[a.row[r]] - a.v0 - c0 - kWaveM * wm - 4 * kq : -1;
-      if (at >= 0 && at < kWaveM) logit(static_cast<int>(at), a.zt + r);
+      const int64_t at = r < rows ? a.ids[a.row[r]] - a.v0 - c0 - G::kWaveM * wm - 4 * kq : -1;
+      if (at >= 0 && at < G::kWaveM) logit(static_cast<int>(at), a.zt + r);
     }
   }
   // the waves that share a row
@@ -674,53 +767,54 @@ __global__ __launch_bounds__(kTileThreads, 1) void stats_kernel(const VocabArgs 
   __syncthreads();
   if (kq == 0)
 #pragma unroll
-    for (int nb = 0; nb < kNB; ++nb)
-      red[wm * kTile + kWaveN * wn + 16 * nb + r16] = make_float2(m[nb], s[nb]);
+    for (int nb = 0; nb < G::kNB; ++nb)
+      red[wm * G::kTile + G::kWaveN * wn + 16 * nb + r16] = make_float2(m[nb], s[nb]);
   __syncthreads();
-  if (tid < kTile) {
-    float2 p[kWavesM];
+  if (tid < G::kTile) {
+    float2 p[G::kWavesM];
     float mm = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWavesM; ++w) {
-      p[w] = red[w * kTile + tid];
+    for (int w = 0; w < G::kWavesM; ++w) {
+      p[w] = red[w * G::kTile + tid];
       mm = fmaxf(mm, p[w].x);
     }
     const float ref = mm == -INFINITY ? 0.0f : mm;
     float ss = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWavesM; ++w) ss = fmaf(p[w].y, exp2_(p[w].x - ref), ss);
+    for (int w = 0; w < G::kWavesM; ++w) ss = fmaf(p[w].y, exp2_(p[w].x - ref), ss);
     a.part[static_cast<int64_t>(tile0 + mt) * a.np + r0 + tid] = make_float2(mm, ss);
   }
 }
 
-// A 256 x 256 tile of bf16 values, staged in LDS and written in rows of 512
-// bytes: an accumulator value's N is its row, its M its column. Rows >= n_rows
+// A tile of bf16 values, staged in LDS and written in whole rows: an accumulator value's N is its row, its M its column. Rows >= n_rows
 // and columns >= n_cols are not written (n_cols a multiple of eight, or vec
-// false: element by element). 16-byte chunk c of row R sits in slot
-// c ^ (R mod 32).
-template <class F>
+// false: element by element). 16-byte chunk c of row R sits in slot c ^ (R mod
+// the chunks of a row).
+template <class G, class F>
 __device__ __forceinline__ void write_tile(char* smem, bf16* dst, int64_t ld, int n_rows, int n_cols,
                                            bool vec, F value) {
+  constexpr int kRow = 2 * G::kTile, kChunks = kRow / 16, kPer = 64 / kChunks;  // rows a wave writes
+  static_assert(G::kTile * kRow <= G::kLds, "the staged tile fits");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave % kWavesM, wn = wave / kWavesM, r16 = lane & 15, kq = lane >> 4;
+  const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
   __syncthreads();
 #pragma unroll
-  for (int nb = 0; nb < kNB; ++nb) {
-    const int r = kWaveN * wn + 16 * nb + r16;
+  for (int nb = 0; nb < G::kNB; ++nb) {
+    const int r = G::kWaveN * wn + 16 * nb + r16;
 #pragma unroll
-    for (int mb = 0; mb < kMB; ++mb) {
+    for (int mb = 0; mb < G::kMB; ++mb) {
       Vec4<bf16>::type v;
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] = value(nb, mb, q);
-      const int c = kWaveM / 8 * wm + 2 * mb + (kq >> 1);
-      *reinterpret_cast<Vec4<bf16>::type*>(smem + r * 512 + (c ^ (r & 31)) * 16 + (kq & 1) * 8) = v;
+      const int c = G::kWaveM / 8 * wm + 2 * mb + (kq >> 1);
+      *reinterpret_cast<Vec4<bf16>::type*>(smem + r * kRow + (c ^ (r % kChunks)) * 16 + (kq & 1) * 8) = v;
     }
   }
   __syncthreads();
 #pragma unroll
-  for (int it = 0; it < kTile / (2 * kWaves); ++it) {
-    const int r = (it * kWaves + wave) * 2 + (lane >> 5), c = lane & 31;
-    const bf16x8 v = lds_read_b128(smem + r * 512 + (c ^ (r & 31)) * 16);
+  for (int it = 0; it < G::kTile / (kPer * G::kWaves); ++it) {
+    const int r = (it * G::kWaves + wave) * kPer + lane / kChunks, c = lane % kChunks;
+    const bf16x8 v = lds_read_b128(smem + r * kRow + (c ^ (r % kChunks)) * 16);
     if (r < n_rows && c * 8 < n_cols) {
       bf16* p = dst + static_cast<int64_t>(r) * ld + c * 8;
       if (vec) {
@@ -738,40 +832,40 @@ __device__ __forceinline__ void write_tile(char* smem, bf16* dst, int64_t ld, in
 // the piece and the packed rows. One rounding to bf16, after the target's
 // weight is subtracted: D enters two products whose other operand is bf16;
 // with fp32 D is kept in three parts.
-template <int PARTS, bool TEACHER>
-__global__ __launch_bounds__(kTileThreads, 1) void grad_logits_kernel(const VocabArgs a) {
-  __shared__ __attribute__((aligned(1024))) char smem[5 * kTileBytes];
+template <class G, int PARTS, bool TEACHER>
+__global__ __launch_bounds__(G::kThreads, G::kBlocks) void grad_logits_kernel(const VocabArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
   int mt, nt;
-  if (!tile_of_block((a.vn + kTile - 1) / kTile, row_tiles(a), mt, nt)) return;
-  const int c0 = mt * kTile, r0 = nt * kTile, rows = a.count[0];
+  if (!tile_of_block(blockIdx.x, (a.vn + G::kTile - 1) / G::kTile, row_tiles<G>(a), mt, nt)) return;
+  const int c0 = mt * G::kTile, r0 = nt * G::kTile, rows = a.count[0];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave % kWavesM, wn = wave / kWavesM, r16 = lane & 15, kq = lane >> 4;
-  LaneIds ids[kNB][kWaveM / 64];
+  const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
+  LaneIds ids[G::kNB][G::kWaveM / 64];
   if constexpr (TEACHER) {
 #pragma unroll
-    for (int nb = 0; nb < kNB; ++nb)
+    for (int nb = 0; nb < G::kNB; ++nb)
 #pragma unroll
-      for (int h = 0; h < kWaveM / 64; ++h)
-        ids[nb][h].load(a, r0 + kWaveN * wn + 16 * nb + r16, rows, c0 + kWaveM * wm + 64 * h, kq);
+      for (int h = 0; h < G::kWaveM / 64; ++h)
+        ids[nb][h].load(a, r0 + G::kWaveN * wn + 16 * nb + r16, rows, c0 + G::kWaveM * wm + 64 * h, kq);
   }
-  TileAcc acc;
-  tile_product<PARTS, false, false>(
+  typename G::Acc acc;
+  tile_product<G, PARTS, false, false>(
       table_operand(a, false, c0, 0),
       rows_operand(a.Xp + static_cast<int64_t>(r0) * a.ldx, a.ldx,
-                   static_cast<int64_t>(a.np) * a.ldx, kTile, a.ldx),
+                   static_cast<int64_t>(a.np) * a.ldx, G::kTile, a.ldx),
       a.ldx / kStepK, smem, acc);
-  const int left = a.vn - c0 - kWaveM * wm - 4 * kq;
+  const int left = a.vn - c0 - G::kWaveM * wm - 4 * kq;
   const float z2 = a.zscale * kLog2e;
 #pragma unroll
-  for (int nb = 0; nb < kNB; ++nb) {
-    const int r = r0 + kWaveN * wn + 16 * nb + r16;
+  for (int nb = 0; nb < G::kNB; ++nb) {
+    const int r = r0 + G::kWaveN * wn + 16 * nb + r16;
     const bool in = r < rows;
     const int n = in ? a.row[r] : 0;
     const float g = in ? a.dloss[n] * a.dscale : 0.0f;
     const float lse2 = in ? a.lse[n] * kLog2e : 0.0f;
-    const int64_t at = in && !TEACHER ? a.ids[n] - a.v0 - c0 - kWaveM * wm - 4 * kq : -1;
+    const int64_t at = in && !TEACHER ? a.ids[n] - a.v0 - c0 - G::kWaveM * wm - 4 * kq : -1;
 #pragma unroll
-    for (int mb = 0; mb < kMB; ++mb)
+    for (int mb = 0; mb < G::kMB; ++mb)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int c = 16 * mb + i;
@@ -781,7 +875,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void grad_logits_kernel(const Voca
       }
     if constexpr (TEACHER) {
 #pragma unroll
-      for (int h = 0; h < kWaveM / 64; ++h)
+      for (int h = 0; h < G::kWaveM / 64; ++h)
         ids[nb][h].each(a, r, kq, [&](int at, int64_t place) {
           const float gq = g * a.qu[place];
 #pragma unroll
@@ -794,46 +888,41 @@ __global__ __launch_bounds__(kTileThreads, 1) void grad_logits_kernel(const Voca
   }
   bf16* dst = a.D + static_cast<int64_t>(r0) * a.ldd + c0;
   if constexpr (PARTS == 1) {
-    write_tile(smem, dst, a.ldd, kTile, kTile, true,
+    write_tile<G>(smem, dst, a.ldd, G::kTile, G::kTile, true,
                [&](int nb, int mb, int i) { return from_float<bf16>(acc.v[mb][nb][i]); });
   } else {
 #pragma unroll
     for (int q = 0; q < 3; ++q)
-      write_tile(smem, dst + static_cast<int64_t>(q) * a.np * a.ldd, a.ldd, kTile, kTile, true,
-                 [&](int nb, int mb, int i) {
-                   bf16 p[3];
-                   split3(acc.v[mb][nb][i], p);
-                   return p[q];
-                 });
+      write_tile<G>(smem, dst + static_cast<int64_t>(q) * a.np * a.ldd, a.ldd, G::kTile, G::kTile, true,
+                 [&](int nb, int mb, int i) { return take_part(acc.v[mb][nb], i); });
   }
 }
 
 // dXacc[split] (+)= D E over the split's part of the piece.
-template <int PARTS>
-__global__ __launch_bounds__(kTileThreads, 1) void dx_kernel(const VocabArgs a) {
-  __shared__ __attribute__((aligned(1024))) char smem[5 * kTileBytes];
+template <class G, int PARTS>
+__device__ __forceinline__ void dx_tile(const VocabArgs& a, int block, char* smem) {
   int mt, nt;
-  const int ct = (a.ldx + kTile - 1) / kTile;
-  if (!tile_of_block(row_tiles(a), ct * a.splits, mt, nt)) return;
+  const int ct = (a.ldx + G::kTile - 1) / G::kTile;
+  if (!tile_of_block(block, row_tiles<G>(a), ct * a.splits, mt, nt)) return;
   const int split = nt / ct;
-  const int c0 = (nt - split * ct) * kTile, r0 = mt * kTile;
+  const int c0 = (nt - split * ct) * G::kTile, r0 = mt * G::kTile;
   const int steps = (a.vn + kStepK - 1) / kStepK, per = (steps + a.splits - 1) / a.splits;
   const int k0 = min(steps, split * per), k1 = min(steps, k0 + per);
-  TileAcc acc;
-  tile_product<PARTS, true, false>(
+  typename G::Acc acc;
+  tile_product<G, PARTS, true, false>(
       table_operand(a, true, k0 * kStepK, c0),
       rows_operand(a.D + static_cast<int64_t>(r0) * a.ldd + k0 * kStepK, a.ldd,
-                   static_cast<int64_t>(a.np) * a.ldd, kTile, a.ldd - k0 * kStepK),
+                   static_cast<int64_t>(a.np) * a.ldd, G::kTile, a.ldd - k0 * kStepK),
       k1 - k0, smem, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave % kWavesM, wn = wave / kWavesM, r16 = lane & 15, kq = lane >> 4;
-  float* dst = a.dXacc + (static_cast<int64_t>(split) * a.np + r0 + kWaveN * wn + r16) * a.ldx + c0 +
-               kWaveM * wm + 4 * kq;
+  const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
+  float* dst = a.dXacc + (static_cast<int64_t>(split) * a.np + r0 + G::kWaveN * wn + r16) * a.ldx + c0 +
+               G::kWaveM * wm + 4 * kq;
 #pragma unroll
-  for (int mb = 0; mb < kMB; ++mb) {
-    if (c0 + kWaveM * wm + 16 * mb >= a.ldx) continue;
+  for (int mb = 0; mb < G::kMB; ++mb) {
+    if (c0 + G::kWaveM * wm + 16 * mb >= a.ldx) continue;
 #pragma unroll
-    for (int nb = 0; nb < kNB; ++nb) {
+    for (int nb = 0; nb < G::kNB; ++nb) {
       f32x4* p = reinterpret_cast<f32x4*>(dst + static_cast<int64_t>(16 * nb) * a.ldx + 16 * mb);
       f32x4 x = acc.v[mb][nb];
       if (a.v0 != 0) {
@@ -847,36 +936,35 @@ __global__ __launch_bounds__(kTileThreads, 1) void dx_kernel(const VocabArgs a) 
 }
 
 // The piece's rows of dE = D^T Xp, rounded once.
-template <typename T>
-__global__ __launch_bounds__(kTileThreads, 1) void de_kernel(const VocabArgs a, T* dE) {
+template <class G, typename T>
+__device__ __forceinline__ void de_tile(const VocabArgs& a, T* dE, int block, char* smem) {
   constexpr int PARTS = kParts<T>;
-  __shared__ __attribute__((aligned(1024))) char smem[5 * kTileBytes];
   int mt, nt;
-  const int ct = (a.ldx + kTile - 1) / kTile;
+  const int ct = (a.ldx + G::kTile - 1) / G::kTile;
   // (bands of eight run over the vocabulary, the longer side)
-  if (!tile_of_block((a.vn + kTile - 1) / kTile, ct, nt, mt)) return;
-  const int c0 = mt * kTile, w0 = nt * kTile, rows = a.count[0];
-  TileAcc acc;
-  tile_product<PARTS, true, true>(
+  if (!tile_of_block(block, (a.vn + G::kTile - 1) / G::kTile, ct, nt, mt)) return;
+  const int c0 = mt * G::kTile, w0 = nt * G::kTile, rows = a.count[0];
+  typename G::Acc acc;
+  tile_product<G, PARTS, true, true>(
       rows_operand(a.Xp + c0, a.ldx, static_cast<int64_t>(a.np) * a.ldx, a.np, a.ldx - c0),
-      rows_operand(a.D + w0, a.ldd, static_cast<int64_t>(a.np) * a.ldd, a.np, kTile),
+      rows_operand(a.D + w0, a.ldd, static_cast<int64_t>(a.np) * a.ldd, a.np, G::kTile),
       (rows + kStepK - 1) / kStepK, smem, acc);
   T* dst = dE + (static_cast<int64_t>(a.v0) + w0) * a.d + c0;
   const int n_rows = a.vn - w0, n_cols = a.d - c0;
   if constexpr (PARTS == 1) {
-    write_tile(smem, dst, a.d, n_rows, n_cols, a.d % 8 == 0 && is_aligned(dE, 16),
+    write_tile<G>(smem, dst, a.d, n_rows, n_cols, a.d % 8 == 0 && is_aligned(dE, 16),
                [&](int nb, int mb, int i) { return from_float<bf16>(acc.v[mb][nb][i]); });
   } else {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = wave % kWavesM, wn = wave / kWavesM, r16 = lane & 15, kq = lane >> 4;
+    const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
     const bool vec = a.d % 4 == 0 && is_aligned(dE, 16);
 #pragma unroll
-    for (int nb = 0; nb < kNB; ++nb) {
-      const int r = kWaveN * wn + 16 * nb + r16;
+    for (int nb = 0; nb < G::kNB; ++nb) {
+      const int r = G::kWaveN * wn + 16 * nb + r16;
       if (r >= n_rows) continue;
 #pragma unroll
-      for (int mb = 0; mb < kMB; ++mb) {
-        const int c = kWaveM * wm + 16 * mb + 4 * kq;
+      for (int mb = 0; mb < G::kMB; ++mb) {
+        const int c = G::kWaveM * wm + 16 * mb + 4 * kq;
         T* p = dst + static_cast<int64_t>(r) * a.d + c;
         if (vec && c + 4 <= n_cols) {
           *reinterpret_cast<f32x4*>(p) = acc.v[mb][nb];
@@ -923,17 +1011,51 @@ __global__ __launch_bounds__(kThreads) void lse_kernel(const VocabArgs a, int ti
   }
 }
 
+// The gradients' products of one piece: dX's tiles in blocks [0, dx_blocks), dE's
+// in the rest. Small problems run both in one launch; large ones run faster one
+// after the other, in kernels of their own (8192 x 4096 x 32768: 3.12 ms
+// against 3.23, the two read different arrays, and each compiles better alone).
+template <class G, typename T, bool DX, bool DE>
+__global__ __launch_bounds__(G::kThreads, G::kBlocks) void products_kernel(const VocabArgs a,
+                                                                           int dx_blocks, T* dE) {
+  __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
+  const int block = blockIdx.x;
+  if (DX && (!DE || block < dx_blocks)) dx_tile<G, kParts<T>>(a, block, smem);
+  else if (DE) de_tile<G, T>(a, dE, block - dx_blocks, smem);
+}
+
 // dX[n] = the row's sums over the splits, rounded once; zero without target.
+// Each thread takes four columns of a row.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void dx_out_kernel(const VocabArgs a, T* dX) {
   const int64_t n = blockIdx.x;
   const int i = a.inv[n];
-  for (int c = threadIdx.x; c < a.d; c += kThreads) {
-    float x = 0.0f;
+  const bool vec = a.d % 4 == 0 && is_aligned(dX, 4 * sizeof(T));
+  const float* src = a.dXacc + static_cast<int64_t>(max(i, 0)) * a.ldx;
+  const int64_t stride = static_cast<int64_t>(a.np) * a.ldx;
+  for (int c = threadIdx.x * 4; c < a.d; c += kThreads * 4) {
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
     if (i >= 0)
-      for (int s = 0; s < a.splits; ++s)
-        x += a.dXacc[(static_cast<int64_t>(s) * a.np + i) * a.ldx + c];
-    dX[n * a.d + c] = from_float<T>(x);
+      for (int s0 = 0; s0 < a.splits; s0 += 4) {
+        f32x4 y[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          y[u] = *reinterpret_cast<const f32x4*>(src + min(s0 + u, a.splits - 1) * stride + c);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (s0 + u < a.splits) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[q] += y[u][q];
+          }
+      }
+    T* p = dX + n * a.d + c;
+    if (vec) {
+      store4<T>(p, x[0], x[1], x[2], x[3]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (c + q < a.d) p[q] = from_float<T>(x[q]);
+    }
   }
 }
 
@@ -964,7 +1086,7 @@ int check_call_shape(const VocabCall& c) {
   if (c.N < 1 || c.N > (1ll << 22)) return fail(DPG_ERR_INVALID_ARG, "N must be in [1, 2^22]");
   if (c.V < 1 || c.V > (1ll << 22)) return fail(DPG_ERR_INVALID_ARG, "V must be in [1, 2^22]");
   if (c.d < 1 || c.d > (1ll << 16)) return fail(DPG_ERR_INVALID_ARG, "d must be in [1, 2^16]");
-  if (c.k < 1 || c.k > 1024) return fail(DPG_ERR_INVALID_ARG, "k must be in [1, 1024]");
+  if (c.k < 1 || c.k > kMaxTop) return fail(DPG_ERR_INVALID_ARG, "k must be in [1, 1024]");
   if (c.dtype != DPG_FP32 && c.dtype != DPG_BF16) return fail(DPG_ERR_INVALID_ARG, "unknown dtype");
   return DPG_OK;
 }
@@ -978,53 +1100,61 @@ int check_call(const VocabCall& c, bool distill) {
   return DPG_OK;
 }
 
-// Bytes of D, and of the packed table, kept at a time.
-constexpr int64_t kPieceBytes = 512ll << 20;
+// Bytes of D, and of the packed table, kept at a time; of a packed table that
+// is needed only where the caller's is not 16-byte aligned.
+constexpr int64_t kPieceBytes = 512ll << 20, kRarePieceBytes = 64ll << 20;
 
 struct VocabPlan {
-  int64_t ldx = 0, np = 0, piece = 0;
+  int64_t ldx = 0, np = 0, piece = 0, packed_piece = 0;
   int32_t splits = 1;
+  bool packed = false;  // the table is packed whatever its alignment
   size_t off_flag, off_count, off_row, off_inv, off_q, off_ent, off_zt, off_qu, off_nu, off_bits,
       off_before, off_Xp, off_Ep, off_part, off_D, off_dX, total;
 };
+
+int64_t whole_pads(int64_t x) { return std::max<int64_t>(kPad, x / kPad * kPad); }
 
 VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, bool distill, bool grad) {
   VocabPlan p;
   const int64_t parts = dtype == DPG_BF16 ? 1 : 3;
   p.ldx = round_up(d, kStepK);
   p.np = round_up(N, kPad);
-  // one piece of the vocabulary: its D, and its packed table where one may be
-  // needed (fp32, rows that are not whole 16 bytes, or an unaligned table)
-  p.piece = kPieceBytes / (p.ldx * 2 * parts);
-  if (grad) p.piece = std::min(p.piece, kPieceBytes / (p.np * 2 * parts));
-  if (distill) p.piece = std::min<int64_t>({p.piece, kPieceBytes / (N * 10) * 64, 64 * kMaxWords});
-  p.piece = std::min(round_up(V, kPad), std::max<int64_t>(kPad, p.piece / kPad * kPad));
+  p.packed = parts > 1 || d % 8 != 0;
+  // one piece of the vocabulary: its D, its teacher ids' bits, and its packed
+  // table
+  const int64_t row_bytes = p.ldx * 2 * parts;
+  p.piece = round_up(V, kPad);
+  if (grad) p.piece = std::min(p.piece, whole_pads(kPieceBytes / (p.np * 2 * parts)));
+  if (distill)
+    p.piece = std::min({p.piece, whole_pads(kPieceBytes / (N * 10) * 64), int64_t{64 * kMaxWords}});
+  if (p.packed) p.piece = std::min(p.piece, whole_pads(kPieceBytes / row_bytes));
+  p.packed_piece = p.packed ? p.piece : std::min(p.piece, whole_pads(kRarePieceBytes / row_bytes));
   // dX has few tiles when rows are few: the sum over the vocabulary is then
-  // split so that the blocks fill the chip's 256 CUs, each with at least
-  // eight K steps
-  const int64_t tiles = p.np / kTile * ceil_div(p.ldx, kTile);
+  // split so that the blocks fill the chip's 256 CUs, each with at least two
+  // K steps
+  const int64_t tiles = p.np / BigTile::kTile * ceil_div(p.ldx, BigTile::kTile);
   p.splits = static_cast<int32_t>(
-      std::max<int64_t>(1, std::min<int64_t>(256 / tiles, p.piece / kStepK / 8)));
+      std::max<int64_t>(1, std::min<int64_t>(256 / tiles, p.piece / kStepK / 2)));
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off += align_up(bytes);
     return at;
   };
-  p.off_flag = take(N * 4);
+  p.off_flag = take(distill ? N * 4 : 0);
   p.off_count = take(4);
   p.off_row = take(N * 4);
   p.off_inv = take(N * 4);
   p.off_q = take(distill ? N * k * 4 : 0);
   p.off_ent = take(distill ? N * 4 : 0);
-  p.off_zt = take(N * k * 4);
+  p.off_zt = take(grad ? 0 : N * k * 4);
   p.off_qu = take(distill ? N * k * 4 : 0);
   p.off_nu = take(distill ? N * 4 : 0);
   p.off_bits = take(distill ? N * (p.piece / 64) * 8 : 0);
   p.off_before = take(distill ? N * (p.piece / 64) * 2 : 0);
   p.off_Xp = take(parts * p.np * p.ldx * 2);
-  p.off_Ep = take(parts * p.piece * p.ldx * 2);
-  p.off_part = take(grad ? 0 : ceil_div(V, kTile) * p.np * 8);
+  p.off_Ep = take(parts * p.packed_piece * p.ldx * 2);
+  p.off_part = take(grad ? 0 : ceil_div(V, SmallTile::kTile) * p.np * 8);
   p.off_D = take(grad ? parts * p.np * p.piece * 2 : 0);
   p.off_dX = take(grad ? p.splits * p.np * p.ldx * 4 : 0);
   p.total = off;
@@ -1058,12 +1188,12 @@ VocabArgs make_args(const VocabCall& c, const VocabPlan& p, char* ws) {
   a.bits = reinterpret_cast<uint64_t*>(ws + p.off_bits);
   a.before = reinterpret_cast<uint16_t*>(ws + p.off_before);
   a.Xp = reinterpret_cast<bf16*>(ws + p.off_Xp);
-  a.Ep = c.dtype == DPG_FP32 || c.d % 8 != 0 || !aligned(c.E, 16)
-             ? reinterpret_cast<bf16*>(ws + p.off_Ep) : nullptr;
+  const bool pack = p.packed || !aligned(c.E, 16);
+  a.Ep = pack ? reinterpret_cast<bf16*>(ws + p.off_Ep) : nullptr;
   a.part = reinterpret_cast<float2*>(ws + p.off_part);
   a.D = reinterpret_cast<bf16*>(ws + p.off_D);
   a.dXacc = reinterpret_cast<float*>(ws + p.off_dX);
-  a.ldd = static_cast<int32_t>(p.piece);
+  a.ldd = static_cast<int32_t>(pack ? p.packed_piece : p.piece);
   a.splits = p.splits;
   return a;
 }
@@ -1072,58 +1202,86 @@ unsigned blocks_of(int64_t n, int64_t per) { return static_cast<unsigned>(ceil_d
 // grid of tile_of_block for mt x nt tiles
 dim3 tile_grid(int64_t mt, int64_t nt) { return dim3(static_cast<unsigned>(round_up(mt * nt, 8))); }
 
-// Target weights, the packed rows and their X.
+// Target weights, then the packed rows; a launch of pack_kernel for rows and
+// the first piece of the table together, for the table alone afterwards.
 template <typename T>
-int prepare_rows(const VocabArgs& a, hipStream_t s) {
-  const dim3 b(kThreads);
-  if (a.t) hipLaunchKernelGGL(teacher_kernel, dim3(blocks_of(a.N, 4)), b, 0, s, a);
-  else hipLaunchKernelGGL(ce_flag_kernel, dim3(blocks_of(a.N, kThreads)), b, 0, s, a);
-  hipLaunchKernelGGL(rows_kernel, dim3(1), dim3(kRowThreads), 0, s, a);
-  hipLaunchKernelGGL(pack_rows_kernel<T>, dim3(static_cast<unsigned>(a.np)), b, 0, s, a);
-  return check_launch("vocab rows");
+void launch_pack(const VocabArgs& a, bool rows, hipStream_t s) {
+  const unsigned rb = rows ? blocks_of(a.N, kPackRows) + kPadBlocks : 0;
+  const unsigned tb = a.Ep ? blocks_of(round_up(a.vn, kPad), 4) : 0;
+  if (rb + tb)
+    hipLaunchKernelGGL(pack_kernel<T>, dim3(rb + tb), dim3(kThreads), 0, s, a, static_cast<int>(rb));
 }
 
-// fn for every piece of the vocabulary, its table packed first where needed,
-// its teacher ids found.
+// fn for every piece of the vocabulary, after its rows are packed and its
+// teacher ids found.
 template <typename T, class F>
 void for_pieces(VocabArgs& a, hipStream_t s, F fn) {
+  if (a.t) hipLaunchKernelGGL(teacher_kernel, dim3(blocks_of(a.N, 4)), dim3(kThreads), 0, s, a);
   for (int64_t v0 = 0; v0 < a.V; v0 += a.ldd) {
     a.v0 = static_cast<int32_t>(v0);
     a.vn = static_cast<int32_t>(std::min<int64_t>(a.ldd, a.V - v0));
-    if (a.Ep)
-      hipLaunchKernelGGL(pack_table_kernel<T>, dim3(static_cast<unsigned>(round_up(a.vn, kPad))),
-                         dim3(kThreads), 0, s, a);
+    launch_pack<T>(a, v0 == 0, s);
     if (a.t)
       hipLaunchKernelGGL(teacher_ids_kernel, dim3(static_cast<unsigned>(a.N)), dim3(kThreads), 0, s, a);
     fn();
   }
 }
 
+// fn with the tile to use for a launch of `tiles` big tiles. Fewer than three
+// for every four CUs leave too much of the chip idle, and a K step of a big
+// tile takes 64 KiB through a CU's LDS where a small one takes 32 (128 rows x
+// 64 against 1000 columns, fp32: 18 us big, 12 us small; 252 big tiles of dX
+// at 999 x 768 x 32003, fp32: 311 us big, 424 us small). With at most 128 rows
+// half of a big tile would be padding (4 rows x 2048 against 50304 columns:
+// 53 us big, 40 us small).
+template <class F>
+void with_tile(int64_t tiles, int64_t rows, F fn) {
+  if (tiles >= 192 && rows > SmallTile::kTile) fn(BigTile());
+  else fn(SmallTile());
+}
+
 template <typename T>
 int run_loss(VocabArgs a, hipStream_t s) {
-  if (const int st = prepare_rows<T>(a, s)) return st;
-  for_pieces<T>(a, s, [&] {
-    const dim3 g = tile_grid(ceil_div(a.vn, kTile), a.np / kTile), b(kTileThreads);
-    const int tile0 = a.v0 / kTile;
-    if (a.t) hipLaunchKernelGGL((stats_kernel<kParts<T>, true>), g, b, 0, s, a, tile0);
-    else hipLaunchKernelGGL((stats_kernel<kParts<T>, false>), g, b, 0, s, a, tile0);
+  with_tile(ceil_div(std::min(a.ldd, a.V), BigTile::kTile) * (a.np / BigTile::kTile), a.N, [&](auto g) {
+    typedef decltype(g) G;
+    for_pieces<T>(a, s, [&] {
+      const dim3 grid = tile_grid(ceil_div(a.vn, G::kTile), a.np / G::kTile), b(G::kThreads);
+      const int tile0 = a.v0 / G::kTile;
+      if (a.t) hipLaunchKernelGGL((stats_kernel<G, kParts<T>, true>), grid, b, 0, s, a, tile0);
+      else hipLaunchKernelGGL((stats_kernel<G, kParts<T>, false>), grid, b, 0, s, a, tile0);
+    });
+    hipLaunchKernelGGL(lse_kernel, dim3(blocks_of(a.N, 4)), dim3(kThreads), 0, s, a,
+                       static_cast<int>(ceil_div(a.V, G::kTile)));
   });
-  hipLaunchKernelGGL(lse_kernel, dim3(blocks_of(a.N, 4)), dim3(kThreads), 0, s, a,
-                     static_cast<int>(ceil_div(a.V, kTile)));
   return check_launch("vocab loss");
 }
 
 template <typename T>
 int run_grad(VocabArgs a, void* dX, void* dE, hipStream_t s) {
-  if (const int st = prepare_rows<T>(a, s)) return st;
-  const dim3 b(kTileThreads);
-  const int64_t rt = a.np / kTile, ct = ceil_div(a.ldx, kTile);
+  const int64_t big = BigTile::kTile, rt = a.np / big, ct = ceil_div(a.ldx, big);
   for_pieces<T>(a, s, [&] {
-    const int64_t vt = ceil_div(a.vn, kTile);
-    if (a.t) hipLaunchKernelGGL((grad_logits_kernel<kParts<T>, true>), tile_grid(vt, rt), b, 0, s, a);
-    else hipLaunchKernelGGL((grad_logits_kernel<kParts<T>, false>), tile_grid(vt, rt), b, 0, s, a);
-    if (dX) hipLaunchKernelGGL(dx_kernel<kParts<T>>, tile_grid(rt, ct * a.splits), b, 0, s, a);
-    if (dE) hipLaunchKernelGGL(de_kernel<T>, tile_grid(vt, ct), b, 0, s, a, static_cast<T*>(dE));
+    const int64_t vt = ceil_div(a.vn, big);
+    with_tile(vt * rt, a.N, [&](auto g) {
+      typedef decltype(g) G;
+      const dim3 grid = tile_grid(ceil_div(a.vn, G::kTile), a.np / G::kTile), b(G::kThreads);
+      if (a.t) hipLaunchKernelGGL((grad_logits_kernel<G, kParts<T>, true>), grid, b, 0, s, a);
+      else hipLaunchKernelGGL((grad_logits_kernel<G, kParts<T>, false>), grid, b, 0, s, a);
+    });
+    with_tile((dX ? rt * ct * a.splits : 0) + (dE ? vt * ct : 0), a.N, [&](auto g) {
+      typedef decltype(g) G;
+      const int64_t gct = ceil_div(a.ldx, G::kTile);
+      const unsigned nx = dX ? tile_grid(a.np / G::kTile, gct * a.splits).x : 0;
+      const unsigned ne = dE ? tile_grid(ceil_div(a.vn, G::kTile), gct).x : 0;
+      const dim3 b(G::kThreads);
+      T* de = static_cast<T*>(dE);
+      if (G::kTile == SmallTile::kTile && dX && dE) {
+        hipLaunchKernelGGL((products_kernel<SmallTile, T, true, true>), dim3(nx + ne), b, 0, s, a,
+                           static_cast<int>(nx), de);
+        return;
+      }
+      if (dX) hipLaunchKernelGGL((products_kernel<G, T, true, false>), dim3(nx), b, 0, s, a, 0, de);
+      if (dE) hipLaunchKernelGGL((products_kernel<G, T, false, true>), dim3(ne), b, 0, s, a, 0, de);
+    });
   });
   if (dX)
     hipLaunchKernelGGL(dx_out_kernel<T>, dim3(static_cast<unsigned>(a.N)), dim3(kThreads), 0, s, a,

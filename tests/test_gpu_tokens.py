@@ -465,3 +465,20 @@ def test_binding_refusals():
         dpg.dpg_embed_grad(ids.view(2, 2), X.view(2, 2, 16), 9, accumulate=True)
     with pytest.raises(dpg.DpgError):
         dpg.dpg_embed_grad(ids.view(2, 2), X.view(2, 2, 16), 0)
+
+
+def test_distillation_id_named_with_and_without_weight():
+    """An id named first with a logit of -inf and again with a finite one."""
+    import dp_grape_projection_amd as dpg
+    X, E, _, _, g = _loss_case(4, 64, 300, 1, "fp32", 11)
+    ids = np.array([[7, 7, 9], [9, 7, 7], [7, 9, 7], [5, 5, 5]])
+    t = np.array([[-np.inf, 1.0, 0.5], [0.5, -np.inf, 1.0], [1.0, 0.5, -np.inf],
+                  [-np.inf, -np.inf, 2.0]], np.float32)
+    q = ot.teacher_weights(ids, t, 300, 1.0)
+    _, _, want_dX, want_dE = ot.target_loss(X, E, ids, q, 1.0, 1.0, g)
+    x, e, y, tt = _dev(X, "fp32"), _dev(E, "fp32"), _dev(ids), _dev(t)
+    loss, lse = dpg.dpg_distill_loss(x, e, y, tt)
+    _check_loss(X, E, ids, q, loss, lse, 1.0, 1.0)
+    dX, dE = dpg.dpg_distill_loss_grad(x, e, y, tt, lse, _dev(g))
+    assert rel_err(_host(dX), want_dX) <= TOL["fp32"]
+    assert rel_err(_host(dE), want_dE) <= TOL["fp32"]
