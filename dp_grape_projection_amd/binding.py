@@ -178,18 +178,25 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 def _require(t: torch.Tensor, name: str, dtype=None, shape=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+# The current stream's handle without building a torch.cuda.Stream (3 us of
+# host time a call), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream_handle(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
@@ -558,8 +565,9 @@ def _ids(t, name: str, shape=None):
 
 
 def _same_device(ref: torch.Tensor, **tensors):
+    at = ref.get_device()
     for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
+        if t is not None and t.get_device() != at:
             raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
 
 

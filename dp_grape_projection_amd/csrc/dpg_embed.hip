@@ -473,6 +473,59 @@ __global__ __launch_bounds__(kThreads) void embed_run_norm_kernel(const TY* dY, 
   if (threadIdx.x == 0) run_sq[pos] = ((red[0] + red[1]) + red[2]) + red[3];
 }
 
+// The same for short samples, without sorting: one block per position compares
+// its id with its sample's other ids (T * 8 bytes of L2 reads a block); the
+// first position of a run lists the others in LDS, in order.
+constexpr int kShortSample = 1024;
+template <typename TY, int W>
+__global__ __launch_bounds__(kThreads) void embed_short_norm_kernel(const int64_t* ids,
+                                                                    const TY* dY, int64_t V, int d,
+                                                                    int T, float scale,
+                                                                    float* run_sq) {
+  __shared__ int list[kShortSample];
+  __shared__ int wave_cnt[kShortSample / 64];
+  __shared__ float red[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int pos = blockIdx.x, first = pos / T * T;
+  const int64_t id = ids[pos];
+  if (id < 0 || id >= V) return;
+  constexpr int kPer = kShortSample / kThreads;
+  uint64_t same[kPer];
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int at = q * kThreads + tid;
+    same[q] = __ballot(at < T && ids[first + min(at, T - 1)] == id);
+    if (lane == 0) wave_cnt[q * 4 + wave] = __popcll(same[q]);
+  }
+  __syncthreads();
+  int all = 0;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    for (int w = 0; w < 4; ++w) {
+      if (w == wave && (same[q] >> lane) & 1)
+        list[all + __popcll(same[q] & ((1ull << lane) - 1))] = first + q * kThreads + tid;
+      all += wave_cnt[q * 4 + w];
+    }
+  }
+  __syncthreads();
+  if (list[0] != pos) {  // the run's first position
+    if (tid == 0) run_sq[pos] = 0.0f;
+    return;
+  }
+  float sq = 0.0f;
+  for (int g = 0; g * kThreads * 8 < d; ++g) {
+    const RowCols<W> rc(g, tid, kThreads, d);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    add_rows(dY, list, 0, all, rc, [](int) { return 1.0f; }, acc);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sq = fmaf(scale * acc[q], scale * acc[q], sq);
+  }
+  sq = wave_sum(sq);
+  if (lane == 0) red[wave] = sq;
+  __syncthreads();
+  if (tid == 0) run_sq[pos] = ((red[0] + red[1]) + red[2]) + red[3];
+}
+
 // norm_sq[i] += the run norms at sample i's positions, in a fixed order.
 __global__ __launch_bounds__(kThreads) void embed_norm_sum_kernel(const int64_t* ids, int64_t V,
                                                                   int T, const float* run_sq,
@@ -571,6 +624,8 @@ SortPlan plan_sort(int64_t n, int64_t V, int64_t d) {
   p.bins = static_cast<int>(((V - 1) >> p.g_log2) + 1);
   p.off_order = align_up((static_cast<size_t>(1) << p.g_log2) * (p.bins + 1) * 4);
   p.off_run = p.off_order + align_up(static_cast<size_t>(n) * 4);
+  // (up to 128 tokens, a launch for the chunks costs more than the longest sum)
+  if (n <= 128) p.chunk = 128;
   while (n > 512ll * p.chunk) p.chunk *= 2;
   p.chunks = static_cast<int>(ceil_div(n, p.chunk));
   // (the norms' runs and the gradient's chunks are never needed together)
@@ -666,11 +721,23 @@ int dpg_embed_norms(const int64_t* ids, const void* dY, int64_t B, int64_t T, in
   if (const int st = check_ws(workspace, workspace_bytes, p.total)) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  if (const int st = sort_tokens(p, ids, B * T, V, ws, s)) return st;
+  // few positions of short samples are compared with each other, others sorted:
+  // at 128 positions 5 us against 8 + 3, at 2331 (T = 333) 13 against 9 + 11, at
+  // 8192 (T = 512) 34 against 10 + 24, and comparing grows with T
+  const bool sorted = T > kShortSample || B * T > 4096;
+  if (sorted)
+    if (const int st = sort_tokens(p, ids, B * T, V, ws, s)) return st;
   float* run_sq = reinterpret_cast<float*>(ws + p.off_run);
   auto go = [&](auto zero) {
     typedef decltype(zero) TY;
     with_width(row_vector(d, dY, dY), [&](auto w) {
+      if (!sorted) {
+        hipLaunchKernelGGL((embed_short_norm_kernel<TY, decltype(w)::value>),
+                           dim3(static_cast<unsigned>(B * T)), dim3(kThreads), 0, s, ids,
+                           static_cast<const TY*>(dY), V, static_cast<int>(d),
+                           static_cast<int>(T), static_cast<float>(scale), run_sq);
+        return;
+      }
       hipLaunchKernelGGL((embed_run_norm_kernel<TY, decltype(w)::value>),
                          dim3(static_cast<unsigned>(B * T)), dim3(kThreads), 0, s,
                          static_cast<const TY*>(dY), static_cast<int>(d), p.sorted(ids, ws),

@@ -89,6 +89,9 @@ struct VocabArgs {
   int32_t* count;       // [1] packed rows
   int32_t* row;         // [N] packed -> row
   int32_t* inv;         // [N] row -> packed, -1
+  int32_t* target;      // [np] packed: cross entropy's target, else -1
+  float* g;             // [np] packed: dloss c tau, 0 past the last row
+  float* lse2;          // [np] packed: lse log2(e), 0 past the last row
   float* q;             // [N][k] target weights (distillation)
   float* ent;           // [N] sum q ln q (distillation)
   float* zt;            // [N][k] packed: logits of the target, or of the
@@ -246,6 +249,10 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
     const int end = (before + kPad - 1) / kPad * kPad;
     for (int q = 0; q < kPackRows / 4; ++q) {
       const int i = before + pad * kPackRows + q * 4 + wave;
+      if (i < end && lane == 0) {
+        a.target[i] = -1;
+        if (a.dloss) a.g[i] = a.lse2[i] = 0.0f;
+      }
       if (i < end)
         pack_row(static_cast<const T*>(a.X), a.Xp + static_cast<int64_t>(i) * a.ldx, 0, a.ldx,
                  part_stride, true, lane);
@@ -257,7 +264,14 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
   const uint64_t b = __ballot(mine_on);
   if (wave == 0 && lane < kPackRows && mine < a.N) {
     const int at = before + __popcll(b & ((1ull << lane) - 1));
-    if (mine_on) a.row[at] = mine;
+    if (mine_on) {
+      a.row[at] = mine;
+      a.target[at] = a.t ? -1 : static_cast<int32_t>(a.ids[mine]);
+      if (a.dloss) {
+        a.g[at] = a.dloss[mine] * a.dscale;
+        a.lse2[at] = a.lse[mine] * kLog2e;
+      }
+    }
     a.inv[mine] = mine_on ? at : -1;
   }
   const bool vec = a.d % VN == 0 && is_aligned(a.X, 16);
@@ -672,18 +686,19 @@ __device__ __forceinline__ Operand rows_operand(const bf16* base, int64_t ld, in
 // row: the 64 columns from column c0 of the piece, of them the lane's quarter
 // (4 kq .. 4 kq + 3 of every 16).
 struct LaneIds {
-  uint64_t word, mine;
-  int64_t at;  // the word's index
-  __device__ __forceinline__ void load(const VocabArgs& a, int r, int rows, int c0, int kq) {
-    at = static_cast<int64_t>(r) * (a.ldd / 64) + c0 / 64;
-    word = r < rows ? a.bits[at] : 0;
-    mine = word & (0x000F000F000F000Full << (4 * kq));
+  uint64_t word;
+  __device__ __forceinline__ static int64_t index(const VocabArgs& a, int r, int c0) {
+    return static_cast<int64_t>(r) * (a.ldd / 64) + c0 / 64;
+  }
+  __device__ __forceinline__ void load(const VocabArgs& a, int r, int rows, int c0) {
+    word = r < rows ? a.bits[index(a, r, c0)] : 0;
   }
   // fn(column - 4 kq in the accumulator's order, place in qu) for each of them
   template <class F>
-  __device__ __forceinline__ void each(const VocabArgs& a, int r, int kq, F fn) {
+  __device__ __forceinline__ void each(const VocabArgs& a, int r, int c0, int kq, F fn) const {
+    uint64_t mine = word & (0x000F000F000F000Full << (4 * kq));
     if (!mine) return;
-    const int64_t base = static_cast<int64_t>(r) * a.k + a.before[at];
+    const int64_t base = static_cast<int64_t>(r) * a.k + a.before[index(a, r, c0)];
     while (mine) {
       const int b = __ffsll(static_cast<unsigned long long>(mine)) - 1;
       mine &= mine - 1;
@@ -692,76 +707,110 @@ struct LaneIds {
   }
 };
 
-// Each row's maximum and sum of exponentials over a 256-column tile, and
-// cross entropy's target logit. Works in base 2: z log2(e).
-template <class G, int PARTS, bool TEACHER>
-__global__ __launch_bounds__(G::kThreads, G::kBlocks) void stats_kernel(const VocabArgs a, int tile0) {
-  __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
-  int mt, nt;
-  if (!tile_of_block(blockIdx.x, (a.vn + G::kTile - 1) / G::kTile, row_tiles<G>(a), mt, nt)) return;
-  const int c0 = mt * G::kTile, r0 = nt * G::kTile, rows = a.count[0];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
-  LaneIds ids[G::kNB][G::kWaveM / 64];
-  if constexpr (TEACHER) {
-#pragma unroll
-    for (int nb = 0; nb < G::kNB; ++nb)
-#pragma unroll
-      for (int h = 0; h < G::kWaveM / 64; ++h)
-        ids[nb][h].load(a, r0 + G::kWaveN * wn + 16 * nb + r16, rows, c0 + G::kWaveM * wm + 64 * h, kq);
-  }
-  typename G::Acc acc;
+// A 256 x 256 (128 x 128) tile of logits z / (zscale), before its scale: E's
+// rows against packed rows.
+template <class G, int PARTS>
+__device__ __forceinline__ void logits_tile(const VocabArgs& a, int c0, int r0, char* smem,
+                                            typename G::Acc& acc) {
   tile_product<G, PARTS, false, false>(
       table_operand(a, false, c0, 0),
       rows_operand(a.Xp + static_cast<int64_t>(r0) * a.ldx, a.ldx,
                    static_cast<int64_t>(a.np) * a.ldx, G::kTile, a.ldx),
       a.ldx / kStepK, smem, acc);
-  const int left = a.vn - c0 - G::kWaveM * wm - 4 * kq;  // columns from the lane's first
-  const float z2 = a.zscale * kLog2e;
+}
+
+// fn(std::true_type) where a tile reaches past the piece's last column,
+// fn(std::false_type) for the others, whose columns need no test.
+template <class F>
+__device__ __forceinline__ void with_edge(bool edge, F fn) {
+  if (edge) fn(std::true_type{});
+  else fn(std::false_type{});
+}
+
+// Each row's maximum and sum of exponentials over a tile's columns, and the
+// logits of the targets there. Works in base 2: z log2(e). What a row needs is
+// loaded before the product, so that its latency hides behind it.
+template <class G, int PARTS, bool TEACHER>
+__global__ __launch_bounds__(G::kThreads, G::kBlocks) void stats_kernel(const VocabArgs a, int tile0) {
+  __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
+  int mt, nt;
+  if (!tile_of_block(blockIdx.x, (a.vn + G::kTile - 1) / G::kTile, row_tiles<G>(a), mt, nt)) return;
+  const int c0 = mt * G::kTile, r0 = nt * G::kTile;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
+  const int cl = c0 + G::kWaveM * wm + 4 * kq, rl = r0 + G::kWaveN * wn + r16;  // the lane's first
+  LaneIds ids[G::kNB][G::kWaveM / 64];
+  int at[G::kNB];
+#pragma unroll
+  for (int nb = 0; nb < G::kNB; ++nb) {
+    if constexpr (TEACHER) {
+#pragma unroll
+      for (int h = 0; h < G::kWaveM / 64; ++h)
+        ids[nb][h].load(a, rl + 16 * nb, a.count[0], c0 + G::kWaveM * wm + 64 * h);
+    } else {
+      at[nb] = a.target[rl + 16 * nb];
+    }
+  }
+  typename G::Acc acc;
+  logits_tile<G, PARTS>(a, c0, r0, smem, acc);
+  const int left = a.vn - cl;
+  float z2 = a.zscale * kLog2e;
   float m[G::kNB], s[G::kNB];
 #pragma unroll
   for (int nb = 0; nb < G::kNB; ++nb) {
-    m[nb] = -INFINITY;
+    auto logit = [&](int at, float* to) {  // (written where the lane holds it)
+      float z = 0.0f;
 #pragma unroll
-    for (int mb = 0; mb < G::kMB; ++mb)
+      for (int mb = 0; mb < G::kMB; ++mb)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float z = acc.v[mb][nb][i] * z2;
-        acc.v[mb][nb][i] = z;
-        if (16 * mb + i < left) m[nb] = fmaxf(m[nb], z);
-      }
-    m[nb] = fmaxf(m[nb], __shfl_xor(m[nb], 16, 64));
-    m[nb] = fmaxf(m[nb], __shfl_xor(m[nb], 32, 64));
-    s[nb] = 0.0f;
-    // (a wave whose columns all lie past the end has no maximum)
-    const float ref = m[nb] == -INFINITY ? 0.0f : m[nb];
+        for (int i = 0; i < 4; ++i) z = at == 16 * mb + i ? acc.v[mb][nb][i] : z;
+      if ((at & 15) < 4) *to = z * a.zscale;
+    };
+    const int r = rl + 16 * nb;
+    if constexpr (TEACHER) {
 #pragma unroll
-    for (int mb = 0; mb < G::kMB; ++mb)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (16 * mb + i < left) s[nb] += exp2_(acc.v[mb][nb][i] - ref);
-    s[nb] += __shfl_xor(s[nb], 16, 64);
-    s[nb] += __shfl_xor(s[nb], 32, 64);
+      for (int h = 0; h < G::kWaveM / 64; ++h)
+        ids[nb][h].each(a, r, c0 + G::kWaveM * wm + 64 * h, kq, [&](int at, int64_t place) { logit(64 * h + at, a.zt + place); });
+    } else {
+      const int c = at[nb] - a.v0 - cl;
+      if (at[nb] >= 0 && c >= 0 && c < G::kWaveM) logit(c, a.zt + r);
+    }
   }
+  if (z2 < 0.0f) {
+    z2 = -z2;
 #pragma unroll
-  for (int nb = 0; nb < G::kNB; ++nb) {
-    const int r = r0 + G::kWaveN * wn + 16 * nb + r16;
-    auto logit = [&](int at, float* to) {
+    for (int mb = 0; mb < G::kMB; ++mb)
+#pragma unroll
+      for (int nb = 0; nb < G::kNB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc.v[mb][nb][i] = -acc.v[mb][nb][i];
+  }
+  with_edge(c0 + G::kTile > a.vn, [&](auto edge) {
+    constexpr bool E = decltype(edge)::value;
+#pragma unroll
+    for (int nb = 0; nb < G::kNB; ++nb) {
+      float x = -INFINITY;
 #pragma unroll
       for (int mb = 0; mb < G::kMB; ++mb)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (at == 16 * mb + i) *to = acc.v[mb][nb][i] * kLn2;
-    };
-    if constexpr (TEACHER) {
+          if (!E || 16 * mb + i < left) x = fmaxf(x, acc.v[mb][nb][i]);
+      x = fmaxf(x, __shfl_xor(x, 16, 64));
+      x = fmaxf(x, __shfl_xor(x, 32, 64));
+      // (a wave whose columns all lie past the end has no maximum)
+      const float ref = x == -INFINITY ? 0.0f : x * z2;
+      float t = 0.0f;
 #pragma unroll
-      for (int h = 0; h < G::kWaveM / 64; ++h)
-        ids[nb][h].each(a, r, kq, [&](int at, int64_t place) { logit(64 * h + at, a.zt + place); });
-    } else {
-      const int64_t at = r < rows ? a.ids[a.row[r]] - a.v0 - c0 - G::kWaveM * wm - 4 * kq : -1;
-      if (at >= 0 && at < G::kWaveM) logit(static_cast<int>(at), a.zt + r);
+      for (int mb = 0; mb < G::kMB; ++mb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!E || 16 * mb + i < left) t += exp2_(fmaf(acc.v[mb][nb][i], z2, -ref));
+      t += __shfl_xor(t, 16, 64);
+      t += __shfl_xor(t, 32, 64);
+      m[nb] = x == -INFINITY ? x : ref;
+      s[nb] = t;
     }
-  }
+  });
   // the waves that share a row
   float2* red = reinterpret_cast<float2*>(smem);
   __syncthreads();
@@ -837,53 +886,64 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void grad_logits_kernel(co
   __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
   int mt, nt;
   if (!tile_of_block(blockIdx.x, (a.vn + G::kTile - 1) / G::kTile, row_tiles<G>(a), mt, nt)) return;
-  const int c0 = mt * G::kTile, r0 = nt * G::kTile, rows = a.count[0];
+  const int c0 = mt * G::kTile, r0 = nt * G::kTile;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
+  const int cl = c0 + G::kWaveM * wm + 4 * kq, rl = r0 + G::kWaveN * wn + r16;  // the lane's first
   LaneIds ids[G::kNB][G::kWaveM / 64];
-  if constexpr (TEACHER) {
-#pragma unroll
-    for (int nb = 0; nb < G::kNB; ++nb)
-#pragma unroll
-      for (int h = 0; h < G::kWaveM / 64; ++h)
-        ids[nb][h].load(a, r0 + G::kWaveN * wn + 16 * nb + r16, rows, c0 + G::kWaveM * wm + 64 * h, kq);
-  }
-  typename G::Acc acc;
-  tile_product<G, PARTS, false, false>(
-      table_operand(a, false, c0, 0),
-      rows_operand(a.Xp + static_cast<int64_t>(r0) * a.ldx, a.ldx,
-                   static_cast<int64_t>(a.np) * a.ldx, G::kTile, a.ldx),
-      a.ldx / kStepK, smem, acc);
-  const int left = a.vn - c0 - G::kWaveM * wm - 4 * kq;
-  const float z2 = a.zscale * kLog2e;
+  int at[G::kNB];
+  float g[G::kNB], lse2[G::kNB];
 #pragma unroll
   for (int nb = 0; nb < G::kNB; ++nb) {
-    const int r = r0 + G::kWaveN * wn + 16 * nb + r16;
-    const bool in = r < rows;
-    const int n = in ? a.row[r] : 0;
-    const float g = in ? a.dloss[n] * a.dscale : 0.0f;
-    const float lse2 = in ? a.lse[n] * kLog2e : 0.0f;
-    const int64_t at = in && !TEACHER ? a.ids[n] - a.v0 - c0 - G::kWaveM * wm - 4 * kq : -1;
-#pragma unroll
-    for (int mb = 0; mb < G::kMB; ++mb)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = 16 * mb + i;
-        float p = exp2_(fmaf(acc.v[mb][nb][i], z2, -lse2));
-        if (!TEACHER && at == c) p -= 1.0f;
-        acc.v[mb][nb][i] = in && c < left ? g * p : 0.0f;
-      }
     if constexpr (TEACHER) {
 #pragma unroll
       for (int h = 0; h < G::kWaveM / 64; ++h)
-        ids[nb][h].each(a, r, kq, [&](int at, int64_t place) {
-          const float gq = g * a.qu[place];
+        ids[nb][h].load(a, rl + 16 * nb, a.count[0], c0 + G::kWaveM * wm + 64 * h);
+    } else {
+      at[nb] = a.target[rl + 16 * nb];
+    }
+  }
+  auto load_rows = [&] {
 #pragma unroll
-          for (int mb = 4 * h; mb < 4 * h + 4; ++mb)
+    for (int nb = 0; nb < G::kNB; ++nb) {
+      g[nb] = a.g[rl + 16 * nb];
+      lse2[nb] = a.lse2[rl + 16 * nb];
+    }
+  };
+  if (!TEACHER) load_rows();  // (with the teacher's bits the registers are full)
+  typename G::Acc acc;
+  logits_tile<G, PARTS>(a, c0, r0, smem, acc);
+  if (TEACHER) load_rows();
+  const int left = a.vn - cl;
+  const float z2 = a.zscale * kLog2e;
+  with_edge(c0 + G::kTile > a.vn, [&](auto edge) {
+    constexpr bool E = decltype(edge)::value;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (64 * h + at == 16 * mb + i) acc.v[mb][nb][i] -= gq;
-        });
+    for (int nb = 0; nb < G::kNB; ++nb)
+#pragma unroll
+      for (int mb = 0; mb < G::kMB; ++mb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = g[nb] * exp2_(fmaf(acc.v[mb][nb][i], z2, -lse2[nb]));
+          acc.v[mb][nb][i] = !E || 16 * mb + i < left ? x : 0.0f;
+        }
+  });
+#pragma unroll
+  for (int nb = 0; nb < G::kNB; ++nb) {
+    auto subtract = [&](int at, float q) {
+#pragma unroll
+      for (int mb = 0; mb < G::kMB; ++mb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc.v[mb][nb][i] -= at == 16 * mb + i ? q : 0.0f;
+    };
+    if constexpr (TEACHER) {
+#pragma unroll
+      for (int h = 0; h < G::kWaveM / 64; ++h)
+        ids[nb][h].each(a, rl + 16 * nb, c0 + G::kWaveM * wm + 64 * h, kq,
+                        [&](int at, int64_t place) { subtract(64 * h + at, g[nb] * a.qu[place]); });
+    } else {
+      const int c = at[nb] - a.v0 - cl;
+      if (at[nb] >= 0 && c >= 0 && c < G::kWaveM) subtract(c, g[nb]);
     }
   }
   bf16* dst = a.D + static_cast<int64_t>(r0) * a.ldd + c0;
@@ -1108,7 +1168,7 @@ struct VocabPlan {
   int64_t ldx = 0, np = 0, piece = 0, packed_piece = 0;
   int32_t splits = 1;
   bool packed = false;  // the table is packed whatever its alignment
-  size_t off_flag, off_count, off_row, off_inv, off_q, off_ent, off_zt, off_qu, off_nu, off_bits,
+  size_t off_flag, off_count, off_row, off_inv, off_target, off_g, off_lse2, off_q, off_ent, off_zt, off_qu, off_nu, off_bits,
       off_before, off_Xp, off_Ep, off_part, off_D, off_dX, total;
 };
 
@@ -1145,6 +1205,9 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   p.off_count = take(4);
   p.off_row = take(N * 4);
   p.off_inv = take(N * 4);
+  p.off_target = take(p.np * 4);
+  p.off_g = take(grad ? p.np * 4 : 0);
+  p.off_lse2 = take(grad ? p.np * 4 : 0);
   p.off_q = take(distill ? N * k * 4 : 0);
   p.off_ent = take(distill ? N * 4 : 0);
   p.off_zt = take(grad ? 0 : N * k * 4);
@@ -1180,6 +1243,9 @@ VocabArgs make_args(const VocabCall& c, const VocabPlan& p, char* ws) {
   a.count = reinterpret_cast<int32_t*>(ws + p.off_count);
   a.row = reinterpret_cast<int32_t*>(ws + p.off_row);
   a.inv = reinterpret_cast<int32_t*>(ws + p.off_inv);
+  a.target = reinterpret_cast<int32_t*>(ws + p.off_target);
+  a.g = reinterpret_cast<float*>(ws + p.off_g);
+  a.lse2 = reinterpret_cast<float*>(ws + p.off_lse2);
   a.q = reinterpret_cast<float*>(ws + p.off_q);
   a.ent = reinterpret_cast<float*>(ws + p.off_ent);
   a.zt = reinterpret_cast<float*>(ws + p.off_zt);
