@@ -13,3 +13,4 @@ from .binding import (  # noqa: F401
     project_workspace_size, static_scratch_bytes, timing_enable, timing_read, version,
 )
 from .streaming import GrapeOptimizer, ProjectedLinear  # noqa: F401
+from .tokens import TokenEmbedding, distill_cross_entropy, vocab_cross_entropy  # noqa: F401

@@ -70,14 +70,23 @@ class GrapeOptimizer:
     the first projected layer must require grad (for instance x.requires_grad_
     on the model input) so that autograd reaches every layer.
     proj_step = step when proj_period = 1, else (step - 1) // proj_period + 1
-    (P then changes every proj_period steps)."""
+    (P then changes every proj_period steps).
+
+    embeddings: TokenEmbedding tables that take part. A table's gradient is
+    not projected: its per-sample norms join the clip (dpg_embed_norms), its
+    sum takes the clip factors (dpg_embed_grad) and noise sigma C Z from the
+    stream of its own layer id, and the update is plain:
+    table -= table_lr * (sum_i s_i g_i + sigma C Z) / B."""
 
     def __init__(self, layers: Sequence[ProjectedLinear], r: int, clip_C: float,
                  sigma: float, seed: int, lr: float, beta1: float = 0.9,
                  beta2: float = 0.999, eps: float = 1e-8, proj_period: int = 1,
-                 keep_inputs: bool = False):
+                 keep_inputs: bool = False, embeddings: Sequence = (),
+                 table_lr: Optional[float] = None):
         self.layers: List[ProjectedLinear] = list(layers)
-        ids = [l.layer_id for l in self.layers]
+        self.embeddings = list(embeddings)
+        self.table_lr = lr if table_lr is None else table_lr
+        ids = [l.layer_id for l in self.layers + self.embeddings]
         if len(set(ids)) != len(ids):
             raise ValueError("layer ids must be unique")
         self.r, self.clip_C, self.sigma, self.seed = int(r), clip_C, sigma, int(seed)
@@ -95,7 +104,8 @@ class GrapeOptimizer:
         self.dtype: Optional[torch.dtype] = None
         self.last_norms: Optional[torch.Tensor] = None
         self.last_G_priv: Optional[List[torch.Tensor]] = None
-        for l in self.layers:
+        self.tokens: Dict[int, tuple] = {}  # layer id -> (ids, dY) of this step
+        for l in self.layers + self.embeddings:
             l._grape = self
 
     @property
@@ -106,16 +116,47 @@ class GrapeOptimizer:
         self.t += 1
         self._done.clear()
         self.inputs.clear()
+        self.tokens.clear()
         if self.norm_sq is not None:
             self.norm_sq.zero_()
 
-    def _capture(self, layer: ProjectedLinear, x: torch.Tensor, y: torch.Tensor):
+    def _begin(self, B: int, device) -> None:
         if self.t == 0:
             raise RuntimeError("call zero_grad() before the forward pass of a step")
+        if self.norm_sq is None or int(self.norm_sq.shape[0]) != B:
+            self.norm_sq = torch.zeros(B, dtype=torch.float32, device=device)
+
+    def _capture_tokens(self, layer, ids: torch.Tensor, y: torch.Tensor):
+        self._begin(int(ids.shape[0]), y.device)
+
+        def on_grad(g: torch.Tensor):
+            if layer.layer_id in self._done:
+                raise RuntimeError(f"layer {layer.layer_id} ran twice in one step")
+            dY = g.detach().contiguous()
+            _b.dpg_embed_norms(ids, dY, int(layer.table.shape[0]), self.norm_sq,
+                               scale=layer.scale)
+            self.tokens[layer.layer_id] = (ids, dY)
+            self._done.add(layer.layer_id)
+            return None
+
+        y.register_hook(on_grad)
+
+    def _update_table(self, layer, norms: torch.Tensor) -> None:
+        ids, dY = self.tokens[layer.layer_id]
+        V, d = (int(n) for n in layer.table.shape)
+        B = int(ids.shape[0])
+        s = torch.clamp(self.clip_C / norms, max=1.0)  # norm 0 gives inf, so 1
+        G = _b.dpg_embed_grad(ids, dY, V, scale=layer.scale, sample_scales=s)
+        if self.sigma > 0:
+            Z = _b.dpg_philox_normals(self.seed, layer.layer_id, self.t, 1, 0, V * d,
+                                      device=G.device)
+            G.add_(Z.view(V, d), alpha=self.sigma * self.clip_C)
+        layer.table.add_(G, alpha=-self.table_lr / B)
+
+    def _capture(self, layer: ProjectedLinear, x: torch.Tensor, y: torch.Tensor):
         A = x.detach().contiguous()
         B = int(A.shape[0])
-        if self.norm_sq is None or int(self.norm_sq.shape[0]) != B:
-            self.norm_sq = torch.zeros(B, dtype=torch.float32, device=A.device)
+        self._begin(B, A.device)
         if self.dtype is None:
             self.dtype = A.dtype
 
@@ -137,7 +178,8 @@ class GrapeOptimizer:
         y.register_hook(on_grad)
 
     def step(self) -> None:
-        missing = [l.layer_id for l in self.layers if l.layer_id not in self._done]
+        missing = [l.layer_id for l in self.layers + self.embeddings
+                   if l.layer_id not in self._done]
         if missing:
             raise RuntimeError(f"no gradient reached layers {missing}")
         ids = [l.layer_id for l in self.layers]
@@ -148,4 +190,6 @@ class GrapeOptimizer:
                                 self.r, self.lr, self.beta1, self.beta2, self.eps,
                                 self.seed, self.t, self.proj_step, layer_ids=ids,
                                 dtype=self.dtype or torch.bfloat16)
+        for l in self.embeddings:
+            self._update_table(l, norms)
         self.last_norms, self.last_G_priv = norms, G_priv
