@@ -560,11 +560,10 @@ __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& o
 #pragma unroll
     for (int n = 0; n < G::kNB; ++n) acc.v[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (n_steps <= 0) return;
-  // Copies in issue order: A and B of step 0; B of step 1, A of steps 1 and
-  // 2; then after the barrier in the last sub-step of step s, B of step s + 2
-  // and A of step s + 3, spread over that sub-step and the next three. Before
-  // that barrier step s + 1's copies are complete once at most those of A's
-  // step s + 2 are in flight: loads return in order.
+  // Copies in issue order: A and B of step 0, B and A of step 1; then during
+  // step s, A of step s + 2 in its first sub-step and, after the barrier in its
+  // last, B of step s + 2. Before that barrier step s + 1's copies are complete
+  // once at most those of A's step s + 2 are in flight: loads return in order.
   issue_a(0, 0, G::kCopies);
   issue_b(0, 0, G::kCopies);
   wait_vm_n<0>();
@@ -573,26 +572,20 @@ __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& o
     issue_b(1, 0, G::kCopies);
     issue_a(1, 0, G::kCopies);
   }
-  if (n_steps > 2) issue_a(2, 0, G::kCopies);
 #pragma unroll
   for (int n = 0; n < G::kNB; ++n) read_b(n, 0, 0, 0);
 #pragma unroll
   for (int m = 0; m < G::kMB; ++m) read_a(m, 0, 0);
-  int sta = 0;
-  // copies of sub-step kk (counted from the one with the barrier) of `s`
-  constexpr int kPer = G::kCopies;
-  static_assert(KK == 2 && kPer <= G::kMB && G::kNB <= G::kMB, "B's copies in the last sub-step, A's in the next first");
-  auto refill = [&](int s, int sta_s, int slot, int i) {
-    const int q = slot * kPer + i;  // of 2 G::kCopies: B's, then A's
-    if (q < G::kCopies) {
-      if (s + 2 < n_steps) issue_b(s & 1, q, q + 1);
-    } else {
-      if (s + 3 < n_steps) issue_a(sta_s, q - G::kCopies, q - G::kCopies + 1);
-    }
-  };
-  int prev_sta = 0;
-  for (int s = 0; s < n_steps; ++s) {
-    const int next = sta == 2 ? 0 : sta + 1;
+  static_assert(KK == 2 && G::kCopies <= G::kMB && G::kNB <= G::kMB, "one copy or fragment a row");
+  // A's stages of steps s, s + 1 and s + 2, and B's of step s
+  int sta = 0, sta1 = 1, sta2 = 2, stb = 0;
+  // MORE: there is a step s + 2 (else NEXT, at run time, a step s + 1). The two
+  // last steps are an instance of their own: with tests inside one loop body the
+  // compiler assumed on joining paths that older fragment reads might be in
+  // flight, and made the products wait for the newest.
+  auto step = [&](auto more, bool next) {
+    constexpr bool MORE = decltype(more)::value;
+    const bool NEXT = MORE || next;
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
       const int cur = kk & 1, nxt = cur ^ 1;
@@ -604,32 +597,36 @@ __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& o
         for (int n = 0; n < G::kNB; ++n)
           acc.v[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[m], fb[cur][n], acc.v[m][n], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
-        if (last && m == 0) {
-          if (s + 1 < n_steps) {
-            wait_lgkm0();  // this wave's reads of step s are complete
-            if (s + 2 < n_steps) wait_vm_n<G::kCopies>();
-            else wait_vm_n<0>();
-            lds_barrier();
-          }
+        if (last && m == 0 && NEXT) {
+          wait_lgkm0();  // this wave's reads of step s are complete
+          wait_vm_n<MORE ? G::kCopies : 0>();
+          lds_barrier();
         }
         // the next sub-step's fragments
         if (!last) {
           read_a(m, sta, kk + 1);
-          if (m < G::kNB) read_b(m, s & 1, kk + 1, nxt);
-        } else if (s + 1 < n_steps) {
-          read_a(m, next, 0);
-          if (m < G::kNB) read_b(m, (s + 1) & 1, 0, nxt);
+          if (m < G::kNB) read_b(m, stb, kk + 1, nxt);
+        } else if (NEXT) {
+          read_a(m, sta1, 0);
+          if (m < G::kNB) read_b(m, stb ^ 1, 0, nxt);
         }
         // the refills
-        if (m < kPer) {
-          if (last) refill(s, sta, 0, m);
-          else if (s > 0) refill(s - 1, prev_sta, 1, m);
+        if (MORE && m < G::kCopies) {
+          if (kk == 0) issue_a(sta2, m, m + 1);
+          if (last) issue_b(stb, m, m + 1);
         }
       }
     }
-    prev_sta = sta;
-    sta = next;
-  }
+    const int t = sta;
+    sta = sta1;
+    sta1 = sta2;
+    sta2 = t;
+    stb ^= 1;
+  };
+  int s = 0;
+  for (; s + 2 < n_steps; ++s) step(std::true_type{}, true);
+#pragma unroll 1
+  for (; s < n_steps; ++s) step(std::false_type{}, s + 1 < n_steps);
 }
 
 // The tile (m, n) of a block among mt x nt: each XCD takes a
