@@ -1157,6 +1157,21 @@ int check_call(const VocabCall& c, bool distill) {
   return DPG_OK;
 }
 
+// Whether a launch of `tiles` big tiles takes them. Fewer than three for every
+// four CUs leave too much of the chip idle, and a K step of a big tile takes 64
+// KiB through a CU's LDS where a small one takes 32 (128 rows x 64 against 1000
+// columns, fp32: 18 us big, 12 us small; 252 big tiles of dX at 999 x 768 x
+// 32003, fp32: 311 us big, 424 us small). With at most 128 rows half of a big
+// tile would be padding (4 rows x 2048 against 50304 columns: 53 us big, 40 us
+// small).
+bool big_tiles(int64_t tiles, int64_t rows) { return tiles >= 192 && rows > SmallTile::kTile; }
+
+template <class F>
+void with_tile(int64_t tiles, int64_t rows, F fn) {
+  if (big_tiles(tiles, rows)) fn(BigTile());
+  else fn(SmallTile());
+}
+
 // Bytes of D, and of the packed table, kept at a time; of a packed table that
 // is needed only where the caller's is not 16-byte aligned.
 constexpr int64_t kPieceBytes = 512ll << 20, kRarePieceBytes = 64ll << 20;
@@ -1214,7 +1229,9 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   p.off_before = take(distill ? N * (p.piece / 64) * 2 : 0);
   p.off_Xp = take(parts * p.np * p.ldx * 2);
   p.off_Ep = take(parts * p.packed_piece * p.ldx * 2);
-  p.off_part = take(grad ? 0 : ceil_div(V, SmallTile::kTile) * p.np * 8);
+  const bool big = big_tiles(
+      ceil_div(std::min(p.packed_piece, V), BigTile::kTile) * (p.np / BigTile::kTile), N);
+  p.off_part = take(grad ? 0 : ceil_div(V, big ? BigTile::kTile : SmallTile::kTile) * p.np * 8);
   p.off_D = take(grad ? parts * p.np * p.piece * 2 : 0);
   p.off_dX = take(grad ? p.splits * p.np * p.ldx * 4 : 0);
   p.total = off;
@@ -1288,19 +1305,6 @@ void for_pieces(VocabArgs& a, hipStream_t s, F fn) {
       hipLaunchKernelGGL(teacher_ids_kernel, dim3(static_cast<unsigned>(a.N)), dim3(kThreads), 0, s, a);
     fn();
   }
-}
-
-// fn with the tile to use for a launch of `tiles` big tiles. Fewer than three
-// for every four CUs leave too much of the chip idle, and a K step of a big
-// tile takes 64 KiB through a CU's LDS where a small one takes 32 (128 rows x
-// 64 against 1000 columns, fp32: 18 us big, 12 us small; 252 big tiles of dX
-// at 999 x 768 x 32003, fp32: 311 us big, 424 us small). With at most 128 rows
-// half of a big tile would be padding (4 rows x 2048 against 50304 columns:
-// 53 us big, 40 us small).
-template <class F>
-void with_tile(int64_t tiles, int64_t rows, F fn) {
-  if (tiles >= 192 && rows > SmallTile::kTile) fn(BigTile());
-  else fn(SmallTile());
 }
 
 template <typename T>

@@ -396,10 +396,13 @@ int dpg_vocab_loss(const void* X, const void* E, const int64_t* targets, int64_t
  *     dX = D E  [N][d],   dE = D^T X  [V][d]        (both in dtype)
  * with lse as dpg_vocab_loss wrote it. The logits are recomputed in pieces
  * of the vocabulary, and one piece of D is kept at a time (at most 512 MiB,
- * but at least 256 columns, in dtype: bf16 D is D rounded once, the products
- * accumulate in fp32). dX or dE may be NULL (not computed); rows without a
+ * but at least 256 columns). Products run on bf16 operands and accumulate in
+ * fp32: with bf16 inputs D is rounded to bf16 once, with fp32 inputs every
+ * operand, D too, is split exactly into three bf16 parts, so that products
+ * keep fp32's accuracy. dX or dE may be NULL (not computed); rows without a
  * target get a zero dX. dloss_n may carry a sample's mean and clip factor:
- * the gradient of each row's loss involves no other row of X.
+ * the gradient of each row's loss involves no other row of X. Results do not
+ * vary from run to run.
  *   workspace  dpg_vocab_loss_workspace_size(..., grad = 1) bytes
  */
 int dpg_vocab_loss_grad(const void* X, const void* E, const int64_t* targets, const float* lse,
