@@ -29,24 +29,52 @@ namespace {
 constexpr int kPad = 256;     // packed rows and pieces are padded to whole tiles
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// fp32 operands are split exactly into three bf16 parts (8 + 8 + 8 bits of
-// the significand, each part truncated), x = h + m + l, and a product is six
-// bf16 products: every pair of parts but m l, l m and l l, which lie below
-// 2^-24 of it. The matrix cores run bf16 16 times as fast as fp32, so this is
-// 2.6 times as fast as their fp32 instructions at fp32's accuracy. Small
-// products are added first, so that the sum is rounded at its full size only
-// in the last pass over K.
-template <int PARTS> struct Combos;  // PARTS: bf16 parts of an operand
+// fp32 products on the 16-bit matrix instructions, which are 16 times as fast as
+// the fp32 ones.
+//
+// The logits: every row of X and of E is scaled by a power of two, so that its
+// largest magnitude lies in [2^13, 2^14), and split into two fp16 parts of 11
+// bits, x = h + l. What is left of an element is at most 2^-23 of it, or 2^-38 of
+// its row's largest where that is more (fp16 has no smaller step). A product is
+// three fp16 products, all pairs but l l, which is at most 2^-22 of it.
+//
+// dX and dE: a column of D may hold nothing but tiny entries (an unlikely token),
+// which no scale of a row can keep, so the operands are split exactly into three
+// bf16 parts of 8 bits, each part truncated, x = h + m + l, with fp32's exponent
+// range. A product is six bf16 products, all pairs but m l, l m and l l, below
+// 2^-22 of it.
+//
+// Small products are added first, so that the sum is rounded at its full size
+// only in the last pass over K. Loss and dX at 999 x 768 x 32003: 643 us; 802
+// with three bf16 parts in the logits too.
+template <int PARTS> struct Combos;  // parts of an operand: 1 and 3 bf16, 2 fp16
 template <> struct Combos<1> {
   static constexpr int n = 1;
   __device__ __forceinline__ static int a(int) { return 0; }
   __device__ __forceinline__ static int b(int) { return 0; }
+};
+template <> struct Combos<2> {
+  static constexpr int n = 3;  // (l,h) (h,l) (h,h)
+  __device__ __forceinline__ static int a(int c) { return (0x001 >> (4 * c)) & 15; }
+  __device__ __forceinline__ static int b(int c) { return (0x010 >> (4 * c)) & 15; }
 };
 template <> struct Combos<3> {
   static constexpr int n = 6;  // (l,h) (h,l) (m,m) (m,h) (h,m) (h,h)
   __device__ __forceinline__ static int a(int c) { return (0x001102 >> (4 * c)) & 15; }
   __device__ __forceinline__ static int b(int c) { return (0x010120 >> (4 * c)) & 15; }
 };
+// Parts of the logits' operands where the others have PARTS.
+template <int PARTS> constexpr int kLogitParts = PARTS == 3 ? 2 : 1;
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+template <int PARTS>
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+  if constexpr (PARTS == 2)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
 template <typename T> constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
 
 // Takes the leading part off a value: x becomes the rest (zero for infinities
@@ -101,8 +129,12 @@ struct VocabArgs {
   uint64_t* bits;       // [N][ldd / 64] packed: the piece's columns that are
                         // teacher ids
   uint16_t* before;     // [N][ldd / 64] packed: index in qu of a word's first
-  bf16* Xp;             // [parts][np][ldx] packed rows of X
+  bf16* Xp;             // [parts][np][ldx] packed rows of X, or null
   bf16* Ep;             // [parts][piece][ldx] the piece's rows of E, or null
+  _Float16* Xh;         // fp32: [2][np][ldx] packed rows of X for the logits
+  _Float16* Eh;         // fp32: [2][piece][ldx] the piece's rows of E for them
+  float* sx;            // fp32: [np] scale of a row's logits
+  float* se;            // fp32: [piece] scale of a column's logits
   float2* part;         // [col tiles][np] packed: tile maximum and sum, base 2
   bf16* D;              // [parts][np][ldd] packed: one piece of D
   float* dXacc;         // [splits][np][ldx] packed
@@ -201,6 +233,47 @@ __device__ __forceinline__ void pack_row(const T* src, bf16* dst, int d, int ldx
   }
 }
 
+// One fp32 row for the logits: scaled, in two fp16 parts; returns the factor that
+// undoes the scale. A row with an infinity or NaN is not scaled.
+__device__ __forceinline__ float pack_row_half(const float* src, _Float16* dst, int d, int ldx,
+                                               int64_t part_stride, bool vec, int lane) {
+  float m = 0.0f;
+  if (vec) {
+    for (int c = lane * 4; c < d; c += 256) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(src + c);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) m = fmaxf(m, fabsf(x[q]));
+    }
+  } else {
+    for (int c = lane; c < d; c += 64) m = fmaxf(m, fabsf(src[c]));
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  int e = 14;
+  if (m > 0.0f && m < INFINITY) e = max(__builtin_amdgcn_frexp_expf(m), -100);
+  for (int c = lane * 4; c < ldx; c += 256) {
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    if (vec) {
+      if (c < d) x = *reinterpret_cast<const f32x4*>(src + c);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (c + q < d) x[q] = src[c + q];
+    }
+    f16x4 h, l;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float y = ldexpf(x[q], 14 - e);
+      h[q] = static_cast<_Float16>(y);
+      const float r = y - static_cast<float>(h[q]);
+      l[q] = static_cast<_Float16>(fabsf(y) < INFINITY ? r : 0.0f);
+    }
+    *reinterpret_cast<f16x4*>(dst + c) = h;
+    *reinterpret_cast<f16x4*>(dst + part_stride + c) = l;
+  }
+  return ldexpf(1.0f, e - 14);
+}
+
 // Packs rows and table in one launch. Blocks [0, row_blocks - kPadBlocks):
 // kPackRows rows of X each. A row's packed index is the number of rows before it that have a
 // target, which each block counts for itself (8 bytes of L2 reads for every
@@ -215,10 +288,14 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
   const int block = static_cast<int>(blockIdx.x);
   if (block >= row_blocks) {
     const bool vec = a.d % VN == 0 && is_aligned(a.E, 16);
-    const int i = (block - row_blocks) * 4 + wave;
-    pack_row(static_cast<const T*>(a.E) + (static_cast<int64_t>(a.v0) + i) * a.d,
-             a.Ep + static_cast<int64_t>(i) * a.ldx, i < a.vn ? a.d : 0, a.ldx,
-             static_cast<int64_t>(a.ldd) * a.ldx, vec, lane);
+    const int i = (block - row_blocks) * 4 + wave, d = i < a.vn ? a.d : 0;
+    const T* src = static_cast<const T*>(a.E) + (static_cast<int64_t>(a.v0) + i) * a.d;
+    const int64_t at = static_cast<int64_t>(i) * a.ldx, stride = static_cast<int64_t>(a.ldd) * a.ldx;
+    if constexpr (kParts<T> == 3) {
+      const float f = pack_row_half(src, a.Eh + at, d, a.ldx, stride, vec, lane);
+      if (lane == 0) a.se[i] = f;
+    }
+    if (a.Ep) pack_row(src, a.Ep + at, d, a.ldx, stride, vec, lane);
     return;
   }
   __shared__ int wave_cnt[4];
@@ -242,7 +319,14 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
   if (lane == 0) wave_cnt[wave] = c;
   __syncthreads();
   const int before = (wave_cnt[0] + wave_cnt[1]) + (wave_cnt[2] + wave_cnt[3]);
-  const int64_t part_stride = static_cast<int64_t>(a.np) * a.ldx;
+  auto pack = [&](const T* src, int i, int d, bool vec) {  // packed row i
+    const int64_t at = static_cast<int64_t>(i) * a.ldx, stride = static_cast<int64_t>(a.np) * a.ldx;
+    if constexpr (kParts<T> == 3) {
+      const float f = pack_row_half(src, a.Xh + at, d, a.ldx, stride, vec, lane);
+      if (lane == 0) a.sx[i] = f;
+    }
+    if (a.Xp) pack_row(src, a.Xp + at, d, a.ldx, stride, vec, lane);
+  };
   const int pad = block - (row_blocks - kPadBlocks);
   if (pad >= 0) {
     if (tid == 0 && pad == 0) a.count[0] = before;
@@ -253,9 +337,7 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
         a.target[i] = -1;
         if (a.dloss) a.g[i] = a.lse2[i] = 0.0f;
       }
-      if (i < end)
-        pack_row(static_cast<const T*>(a.X), a.Xp + static_cast<int64_t>(i) * a.ldx, 0, a.ldx,
-                 part_stride, true, lane);
+      if (i < end) pack(static_cast<const T*>(a.X), i, 0, true);
     }
     return;
   }
@@ -280,8 +362,7 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
     const int r = q * 4 + wave;
     if (!((b >> r) & 1)) continue;
     const int at = before + __popcll(b & ((1ull << r) - 1));
-    pack_row(static_cast<const T*>(a.X) + static_cast<int64_t>(n0 + r) * a.d,
-             a.Xp + static_cast<int64_t>(at) * a.ldx, a.d, a.ldx, part_stride, vec, lane);
+    pack(static_cast<const T*>(a.X) + static_cast<int64_t>(n0 + r) * a.d, at, a.d, vec);
   }
 }
 
@@ -595,7 +676,7 @@ __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& o
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int n = 0; n < G::kNB; ++n)
-          acc.v[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[m], fb[cur][n], acc.v[m][n], 0, 0, 0);
+          acc.v[m][n] = mfma<PARTS>(fa[m], fb[cur][n], acc.v[m][n]);
         __builtin_amdgcn_sched_barrier(0);
         if (last && m == 0 && NEXT) {
           wait_lgkm0();  // this wave's reads of step s are complete
@@ -704,16 +785,37 @@ struct LaneIds {
   }
 };
 
-// A 256 x 256 (128 x 128) tile of logits z / (zscale), before its scale: E's
-// rows against packed rows.
+// A tile of logits before their scale, E's rows against packed rows: with fp32
+// operands the columns' scales are taken out, the rows' are left to the caller.
 template <class G, int PARTS>
 __device__ __forceinline__ void logits_tile(const VocabArgs& a, int c0, int r0, char* smem,
                                             typename G::Acc& acc) {
-  tile_product<G, PARTS, false, false>(
-      table_operand(a, false, c0, 0),
-      rows_operand(a.Xp + static_cast<int64_t>(r0) * a.ldx, a.ldx,
-                   static_cast<int64_t>(a.np) * a.ldx, G::kTile, a.ldx),
-      a.ldx / kStepK, smem, acc);
+  constexpr int LP = kLogitParts<PARTS>;
+  const bf16* x = LP == 2 ? reinterpret_cast<const bf16*>(a.Xh) : a.Xp;
+  const Operand rows = rows_operand(x + static_cast<int64_t>(r0) * a.ldx, a.ldx,
+                                    static_cast<int64_t>(a.np) * a.ldx, G::kTile, a.ldx);
+  const Operand table =
+      LP == 2 ? rows_operand(reinterpret_cast<const bf16*>(a.Eh) + static_cast<int64_t>(c0) * a.ldx,
+                             a.ldx, static_cast<int64_t>(a.ldd) * a.ldx, G::kTile, a.ldx)
+              : table_operand(a, false, c0, 0);
+  tile_product<G, LP, false, false>(table, rows, a.ldx / kStepK, smem, acc);
+  if constexpr (LP == 2) {
+    const int lane = threadIdx.x & 63, wm = (threadIdx.x >> 6) % G::kWavesM;
+    const float* se = a.se + c0 + G::kWaveM * wm + 4 * (lane >> 4);
+#pragma unroll
+    for (int mb = 0; mb < G::kMB; ++mb) {
+      const f32x4 f = *reinterpret_cast<const f32x4*>(se + 16 * mb);
+#pragma unroll
+      for (int nb = 0; nb < G::kNB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc.v[mb][nb][i] *= f[i];
+    }
+  }
+}
+// The scale that logits_tile left to packed row r.
+template <int PARTS>
+__device__ __forceinline__ float row_scale(const VocabArgs& a, int r) {
+  return PARTS == 3 ? a.sx[r] : 1.0f;
 }
 
 // fn(std::true_type) where a tile reaches past the piece's last column,
@@ -751,8 +853,9 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void stats_kernel(const Vo
   typename G::Acc acc;
   logits_tile<G, PARTS>(a, c0, r0, smem, acc);
   const int left = a.vn - cl;
-  float z2 = a.zscale * kLog2e;
-  float m[G::kNB], s[G::kNB];
+  float zrow[G::kNB], m[G::kNB], s[G::kNB];
+#pragma unroll
+  for (int nb = 0; nb < G::kNB; ++nb) zrow[nb] = a.zscale * row_scale<PARTS>(a, rl + 16 * nb);
 #pragma unroll
   for (int nb = 0; nb < G::kNB; ++nb) {
     auto logit = [&](int at, float* to) {  // (written where the lane holds it)
@@ -761,7 +864,7 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void stats_kernel(const Vo
       for (int mb = 0; mb < G::kMB; ++mb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) z = at == 16 * mb + i ? acc.v[mb][nb][i] : z;
-      if ((at & 15) < 4) *to = z * a.zscale;
+      if ((at & 15) < 4) *to = z * zrow[nb];
     };
     const int r = rl + 16 * nb;
     if constexpr (TEACHER) {
@@ -773,8 +876,7 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void stats_kernel(const Vo
       if (at[nb] >= 0 && c >= 0 && c < G::kWaveM) logit(c, a.zt + r);
     }
   }
-  if (z2 < 0.0f) {
-    z2 = -z2;
+  if (a.zscale < 0.0f) {
 #pragma unroll
     for (int mb = 0; mb < G::kMB; ++mb)
 #pragma unroll
@@ -794,6 +896,7 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void stats_kernel(const Vo
           if (!E || 16 * mb + i < left) x = fmaxf(x, acc.v[mb][nb][i]);
       x = fmaxf(x, __shfl_xor(x, 16, 64));
       x = fmaxf(x, __shfl_xor(x, 32, 64));
+      const float z2 = fabsf(zrow[nb]) * kLog2e;
       // (a wave whose columns all lie past the end has no maximum)
       const float ref = x == -INFINITY ? 0.0f : x * z2;
       float t = 0.0f;
@@ -907,12 +1010,16 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void grad_logits_kernel(co
       lse2[nb] = a.lse2[rl + 16 * nb];
     }
   };
-  if (!TEACHER) load_rows();  // (with the teacher's bits the registers are full)
+  // (with the teacher's bits or two parts of each operand the registers are full)
+  constexpr bool kEarly = !TEACHER && PARTS == 1;
+  if (kEarly) load_rows();
   typename G::Acc acc;
   logits_tile<G, PARTS>(a, c0, r0, smem, acc);
-  if (TEACHER) load_rows();
+  if (!kEarly) load_rows();
   const int left = a.vn - cl;
-  const float z2 = a.zscale * kLog2e;
+  float z2[G::kNB];
+#pragma unroll
+  for (int nb = 0; nb < G::kNB; ++nb) z2[nb] = a.zscale * kLog2e * row_scale<PARTS>(a, rl + 16 * nb);
   with_edge(c0 + G::kTile > a.vn, [&](auto edge) {
     constexpr bool E = decltype(edge)::value;
 #pragma unroll
@@ -921,7 +1028,7 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void grad_logits_kernel(co
       for (int mb = 0; mb < G::kMB; ++mb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float x = g[nb] * exp2_(fmaf(acc.v[mb][nb][i], z2, -lse2[nb]));
+          const float x = g[nb] * exp2_(fmaf(acc.v[mb][nb][i], z2[nb], -lse2[nb]));
           acc.v[mb][nb][i] = !E || 16 * mb + i < left ? x : 0.0f;
         }
   });
@@ -1181,7 +1288,7 @@ struct VocabPlan {
   int32_t splits = 1;
   bool packed = false;  // the table is packed whatever its alignment
   size_t off_flag, off_count, off_row, off_inv, off_target, off_g, off_lse2, off_q, off_ent, off_zt, off_qu, off_nu, off_bits,
-      off_before, off_Xp, off_Ep, off_part, off_D, off_dX, total;
+      off_before, off_Xp, off_Ep, off_Xh, off_Eh, off_sx, off_se, off_part, off_D, off_dX, total;
 };
 
 int64_t whole_pads(int64_t x) { return std::max<int64_t>(kPad, x / kPad * kPad); }
@@ -1227,8 +1334,14 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   p.off_nu = take(distill ? N * 4 : 0);
   p.off_bits = take(distill ? N * (p.piece / 64) * 8 : 0);
   p.off_before = take(distill ? N * (p.piece / 64) * 2 : 0);
-  p.off_Xp = take(parts * p.np * p.ldx * 2);
-  p.off_Ep = take(parts * p.packed_piece * p.ldx * 2);
+  // (the loss of fp32 operands needs only their fp16 parts)
+  const bool half = parts > 1, whole = !half || grad;
+  p.off_Xp = take(whole ? parts * p.np * p.ldx * 2 : 0);
+  p.off_Ep = take(whole ? parts * p.packed_piece * p.ldx * 2 : 0);
+  p.off_Xh = take(half ? 2 * p.np * p.ldx * 2 : 0);
+  p.off_Eh = take(half ? 2 * p.piece * p.ldx * 2 : 0);
+  p.off_sx = take(half ? p.np * 4 : 0);
+  p.off_se = take(half ? p.piece * 4 : 0);
   const bool big = big_tiles(
       ceil_div(std::min(p.packed_piece, V), BigTile::kTile) * (p.np / BigTile::kTile), N);
   p.off_part = take(grad ? 0 : ceil_div(V, big ? BigTile::kTile : SmallTile::kTile) * p.np * 8);
@@ -1238,7 +1351,8 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   return p;
 }
 
-VocabArgs make_args(const VocabCall& c, const VocabPlan& p, char* ws) {
+// rows, table: the gradient needs X's, E's bf16 parts.
+VocabArgs make_args(const VocabCall& c, const VocabPlan& p, char* ws, bool rows, bool table) {
   VocabArgs a{};
   a.X = c.X;
   a.E = c.E;
@@ -1267,9 +1381,15 @@ VocabArgs make_args(const VocabCall& c, const VocabPlan& p, char* ws) {
   a.nu = reinterpret_cast<int32_t*>(ws + p.off_nu);
   a.bits = reinterpret_cast<uint64_t*>(ws + p.off_bits);
   a.before = reinterpret_cast<uint16_t*>(ws + p.off_before);
-  a.Xp = reinterpret_cast<bf16*>(ws + p.off_Xp);
-  const bool pack = p.packed || !aligned(c.E, 16);
-  a.Ep = pack ? reinterpret_cast<bf16*>(ws + p.off_Ep) : nullptr;
+  const bool half = c.dtype == DPG_FP32, pack = p.packed || !aligned(c.E, 16);
+  a.Xp = !half || rows ? reinterpret_cast<bf16*>(ws + p.off_Xp) : nullptr;
+  a.Ep = pack && (!half || table) ? reinterpret_cast<bf16*>(ws + p.off_Ep) : nullptr;
+  if (half) {
+    a.Xh = reinterpret_cast<_Float16*>(ws + p.off_Xh);
+    a.Eh = reinterpret_cast<_Float16*>(ws + p.off_Eh);
+    a.sx = reinterpret_cast<float*>(ws + p.off_sx);
+    a.se = reinterpret_cast<float*>(ws + p.off_se);
+  }
   a.part = reinterpret_cast<float2*>(ws + p.off_part);
   a.D = reinterpret_cast<bf16*>(ws + p.off_D);
   a.dXacc = reinterpret_cast<float*>(ws + p.off_dX);
@@ -1287,7 +1407,7 @@ dim3 tile_grid(int64_t mt, int64_t nt) { return dim3(static_cast<unsigned>(round
 template <typename T>
 void launch_pack(const VocabArgs& a, bool rows, hipStream_t s) {
   const unsigned rb = rows ? blocks_of(a.N, kPackRows) + kPadBlocks : 0;
-  const unsigned tb = a.Ep ? blocks_of(round_up(a.vn, kPad), 4) : 0;
+  const unsigned tb = a.Ep || a.Eh ? blocks_of(round_up(a.vn, kPad), 4) : 0;
   if (rb + tb)
     hipLaunchKernelGGL(pack_kernel<T>, dim3(rb + tb), dim3(kThreads), 0, s, a, static_cast<int>(rb));
 }
@@ -1372,7 +1492,7 @@ int loss_impl(const VocabCall& c, bool distill, float* loss, float* lse, void* w
   if (!loss || !lse) return fail(DPG_ERR_INVALID_ARG, "loss and lse must not be NULL");
   const VocabPlan p = plan_vocab(c.N, c.d, c.V, c.k, c.dtype, distill, false);
   if (const int st = check_ws(workspace, workspace_bytes, p.total)) return st;
-  VocabArgs a = make_args(c, p, static_cast<char*>(workspace));
+  VocabArgs a = make_args(c, p, static_cast<char*>(workspace), false, false);
   a.loss = loss;
   a.lse = lse;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -1387,7 +1507,7 @@ int grad_impl(const VocabCall& c, bool distill, const float* lse, const float* d
   if (!dX && !dE) return fail(DPG_ERR_INVALID_ARG, "dX and dE are both NULL");
   const VocabPlan p = plan_vocab(c.N, c.d, c.V, c.k, c.dtype, distill, true);
   if (const int st = check_ws(workspace, workspace_bytes, p.total)) return st;
-  VocabArgs a = make_args(c, p, static_cast<char*>(workspace));
+  VocabArgs a = make_args(c, p, static_cast<char*>(workspace), dE != nullptr, dX != nullptr);
   a.lse = const_cast<float*>(lse);
   a.dloss = dloss;
   hipStream_t s = static_cast<hipStream_t>(stream);

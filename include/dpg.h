@@ -396,13 +396,15 @@ int dpg_vocab_loss(const void* X, const void* E, const int64_t* targets, int64_t
  *     dX = D E  [N][d],   dE = D^T X  [V][d]        (both in dtype)
  * with lse as dpg_vocab_loss wrote it. The logits are recomputed in pieces
  * of the vocabulary, and one piece of D is kept at a time (at most 512 MiB,
- * but at least 256 columns). Products run on bf16 operands and accumulate in
- * fp32: with bf16 inputs D is rounded to bf16 once, with fp32 inputs every
- * operand, D too, is split exactly into three bf16 parts, so that products
- * keep fp32's accuracy. dX or dE may be NULL (not computed); rows without a
- * target get a zero dX. dloss_n may carry a sample's mean and clip factor:
- * the gradient of each row's loss involves no other row of X. Results do not
- * vary from run to run.
+ * but at least 256 columns). Products run on 16-bit operands and accumulate in
+ * fp32: with bf16 inputs D is rounded to bf16 once; with fp32 inputs operands
+ * are split, for the logits into two fp16 parts after a scale per row (an
+ * element keeps 2^-23 of itself or 2^-38 of its row's largest), for dX and dE
+ * exactly into three bf16 parts, so that products keep fp32's accuracy (an
+ * infinity in X or E makes the rows it meets NaN). dX or dE may be NULL (not
+ * computed); rows without a target get a zero dX. dloss_n may carry a
+ * sample's mean and clip factor: the gradient of each row's loss involves no
+ * other row of X. Results do not vary from run to run.
  *   workspace  dpg_vocab_loss_workspace_size(..., grad = 1) bytes
  */
 int dpg_vocab_loss_grad(const void* X, const void* E, const int64_t* targets, const float* lse,

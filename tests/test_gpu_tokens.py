@@ -482,3 +482,35 @@ def test_distillation_id_named_with_and_without_weight():
     dX, dE = dpg.dpg_distill_loss_grad(x, e, y, tt, lse, _dev(g))
     assert rel_err(_host(dX), want_dX) <= TOL["fp32"]
     assert rel_err(_host(dE), want_dE) <= TOL["fp32"]
+
+
+def test_fp32_rows_of_very_different_size():
+    """fp32 rows of X and of E of sizes from 2^-60 to 2^3, some with one
+    element 2^12 above the rest. A logit is off by at most the fp32 bar of the sum
+    of its products' magnitudes, and 2^-38 of either row's largest element times
+    the other's sum (twice that with both); the loss by two logits' errors."""
+    import torch
+    import dp_grape_projection_amd as dpg
+    N, d, V = 300, 72, 519
+    r = np.random.default_rng(91)
+    px, pe = r.integers(-60, 41, N), r.integers(-40, 61, V)
+    E = r.standard_normal((V, d)) * 2.0 ** np.minimum(pe, 0)[:, None]
+    X = r.standard_normal((N, d)) * 2.0 ** np.minimum(px, 3)[:, None]
+    X[::3, 5] *= 2.0 ** 12
+    E[::4, 5] *= 2.0 ** -10
+    E[1::4, 9] *= 2.0 ** 12
+    X[:, 9] *= 2.0 ** -10
+    X, E = _round(X, "fp32"), _round(E, "fp32")
+    y = r.integers(0, V, N)
+    z = X @ E.T
+    m = z.max(axis=1)
+    lse = m + np.log(np.exp(z - m[:, None]).sum(axis=1))
+    loss = lse - z[np.arange(N), y]
+    aX, aE = np.abs(X), np.abs(E)
+    dz = (1e-5 * (aX @ aE.T) + 2.0 ** -37 * (np.outer(aX.max(1), aE.sum(1)) + np.outer(aX.sum(1), aE.max(1))))
+    bar = 2 * dz.max(axis=1) + 2e-5 * np.maximum(1.0, np.abs(lse))
+    print("[tokens] fp32 rows of very different size", flush=True)
+    got, got_lse = dpg.dpg_vocab_loss(_dev(X, "fp32"), _dev(E, "fp32"), _dev(y))
+    torch.cuda.synchronize()
+    assert (np.abs(_host(got_lse) - lse) <= bar).all()
+    assert (np.abs(_host(got) - loss) <= bar).all()
