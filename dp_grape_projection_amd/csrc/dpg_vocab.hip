@@ -141,6 +141,8 @@ struct VocabArgs {
   int32_t ldd;          // columns of a piece (a multiple of kPad)
   int32_t v0, vn;       // the piece: vocabulary rows v0 .. v0 + vn - 1
   int32_t splits;       // parts of the vocabulary piece dX is summed in
+  int32_t splits_e;     // parts of the packed rows dE is summed in
+  float* dEacc;         // [splits_e][ldd][ldx], where splits_e > 1
 };
 
 // ------------------------------------------------------------------- rows --
@@ -187,79 +189,80 @@ __global__ __launch_bounds__(kThreads) void teacher_kernel(const VocabArgs a) {
   }
 }
 
-// One value as PARTS bf16 parts, `stride` elements apart.
-template <int PARTS>
-__device__ __forceinline__ void store_parts(bf16* dst, int64_t stride, float x) {
-  if constexpr (PARTS == 1) {
-    dst[0] = from_float<bf16>(x);
+// 16 bytes at any element's address: rows of an odd width start anywhere, and the
+// global loads and stores take any address (216 MB of rows of 1001 bf16 packed:
+// 145 us element by element, 73 us so).
+template <typename T>
+struct AnyVec16 {
+  typedef typename Vec16<T>::type type __attribute__((aligned(sizeof(T))));
+};
+// Elements c .. of a row of d, zero beyond it.
+template <typename T>
+__device__ __forceinline__ typename Vec16<T>::type load_row(const T* src, int c, int d) {
+  constexpr int VN = Vec16<T>::N;
+  typename Vec16<T>::type x;
+  if (c + VN <= d) {
+    x = *reinterpret_cast<const typename AnyVec16<T>::type*>(src + c);
   } else {
-    bf16 p[3];
-    split3(x, p);
 #pragma unroll
-    for (int q = 0; q < 3; ++q) dst[q * stride] = p[q];
+    for (int q = 0; q < VN; ++q) x[q] = c + q < d ? src[c + q] : zero_val<T>();
+  }
+  return x;
+}
+// n of a row's elements from p on (all 16 bytes of them, or fewer at its end).
+template <typename T>
+__device__ __forceinline__ void store_row(T* p, int n, typename Vec16<T>::type x) {
+  constexpr int VN = Vec16<T>::N;
+  if (n >= VN) {
+    *reinterpret_cast<typename AnyVec16<T>::type*>(p) = x;
+  } else {
+#pragma unroll
+    for (int q = 0; q < VN; ++q)
+      if (q < n) p[q] = x[q];
   }
 }
 
 // One row of d values as parts, zero beyond d, by 64 lanes.
 template <typename T>
 __device__ __forceinline__ void pack_row(const T* src, bf16* dst, int d, int ldx, int64_t part_stride,
-                                         bool vec, int lane) {
+                                         int lane) {
   constexpr int VN = Vec16<T>::N;
-  if (vec) {  // d a multiple of VN, src 16-byte aligned
-    for (int c = lane * VN; c < ldx; c += 64 * VN) {
-      typename Vec16<T>::type x;
+  for (int c = lane * VN; c < ldx; c += 64 * VN) {
+    const typename Vec16<T>::type x = load_row(src, c, d);
+    if constexpr (kParts<T> == 1) {
+      *reinterpret_cast<bf16x8*>(dst + c) = x;
+    } else {
+      Vec4<bf16>::type y[3];
 #pragma unroll
-      for (int q = 0; q < VN; ++q) x[q] = zero_val<T>();
-      if (c < d) x = *reinterpret_cast<const typename Vec16<T>::type*>(src + c);
-      if constexpr (kParts<T> == 1) {
-        *reinterpret_cast<bf16x8*>(dst + c) = x;
-      } else {
-        Vec4<bf16>::type y[3];
+      for (int q = 0; q < 4; ++q) {
+        bf16 p[3];
+        split3(x[q], p);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          bf16 p[3];
-          split3(x[q], p);
-#pragma unroll
-          for (int j = 0; j < 3; ++j) y[j][q] = p[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 3; ++j)
-          *reinterpret_cast<Vec4<bf16>::type*>(dst + j * part_stride + c) = y[j];
+        for (int j = 0; j < 3; ++j) y[j][q] = p[j];
       }
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        *reinterpret_cast<Vec4<bf16>::type*>(dst + j * part_stride + c) = y[j];
     }
-  } else {
-    for (int c = lane; c < ldx; c += 64)
-      store_parts<kParts<T>>(dst + c, part_stride, c < d ? to_float(src[c]) : 0.0f);
   }
 }
 
 // One fp32 row for the logits: scaled, in two fp16 parts; returns the factor that
 // undoes the scale. A row with an infinity or NaN is not scaled.
 __device__ __forceinline__ float pack_row_half(const float* src, _Float16* dst, int d, int ldx,
-                                               int64_t part_stride, bool vec, int lane) {
+                                               int64_t part_stride, int lane) {
   float m = 0.0f;
-  if (vec) {
-    for (int c = lane * 4; c < d; c += 256) {
-      const f32x4 x = *reinterpret_cast<const f32x4*>(src + c);
+  for (int c = lane * 4; c < d; c += 256) {
+    const f32x4 x = load_row(src, c, d);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) m = fmaxf(m, fabsf(x[q]));
-    }
-  } else {
-    for (int c = lane; c < d; c += 64) m = fmaxf(m, fabsf(src[c]));
+    for (int q = 0; q < 4; ++q) m = fmaxf(m, fabsf(x[q]));
   }
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
   int e = 14;
   if (m > 0.0f && m < INFINITY) e = max(__builtin_amdgcn_frexp_expf(m), -100);
   for (int c = lane * 4; c < ldx; c += 256) {
-    f32x4 x = {0.f, 0.f, 0.f, 0.f};
-    if (vec) {
-      if (c < d) x = *reinterpret_cast<const f32x4*>(src + c);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (c + q < d) x[q] = src[c + q];
-    }
+    const f32x4 x = load_row(src, c, d);
     f16x4 h, l;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -284,18 +287,16 @@ constexpr int kPackRows = 16, kPadBlocks = kPad / kPackRows;
 template <typename T>
 __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int row_blocks) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  constexpr int VN = Vec16<T>::N;
   const int block = static_cast<int>(blockIdx.x);
   if (block >= row_blocks) {
-    const bool vec = a.d % VN == 0 && is_aligned(a.E, 16);
     const int i = (block - row_blocks) * 4 + wave, d = i < a.vn ? a.d : 0;
     const T* src = static_cast<const T*>(a.E) + (static_cast<int64_t>(a.v0) + i) * a.d;
     const int64_t at = static_cast<int64_t>(i) * a.ldx, stride = static_cast<int64_t>(a.ldd) * a.ldx;
     if constexpr (kParts<T> == 3) {
-      const float f = pack_row_half(src, a.Eh + at, d, a.ldx, stride, vec, lane);
+      const float f = pack_row_half(src, a.Eh + at, d, a.ldx, stride, lane);
       if (lane == 0) a.se[i] = f;
     }
-    if (a.Ep) pack_row(src, a.Ep + at, d, a.ldx, stride, vec, lane);
+    if (a.Ep) pack_row(src, a.Ep + at, d, a.ldx, stride, lane);
     return;
   }
   __shared__ int wave_cnt[4];
@@ -319,13 +320,13 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
   if (lane == 0) wave_cnt[wave] = c;
   __syncthreads();
   const int before = (wave_cnt[0] + wave_cnt[1]) + (wave_cnt[2] + wave_cnt[3]);
-  auto pack = [&](const T* src, int i, int d, bool vec) {  // packed row i
+  auto pack = [&](const T* src, int i, int d) {  // packed row i
     const int64_t at = static_cast<int64_t>(i) * a.ldx, stride = static_cast<int64_t>(a.np) * a.ldx;
     if constexpr (kParts<T> == 3) {
-      const float f = pack_row_half(src, a.Xh + at, d, a.ldx, stride, vec, lane);
+      const float f = pack_row_half(src, a.Xh + at, d, a.ldx, stride, lane);
       if (lane == 0) a.sx[i] = f;
     }
-    if (a.Xp) pack_row(src, a.Xp + at, d, a.ldx, stride, vec, lane);
+    if (a.Xp) pack_row(src, a.Xp + at, d, a.ldx, stride, lane);
   };
   const int pad = block - (row_blocks - kPadBlocks);
   if (pad >= 0) {
@@ -337,7 +338,7 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
         a.target[i] = -1;
         if (a.dloss) a.g[i] = a.lse2[i] = 0.0f;
       }
-      if (i < end) pack(static_cast<const T*>(a.X), i, 0, true);
+      if (i < end) pack(static_cast<const T*>(a.X), i, 0);
     }
     return;
   }
@@ -356,13 +357,12 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
     }
     a.inv[mine] = mine_on ? at : -1;
   }
-  const bool vec = a.d % VN == 0 && is_aligned(a.X, 16);
 #pragma unroll
   for (int q = 0; q < kPackRows / 4; ++q) {
     const int r = q * 4 + wave;
     if (!((b >> r) & 1)) continue;
     const int at = before + __popcll(b & ((1ull << r) - 1));
-    pack(static_cast<const T*>(a.X) + static_cast<int64_t>(n0 + r) * a.d, at, a.d, vec);
+    pack(static_cast<const T*>(a.X) + static_cast<int64_t>(n0 + r) * a.d, at, a.d);
   }
 }
 
@@ -936,12 +936,11 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void stats_kernel(const Vo
 }
 
 // A tile of bf16 values, staged in LDS and written in whole rows: an accumulator value's N is its row, its M its column. Rows >= n_rows
-// and columns >= n_cols are not written (n_cols a multiple of eight, or vec
-// false: element by element). 16-byte chunk c of row R sits in slot c ^ (R mod
+// and columns >= n_cols are not written. 16-byte chunk c of row R sits in slot c ^ (R mod
 // the chunks of a row).
 template <class G, class F>
 __device__ __forceinline__ void write_tile(char* smem, bf16* dst, int64_t ld, int n_rows, int n_cols,
-                                           bool vec, F value) {
+                                           F value) {
   constexpr int kRow = 2 * G::kTile, kChunks = kRow / 16, kPer = 64 / kChunks;  // rows a wave writes
   static_assert(G::kTile * kRow <= G::kLds, "the staged tile fits");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -964,16 +963,8 @@ __device__ __forceinline__ void write_tile(char* smem, bf16* dst, int64_t ld, in
   for (int it = 0; it < G::kTile / (kPer * G::kWaves); ++it) {
     const int r = (it * G::kWaves + wave) * kPer + lane / kChunks, c = lane % kChunks;
     const bf16x8 v = lds_read_b128(smem + r * kRow + (c ^ (r % kChunks)) * 16);
-    if (r < n_rows && c * 8 < n_cols) {
-      bf16* p = dst + static_cast<int64_t>(r) * ld + c * 8;
-      if (vec) {
-        *reinterpret_cast<bf16x8*>(p) = v;
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (c * 8 + q < n_cols) p[q] = v[q];
-      }
-    }
+    if (r < n_rows && c * 8 < n_cols)
+      store_row(dst + static_cast<int64_t>(r) * ld + c * 8, n_cols - c * 8, v);
   }
 }
 
@@ -1052,13 +1043,39 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void grad_logits_kernel(co
   }
   bf16* dst = a.D + static_cast<int64_t>(r0) * a.ldd + c0;
   if constexpr (PARTS == 1) {
-    write_tile<G>(smem, dst, a.ldd, G::kTile, G::kTile, true,
+    write_tile<G>(smem, dst, a.ldd, G::kTile, G::kTile,
                [&](int nb, int mb, int i) { return from_float<bf16>(acc.v[mb][nb][i]); });
   } else {
 #pragma unroll
     for (int q = 0; q < 3; ++q)
-      write_tile<G>(smem, dst + static_cast<int64_t>(q) * a.np * a.ldd, a.ldd, G::kTile, G::kTile, true,
+      write_tile<G>(smem, dst + static_cast<int64_t>(q) * a.np * a.ldd, a.ldd, G::kTile, G::kTile,
                  [&](int nb, int mb, int i) { return take_part(acc.v[mb][nb], i); });
+  }
+}
+
+// Writes a tile to rows of ld floats, or adds it to them: an accumulator value's N
+// is its row, its M its column. Columns >= n_cols (a multiple of 16) stay.
+template <class G>
+__device__ __forceinline__ void add_tile(float* dst, int64_t ld, int n_cols, bool add,
+                                         const typename G::Acc& acc) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
+#pragma unroll
+  for (int mb = 0; mb < G::kMB; ++mb) {
+    const int c = G::kWaveM * wm + 16 * mb;
+    if (c >= n_cols) continue;
+#pragma unroll
+    for (int nb = 0; nb < G::kNB; ++nb) {
+      f32x4* p = reinterpret_cast<f32x4*>(
+          dst + static_cast<int64_t>(G::kWaveN * wn + 16 * nb + r16) * ld + c + 4 * kq);
+      f32x4 x = acc.v[mb][nb];
+      if (add) {
+        const f32x4 y = *p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] += y[i];
+      }
+      *p = x;
+    }
   }
 }
 
@@ -1078,50 +1095,44 @@ __device__ __forceinline__ void dx_tile(const VocabArgs& a, int block, char* sme
       rows_operand(a.D + static_cast<int64_t>(r0) * a.ldd + k0 * kStepK, a.ldd,
                    static_cast<int64_t>(a.np) * a.ldd, G::kTile, a.ldd - k0 * kStepK),
       k1 - k0, smem, acc);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
-  float* dst = a.dXacc + (static_cast<int64_t>(split) * a.np + r0 + G::kWaveN * wn + r16) * a.ldx + c0 +
-               G::kWaveM * wm + 4 * kq;
-#pragma unroll
-  for (int mb = 0; mb < G::kMB; ++mb) {
-    if (c0 + G::kWaveM * wm + 16 * mb >= a.ldx) continue;
-#pragma unroll
-    for (int nb = 0; nb < G::kNB; ++nb) {
-      f32x4* p = reinterpret_cast<f32x4*>(dst + static_cast<int64_t>(16 * nb) * a.ldx + 16 * mb);
-      f32x4 x = acc.v[mb][nb];
-      if (a.v0 != 0) {
-        const f32x4 y = *p;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] += y[i];
-      }
-      *p = x;
-    }
-  }
+  add_tile<G>(a.dXacc + (static_cast<int64_t>(split) * a.np + r0) * a.ldx + c0, a.ldx, a.ldx - c0,
+              a.v0 != 0, acc);
 }
 
-// The piece's rows of dE = D^T Xp, rounded once.
+// The piece's rows of dE = D^T Xp, rounded once; with several splits of the packed
+// rows, each split's sums.
 template <class G, typename T>
 __device__ __forceinline__ void de_tile(const VocabArgs& a, T* dE, int block, char* smem) {
   constexpr int PARTS = kParts<T>;
   int mt, nt;
   const int ct = (a.ldx + G::kTile - 1) / G::kTile;
   // (bands of eight run over the vocabulary, the longer side)
-  if (!tile_of_block(block, (a.vn + G::kTile - 1) / G::kTile, ct, nt, mt)) return;
-  const int c0 = mt * G::kTile, w0 = nt * G::kTile, rows = a.count[0];
+  if (!tile_of_block(block, (a.vn + G::kTile - 1) / G::kTile, ct * a.splits_e, nt, mt)) return;
+  const int split = mt / ct;
+  const int c0 = (mt - split * ct) * G::kTile, w0 = nt * G::kTile;
+  const int steps = (a.count[0] + kStepK - 1) / kStepK, per = (steps + a.splits_e - 1) / a.splits_e;
+  const int k0 = min(steps, split * per), k1 = min(steps, k0 + per);
+  const int64_t row = static_cast<int64_t>(k0) * kStepK;
   typename G::Acc acc;
   tile_product<G, PARTS, true, true>(
-      rows_operand(a.Xp + c0, a.ldx, static_cast<int64_t>(a.np) * a.ldx, a.np, a.ldx - c0),
-      rows_operand(a.D + w0, a.ldd, static_cast<int64_t>(a.np) * a.ldd, a.np, G::kTile),
-      (rows + kStepK - 1) / kStepK, smem, acc);
+      rows_operand(a.Xp + row * a.ldx + c0, a.ldx, static_cast<int64_t>(a.np) * a.ldx,
+                   a.np - k0 * kStepK, a.ldx - c0),
+      rows_operand(a.D + row * a.ldd + w0, a.ldd, static_cast<int64_t>(a.np) * a.ldd,
+                   a.np - k0 * kStepK, G::kTile),
+      k1 - k0, smem, acc);
+  if (a.splits_e > 1) {
+    add_tile<G>(a.dEacc + (static_cast<int64_t>(split) * a.ldd + w0) * a.ldx + c0, a.ldx, a.ldx - c0,
+                false, acc);
+    return;
+  }
   T* dst = dE + (static_cast<int64_t>(a.v0) + w0) * a.d + c0;
   const int n_rows = a.vn - w0, n_cols = a.d - c0;
   if constexpr (PARTS == 1) {
-    write_tile<G>(smem, dst, a.d, n_rows, n_cols, a.d % 8 == 0 && is_aligned(dE, 16),
+    write_tile<G>(smem, dst, a.d, n_rows, n_cols,
                [&](int nb, int mb, int i) { return from_float<bf16>(acc.v[mb][nb][i]); });
   } else {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
-    const bool vec = a.d % 4 == 0 && is_aligned(dE, 16);
 #pragma unroll
     for (int nb = 0; nb < G::kNB; ++nb) {
       const int r = G::kWaveN * wn + 16 * nb + r16;
@@ -1129,14 +1140,7 @@ __device__ __forceinline__ void de_tile(const VocabArgs& a, T* dE, int block, ch
 #pragma unroll
       for (int mb = 0; mb < G::kMB; ++mb) {
         const int c = G::kWaveM * wm + 16 * mb + 4 * kq;
-        T* p = dst + static_cast<int64_t>(r) * a.d + c;
-        if (vec && c + 4 <= n_cols) {
-          *reinterpret_cast<f32x4*>(p) = acc.v[mb][nb];
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (c + q < n_cols) p[q] = acc.v[mb][nb][q];
-        }
+        store_row(dst + static_cast<int64_t>(r) * a.d + c, n_cols - c, acc.v[mb][nb]);
       }
     }
   }
@@ -1152,15 +1156,28 @@ __global__ __launch_bounds__(kThreads) void lse_kernel(const VocabArgs a, int ti
     if (lane == 0) a.loss[n] = 0.0f, a.lse[n] = 0.0f;
     return;
   }
-  float m = -INFINITY;
-  for (int t = lane; t < tiles; t += 64) m = fmaxf(m, a.part[static_cast<int64_t>(t) * a.np + i].x);
+  // eight tiles of a lane in flight: with few rows their latency is the time
+  float m = -INFINITY, s = 0.0f;
+  for (int t0 = lane; t0 < tiles; t0 += 8 * 64) {
+    float2 p[8];
+    float mm = m;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      p[u] = a.part[static_cast<int64_t>(min(t0 + u * 64, tiles - 1)) * a.np + i];
+      if (t0 + u * 64 >= tiles) p[u] = make_float2(-INFINITY, 0.0f);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) mm = fmaxf(mm, p[u].x);
+    const float ref = mm == -INFINITY ? 0.0f : mm;
+    s *= exp2_(m - ref);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s = fmaf(p[u].y, exp2_(p[u].x - ref), s);
+    m = mm;
+  }
+  const float lane_m = m;
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-  float s = 0.0f;
-  for (int t = lane; t < tiles; t += 64) {
-    const float2 p = a.part[static_cast<int64_t>(t) * a.np + i];
-    s = fmaf(p.y, exp2_(p.x - m), s);
-  }
+  s *= exp2_(lane_m - (m == -INFINITY ? 0.0f : m));
   s = wave_sum(s);
   const float lse = kLn2 * m + logf(s);
   float qz = 0.0f;
@@ -1188,31 +1205,36 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void products_kernel(const
   else if (DE) de_tile<G, T>(a, dE, block - dx_blocks, smem);
 }
 
-// dX[n] = the row's sums over the splits, rounded once; zero without target.
-// Each thread takes four columns of a row.
+// Row n of a gradient: its sums in `splits` arrays (stride floats apart) of rows
+// of a.ldx, added in order and rounded once. With inv, row inv[n] of them, and
+// zero where that is negative (a row without target). lanes = 2^lane_bits
+// threads a row, each four columns at a time, so that narrow rows share a block.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void dx_out_kernel(const VocabArgs a, T* dX) {
-  const int64_t n = blockIdx.x;
-  const int i = a.inv[n];
-  const bool vec = a.d % 4 == 0 && is_aligned(dX, 4 * sizeof(T));
-  const float* src = a.dXacc + static_cast<int64_t>(max(i, 0)) * a.ldx;
-  const int64_t stride = static_cast<int64_t>(a.np) * a.ldx;
-  for (int c = threadIdx.x * 4; c < a.d; c += kThreads * 4) {
+__global__ __launch_bounds__(kThreads) void out_kernel(const VocabArgs a, const float* sums,
+                                                       int64_t stride, int splits, const int32_t* inv,
+                                                       int64_t rows, int lane_bits, T* out) {
+  const int64_t n = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> lane_bits;
+  if (n >= rows) return;
+  const int64_t i = inv ? inv[n] : n;
+  const bool vec = a.d % 4 == 0 && is_aligned(out, 4 * sizeof(T));
+  const float* src = sums + (i < 0 ? 0 : i) * a.ldx;
+  const int lanes = 1 << lane_bits;
+  for (int c = (threadIdx.x & (lanes - 1)) * 4; c < a.d; c += lanes * 4) {
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
     if (i >= 0)
-      for (int s0 = 0; s0 < a.splits; s0 += 4) {
-        f32x4 y[4];
+      for (int s0 = 0; s0 < splits; s0 += 8) {  // (eight loads in flight)
+        f32x4 y[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          y[u] = *reinterpret_cast<const f32x4*>(src + min(s0 + u, a.splits - 1) * stride + c);
+        for (int u = 0; u < 8; ++u)
+          y[u] = *reinterpret_cast<const f32x4*>(src + min(s0 + u, splits - 1) * stride + c);
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (s0 + u < a.splits) {
+        for (int u = 0; u < 8; ++u)
+          if (s0 + u < splits) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) x[q] += y[u][q];
           }
       }
-    T* p = dX + n * a.d + c;
+    T* p = out + n * a.d + c;
     if (vec) {
       store4<T>(p, x[0], x[1], x[2], x[3]);
     } else {
@@ -1283,12 +1305,44 @@ void with_tile(int64_t tiles, int64_t rows, F fn) {
 // is needed only where the caller's is not 16-byte aligned.
 constexpr int64_t kPieceBytes = 512ll << 20, kRarePieceBytes = 64ll << 20;
 
+// Tiles and splits of K for an output of m x n values over `steps` K steps of
+// `combos` products. Modelled on measurements: a K step takes 1.7 us in a big
+// tile, 1.3 in a small one with two on each CU, 0.7 with one, and a block 4 us
+// around its steps; the splits' sums are written and read at 4 TB/s. What counts
+// is that the last round of blocks leaves few CUs idle.
+// dE at 6633 x 576 x 2325, fp32 (30 big tiles of 624 steps): 692 us without
+// splits, 145 us with 8 and their sum.
+struct Split {
+  bool big;
+  int32_t splits;
+};
+Split choose_split(int64_t m, int64_t n, int64_t steps, int combos, bool sums_anyway) {
+  Split best{true, 1};
+  double best_us = 1e30;
+  for (const bool big : {true, false}) {
+    const int64_t tile = big ? BigTile::kTile : SmallTile::kTile, slots = big ? 256 : 512;
+    const int64_t tiles = ceil_div(m, tile) * ceil_div(n, tile);
+    const int64_t most = std::max<int64_t>(1, std::min(slots / tiles, steps / 2));
+    for (int64_t k = 1; k <= most; ++k) {
+      const int64_t blocks = tiles * k;
+      const double step = big ? 1.7 : blocks > 256 ? 1.3 : 0.7;
+      double us = static_cast<double>(ceil_div(blocks, slots)) *
+                  (static_cast<double>(ceil_div(steps, k) * combos) * step + 4.0);
+      if (k > 1 || sums_anyway)
+        us += (sums_anyway ? 0.0 : 5.0) + static_cast<double>(k * m * n) * 8 / 4e6;
+      if (us < best_us) best_us = us, best = {big, static_cast<int32_t>(k)};
+    }
+  }
+  return best;
+}
+
 struct VocabPlan {
   int64_t ldx = 0, np = 0, piece = 0, packed_piece = 0;
-  int32_t splits = 1;
+  int32_t splits = 1, splits_e = 1;
+  bool big_x = false, big_e = false;  // dX's and dE's tiles
   bool packed = false;  // the table is packed whatever its alignment
   size_t off_flag, off_count, off_row, off_inv, off_target, off_g, off_lse2, off_q, off_ent, off_zt, off_qu, off_nu, off_bits,
-      off_before, off_Xp, off_Ep, off_Xh, off_Eh, off_sx, off_se, off_part, off_D, off_dX, total;
+      off_before, off_Xp, off_Ep, off_Xh, off_Eh, off_sx, off_se, off_part, off_D, off_dX, off_dE, total;
 };
 
 int64_t whole_pads(int64_t x) { return std::max<int64_t>(kPad, x / kPad * kPad); }
@@ -1308,12 +1362,14 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
     p.piece = std::min({p.piece, whole_pads(kPieceBytes / (N * 10) * 64), int64_t{64 * kMaxWords}});
   if (p.packed) p.piece = std::min(p.piece, whole_pads(kPieceBytes / row_bytes));
   p.packed_piece = p.packed ? p.piece : std::min(p.piece, whole_pads(kRarePieceBytes / row_bytes));
-  // dX has few tiles when rows are few: the sum over the vocabulary is then
-  // split so that the blocks fill the chip's 256 CUs, each with at least two
-  // K steps
-  const int64_t tiles = p.np / BigTile::kTile * ceil_div(p.ldx, BigTile::kTile);
-  p.splits = static_cast<int32_t>(
-      std::max<int64_t>(1, std::min<int64_t>(256 / tiles, p.piece / kStepK / 2)));
+  if (grad) {
+    const int combos = parts == 1 ? 1 : Combos<3>::n;
+    const int64_t piece_rows = std::min(V, p.piece);
+    const Split x = choose_split(N, p.ldx, ceil_div(piece_rows, kStepK), combos, true);
+    const Split e = choose_split(piece_rows, p.ldx, ceil_div(N, kStepK), combos, false);
+    p.big_x = x.big, p.splits = x.splits;
+    p.big_e = e.big, p.splits_e = e.splits;
+  }
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -1347,6 +1403,7 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   p.off_part = take(grad ? 0 : ceil_div(V, big ? BigTile::kTile : SmallTile::kTile) * p.np * 8);
   p.off_D = take(grad ? parts * p.np * p.piece * 2 : 0);
   p.off_dX = take(grad ? p.splits * p.np * p.ldx * 4 : 0);
+  p.off_dE = take(p.splits_e > 1 ? p.splits_e * p.piece * p.ldx * 4 : 0);
   p.total = off;
   return p;
 }
@@ -1395,6 +1452,8 @@ VocabArgs make_args(const VocabCall& c, const VocabPlan& p, char* ws, bool rows,
   a.dXacc = reinterpret_cast<float*>(ws + p.off_dX);
   a.ldd = static_cast<int32_t>(pack ? p.packed_piece : p.piece);
   a.splits = p.splits;
+  a.splits_e = p.splits_e;
+  a.dEacc = reinterpret_cast<float*>(ws + p.off_dE);
   return a;
 }
 
@@ -1443,36 +1502,63 @@ int run_loss(VocabArgs a, hipStream_t s) {
   return check_launch("vocab loss");
 }
 
+// Each row's sums over the splits, rounded.
 template <typename T>
-int run_grad(VocabArgs a, void* dX, void* dE, hipStream_t s) {
-  const int64_t big = BigTile::kTile, rt = a.np / big, ct = ceil_div(a.ldx, big);
+void launch_out(const VocabArgs& a, const float* sums, int64_t stride, int splits, const int32_t* inv,
+                int64_t rows, T* out, hipStream_t s) {
+  int bits = 0;
+  while (bits < 8 && 4 << bits < a.d) ++bits;
+  hipLaunchKernelGGL(out_kernel<T>, dim3(blocks_of(rows, kThreads >> bits)), dim3(kThreads), 0, s, a,
+                     sums, stride, splits, inv, rows, bits, out);
+}
+
+template <class F>
+void with_tile(bool big, F fn) {
+  if (big) fn(BigTile());
+  else fn(SmallTile());
+}
+
+template <typename T>
+int run_grad(VocabArgs a, const VocabPlan& p, void* dX, void* dE, hipStream_t s) {
   for_pieces<T>(a, s, [&] {
-    const int64_t vt = ceil_div(a.vn, big);
-    with_tile(vt * rt, a.N, [&](auto g) {
+    with_tile(ceil_div(a.vn, BigTile::kTile) * (a.np / BigTile::kTile), a.N, [&](auto g) {
       typedef decltype(g) G;
       const dim3 grid = tile_grid(ceil_div(a.vn, G::kTile), a.np / G::kTile), b(G::kThreads);
       if (a.t) hipLaunchKernelGGL((grad_logits_kernel<G, kParts<T>, true>), grid, b, 0, s, a);
       else hipLaunchKernelGGL((grad_logits_kernel<G, kParts<T>, false>), grid, b, 0, s, a);
     });
-    with_tile((dX ? rt * ct * a.splits : 0) + (dE ? vt * ct : 0), a.N, [&](auto g) {
-      typedef decltype(g) G;
-      const int64_t gct = ceil_div(a.ldx, G::kTile);
-      const unsigned nx = dX ? tile_grid(a.np / G::kTile, gct * a.splits).x : 0;
-      const unsigned ne = dE ? tile_grid(ceil_div(a.vn, G::kTile), gct).x : 0;
-      const dim3 b(G::kThreads);
-      T* de = static_cast<T*>(dE);
-      if (G::kTile == SmallTile::kTile && dX && dE) {
-        hipLaunchKernelGGL((products_kernel<SmallTile, T, true, true>), dim3(nx + ne), b, 0, s, a,
-                           static_cast<int>(nx), de);
-        return;
-      }
-      if (dX) hipLaunchKernelGGL((products_kernel<G, T, true, false>), dim3(nx), b, 0, s, a, 0, de);
-      if (dE) hipLaunchKernelGGL((products_kernel<G, T, false, true>), dim3(ne), b, 0, s, a, 0, de);
-    });
+    T* de = static_cast<T*>(dE);
+    auto blocks_x = [&](int64_t tile) {
+      return tile_grid(a.np / tile, ceil_div(a.ldx, tile) * a.splits).x;
+    };
+    auto blocks_e = [&](int64_t tile) {
+      return tile_grid(ceil_div(a.vn, tile), ceil_div(a.ldx, tile) * a.splits_e).x;
+    };
+    if (dX && dE && !p.big_x && !p.big_e) {
+      const unsigned nx = blocks_x(SmallTile::kTile), ne = blocks_e(SmallTile::kTile);
+      hipLaunchKernelGGL((products_kernel<SmallTile, T, true, true>), dim3(nx + ne),
+                         dim3(SmallTile::kThreads), 0, s, a, static_cast<int>(nx), de);
+    } else {
+      if (dX)
+        with_tile(p.big_x, [&](auto g) {
+          typedef decltype(g) G;
+          hipLaunchKernelGGL((products_kernel<G, T, true, false>), dim3(blocks_x(G::kTile)),
+                             dim3(G::kThreads), 0, s, a, 0, de);
+        });
+      if (dE)
+        with_tile(p.big_e, [&](auto g) {
+          typedef decltype(g) G;
+          hipLaunchKernelGGL((products_kernel<G, T, false, true>), dim3(blocks_e(G::kTile)),
+                             dim3(G::kThreads), 0, s, a, 0, de);
+        });
+    }
+    if (dE && a.splits_e > 1)
+      launch_out<T>(a, a.dEacc, static_cast<int64_t>(a.ldd) * a.ldx, a.splits_e, nullptr, a.vn,
+                    de + static_cast<int64_t>(a.v0) * a.d, s);
   });
   if (dX)
-    hipLaunchKernelGGL(dx_out_kernel<T>, dim3(static_cast<unsigned>(a.N)), dim3(kThreads), 0, s, a,
-                       static_cast<T*>(dX));
+    launch_out<T>(a, a.dXacc, static_cast<int64_t>(a.np) * a.ldx, a.splits, a.inv, a.N,
+                  static_cast<T*>(dX), s);
   return check_launch("vocab gradient");
 }
 
@@ -1511,7 +1597,7 @@ int grad_impl(const VocabCall& c, bool distill, const float* lse, const float* d
   a.lse = const_cast<float*>(lse);
   a.dloss = dloss;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return c.dtype == DPG_BF16 ? run_grad<bf16>(a, dX, dE, s) : run_grad<float>(a, dX, dE, s);
+  return c.dtype == DPG_BF16 ? run_grad<bf16>(a, p, dX, dE, s) : run_grad<float>(a, p, dX, dE, s);
 }
 
 int size_impl(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, int32_t grad, bool distill,

@@ -514,3 +514,27 @@ def test_fp32_rows_of_very_different_size():
     torch.cuda.synchronize()
     assert (np.abs(_host(got_lse) - lse) <= bar).all()
     assert (np.abs(_host(got) - loss) <= bar).all()
+
+
+@pytest.mark.parametrize("act", ["fp32", "bf16"])
+@pytest.mark.parametrize("N,d,V", [(1500, 70, 300), (3000, 129, 130)])
+def test_gradients_of_many_rows_and_few_columns(N, d, V, act):
+    """Long sums for few outputs, which are split over blocks, into buffers that
+    start one element off."""
+    import torch
+    import dp_grape_projection_amd as dpg
+    print(f"[vocab] many rows N={N} d={d} V={V} {act}", flush=True)
+    X, E, ids, _, g = _loss_case(N, d, V, 1, act, 5)
+    ids = ids[:, 0]
+    q = ((ids >= 0) & (ids < V)).astype(np.float64)
+    _, want_lse, want_dX, want_dE = ot.target_loss(X, E, ids, q, 1.0, 1.0, g)
+    x, e, y = _dev(X, act, 1), _dev(E, act, 1), _dev(ids)
+    loss, lse = dpg.dpg_vocab_loss(x, e, y)
+    _check_loss(X, E, ids, q, loss, lse, 1.0, 1.0)
+    dX, dE = _dev(np.full((N, d), 7.0), act, 1), _dev(np.full((V, d), 7.0), act, 1)
+    out = dpg.dpg_vocab_loss_grad(x, e, y, lse, _dev(g), dX=dX, dE=dE)
+    assert out[0] is dX and out[1] is dE
+    assert rel_err(_host(dX), want_dX) <= TOL[act]
+    assert rel_err(_host(dE), want_dE) <= TOL[act]
+    again = dpg.dpg_vocab_loss_grad(x, e, y, lse, _dev(g))
+    assert torch.equal(again[0], dX) and torch.equal(again[1], dE)
