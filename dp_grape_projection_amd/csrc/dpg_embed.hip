@@ -13,7 +13,6 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
-#include <type_traits>
 
 #include "dpg.h"
 #include "dpg_device.hpp"
@@ -29,101 +28,79 @@ constexpr int kSortBatch = kSortThreads * kSortItems;
 // vocabularies above 256 times this.
 constexpr int kSortBins = 8192;
 
-// Rows are taken in groups of 8 columns a thread: in vectors of W elements,
-// 8 (16-byte aligned rows), 2 (4-byte aligned rows) or 1. A thread's 8 / W
-// vectors lie tpr * W columns apart, so that the threads of a row read and
-// write neighbouring vectors. col(q) is the first column of vector q.
-template <int W>
-struct RowCols {
-  int c0, step, d;
-  __device__ __forceinline__ RowCols(int group, int t, int tpr, int d_)
-      : c0(group * tpr * 8 + t * W), step(tpr * W), d(d_) {}
-  __device__ __forceinline__ int col(int q) const { return c0 + q * step; }
-  // (rows are whole vectors)
-  __device__ __forceinline__ bool in(int q) const { return col(q) < d; }
+// A thread takes eight columns of a row at a time, 16-byte vectors at any
+// element's address (the global loads and stores take them). The last thread of
+// a row whose width is no multiple of eight takes the row's last eight columns,
+// of which the first `skip` are its neighbour's too: both compute the same values
+// for them. Rows narrower than eight are taken element by element.
+struct Cols {
+  int at, skip, n;
+  __device__ __forceinline__ Cols(int c, int d)
+      : at(d < 8 ? 0 : min(c, d - 8)), skip(c - at), n(min(d, 8)) {}
 };
+typedef f32x4 any_f32x4 __attribute__((aligned(4)));
+typedef u32x4 any_u32x4 __attribute__((aligned(2)));
 
-template <int W>
-__device__ __forceinline__ void load8(const float* p, const RowCols<W>& rc, float (&v)[8]) {
+__device__ __forceinline__ void load8(const float* p, const Cols& k, float (&v)[8]) {
+  const float* x = p + k.at;
+  if (k.n == 8) {
+    const f32x4 a = *reinterpret_cast<const any_f32x4*>(x);
+    const f32x4 b = *reinterpret_cast<const any_f32x4*>(x + 4);
 #pragma unroll
-  for (int q = 0; q < 8 / W; ++q) {
-    const float* x = p + rc.col(q);
-    const bool in = rc.in(q);
-    if constexpr (W == 8) {
-      f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
-      if (in) a = *reinterpret_cast<const f32x4*>(x), b = *reinterpret_cast<const f32x4*>(x + 4);
+    for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+  } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
-    } else {
-#pragma unroll
-      for (int j = 0; j < W; ++j) v[q * W + j] = in ? x[j] : 0.0f;
-    }
+    for (int q = 0; q < 8; ++q) v[q] = q < k.n ? x[q] : 0.0f;
   }
 }
-template <int W>
-__device__ __forceinline__ void load8(const bf16* p, const RowCols<W>& rc, float (&v)[8]) {
+__device__ __forceinline__ void load8(const bf16* p, const Cols& k, float (&v)[8]) {
+  const bf16* x = p + k.at;
+  if (k.n == 8) {
+    const u32x4 a = *reinterpret_cast<const any_u32x4*>(x);
 #pragma unroll
-  for (int q = 0; q < 8 / W; ++q) {
-    const bf16* x = p + rc.col(q);
-    const bool in = rc.in(q);
-    if constexpr (W == 8) {
-      u32x4 a = {0u, 0u, 0u, 0u};
-      if (in) a = *reinterpret_cast<const u32x4*>(x);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t w = a[j];
-        v[2 * j] = __builtin_bit_cast(float, w << 16);
-        v[2 * j + 1] = __builtin_bit_cast(float, w & 0xFFFF0000u);
-      }
-    } else if constexpr (W == 2) {
-      const uint32_t w = in ? *reinterpret_cast<const uint32_t*>(x) : 0u;
-      v[2 * q] = __builtin_bit_cast(float, w << 16);
-      v[2 * q + 1] = __builtin_bit_cast(float, w & 0xFFFF0000u);
-    } else {
-      v[q] = in ? to_float(x[0]) : 0.0f;
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w = a[j];
+      v[2 * j] = __builtin_bit_cast(float, w << 16);
+      v[2 * j + 1] = __builtin_bit_cast(float, w & 0xFFFF0000u);
     }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = q < k.n ? to_float(x[q]) : 0.0f;
   }
 }
-template <int W>
-__device__ __forceinline__ void store8(float* p, const RowCols<W>& rc, const float (&v)[8]) {
+// own: only the columns that are no neighbour's.
+__device__ __forceinline__ void store8(float* p, const Cols& k, const float (&v)[8], bool own) {
+  float* x = p + k.at;
+  if (k.n == 8 && !(own && k.skip)) {
+    f32x4 a, b;
 #pragma unroll
-  for (int q = 0; q < 8 / W; ++q) {
-    if (!rc.in(q)) continue;
-    float* x = p + rc.col(q);
-    if constexpr (W == 8) {
-      f32x4 a, b;
+    for (int j = 0; j < 4; ++j) a[j] = v[j], b[j] = v[4 + j];
+    *reinterpret_cast<any_f32x4*>(x) = a;
+    *reinterpret_cast<any_f32x4*>(x + 4) = b;
+  } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a[j] = v[j], b[j] = v[4 + j];
-      *reinterpret_cast<f32x4*>(x) = a;
-      *reinterpret_cast<f32x4*>(x + 4) = b;
-    } else {
-#pragma unroll
-      for (int j = 0; j < W; ++j) x[j] = v[q * W + j];
-    }
+    for (int q = 0; q < 8; ++q)
+      if (q >= k.skip && q < k.n) x[q] = v[q];
   }
 }
-template <int W>
-__device__ __forceinline__ void store8(bf16* p, const RowCols<W>& rc, const float (&v)[8]) {
+__device__ __forceinline__ void store8(bf16* p, const Cols& k, const float (&v)[8], bool own) {
+  bf16* x = p + k.at;
+  bf16x8 a;
 #pragma unroll
-  for (int q = 0; q < 8 / W; ++q) {
-    if (!rc.in(q)) continue;
-    bf16* x = p + rc.col(q);
-    if constexpr (W == 1) {
-      x[0] = from_float<bf16>(v[q]);
-    } else {
-      typedef __attribute__((__vector_size__(W * sizeof(__bf16)))) __bf16 vec;
-      vec a;
+  for (int q = 0; q < 8; ++q) a[q] = from_float<bf16>(v[q]);
+  if (k.n == 8 && !(own && k.skip)) {
+    *reinterpret_cast<any_u32x4*>(x) = __builtin_bit_cast(u32x4, a);
+  } else {
 #pragma unroll
-      for (int j = 0; j < W; ++j) a[j] = from_float<bf16>(v[q * W + j]);
-      *reinterpret_cast<vec*>(x) = a;
-    }
+    for (int q = 0; q < 8; ++q)
+      if (q >= k.skip && q < k.n) x[q] = a[q];
   }
 }
 
 // ----------------------------------------------------------------- lookup --
 
 // 1 << tpr_log2 threads per row.
-template <typename TE, typename TY, int W>
+template <typename TE, typename TY>
 __global__ __launch_bounds__(kThreads) void embed_kernel(const int64_t* ids, int64_t n,
                                                          const TE* E, int64_t V, int d,
                                                          float scale, int tpr_log2, TY* Y) {
@@ -135,15 +112,15 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(const int64_t* ids, int
   const bool ok = id >= 0 && id < V;
   const TE* src = E + (ok ? id : 0) * d;
   TY* dst = Y + row * d;
-  for (int g = 0; g * tpr * 8 < d; ++g) {
-    const RowCols<W> rc(g, threadIdx.x & (tpr - 1), tpr, d);
+  for (int c = (threadIdx.x & (tpr - 1)) * 8; c < d; c += tpr * 8) {
+    const Cols k(c, d);
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (ok) {
-      load8(src, rc, v);
+      load8(src, k, v);
 #pragma unroll
       for (int q = 0; q < 8; ++q) v[q] *= scale;
     }
-    store8(dst, rc, v);
+    store8(dst, k, v, false);
   }
 }
 
@@ -301,9 +278,9 @@ __global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const int64_t*
 
 // acc += sum over j in [j0, j1) of w(order[j]) dY[order[j]], in order, eight
 // rows in flight.
-template <int W, typename TY, class F>
+template <typename TY, class F>
 __device__ __forceinline__ void add_rows(const TY* dY, const int* order, int j0, int j1,
-                                         const RowCols<W>& rc, F weight, float (&acc)[8]) {
+                                         int d, const Cols& k, F weight, float (&acc)[8]) {
   constexpr int U = 8;
   for (int j = j0; j < j1; j += U) {
     int pos[U];
@@ -314,7 +291,7 @@ __device__ __forceinline__ void add_rows(const TY* dY, const int* order, int j0,
     for (int u = 0; u < U; ++u)
       if (j + u < j1) {
         w[u] = weight(pos[u]);
-        load8(dY + static_cast<int64_t>(pos[u]) * rc.d, rc, x[u]);
+        load8(dY + static_cast<int64_t>(pos[u]) * d, k, x[u]);
       }
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -354,14 +331,14 @@ struct SampleWeight {
 // begins inside the chunk. (No long token lies wholly inside a chunk.) Without
 // this the most frequent token's sum, 459 rows of 7168 in a 1 / rank
 // distribution over 50304 tokens, outlasts all others: 490 us against 90.
-template <typename TY, int W>
+template <typename TY>
 __global__ __launch_bounds__(kThreads) void embed_chunk_kernel(const TY* dY, int d, SortedIds o,
                                                                SampleWeight weight, int tpr_log2,
                                                                float* part) {
   const int tpr = 1 << tpr_log2;
   const int total = o.total(), rows = kThreads >> tpr_log2;
-  const int c = blockIdx.x * rows + (threadIdx.x >> tpr_log2);
-  const int j0 = c * o.chunk, j1 = min(total, j0 + o.chunk);
+  const int chunk = blockIdx.x * rows + (threadIdx.x >> tpr_log2);
+  const int j0 = chunk * o.chunk, j1 = min(total, j0 + o.chunk);
   if (j0 >= j1) return;
   const int* first = o.range(o.ids[o.order[j0]]);
   const int* last = o.range(o.ids[o.order[j1 - 1]]);
@@ -369,17 +346,17 @@ __global__ __launch_bounds__(kThreads) void embed_chunk_kernel(const TY* dY, int
   const int slot = blockIdx.y;
   const int b = slot == 0 ? j0 : lb, e = slot == 0 ? min(fe, j1) : j1;
   if (slot == 0 ? fe - fb <= o.chunk : (lb <= j0 || le - lb <= o.chunk)) return;
-  for (int g = 0; g * tpr * 8 < d; ++g) {
-    const RowCols<W> rc(g, threadIdx.x & (tpr - 1), tpr, d);
+  for (int c = (threadIdx.x & (tpr - 1)) * 8; c < d; c += tpr * 8) {
+    const Cols k(c, d);
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    add_rows(dY, o.order, b, e, rc, weight, acc);
-    store8(part + (static_cast<int64_t>(c) * 2 + slot) * d, rc, acc);
+    add_rows(dY, o.order, b, e, d, k, weight, acc);
+    store8(part + (static_cast<int64_t>(chunk) * 2 + slot) * d, k, acc, false);
   }
 }
 
 // 1 << tpr_log2 threads per vocabulary row: its positions are added in order
 // (its chunks' sums, for a long token).
-template <typename TY, typename TE, int W>
+template <typename TY, typename TE>
 __global__ __launch_bounds__(kThreads) void embed_grad_kernel(const TY* dY, int64_t V, int d,
                                                               SortedIds o, SampleWeight weight,
                                                               const float* part, int tpr_log2,
@@ -392,23 +369,23 @@ __global__ __launch_bounds__(kThreads) void embed_grad_kernel(const TY* dY, int6
   const int j0 = st[0], j1 = st[1];
   if (accumulate && j0 == j1) return;
   TE* dst = dE + v * d;
-  for (int g = 0; g * tpr * 8 < d; ++g) {
-    const RowCols<W> rc(g, threadIdx.x & (tpr - 1), tpr, d);
+  for (int c = (threadIdx.x & (tpr - 1)) * 8; c < d; c += tpr * 8) {
+    const Cols k(c, d);
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (j1 - j0 <= o.chunk) {
-      add_rows(dY, o.order, j0, j1, rc, weight, acc);
+      add_rows(dY, o.order, j0, j1, d, k, weight, acc);
     } else {
-      const int c0 = j0 / o.chunk, c1 = (j1 - 1) / o.chunk;
-      for (int c = c0; c <= c1; c += 8) {
+      const int h0 = j0 / o.chunk, h1 = (j1 - 1) / o.chunk;
+      for (int h = h0; h <= h1; h += 8) {
         float x[8][8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const int at = min(c + u, c1);
-          load8(part + (static_cast<int64_t>(at) * 2 + (at == c0 && j0 % o.chunk != 0)) * d, rc, x[u]);
+          const int at = min(h + u, h1);
+          load8(part + (static_cast<int64_t>(at) * 2 + (at == h0 && j0 % o.chunk != 0)) * d, k, x[u]);
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-          if (c + u <= c1) {
+          if (h + u <= h1) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) acc[q] += x[u][q];
           }
@@ -416,11 +393,11 @@ __global__ __launch_bounds__(kThreads) void embed_grad_kernel(const TY* dY, int6
     }
     if (accumulate) {
       float x[8];
-      load8(dst, rc, x);
+      load8(dst, k, x);
 #pragma unroll
       for (int q = 0; q < 8; ++q) acc[q] += x[q];
     }
-    store8(dst, rc, acc);
+    store8(dst, k, acc, accumulate != 0);
   }
 }
 
@@ -429,7 +406,7 @@ __global__ __launch_bounds__(kThreads) void embed_grad_kernel(const TY* dY, int6
 // 1 << tpr_log2 threads per entry of `order`: the first entry of a (token,
 // sample) run adds the run's rows and writes the squared norm of the sum at
 // its position, the others write zero.
-template <typename TY, int W>
+template <typename TY>
 __global__ __launch_bounds__(kThreads) void embed_run_norm_kernel(const TY* dY, int d, SortedIds o,
                                                                   int T, float scale,
                                                                   float* run_sq) {
@@ -460,12 +437,13 @@ __global__ __launch_bounds__(kThreads) void embed_run_norm_kernel(const TY* dY, 
     e += 64;
   }
   float sq = 0.0f;
-  for (int g = 0; g * kThreads * 8 < d; ++g) {
-    const RowCols<W> rc(g, threadIdx.x, kThreads, d);
+  for (int c = threadIdx.x * 8; c < d; c += kThreads * 8) {
+    const Cols k(c, d);
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    add_rows(dY, o.order, j, e, rc, [](int) { return 1.0f; }, acc);
+    add_rows(dY, o.order, j, e, d, k, [](int) { return 1.0f; }, acc);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) sq = fmaf(scale * acc[q], scale * acc[q], sq);
+    for (int q = 0; q < 8; ++q)
+      if (q >= k.skip) sq = fmaf(scale * acc[q], scale * acc[q], sq);
   }
   sq = wave_sum(sq);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sq;
@@ -477,7 +455,7 @@ __global__ __launch_bounds__(kThreads) void embed_run_norm_kernel(const TY* dY, 
 // its id with its sample's other ids (T * 8 bytes of L2 reads a block); the
 // first position of a run lists the others in LDS, in order.
 constexpr int kShortSample = 1024;
-template <typename TY, int W>
+template <typename TY>
 __global__ __launch_bounds__(kThreads) void embed_short_norm_kernel(const int64_t* ids,
                                                                     const TY* dY, int64_t V, int d,
                                                                     int T, float scale,
@@ -513,12 +491,13 @@ __global__ __launch_bounds__(kThreads) void embed_short_norm_kernel(const int64_
     return;
   }
   float sq = 0.0f;
-  for (int g = 0; g * kThreads * 8 < d; ++g) {
-    const RowCols<W> rc(g, tid, kThreads, d);
+  for (int c = tid * 8; c < d; c += kThreads * 8) {
+    const Cols k(c, d);
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    add_rows(dY, list, 0, all, rc, [](int) { return 1.0f; }, acc);
+    add_rows(dY, list, 0, all, d, k, [](int) { return 1.0f; }, acc);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) sq = fmaf(scale * acc[q], scale * acc[q], sq);
+    for (int q = 0; q < 8; ++q)
+      if (q >= k.skip) sq = fmaf(scale * acc[q], scale * acc[q], sq);
   }
   sq = wave_sum(sq);
   if (lane == 0) red[wave] = sq;
@@ -554,19 +533,6 @@ int check_launch(const char* what) {
 }
 
 bool valid_dtype(int32_t t) { return t == DPG_FP32 || t == DPG_BF16; }
-bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-// Elements a vector access may take in rows of d columns of these arrays.
-int row_vector(int64_t d, const void* p, const void* q) {
-  if (d % 8 == 0 && aligned(p, 16) && aligned(q, 16)) return 8;
-  return d % 2 == 0 && aligned(p, 4) && aligned(q, 4) ? 2 : 1;
-}
-// fn with the width as a constant.
-template <class F>
-void with_width(int w, F fn) {
-  if (w == 8) fn(std::integral_constant<int, 8>{});
-  else if (w == 2) fn(std::integral_constant<int, 2>{});
-  else fn(std::integral_constant<int, 1>{});
-}
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
 // log2 of the threads that share a row of d columns: one per unit of eight
@@ -646,12 +612,10 @@ template <typename TE, typename TY>
 void launch_embed(const int64_t* ids, int64_t n, const void* E, int64_t V, int64_t d, double scale,
                   void* Y, hipStream_t s) {
   const int l = row_threads_log2(d);
-  with_width(row_vector(d, E, Y), [&](auto w) {
-    hipLaunchKernelGGL((embed_kernel<TE, TY, decltype(w)::value>),
-                       dim3(static_cast<unsigned>(ceil_div(n, kThreads >> l))), dim3(kThreads), 0,
-                       s, ids, n, static_cast<const TE*>(E), V, static_cast<int>(d),
-                       static_cast<float>(scale), l, static_cast<TY*>(Y));
-  });
+  hipLaunchKernelGGL((embed_kernel<TE, TY>),
+                     dim3(static_cast<unsigned>(ceil_div(n, kThreads >> l))), dim3(kThreads), 0, s,
+                     ids, n, static_cast<const TE*>(E), V, static_cast<int>(d),
+                     static_cast<float>(scale), l, static_cast<TY*>(Y));
 }
 
 template <typename TY, typename TE>
@@ -664,15 +628,13 @@ void launch_embed_grad(const SortPlan& p, const int64_t* ids, const void* dY, in
   const SampleWeight weight{sample_scales, static_cast<float>(scale), static_cast<int>(T)};
   float* part = reinterpret_cast<float*>(ws + p.off_part);
   const TY* dy = static_cast<const TY*>(dY);
-  with_width(row_vector(d, dY, dE), [&](auto w) {
-    if (n > p.chunk)
-      hipLaunchKernelGGL((embed_chunk_kernel<TY, decltype(w)::value>),
-                         dim3(static_cast<unsigned>(ceil_div(p.chunks, kThreads >> l)), 2), b, 0, s,
-                         dy, static_cast<int>(d), o, weight, l, part);
-    hipLaunchKernelGGL((embed_grad_kernel<TY, TE, decltype(w)::value>),
-                       dim3(static_cast<unsigned>(ceil_div(V, kThreads >> l))), b, 0, s, dy, V,
-                       static_cast<int>(d), o, weight, part, l, accumulate, static_cast<TE*>(dE));
-  });
+  if (n > p.chunk)
+    hipLaunchKernelGGL(embed_chunk_kernel<TY>,
+                       dim3(static_cast<unsigned>(ceil_div(p.chunks, kThreads >> l)), 2), b, 0, s, dy,
+                       static_cast<int>(d), o, weight, l, part);
+  hipLaunchKernelGGL((embed_grad_kernel<TY, TE>),
+                     dim3(static_cast<unsigned>(ceil_div(V, kThreads >> l))), b, 0, s, dy, V,
+                     static_cast<int>(d), o, weight, part, l, accumulate, static_cast<TE*>(dE));
 }
 
 }  // namespace
@@ -730,19 +692,15 @@ int dpg_embed_norms(const int64_t* ids, const void* dY, int64_t B, int64_t T, in
   float* run_sq = reinterpret_cast<float*>(ws + p.off_run);
   auto go = [&](auto zero) {
     typedef decltype(zero) TY;
-    with_width(row_vector(d, dY, dY), [&](auto w) {
-      if (!sorted) {
-        hipLaunchKernelGGL((embed_short_norm_kernel<TY, decltype(w)::value>),
-                           dim3(static_cast<unsigned>(B * T)), dim3(kThreads), 0, s, ids,
-                           static_cast<const TY*>(dY), V, static_cast<int>(d),
-                           static_cast<int>(T), static_cast<float>(scale), run_sq);
-        return;
-      }
-      hipLaunchKernelGGL((embed_run_norm_kernel<TY, decltype(w)::value>),
-                         dim3(static_cast<unsigned>(B * T)), dim3(kThreads), 0, s,
-                         static_cast<const TY*>(dY), static_cast<int>(d), p.sorted(ids, ws),
-                         static_cast<int>(T), static_cast<float>(scale), run_sq);
-    });
+    if (!sorted) {
+      hipLaunchKernelGGL(embed_short_norm_kernel<TY>, dim3(static_cast<unsigned>(B * T)),
+                         dim3(kThreads), 0, s, ids, static_cast<const TY*>(dY), V,
+                         static_cast<int>(d), static_cast<int>(T), static_cast<float>(scale), run_sq);
+      return;
+    }
+    hipLaunchKernelGGL(embed_run_norm_kernel<TY>, dim3(static_cast<unsigned>(B * T)),
+                       dim3(kThreads), 0, s, static_cast<const TY*>(dY), static_cast<int>(d),
+                       p.sorted(ids, ws), static_cast<int>(T), static_cast<float>(scale), run_sq);
   };
   if (dtype == DPG_BF16) go(bf16());
   else go(0.0f);
