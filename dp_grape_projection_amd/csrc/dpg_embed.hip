@@ -37,37 +37,49 @@ struct Cols {
   int at, skip, n;
   __device__ __forceinline__ Cols(int c, int d)
       : at(d < 8 ? 0 : min(c, d - 8)), skip(c - at), n(min(d, 8)) {}
+  // (past the row's end, all eight columns are skipped, and loads stay inside)
 };
 typedef f32x4 any_f32x4 __attribute__((aligned(4)));
 typedef u32x4 any_u32x4 __attribute__((aligned(2)));
 
-__device__ __forceinline__ void load8(const float* p, const Cols& k, float (&v)[8]) {
-  const float* x = p + k.at;
-  if (k.n == 8) {
-    const f32x4 a = *reinterpret_cast<const any_f32x4*>(x);
-    const f32x4 b = *reinterpret_cast<const any_f32x4*>(x + 4);
+// Eight columns as loaded; expanded where they are used, so that loads do not wait
+// for one another.
+template <typename T> struct Raw8;
+template <> struct Raw8<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const float* p, const Cols& k) {
+    const float* x = p + k.at;
+    if (k.n == 8) {
+      a = *reinterpret_cast<const any_f32x4*>(x);
+      b = *reinterpret_cast<const any_f32x4*>(x + 4);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = q < k.n ? x[q] : 0.0f;
-  }
-}
-__device__ __forceinline__ void load8(const bf16* p, const Cols& k, float (&v)[8]) {
-  const bf16* x = p + k.at;
-  if (k.n == 8) {
-    const u32x4 a = *reinterpret_cast<const any_u32x4*>(x);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t w = a[j];
-      v[2 * j] = __builtin_bit_cast(float, w << 16);
-      v[2 * j + 1] = __builtin_bit_cast(float, w & 0xFFFF0000u);
+      for (int q = 0; q < 4; ++q) {
+        a[q] = q < k.n ? x[q] : 0.0f;
+        b[q] = 4 + q < k.n ? x[4 + q] : 0.0f;
+      }
     }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = q < k.n ? to_float(x[q]) : 0.0f;
   }
-}
+  __device__ __forceinline__ float operator[](int q) const { return q < 4 ? a[q & 3] : b[q & 3]; }
+};
+template <> struct Raw8<bf16> {
+  u32x4 a;
+  __device__ __forceinline__ void load(const bf16* p, const Cols& k) {
+    const bf16* x = p + k.at;
+    if (k.n == 8) {
+      a = *reinterpret_cast<const any_u32x4*>(x);
+    } else {
+      bf16x8 v;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = q < k.n ? x[q] : zero_val<bf16>();
+      a = __builtin_bit_cast(u32x4, v);
+    }
+  }
+  __device__ __forceinline__ float operator[](int q) const {
+    const uint32_t w = a[q >> 1];
+    return __builtin_bit_cast(float, q & 1 ? w & 0xFFFF0000u : w << 16);
+  }
+};
 // own: only the columns that are no neighbour's.
 __device__ __forceinline__ void store8(float* p, const Cols& k, const float (&v)[8], bool own) {
   float* x = p + k.at;
@@ -116,9 +128,10 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(const int64_t* ids, int
     const Cols k(c, d);
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (ok) {
-      load8(src, k, v);
+      Raw8<TE> x;
+      x.load(src, k);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] *= scale;
+      for (int q = 0; q < 8; ++q) v[q] = scale * x[q];
     }
     store8(dst, k, v, false);
   }
@@ -284,15 +297,14 @@ __device__ __forceinline__ void add_rows(const TY* dY, const int* order, int j0,
   constexpr int U = 8;
   for (int j = j0; j < j1; j += U) {
     int pos[U];
-    float w[U], x[U][8];
+    float w[U];
+    Raw8<TY> x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) pos[u] = order[min(j + u, j1 - 1)];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (j + u < j1) {
-        w[u] = weight(pos[u]);
-        load8(dY + static_cast<int64_t>(pos[u]) * d, k, x[u]);
-      }
+    for (int u = 0; u < U; ++u) w[u] = weight(pos[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u].load(dY + static_cast<int64_t>(pos[u]) * d, k);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (j + u < j1) {
@@ -377,11 +389,11 @@ __global__ __launch_bounds__(kThreads) void embed_grad_kernel(const TY* dY, int6
     } else {
       const int h0 = j0 / o.chunk, h1 = (j1 - 1) / o.chunk;
       for (int h = h0; h <= h1; h += 8) {
-        float x[8][8];
+        Raw8<float> x[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const int at = min(h + u, h1);
-          load8(part + (static_cast<int64_t>(at) * 2 + (at == h0 && j0 % o.chunk != 0)) * d, k, x[u]);
+          x[u].load(part + (static_cast<int64_t>(at) * 2 + (at == h0 && j0 % o.chunk != 0)) * d, k);
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u)
@@ -392,8 +404,8 @@ __global__ __launch_bounds__(kThreads) void embed_grad_kernel(const TY* dY, int6
       }
     }
     if (accumulate) {
-      float x[8];
-      load8(dst, k, x);
+      Raw8<TE> x;
+      x.load(dst, k);
 #pragma unroll
       for (int q = 0; q < 8; ++q) acc[q] += x[q];
     }
@@ -403,14 +415,75 @@ __global__ __launch_bounds__(kThreads) void embed_grad_kernel(const TY* dY, int6
 
 // ------------------------------------------------------------------ norms --
 
-// 1 << tpr_log2 threads per entry of `order`: the first entry of a (token,
+// ||scale sum over j in [j0, j1) of dY[list[j]]||^2, by one block; the same value
+// in thread 0 only. 1 << tpr_log2 threads share a row; where that leaves threads
+// over, each group of so many adds a part of a long run, and the parts are added
+// in order. A wave reads 64 entries of the list at once, so that the rows' loads
+// do not wait for their positions.
+template <typename TY>
+__device__ __forceinline__ float run_norm(const TY* dY, int d, const int* list, int j0, int j1,
+                                          int tpr_log2, float scale) {
+  constexpr int U = 8;
+  __shared__ float parts[kThreads * 8];
+  __shared__ float red[4];
+  const int tid = threadIdx.x, lane = tid & 63;
+  // (a group is one or more whole waves)
+  const int tpr = max(64, 1 << tpr_log2), groups = j1 - j0 > U ? kThreads / tpr : 1;
+  const int group = __builtin_amdgcn_readfirstlane(tid / tpr), t = tid % tpr;
+  const int per = (j1 - j0 + groups - 1) / groups;
+  const int b = j0 + group * per, e = group < groups ? min(j1, b + per) : b;
+  float sq = 0.0f;
+  for (int c0 = 0; c0 < d; c0 += tpr * 8) {
+    const int c = c0 + t * 8;
+    const Cols k(c, d);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int j = b; j < e; j += 64) {
+      const int mine = list[min(j + lane, e - 1)], m = min(64, e - j);
+      for (int u0 = 0; u0 < m; u0 += U) {
+        Raw8<TY> x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int pos = __builtin_amdgcn_readlane(mine, u0 + u);
+          x[u].load(dY + static_cast<int64_t>(pos) * d, k);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (u0 + u < m) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) acc[q] += x[u][q];
+          }
+      }
+    }
+    if (groups > 1) {
+      if (c0) __syncthreads();
+#pragma unroll
+      for (int q = 0; q < 8; ++q) parts[tid * 8 + q] = acc[q];
+      __syncthreads();
+      if (group == 0)
+        for (int g = 1; g < groups; ++g) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) acc[q] += parts[(g * tpr + t) * 8 + q];
+        }
+    }
+    if (group == 0) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q >= k.skip) sq = fmaf(scale * acc[q], scale * acc[q], sq);
+    }
+  }
+  sq = wave_sum(sq);
+  if (lane == 0) red[tid >> 6] = sq;
+  __syncthreads();
+  return ((red[0] + red[1]) + red[2]) + red[3];
+}
+
+// One block per entry of `order`: the first entry of a (token,
 // sample) run adds the run's rows and writes the squared norm of the sum at
 // its position, the others write zero.
 template <typename TY>
 __global__ __launch_bounds__(kThreads) void embed_run_norm_kernel(const TY* dY, int d, SortedIds o,
                                                                   int T, float scale,
-                                                                  float* run_sq) {
-  __shared__ float red[4];
+                                                                  int tpr_log2, float* run_sq) {
   const int j = blockIdx.x;
   if (j >= o.total()) return;
   const int pos = o.order[j];
@@ -436,19 +509,8 @@ __global__ __launch_bounds__(kThreads) void embed_run_norm_kernel(const TY* dY, 
     }
     e += 64;
   }
-  float sq = 0.0f;
-  for (int c = threadIdx.x * 8; c < d; c += kThreads * 8) {
-    const Cols k(c, d);
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    add_rows(dY, o.order, j, e, d, k, [](int) { return 1.0f; }, acc);
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (q >= k.skip) sq = fmaf(scale * acc[q], scale * acc[q], sq);
-  }
-  sq = wave_sum(sq);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sq;
-  __syncthreads();
-  if (threadIdx.x == 0) run_sq[pos] = ((red[0] + red[1]) + red[2]) + red[3];
+  const float sq = run_norm(dY, d, o.order, j, e, tpr_log2, scale);
+  if (threadIdx.x == 0) run_sq[pos] = sq;
 }
 
 // The same for short samples, without sorting: one block per position compares
@@ -459,10 +521,9 @@ template <typename TY>
 __global__ __launch_bounds__(kThreads) void embed_short_norm_kernel(const int64_t* ids,
                                                                     const TY* dY, int64_t V, int d,
                                                                     int T, float scale,
-                                                                    float* run_sq) {
+                                                                    int tpr_log2, float* run_sq) {
   __shared__ int list[kShortSample];
   __shared__ int wave_cnt[kShortSample / 64];
-  __shared__ float red[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int pos = blockIdx.x, first = pos / T * T;
   const int64_t id = ids[pos];
@@ -490,19 +551,8 @@ __global__ __launch_bounds__(kThreads) void embed_short_norm_kernel(const int64_
     if (tid == 0) run_sq[pos] = 0.0f;
     return;
   }
-  float sq = 0.0f;
-  for (int c = tid * 8; c < d; c += kThreads * 8) {
-    const Cols k(c, d);
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    add_rows(dY, list, 0, all, d, k, [](int) { return 1.0f; }, acc);
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (q >= k.skip) sq = fmaf(scale * acc[q], scale * acc[q], sq);
-  }
-  sq = wave_sum(sq);
-  if (lane == 0) red[wave] = sq;
-  __syncthreads();
-  if (tid == 0) run_sq[pos] = ((red[0] + red[1]) + red[2]) + red[3];
+  const float sq = run_norm(dY, d, list, 0, all, tpr_log2, scale);
+  if (tid == 0) run_sq[pos] = sq;
 }
 
 // norm_sq[i] += the run norms at sample i's positions, in a fixed order.
@@ -690,17 +740,18 @@ int dpg_embed_norms(const int64_t* ids, const void* dY, int64_t B, int64_t T, in
   if (sorted)
     if (const int st = sort_tokens(p, ids, B * T, V, ws, s)) return st;
   float* run_sq = reinterpret_cast<float*>(ws + p.off_run);
+  const int l = row_threads_log2(d);
   auto go = [&](auto zero) {
     typedef decltype(zero) TY;
     if (!sorted) {
       hipLaunchKernelGGL(embed_short_norm_kernel<TY>, dim3(static_cast<unsigned>(B * T)),
                          dim3(kThreads), 0, s, ids, static_cast<const TY*>(dY), V,
-                         static_cast<int>(d), static_cast<int>(T), static_cast<float>(scale), run_sq);
+                         static_cast<int>(d), static_cast<int>(T), static_cast<float>(scale), l, run_sq);
       return;
     }
     hipLaunchKernelGGL(embed_run_norm_kernel<TY>, dim3(static_cast<unsigned>(B * T)),
                        dim3(kThreads), 0, s, static_cast<const TY*>(dY), static_cast<int>(d),
-                       p.sorted(ids, ws), static_cast<int>(T), static_cast<float>(scale), run_sq);
+                       p.sorted(ids, ws), static_cast<int>(T), static_cast<float>(scale), l, run_sq);
   };
   if (dtype == DPG_BF16) go(bf16());
   else go(0.0f);
