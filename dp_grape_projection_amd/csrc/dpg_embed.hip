@@ -13,6 +13,7 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
+#include <type_traits>
 
 #include "dpg.h"
 #include "dpg_device.hpp"
@@ -28,51 +29,77 @@ constexpr int kSortBatch = kSortThreads * kSortItems;
 // vocabularies above 256 times this.
 constexpr int kSortBins = 8192;
 
-// A thread takes eight columns of a row at a time, 16-byte vectors at any
-// element's address (the global loads and stores take them). The last thread of
-// a row whose width is no multiple of eight takes the row's last eight columns,
-// of which the first `skip` are its neighbour's too: both compute the same values
-// for them. Rows narrower than eight are taken element by element.
+// A thread takes eight columns of a row at a time, in two halves of four, in
+// vectors at any element's address (the global loads and stores take them). WIDE:
+// the halves lie side by side. SPLIT: they lie tpr * 4 columns apart, so that the
+// threads of a row write neighbouring 16-byte vectors of floats (the gradient of
+// a 50304 x 2048 fp32 table: 80 us side by side, 70 us apart). Where a half would
+// reach past the row's end, it takes the last columns of the row, of which the
+// first `skip` are another thread's too: both compute the same values for them.
+// NARROW: a row has fewer than eight columns; one thread takes it element by
+// element.
+enum Kind { WIDE, SPLIT, NARROW };
+template <Kind K>
 struct Cols {
-  int at, skip, n;
-  __device__ __forceinline__ Cols(int c, int d)
-      : at(d < 8 ? 0 : min(c, d - 8)), skip(c - at), n(min(d, 8)) {}
-  // (past the row's end, all eight columns are skipped, and loads stay inside)
+  int at[2], skip[2], n;
+  // column c of a row of d; past the end, all columns are skipped, and loads stay
+  // inside
+  __device__ __forceinline__ Cols(int c, int apart, int d) : n(K == NARROW ? d : 8) {
+    if (K == SPLIT) {
+      at[0] = min(c, d - 4), at[1] = min(c + apart, d - 4);
+      skip[0] = min(c - at[0], 4), skip[1] = min(c + apart - at[1], 4);
+    } else if (K == WIDE) {
+      at[0] = min(c, d - 8), at[1] = at[0] + 4;
+      skip[0] = min(c - at[0], 4), skip[1] = max(min(c - at[0] - 4, 4), 0);
+    } else {
+      at[0] = 0, at[1] = 4, skip[0] = skip[1] = c;
+    }
+  }
+  __device__ __forceinline__ bool mine(int q) const { return (q & 3) >= skip[q >> 2] && q < n; }
+  // whether every column is to be written as part of a vector
+  __device__ __forceinline__ bool vector(bool own) const {
+    return K != NARROW && !(own && (skip[0] || skip[1]));
+  }
+  // thread t's first column in a group of tpr * 8
+  __device__ __forceinline__ static int first(int t) { return t * (K == SPLIT ? 4 : 8); }
 };
 typedef f32x4 any_f32x4 __attribute__((aligned(4)));
 typedef u32x4 any_u32x4 __attribute__((aligned(2)));
+typedef uint32_t two_words __attribute__((ext_vector_type(2)));
+typedef two_words any_two_words __attribute__((aligned(2)));
 
 // Eight columns as loaded; expanded where they are used, so that loads do not wait
 // for one another.
 template <typename T> struct Raw8;
 template <> struct Raw8<float> {
-  f32x4 a, b;
-  __device__ __forceinline__ void load(const float* p, const Cols& k) {
-    const float* x = p + k.at;
-    if (k.n == 8) {
-      a = *reinterpret_cast<const any_f32x4*>(x);
-      b = *reinterpret_cast<const any_f32x4*>(x + 4);
+  f32x4 v[2];
+  template <Kind K>
+  __device__ __forceinline__ void load(const float* p, const Cols<K>& k) {
+    if constexpr (K == NARROW) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q >> 2][q & 3] = q < k.n ? p[q] : 0.0f;
     } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        a[q] = q < k.n ? x[q] : 0.0f;
-        b[q] = 4 + q < k.n ? x[4 + q] : 0.0f;
-      }
+      for (int h = 0; h < 2; ++h) v[h] = *reinterpret_cast<const any_f32x4*>(p + k.at[h]);
     }
   }
-  __device__ __forceinline__ float operator[](int q) const { return q < 4 ? a[q & 3] : b[q & 3]; }
+  __device__ __forceinline__ float operator[](int q) const { return v[q >> 2][q & 3]; }
 };
 template <> struct Raw8<bf16> {
   u32x4 a;
-  __device__ __forceinline__ void load(const bf16* p, const Cols& k) {
-    const bf16* x = p + k.at;
-    if (k.n == 8) {
-      a = *reinterpret_cast<const any_u32x4*>(x);
-    } else {
+  template <Kind K>
+  __device__ __forceinline__ void load(const bf16* p, const Cols<K>& k) {
+    if constexpr (K == NARROW) {
       bf16x8 v;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = q < k.n ? x[q] : zero_val<bf16>();
+      for (int q = 0; q < 8; ++q) v[q] = q < k.n ? p[q] : zero_val<bf16>();
       a = __builtin_bit_cast(u32x4, v);
+    } else if constexpr (K == SPLIT) {
+      const two_words x = *reinterpret_cast<const any_two_words*>(p + k.at[0]);
+      const two_words y = *reinterpret_cast<const any_two_words*>(p + k.at[1]);
+      a = u32x4{x[0], x[1], y[0], y[1]};
+    } else {
+      a = *reinterpret_cast<const any_u32x4*>(p + k.at[0]);
     }
   }
   __device__ __forceinline__ float operator[](int q) const {
@@ -80,39 +107,39 @@ template <> struct Raw8<bf16> {
     return __builtin_bit_cast(float, q & 1 ? w & 0xFFFF0000u : w << 16);
   }
 };
-// own: only the columns that are no neighbour's.
-__device__ __forceinline__ void store8(float* p, const Cols& k, const float (&v)[8], bool own) {
-  float* x = p + k.at;
-  if (k.n == 8 && !(own && k.skip)) {
-    f32x4 a, b;
+// own: only the columns that are no other thread's.
+template <Kind K>
+__device__ __forceinline__ void store8(float* p, const Cols<K>& k, const float (&v)[8], bool own) {
+  if (k.vector(own)) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) a[j] = v[j], b[j] = v[4 + j];
-    *reinterpret_cast<any_f32x4*>(x) = a;
-    *reinterpret_cast<any_f32x4*>(x + 4) = b;
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<any_f32x4*>(p + k.at[h]) =
+          f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
   } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      if (q >= k.skip && q < k.n) x[q] = v[q];
+      if (k.mine(q)) p[k.at[q >> 2] + (q & 3)] = v[q];
   }
 }
-__device__ __forceinline__ void store8(bf16* p, const Cols& k, const float (&v)[8], bool own) {
-  bf16* x = p + k.at;
+template <Kind K>
+__device__ __forceinline__ void store8(bf16* p, const Cols<K>& k, const float (&v)[8], bool own) {
+  static_assert(K != SPLIT, "eight bf16 columns are one vector");
   bf16x8 a;
 #pragma unroll
   for (int q = 0; q < 8; ++q) a[q] = from_float<bf16>(v[q]);
-  if (k.n == 8 && !(own && k.skip)) {
-    *reinterpret_cast<any_u32x4*>(x) = __builtin_bit_cast(u32x4, a);
+  if (k.vector(own)) {
+    *reinterpret_cast<any_u32x4*>(p + k.at[0]) = __builtin_bit_cast(u32x4, a);
   } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      if (q >= k.skip && q < k.n) x[q] = a[q];
+      if (k.mine(q)) p[k.at[q >> 2] + (q & 3)] = a[q];
   }
 }
 
 // ----------------------------------------------------------------- lookup --
 
 // 1 << tpr_log2 threads per row.
-template <typename TE, typename TY>
+template <typename TE, typename TY, Kind K>
 __global__ __launch_bounds__(kThreads) void embed_kernel(const int64_t* ids, int64_t n,
                                                          const TE* E, int64_t V, int d,
                                                          float scale, int tpr_log2, TY* Y) {
@@ -124,8 +151,8 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(const int64_t* ids, int
   const bool ok = id >= 0 && id < V;
   const TE* src = E + (ok ? id : 0) * d;
   TY* dst = Y + row * d;
-  for (int c = (threadIdx.x & (tpr - 1)) * 8; c < d; c += tpr * 8) {
-    const Cols k(c, d);
+  for (int c = Cols<K>::first(threadIdx.x & (tpr - 1)); c < d; c += tpr * 8) {
+    const Cols<K> k(c, 0, d);
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (ok) {
       Raw8<TE> x;
@@ -291,9 +318,9 @@ __global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const int64_t*
 
 // acc += sum over j in [j0, j1) of w(order[j]) dY[order[j]], in order, eight
 // rows in flight.
-template <typename TY, class F>
+template <typename TY, Kind K, class F>
 __device__ __forceinline__ void add_rows(const TY* dY, const int* order, int j0, int j1,
-                                         int d, const Cols& k, F weight, float (&acc)[8]) {
+                                         int d, const Cols<K>& k, F weight, float (&acc)[8]) {
   constexpr int U = 8;
   for (int j = j0; j < j1; j += U) {
     int pos[U];
@@ -343,7 +370,7 @@ struct SampleWeight {
 // begins inside the chunk. (No long token lies wholly inside a chunk.) Without
 // this the most frequent token's sum, 459 rows of 7168 in a 1 / rank
 // distribution over 50304 tokens, outlasts all others: 490 us against 90.
-template <typename TY>
+template <typename TY, Kind K>
 __global__ __launch_bounds__(kThreads) void embed_chunk_kernel(const TY* dY, int d, SortedIds o,
                                                                SampleWeight weight, int tpr_log2,
                                                                float* part) {
@@ -358,8 +385,8 @@ __global__ __launch_bounds__(kThreads) void embed_chunk_kernel(const TY* dY, int
   const int slot = blockIdx.y;
   const int b = slot == 0 ? j0 : lb, e = slot == 0 ? min(fe, j1) : j1;
   if (slot == 0 ? fe - fb <= o.chunk : (lb <= j0 || le - lb <= o.chunk)) return;
-  for (int c = (threadIdx.x & (tpr - 1)) * 8; c < d; c += tpr * 8) {
-    const Cols k(c, d);
+  for (int c = Cols<K>::first(threadIdx.x & (tpr - 1)); c < d; c += tpr * 8) {
+    const Cols<K> k(c, 0, d);
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     add_rows(dY, o.order, b, e, d, k, weight, acc);
     store8(part + (static_cast<int64_t>(chunk) * 2 + slot) * d, k, acc, false);
@@ -368,7 +395,7 @@ __global__ __launch_bounds__(kThreads) void embed_chunk_kernel(const TY* dY, int
 
 // 1 << tpr_log2 threads per vocabulary row: its positions are added in order
 // (its chunks' sums, for a long token).
-template <typename TY, typename TE>
+template <typename TY, typename TE, Kind K>
 __global__ __launch_bounds__(kThreads) void embed_grad_kernel(const TY* dY, int64_t V, int d,
                                                               SortedIds o, SampleWeight weight,
                                                               const float* part, int tpr_log2,
@@ -381,8 +408,8 @@ __global__ __launch_bounds__(kThreads) void embed_grad_kernel(const TY* dY, int6
   const int j0 = st[0], j1 = st[1];
   if (accumulate && j0 == j1) return;
   TE* dst = dE + v * d;
-  for (int c = (threadIdx.x & (tpr - 1)) * 8; c < d; c += tpr * 8) {
-    const Cols k(c, d);
+  for (int c = Cols<K>::first(threadIdx.x & (tpr - 1)); c < d; c += tpr * 8) {
+    const Cols<K> k(c, tpr * 4, d);
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (j1 - j0 <= o.chunk) {
       add_rows(dY, o.order, j0, j1, d, k, weight, acc);
@@ -420,7 +447,7 @@ __global__ __launch_bounds__(kThreads) void embed_grad_kernel(const TY* dY, int6
 // over, each group of so many adds a part of a long run, and the parts are added
 // in order. A wave reads 64 entries of the list at once, so that the rows' loads
 // do not wait for their positions.
-template <typename TY>
+template <typename TY, Kind K>
 __device__ __forceinline__ float run_norm(const TY* dY, int d, const int* list, int j0, int j1,
                                           int tpr_log2, float scale) {
   constexpr int U = 8;
@@ -435,7 +462,7 @@ __device__ __forceinline__ float run_norm(const TY* dY, int d, const int* list, 
   float sq = 0.0f;
   for (int c0 = 0; c0 < d; c0 += tpr * 8) {
     const int c = c0 + t * 8;
-    const Cols k(c, d);
+    const Cols<K> k(c, 0, d);
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int j = b; j < e; j += 64) {
       const int mine = list[min(j + lane, e - 1)], m = min(64, e - j);
@@ -468,7 +495,7 @@ __device__ __forceinline__ float run_norm(const TY* dY, int d, const int* list, 
     if (group == 0) {
 #pragma unroll
       for (int q = 0; q < 8; ++q)
-        if (q >= k.skip) sq = fmaf(scale * acc[q], scale * acc[q], sq);
+        if (k.mine(q)) sq = fmaf(scale * acc[q], scale * acc[q], sq);
     }
   }
   sq = wave_sum(sq);
@@ -480,7 +507,7 @@ __device__ __forceinline__ float run_norm(const TY* dY, int d, const int* list, 
 // One block per entry of `order`: the first entry of a (token,
 // sample) run adds the run's rows and writes the squared norm of the sum at
 // its position, the others write zero.
-template <typename TY>
+template <typename TY, Kind K>
 __global__ __launch_bounds__(kThreads) void embed_run_norm_kernel(const TY* dY, int d, SortedIds o,
                                                                   int T, float scale,
                                                                   int tpr_log2, float* run_sq) {
@@ -509,7 +536,7 @@ __global__ __launch_bounds__(kThreads) void embed_run_norm_kernel(const TY* dY, 
     }
     e += 64;
   }
-  const float sq = run_norm(dY, d, o.order, j, e, tpr_log2, scale);
+  const float sq = run_norm<TY, K>(dY, d, o.order, j, e, tpr_log2, scale);
   if (threadIdx.x == 0) run_sq[pos] = sq;
 }
 
@@ -517,7 +544,7 @@ __global__ __launch_bounds__(kThreads) void embed_run_norm_kernel(const TY* dY, 
 // its id with its sample's other ids (T * 8 bytes of L2 reads a block); the
 // first position of a run lists the others in LDS, in order.
 constexpr int kShortSample = 1024;
-template <typename TY>
+template <typename TY, Kind K>
 __global__ __launch_bounds__(kThreads) void embed_short_norm_kernel(const int64_t* ids,
                                                                     const TY* dY, int64_t V, int d,
                                                                     int T, float scale,
@@ -551,7 +578,7 @@ __global__ __launch_bounds__(kThreads) void embed_short_norm_kernel(const int64_
     if (tid == 0) run_sq[pos] = 0.0f;
     return;
   }
-  const float sq = run_norm(dY, d, list, 0, all, tpr_log2, scale);
+  const float sq = run_norm<TY, K>(dY, d, list, 0, all, tpr_log2, scale);
   if (tid == 0) run_sq[pos] = sq;
 }
 
@@ -562,9 +589,17 @@ __global__ __launch_bounds__(kThreads) void embed_norm_sum_kernel(const int64_t*
   __shared__ float red[4];
   const int64_t base = static_cast<int64_t>(blockIdx.x) * T;
   float t = 0.0f;
-  for (int k = threadIdx.x; k < T; k += kThreads) {
-    const int64_t id = ids[base + k];
-    if (id >= 0 && id < V) t += run_sq[base + k];
+  for (int k0 = threadIdx.x; k0 < T; k0 += 4 * kThreads) {  // (four loads in flight)
+    int64_t id[4];
+    float x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t at = base + min(k0 + u * kThreads, T - 1);
+      id[u] = ids[at], x[u] = run_sq[at];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (k0 + u * kThreads < T && id[u] >= 0 && id[u] < V) t += x[u];
   }
   t = wave_sum(t);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = t;
@@ -584,6 +619,13 @@ int check_launch(const char* what) {
 
 bool valid_dtype(int32_t t) { return t == DPG_FP32 || t == DPG_BF16; }
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+// fn with how a thread takes a row of d columns.
+template <class F>
+void with_kind(int64_t d, F fn) {
+  if (d < 8) fn(std::integral_constant<Kind, NARROW>{});
+  else fn(std::integral_constant<Kind, WIDE>{});
+}
 
 // log2 of the threads that share a row of d columns: one per unit of eight
 // columns, at most a block.
@@ -662,10 +704,12 @@ template <typename TE, typename TY>
 void launch_embed(const int64_t* ids, int64_t n, const void* E, int64_t V, int64_t d, double scale,
                   void* Y, hipStream_t s) {
   const int l = row_threads_log2(d);
-  hipLaunchKernelGGL((embed_kernel<TE, TY>),
-                     dim3(static_cast<unsigned>(ceil_div(n, kThreads >> l))), dim3(kThreads), 0, s,
-                     ids, n, static_cast<const TE*>(E), V, static_cast<int>(d),
-                     static_cast<float>(scale), l, static_cast<TY*>(Y));
+  with_kind(d, [&](auto k) {
+    hipLaunchKernelGGL((embed_kernel<TE, TY, decltype(k)::value>),
+                       dim3(static_cast<unsigned>(ceil_div(n, kThreads >> l))), dim3(kThreads), 0, s,
+                       ids, n, static_cast<const TE*>(E), V, static_cast<int>(d),
+                       static_cast<float>(scale), l, static_cast<TY*>(Y));
+  });
 }
 
 template <typename TY, typename TE>
@@ -678,13 +722,16 @@ void launch_embed_grad(const SortPlan& p, const int64_t* ids, const void* dY, in
   const SampleWeight weight{sample_scales, static_cast<float>(scale), static_cast<int>(T)};
   float* part = reinterpret_cast<float*>(ws + p.off_part);
   const TY* dy = static_cast<const TY*>(dY);
-  if (n > p.chunk)
-    hipLaunchKernelGGL(embed_chunk_kernel<TY>,
-                       dim3(static_cast<unsigned>(ceil_div(p.chunks, kThreads >> l)), 2), b, 0, s, dy,
-                       static_cast<int>(d), o, weight, l, part);
-  hipLaunchKernelGGL((embed_grad_kernel<TY, TE>),
-                     dim3(static_cast<unsigned>(ceil_div(V, kThreads >> l))), b, 0, s, dy, V,
-                     static_cast<int>(d), o, weight, part, l, accumulate, static_cast<TE*>(dE));
+  with_kind(d, [&](auto k) {
+    constexpr Kind K = decltype(k)::value;
+    if (n > p.chunk)
+      hipLaunchKernelGGL((embed_chunk_kernel<TY, K>),
+                         dim3(static_cast<unsigned>(ceil_div(p.chunks, kThreads >> l)), 2), b, 0, s,
+                         dy, static_cast<int>(d), o, weight, l, part);
+    hipLaunchKernelGGL((embed_grad_kernel<TY, TE, K == WIDE && sizeof(TE) == 4 ? SPLIT : K>),
+                       dim3(static_cast<unsigned>(ceil_div(V, kThreads >> l))), b, 0, s, dy, V,
+                       static_cast<int>(d), o, weight, part, l, accumulate, static_cast<TE*>(dE));
+  });
 }
 
 }  // namespace
@@ -743,15 +790,18 @@ int dpg_embed_norms(const int64_t* ids, const void* dY, int64_t B, int64_t T, in
   const int l = row_threads_log2(d);
   auto go = [&](auto zero) {
     typedef decltype(zero) TY;
-    if (!sorted) {
-      hipLaunchKernelGGL(embed_short_norm_kernel<TY>, dim3(static_cast<unsigned>(B * T)),
-                         dim3(kThreads), 0, s, ids, static_cast<const TY*>(dY), V,
-                         static_cast<int>(d), static_cast<int>(T), static_cast<float>(scale), l, run_sq);
-      return;
-    }
-    hipLaunchKernelGGL(embed_run_norm_kernel<TY>, dim3(static_cast<unsigned>(B * T)),
-                       dim3(kThreads), 0, s, static_cast<const TY*>(dY), static_cast<int>(d),
-                       p.sorted(ids, ws), static_cast<int>(T), static_cast<float>(scale), l, run_sq);
+    with_kind(d, [&](auto k) {
+      constexpr Kind K = decltype(k)::value;
+      const dim3 grid(static_cast<unsigned>(B * T)), b(kThreads);
+      if (sorted)
+        hipLaunchKernelGGL((embed_run_norm_kernel<TY, K>), grid, b, 0, s,
+                           static_cast<const TY*>(dY), static_cast<int>(d), p.sorted(ids, ws),
+                           static_cast<int>(T), static_cast<float>(scale), l, run_sq);
+      else
+        hipLaunchKernelGGL((embed_short_norm_kernel<TY, K>), grid, b, 0, s, ids,
+                           static_cast<const TY*>(dY), V, static_cast<int>(d), static_cast<int>(T),
+                           static_cast<float>(scale), l, run_sq);
+    });
   };
   if (dtype == DPG_BF16) go(bf16());
   else go(0.0f);
