@@ -727,6 +727,9 @@ __device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t 
 __device__ __forceinline__ bf16x8 lds_read_b128(const char* __restrict__ p) {
   return *reinterpret_cast<const bf16x8*>(p);
 }
+__device__ __forceinline__ float lds_read_f32(const char* __restrict__ p) {
+  return *reinterpret_cast<const float*>(p);
+}
 __device__ __forceinline__ float lds_read_f32(const float* __restrict__ p) { return *p; }
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));

@@ -63,6 +63,8 @@ template <> struct Combos<3> {
   __device__ __forceinline__ static int a(int c) { return (0x001102 >> (4 * c)) & 15; }
   __device__ __forceinline__ static int b(int c) { return (0x010120 >> (4 * c)) & 15; }
 };
+// Instead of a count of parts: fp32 operands of which the table is read as it is.
+constexpr int kRaw = 0;
 // Parts of the logits' operands where the others have PARTS.
 template <int PARTS> constexpr int kLogitParts = PARTS == 3 ? 2 : 1;
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -323,8 +325,10 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
   auto pack = [&](const T* src, int i, int d) {  // packed row i
     const int64_t at = static_cast<int64_t>(i) * a.ldx, stride = static_cast<int64_t>(a.np) * a.ldx;
     if constexpr (kParts<T> == 3) {
-      const float f = pack_row_half(src, a.Xh + at, d, a.ldx, stride, lane);
-      if (lane == 0) a.sx[i] = f;
+      if (a.Xh) {
+        const float f = pack_row_half(src, a.Xh + at, d, a.ldx, stride, lane);
+        if (lane == 0) a.sx[i] = f;
+      }
     }
     if (a.Xp) pack_row(src, a.Xp + at, d, a.ldx, stride, lane);
   };
@@ -710,6 +714,176 @@ __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& o
   for (; s < n_steps; ++s) step(std::false_type{}, s + 1 < n_steps);
 }
 
+// acc = A B^T with A the table in fp32, as the caller has it, in 128 x 128 tiles.
+// With few rows the table's bytes are the time, and packing it first would read
+// and write them two to three times more (30 rows x 1024 against 111117 columns:
+// loss 374 us packed, 150 us as it is). A K step of 64 stays in fp32 in LDS and is
+// split into three bf16 parts in registers; the six products follow per K step, the
+// small ones first. A K step is 32 KiB of A and 48 KiB of B's parts, and one is
+// copied while the one before it is used.
+// A is as Operand says, in floats: rows (M) by K, or with KMAJOR rows of K by
+// columns (M), both with 16-byte aligned rows. n_rows: B's rows that count.
+struct RawOperand {
+  const float* base;
+  int64_t ld;
+  int rows, cols;
+};
+constexpr int kRawStage = 5 * SmallTile::kTileBytes;
+
+template <bool KMAJOR>
+__device__ __forceinline__ void raw_product(const RawOperand& oa, const Operand& ob, int n_k,
+                                            int n_rows, char* smem, SmallTile::Acc& acc) {
+  typedef SmallTile G;
+  typedef Combos<3> C;
+  const int tid = threadIdx.x, lane = tid & 63, q16 = lane & 15, kq = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave % G::kWavesM, wn = wave / G::kWavesM;
+  // rows: two copies of 32 floats a row for a K step. The copier counts in pairs of
+  // bytes, of which a float is two.
+  Copier<G, false> ca, cb[3];
+  ca.init({reinterpret_cast<const bf16*>(oa.base), oa.ld * 2, 0, oa.rows, oa.cols * 2}, lane, wave);
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    Operand o = ob;
+    o.base += q * ob.part_stride;
+    cb[q].init(o, lane, wave);
+  }
+  // k-major: a copy takes two rows of K of 512 bytes; 16-byte chunk c of row k lies in
+  // slot c ^ 4 (k / 8 mod 4), so that the four rows that a read touches lie in
+  // different banks
+  const char* at = reinterpret_cast<const char*>(oa.base);
+  const uint32_t ldb = static_cast<uint32_t>(oa.ld) * 4u;
+  int left = oa.rows;  // rows of K from the step to copy on
+  // rows of B that the waves read: whole blocks, zero past n_rows
+  const int read_rows = n_rows <= 16 ? 16 : n_rows <= 32 ? 32 : (n_rows + 63) / 64 * 64;
+  const uint32_t last = static_cast<uint32_t>(oa.cols) / 4u - 1u;
+  auto issue = [&](char* stage) {
+    if constexpr (KMAJOR) {
+      const __amdgpu_buffer_rsrc_t rs = tile_rsrc(at);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int g = q * G::kWaves + wave, k = 2 * g + (lane >> 5);
+        const uint32_t c = static_cast<uint32_t>((lane & 31) ^ (4 * ((k >> 3) & 3)));
+        copy_to_lds(rs, static_cast<uint32_t>(min(k, left - 1)) * ldb + min(c, last) * 16u, 0,
+                    stage + g * 1024);
+      }
+      at += static_cast<uint64_t>(ldb) * kStepK;
+      left -= kStepK;
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ca.issue(stage + h * G::kTileBytes, wave, 0, G::kCopies);
+        ca.next_step();
+      }
+    }
+    // (a wave's copies of B are 32 rows apart, eight rows each)
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+#pragma unroll
+      for (int j = 0; j < G::kCopies; ++j)
+        if ((j * G::kWaves + wave) * 8 < read_rows)
+          cb[q].issue(stage + (2 + q) * G::kTileBytes, wave, j, j + 1);
+      cb[q].next_step();
+    }
+  };
+  auto read_a = [&](const char* stage, int kk, int m, bf16x8 (&f)[3]) {
+    float x[8];
+    const int r = G::kWaveM * wm + 16 * m + q16;
+    if constexpr (KMAJOR) {
+      const char* p = stage + ((r >> 2) ^ (4 * kq)) * 16 + (r & 3) * 4;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = lds_read_f32(p + (32 * kk + 8 * kq + i) * 512);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 v = __builtin_bit_cast(
+            f32x4, lds_read_b128(stage + kk * G::kTileBytes + r * 128 +
+                                 ((2 * kq + h) ^ ((r >> 1) & 7)) * 16));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[4 * h + i] = v[i];
+      }
+    }
+    // the first part is truncated, so that no finite value becomes an infinity,
+    // the others are rounded: exact as well, and without a test
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float h = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x[i]) & 0xFFFF0000u);
+      f[0][i] = static_cast<bf16>(h);
+      x[i] -= h;
+      f[1][i] = static_cast<bf16>(x[i]);
+      f[2][i] = static_cast<bf16>(x[i] - static_cast<float>(f[1][i]));
+    }
+  };
+#pragma unroll
+  for (int m = 0; m < G::kMB; ++m)
+#pragma unroll
+    for (int n = 0; n < G::kNB; ++n) acc.v[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (n_k <= 0) return;
+  // NB: blocks of 16 of B's rows that count for this wave. HALF: there are at most 64
+  // rows, which all waves take, those of each wn one half of the K step.
+  auto run = [&](auto nb, auto half) {
+    constexpr int NB = decltype(nb)::value;
+    constexpr bool HALF = decltype(half)::value;
+    issue(smem);
+    for (int s = 0; s < n_k; ++s) {
+      const char* stage = smem + (s & 1) * kRawStage;
+      wait_lgkm0();  // this wave's reads of step s - 1 are complete
+      wait_vm_n<0>();
+      lds_barrier();
+      if (s + 1 < n_k) issue(smem + ((s + 1) & 1) * kRawStage);
+      if constexpr (NB > 0) {
+#pragma unroll
+        for (int kk0 = 0; kk0 < (HALF ? 1 : 2); ++kk0) {
+          const int kk = HALF ? wn : kk0;
+          bf16x8 fb[3][NB];
+#pragma unroll
+          for (int q = 0; q < 3; ++q)
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+              fb[q][n] = tile_frag<G, false>(stage + (2 + q) * G::kTileBytes, kk,
+                                             (HALF ? 0 : G::kWaveN * wn) + 16 * n, lane);
+#pragma unroll
+          for (int m = 0; m < G::kMB; ++m) {
+            bf16x8 fa[3];
+            read_a(stage, kk, m, fa);
+#pragma unroll
+            for (int c = 0; c < C::n; ++c)
+#pragma unroll
+              for (int n = 0; n < NB; ++n)
+                acc.v[m][n] = mfma<3>(fa[C::a(c)], fb[C::b(c)][n], acc.v[m][n]);
+          }
+        }
+      }
+    }
+  };
+  if (n_rows > G::kWaveN) {
+    if (wn == 0 || n_rows > G::kWaveN + 32) run(std::integral_constant<int, 4>{}, std::false_type{});
+    else run(std::integral_constant<int, 2>{}, std::false_type{});
+    return;
+  }
+  if (n_rows <= 16) run(std::integral_constant<int, 1>{}, std::true_type{});
+  else if (n_rows <= 32) run(std::integral_constant<int, 2>{}, std::true_type{});
+  else run(std::integral_constant<int, 4>{}, std::true_type{});
+  // the second half's sums join the first's
+  f32x4* sums = reinterpret_cast<f32x4*>(smem) + wm * (G::kMB * G::kNB * 64) + lane;
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < G::kMB; ++m)
+#pragma unroll
+    for (int n = 0; n < G::kNB; ++n)
+      if (wn == 1) {
+        sums[(m * G::kNB + n) * 64] = acc.v[m][n];
+        acc.v[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+  __syncthreads();
+  if (wn == 0) {
+#pragma unroll
+    for (int m = 0; m < G::kMB; ++m)
+#pragma unroll
+      for (int n = 0; n < G::kNB; ++n) acc.v[m][n] += sums[(m * G::kNB + n) * 64];
+  }
+}
+
 // The tile (m, n) of a block among mt x nt: each XCD takes a
 // contiguous run of them, in bands of eight m, so that the blocks an XCD runs
 // together share eight A and four B tiles in its L2. False past the last.
@@ -791,6 +965,14 @@ template <class G, int PARTS>
 __device__ __forceinline__ void logits_tile(const VocabArgs& a, int c0, int r0, char* smem,
                                             typename G::Acc& acc) {
   constexpr int LP = kLogitParts<PARTS>;
+  if constexpr (PARTS == kRaw) {
+    const RawOperand e = {static_cast<const float*>(a.E) + (static_cast<int64_t>(a.v0) + c0) * a.d,
+                          a.d, a.vn - c0, a.d};
+    raw_product<false>(e, rows_operand(a.Xp + static_cast<int64_t>(r0) * a.ldx, a.ldx,
+                                       static_cast<int64_t>(a.np) * a.ldx, G::kTile, a.ldx),
+                       a.ldx / kStepK, a.count[0] - r0, smem, acc);
+    return;
+  }
   const bf16* x = LP == 2 ? reinterpret_cast<const bf16*>(a.Xh) : a.Xp;
   const Operand rows = rows_operand(x + static_cast<int64_t>(r0) * a.ldx, a.ldx,
                                     static_cast<int64_t>(a.np) * a.ldx, G::kTile, a.ldx);
@@ -818,6 +1000,10 @@ __device__ __forceinline__ float row_scale(const VocabArgs& a, int r) {
   return PARTS == 3 ? a.sx[r] : 1.0f;
 }
 
+// LDS of a logits kernel, and its blocks on a CU.
+template <class G, int PARTS> constexpr int kLdsOf = PARTS == kRaw ? 2 * kRawStage : G::kLds;
+template <class G, int PARTS> constexpr int kBlocksOf = PARTS == kRaw ? 1 : G::kBlocks;
+
 // fn(std::true_type) where a tile reaches past the piece's last column,
 // fn(std::false_type) for the others, whose columns need no test.
 template <class F>
@@ -830,8 +1016,9 @@ __device__ __forceinline__ void with_edge(bool edge, F fn) {
 // logits of the targets there. Works in base 2: z log2(e). What a row needs is
 // loaded before the product, so that its latency hides behind it.
 template <class G, int PARTS, bool TEACHER>
-__global__ __launch_bounds__(G::kThreads, G::kBlocks) void stats_kernel(const VocabArgs a, int tile0) {
-  __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
+__global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void stats_kernel(const VocabArgs a,
+                                                                               int tile0) {
+  __shared__ __attribute__((aligned(1024))) char smem[kLdsOf<G, PARTS>];
   int mt, nt;
   if (!tile_of_block(blockIdx.x, (a.vn + G::kTile - 1) / G::kTile, row_tiles<G>(a), mt, nt)) return;
   const int c0 = mt * G::kTile, r0 = nt * G::kTile;
@@ -973,8 +1160,9 @@ __device__ __forceinline__ void write_tile(char* smem, bf16* dst, int64_t ld, in
 // weight is subtracted: D enters two products whose other operand is bf16;
 // with fp32 D is kept in three parts.
 template <class G, int PARTS, bool TEACHER>
-__global__ __launch_bounds__(G::kThreads, G::kBlocks) void grad_logits_kernel(const VocabArgs a) {
-  __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
+__global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void grad_logits_kernel(
+    const VocabArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[kLdsOf<G, PARTS>];
   int mt, nt;
   if (!tile_of_block(blockIdx.x, (a.vn + G::kTile - 1) / G::kTile, row_tiles<G>(a), mt, nt)) return;
   const int c0 = mt * G::kTile, r0 = nt * G::kTile;
@@ -1090,11 +1278,16 @@ __device__ __forceinline__ void dx_tile(const VocabArgs& a, int block, char* sme
   const int steps = (a.vn + kStepK - 1) / kStepK, per = (steps + a.splits - 1) / a.splits;
   const int k0 = min(steps, split * per), k1 = min(steps, k0 + per);
   typename G::Acc acc;
-  tile_product<G, PARTS, true, false>(
-      table_operand(a, true, k0 * kStepK, c0),
-      rows_operand(a.D + static_cast<int64_t>(r0) * a.ldd + k0 * kStepK, a.ldd,
-                   static_cast<int64_t>(a.np) * a.ldd, G::kTile, a.ldd - k0 * kStepK),
-      k1 - k0, smem, acc);
+  const Operand d = rows_operand(a.D + static_cast<int64_t>(r0) * a.ldd + k0 * kStepK, a.ldd,
+                                 static_cast<int64_t>(a.np) * a.ldd, G::kTile, a.ldd - k0 * kStepK);
+  if constexpr (PARTS == kRaw) {
+    const int64_t row = static_cast<int64_t>(a.v0) + k0 * kStepK;
+    const RawOperand e = {static_cast<const float*>(a.E) + row * a.d + c0, a.d, a.vn - k0 * kStepK,
+                          a.d - c0};
+    raw_product<true>(e, d, k1 - k0, a.count[0] - r0, smem, acc);
+  } else {
+    tile_product<G, PARTS, true, false>(table_operand(a, true, k0 * kStepK, c0), d, k1 - k0, smem, acc);
+  }
   add_tile<G>(a.dXacc + (static_cast<int64_t>(split) * a.np + r0) * a.ldx + c0, a.ldx, a.ldx - c0,
               a.v0 != 0, acc);
 }
@@ -1203,6 +1396,12 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void products_kernel(const
   const int block = blockIdx.x;
   if (DX && (!DE || block < dx_blocks)) dx_tile<G, kParts<T>>(a, block, smem);
   else if (DE) de_tile<G, T>(a, dE, block - dx_blocks, smem);
+}
+
+// dX's tiles with the table as the caller has it.
+__global__ __launch_bounds__(SmallTile::kThreads, 1) void raw_dx_kernel(const VocabArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[2 * kRawStage];
+  dx_tile<SmallTile, kRaw>(a, blockIdx.x, smem);
 }
 
 // Row n of a gradient: its sums in `splits` arrays (stride floats apart) of rows
@@ -1341,6 +1540,7 @@ struct VocabPlan {
   int32_t splits = 1, splits_e = 1;
   bool big_x = false, big_e = false;  // dX's and dE's tiles
   bool packed = false;  // the table is packed whatever its alignment
+  bool raw = false;     // but fp32 rows of whole 16 bytes are read as they are
   size_t off_flag, off_count, off_row, off_inv, off_target, off_g, off_lse2, off_q, off_ent, off_zt, off_qu, off_nu, off_bits,
       off_before, off_Xp, off_Ep, off_Xh, off_Eh, off_sx, off_se, off_part, off_D, off_dX, off_dE, total;
 };
@@ -1353,6 +1553,7 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   p.ldx = round_up(d, kStepK);
   p.np = round_up(N, kPad);
   p.packed = parts > 1 || d % 8 != 0;
+  p.raw = parts > 1 && N <= SmallTile::kTile && d % 4 == 0;
   // one piece of the vocabulary: its D, its teacher ids' bits, and its packed
   // table
   const int64_t row_bytes = p.ldx * 2 * parts;
@@ -1368,6 +1569,12 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
     const Split x = choose_split(N, p.ldx, ceil_div(piece_rows, kStepK), combos, true);
     const Split e = choose_split(piece_rows, p.ldx, ceil_div(N, kStepK), combos, false);
     p.big_x = x.big, p.splits = x.splits;
+    if (p.raw) {  // memory bound: one block a CU, each with at least two K steps
+      const int64_t tiles = ceil_div(d, SmallTile::kTile);
+      p.big_x = false;
+      p.splits = static_cast<int32_t>(std::max<int64_t>(
+          1, std::min(256 / tiles, ceil_div(piece_rows, kStepK) / 2)));
+    }
     p.big_e = e.big, p.splits_e = e.splits;
   }
   size_t off = 0;
@@ -1391,7 +1598,7 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   p.off_bits = take(distill ? N * (p.piece / 64) * 8 : 0);
   p.off_before = take(distill ? N * (p.piece / 64) * 2 : 0);
   // (the loss of fp32 operands needs only their fp16 parts)
-  const bool half = parts > 1, whole = !half || grad;
+  const bool half = parts > 1, whole = !half || grad || p.raw;
   p.off_Xp = take(whole ? parts * p.np * p.ldx * 2 : 0);
   p.off_Ep = take(whole ? parts * p.packed_piece * p.ldx * 2 : 0);
   p.off_Xh = take(half ? 2 * p.np * p.ldx * 2 : 0);
@@ -1409,7 +1616,7 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
 }
 
 // rows, table: the gradient needs X's, E's bf16 parts.
-VocabArgs make_args(const VocabCall& c, const VocabPlan& p, char* ws, bool rows, bool table) {
+VocabArgs make_args(const VocabCall& c, VocabPlan& p, char* ws, bool rows, bool table) {
   VocabArgs a{};
   a.X = c.X;
   a.E = c.E;
@@ -1438,9 +1645,11 @@ VocabArgs make_args(const VocabCall& c, const VocabPlan& p, char* ws, bool rows,
   a.nu = reinterpret_cast<int32_t*>(ws + p.off_nu);
   a.bits = reinterpret_cast<uint64_t*>(ws + p.off_bits);
   a.before = reinterpret_cast<uint16_t*>(ws + p.off_before);
-  const bool half = c.dtype == DPG_FP32, pack = p.packed || !aligned(c.E, 16);
+  const bool fp32 = c.dtype == DPG_FP32, pack = p.packed || !aligned(c.E, 16);
+  p.raw = p.raw && aligned(c.E, 16);
+  const bool half = fp32 && !p.raw;
   a.Xp = !half || rows ? reinterpret_cast<bf16*>(ws + p.off_Xp) : nullptr;
-  a.Ep = pack && (!half || table) ? reinterpret_cast<bf16*>(ws + p.off_Ep) : nullptr;
+  a.Ep = pack && !p.raw && (!half || table) ? reinterpret_cast<bf16*>(ws + p.off_Ep) : nullptr;
   if (half) {
     a.Xh = reinterpret_cast<_Float16*>(ws + p.off_Xh);
     a.Eh = reinterpret_cast<_Float16*>(ws + p.off_Eh);
@@ -1486,15 +1695,28 @@ void for_pieces(VocabArgs& a, hipStream_t s, F fn) {
   }
 }
 
+// fn with the parts of the logits kernels' operands, kRaw where the table is read as
+// it is (with small tiles).
+template <typename T, class G, class F>
+void with_raw(bool raw, F fn) {
+  if constexpr (kParts<T> == 3 && G::kTile == SmallTile::kTile) {
+    if (raw) return fn(std::integral_constant<int, kRaw>{});
+  }
+  fn(std::integral_constant<int, kParts<T>>{});
+}
+
 template <typename T>
-int run_loss(VocabArgs a, hipStream_t s) {
+int run_loss(VocabArgs a, const VocabPlan& p, hipStream_t s) {
   with_tile(ceil_div(std::min(a.ldd, a.V), BigTile::kTile) * (a.np / BigTile::kTile), a.N, [&](auto g) {
     typedef decltype(g) G;
     for_pieces<T>(a, s, [&] {
       const dim3 grid = tile_grid(ceil_div(a.vn, G::kTile), a.np / G::kTile), b(G::kThreads);
       const int tile0 = a.v0 / G::kTile;
-      if (a.t) hipLaunchKernelGGL((stats_kernel<G, kParts<T>, true>), grid, b, 0, s, a, tile0);
-      else hipLaunchKernelGGL((stats_kernel<G, kParts<T>, false>), grid, b, 0, s, a, tile0);
+      with_raw<T, G>(p.raw, [&](auto parts) {
+        constexpr int P = decltype(parts)::value;
+        if (a.t) hipLaunchKernelGGL((stats_kernel<G, P, true>), grid, b, 0, s, a, tile0);
+        else hipLaunchKernelGGL((stats_kernel<G, P, false>), grid, b, 0, s, a, tile0);
+      });
     });
     hipLaunchKernelGGL(lse_kernel, dim3(blocks_of(a.N, 4)), dim3(kThreads), 0, s, a,
                        static_cast<int>(ceil_div(a.V, G::kTile)));
@@ -1524,8 +1746,11 @@ int run_grad(VocabArgs a, const VocabPlan& p, void* dX, void* dE, hipStream_t s)
     with_tile(ceil_div(a.vn, BigTile::kTile) * (a.np / BigTile::kTile), a.N, [&](auto g) {
       typedef decltype(g) G;
       const dim3 grid = tile_grid(ceil_div(a.vn, G::kTile), a.np / G::kTile), b(G::kThreads);
-      if (a.t) hipLaunchKernelGGL((grad_logits_kernel<G, kParts<T>, true>), grid, b, 0, s, a);
-      else hipLaunchKernelGGL((grad_logits_kernel<G, kParts<T>, false>), grid, b, 0, s, a);
+      with_raw<T, G>(p.raw, [&](auto parts) {
+        constexpr int P = decltype(parts)::value;
+        if (a.t) hipLaunchKernelGGL((grad_logits_kernel<G, P, true>), grid, b, 0, s, a);
+        else hipLaunchKernelGGL((grad_logits_kernel<G, P, false>), grid, b, 0, s, a);
+      });
     });
     T* de = static_cast<T*>(dE);
     auto blocks_x = [&](int64_t tile) {
@@ -1534,12 +1759,15 @@ int run_grad(VocabArgs a, const VocabPlan& p, void* dX, void* dE, hipStream_t s)
     auto blocks_e = [&](int64_t tile) {
       return tile_grid(ceil_div(a.vn, tile), ceil_div(a.ldx, tile) * a.splits_e).x;
     };
-    if (dX && dE && !p.big_x && !p.big_e) {
+    if (dX && dE && !p.raw && !p.big_x && !p.big_e) {
       const unsigned nx = blocks_x(SmallTile::kTile), ne = blocks_e(SmallTile::kTile);
       hipLaunchKernelGGL((products_kernel<SmallTile, T, true, true>), dim3(nx + ne),
                          dim3(SmallTile::kThreads), 0, s, a, static_cast<int>(nx), de);
     } else {
-      if (dX)
+      if (dX && p.raw)
+        hipLaunchKernelGGL(raw_dx_kernel, dim3(blocks_x(SmallTile::kTile)),
+                           dim3(SmallTile::kThreads), 0, s, a);
+      else if (dX)
         with_tile(p.big_x, [&](auto g) {
           typedef decltype(g) G;
           hipLaunchKernelGGL((products_kernel<G, T, true, false>), dim3(blocks_x(G::kTile)),
@@ -1576,13 +1804,13 @@ int loss_impl(const VocabCall& c, bool distill, float* loss, float* lse, void* w
   record_error(DPG_OK, "");
   if (const int st = check_call(c, distill)) return st;
   if (!loss || !lse) return fail(DPG_ERR_INVALID_ARG, "loss and lse must not be NULL");
-  const VocabPlan p = plan_vocab(c.N, c.d, c.V, c.k, c.dtype, distill, false);
+  VocabPlan p = plan_vocab(c.N, c.d, c.V, c.k, c.dtype, distill, false);
   if (const int st = check_ws(workspace, workspace_bytes, p.total)) return st;
   VocabArgs a = make_args(c, p, static_cast<char*>(workspace), false, false);
   a.loss = loss;
   a.lse = lse;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return c.dtype == DPG_BF16 ? run_loss<bf16>(a, s) : run_loss<float>(a, s);
+  return c.dtype == DPG_BF16 ? run_loss<bf16>(a, p, s) : run_loss<float>(a, p, s);
 }
 
 int grad_impl(const VocabCall& c, bool distill, const float* lse, const float* dloss, void* dX,
@@ -1591,7 +1819,7 @@ int grad_impl(const VocabCall& c, bool distill, const float* lse, const float* d
   if (const int st = check_call(c, distill)) return st;
   if (!lse || !dloss) return fail(DPG_ERR_INVALID_ARG, "lse and dloss must not be NULL");
   if (!dX && !dE) return fail(DPG_ERR_INVALID_ARG, "dX and dE are both NULL");
-  const VocabPlan p = plan_vocab(c.N, c.d, c.V, c.k, c.dtype, distill, true);
+  VocabPlan p = plan_vocab(c.N, c.d, c.V, c.k, c.dtype, distill, true);
   if (const int st = check_ws(workspace, workspace_bytes, p.total)) return st;
   VocabArgs a = make_args(c, p, static_cast<char*>(workspace), dE != nullptr, dX != nullptr);
   a.lse = const_cast<float*>(lse);

@@ -538,3 +538,59 @@ def test_gradients_of_many_rows_and_few_columns(N, d, V, act):
     assert rel_err(_host(dE), want_dE) <= TOL[act]
     again = dpg.dpg_vocab_loss_grad(x, e, y, lse, _dev(g))
     assert torch.equal(again[0], dX) and torch.equal(again[1], dE)
+
+
+@pytest.mark.parametrize("N,d,V", [(128, 132, 700), (97, 260, 515), (16, 20, 130), (33, 4, 129),
+                                   (64, 1000, 257), (7, 512, 5000)])
+def test_few_fp32_rows(N, d, V):
+    """At most 128 fp32 rows, whose table is read as it is where its rows are whole
+    16 bytes, and packed otherwise (one element off): both against the reference."""
+    import dp_grape_projection_amd as dpg
+    print(f"[tokens] few fp32 rows N={N} d={d} V={V}", flush=True)
+    X, E, ids, t, g = _loss_case(N, d, V, 6, "fp32", 7)
+    y = ids[:, 0]
+    q1 = ((y >= 0) & (y < V)).astype(np.float64)
+    qk = ot.teacher_weights(ids, t, V, 2.0)
+    _, _, dX1, dE1 = ot.target_loss(X, E, y, q1, -0.9, 1.0, g)
+    _, _, dXk, dEk = ot.target_loss(X, E, ids, qk, 1.1, 2.0, g)
+    Xp = _poison(X, ids, V)
+    for offset in (0, 1):
+        x, e = _dev(Xp, "fp32"), _dev(E, "fp32", offset)
+        loss, lse = dpg.dpg_vocab_loss(x, e, _dev(y), scale=-0.9)
+        on = np.flatnonzero(q1 > 0)
+        _check_loss(X[on], E, y[on], q1[on], loss[on], lse[on], -0.9, 1.0)
+        dX, dE = dpg.dpg_vocab_loss_grad(x, e, _dev(y), lse, _dev(g), scale=-0.9)
+        assert np.isfinite(_host(dX)).all() and np.isfinite(_host(dE)).all()
+        assert rel_err(_host(dX), dX1) <= TOL["fp32"]
+        assert rel_err(_host(dE), dE1) <= TOL["fp32"]
+        loss, lse = dpg.dpg_distill_loss(x, e, _dev(ids), _dev(t), temperature=2.0, scale=1.1)
+        _check_loss(X, E, ids, qk, loss, lse, 1.1, 2.0)
+        dX, dE = dpg.dpg_distill_loss_grad(x, e, _dev(ids), _dev(t), lse, _dev(g),
+                                           temperature=2.0, scale=1.1)
+        assert np.isfinite(_host(dX)).all() and np.isfinite(_host(dE)).all()
+        assert rel_err(_host(dX), dXk) <= TOL["fp32"]
+        assert rel_err(_host(dE), dEk) <= TOL["fp32"]
+
+
+def test_few_fp32_rows_in_several_pieces():
+    import torch
+    import dp_grape_projection_amd as dpg
+    N, d, V = 9, 4096, 45000
+    g0 = torch.Generator(device="cuda").manual_seed(8)
+    X = torch.randn(N, d, generator=g0, device="cuda")
+    E = torch.randn(V, d, generator=g0, device="cuda") / 32
+    y = torch.randint(0, V, (N,), generator=g0, device="cuda")
+    y[3] = -1
+    w = torch.rand(N, generator=g0, device="cuda")
+    loss, lse = dpg.dpg_vocab_loss(X, E, y)
+    dX, dE = dpg.dpg_vocab_loss_grad(X, E, y, lse, w)
+    on = (y >= 0).double()
+    z = X.double() @ E.double().t()
+    want = (torch.logsumexp(z, 1) - z.gather(1, y.clamp(min=0)[:, None])[:, 0]) * on
+    assert (loss.double() - want).abs().max().item() <= 4e-5
+    D = torch.softmax(z, 1).scatter_add(1, y.clamp(min=0)[:, None],
+                                        -torch.ones((N, 1), dtype=torch.float64, device="cuda"))
+    D = D * (w.double() * on)[:, None]
+    assert rel_err(_host(dX), (D @ E.double()).cpu().numpy()) <= TOL["fp32"]
+    err = (dE.double() - D.t() @ X.double()).norm() / (D.t() @ X.double()).norm()
+    assert err.item() <= TOL["fp32"]
