@@ -1535,6 +1535,12 @@ Split choose_split(int64_t m, int64_t n, int64_t steps, int combos, bool sums_an
   return best;
 }
 
+// Least table (elements) that few fp32 rows read as it is: packing a smaller one
+// costs less than splitting it in every block (loss and gradients of 128 rows x 64
+// against 1000 columns: 49 us packed, 58 as it is; 98 x 1024 x 9349: 181 and 189;
+// loss of 24 x 1024 x 9019: 52 and 37).
+constexpr int64_t kRawElements = 8ll << 20;
+
 struct VocabPlan {
   int64_t ldx = 0, np = 0, piece = 0, packed_piece = 0;
   int32_t splits = 1, splits_e = 1;
@@ -1553,7 +1559,7 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   p.ldx = round_up(d, kStepK);
   p.np = round_up(N, kPad);
   p.packed = parts > 1 || d % 8 != 0;
-  p.raw = parts > 1 && N <= SmallTile::kTile && d % 4 == 0;
+  p.raw = parts > 1 && N <= SmallTile::kTile && d % 4 == 0 && V * d >= kRawElements;
   // one piece of the vocabulary: its D, its teacher ids' bits, and its packed
   // table
   const int64_t row_bytes = p.ldx * 2 * parts;

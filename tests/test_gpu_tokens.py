@@ -594,3 +594,46 @@ def test_few_fp32_rows_in_several_pieces():
     assert rel_err(_host(dX), (D @ E.double()).cpu().numpy()) <= TOL["fp32"]
     err = (dE.double() - D.t() @ X.double()).norm() / (D.t() @ X.double()).norm()
     assert err.item() <= TOL["fp32"]
+
+
+@pytest.mark.parametrize("N,d,V", [(128, 1028, 8200), (97, 260, 33000), (33, 4100, 2050),
+                                   (16, 1000, 8500), (65, 1024, 8193), (64, 516, 16500)])
+def test_few_fp32_rows_of_a_large_table(N, d, V):
+    """A table large enough to be read as it is, against float64; one element off,
+    where it is packed, it meets the same bars."""
+    import torch
+    import dp_grape_projection_amd as dpg
+    print(f"[tokens] few fp32 rows, large table N={N} d={d} V={V}", flush=True)
+    g0 = torch.Generator(device="cuda").manual_seed(9)
+    X = torch.randn(N, d, generator=g0, device="cuda")
+    E = torch.randn(V, d, generator=g0, device="cuda") * 2 / math.sqrt(d)
+    k = 5
+    ids = torch.randint(-V // 8, V, (N, k), generator=g0, device="cuda")
+    ids[N // 2] = -1
+    X[N // 2] = float("nan")                  # a row without target
+    t = torch.randn(N, k, generator=g0, device="cuda") * 2
+    w = torch.rand(N, generator=g0, device="cuda")
+    E1 = torch.empty(V * d + 1, device="cuda")[1:].view(V, d).copy_(E)
+    got, off = [], []
+    for e, out in ((E, got), (E1, off)):
+        out.extend(dpg.dpg_distill_loss(X, e, ids, t, temperature=2.0))
+        out.extend(dpg.dpg_distill_loss_grad(X, e, ids, t, out[1], w, temperature=2.0))
+    valid = ids >= 0
+    on = valid.any(1)
+    Xd = torch.where(on[:, None], X, 0.0).double()
+    z = Xd @ E.double().t() / 2
+    q = torch.where(valid, t.double() / 2, -math.inf).softmax(1).nan_to_num(0.0)
+    dist = torch.zeros_like(z).scatter_add(1, ids.clamp(min=0), q)
+    lse = torch.logsumexp(z, 1)
+    loss = 4 * (torch.xlogy(q, q).sum(1) - (dist * z).sum(1) + lse) * on
+    D = (z.softmax(1) - dist) * (w.double() * 2 * on)[:, None]
+    want = [loss, lse * on, D @ E.double(), D.t() @ Xd]
+    bar = 2e-5 * max(1.0, lse.abs().max().item()) * 4
+    for a, b, c in zip(got, off, want):
+        assert torch.isfinite(a).all() and torch.isfinite(b).all()
+        if a.dim() == 1:
+            assert (a.double() - c).abs().max().item() <= bar
+            assert (b.double() - c).abs().max().item() <= bar
+        else:
+            assert rel_err(_host(a), c.cpu().numpy()) <= TOL["fp32"]
+            assert rel_err(_host(b), c.cpu().numpy()) <= TOL["fp32"]
