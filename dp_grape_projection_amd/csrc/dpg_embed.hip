@@ -138,7 +138,8 @@ __device__ __forceinline__ void store8(bf16* p, const Cols<K>& k, const float (&
 
 // ----------------------------------------------------------------- lookup --
 
-// 1 << tpr_log2 threads per row.
+// 1 << tpr_log2 threads per row. Bound by memory (8192 rows of 2048, fp32 to bf16: 17
+// us, 5.9 TB/s with every row from HBM) and, for few rows, by the launch.
 template <typename TE, typename TY, Kind K>
 __global__ __launch_bounds__(kThreads) void embed_kernel(const int64_t* ids, int64_t n,
                                                          const TE* E, int64_t V, int d,
@@ -176,7 +177,7 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(const int64_t* ids, int
 //
 // Reading all ids in each block costs N * 8 bytes of L2 reads per block, 64
 // KiB at N = 8192, and saves the four to six dependent launches of a radix
-// sort. Placement takes a batch of ids at a time: each wave finds, among 64
+// sort (8192 ids: 10 us, of which most are the dependent phases). Placement takes a batch of ids at a time: each wave finds, among 64
 // of the block's own entries, those that share a bin (one step per distinct
 // bin), and one wave then runs through the groups of 64 in order with one LDS
 // read and write each.
@@ -317,7 +318,9 @@ __global__ __launch_bounds__(kSortThreads) void token_sort_kernel(const int64_t*
 // ------------------------------------------------------------ sorted sums --
 
 // acc += sum over j in [j0, j1) of w(order[j]) dY[order[j]], in order, eight
-// rows in flight.
+// rows in flight: a row's latency, some 2 us under load, is what long sums are made
+// of (chunks of 16 rows at 8192 x 2048: 13 us with loads that wait for one another,
+// 8 so).
 template <typename TY, Kind K, class F>
 __device__ __forceinline__ void add_rows(const TY* dY, const int* order, int j0, int j1,
                                          int d, const Cols<K>& k, F weight, float (&acc)[8]) {
@@ -394,7 +397,8 @@ __global__ __launch_bounds__(kThreads) void embed_chunk_kernel(const TY* dY, int
 }
 
 // 1 << tpr_log2 threads per vocabulary row: its positions are added in order
-// (its chunks' sums, for a long token).
+// (its chunks' sums, for a long token). Bound by writing the table (50304 x 2048, fp32:
+// 70 us, 5.9 TB/s; a fill reaches 6.7).
 template <typename TY, typename TE, Kind K>
 __global__ __launch_bounds__(kThreads) void embed_grad_kernel(const TY* dY, int64_t V, int d,
                                                               SortedIds o, SampleWeight weight,
@@ -446,7 +450,8 @@ __global__ __launch_bounds__(kThreads) void embed_grad_kernel(const TY* dY, int6
 // in thread 0 only. 1 << tpr_log2 threads share a row; where that leaves threads
 // over, each group of so many adds a part of a long run, and the parts are added
 // in order. A wave reads 64 entries of the list at once, so that the rows' loads
-// do not wait for their positions.
+// do not wait for their positions. (2 x 3957 positions over 632 tokens, d 576: 122 us
+// in one chain of batches, 30 us so; 16 x 512 over 50304, d 2048: 18 us.)
 template <typename TY, Kind K>
 __device__ __forceinline__ float run_norm(const TY* dY, int d, const int* list, int j0, int j1,
                                           int tpr_log2, float scale) {

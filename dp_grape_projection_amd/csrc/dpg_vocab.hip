@@ -284,7 +284,9 @@ __device__ __forceinline__ float pack_row_half(const float* src, _Float16* dst, 
 // target, which each block counts for itself (8 bytes of L2 reads for every
 // earlier row, instead of a launch that counts and one that waits for it). The
 // kPad / kPackRows blocks after them zero Xp up to the next multiple of kPad.
-// The rest: rows of the first piece of the table, where it is packed.
+// The rest: rows of the first piece of the table, where it is packed. Bound by memory
+// with a table (107911 rows of 1001 bf16: 73 us, 5.9 TB/s), without by the counts and
+// the rows' latency (8192 rows of 4096: 45 us).
 constexpr int kPackRows = 16, kPadBlocks = kPad / kPackRows;
 template <typename T>
 __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int row_blocks) {
@@ -373,7 +375,9 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
 // Distillation: where a packed row's teacher ids lie in the piece, as one bit
 // per column, so that the tiles' epilogues find them; one block per row. The
 // row's distinct ids get consecutive places in qu, in ascending order; an id
-// named more than once gets its weights' sum, in the order they are named.
+// named more than once gets its weights' sum, in the order they are named. It writes
+// 10 bytes per row and word (4096 rows of 786 words: 20 us, bound by the block's
+// dependent phases).
 constexpr int kMaxWords = 4096;  // 64-column words of a piece
 constexpr int kMaxTop = 1024;    // entries of a teacher's row
 __global__ __launch_bounds__(kThreads) void teacher_ids_kernel(const VocabArgs a) {
@@ -469,6 +473,13 @@ __global__ __launch_bounds__(kThreads) void teacher_ids_kernel(const VocabArgs a
 // runs down its columns ("k-major") as 64 rows of the tile's width, read with
 // the transposing LDS load. The direct copies of A run two K steps ahead of
 // their use (three stages), those of B one (two stages): 160 KiB of LDS a CU.
+//
+// What bounds it is the power limit: the logits of 7187 rows x 4096 against 128000
+// columns take 5.9 ms, 1275 TFLOP/s with the clock at 1.59 GHz and the matrix cores
+// 79 % busy (the library's product of 8192 x 4096 x 65536: 1446 at 1.65 GHz, 84 %).
+// Hence the 16x16x32 instructions, which draw less than 32x32x16 (25.0 against 25.7
+// ms for loss and gradients at 8192 x 4096 x 128000), and a K loop that keeps copies,
+// fragment reads and products apart by scheduling barriers.
 //
 // Copies never leave their arrays: Xp, Ep and D are padded to whole tiles;
 // rows and chunks of E beyond its end are clamped to the last ones, and meet
@@ -1122,9 +1133,9 @@ __global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void stats_kern
   }
 }
 
-// A tile of bf16 values, staged in LDS and written in whole rows: an accumulator value's N is its row, its M its column. Rows >= n_rows
-// and columns >= n_cols are not written. 16-byte chunk c of row R sits in slot c ^ (R mod
-// the chunks of a row).
+// A tile of bf16 values, staged in LDS and written in whole rows: an accumulator
+// value's N is its row, its M its column. Rows >= n_rows and columns >= n_cols are
+// not written. 16-byte chunk c of row R sits in slot c ^ (R mod the chunks of a row).
 template <class G, class F>
 __device__ __forceinline__ void write_tile(char* smem, bf16* dst, int64_t ld, int n_rows, int n_cols,
                                            F value) {
@@ -1339,7 +1350,8 @@ __device__ __forceinline__ void de_tile(const VocabArgs& a, T* dE, int block, ch
   }
 }
 
-// lse and loss of every row from its tile partials: one wave per row.
+// lse and loss of every row from its tile partials: one wave per row. Bound by the
+// partials' latency (12 us for 8192 rows of 197 tiles, 4 us for 4 rows of 393).
 __global__ __launch_bounds__(kThreads) void lse_kernel(const VocabArgs a, int tiles) {
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (n >= a.N) return;
@@ -1488,8 +1500,8 @@ int check_call(const VocabCall& c, bool distill) {
 // Whether a launch of `tiles` big tiles takes them. Fewer than three for every
 // four CUs leave too much of the chip idle, and a K step of a big tile takes 64
 // KiB through a CU's LDS where a small one takes 32 (128 rows x 64 against 1000
-// columns, fp32: 18 us big, 12 us small; 252 big tiles of dX at 999 x 768 x
-// 32003, fp32: 311 us big, 424 us small). With at most 128 rows half of a big
+// columns, fp32: 18 us big, 12 us small; 252 big tiles of a product of six at 999 x
+// 768 x 32003: 311 us big, 424 us small). With at most 128 rows half of a big
 // tile would be padding (4 rows x 2048 against 50304 columns: 53 us big, 40 us
 // small).
 bool big_tiles(int64_t tiles, int64_t rows) { return tiles >= 192 && rows > SmallTile::kTile; }
