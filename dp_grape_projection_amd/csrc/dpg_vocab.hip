@@ -728,7 +728,7 @@ __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& o
 // acc = A B^T with A the table in fp32, as the caller has it, in 128 x 128 tiles.
 // With few rows the table's bytes are the time, and packing it first would read
 // and write them two to three times more (30 rows x 1024 against 111117 columns:
-// loss 374 us packed, 150 us as it is). A K step of 64 stays in fp32 in LDS and is
+// loss 374 us packed, 137 us as it is). A K step of 64 stays in fp32 in LDS and is
 // split into three bf16 parts in registers; the six products follow per K step, the
 // small ones first. A K step is 32 KiB of A and 48 KiB of B's parts, and one is
 // copied while the one before it is used.
@@ -1558,7 +1558,7 @@ struct VocabPlan {
   int32_t splits = 1, splits_e = 1;
   bool big_x = false, big_e = false;  // dX's and dE's tiles
   bool packed = false;  // the table is packed whatever its alignment
-  bool raw = false;     // but fp32 rows of whole 16 bytes are read as they are
+  bool raw = false;     // fp32, and the table is read as it is where it is aligned
   size_t off_flag, off_count, off_row, off_inv, off_target, off_g, off_lse2, off_q, off_ent, off_zt, off_qu, off_nu, off_bits,
       off_before, off_Xp, off_Ep, off_Xh, off_Eh, off_sx, off_se, off_part, off_D, off_dX, off_dE, total;
 };
@@ -1570,8 +1570,8 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   const int64_t parts = dtype == DPG_BF16 ? 1 : 3;
   p.ldx = round_up(d, kStepK);
   p.np = round_up(N, kPad);
-  p.packed = parts > 1 || d % 8 != 0;
   p.raw = parts > 1 && N <= SmallTile::kTile && d % 4 == 0 && V * d >= kRawElements;
+  p.packed = parts > 1 ? !p.raw : d % 8 != 0;
   // one piece of the vocabulary: its D, its teacher ids' bits, and its packed
   // table
   const int64_t row_bytes = p.ldx * 2 * parts;
@@ -1620,9 +1620,9 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   p.off_Xp = take(whole ? parts * p.np * p.ldx * 2 : 0);
   p.off_Ep = take(whole ? parts * p.packed_piece * p.ldx * 2 : 0);
   p.off_Xh = take(half ? 2 * p.np * p.ldx * 2 : 0);
-  p.off_Eh = take(half ? 2 * p.piece * p.ldx * 2 : 0);
+  p.off_Eh = take(half ? 2 * p.packed_piece * p.ldx * 2 : 0);
   p.off_sx = take(half ? p.np * 4 : 0);
-  p.off_se = take(half ? p.piece * 4 : 0);
+  p.off_se = take(half ? p.packed_piece * 4 : 0);
   const bool big = big_tiles(
       ceil_div(std::min(p.packed_piece, V), BigTile::kTile) * (p.np / BigTile::kTile), N);
   p.off_part = take(grad ? 0 : ceil_div(V, big ? BigTile::kTile : SmallTile::kTile) * p.np * 8);
@@ -1667,7 +1667,7 @@ VocabArgs make_args(const VocabCall& c, VocabPlan& p, char* ws, bool rows, bool 
   p.raw = p.raw && aligned(c.E, 16);
   const bool half = fp32 && !p.raw;
   a.Xp = !half || rows ? reinterpret_cast<bf16*>(ws + p.off_Xp) : nullptr;
-  a.Ep = pack && !p.raw && (!half || table) ? reinterpret_cast<bf16*>(ws + p.off_Ep) : nullptr;
+  a.Ep = pack && (!half || table) ? reinterpret_cast<bf16*>(ws + p.off_Ep) : nullptr;
   if (half) {
     a.Xh = reinterpret_cast<_Float16*>(ws + p.off_Xh);
     a.Eh = reinterpret_cast<_Float16*>(ws + p.off_Eh);

@@ -637,3 +637,27 @@ def test_few_fp32_rows_of_a_large_table(N, d, V):
         else:
             assert rel_err(_host(a), c.cpu().numpy()) <= TOL["fp32"]
             assert rel_err(_host(b), c.cpu().numpy()) <= TOL["fp32"]
+
+
+def test_few_fp32_rows_of_an_unaligned_table_in_pieces():
+    """One element off, a table is packed 64 MiB at a time."""
+    import torch
+    import dp_grape_projection_amd as dpg
+    N, d, V = 5, 1000, 30000
+    g0 = torch.Generator(device="cuda").manual_seed(10)
+    X = torch.randn(N, d, generator=g0, device="cuda")
+    E = torch.randn(V * d + 1, generator=g0, device="cuda")[1:].view(V, d)
+    y = torch.tensor([0, 29999, -1, 15000, 11008], device="cuda")
+    w = torch.rand(N, generator=g0, device="cuda")
+    loss, lse = dpg.dpg_vocab_loss(X, E, y, scale=0.05)
+    dX, dE = dpg.dpg_vocab_loss_grad(X, E, y, lse, w, scale=0.05)
+    on = (y >= 0).double()
+    z = 0.05 * (X.double() @ E.double().t())
+    at = y.clamp(min=0)[:, None]
+    want = (torch.logsumexp(z, 1) - z.gather(1, at)[:, 0]) * on
+    assert (loss.double() - want).abs().max().item() <= 4e-5 * max(1.0, want.max().item())
+    D = torch.softmax(z, 1).scatter_add(1, at, -torch.ones_like(at, dtype=torch.float64))
+    D = D * (0.05 * w.double() * on)[:, None]
+    assert torch.isfinite(dX).all() and torch.isfinite(dE).all()
+    assert rel_err(_host(dX), (D @ E.double()).cpu().numpy()) <= TOL["fp32"]
+    assert rel_err(_host(dE), (D.t() @ X.double()).cpu().numpy()) <= TOL["fp32"]
