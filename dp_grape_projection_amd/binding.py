@@ -611,10 +611,16 @@ def _embed_args(ids, dY, V):
     return int(ids.shape[0]), int(ids.shape[1]), int(dY.shape[2])
 
 
-def _embed_workspace(lib, B, T, V, d, device, workspace):
-    need = ctypes.c_size_t(0)
-    _check(lib, lib.dpg_embed_workspace_size(B, T, int(V), d, ctypes.byref(need)))
-    return _workspace(need.value, device, workspace)
+# (a size depends on its arguments alone, and asking costs as much as a launch)
+@functools.lru_cache(maxsize=1024)
+def _embed_workspace_size(B, T, V, d):
+    lib, need = load_library(), ctypes.c_size_t(0)
+    _check(lib, lib.dpg_embed_workspace_size(B, T, V, d, ctypes.byref(need)))
+    return need.value
+
+
+def _embed_workspace(B, T, V, d, device, workspace):
+    return _workspace(_embed_workspace_size(B, T, int(V), d), device, workspace)
 
 
 @_on_stream
@@ -630,7 +636,7 @@ def dpg_embed_norms(ids: torch.Tensor, dY: torch.Tensor, V: int, norm_sq: torch.
     _require(norm_sq, "norm_sq", torch.float32, (B,))
     _same_device(dY, norm_sq=norm_sq)
     code = _dtype_code(dY.dtype)
-    ws, ws_bytes = _embed_workspace(lib, B, T, V, d, dY.device, workspace)
+    ws, ws_bytes = _embed_workspace(B, T, V, d, dY.device, workspace)
     _check(lib, lib.dpg_embed_norms(_ptr(ids), _ptr(dY), B, T, int(V), d, code, float(scale),
                                     _ptr(norm_sq), ws.data_ptr(), ws_bytes,
                                     _stream_handle(stream)))
@@ -659,7 +665,7 @@ def dpg_embed_grad(ids: torch.Tensor, dY: torch.Tensor, V: int, scale: float = 1
         _require(sample_scales, "sample_scales", torch.float32, (B,))
     _same_device(dY, dE=dE, sample_scales=sample_scales)
     code, table = _dtype_code(dY.dtype), _dtype_code(dE.dtype)
-    ws, ws_bytes = _embed_workspace(lib, B, T, V, d, dY.device, workspace)
+    ws, ws_bytes = _embed_workspace(B, T, V, d, dY.device, workspace)
     _check(lib, lib.dpg_embed_grad(_ptr(ids), _ptr(dY), B, T, int(V), d, code, float(scale),
                                    _ptr(sample_scales), table, 1 if accumulate else 0,
                                    _ptr(dE), ws.data_ptr(), ws_bytes,
@@ -708,14 +714,19 @@ def _loss_grads(X, E, lse, dloss, need_dX, need_dE, dX, dE):
     return dX, dE
 
 
-def _vocab_workspace(lib, N, d, V, k, code, grad, device, workspace):
-    need = ctypes.c_size_t(0)
+@functools.lru_cache(maxsize=1024)
+def _vocab_workspace_size(N, d, V, k, code, grad):
+    lib, need = load_library(), ctypes.c_size_t(0)
     if k is None:
         st = lib.dpg_vocab_loss_workspace_size(N, d, V, code, grad, ctypes.byref(need))
     else:
         st = lib.dpg_distill_loss_workspace_size(N, d, V, k, code, grad, ctypes.byref(need))
     _check(lib, st)
-    return _workspace(need.value, device, workspace)
+    return need.value
+
+
+def _vocab_workspace(N, d, V, k, code, grad, device, workspace):
+    return _workspace(_vocab_workspace_size(N, d, V, k, code, grad), device, workspace)
 
 
 @_on_stream
@@ -733,7 +744,7 @@ def dpg_vocab_loss(X: torch.Tensor, E: torch.Tensor, targets: torch.Tensor,
     loss, lse = _loss_outputs(X, loss, lse)
     if N == 0:
         return loss, lse
-    ws, ws_bytes = _vocab_workspace(lib, N, d, V, None, code, 0, X.device, workspace)
+    ws, ws_bytes = _vocab_workspace(N, d, V, None, code, 0, X.device, workspace)
     _check(lib, lib.dpg_vocab_loss(_ptr(X), _ptr(E), _ptr(targets), N, d, V, code,
                                    float(scale), _ptr(loss), _ptr(lse), ws.data_ptr(),
                                    ws_bytes, _stream_handle(stream)))
@@ -755,7 +766,7 @@ def dpg_vocab_loss_grad(X: torch.Tensor, E: torch.Tensor, targets: torch.Tensor,
     dX, dE = _loss_grads(X, E, lse, dloss, need_dX, need_dE, dX, dE)
     if N == 0:
         return dX, None if dE is None else dE.zero_()
-    ws, ws_bytes = _vocab_workspace(lib, N, d, V, None, code, 1, X.device, workspace)
+    ws, ws_bytes = _vocab_workspace(N, d, V, None, code, 1, X.device, workspace)
     _check(lib, lib.dpg_vocab_loss_grad(_ptr(X), _ptr(E), _ptr(targets), _ptr(lse),
                                         _ptr(dloss), N, d, V, code, float(scale), _ptr(dX),
                                         _ptr(dE), ws.data_ptr(), ws_bytes,
@@ -790,7 +801,7 @@ def dpg_distill_loss(X: torch.Tensor, E: torch.Tensor, top_ids: torch.Tensor,
     loss, lse = _loss_outputs(X, loss, lse)
     if N == 0:
         return loss, lse
-    ws, ws_bytes = _vocab_workspace(lib, N, d, V, k, code, 0, X.device, workspace)
+    ws, ws_bytes = _vocab_workspace(N, d, V, k, code, 0, X.device, workspace)
     _check(lib, lib.dpg_distill_loss(_ptr(X), _ptr(E), _ptr(top_ids), _ptr(top_logits), N, d,
                                      V, k, code, float(scale), float(temperature),
                                      _ptr(loss), _ptr(lse), ws.data_ptr(), ws_bytes,
@@ -813,7 +824,7 @@ def dpg_distill_loss_grad(X: torch.Tensor, E: torch.Tensor, top_ids: torch.Tenso
     dX, dE = _loss_grads(X, E, lse, dloss, need_dX, need_dE, dX, dE)
     if N == 0:
         return dX, None if dE is None else dE.zero_()
-    ws, ws_bytes = _vocab_workspace(lib, N, d, V, k, code, 1, X.device, workspace)
+    ws, ws_bytes = _vocab_workspace(N, d, V, k, code, 1, X.device, workspace)
     _check(lib, lib.dpg_distill_loss_grad(
         _ptr(X), _ptr(E), _ptr(top_ids), _ptr(top_logits), _ptr(lse), _ptr(dloss), N, d, V, k,
         code, float(scale), float(temperature), _ptr(dX), _ptr(dE), ws.data_ptr(), ws_bytes,

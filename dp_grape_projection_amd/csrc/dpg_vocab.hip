@@ -1534,7 +1534,8 @@ Split choose_split(int64_t m, int64_t n, int64_t steps, int combos, bool sums_an
     const int64_t tile = big ? BigTile::kTile : SmallTile::kTile, slots = big ? 256 : 512;
     const int64_t tiles = ceil_div(m, tile) * ceil_div(n, tile);
     const int64_t most = std::max<int64_t>(1, std::min(slots / tiles, steps / 2));
-    for (int64_t k = 1; k <= most; ++k) {
+    // (every count up to 16, then steps of an eighth, and the most)
+    for (int64_t k = 1; k <= most; k = k < most ? std::min(k + std::max<int64_t>(1, k / 8), most) : k + 1) {
       const int64_t blocks = tiles * k;
       const double step = big ? 1.7 : blocks > 256 ? 1.3 : 0.7;
       double us = static_cast<double>(ceil_div(blocks, slots)) *
@@ -1575,7 +1576,8 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   // one piece of the vocabulary: its D, its teacher ids' bits, and its packed
   // table
   const int64_t row_bytes = p.ldx * 2 * parts;
-  p.piece = round_up(V, kPad);
+  // (at most 2^23 small tiles a launch, whose threads stay under 2^32)
+  p.piece = std::min(round_up(V, kPad), whole_pads((int64_t{1} << 37) / p.np));
   if (grad) p.piece = std::min(p.piece, whole_pads(kPieceBytes / (p.np * 2 * parts)));
   if (distill)
     p.piece = std::min({p.piece, whole_pads(kPieceBytes / (N * 10) * 64), int64_t{64 * kMaxWords}});
