@@ -513,6 +513,10 @@ struct Geometry {
 };
 typedef Geometry<256, 8, 4> BigTile;
 typedef Geometry<128, 4, 4> SmallTile;
+// For logits alone: tiles of 64 x 64 where small ones would leave half of the CUs idle
+// (logits of 185 x 200 against 5003 columns, fp32: 14 us
+// small, 8.5 tiny; 228 x 2370 x 4932, bf16: 22 and 18).
+typedef Geometry<64, 4, 1> TinyTile;
 
 // Slot of 16-byte chunk c in row k of a k-major tile. Of the
 // transposing read, 16 lanes take 32 bytes from each of four rows, and the
@@ -1506,10 +1510,17 @@ int check_call(const VocabCall& c, bool distill) {
 // small).
 bool big_tiles(int64_t tiles, int64_t rows) { return tiles >= 192 && rows > SmallTile::kTile; }
 
+// The logits' tiles for a piece of vn columns, of a table that is packed or not (raw).
+enum Tile { kBig, kSmall, kTiny };
+Tile logits_tiles(int64_t vn, int64_t N, bool raw) {
+  if (big_tiles(ceil_div(vn, BigTile::kTile) * ceil_div(N, BigTile::kTile), N)) return kBig;
+  return raw || ceil_div(vn, SmallTile::kTile) * ceil_div(N, SmallTile::kTile) > 128 ? kSmall : kTiny;
+}
 template <class F>
-void with_tile(int64_t tiles, int64_t rows, F fn) {
-  if (big_tiles(tiles, rows)) fn(BigTile());
-  else fn(SmallTile());
+void with_tile(Tile t, F fn) {
+  if (t == kBig) fn(BigTile());
+  else if (t == kSmall) fn(SmallTile());
+  else fn(TinyTile());
 }
 
 // Bytes of D, and of the packed table, kept at a time; of a packed table that
@@ -1625,9 +1636,10 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   p.off_Eh = take(half ? 2 * p.packed_piece * p.ldx * 2 : 0);
   p.off_sx = take(half ? p.np * 4 : 0);
   p.off_se = take(half ? p.packed_piece * 4 : 0);
-  const bool big = big_tiles(
-      ceil_div(std::min(p.packed_piece, V), BigTile::kTile) * (p.np / BigTile::kTile), N);
-  p.off_part = take(grad ? 0 : ceil_div(V, big ? BigTile::kTile : SmallTile::kTile) * p.np * 8);
+  // (an unaligned table has smaller pieces, and perhaps smaller tiles)
+  const Tile t = logits_tiles(std::min(p.packed_piece, V), N, false);
+  const int64_t tile = t == kBig ? BigTile::kTile : t == kSmall ? SmallTile::kTile : TinyTile::kTile;
+  p.off_part = take(grad ? 0 : ceil_div(V, tile) * p.np * 8);
   p.off_D = take(grad ? parts * p.np * p.piece * 2 : 0);
   p.off_dX = take(grad ? p.splits * p.np * p.ldx * 4 : 0);
   p.off_dE = take(p.splits_e > 1 ? p.splits_e * p.piece * p.ldx * 4 : 0);
@@ -1727,7 +1739,7 @@ void with_raw(bool raw, F fn) {
 
 template <typename T>
 int run_loss(VocabArgs a, const VocabPlan& p, hipStream_t s) {
-  with_tile(ceil_div(std::min(a.ldd, a.V), BigTile::kTile) * (a.np / BigTile::kTile), a.N, [&](auto g) {
+  with_tile(logits_tiles(std::min(a.ldd, a.V), a.N, p.raw), [&](auto g) {
     typedef decltype(g) G;
     for_pieces<T>(a, s, [&] {
       const dim3 grid = tile_grid(ceil_div(a.vn, G::kTile), a.np / G::kTile), b(G::kThreads);
@@ -1754,16 +1766,10 @@ void launch_out(const VocabArgs& a, const float* sums, int64_t stride, int split
                      sums, stride, splits, inv, rows, bits, out);
 }
 
-template <class F>
-void with_tile(bool big, F fn) {
-  if (big) fn(BigTile());
-  else fn(SmallTile());
-}
-
 template <typename T>
 int run_grad(VocabArgs a, const VocabPlan& p, void* dX, void* dE, hipStream_t s) {
   for_pieces<T>(a, s, [&] {
-    with_tile(ceil_div(a.vn, BigTile::kTile) * (a.np / BigTile::kTile), a.N, [&](auto g) {
+    with_tile(logits_tiles(a.vn, a.N, p.raw), [&](auto g) {
       typedef decltype(g) G;
       const dim3 grid = tile_grid(ceil_div(a.vn, G::kTile), a.np / G::kTile), b(G::kThreads);
       with_raw<T, G>(p.raw, [&](auto parts) {
@@ -1788,16 +1794,18 @@ int run_grad(VocabArgs a, const VocabPlan& p, void* dX, void* dE, hipStream_t s)
         hipLaunchKernelGGL(raw_dx_kernel, dim3(blocks_x(SmallTile::kTile)),
                            dim3(SmallTile::kThreads), 0, s, a);
       else if (dX)
-        with_tile(p.big_x, [&](auto g) {
+        with_tile(p.big_x ? kBig : kSmall, [&](auto g) {
           typedef decltype(g) G;
-          hipLaunchKernelGGL((products_kernel<G, T, true, false>), dim3(blocks_x(G::kTile)),
-                             dim3(G::kThreads), 0, s, a, 0, de);
+          if constexpr (!std::is_same<G, TinyTile>::value)
+            hipLaunchKernelGGL((products_kernel<G, T, true, false>), dim3(blocks_x(G::kTile)),
+                               dim3(G::kThreads), 0, s, a, 0, de);
         });
       if (dE)
-        with_tile(p.big_e, [&](auto g) {
+        with_tile(p.big_e ? kBig : kSmall, [&](auto g) {
           typedef decltype(g) G;
-          hipLaunchKernelGGL((products_kernel<G, T, false, true>), dim3(blocks_e(G::kTile)),
-                             dim3(G::kThreads), 0, s, a, 0, de);
+          if constexpr (!std::is_same<G, TinyTile>::value)
+            hipLaunchKernelGGL((products_kernel<G, T, false, true>), dim3(blocks_e(G::kTile)),
+                               dim3(G::kThreads), 0, s, a, 0, de);
         });
     }
     if (dE && a.splits_e > 1)
