@@ -513,9 +513,10 @@ struct Geometry {
 };
 typedef Geometry<256, 8, 4> BigTile;
 typedef Geometry<128, 4, 4> SmallTile;
-// For logits alone: tiles of 64 x 64 where small ones would leave half of the CUs idle
-// (logits of 185 x 200 against 5003 columns, fp32: 14 us
-// small, 8.5 tiny; 228 x 2370 x 4932, bf16: 22 and 18).
+// For logits alone, where there are no more small tiles than CUs: a K step is then the
+// latency of its reads and products, not their rate (logits of 185 x 200 against 5003
+// columns, fp32, 80 small tiles: 14 us small, 8.5 tiny; 10 x 2000 x 25000, bf16, 196:
+// 22 and 20.5; 80 x 1024 x 50304, 393: 19 and 25).
 typedef Geometry<64, 4, 1> TinyTile;
 
 // Slot of 16-byte chunk c in row k of a k-major tile. Of the
@@ -1514,7 +1515,7 @@ bool big_tiles(int64_t tiles, int64_t rows) { return tiles >= 192 && rows > Smal
 enum Tile { kBig, kSmall, kTiny };
 Tile logits_tiles(int64_t vn, int64_t N, bool raw) {
   if (big_tiles(ceil_div(vn, BigTile::kTile) * ceil_div(N, BigTile::kTile), N)) return kBig;
-  return raw || ceil_div(vn, SmallTile::kTile) * ceil_div(N, SmallTile::kTile) > 128 ? kSmall : kTiny;
+  return raw || ceil_div(vn, SmallTile::kTile) * ceil_div(N, SmallTile::kTile) > 256 ? kSmall : kTiny;
 }
 template <class F>
 void with_tile(Tile t, F fn) {
