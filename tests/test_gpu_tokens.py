@@ -661,3 +661,28 @@ def test_few_fp32_rows_of_an_unaligned_table_in_pieces():
     assert torch.isfinite(dX).all() and torch.isfinite(dE).all()
     assert rel_err(_host(dX), (D @ E.double()).cpu().numpy()) <= TOL["fp32"]
     assert rel_err(_host(dE), (D.t() @ X.double()).cpu().numpy()) <= TOL["fp32"]
+
+
+@pytest.mark.parametrize("N,d,V", [(129, 1024, 8300), (500, 260, 33000), (385, 4100, 2050)])
+def test_fp32_gradients_of_a_few_hundred_rows(N, d, V):
+    """dX from a table read as it is, and from a packed one (one element off)."""
+    import torch
+    import dp_grape_projection_amd as dpg
+    print(f"[tokens] a few hundred fp32 rows N={N} d={d} V={V}", flush=True)
+    g0 = torch.Generator(device="cuda").manual_seed(11)
+    X = torch.randn(N, d, generator=g0, device="cuda")
+    E = torch.randn(V, d, generator=g0, device="cuda") * 2 / math.sqrt(d)
+    E1 = torch.empty(V * d + 1, device="cuda")[1:].view(V, d).copy_(E)
+    y = torch.randint(-V // 8, V, (N,), generator=g0, device="cuda")
+    w = torch.rand(N, generator=g0, device="cuda")
+    on = (y >= 0).double()[:, None]
+    D = (X.double() @ E.double().t()).softmax(1)
+    D = D.scatter_add(1, y.clamp(min=0)[:, None], -torch.ones_like(on)) * w.double()[:, None] * on
+    want_dX, want_dE = (D @ E.double()).cpu().numpy(), (D.t() @ X.double()).cpu().numpy()
+    for e in (E, E1):
+        _, lse = dpg.dpg_vocab_loss(X, e, y)
+        dX, dE = dpg.dpg_vocab_loss_grad(X, e, y, lse, w)
+        only, _ = dpg.dpg_vocab_loss_grad(X, e, y, lse, w, need_dE=False)
+        assert torch.isfinite(dX).all() and torch.isfinite(dE).all() and torch.equal(dX, only)
+        assert rel_err(_host(dX), want_dX) <= TOL["fp32"]
+        assert rel_err(_host(dE), want_dE) <= TOL["fp32"]
