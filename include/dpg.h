@@ -399,9 +399,10 @@ int dpg_vocab_loss(const void* X, const void* E, const int64_t* targets, int64_t
  * but at least 256 columns). Products run on 16-bit operands and accumulate in
  * fp32: with bf16 inputs D is rounded to bf16 once; with fp32 inputs operands
  * are split, for the logits into two fp16 parts after a scale per row (an
- * element keeps 2^-23 of itself or 2^-38 of its row's largest), for dX and dE
- * exactly into three bf16 parts, so that products keep fp32's accuracy (an
- * infinity in X or E makes the rows it meets NaN). dX or dE may be NULL (not
+ * element keeps 2^-23 of itself or 2^-38 of its row's largest), for dX, dE and
+ * the logits of at most 128 rows against a table of 32 MiB or more exactly into
+ * three bf16 parts, so that products keep fp32's accuracy (an infinity in X or
+ * E makes the rows it meets NaN). dX or dE may be NULL (not
  * computed); rows without a target get a zero dX. dloss_n may carry a
  * sample's mean and clip factor: the gradient of each row's loss involves no
  * other row of X. Results do not vary from run to run.
