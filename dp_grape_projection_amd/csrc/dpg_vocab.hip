@@ -115,12 +115,15 @@ struct VocabArgs {
   float* loss;          // [N]
   float* lse;           // [N]: written by the loss, read by the gradient
   // workspace
-  int32_t* flag;        // [N] row has a target
+  int32_t* flag;        // [N] distillation: row has a target (kOn), of which one
+                        // entry has nearly all the weight (kPeaked)
   int32_t* count;       // [1] packed rows
   int32_t* row;         // [N] packed -> row
   int32_t* inv;         // [N] row -> packed, -1
   int32_t* target;      // [np] packed: cross entropy's target, else -1
-  float* g;             // [np] packed: dloss c tau, 0 past the last row
+  float* g;             // [np] packed: the part of dloss c tau that D carries, 0
+                        // past the last row
+  float* gx;            // bf16: [np] packed: the other part, which dX and Xg carry
   float* lse2;          // [np] packed: lse log2(e), 0 past the last row
   float* q;             // [N][k] target weights (distillation)
   float* ent;           // [N] sum q ln q (distillation)
@@ -132,6 +135,7 @@ struct VocabArgs {
                         // teacher ids
   uint16_t* before;     // [N][ldd / 64] packed: index in qu of a word's first
   bf16* Xp;             // [parts][np][ldx] packed rows of X, or null
+  bf16* Xg;             // bf16: [np][ldx] packed rows of gx X for dE, or null
   bf16* Ep;             // [parts][piece][ldx] the piece's rows of E, or null
   _Float16* Xh;         // fp32: [2][np][ldx] packed rows of X for the logits
   _Float16* Eh;         // fp32: [2][piece][ldx] the piece's rows of E for them
@@ -148,6 +152,32 @@ struct VocabArgs {
 };
 
 // ------------------------------------------------------------------- rows --
+
+// Where a row's factor g = dloss c tau meets its D. With fp32 operands D carries it,
+// in three exact parts. With bf16 operands D is rounded once. Where one entry of q
+// is close to 1 (cross entropy; a teacher sure of its token), D's large entry is
+// close to -g in every such row of a sample, and its rounding would be that of g, a
+// common factor of up to 2^-8 on the whole sample's gradients, in which independent
+// roundings average out. There D is a (p - q) with an a of 8 bits, whose large entry
+// bf16 holds nearly exactly, dX takes g / a in fp32 at its end and dE through a second
+// copy of the row of X, rounded element by element. Where no entry is close to 1, D's roundings are
+// independent of each other, and D carries g: a second rounding, of X, would only
+// add to them. (1024 rows of width 512 against 3000 columns, four samples, relative
+// errors of dX and dE: cross entropy 2.9e-3 and 2.9e-3 with g in D, 2.0e-3 and 2.6e-3
+// without; 16 teacher entries 2.3e-3 and 2.3e-3 with g, 2.3e-3 and 2.9e-3 without.)
+// The bar is where bf16 rounds an entry to 1.
+enum { kOff = 0, kOn = 1, kPeaked = 2 };
+constexpr float kPeak = 1.0f - 0x1p-9f;
+
+// a for a factor g: 1, so that X takes a power of two exactly, but 181/128 for other
+// g close to a multiple of a quarter of their power of two. Such a g moves all of the
+// bf16 values of X the same way (1 / 511 none of them): the rounded copies would be
+// off together, by up to 1.9e-3 with a = 1, where 4.7e-4 is left with this choice
+// (400000 normal values, factors about every 1/128 of [1, 2) and 1/3).
+__device__ __forceinline__ float factor_in_d(float g) {
+  const float t = 8.0f * __builtin_amdgcn_frexp_mantf(fabsf(g));  // quarters, in [4, 8)
+  return t != 4.0f && fabsf(t - rintf(t)) < 0.125f ? 181.0f / 128 : 1.0f;
+}
 
 // Distillation: one wave per row. q_j = exp(t_j / tau - m) / sum over the
 // entries whose id lies in [0, V); entries outside get q = 0, and a row
@@ -186,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void teacher_kernel(const VocabArgs a) {
   e = wave_sum(e);
   for (int j = lane; j < a.k; j += 64) q[j] = on ? q[j] / s : 0.0f;
   if (lane == 0) {
-    a.flag[n] = on;
+    a.flag[n] = !on ? kOff : 1.0f / s >= kPeak ? kPeaked : kOn;  // (the largest q is 1 / s)
     a.ent[n] = on ? e / s - logf(s) : 0.0f;  // sum q ln q, ln q = x - ln s
   }
 }
@@ -224,14 +254,19 @@ __device__ __forceinline__ void store_row(T* p, int n, typename Vec16<T>::type x
   }
 }
 
-// One row of d values as parts, zero beyond d, by 64 lanes.
+// One row of d values as parts, zero beyond d, by 64 lanes; bf16 values times a
+// factor, where it is not 1.
 template <typename T>
 __device__ __forceinline__ void pack_row(const T* src, bf16* dst, int d, int ldx, int64_t part_stride,
-                                         int lane) {
+                                         int lane, float factor = 1.0f) {
   constexpr int VN = Vec16<T>::N;
   for (int c = lane * VN; c < ldx; c += 64 * VN) {
-    const typename Vec16<T>::type x = load_row(src, c, d);
+    typename Vec16<T>::type x = load_row(src, c, d);
     if constexpr (kParts<T> == 1) {
+      if (factor != 1.0f) {
+#pragma unroll
+        for (int q = 0; q < VN; ++q) x[q] = from_float<bf16>(factor * static_cast<float>(x[q]));
+      }
       *reinterpret_cast<bf16x8*>(dst + c) = x;
     } else {
       Vec4<bf16>::type y[3];
@@ -307,9 +342,15 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
   const int n0 = min(block * kPackRows, static_cast<int>(a.N));
   const int64_t* ids = a.ids;
   auto on = [&](int n) {
-    if (a.t) return a.flag[n] != 0;
+    if (a.t) return a.flag[n] != kOff;
     const int64_t id = ids[n];
     return id >= 0 && id < a.V;
+  };
+  auto in_d = [&](int n, float g) {  // the part of row n's factor g that D carries
+    return kParts<T> == 1 && (!a.t || a.flag[n] == kPeaked) ? factor_in_d(g) : g;
+  };
+  auto in_x = [&](int n, float g) {  // and the one that dX and Xg do
+    return kParts<T> == 1 && (!a.t || a.flag[n] == kPeaked) ? g / factor_in_d(g) : 1.0f;
   };
   int c = 0;
   for (int j0 = tid; j0 < n0; j0 += 8 * kThreads) {
@@ -324,7 +365,7 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
   if (lane == 0) wave_cnt[wave] = c;
   __syncthreads();
   const int before = (wave_cnt[0] + wave_cnt[1]) + (wave_cnt[2] + wave_cnt[3]);
-  auto pack = [&](const T* src, int i, int d) {  // packed row i
+  auto pack = [&](const T* src, int i, int d, float gx) {  // packed row i
     const int64_t at = static_cast<int64_t>(i) * a.ldx, stride = static_cast<int64_t>(a.np) * a.ldx;
     if constexpr (kParts<T> == 3) {
       if (a.Xh) {
@@ -333,6 +374,9 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
       }
     }
     if (a.Xp) pack_row(src, a.Xp + at, d, a.ldx, stride, lane);
+    if constexpr (kParts<T> == 1) {
+      if (a.Xg) pack_row(src, a.Xg + at, d, a.ldx, stride, lane, gx);
+    }
   };
   const int pad = block - (row_blocks - kPadBlocks);
   if (pad >= 0) {
@@ -344,7 +388,7 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
         a.target[i] = -1;
         if (a.dloss) a.g[i] = a.lse2[i] = 0.0f;
       }
-      if (i < end) pack(static_cast<const T*>(a.X), i, 0);
+      if (i < end) pack(static_cast<const T*>(a.X), i, 0, 1.0f);
     }
     return;
   }
@@ -357,7 +401,9 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
       a.row[at] = mine;
       a.target[at] = a.t ? -1 : static_cast<int32_t>(a.ids[mine]);
       if (a.dloss) {
-        a.g[at] = a.dloss[mine] * a.dscale;
+        const float g = a.dloss[mine] * a.dscale;
+        a.g[at] = in_d(mine, g);
+        if (kParts<T> == 1) a.gx[at] = in_x(mine, g);
         a.lse2[at] = a.lse[mine] * kLog2e;
       }
     }
@@ -368,7 +414,8 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
     const int r = q * 4 + wave;
     if (!((b >> r) & 1)) continue;
     const int at = before + __popcll(b & ((1ull << r) - 1));
-    pack(static_cast<const T*>(a.X) + static_cast<int64_t>(n0 + r) * a.d, at, a.d);
+    const float gx = a.Xg ? in_x(n0 + r, a.dloss[n0 + r] * a.dscale) : 1.0f;
+    pack(static_cast<const T*>(a.X) + static_cast<int64_t>(n0 + r) * a.d, at, a.d, gx);
   }
 }
 
@@ -1171,10 +1218,10 @@ __device__ __forceinline__ void write_tile(char* smem, bf16* dst, int64_t ld, in
   }
 }
 
-// One tile of D for the piece: dloss_n c tau (exp(z - lse_n) - q), zero beyond
-// the piece and the packed rows. One rounding to bf16, after the target's
-// weight is subtracted: D enters two products whose other operand is bf16;
-// with fp32 D is kept in three parts.
+// One tile of D for the piece: g_n (exp(z - lse_n) - q), zero beyond the piece and
+// the packed rows. One rounding to bf16, after the target's weight is subtracted: D
+// enters two products whose other operand is bf16; with fp32 D is kept in three
+// parts.
 template <class G, int PARTS, bool TEACHER>
 __global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void grad_logits_kernel(
     const VocabArgs a) {
@@ -1308,7 +1355,7 @@ __device__ __forceinline__ void dx_tile(const VocabArgs& a, int block, char* sme
               a.v0 != 0, acc);
 }
 
-// The piece's rows of dE = D^T Xp, rounded once; with several splits of the packed
+// The piece's rows of dE = D^T X, rounded once; with several splits of the packed
 // rows, each split's sums.
 template <class G, typename T>
 __device__ __forceinline__ void de_tile(const VocabArgs& a, T* dE, int block, char* smem) {
@@ -1324,8 +1371,8 @@ __device__ __forceinline__ void de_tile(const VocabArgs& a, T* dE, int block, ch
   const int64_t row = static_cast<int64_t>(k0) * kStepK;
   typename G::Acc acc;
   tile_product<G, PARTS, true, true>(
-      rows_operand(a.Xp + row * a.ldx + c0, a.ldx, static_cast<int64_t>(a.np) * a.ldx,
-                   a.np - k0 * kStepK, a.ldx - c0),
+      rows_operand((PARTS == 1 ? a.Xg : a.Xp) + row * a.ldx + c0, a.ldx,
+                   static_cast<int64_t>(a.np) * a.ldx, a.np - k0 * kStepK, a.ldx - c0),
       rows_operand(a.D + row * a.ldd + w0, a.ldd, static_cast<int64_t>(a.np) * a.ldd,
                    a.np - k0 * kStepK, G::kTile),
       k1 - k0, smem, acc);
@@ -1422,18 +1469,21 @@ __global__ __launch_bounds__(SmallTile::kThreads, 1) void raw_dx_kernel(const Vo
 }
 
 // Row n of a gradient: its sums in `splits` arrays (stride floats apart) of rows
-// of a.ldx, added in order and rounded once. With inv, row inv[n] of them, and
-// zero where that is negative (a row without target). lanes = 2^lane_bits
+// of a.ldx, added in order and rounded once. With inv, row inv[n] of them, times its
+// factor where there are any, and zero where that is negative (a row without
+// target). lanes = 2^lane_bits
 // threads a row, each four columns at a time, so that narrow rows share a block.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void out_kernel(const VocabArgs a, const float* sums,
                                                        int64_t stride, int splits, const int32_t* inv,
-                                                       int64_t rows, int lane_bits, T* out) {
+                                                       const float* factor, int64_t rows,
+                                                       int lane_bits, T* out) {
   const int64_t n = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> lane_bits;
   if (n >= rows) return;
   const int64_t i = inv ? inv[n] : n;
   const bool vec = a.d % 4 == 0 && is_aligned(out, 4 * sizeof(T));
   const float* src = sums + (i < 0 ? 0 : i) * a.ldx;
+  const float f = factor && i >= 0 ? factor[i] : 1.0f;
   const int lanes = 1 << lane_bits;
   for (int c = (threadIdx.x & (lanes - 1)) * 4; c < a.d; c += lanes * 4) {
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
@@ -1450,6 +1500,8 @@ __global__ __launch_bounds__(kThreads) void out_kernel(const VocabArgs a, const 
             for (int q = 0; q < 4; ++q) x[q] += y[u][q];
           }
       }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] *= f;
     T* p = out + n * a.d + c;
     if (vec) {
       store4<T>(p, x[0], x[1], x[2], x[3]);
@@ -1574,8 +1626,8 @@ struct VocabPlan {
   bool big_x = false, big_e = false;  // dX's and dE's tiles
   bool packed = false;  // the table is packed whatever its alignment
   bool raw = false;     // fp32, and the table is read as it is where it is aligned
-  size_t off_flag, off_count, off_row, off_inv, off_target, off_g, off_lse2, off_q, off_ent, off_zt, off_qu, off_nu, off_bits,
-      off_before, off_Xp, off_Ep, off_Xh, off_Eh, off_sx, off_se, off_part, off_D, off_dX, off_dE, total;
+  size_t off_flag, off_count, off_row, off_inv, off_target, off_g, off_gx, off_lse2, off_q, off_ent, off_zt, off_qu, off_nu, off_bits,
+      off_before, off_Xp, off_Xg, off_Ep, off_Xh, off_Eh, off_sx, off_se, off_part, off_D, off_dX, off_dE, total;
 };
 
 int64_t whole_pads(int64_t x) { return std::max<int64_t>(kPad, x / kPad * kPad); }
@@ -1623,6 +1675,7 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   p.off_inv = take(N * 4);
   p.off_target = take(p.np * 4);
   p.off_g = take(grad ? p.np * 4 : 0);
+  p.off_gx = take(grad && parts == 1 ? p.np * 4 : 0);
   p.off_lse2 = take(grad ? p.np * 4 : 0);
   p.off_q = take(distill ? N * k * 4 : 0);
   p.off_ent = take(distill ? N * 4 : 0);
@@ -1634,6 +1687,7 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   // (the loss of fp32 operands needs only their fp16 parts)
   const bool half = parts > 1, whole = !half || grad || p.raw;
   p.off_Xp = take(whole ? parts * p.np * p.ldx * 2 : 0);
+  p.off_Xg = take(grad && parts == 1 ? p.np * p.ldx * 2 : 0);
   p.off_Ep = take(whole ? parts * p.packed_piece * p.ldx * 2 : 0);
   p.off_Xh = take(half ? 2 * p.np * p.ldx * 2 : 0);
   p.off_Eh = take(half ? 2 * p.packed_piece * p.ldx * 2 : 0);
@@ -1650,7 +1704,7 @@ VocabPlan plan_vocab(int64_t N, int64_t d, int64_t V, int32_t k, int32_t dtype, 
   return p;
 }
 
-// rows, table: the gradient needs X's, E's bf16 parts.
+// rows, table: the gradient needs X's, E's bf16 parts (for dE, for dX).
 VocabArgs make_args(const VocabCall& c, VocabPlan& p, char* ws, bool rows, bool table) {
   VocabArgs a{};
   a.X = c.X;
@@ -1672,6 +1726,7 @@ VocabArgs make_args(const VocabCall& c, VocabPlan& p, char* ws, bool rows, bool 
   a.inv = reinterpret_cast<int32_t*>(ws + p.off_inv);
   a.target = reinterpret_cast<int32_t*>(ws + p.off_target);
   a.g = reinterpret_cast<float*>(ws + p.off_g);
+  a.gx = reinterpret_cast<float*>(ws + p.off_gx);
   a.lse2 = reinterpret_cast<float*>(ws + p.off_lse2);
   a.q = reinterpret_cast<float*>(ws + p.off_q);
   a.ent = reinterpret_cast<float*>(ws + p.off_ent);
@@ -1684,6 +1739,7 @@ VocabArgs make_args(const VocabCall& c, VocabPlan& p, char* ws, bool rows, bool 
   p.raw = p.raw && aligned(c.E, 16);
   const bool half = fp32 && !p.raw;
   a.Xp = !half || rows ? reinterpret_cast<bf16*>(ws + p.off_Xp) : nullptr;
+  a.Xg = !fp32 && rows ? reinterpret_cast<bf16*>(ws + p.off_Xg) : nullptr;
   a.Ep = pack && (!half || table) ? reinterpret_cast<bf16*>(ws + p.off_Ep) : nullptr;
   if (half) {
     a.Xh = reinterpret_cast<_Float16*>(ws + p.off_Xh);
@@ -1762,11 +1818,11 @@ int run_loss(VocabArgs a, const VocabPlan& p, hipStream_t s) {
 // Each row's sums over the splits, rounded.
 template <typename T>
 void launch_out(const VocabArgs& a, const float* sums, int64_t stride, int splits, const int32_t* inv,
-                int64_t rows, T* out, hipStream_t s) {
+                const float* factor, int64_t rows, T* out, hipStream_t s) {
   int bits = 0;
   while (bits < 8 && 4 << bits < a.d) ++bits;
   hipLaunchKernelGGL(out_kernel<T>, dim3(blocks_of(rows, kThreads >> bits)), dim3(kThreads), 0, s, a,
-                     sums, stride, splits, inv, rows, bits, out);
+                     sums, stride, splits, inv, factor, rows, bits, out);
 }
 
 template <typename T>
@@ -1812,12 +1868,12 @@ int run_grad(VocabArgs a, const VocabPlan& p, void* dX, void* dE, hipStream_t s)
         });
     }
     if (dE && a.splits_e > 1)
-      launch_out<T>(a, a.dEacc, static_cast<int64_t>(a.ldd) * a.ldx, a.splits_e, nullptr, a.vn,
+      launch_out<T>(a, a.dEacc, static_cast<int64_t>(a.ldd) * a.ldx, a.splits_e, nullptr, nullptr, a.vn,
                     de + static_cast<int64_t>(a.v0) * a.d, s);
   });
   if (dX)
-    launch_out<T>(a, a.dXacc, static_cast<int64_t>(a.np) * a.ldx, a.splits, a.inv, a.N,
-                  static_cast<T*>(dX), s);
+    launch_out<T>(a, a.dXacc, static_cast<int64_t>(a.np) * a.ldx, a.splits, a.inv,
+                  kParts<T> == 1 ? a.gx : nullptr, a.N, static_cast<T*>(dX), s);
   return check_launch("vocab gradient");
 }
 

@@ -1,0 +1,87 @@
+"""How exact the token operators are where a row's own factor, or a long sum,
+decides: the gradients of bf16 losses under per-sample factors, against float64.
+
+A bf16 value is off by at most 2^-8 of itself, values of spread size by 1.6e-3 of
+their norm. dX carries that once for its own rounding. D = p - q is rounded too: a
+row's target entry, -(1 - p) with p of some 1 / V here, by at most p, the entries p
+by 1.6e-3 of a part that is small where p is spread thin. So dX is within 2.0e-3 of
+its norm, and its size along the exact gradient, where independent roundings average
+to nothing, within 2^-10 (p, 3e-4 on average, is the rest). A factor of the row
+that is rounded with D shows at up to 2^-8 in both. dE takes the factor with the rows
+of X, whose roundings are nearly independent of each other: its size along the exact
+gradient is held to 2^-10 as well."""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import tokens as ot
+
+pytestmark = pytest.mark.gpu
+
+V, D, T = 3001, 192, 64
+SIZE_BAR, DX_BAR = 2.0 ** -10, 2.0e-3
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu_and_library():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import dp_grape_projection_amd as dpg
+    dpg.load_library()     # fails loudly when libdpg.so is missing
+
+
+def _bf16(a):
+    import torch
+    return torch.from_numpy(np.asarray(a, np.float32)).bfloat16().cuda()
+
+
+def _size(got, want):
+    """How large `got` is along `want`, minus one."""
+    return float((got * want).sum() / (want * want).sum()) - 1.0
+
+
+# factors of a whole sample: half a bf16 step off a bf16 value, on either side, and
+# others as a mean over a sample's tokens with a clip factor gives them
+FACTORS = [1.0 + 0.98 * 2.0 ** -8, 1.4140625 + 0.98 * 2.0 ** -8, 0.37 / 61, 1.0 / 57,
+           1.0 / 511, 0.0, -3.0 / 4, 1.0 / 128]
+
+
+@pytest.mark.parametrize("which", ["vocab", "distill k 1", "distill k 9"])
+def test_a_samples_factor_is_no_common_error(which):
+    import torch
+    import dp_grape_projection_amd as dpg
+    r = np.random.default_rng(31)
+    N = T * len(FACTORS)
+    x = _bf16(r.standard_normal((N, D)))
+    e = _bf16(r.standard_normal((V, D)) / math.sqrt(D))
+    X, E = (a.double().cpu().numpy() for a in (x, e))
+    k = 9 if which.endswith("9") else 1
+    ids = np.stack([r.permutation(V)[:k] for _ in range(N)])
+    t = (r.standard_normal((N, k)) * 2.0).astype(np.float32)
+    g = np.repeat(np.float32(FACTORS), T)
+    q = ot.teacher_weights(ids, t, V, 1.0) if k > 1 else np.ones((N, 1))
+    args = (torch.from_numpy(ids[:, 0]).cuda(),) if which == "vocab" else (
+        torch.from_numpy(ids).cuda(), torch.from_numpy(t).cuda())
+    fn, grad = ((dpg.dpg_vocab_loss, dpg.dpg_vocab_loss_grad) if which == "vocab" else
+                (dpg.dpg_distill_loss, dpg.dpg_distill_loss_grad))
+    lse = fn(x, e, *args)[1]
+    for i, f in enumerate(FACTORS):
+        rows = slice(i * T, (i + 1) * T)
+        # the other samples have no factor: their part of dE is nothing
+        w = np.zeros(N, np.float32)
+        w[rows] = g[rows]
+        dX, dE = (a.double().cpu().numpy() for a in grad(x, e, *args, lse, torch.from_numpy(w).cuda()))
+        _, _, want_dX, want_dE = ot.target_loss(X[rows], E, ids[rows], q[rows], 1.0, 1.0, g[rows])
+        if f == 0.0:
+            assert not dX.any() and not dE.any()
+            continue
+        rel = np.linalg.norm(dX[rows] - want_dX) / np.linalg.norm(want_dX)
+        sizes = _size(dX[rows], want_dX), _size(dE, want_dE)
+        print(f"[precision] {which} factor {f:.6f}: dX {rel:.2e}, sizes {sizes[0]:+.1e} {sizes[1]:+.1e}",
+              flush=True)
+        assert abs(sizes[0]) <= SIZE_BAR, (f, sizes)
+        assert abs(sizes[1]) <= SIZE_BAR, (f, sizes)
+        if k == 1:
+            assert rel <= DX_BAR, (f, rel)
