@@ -43,6 +43,27 @@ class TokenEmbedding(torch.nn.Module):
         return y
 
 
+class _FirstDerivative(torch.autograd.Function):
+    """A gradient as a function of what it was computed from, without a derivative
+    of its own: the library has none, and a gradient without a graph would count as
+    a constant in a second backward pass."""
+
+    @staticmethod
+    def forward(ctx, grad, *inputs):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the token losses have no second derivative")
+
+
+def _gradients(grads, *inputs):
+    # grad mode is on in a backward pass only when it builds a graph itself
+    if torch.is_grad_enabled():
+        return tuple(None if g is None else _FirstDerivative.apply(g, *inputs) for g in grads)
+    return tuple(grads)
+
+
 class _VocabLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, E, targets, scale):
@@ -57,7 +78,7 @@ class _VocabLoss(torch.autograd.Function):
         dX, dE = _b.dpg_vocab_loss_grad(X, E, targets, lse, dloss.contiguous(),
                                         scale=ctx.scale, need_dX=ctx.needs_input_grad[0],
                                         need_dE=ctx.needs_input_grad[1])
-        return dX, dE, None, None
+        return (*_gradients((dX, dE), X, E, dloss), None, None)
 
 
 class _DistillLoss(torch.autograd.Function):
@@ -75,13 +96,13 @@ class _DistillLoss(torch.autograd.Function):
         dX, dE = _b.dpg_distill_loss_grad(X, E, top_ids, top_logits, lse, dloss.contiguous(),
                                           need_dX=ctx.needs_input_grad[0],
                                           need_dE=ctx.needs_input_grad[1], **ctx.args)
-        return dX, dE, None, None, None, None
+        return (*_gradients((dX, dE), X, E, dloss), None, None, None, None)
 
 
 def vocab_cross_entropy(X: torch.Tensor, E: torch.Tensor, targets: torch.Tensor,
                         scale: float = 1.0) -> torch.Tensor:
     """Per-row softmax cross entropy of X [..., d] against the table E [V, d]
-    (same type) without an array of logits; differentiable in X and E. Rows
+    (same type) without an array of logits; differentiable once in X and E. Rows
     whose target lies outside [0, V) give 0. Returns fp32 of X's leading shape."""
     return _VocabLoss.apply(X.contiguous(), E.contiguous(), targets.contiguous(), scale)
 
@@ -90,6 +111,6 @@ def distill_cross_entropy(X: torch.Tensor, E: torch.Tensor, top_ids: torch.Tenso
                           top_logits: torch.Tensor, temperature: float = 1.0,
                           scale: float = 1.0) -> torch.Tensor:
     """Per-row tau^2 KL of X [..., d] against the table E [V, d] from a teacher's
-    top k logits (top_ids, top_logits [..., k]); differentiable in X and E."""
+    top k logits (top_ids, top_logits [..., k]); differentiable once in X and E."""
     return _DistillLoss.apply(X.contiguous(), E.contiguous(), top_ids.contiguous(),
                               top_logits.contiguous(), temperature, scale)

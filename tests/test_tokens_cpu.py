@@ -1,0 +1,104 @@
+"""The modules and functions around the token operators on the CPU: the library's
+calls are replaced by their formulas in torch, so that what tokens.py and
+streaming.py do with them can be tested without a GPU."""
+import math
+
+import pytest
+import torch
+
+import dp_grape_projection_amd as dpg
+from dp_grape_projection_amd import binding
+
+
+def _vocab(X, E, targets, scale):
+    z = scale * X.flatten(0, -2) @ E.t()
+    y = targets.flatten()
+    on = (y >= 0) & (y < E.shape[0])
+    at = torch.where(on, y, 0)[:, None]
+    return z, on, torch.zeros_like(z).scatter_(1, at, 1.0) * on[:, None]
+
+
+def _losses(z, on, q, shape):
+    lse = torch.logsumexp(z, 1) * on
+    return ((lse - (z * q).sum(1)) * on).view(shape), lse.view(shape)
+
+
+def _grads(z, on, q, X, E, dloss, factor, need_dX, need_dE):
+    D = (torch.softmax(z, 1) * on[:, None] - q) * (factor * dloss.flatten()[:, None])
+    return ((D @ E).view(X.shape) if need_dX else None,
+            D.t() @ X.flatten(0, -2) if need_dE else None)
+
+
+@pytest.fixture
+def formulas(monkeypatch):
+    """dpg_vocab_loss and dpg_distill_loss with their gradients, as formulas. Like the
+    library's, their outputs carry no graph."""
+    @torch.no_grad()
+    def vocab(X, E, targets, scale=1.0):
+        return _losses(*_vocab(X, E, targets, scale), X.shape[:-1])
+
+    @torch.no_grad()
+    def vocab_grad(X, E, targets, lse, dloss, scale=1.0, need_dX=True, need_dE=True):
+        return _grads(*_vocab(X, E, targets, scale), X, E, dloss, scale, need_dX, need_dE)
+
+    def teacher(X, E, top_ids, top_logits, tau, scale):
+        z = scale / tau * X.flatten(0, -2) @ E.t()
+        q = torch.softmax(top_logits.flatten(0, -2) / tau, 1)
+        q = torch.zeros_like(z).scatter_add_(1, top_ids.flatten(0, -2), q)
+        return z, torch.ones(z.shape[0], dtype=torch.bool), q
+
+    @torch.no_grad()
+    def distill(X, E, top_ids, top_logits, temperature=1.0, scale=1.0):
+        return _losses(*teacher(X, E, top_ids, top_logits, temperature, scale), X.shape[:-1])
+
+    @torch.no_grad()
+    def distill_grad(X, E, top_ids, top_logits, lse, dloss, temperature=1.0, scale=1.0,
+                     need_dX=True, need_dE=True):
+        return _grads(*teacher(X, E, top_ids, top_logits, temperature, scale), X, E, dloss,
+                      scale * temperature, need_dX, need_dE)
+
+    for name, fn in (("dpg_vocab_loss", vocab), ("dpg_vocab_loss_grad", vocab_grad),
+                     ("dpg_distill_loss", distill), ("dpg_distill_loss_grad", distill_grad)):
+        monkeypatch.setattr(binding, name, fn)
+
+
+def _loss_inputs():
+    g = torch.Generator().manual_seed(4)
+    X = torch.randn(2, 3, 8, generator=g, requires_grad=True)
+    E = torch.randn(11, 8, generator=g, requires_grad=True)
+    y = torch.randint(0, 11, (2, 3), generator=g)
+    top = torch.stack([y, (y + 3) % 11], -1)
+    return X, E, y, top, torch.randn(2, 3, 2, generator=g)
+
+
+def _loss(which, X, E, y, top, t):
+    if which == "vocab":
+        return dpg.vocab_cross_entropy(X, E, y, scale=0.7)
+    return dpg.distill_cross_entropy(X, E, top, t, temperature=1.5)
+
+
+@pytest.mark.parametrize("which", ["vocab", "distill"])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_a_second_derivative_is_refused(formulas, which, weighted):
+    """A penalty on the gradient must not lose its part of the result silently,
+    whether or not what arrives at the loss's backward has a graph of its own."""
+    X, E, y, top, t = _loss_inputs()
+    w = torch.ones(2, 3, requires_grad=weighted)
+    total = (_loss(which, X, E, y, top, t) * w).sum()
+    dX, dE = torch.autograd.grad(total, (X, E), create_graph=True)
+    for part in (dX, dE):
+        with pytest.raises(RuntimeError, match="second derivative"):
+            (part.square().sum() + X.sum() + E.sum()).backward(retain_graph=True)
+
+
+@pytest.mark.parametrize("which", ["vocab", "distill"])
+def test_a_first_derivative_that_keeps_its_graph(formulas, which):
+    """create_graph alone changes no value."""
+    X, E, y, top, t = _loss_inputs()
+    want = torch.autograd.grad(_loss(which, X, E, y, top, t).sum(), (X, E))
+    got = torch.autograd.grad(_loss(which, X, E, y, top, t).sum(), (X, E), create_graph=True)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    frozen = E.detach()
+    dX, = torch.autograd.grad(_loss(which, X, frozen, y, top, t).sum(), X, create_graph=True)
+    assert torch.equal(dX, want[0])
