@@ -111,6 +111,10 @@ def distill_cross_entropy(X: torch.Tensor, E: torch.Tensor, top_ids: torch.Tenso
                           top_logits: torch.Tensor, temperature: float = 1.0,
                           scale: float = 1.0) -> torch.Tensor:
     """Per-row tau^2 KL of X [..., d] against the table E [V, d] from a teacher's
-    top k logits (top_ids, top_logits [..., k]); differentiable once in X and E."""
+    top k logits (top_ids, top_logits [..., k]); differentiable once in X and E. The
+    teacher's logits are data: they get no gradient, and ones that ask for one
+    are refused (detach them)."""
+    if torch.is_grad_enabled() and top_logits.requires_grad:
+        raise ValueError("top_logits must not require grad: the teacher gets no gradient")
     return _DistillLoss.apply(X.contiguous(), E.contiguous(), top_ids.contiguous(),
                               top_logits.contiguous(), temperature, scale)

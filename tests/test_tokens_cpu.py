@@ -102,3 +102,14 @@ def test_a_first_derivative_that_keeps_its_graph(formulas, which):
     frozen = E.detach()
     dX, = torch.autograd.grad(_loss(which, X, frozen, y, top, t).sum(), X, create_graph=True)
     assert torch.equal(dX, want[0])
+
+
+def test_a_teacher_that_wants_a_gradient_is_refused(formulas):
+    X, E, y, top, t = _loss_inputs()
+    t.requires_grad_()
+    with pytest.raises(ValueError, match="top_logits"):
+        dpg.distill_cross_entropy(X, E, top, t)
+    with torch.no_grad():                        # nothing is lost without a graph
+        dpg.distill_cross_entropy(X, E, top, t)
+    dpg.distill_cross_entropy(X, E, top, t.detach()).sum().backward()
+    assert X.grad is not None and t.grad is None
