@@ -128,6 +128,9 @@ class GrapeOptimizer:
 
     def _capture_tokens(self, layer, ids: torch.Tensor, y: torch.Tensor):
         self._begin(int(ids.shape[0]), y.device)
+        # the lookup's own ids: the caller's buffer may hold the next batch's before
+        # step(), and a gradient by other ids than its norms would not be clipped
+        ids = ids.clone()
 
         def on_grad(g: torch.Tensor):
             if layer.layer_id in self._done:

@@ -113,3 +113,112 @@ def test_a_teacher_that_wants_a_gradient_is_refused(formulas):
         dpg.distill_cross_entropy(X, E, top, t)
     dpg.distill_cross_entropy(X, E, top, t.detach()).sum().backward()
     assert X.grad is not None and t.grad is None
+
+
+# ------------------------------------------- the table in the private step --
+
+V, D_IN, D_OUT = 9, 6, 4
+
+
+def _table_sum(ids, dY, V, scale, s):
+    G = torch.zeros(V, dY.shape[-1])
+    for b, row in enumerate(ids.tolist()):
+        for t, v in enumerate(row):
+            if 0 <= v < V:
+                G[v] += scale * float(s[b]) * dY[b, t]
+    return G
+
+
+@pytest.fixture
+def private(monkeypatch):
+    """A table and a projected layer under a GrapeOptimizer, on the CPU; `calls`
+    lists the library's calls in order, `fail` names one that raises."""
+    class Setup:
+        calls, fail = [], None
+
+    def step_call(fn):
+        def wrapper(*args, **kw):
+            Setup.calls.append(fn.__name__)
+            if Setup.fail == fn.__name__:
+                raise dpg.DpgError(fn.__name__)
+            with torch.no_grad():
+                return fn(*args, **kw)
+        monkeypatch.setattr(binding, fn.__name__, wrapper)
+
+    @step_call
+    def dpg_embed(ids, E, scale=1.0, dtype=None):
+        ok = (ids >= 0) & (ids < E.shape[0])
+        return (scale * E[torch.where(ok, ids, 0)] * ok[..., None]).to(dtype or E.dtype)
+
+    @step_call
+    def dpg_embed_norms(ids, dY, V, norm_sq, scale=1.0):
+        for b in range(ids.shape[0]):
+            norm_sq[b] += _table_sum(ids[b:b + 1], dY[b:b + 1], V, scale, [1.0]).square().sum()
+
+    @step_call
+    def dpg_embed_grad(ids, dY, V, scale=1.0, sample_scales=None):
+        return _table_sum(ids, dY, V, scale, sample_scales)
+
+    @step_call
+    def dpg_philox_normals(seed, layer_id, step_word, tag, start, n, device=None):
+        return torch.randn(n, generator=torch.Generator().manual_seed(seed))
+
+    @step_call
+    def dpg_project_layer(A, dY, r, seed, proj_step, layer_id, norm_sq, G_hat=None):
+        G = torch.einsum("btk,bto->bko", A, dY)[:, :r].contiguous()
+        norm_sq += G.square().sum((1, 2))
+        return G
+
+    @step_call
+    def dpg_clip_sum_noise(G_hat, r, C, sigma, seed, step, norm_sq, layer_ids=None):
+        norms = norm_sq.sqrt()
+        s = torch.clamp(C / norms, max=1.0)[:, None, None]
+        return [(s * G).sum(0) for G in G_hat], norms
+
+    @step_call
+    def dpg_adam_backproject(G, W, m, v, r, lr, *args, **kw):
+        for w, g in zip(W, G):
+            w[:r] -= lr * g
+
+    def build(sigma=0.0, **kw):
+        torch.manual_seed(3)
+        Setup.emb = dpg.TokenEmbedding(V, D_IN, layer_id=1, scale=1.5, dtype=torch.float32,
+                                       device="cpu")
+        Setup.lin = dpg.ProjectedLinear(D_IN, D_OUT, layer_id=2, device="cpu")
+        Setup.opt = dpg.GrapeOptimizer([Setup.lin], r=3, clip_C=0.3, sigma=sigma, seed=5, lr=0.1,
+                                       embeddings=[Setup.emb], table_lr=0.5, **kw)
+        Setup.calls.clear()
+        return Setup
+    Setup.build = staticmethod(build)
+    return Setup
+
+
+def _ids():
+    return torch.tensor([[0, 4, 4, -1], [8, 0, 2, 2], [7, 7, 7, 7]])
+
+
+def _step(s, ids, between=()):
+    """One step; between: what happens after the forward pass, the backward pass."""
+    s.opt.zero_grad()
+    y = s.emb(ids)
+    out = s.lin(y)
+    for fn in between[:1]:
+        fn(y)
+    (out * torch.arange(1.0, 13.0).view(3, 4, 1)).sum().backward()
+    for fn in between[1:]:
+        fn(y)
+    s.opt.step()
+    return s.emb.table.clone()
+
+
+@pytest.mark.parametrize("when", ["after the forward pass", "after the backward pass"])
+def test_a_refilled_id_buffer_does_not_reach_the_step(private, when):
+    """Norms, clip factors and the gradient belong to the ids of the lookup."""
+    want = _step(private.build(), _ids())
+    ids = _ids()
+
+    def refill(y):
+        ids.copy_((ids + 3) % V)
+    keep = lambda y: None
+    got = _step(private.build(), ids, (refill, keep) if "forward" in when else (keep, refill))
+    assert torch.equal(got, want)
