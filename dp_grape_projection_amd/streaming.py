@@ -105,6 +105,7 @@ class GrapeOptimizer:
         self.last_norms: Optional[torch.Tensor] = None
         self.last_G_priv: Optional[List[torch.Tensor]] = None
         self.tokens: Dict[int, tuple] = {}  # layer id -> (ids, dY) of this step
+        self._dY_version: Dict[int, int] = {}     # of those dY when their norms were taken
         for l in self.layers + self.embeddings:
             l._grape = self
 
@@ -139,6 +140,7 @@ class GrapeOptimizer:
             _b.dpg_embed_norms(ids, dY, int(layer.table.shape[0]), self.norm_sq,
                                scale=layer.scale)
             self.tokens[layer.layer_id] = (ids, dY)
+            self._dY_version[layer.layer_id] = dY._version
             self._done.add(layer.layer_id)
             return None
 
@@ -185,6 +187,11 @@ class GrapeOptimizer:
                    if l.layer_id not in self._done]
         if missing:
             raise RuntimeError(f"no gradient reached layers {missing}")
+        # (dY may share its memory with the lookup output's .grad)
+        changed = [i for i, (_, dY) in self.tokens.items() if dY._version != self._dY_version[i]]
+        if changed:
+            raise RuntimeError(f"the gradients of layers {changed} changed after their norms "
+                               "were taken")
         ids = [l.layer_id for l in self.layers]
         G_priv, norms = _b.dpg_clip_sum_noise(
             [self.G_hat[i] for i in ids], self.r, self.clip_C, self.sigma,

@@ -222,3 +222,12 @@ def test_a_refilled_id_buffer_does_not_reach_the_step(private, when):
     keep = lambda y: None
     got = _step(private.build(), ids, (refill, keep) if "forward" in when else (keep, refill))
     assert torch.equal(got, want)
+
+
+def test_a_changed_gradient_is_reported(private):
+    """The table's gradient must be the one whose norms were taken."""
+    s = private.build()
+    old = s.emb.table.clone()
+    with pytest.raises(RuntimeError, match="changed"):
+        _step(s, _ids(), (lambda y: None, lambda y: y.grad.mul_(100.0)))
+    assert torch.equal(s.emb.table, old)
