@@ -89,6 +89,9 @@ class GrapeOptimizer:
         ids = [l.layer_id for l in self.layers + self.embeddings]
         if len(set(ids)) != len(ids):
             raise ValueError("layer ids must be unique")
+        if sigma > 0 and any(l.table.numel() >= 1 << 32 for l in self.embeddings):
+            raise ValueError("a table's noise has one stream entry per element: V * d must be "
+                             "below 2^32")
         self.r, self.clip_C, self.sigma, self.seed = int(r), clip_C, sigma, int(seed)
         self.lr, self.beta1, self.beta2, self.eps = lr, beta1, beta2, eps
         self.proj_period = int(proj_period)
@@ -146,17 +149,17 @@ class GrapeOptimizer:
 
         y.register_hook(on_grad)
 
-    def _update_table(self, layer, norms: torch.Tensor) -> None:
+    def _table_update(self, layer, norms: torch.Tensor) -> torch.Tensor:
+        """sum_i s_i g_i + sigma C Z of one table, nothing written."""
         ids, dY = self.tokens[layer.layer_id]
         V, d = (int(n) for n in layer.table.shape)
-        B = int(ids.shape[0])
         s = torch.clamp(self.clip_C / norms, max=1.0)  # norm 0 gives inf, so 1
         G = _b.dpg_embed_grad(ids, dY, V, scale=layer.scale, sample_scales=s)
         if self.sigma > 0:
             Z = _b.dpg_philox_normals(self.seed, layer.layer_id, self.t, 1, 0, V * d,
                                       device=G.device)
             G.add_(Z.view(V, d), alpha=self.sigma * self.clip_C)
-        layer.table.add_(G, alpha=-self.table_lr / B)
+        return G
 
     def _capture(self, layer: ProjectedLinear, x: torch.Tensor, y: torch.Tensor):
         A = x.detach().contiguous()
@@ -196,10 +199,13 @@ class GrapeOptimizer:
         G_priv, norms = _b.dpg_clip_sum_noise(
             [self.G_hat[i] for i in ids], self.r, self.clip_C, self.sigma,
             self.seed, self.t, self.norm_sq, layer_ids=ids)
+        # all that can fail (memory, an argument) before the first write, so that no
+        # step is applied in part
+        updates = [self._table_update(l, norms) for l in self.embeddings]
         _b.dpg_adam_backproject(G_priv, [l.W for l in self.layers], self.m, self.v,
                                 self.r, self.lr, self.beta1, self.beta2, self.eps,
                                 self.seed, self.t, self.proj_step, layer_ids=ids,
                                 dtype=self.dtype or torch.bfloat16)
-        for l in self.embeddings:
-            self._update_table(l, norms)
+        for l, G in zip(self.embeddings, updates):
+            l.table.add_(G, alpha=-self.table_lr / len(norms))
         self.last_norms, self.last_G_priv = norms, G_priv

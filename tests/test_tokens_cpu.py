@@ -140,7 +140,7 @@ def private(monkeypatch):
         def wrapper(*args, **kw):
             Setup.calls.append(fn.__name__)
             if Setup.fail == fn.__name__:
-                raise dpg.DpgError(fn.__name__)
+                raise RuntimeError(fn.__name__)
             with torch.no_grad():
                 return fn(*args, **kw)
         monkeypatch.setattr(binding, fn.__name__, wrapper)
@@ -231,3 +231,32 @@ def test_a_changed_gradient_is_reported(private):
     with pytest.raises(RuntimeError, match="changed"):
         _step(s, _ids(), (lambda y: None, lambda y: y.grad.mul_(100.0)))
     assert torch.equal(s.emb.table, old)
+
+
+@pytest.mark.parametrize("fail", ["dpg_embed_grad", "dpg_philox_normals", "dpg_clip_sum_noise",
+                                  "dpg_adam_backproject"])
+def test_a_step_that_fails_changes_nothing(private, fail):
+    """What can fail comes before the first write to a weight or a table."""
+    s = private.build(sigma=0.5)
+    table, W = s.emb.table.clone(), s.lin.W.clone()
+    s.fail = fail
+    with pytest.raises(RuntimeError, match=fail):
+        _step(s, _ids())
+    assert torch.equal(s.emb.table, table) and torch.equal(s.lin.W, W)
+    s.fail = None
+    s.opt.step()                                 # and can be taken again
+    assert not torch.equal(s.emb.table, table) and not torch.equal(s.lin.W, W)
+    got, got_W = s.emb.table.clone(), s.lin.W.clone()
+    other = private.build(sigma=0.5)
+    assert torch.equal(_step(other, _ids()), got) and torch.equal(other.lin.W, got_W)
+
+
+def test_a_table_past_the_noise_stream_is_refused():
+    """The noise of one layer and step has fewer than 2^32 entries."""
+    emb = dpg.TokenEmbedding(2 ** 21, 2 ** 11, layer_id=1, device="meta",
+                             table=torch.empty((2 ** 21, 2 ** 11), device="meta"))
+    lin = dpg.ProjectedLinear(D_IN, D_OUT, layer_id=2, device="cpu")
+    args = dict(r=3, clip_C=1.0, seed=5, lr=0.1, embeddings=[emb])
+    with pytest.raises(ValueError, match="2\\^32"):
+        dpg.GrapeOptimizer([lin], sigma=0.5, **args)
+    dpg.GrapeOptimizer([lin], sigma=0.0, **args)
