@@ -35,6 +35,7 @@ class TokenEmbedding(torch.nn.Module):
         self._grape = None  # the GrapeOptimizer driving this table, if any
 
     def forward(self, ids: torch.Tensor) -> torch.Tensor:
+        ids = ids.contiguous()
         y = _b.dpg_embed(ids, self.table, scale=self.scale, dtype=self.dtype)
         if torch.is_grad_enabled():
             y.requires_grad_()

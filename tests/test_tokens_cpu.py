@@ -147,11 +147,15 @@ def private(monkeypatch):
 
     @step_call
     def dpg_embed(ids, E, scale=1.0, dtype=None):
+        if not ids.is_contiguous():
+            raise ValueError("ids must be contiguous")
         ok = (ids >= 0) & (ids < E.shape[0])
         return (scale * E[torch.where(ok, ids, 0)] * ok[..., None]).to(dtype or E.dtype)
 
     @step_call
     def dpg_embed_norms(ids, dY, V, norm_sq, scale=1.0):
+        if not ids.is_contiguous():
+            raise ValueError("ids must be contiguous")
         for b in range(ids.shape[0]):
             norm_sq[b] += _table_sum(ids[b:b + 1], dY[b:b + 1], V, scale, [1.0]).square().sum()
 
@@ -260,3 +264,11 @@ def test_a_table_past_the_noise_stream_is_refused():
     with pytest.raises(ValueError, match="2\\^32"):
         dpg.GrapeOptimizer([lin], sigma=0.5, **args)
     dpg.GrapeOptimizer([lin], sigma=0.0, **args)
+
+
+def test_ids_of_any_strides(private):
+    """A next-token split, seq[:, :-1], and a batch laid out the other way round."""
+    want = _step(private.build(), _ids())
+    seq = torch.cat([_ids(), _ids()[:, :1]], 1)
+    assert torch.equal(_step(private.build(), seq[:, :-1]), want)
+    assert torch.equal(_step(private.build(), _ids().t().contiguous().t()), want)
