@@ -682,7 +682,9 @@ def _loss_args(X, E, ids, name, k_shape=()):
     _ids(ids, name, (*X.shape[:-1], *k_shape))
     _same_device(X, E=E, **{name: ids})
     d = int(X.shape[-1])
-    return X.numel() // max(d, 1), d, int(E.shape[0]), _dtype_code(X.dtype)
+    # (a width of zero has rows all the same, which the library refuses)
+    N = X.numel() // d if d else math.prod(X.shape[:-1])
+    return N, d, int(E.shape[0]), _dtype_code(X.dtype)
 
 
 def _loss_outputs(X, loss, lse):
