@@ -636,6 +636,8 @@ def dpg_embed_norms(ids: torch.Tensor, dY: torch.Tensor, V: int, norm_sq: torch.
     _require(norm_sq, "norm_sq", torch.float32, (B,))
     _same_device(dY, norm_sq=norm_sq)
     code = _dtype_code(dY.dtype)
+    if ids.numel() == 0:
+        return norm_sq
     ws, ws_bytes = _embed_workspace(B, T, V, d, dY.device, workspace)
     _check(lib, lib.dpg_embed_norms(_ptr(ids), _ptr(dY), B, T, int(V), d, code, float(scale),
                                     _ptr(norm_sq), ws.data_ptr(), ws_bytes,
@@ -665,6 +667,8 @@ def dpg_embed_grad(ids: torch.Tensor, dY: torch.Tensor, V: int, scale: float = 1
         _require(sample_scales, "sample_scales", torch.float32, (B,))
     _same_device(dY, dE=dE, sample_scales=sample_scales)
     code, table = _dtype_code(dY.dtype), _dtype_code(dE.dtype)
+    if ids.numel() == 0:
+        return dE if accumulate else dE.zero_()
     ws, ws_bytes = _embed_workspace(B, T, V, d, dY.device, workspace)
     _check(lib, lib.dpg_embed_grad(_ptr(ids), _ptr(dY), B, T, int(V), d, code, float(scale),
                                    _ptr(sample_scales), table, 1 if accumulate else 0,

@@ -31,3 +31,25 @@ def test_losses_of_width_zero_are_refused():
         dpg.dpg_distill_loss_grad(X, E, ids.view(4, 1), f.view(4, 1), f, f)
     loss, lse = dpg.dpg_vocab_loss(X[:0], E, ids[:0])
     assert loss.shape == lse.shape == (0,)
+
+
+@pytest.mark.parametrize("B,T", [(0, 4), (3, 0), (0, 0)])
+def test_an_empty_batch_adds_nothing(B, T):
+    """As the lookup and the losses do, the norms and the gradient take a batch of no
+    samples or of no tokens."""
+    import torch
+    import dp_grape_projection_amd as dpg
+    ids = torch.empty((B, T), dtype=torch.int64, device="cuda")
+    dY = torch.empty((B, T, 12), device="cuda")
+    norm_sq = torch.arange(1.0, B + 1.0, device="cuda")
+    assert dpg.dpg_embed_norms(ids, dY, 9, norm_sq) is norm_sq
+    assert torch.equal(norm_sq, torch.arange(1.0, B + 1.0, device="cuda"))
+    s = torch.ones(B, device="cuda")
+    dE = dpg.dpg_embed_grad(ids, dY, 9, sample_scales=s,
+                            dE=torch.full((9, 12), float("nan"), device="cuda"))
+    assert not dE.any()
+    old = torch.randn(9, 12, device="cuda")
+    kept = dpg.dpg_embed_grad(ids, dY, 9, dE=old.clone(), accumulate=True)
+    assert torch.equal(kept, old)
+    with pytest.raises(ValueError):
+        dpg.dpg_embed_grad(ids, dY, 9, dE=old[:, :8].contiguous())
