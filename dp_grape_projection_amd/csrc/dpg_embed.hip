@@ -448,10 +448,14 @@ __global__ __launch_bounds__(kThreads) void embed_grad_kernel(const TY* dY, int6
 
 // ||scale sum over j in [j0, j1) of dY[list[j]]||^2, by one block; the same value
 // in thread 0 only. 1 << tpr_log2 threads share a row; where that leaves threads
-// over, each group of so many adds a part of a long run, and the parts are added
-// in order. A wave reads 64 entries of the list at once, so that the rows' loads
-// do not wait for their positions. (2 x 3957 positions over 632 tokens, d 576: 122 us
-// in one chain of batches, 30 us so; 16 x 512 over 50304, d 2048: 18 us.)
+// over (d up to 1024), each group of so many adds a part of a long run, and the parts
+// are added in order; wider rows' runs are one chain. A wave reads 64 entries of the
+// list at once, so that the rows' loads do not wait for their positions. (2 x 3957
+// positions over 632 tokens, d 576: 122 us in one chain of batches, 30 us so; 16 x 512
+// over 50304, d 2048: 18 us.) Rows are added in fp32 64 at a time and those sums in
+// 64 bits: in one fp32 chain the terms of a long run of like sign fall below the sum's
+// last bits (2^20 equal rows of 5 columns: off by 2.1e-3, and a sample whose norm is
+// too small is clipped too little).
 template <typename TY, Kind K>
 __device__ __forceinline__ float run_norm(const TY* dY, int d, const int* list, int j0, int j1,
                                           int tpr_log2, float scale) {
@@ -468,9 +472,12 @@ __device__ __forceinline__ float run_norm(const TY* dY, int d, const int* list, 
   for (int c0 = 0; c0 < d; c0 += tpr * 8) {
     const int c = c0 + t * 8;
     const Cols<K> k(c, 0, d);
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float acc[8];
+    double sum[8] = {0., 0., 0., 0., 0., 0., 0., 0.};
     for (int j = b; j < e; j += 64) {
       const int mine = list[min(j + lane, e - 1)], m = min(64, e - j);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) acc[q] = 0.0f;
       for (int u0 = 0; u0 < m; u0 += U) {
         Raw8<TY> x[U];
 #pragma unroll
@@ -485,9 +492,12 @@ __device__ __forceinline__ float run_norm(const TY* dY, int d, const int* list, 
             for (int q = 0; q < 8; ++q) acc[q] += x[u][q];
           }
       }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) sum[q] += acc[q];
     }
-    if (groups > 1) {
-      if (c0) __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[q] = static_cast<float>(sum[q]);
+    if (groups > 1) {  // (then this loop's only pass)
 #pragma unroll
       for (int q = 0; q < 8; ++q) parts[tid * 8 + q] = acc[q];
       __syncthreads();

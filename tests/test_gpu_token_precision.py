@@ -85,3 +85,35 @@ def test_a_samples_factor_is_no_common_error(which):
         assert abs(sizes[1]) <= SIZE_BAR, (f, sizes)
         if k == 1:
             assert rel <= DX_BAR, (f, rel)
+
+
+# T, d, act: one token all along a sample (padding that is a token, say); rows of up to
+# and of more than a block's 2048 columns, sorted samples and short ones
+RUNS = [(2 ** 17, 1032, "bf16"), (2 ** 16, 2061, "fp32"), (2 ** 20, 24, "bf16"), (2 ** 20, 5, "fp32"),
+        (1000, 2061, "bf16"), (700, 4104, "fp32"), (3000, 2056, "bf16")]
+
+
+@pytest.mark.parametrize("T,d,act", RUNS)
+def test_norms_of_a_token_repeated_all_along(T, d, act):
+    """The sum of T equal rows of like sign, whose terms fall below the sum's last
+    bits one by one. The bar is that of the other fp32 results, 1e-5: sums of at most
+    64 terms in fp32, 64 * 2^-24, and what follows them in 64 bits."""
+    import torch
+    import dp_grape_projection_amd as dpg
+    g = torch.Generator(device="cuda").manual_seed(41)
+    x = torch.rand(d, generator=g, device="cuda") + 0.1
+    x = x.bfloat16() if act == "bf16" else x
+    B = 1 if T > 4096 else 2
+    dY = x.expand(B, T, d).contiguous()
+    ids = torch.full((B, T), 3, device="cuda")
+    ids[-1, T // 3] = -1                           # two rows less
+    ids[-1, T // 2] = 9
+    norm_sq = torch.full((B,), 0.5, device="cuda")
+    dpg.dpg_embed_norms(ids, dY, 9, norm_sq, scale=0.25)
+    unit = float(x.double().square().sum()) * 0.0625
+    for b in range(B):
+        n = T - 2 if b == B - 1 else T
+        want = 0.5 + unit * n * n
+        err = abs(float(norm_sq[b]) / want - 1.0)
+        print(f"[precision] norm of {n} rows of {d} {act}: {err:.1e}", flush=True)
+        assert err <= 1e-5
