@@ -117,3 +117,18 @@ def test_norms_of_a_token_repeated_all_along(T, d, act):
         err = abs(float(norm_sq[b]) / want - 1.0)
         print(f"[precision] norm of {n} rows of {d} {act}: {err:.1e}", flush=True)
         assert err <= 1e-5
+
+
+def test_norms_of_many_tokens_of_equal_size():
+    """A sample of 2^22 different tokens, whose squares are added up."""
+    import torch
+    import dp_grape_projection_amd as dpg
+    T, d = 2 ** 22, 4
+    x = torch.tensor([0.3, -0.7, 0.11, 0.9], device="cuda")
+    ids = torch.arange(T, device="cuda").flip(0).view(1, T)
+    norm_sq = torch.zeros(1, device="cuda")
+    dpg.dpg_embed_norms(ids, x.expand(1, T, d).contiguous(), T, norm_sq)
+    want = float(x.double().square().sum()) * T
+    err = abs(float(norm_sq[0]) / want - 1.0)
+    print(f"[precision] norms of {T} tokens: {err:.1e}", flush=True)
+    assert err <= 1e-5
