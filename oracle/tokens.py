@@ -12,7 +12,6 @@ import numpy as np
 
 __all__ = [
     "embed", "embed_grad", "embed_norms_sq", "teacher_weights", "target_loss",
-    "one_hot_targets",
 ]
 
 
@@ -58,12 +57,6 @@ def teacher_weights(top_ids, top_logits, V, tau):
             w = np.exp(t[at][ok] - t[at][ok].max())
             q[at][ok] = w / w.sum()
     return q
-
-
-def one_hot_targets(targets):
-    """Cross entropy as a target distribution of one entry per row."""
-    ids = np.asarray(targets)[..., None]
-    return ids
 
 
 def target_loss(X, E, ids, q, scale=1.0, tau=1.0, dloss=None):
