@@ -317,11 +317,13 @@ __device__ __forceinline__ float pack_row_half(const float* src, _Float16* dst, 
 // Packs rows and table in one launch. Blocks [0, row_blocks - kPadBlocks):
 // kPackRows rows of X each. A row's packed index is the number of rows before it that have a
 // target, which each block counts for itself (8 bytes of L2 reads for every
-// earlier row, instead of a launch that counts and one that waits for it). The
+// earlier row, instead of a launch that counts and one that waits for it). That
+// grows with the square of the rows: with 64 columns 9 us for 8192 rows, 31 for 2^15,
+// 0.31 ms for 2^17, and at 2^20 20 ms, more than the products of a small table. The
 // kPad / kPackRows blocks after them zero Xp up to the next multiple of kPad.
 // The rest: rows of the first piece of the table, where it is packed. Bound by memory
 // with a table (107911 rows of 1001 bf16: 73 us, 5.9 TB/s), without by the counts and
-// the rows' latency (8192 rows of 4096: 45 us).
+// the rows' latency (8192 rows of 4096: 45 us, 66 with the second copy for dE).
 constexpr int kPackRows = 16, kPadBlocks = kPad / kPackRows;
 template <typename T>
 __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int row_blocks) {
@@ -522,8 +524,9 @@ __global__ __launch_bounds__(kThreads) void teacher_ids_kernel(const VocabArgs a
 // their use (three stages), those of B one (two stages): 160 KiB of LDS a CU.
 //
 // What bounds it is the power limit: the logits of 7187 rows x 4096 against 128000
-// columns take 5.9 ms, 1275 TFLOP/s with the clock at 1.59 GHz and the matrix cores
-// 79 % busy (the library's product of 8192 x 4096 x 65536: 1446 at 1.65 GHz, 84 %).
+// columns take 5.4 to 6.2 ms, as the card's power and warmth allow, 1400 to 1220
+// TFLOP/s (6.15 ms with the clock at 1.54 GHz and the matrix cores 78 % busy; the
+// library's product of 8192 x 4096 x 65536: 1446 TFLOP/s at 1.65 GHz, 84 %).
 // Hence the 16x16x32 instructions, which draw less than 32x32x16 (25.0 against 25.7
 // ms for loss and gradients at 8192 x 4096 x 128000), and a K loop that keeps copies,
 // fragment reads and products apart by scheduling barriers.

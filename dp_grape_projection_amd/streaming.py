@@ -76,7 +76,9 @@ class GrapeOptimizer:
     not projected: its per-sample norms join the clip (dpg_embed_norms), its
     sum takes the clip factors (dpg_embed_grad) and noise sigma C Z from the
     stream of its own layer id, and the update is plain:
-    table -= table_lr * (sum_i s_i g_i + sigma C Z) / B."""
+    table -= table_lr * (sum_i s_i g_i + sigma C Z) / B.
+    g is the lookup's gradient alone. The losses' [V, d] tables are not clipped here:
+    keep them frozen, as a table that serves both ends is for its part in the loss."""
 
     def __init__(self, layers: Sequence[ProjectedLinear], r: int, clip_C: float,
                  sigma: float, seed: int, lr: float, beta1: float = 0.9,

@@ -104,7 +104,9 @@ def vocab_cross_entropy(X: torch.Tensor, E: torch.Tensor, targets: torch.Tensor,
                         scale: float = 1.0) -> torch.Tensor:
     """Per-row softmax cross entropy of X [..., d] against the table E [V, d]
     (same type) without an array of logits; differentiable once in X and E. Rows
-    whose target lies outside [0, V) give 0. Returns fp32 of X's leading shape."""
+    whose target lies outside [0, V) give 0. Returns fp32 of X's leading shape.
+    E's gradient is an ordinary one: no call gives its norms per sample, so a table
+    trained by it is outside a GrapeOptimizer's clip."""
     return _VocabLoss.apply(X.contiguous(), E.contiguous(), targets.contiguous(), scale)
 
 

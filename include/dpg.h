@@ -327,6 +327,12 @@ int dpg_rc_norms(const dpg_layer_grad* layers, int32_t n_layers, int64_t B,
  * token of the vocabulary); the same table may serve the lookup and the
  * losses. Token ids are int64. An id outside [0, V) marks a position that
  * takes no part (padding, a prompt without loss): nothing is read through it.
+ *
+ * What is private: the clip covers the gradient of the lookup's table, whose
+ * norms per sample dpg_embed_norms gives. No call gives such norms for the dE of
+ * the losses. A table trained through that dE is outside the clip, whatever
+ * factors dloss carries, and one that serves both ends takes only the lookup's
+ * part of its gradient in the private step.
  */
 
 /*
@@ -345,7 +351,7 @@ int dpg_embed_workspace_size(int64_t B, int64_t T, int64_t V, int64_t d, size_t*
 /*
  * dpg_embed_norms: each sample's squared gradient norm of the table,
  *     norm_sq[i] += sum_v || scale * sum_{t: ids[i][t] = v} dY[i][t] ||^2
- * for the clip across all of a model's trained tensors: it adds to the
+ * (sums of more than 64 rows, and of the squares, in 64 bits) for the clip across all of a model's trained tensors: it adds to the
  * buffer that dpg_project_layer adds to (same ordering rule).
  *   ids       device [B][T] int64
  *   dY        device [B][T][d], dtype: gradient of the lookup's output
@@ -404,8 +410,9 @@ int dpg_vocab_loss(const void* X, const void* E, const int64_t* targets, int64_t
  * are split, for the logits into two fp16 parts after a scale per row (an
  * element keeps 2^-23 of itself or 2^-38 of its row's largest), for dX, dE and
  * the logits of at most 128 rows against a table of 32 MiB or more exactly into
- * three bf16 parts, so that products keep fp32's accuracy (an infinity in X or
- * E makes the rows it meets NaN). dX or dE may be NULL (not
+ * three bf16 parts, so that products keep fp32's accuracy. An infinity in X or E
+ * can make NaN of all that it meets, with either type, also where the exact logit
+ * would be infinite. dX or dE may be NULL (not
  * computed); rows without a target get a zero dX. dloss_n may carry a
  * sample's mean and clip factor: the gradient of each row's loss involves no
  * other row of X. Results do not vary from run to run.
@@ -459,7 +466,7 @@ int dpg_philox_normals(uint64_t seed, uint32_t layer_id, uint32_t step_word,
 
 /*
  * Kernel-timing diagnostics. While enabled (process-wide), every kernel that
- * the step calls enqueue (both forms) is bracketed by a
+ * the step calls enqueue (both forms; not the token operators) is bracketed by a
  * pair of HIP events recorded on the call's own stream. dpg_timing_read waits
  * for those events, adds each launch's elapsed time to the total of its
  * kernel kind and returns, for kinds 0 .. n_kinds-1, the total milliseconds
