@@ -27,6 +27,7 @@ namespace dpg {
 namespace {
 
 constexpr int kPad = 256;     // packed rows and pieces are padded to whole tiles
+constexpr int kMaxTop = 1024; // entries of a teacher's row
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // fp32 products on the 16-bit matrix instructions, which are 16 times as fast as
@@ -67,6 +68,7 @@ template <> struct Combos<3> {
 constexpr int kRaw = 0;
 // Parts of the logits' operands where the others have PARTS.
 template <int PARTS> constexpr int kLogitParts = PARTS == 3 ? 2 : 1;
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 template <int PARTS>
@@ -115,15 +117,15 @@ struct VocabArgs {
   float* loss;          // [N]
   float* lse;           // [N]: written by the loss, read by the gradient
   // workspace
-  int32_t* flag;        // [N] distillation: row has a target (kOn), of which one
-                        // entry has nearly all the weight (kPeaked)
+  int32_t* flag;        // [N] distillation: row has a target (kOn), or one whose
+                        // entry j has nearly all the weight (kPeaked + j)
   int32_t* count;       // [1] packed rows
   int32_t* row;         // [N] packed -> row
   int32_t* inv;         // [N] row -> packed, -1
   int32_t* target;      // [np] packed: cross entropy's target, else -1
-  float* g;             // [np] packed: the part of dloss c tau that D carries, 0
+  float* g;             // [np] packed: the factor of dloss c tau that D carries, 0
                         // past the last row
-  float* gx;            // bf16: [np] packed: the other part, which dX and Xg carry
+  float* gx;            // bf16: [np] packed: the other one, which dX and Xg carry
   float* lse2;          // [np] packed: lse log2(e), 0 past the last row
   float* q;             // [N][k] target weights (distillation)
   float* ent;           // [N] sum q ln q (distillation)
@@ -135,7 +137,7 @@ struct VocabArgs {
                         // teacher ids
   uint16_t* before;     // [N][ldd / 64] packed: index in qu of a word's first
   bf16* Xp;             // [parts][np][ldx] packed rows of X, or null
-  bf16* Xg;             // bf16: [np][ldx] packed rows of gx X for dE, or null
+  bf16* Xg;             // bf16: [np][ldx] packed rows of X times gx for dE, or null
   bf16* Ep;             // [parts][piece][ldx] the piece's rows of E, or null
   _Float16* Xh;         // fp32: [2][np][ldx] packed rows of X for the logits
   _Float16* Eh;         // fp32: [2][piece][ldx] the piece's rows of E for them
@@ -154,29 +156,33 @@ struct VocabArgs {
 // ------------------------------------------------------------------- rows --
 
 // Where a row's factor g = dloss c tau meets its D. With fp32 operands D carries it,
-// in three exact parts. With bf16 operands D is rounded once. Where one entry of q
-// is close to 1 (cross entropy; a teacher sure of its token), D's large entry is
-// close to -g in every such row of a sample, and its rounding would be that of g, a
-// common factor of up to 2^-8 on the whole sample's gradients, in which independent
-// roundings average out. There D is a (p - q) with an a of 8 bits, whose large entry
-// bf16 holds nearly exactly, dX takes g / a in fp32 at its end and dE through a second
-// copy of the row of X, rounded element by element. Where no entry is close to 1, D's roundings are
-// independent of each other, and D carries g: a second rounding, of X, would only
-// add to them. (1024 rows of width 512 against 3000 columns, four samples, relative
-// errors of dX and dE: cross entropy 2.9e-3 and 2.9e-3 with g in D, 2.0e-3 and 2.6e-3
-// without; 16 teacher entries 2.3e-3 and 2.3e-3 with g, 2.3e-3 and 2.9e-3 without.)
-// The bar is where bf16 rounds an entry to 1.
+// in three exact parts. With bf16 operands D is rounded once. Where one entry of q has
+// most of the weight (cross entropy; a teacher sure of its token), so has one entry of
+// D, and all of the row's gradient is off by that entry's rounding: by up to 2^-8, and
+// for a whole sample the same way, where its rows share g and p is small. There D
+// carries t / (q - p) of that entry instead of g, which makes it -t, of 8 bits at most,
+// and dX takes the rest of the factor in fp32 at its end, dE through a second copy of
+// the row of X, rounded element by element. Other rows' D has several entries whose
+// roundings are independent of each other, and carries g: a second rounding, of X,
+// would only add to them. (Errors of dX and dE over those of gradients that are rounded
+// once, in 150 cases of 1 to 8192 rows, mean and worst: cross entropy 1.43, 2.1 and 1.39,
+// 2.2 with g in D, 1.00, 1.03 and 1.29, 1.48 so; teachers of which few are sure 1.41, 1.7
+// and 1.38, 1.7 with g, 1.31, 1.52 and 1.36, 1.52 so. Finding p takes the packing 3 us.)
+// kPeaked + j: entry j is that one, of at least kPeak; what D has there is at least
+// kPeakD (or D's other entries count as much).
 enum { kOff = 0, kOn = 1, kPeaked = 2 };
-constexpr float kPeak = 1.0f - 0x1p-9f;
+constexpr float kPeak = 0.75f, kPeakD = 0.25f;
 
-// a for a factor g: 1, so that X takes a power of two exactly, but 181/128 for other
-// g close to a multiple of a quarter of their power of two. Such a g moves all of the
-// bf16 values of X the same way (1 / 511 none of them): the rounded copies would be
-// off together, by up to 1.9e-3 with a = 1, where 4.7e-4 is left with this choice
-// (400000 normal values, factors about every 1/128 of [1, 2) and 1/3).
-__device__ __forceinline__ float factor_in_d(float g) {
-  const float t = 8.0f * __builtin_amdgcn_frexp_mantf(fabsf(g));  // quarters, in [4, 8)
-  return t != 4.0f && fabsf(t - rintf(t)) < 0.125f ? 181.0f / 128 : 1.0f;
+// t for a row whose dE takes the factor g / t with X. 181/128 where g is close to a
+// multiple of a quarter of its power of two: such a g moves all of the bf16 values of X
+// the same way (1 / 511 none of them), and the rounded copies would be off together,
+// by up to 1.9e-3 with t = 1, where 4.7e-4 is left so (400000 normal values, factors
+// about every 1/128 of [1, 2) and 1/3). But 1 within 2^-11 of a power of two (g = 1, p
+// small), which is then as near, and whose copy of X is exact.
+__device__ __forceinline__ float peak_in_d(float g) {
+  const float m = 8.0f * __builtin_amdgcn_frexp_mantf(fabsf(g));  // quarters, in [4, 8)
+  const bool power = m < 4.0f + 0x1p-9f || m > 8.0f - 0x1p-8f;
+  return !power && fabsf(m - rintf(m)) < 0.125f ? 181.0f / 128 : 1.0f;
 }
 
 // Distillation: one wave per row. q_j = exp(t_j / tau - m) / sum over the
@@ -202,11 +208,13 @@ __global__ __launch_bounds__(kThreads) void teacher_kernel(const VocabArgs a) {
   nan = __any(nan);
   const bool on = m > -INFINITY || nan;
   float s = 0.0f, e = 0.0f;
+  int top = kMaxTop;  // the first entry with the largest logit
   for (int j = lane; j < a.k; j += 64) {
     float w = 0.0f;
     if (on && id[j] >= 0 && id[j] < a.V) {
       const float x = (t[j] - m) * inv_tau;
       w = expf(x);
+      if (t[j] == m) top = min(top, j);
       if (w != 0.0f) e = fmaf(w, x, e);
     }
     q[j] = w;
@@ -214,9 +222,11 @@ __global__ __launch_bounds__(kThreads) void teacher_kernel(const VocabArgs a) {
   }
   s = wave_sum(s);
   e = wave_sum(e);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) top = min(top, __shfl_xor(top, off, 64));
   for (int j = lane; j < a.k; j += 64) q[j] = on ? q[j] / s : 0.0f;
   if (lane == 0) {
-    a.flag[n] = !on ? kOff : 1.0f / s >= kPeak ? kPeaked : kOn;  // (the largest q is 1 / s)
+    a.flag[n] = !on ? kOff : 1.0f / s >= kPeak ? kPeaked + top : kOn;  // (the largest q is 1 / s)
     a.ent[n] = on ? e / s - logf(s) : 0.0f;  // sum q ln q, ln q = x - ln s
   }
 }
@@ -254,19 +264,14 @@ __device__ __forceinline__ void store_row(T* p, int n, typename Vec16<T>::type x
   }
 }
 
-// One row of d values as parts, zero beyond d, by 64 lanes; bf16 values times a
-// factor, where it is not 1.
+// One row of d values as parts, zero beyond d, by 64 lanes.
 template <typename T>
 __device__ __forceinline__ void pack_row(const T* src, bf16* dst, int d, int ldx, int64_t part_stride,
-                                         int lane, float factor = 1.0f) {
+                                         int lane) {
   constexpr int VN = Vec16<T>::N;
   for (int c = lane * VN; c < ldx; c += 64 * VN) {
-    typename Vec16<T>::type x = load_row(src, c, d);
+    const typename Vec16<T>::type x = load_row(src, c, d);
     if constexpr (kParts<T> == 1) {
-      if (factor != 1.0f) {
-#pragma unroll
-        for (int q = 0; q < VN; ++q) x[q] = from_float<bf16>(factor * static_cast<float>(x[q]));
-      }
       *reinterpret_cast<bf16x8*>(dst + c) = x;
     } else {
       Vec4<bf16>::type y[3];
@@ -323,7 +328,8 @@ __device__ __forceinline__ float pack_row_half(const float* src, _Float16* dst, 
 // kPad / kPackRows blocks after them zero Xp up to the next multiple of kPad.
 // The rest: rows of the first piece of the table, where it is packed. Bound by memory
 // with a table (107911 rows of 1001 bf16: 73 us, 5.9 TB/s), without by the counts and
-// the rows' latency (8192 rows of 4096: 45 us, 66 with the second copy for dE).
+// the rows' latency (8192 rows of 4096: 34 us for the loss, 75 for the gradients,
+// with the targets' logits and the second copy).
 constexpr int kPackRows = 16, kPadBlocks = kPad / kPackRows;
 template <typename T>
 __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int row_blocks) {
@@ -348,12 +354,6 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
     const int64_t id = ids[n];
     return id >= 0 && id < a.V;
   };
-  auto in_d = [&](int n, float g) {  // the part of row n's factor g that D carries
-    return kParts<T> == 1 && (!a.t || a.flag[n] == kPeaked) ? factor_in_d(g) : g;
-  };
-  auto in_x = [&](int n, float g) {  // and the one that dX and Xg do
-    return kParts<T> == 1 && (!a.t || a.flag[n] == kPeaked) ? g / factor_in_d(g) : 1.0f;
-  };
   int c = 0;
   for (int j0 = tid; j0 < n0; j0 += 8 * kThreads) {
 #pragma unroll
@@ -367,31 +367,58 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
   if (lane == 0) wave_cnt[wave] = c;
   __syncthreads();
   const int before = (wave_cnt[0] + wave_cnt[1]) + (wave_cnt[2] + wave_cnt[3]);
-  auto pack = [&](const T* src, int i, int d, float gx) {  // packed row i
-    const int64_t at = static_cast<int64_t>(i) * a.ldx, stride = static_cast<int64_t>(a.np) * a.ldx;
-    if constexpr (kParts<T> == 3) {
-      if (a.Xh) {
-        const float f = pack_row_half(src, a.Xh + at, d, a.ldx, stride, lane);
-        if (lane == 0) a.sx[i] = f;
+  // a wave's rows: d columns from src[q] on, to packed row to[q] where it is not
+  // negative, side by side, so that their latencies are
+  constexpr int R = kPackRows / 4;
+  auto pack = [&](const T* const (&src)[R], const int (&to)[R], int d, const float (&gx)[R]) {
+    if constexpr (kParts<T> == 1) {
+      constexpr int VN = Vec16<T>::N;
+      for (int c = lane * VN; c < a.ldx; c += 64 * VN) {
+        typename Vec16<T>::type x[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+          if (to[q] >= 0) x[q] = load_row(src[q], c, d);
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+          if (to[q] >= 0) {
+            const int64_t at = static_cast<int64_t>(to[q]) * a.ldx + c;
+            *reinterpret_cast<bf16x8*>(a.Xp + at) = x[q];
+            if (!a.Xg) continue;
+#pragma unroll
+            for (int i = 0; i < VN; ++i) x[q][i] = from_float<bf16>(gx[q] * static_cast<float>(x[q][i]));
+            *reinterpret_cast<bf16x8*>(a.Xg + at) = x[q];
+          }
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        if (to[q] < 0) continue;
+        const int64_t at = static_cast<int64_t>(to[q]) * a.ldx, stride = static_cast<int64_t>(a.np) * a.ldx;
+        if (a.Xh) {
+          const float f = pack_row_half(src[q], a.Xh + at, d, a.ldx, stride, lane);
+          if (lane == 0) a.sx[to[q]] = f;
+        }
+        if (a.Xp) pack_row(src[q], a.Xp + at, d, a.ldx, stride, lane);
       }
     }
-    if (a.Xp) pack_row(src, a.Xp + at, d, a.ldx, stride, lane);
-    if constexpr (kParts<T> == 1) {
-      if (a.Xg) pack_row(src, a.Xg + at, d, a.ldx, stride, lane, gx);
-    }
   };
+  const T* src[R];
+  int to[R];
+  float gx[R];
   const int pad = block - (row_blocks - kPadBlocks);
   if (pad >= 0) {
     if (tid == 0 && pad == 0) a.count[0] = before;
     const int end = (before + kPad - 1) / kPad * kPad;
-    for (int q = 0; q < kPackRows / 4; ++q) {
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
       const int i = before + pad * kPackRows + q * 4 + wave;
       if (i < end && lane == 0) {
         a.target[i] = -1;
         if (a.dloss) a.g[i] = a.lse2[i] = 0.0f;
       }
-      if (i < end) pack(static_cast<const T*>(a.X), i, 0, 1.0f);
+      src[q] = static_cast<const T*>(a.X), to[q] = i < end ? i : -1, gx[q] = 1.0f;
     }
+    pack(src, to, 0, gx);
     return;
   }
   const int mine = n0 + lane;
@@ -402,23 +429,75 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
     if (mine_on) {
       a.row[at] = mine;
       a.target[at] = a.t ? -1 : static_cast<int32_t>(a.ids[mine]);
-      if (a.dloss) {
-        const float g = a.dloss[mine] * a.dscale;
-        a.g[at] = in_d(mine, g);
-        if (kParts<T> == 1) a.gx[at] = in_x(mine, g);
-        a.lse2[at] = a.lse[mine] * kLog2e;
-      }
+      if (a.dloss) a.lse2[at] = a.lse[mine] * kLog2e;
     }
     a.inv[mine] = mine_on ? at : -1;
   }
 #pragma unroll
-  for (int q = 0; q < kPackRows / 4; ++q) {
+  for (int q = 0; q < R; ++q) {
     const int r = q * 4 + wave;
-    if (!((b >> r) & 1)) continue;
-    const int at = before + __popcll(b & ((1ull << r) - 1));
-    const float gx = a.Xg ? in_x(n0 + r, a.dloss[n0 + r] * a.dscale) : 1.0f;
-    pack(static_cast<const T*>(a.X) + static_cast<int64_t>(n0 + r) * a.d, at, a.d, gx);
+    const bool there = (b >> r) & 1;
+    src[q] = static_cast<const T*>(a.X) + static_cast<int64_t>(there ? n0 + r : 0) * a.d;
+    to[q] = there ? before + __popcll(b & ((1ull << r) - 1)) : -1;
+    gx[q] = 1.0f;
   }
+  if (a.dloss) {
+    // what D has, but for its factor, at the entry that has most of the weight of a
+    // row's target; 0 where there is none
+    float peak[R] = {};
+    if constexpr (kParts<T> == 1) {
+      constexpr int VN = Vec16<T>::N;
+      const T* e[R];
+      float z[R];
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        const int n = n0 + q * 4 + wave;
+        int64_t id = 0;
+        if (to[q] >= 0 && (!a.t || a.flag[n] >= kPeaked)) {
+          const int64_t at = a.t ? static_cast<int64_t>(n) * a.k + a.flag[n] - kPeaked : n;
+          id = a.ids[at];
+          peak[q] = a.t ? a.q[at] : 1.0f;
+        }
+        e[q] = static_cast<const T*>(a.E) + id * a.d;
+        z[q] = 0.0f;
+      }
+      for (int c = lane * VN; c < a.d; c += 64 * VN) {
+        typename Vec16<T>::type u[R], v[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+          if (peak[q] > 0.0f) u[q] = load_row(src[q], c, a.d), v[q] = load_row(e[q], c, a.d);
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+          if (peak[q] > 0.0f) {
+#pragma unroll
+            for (int i = 0; i < VN; ++i)
+              z[q] = fmaf(static_cast<float>(u[q][i]), static_cast<float>(v[q][i]), z[q]);
+          }
+      }
+#pragma unroll
+      for (int q = 0; q < R; ++q) z[q] = wave_sum(z[q]);
+#pragma unroll
+      for (int q = 0; q < R; ++q)
+        if (peak[q] > 0.0f)
+          peak[q] -= exp2_((z[q] * a.zscale - a.lse[n0 + q * 4 + wave]) * kLog2e);
+    }
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      if (to[q] < 0) continue;
+      const float g = a.dloss[n0 + q * 4 + wave] * a.dscale;
+      float gd = g;
+      if (peak[q] >= kPeakD) {
+        const float t = peak_in_d(g * peak[q]);
+        gd = t / peak[q];
+        gx[q] = g * peak[q] / t;
+      }
+      if (lane == 0) {
+        a.g[to[q]] = gd;
+        if (kParts<T> == 1) a.gx[to[q]] = gx[q];
+      }
+    }
+  }
+  pack(src, to, a.d, gx);
 }
 
 // Distillation: where a packed row's teacher ids lie in the piece, as one bit
@@ -428,7 +507,6 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const VocabArgs a, int r
 // 10 bytes per row and word (4096 rows of 786 words: 20 us, bound by the block's
 // dependent phases).
 constexpr int kMaxWords = 4096;  // 64-column words of a piece
-constexpr int kMaxTop = 1024;    // entries of a teacher's row
 __global__ __launch_bounds__(kThreads) void teacher_ids_kernel(const VocabArgs a) {
   __shared__ uint32_t half[2 * kMaxWords];
   __shared__ uint16_t first[kMaxWords];
@@ -525,7 +603,7 @@ __global__ __launch_bounds__(kThreads) void teacher_ids_kernel(const VocabArgs a
 //
 // What bounds it is the power limit: the logits of 7187 rows x 4096 against 128000
 // columns take 5.4 to 6.2 ms, as the card's power and warmth allow, 1400 to 1220
-// TFLOP/s (6.15 ms with the clock at 1.54 GHz and the matrix cores 78 % busy; the
+// TFLOP/s (6.04 ms with the clock at 1.58 GHz and the matrix cores 78 % busy; the
 // library's product of 8192 x 4096 x 65536: 1446 TFLOP/s at 1.65 GHz, 84 %).
 // Hence the 16x16x32 instructions, which draw less than 32x32x16 (25.0 against 25.7
 // ms for loss and gradients at 8192 x 4096 x 128000), and a K loop that keeps copies,
@@ -534,8 +612,6 @@ __global__ __launch_bounds__(kThreads) void teacher_ids_kernel(const VocabArgs a
 // Copies never leave their arrays: Xp, Ep and D are padded to whole tiles;
 // rows and chunks of E beyond its end are clamped to the last ones, and meet
 // zeros of the other operand.
-
-__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // vmcnt(N) with the other counters left alone.
 template <int N> __device__ __forceinline__ void wait_vm_n() {

@@ -403,10 +403,10 @@ int dpg_vocab_loss(const void* X, const void* E, const int64_t* targets, int64_t
  * with lse as dpg_vocab_loss wrote it. The logits are recomputed in pieces
  * of the vocabulary, and one piece of D is kept at a time (at most 512 MiB,
  * but at least 256 columns). Products run on 16-bit operands and accumulate in
- * fp32: with bf16 inputs D is rounded to bf16 once, without the row's factor (scale
- * tau dloss_n) where one entry of its target has nearly all the weight: dX then
- * takes the factor in fp32, and dE with X, rounded element by element, so that no
- * common error is left on the rows that share a factor; with fp32 inputs operands
+ * fp32: with bf16 inputs D is rounded to bf16 once, scaled so that its entry at the
+ * target loses nothing (a teacher's, if it has at least 3/4 of the weight): dX takes
+ * the rest of the row's factor in fp32, and dE with X, rounded element by element, so
+ * that no common error is left on a row or on rows that share a factor; with fp32 inputs operands
  * are split, for the logits into two fp16 parts after a scale per row (an
  * element keeps 2^-23 of itself or 2^-38 of its row's largest), for dX, dE and
  * the logits of at most 128 rows against a table of 32 MiB or more exactly into

@@ -132,3 +132,35 @@ def test_norms_of_many_tokens_of_equal_size():
     err = abs(float(norm_sq[0]) / want - 1.0)
     print(f"[precision] norms of {T} tokens: {err:.1e}", flush=True)
     assert err <= 1e-5
+
+
+@pytest.mark.parametrize("which", ["vocab", "distill k 1", "distill k 5"])
+@pytest.mark.parametrize("N", [1, 3, 12, 300])
+def test_rows_whose_target_is_no_longer_unlikely(N, which):
+    """Rows of which the model gives the target some percent to a half, so that -(1 - p) is
+    no bf16 value, few enough that nothing averages out; the teacher is sure of its token.
+    dX carries its own rounding, 1.65e-3, and D's of the part that p spreads: 1.8e-3. dE
+    carries its own and that of X times the factor: 2.33e-3, and 2.5e-3 with that part."""
+    import torch
+    import dp_grape_projection_amd as dpg
+    r = np.random.default_rng([61, N])
+    V, d, k = 1000, 512, 5 if which.endswith("5") else 1
+    E = r.standard_normal((V, d)) * 2 / math.sqrt(d)
+    ids = np.stack([r.permutation(V)[:k] for _ in range(N)])
+    x, e = _bf16(r.standard_normal((N, d)) + 1.5 * E[ids[:, 0]]), _bf16(E)
+    X, E = (a.double().cpu().numpy() for a in (x, e))
+    t = r.standard_normal((N, k)).astype(np.float32)
+    t[:, 0] += 9.0
+    g = (0.3 + r.random(N)).astype(np.float32) / 57
+    y, tt, w = torch.from_numpy(ids).cuda(), torch.from_numpy(t).cuda(), torch.from_numpy(g).cuda()
+    if which == "vocab":
+        _, lse = dpg.dpg_vocab_loss(x, e, y[:, 0].contiguous())
+        got = dpg.dpg_vocab_loss_grad(x, e, y[:, 0].contiguous(), lse, w)
+    else:
+        _, lse = dpg.dpg_distill_loss(x, e, y, tt)
+        got = dpg.dpg_distill_loss_grad(x, e, y, tt, lse, w)
+    q = ot.teacher_weights(ids, t, V, 1.0) if k > 1 else np.ones((N, 1))
+    want = ot.target_loss(X, E, ids, q, 1.0, 1.0, g)[2:]
+    rel = [np.linalg.norm(a.double().cpu().numpy() - b) / np.linalg.norm(b) for a, b in zip(got, want)]
+    print(f"[precision] likely targets {which} N {N}: dX {rel[0]:.2e} dE {rel[1]:.2e}", flush=True)
+    assert rel[0] <= 1.8e-3 and rel[1] <= 2.5e-3
