@@ -13,7 +13,7 @@ import functools
 import inspect
 import math
 import os
-from typing import List, Optional, Sequence
+from typing import List, NamedTuple, Optional, Sequence, Union
 
 import torch  # loaded first: libdpg.so then shares torch's HIP runtime
 
@@ -38,6 +38,9 @@ EXPORTED = (
     "dpg_embed", "dpg_embed_workspace_size", "dpg_embed_norms", "dpg_embed_grad",
     "dpg_vocab_loss_workspace_size", "dpg_vocab_loss", "dpg_vocab_loss_grad",
     "dpg_distill_loss_workspace_size", "dpg_distill_loss", "dpg_distill_loss_grad",
+    "dpg_pack_act", "dpg_unpack_act", "dpg_project_layer_packed_workspace_size",
+    "dpg_project_layer_packed", "dpg_gated_workspace_size", "dpg_gated",
+    "dpg_gated_grad_workspace_size", "dpg_gated_grad",
     "dpg_status_string", "dpg_last_error", "dpg_version",
     "dpg_timing_enable", "dpg_timing_read", "dpg_kernel_name",
 )
@@ -139,6 +142,17 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                      vp, vp, sz, vp]
     lib.dpg_distill_loss_grad.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32,
                                           f64, f64, vp, vp, vp, sz, vp]
+    lib.dpg_pack_act.argtypes = [vp, i64, i64, i32, vp, vp, vp]
+    lib.dpg_unpack_act.argtypes = [vp, vp, i64, i64, i32, vp, vp]
+    lib.dpg_project_layer_packed_workspace_size.argtypes = [
+        ctypes.POINTER(LayerGrad), i64, i64, i32, i32, psz]
+    lib.dpg_project_layer_packed.argtypes = [
+        ctypes.POINTER(LayerGrad), vp, vp, i64, i64, i32, i32, u64, u64, vp, vp, vp, sz, vp]
+    lib.dpg_gated_workspace_size.argtypes = [i64, i64, i64, i32, psz]
+    lib.dpg_gated.argtypes = [vp, vp, vp, i64, i64, i64, i32, i32, vp, vp, vp, vp, sz, vp]
+    lib.dpg_gated_grad_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32, psz]
+    lib.dpg_gated_grad.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp,
+                                   vp, vp, vp, vp, vp, sz, vp]
     for name in EXPORTED:
         getattr(lib, name).restype = ctypes.c_int
     lib.dpg_static_scratch_bytes.restype = ctypes.c_size_t
@@ -836,6 +850,272 @@ def dpg_distill_loss_grad(X: torch.Tensor, E: torch.Tensor, top_ids: torch.Tenso
         code, float(scale), float(temperature), _ptr(dX), _ptr(dE), ws.data_ptr(), ws_bytes,
         _stream_handle(stream)))
     return dX, dE
+
+
+def _on_this_device(ref: torch.Tensor):
+    """The library enqueues on the current device's stream."""
+    if ref.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensors on {ref.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+class PackedActivations(NamedTuple):
+    """Activations [..., d] in 8 bits (dpg_pack_act): codes int8 [..., 32 ceil(d / 32)]
+    and exps uint8 [..., ceil(d / 32)], of values that had the type `dtype`."""
+    codes: torch.Tensor
+    exps: torch.Tensor
+    d: int
+    dtype: torch.dtype
+
+    @property
+    def shape(self) -> torch.Size:
+        return torch.Size((*self.codes.shape[:-1], self.d))
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.exps.numel()
+
+
+def _packed_like(rows, d, dtype, device):
+    blocks = -(-d // 32)
+    return PackedActivations(torch.empty((*rows, 32 * blocks), dtype=torch.int8, device=device),
+                             torch.empty((*rows, blocks), dtype=torch.uint8, device=device),
+                             d, dtype)
+
+
+def _require_packed(p: PackedActivations, name: str, shape=None):
+    if not isinstance(p, PackedActivations):
+        raise TypeError(f"{name} must be PackedActivations")
+    _require(p.codes, f"{name}.codes", torch.int8)
+    blocks = -(-p.d // 32)
+    if p.codes.dim() < 1 or int(p.codes.shape[-1]) != 32 * blocks:
+        raise ValueError(f"{name}.codes must be [..., {32 * blocks}] for {p.d} channels")
+    _require(p.exps, f"{name}.exps", torch.uint8, (*p.codes.shape[:-1], blocks))
+    _same_device(p.codes, **{f"{name}.exps": p.exps})
+    if shape is not None and p.shape != torch.Size(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(p.shape)}")
+
+
+def _rows_of(t: torch.Tensor) -> int:
+    """Rows of [..., d] (a width of zero has them all the same)."""
+    return math.prod(t.shape[:-1])
+
+
+@_on_stream
+def dpg_pack_act(X: torch.Tensor, out: Optional[PackedActivations] = None,
+                 stream=None) -> PackedActivations:
+    """X [..., d] (bf16 or fp32) in 8 bits (libdpg): blocks of 32 channels share a power
+    of two, a value is off by at most 2^-7 of its block's largest. A block with an
+    infinity or NaN reads as NaN. out: an earlier result of the same shape to overwrite."""
+    lib = load_library()
+    _require(X, "X")
+    if X.dim() < 1:
+        raise ValueError("X must be [..., d]")
+    _on_this_device(X)
+    d, code = int(X.shape[-1]), _dtype_code(X.dtype)
+    if out is None:
+        out = _packed_like(X.shape[:-1], d, X.dtype, X.device)
+    _require_packed(out, "out", X.shape)
+    if out.dtype != X.dtype:
+        raise TypeError(f"out is of {out.dtype}, X of {X.dtype}")
+    _same_device(X, out=out.codes)
+    N = _rows_of(X)
+    if N:
+        _check(lib, lib.dpg_pack_act(_ptr(X), N, d, code, _ptr(out.codes), _ptr(out.exps),
+                                     _stream_handle(stream)))
+    return out
+
+
+@_on_stream
+def dpg_unpack_act(packed: PackedActivations, dtype: Optional[torch.dtype] = None,
+                   X: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """What dpg_pack_act's codes stand for (libdpg), [..., d] in dtype (default: the type
+    that was packed); exact in bf16 and in fp32."""
+    lib = load_library()
+    _require_packed(packed, "packed")
+    _on_this_device(packed.codes)
+    dtype = dtype or (packed.dtype if X is None else X.dtype)
+    code = _dtype_code(dtype)
+    if X is None:
+        X = torch.empty(packed.shape, dtype=dtype, device=packed.codes.device)
+    _require(X, "X", dtype, packed.shape)
+    _same_device(X, packed=packed.codes)
+    N = _rows_of(X)
+    if N:
+        _check(lib, lib.dpg_unpack_act(_ptr(packed.codes), _ptr(packed.exps), N, packed.d, code,
+                                       _ptr(X), _stream_handle(stream)))
+    return X
+
+
+@_on_stream
+def dpg_project_layer_packed(A: PackedActivations, dY: torch.Tensor, r: int, seed: int,
+                             proj_step: int, layer_id: int, norm_sq: torch.Tensor,
+                             G_hat: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None, stream=None):
+    """dpg_project_layer with the layer's input in 8 bits (libdpg): G_hat[i] =
+    P A_i^T dY_i ([B, r, d_out] fp32) for what A's codes stand for, and norm_sq[i] +=
+    ||G_hat[i]||^2. dY's type is the operands' precision. Returns G_hat."""
+    lib = load_library()
+    _require_packed(A, "A")
+    _require(dY, "dY")
+    if len(A.shape) != 3 or dY.dim() != 3 or tuple(A.shape[:2]) != tuple(dY.shape[:2]):
+        raise ValueError("A and dY must be [B, T, d] with common B, T")
+    B, T = int(dY.shape[0]), int(dY.shape[1])
+    d_out, code = int(dY.shape[2]), _dtype_code(dY.dtype)
+    _on_this_device(dY)
+    if G_hat is None:
+        G_hat = torch.empty((B, r, d_out), dtype=torch.float32, device=dY.device)
+    _require(G_hat, "G_hat", torch.float32, (B, r, d_out))
+    _require(norm_sq, "norm_sq", torch.float32, (B,))
+    _same_device(dY, A=A.codes, G_hat=G_hat, norm_sq=norm_sq)
+    arr = (LayerGrad * 1)()
+    arr[0].d_in, arr[0].d_out, arr[0].layer_id = A.d, d_out, int(layer_id)
+    arr[0].dY = _ptr(dY)
+    need = ctypes.c_size_t(0)
+    _check(lib, lib.dpg_project_layer_packed_workspace_size(arr, B, T, int(r), code,
+                                                            ctypes.byref(need)))
+    ws, ws_bytes = _workspace(need.value, dY.device, workspace)
+    _check(lib, lib.dpg_project_layer_packed(
+        arr, _ptr(A.codes), _ptr(A.exps), B, T, int(r), code, int(seed), int(proj_step),
+        _ptr(G_hat), _ptr(norm_sq), ws.data_ptr(), ws_bytes, _stream_handle(stream)))
+    return G_hat
+
+
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def _act_code(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _gated_args(rows: torch.Tensor, name: str, W_in, W_out):
+    """Checked (N, d, f, dtype code) of rows [..., d], W_in [d, 2 f] and W_out [f, d]."""
+    _require(rows, name)
+    _require(W_in, "W_in", rows.dtype)
+    _require(W_out, "W_out", rows.dtype)
+    if rows.dim() < 1 or W_in.dim() != 2 or W_out.dim() != 2:
+        raise ValueError(f"{name} must be [..., d], W_in [d, 2 f] and W_out [f, d]")
+    d, f = int(rows.shape[-1]), int(W_out.shape[0])
+    if tuple(W_in.shape) != (d, 2 * f) or int(W_out.shape[1]) != d:
+        raise ValueError(f"W_in must be [{d}, 2 f] and W_out [f, {d}], got {tuple(W_in.shape)} "
+                         f"and {tuple(W_out.shape)}")
+    _same_device(rows, W_in=W_in, W_out=W_out)
+    _on_this_device(rows)
+    return _rows_of(rows), d, f, _dtype_code(rows.dtype)
+
+
+@functools.lru_cache(maxsize=1024)
+def _gated_workspace_size(N, d, f, code):
+    lib, need = load_library(), ctypes.c_size_t(0)
+    _check(lib, lib.dpg_gated_workspace_size(N, d, f, code, ctypes.byref(need)))
+    return need.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _gated_grad_workspace_size(N, d, f, code, have_z, weights):
+    lib, need = load_library(), ctypes.c_size_t(0)
+    _check(lib, lib.dpg_gated_grad_workspace_size(N, d, f, code, have_z, weights,
+                                                  ctypes.byref(need)))
+    return need.value
+
+
+@_on_stream
+def dpg_gated(X: torch.Tensor, W_in: torch.Tensor, W_out: torch.Tensor, act: str = "silu",
+              keep: bool = False, Y: Optional[torch.Tensor] = None,
+              Z: Optional[PackedActivations] = None,
+              workspace: Optional[torch.Tensor] = None, stream=None):
+    """The gated feed-forward block (libdpg): Y = (act(X W_gate) * (X W_up)) W_out with
+    W_in = [W_gate | W_up] [d, 2 f], W_out [f, d] and X [..., d] in one type (bf16 or
+    fp32); act "silu", "gelu" or "gelu_tanh". Returns (Y, Z): with keep both projections
+    in 8 bits, PackedActivations of [..., 2, f] for dpg_gated_grad (Z: an earlier one to
+    overwrite), else None."""
+    lib = load_library()
+    N, d, f, code = _gated_args(X, "X", W_in, W_out)
+    act_code = _act_code(act)
+    if Y is None:
+        Y = torch.empty_like(X)
+    _require(Y, "Y", X.dtype, X.shape)
+    if Z is not None and not keep:
+        raise ValueError("Z is given, but keep is not set")
+    if keep:
+        if Z is None:
+            Z = _packed_like((*X.shape[:-1], 2), f, X.dtype, X.device)
+        _require_packed(Z, "Z", (*X.shape[:-1], 2, f))
+        _same_device(X, Z=Z.codes)
+    _same_device(X, Y=Y)
+    if N == 0:
+        return Y, Z
+    ws, ws_bytes = _workspace(_gated_workspace_size(N, d, f, code), X.device, workspace)
+    _check(lib, lib.dpg_gated(_ptr(X), _ptr(W_in), _ptr(W_out), N, d, f, code, act_code, _ptr(Y),
+                              _ptr(Z.codes) if keep else None, _ptr(Z.exps) if keep else None,
+                              ws.data_ptr(), ws_bytes, _stream_handle(stream)))
+    return Y, Z
+
+
+class GatedGrads(NamedTuple):
+    """What dpg_gated_grad returns; None for what was not asked for."""
+    dX: Optional[torch.Tensor]
+    dW_in: Optional[torch.Tensor]
+    dW_out: Optional[torch.Tensor]
+    dZ: Optional[torch.Tensor]   # [..., 2 f]: the gradient of X W_in
+    H: Optional[torch.Tensor]    # [..., f]: what W_out multiplies
+
+
+@_on_stream
+def dpg_gated_grad(dY: torch.Tensor, X: Union[torch.Tensor, PackedActivations, None],
+                   W_in: torch.Tensor, W_out: torch.Tensor, act: str = "silu",
+                   Z: Optional[PackedActivations] = None, need_dX: bool = True,
+                   need_dW=True, need_layers: bool = False,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> GatedGrads:
+    """Gradients of dpg_gated (libdpg) from that of its Y. The projections come from Z,
+    or with Z None are computed again from X. X may be PackedActivations, or None, where
+    Z is given (None: without dW_in). need_dW: one truth value, or one for W_in and one
+    for W_out. need_layers: dZ and H, which with X and dY are what the private step takes
+    of the block's two linear layers."""
+    lib = load_library()
+    N, d, f, code = _gated_args(dY, "dY", W_in, W_out)
+    act_code = _act_code(act)
+    w_in, w_out = need_dW if isinstance(need_dW, (tuple, list)) else (need_dW, need_dW)
+    if Z is not None:
+        _require_packed(Z, "Z", (*dY.shape[:-1], 2, f))
+        _same_device(dY, Z=Z.codes)
+    x = codes = exps = None
+    if isinstance(X, PackedActivations):
+        if Z is None:
+            raise ValueError("Z is needed with X in 8 bits")
+        _require_packed(X, "X", dY.shape)
+        _same_device(dY, X=X.codes)
+        codes, exps = X.codes, X.exps
+    elif X is not None:
+        _require(X, "X", dY.dtype, dY.shape)
+        _same_device(dY, X=X)
+        x = X
+    elif Z is None or w_in:
+        raise ValueError("X is needed: for dW_in, and wherever Z is not given")
+    if not (need_dX or w_in or w_out or need_layers):
+        raise ValueError("need_dX, need_dW or need_layers must be set")
+    lead = dY.shape[:-1]
+    out = GatedGrads(
+        torch.empty_like(dY) if need_dX else None,
+        torch.empty_like(W_in) if w_in else None,
+        torch.empty_like(W_out) if w_out else None,
+        torch.empty((*lead, 2 * f), dtype=dY.dtype, device=dY.device) if need_layers else None,
+        torch.empty((*lead, f), dtype=dY.dtype, device=dY.device) if need_layers else None)
+    if N == 0:
+        for dW in (out.dW_in, out.dW_out):
+            if dW is not None:
+                dW.zero_()
+        return out
+    need = _gated_grad_workspace_size(N, d, f, code, int(Z is not None), int(w_in or w_out))
+    ws, ws_bytes = _workspace(need, dY.device, workspace)
+    _check(lib, lib.dpg_gated_grad(
+        _ptr(x), _ptr(codes), _ptr(exps), _ptr(W_in), _ptr(W_out),
+        None if Z is None else _ptr(Z.codes), None if Z is None else _ptr(Z.exps), _ptr(dY), N, d,
+        f, code, act_code, _ptr(out.dX), _ptr(out.dW_in), _ptr(out.dW_out), _ptr(out.dZ),
+        _ptr(out.H), ws.data_ptr(), ws_bytes, _stream_handle(stream)))
+    return out
 
 
 class PreparedStep:

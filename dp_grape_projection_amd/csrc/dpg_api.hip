@@ -1189,6 +1189,37 @@ int dpg_project_layer(const dpg_layer_grad* layer, int64_t B, int64_t T,
                       nullptr, workspace, workspace_bytes, stream, G_hat, norm_sq);
 }
 
+int dpg_project_layer_packed_workspace_size(const dpg_layer_grad* layer, int64_t B, int64_t T,
+                                            int32_t r, int32_t dtype, size_t* bytes) {
+  if (const int st = dpg_project_workspace_size(layer, 1, B, T, r, dtype, bytes)) return st;
+  *bytes = align_up(*bytes) + align_up(static_cast<size_t>(B * T * layer->d_in) * elem_size(dtype));
+  return DPG_OK;
+}
+
+// A is read back at the workspace's end, where the projection takes it from.
+int dpg_project_layer_packed(const dpg_layer_grad* layer, const int8_t* codes,
+                             const uint8_t* exps, int64_t B, int64_t T, int32_t r, int32_t dtype,
+                             uint64_t seed, uint64_t proj_step, float* G_hat, float* norm_sq,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  size_t need = 0;
+  if (const int st = dpg_project_layer_packed_workspace_size(layer, B, T, r, dtype, &need)) return st;
+  if (!G_hat) return fail(DPG_ERR_INVALID_ARG, "G_hat is NULL");
+  if (!norm_sq) return fail(DPG_ERR_INVALID_ARG, "norm_sq is NULL");
+  if (!codes || !exps || !layer->dY) return fail(DPG_ERR_INVALID_ARG, "NULL data pointer");
+  if (const int st = check_seed_steps(1, proj_step)) return st;
+  if (const int st = check_workspace(workspace, workspace_bytes, need)) return st;
+  const size_t a_bytes = align_up(static_cast<size_t>(B * T * layer->d_in) * elem_size(dtype));
+  dpg_layer_grad L = *layer;
+  char* const A = static_cast<char*>(workspace) + (need - a_bytes);
+  L.A = A;
+  if (launch_unpack8(codes, exps, B * T, L.d_in, A, dtype == DPG_BF16, L.d_in,
+                     static_cast<hipStream_t>(stream)) != hipSuccess)
+    return fail(DPG_ERR_HIP, "unpack: launch failed");
+  return project_impl(&L, 1, B, T, r, dtype, 1.0, 0.0, seed, 1, proj_step, nullptr, workspace,
+                      need - a_bytes, stream, G_hat, norm_sq);
+}
+
 int dpg_clip_workspace_size(int64_t B, size_t* bytes) {
   g_last_error.clear();
   if (!bytes) return fail(DPG_ERR_INVALID_ARG, "bytes is NULL");

@@ -1,0 +1,816 @@
+// The gated feed-forward block and its gradients: dpg_gated, dpg_gated_grad.
+//
+//   G = X W_gate, U = X W_up   (W_in = [W_gate | W_up], [d][2f])
+//   H = act(G) * U             [N][f]
+//   Y = H W_out                [N][d]
+//   dH = dY W_out^T, dU = dH act(G), dG = dH U act'(G)
+//   dX = [dG | dU] W_in^T, dW_in = X^T [dG | dU], dW_out = H^T dY
+//
+// All products run in the tiles of dpg_tile.hpp. The first computes both projections:
+// a wave's 16-column blocks are half of the gate's and half of the same columns of the
+// up projection, so that a lane holds G and U of the same places and H leaves the tile
+// without either being stored. What the backward pass keeps of them is the caller's
+// choice: their 8-bit form (dpg_act8.hpp), written by the same epilogue, or nothing, in
+// which case they are computed again, in fp32, a run of rows at a time. dH never leaves
+// its tile either: the epilogue of its product reads G and U and writes dG, dU and H.
+//
+// Inside, Z = [G | U] and dZ have their halves fq columns apart, f rounded up to 8, so
+// that both halves' rows can be copied 16 bytes at a time; what lies between and after
+// is zero, and so are dZ's and H's rows from N up to whole tiles, which the weights'
+// gradients sum over.
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "dpg.h"
+#include "dpg_act8.hpp"
+#include "dpg_device.hpp"
+#include "dpg_internal.hpp"
+#include "dpg_tile.hpp"
+
+namespace dpg {
+namespace {
+
+constexpr int kPad = 256;  // rows of dZ and H are padded to whole tiles
+constexpr float kLog2e = 1.4426950408889634f;
+
+// A matrix as operands of 16 bits see it: rows of ld elements, in one or three parts.
+struct Mat {
+  const bf16* p;
+  int64_t ld;
+  int64_t part;   // elements between the parts
+  int32_t rows, cols;
+};
+
+struct GatedArgs {
+  Mat x, w_in, w_out, dy, h, dz;
+  int32_t N, d, f, fq, act;
+  int32_t ldh;          // f rounded up to 64
+  int32_t fp;           // f rounded up to 32: the codes of one half of a row of Z
+  int32_t np;           // rows of dz and h that are written (N, or whole tiles)
+  int8_t* codes;        // [N][2][fp], or null
+  uint8_t* exps;        // [N][2][fp / 32]
+  float* zf;            // [N][2][ldh] Z in fp32, where it is computed again
+  void* dz_out;         // [N][2f] the caller's dZ where h and dz are not his own
+  void* h_out;          // [N][f]
+};
+
+// ------------------------------------------------------------ activations --
+
+__device__ __forceinline__ float exp_(float x) { return exp2_(x * kLog2e); }
+__device__ __forceinline__ float sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + exp_(-x));
+}
+
+// act(x), and with it act'(x). The library's exponential and reciprocal instructions
+// (1 ulp) serve all of them.
+template <int ACT>
+__device__ __forceinline__ float act_of(float x) {
+  if constexpr (ACT == DPG_ACT_SILU) {
+    return x * sigmoid(x);
+  } else if constexpr (ACT == DPG_ACT_GELU) {
+    return 0.5f * x * (1.0f + erff(x * 0.70710678f));
+  } else {
+    // (1 + tanh t) / 2 = sigmoid(2 t)
+    return x * sigmoid(1.5957691216f * (x + 0.044715f * x * x * x));
+  }
+}
+template <int ACT>
+__device__ __forceinline__ float act_of(float x, float& slope) {
+  if constexpr (ACT == DPG_ACT_SILU) {
+    const float s = sigmoid(x);
+    slope = s * (1.0f + x * (1.0f - s));
+    return x * s;
+  } else if constexpr (ACT == DPG_ACT_GELU) {
+    const float c = 0.5f * (1.0f + erff(x * 0.70710678f));
+    slope = c + x * (0.3989422804f * exp_(-0.5f * x * x));
+    return x * c;
+  } else {
+    // beyond 20 the sigmoid is 0 or 1 and the slope's second term nothing
+    const float y = __builtin_amdgcn_fmed3f(x, -20.0f, 20.0f);
+    const float s = sigmoid(1.5957691216f * (y + 0.044715f * y * y * y));
+    slope = s + y * s * (1.0f - s) * (1.5957691216f * (1.0f + 0.134145f * y * y));
+    return x * s;
+  }
+}
+template <class F>
+__device__ __forceinline__ void with_act(int act, F fn) {
+  if (act == DPG_ACT_SILU) fn(std::integral_constant<int, DPG_ACT_SILU>{});
+  else if (act == DPG_ACT_GELU) fn(std::integral_constant<int, DPG_ACT_GELU>{});
+  else fn(std::integral_constant<int, DPG_ACT_GELU_TANH>{});
+}
+
+// ---------------------------------------------------------------- packing --
+
+// Copies of matrices as parts, zero-padded to rows of whole K steps: up to four of them
+// in one launch, a wave a row (or half of one, whose halves go fq columns apart).
+struct PackJob {
+  const void* src;   // [rows][halves][cols]
+  bf16* dst;         // rows of ld elements
+  int64_t ld, part;
+  int32_t rows, cols, halves, fq;
+  int64_t wave0;     // first wave of the job
+};
+struct PackArgs {
+  PackJob job[4];
+  int32_t n;
+  int64_t waves;
+};
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void pack_mat_kernel(const PackArgs a) {
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (w >= a.waves) return;
+  int j = 0;
+  while (j + 1 < a.n && w >= a.job[j + 1].wave0) ++j;
+  const PackJob& o = a.job[j];
+  const int64_t at = w - o.wave0, r = at / o.halves;
+  const int h = static_cast<int>(at - r * o.halves);
+  const int width = h + 1 < o.halves ? o.fq : static_cast<int>(o.ld) - h * o.fq;
+  pack_row(static_cast<const T*>(o.src) + at * o.cols, o.dst + r * o.ld + h * o.fq, o.cols, width,
+           o.part, threadIdx.x & 63);
+}
+
+// --------------------------------------------------------------- products --
+
+__device__ __forceinline__ Operand rows_of(const Mat& m, int r0, int k0) {
+  return rows_operand(m.p + static_cast<int64_t>(r0) * m.ld + k0, m.ld, m.part, m.rows - r0, m.cols - k0);
+}
+__device__ __forceinline__ Operand kmajor_of(const Mat& m, int k0, int c0) {
+  return rows_operand(m.p + static_cast<int64_t>(k0) * m.ld + c0, m.ld, m.part, m.rows - k0, m.cols - c0);
+}
+
+// What the tile of both projections leaves: H for the next product, with or without the
+// 8-bit form of G and U, or G and U alone in fp32.
+enum { kH = 0, kHAndCodes = 1, kZ = 2 };
+
+// A tile of G and U: TILE / 2 columns of each by TILE rows.
+template <class G, int PARTS, int OUT>
+__global__ __launch_bounds__(G::kThreads, G::kBlocks) void gate_up_kernel(const GatedArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
+  constexpr int kCols = G::kTile / 2, kHB = G::kMB / 2;  // columns of H; blocks of a half
+  int mt, nt;
+  if (!tile_of_block(blockIdx.x, (a.ldh + kCols - 1) / kCols, (a.N + G::kTile - 1) / G::kTile, mt, nt))
+    return;
+  const int c0 = mt * kCols, r0 = nt * G::kTile;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
+  // (a tile of padding alone computes the last columns, and writes zeros)
+  Operand w = kmajor_of(a.w_in, 0, min(c0, a.fq - 8));
+  w.cols = a.fq - min(c0, a.fq - 8);
+  w.half = a.fq;
+  typename G::Acc acc;
+  tile_product<G, PARTS, true, false>(w, rows_of(a.x, r0, 0), (a.d + kStepK - 1) / kStepK, smem, acc);
+  const int cw = c0 + 16 * kHB * wm + 4 * kq;  // the lane's first column
+  if constexpr (OUT == kZ) {
+#pragma unroll
+    for (int nb = 0; nb < G::kNB; ++nb) {
+      const int r = r0 + G::kWaveN * wn + 16 * nb + r16;
+      if (r >= a.N) continue;
+#pragma unroll
+      for (int mb = 0; mb < G::kMB; ++mb) {
+        const int h = mb / kHB, c = cw + 16 * (mb % kHB);
+        if (c < a.ldh)
+          *reinterpret_cast<f32x4*>(a.zf + (2 * static_cast<int64_t>(r) + h) * a.ldh + c) = acc.v[mb][nb];
+      }
+    }
+    return;
+  } else {
+    typedef Strip<G, kCols> S;
+    constexpr int kCodeRow = 2 * kCols;  // bytes: the codes of G, then of U
+    static_assert(S::kBytes + S::kRows * kCodeRow <= G::kLds, "the strips fit");
+    char* const codes = smem + S::kBytes;
+    const int q = 16 * wn + r16;
+    bf16* const h_dst = const_cast<bf16*>(a.h.p) + static_cast<int64_t>(r0) * a.h.ld + c0;
+#pragma unroll
+    for (int nb = 0; nb < G::kNB; ++nb) {
+      __syncthreads();
+      const int r = r0 + G::kWaveN * wn + 16 * nb + r16;
+      if constexpr (OUT == kHAndCodes) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int p = 0; p < kHB / 2; ++p) {
+            f32x4 v[2];
+            uint32_t top = 0;
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float x = acc.v[kHB * h + 2 * p + m][nb][i];
+                v[m][i] = cw + 32 * p + 16 * m + i < a.f ? x : 0.0f;
+                top = max(top, magnitude_bits(v[m][i]));
+              }
+            top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16, 64)));
+            top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, 64)));
+            const uint32_t b = exponent8(top);
+            const int c = 16 * kHB * wm + 32 * p;  // of the block in the tile
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+              *reinterpret_cast<uint32_t*>(codes + q * kCodeRow + h * kCols + c + 16 * m + 4 * kq) =
+                  codes8(v[m][0], v[m][1], v[m][2], v[m][3], b);
+            if (kq == 0 && r < a.N && c0 + c < a.fp)
+              a.exps[(2 * static_cast<int64_t>(r) + h) * (a.fp / kBlock8) + (c0 + c) / kBlock8] =
+                  static_cast<uint8_t>(b);
+          }
+      }
+      f32x4 hv[kHB];
+      with_act(a.act, [&](auto act) {
+#pragma unroll
+        for (int mb = 0; mb < kHB; ++mb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            hv[mb][i] = cw + 16 * mb + i < a.f
+                            ? act_of<decltype(act)::value>(acc.v[mb][nb][i]) * acc.v[kHB + mb][nb][i]
+                            : 0.0f;
+      });
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part) {
+        if (part) __syncthreads();
+#pragma unroll
+        for (int mb = 0; mb < kHB; ++mb) {
+          Vec4<bf16>::type v;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[i] = PARTS == 1 ? from_float<bf16>(hv[mb][i]) : take_part(hv[mb], i);
+          S::put(smem, q, 16 * kHB * wm + 16 * mb + 4 * kq, v);
+        }
+        __syncthreads();
+        S::write(smem, h_dst + part * a.h.part, a.h.ld, nb, a.N - r0, a.ldh - c0);
+      }
+      if constexpr (OUT == kHAndCodes) {
+        constexpr int kChunks = kCodeRow / 16, kAll = S::kRows * kChunks;
+        typedef uint32_t any_u32x4 __attribute__((ext_vector_type(4), aligned(1)));
+#pragma unroll
+        for (int i = 0; i < (kAll + G::kThreads - 1) / G::kThreads; ++i) {
+          const int at = i * G::kThreads + tid, row = at / kChunks, c = at % kChunks;
+          const int h = c / (kChunks / 2), cb = c % (kChunks / 2) * 16;
+          const int64_t r = r0 + S::row(row, nb);
+          if (at < kAll && r < a.N && c0 + cb < a.fp)
+            *reinterpret_cast<any_u32x4*>(a.codes + (2 * r + h) * a.fp + c0 + cb) =
+                *reinterpret_cast<const any_u32x4*>(codes + row * kCodeRow + c * 16);
+        }
+      }
+    }
+  }
+}
+
+// A tile of dH, from which dG, dU and H follow; CODES: G and U are read from their 8-bit
+// form, else from zf.
+template <class G, int PARTS, bool CODES>
+__global__ __launch_bounds__(G::kThreads, G::kBlocks) void gate_up_grad_kernel(const GatedArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
+  int mt, nt;
+  // columns up to the end of the padding of H and of dZ's second half
+  const int cols = max(a.ldh, static_cast<int>(a.dz.ld) - a.fq);
+  if (!tile_of_block(blockIdx.x, (cols + G::kTile - 1) / G::kTile, (a.np + G::kTile - 1) / G::kTile, mt, nt))
+    return;
+  const int c0 = mt * G::kTile, r0 = nt * G::kTile;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
+  typename G::Acc acc;
+  // (rows and columns past the last compute the last ones again, and are written as zero)
+  tile_product<G, PARTS, false, false>(rows_of(a.w_out, min(c0, a.f - 1), 0),
+                                       rows_of(a.dy, min(r0, a.N - 1), 0),
+                                       (a.d + kStepK - 1) / kStepK, smem, acc);
+  typedef Strip<G, G::kTile> S;
+  static_assert(3 * S::kBytes <= G::kLds, "the strips fit");
+  const int q = 16 * wn + r16;
+  const int cw = c0 + G::kWaveM * wm + 4 * kq;  // the lane's first column
+  bf16* const dz = const_cast<bf16*>(a.dz.p) + static_cast<int64_t>(r0) * a.dz.ld + c0;
+  bf16* const h = const_cast<bf16*>(a.h.p) + static_cast<int64_t>(r0) * a.h.ld + c0;
+#pragma unroll
+  for (int nb = 0; nb < G::kNB; ++nb) {
+    const int r = r0 + G::kWaveN * wn + 16 * nb + r16;
+    const int64_t rz = 2 * static_cast<int64_t>(min(r, a.N - 1));
+    f32x4 dg[G::kMB], du[G::kMB], hv[G::kMB];
+    // G into dg and U into du first
+    if constexpr (CODES) {
+      uint32_t code[2][G::kMB], e[2][G::kMB / 2];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+        for (int mb = 0; mb < G::kMB; ++mb) {
+          const int c = min(cw + 16 * mb, a.fp - 4);
+          code[hf][mb] = *reinterpret_cast<const uint32_t*>(a.codes + (rz + hf) * a.fp + c);
+        }
+#pragma unroll
+        for (int p = 0; p < G::kMB / 2; ++p)
+          e[hf][p] = a.exps[(rz + hf) * (a.fp / kBlock8) + min(cw + 32 * p, a.fp - 4) / kBlock8];
+      }
+#pragma unroll
+      for (int mb = 0; mb < G::kMB; ++mb) {
+        const float sg = step8(e[0][mb / 2]), su = step8(e[1][mb / 2]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dg[mb][i] = value8(code[0][mb], i, sg);
+          du[mb][i] = value8(code[1][mb], i, su);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int mb = 0; mb < G::kMB; ++mb) {
+        const int c = min(cw + 16 * mb, a.ldh - 4);
+        dg[mb] = *reinterpret_cast<const f32x4*>(a.zf + rz * a.ldh + c);
+        du[mb] = *reinterpret_cast<const f32x4*>(a.zf + (rz + 1) * a.ldh + c);
+      }
+    }
+    with_act(a.act, [&](auto act) {
+#pragma unroll
+      for (int mb = 0; mb < G::kMB; ++mb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool there = cw + 16 * mb + i < a.f && r < a.N;
+          const float dh = acc.v[mb][nb][i], u = du[mb][i];
+          float slope;
+          const float v = act_of<decltype(act)::value>(dg[mb][i], slope);
+          hv[mb][i] = there ? v * u : 0.0f;
+          du[mb][i] = there ? dh * v : 0.0f;
+          dg[mb][i] = there ? dh * u * slope : 0.0f;
+        }
+    });
+    if constexpr (PARTS == 3) {
+      // the caller's own, in fp32
+      if (r < a.N) {
+#pragma unroll
+        for (int mb = 0; mb < G::kMB; ++mb) {
+          const int c = cw + 16 * mb;
+          if (c >= a.f) continue;
+          float* z = static_cast<float*>(a.dz_out);
+          if (z) {
+            z += rz * a.f + c;
+            store_row(z, a.f - c, dg[mb]);
+            store_row(z + a.f, a.f - c, du[mb]);
+          }
+          if (a.h_out)
+            store_row(static_cast<float*>(a.h_out) + static_cast<int64_t>(r) * a.f + c, a.f - c, hv[mb]);
+        }
+      }
+    }
+#pragma unroll
+    for (int part = 0; part < PARTS; ++part) {
+      __syncthreads();
+      auto stage = [&](char* s, f32x4 (&x)[G::kMB]) {
+#pragma unroll
+        for (int mb = 0; mb < G::kMB; ++mb) {
+          Vec4<bf16>::type v;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = PARTS == 1 ? from_float<bf16>(x[mb][i]) : take_part(x[mb], i);
+          S::put(s, q, G::kWaveM * wm + 16 * mb + 4 * kq, v);
+        }
+      };
+      stage(smem, dg);
+      stage(smem + S::kBytes, du);
+      stage(smem + 2 * S::kBytes, hv);
+      __syncthreads();
+      const int64_t off = part * a.dz.part;
+      S::write(smem, dz + off, a.dz.ld, nb, a.np - r0, a.fq - c0);
+      S::write(smem + S::kBytes, dz + off + a.fq, a.dz.ld, nb, a.np - r0,
+               static_cast<int>(a.dz.ld) - a.fq - c0);
+      S::write(smem + 2 * S::kBytes, h + part * a.h.part, a.h.ld, nb, a.np - r0,
+               static_cast<int>(a.h.ld) - c0);
+      if constexpr (PARTS == 1) {
+        if (a.dz_out) {
+          bf16* z = static_cast<bf16*>(a.dz_out) + 2 * static_cast<int64_t>(r0) * a.f + c0;
+          S::write(smem, z, 2 * static_cast<int64_t>(a.f), nb, a.N - r0, a.f - c0);
+          S::write(smem + S::kBytes, z + a.f, 2 * static_cast<int64_t>(a.f), nb, a.N - r0, a.f - c0);
+        }
+        if (a.h_out)
+          S::write(smem + 2 * S::kBytes, static_cast<bf16*>(a.h_out) + static_cast<int64_t>(r0) * a.f + c0,
+                   a.f, nb, a.N - r0, a.f - c0);
+      }
+    }
+  }
+}
+
+// out[n][h m + c] = sum_k b[n][k] a[h][c][k] for the halves h of A (its columns or rows
+// half apart): one product, or a part of its K whose sums are added afterwards.
+struct ProductArgs {
+  Mat a, b;
+  int32_t half, halves;
+  int32_t m, n;        // columns of a half of the output, rows
+  int32_t steps;       // of K
+  int32_t splits;
+  void* out;           // [n][halves m]
+  float* acc;          // [splits][np][ldm], where splits > 1
+  int32_t np, ldm;     // rows, and halves times m rounded up to 64
+};
+
+template <class G, typename T, bool KA, bool KB>
+__global__ __launch_bounds__(G::kThreads, G::kBlocks) void product_kernel(const ProductArgs a) {
+  constexpr int PARTS = kParts<T>;
+  __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
+  const int mh = (a.m + G::kTile - 1) / G::kTile, nh = (a.n + G::kTile - 1) / G::kTile;
+  int mt, nt;
+  if (!tile_of_block(blockIdx.x, mh * a.halves, nh * a.splits, mt, nt)) return;
+  const int split = nt / nh, half = mt / mh;
+  const int m0 = (mt - half * mh) * G::kTile, n0 = (nt - split * nh) * G::kTile;
+  const int per = (a.steps + a.splits - 1) / a.splits;
+  const int k0 = min(a.steps, split * per), k1 = min(a.steps, k0 + per), kk = k0 * kStepK;
+  Operand oa, ob;
+  if constexpr (KA) {
+    oa = kmajor_of(a.a, kk, half * a.half + m0);
+  } else {
+    oa = rows_of(a.a, m0, kk);
+  }
+  if constexpr (KB) ob = kmajor_of(a.b, kk, n0);
+  else ob = rows_of(a.b, n0, kk);
+  typename G::Acc acc;
+  tile_product<G, PARTS, KA, KB>(oa, ob, k1 - k0, smem, acc);
+  if (a.splits > 1) {
+    const int c = half * (a.ldm / a.halves) + m0;
+    add_tile<G>(a.acc + (static_cast<int64_t>(split) * a.np + n0) * a.ldm + c, a.ldm,
+                a.ldm / a.halves - m0, false, acc);
+    return;
+  }
+  const int64_t ld = static_cast<int64_t>(a.halves) * a.m;
+  T* dst = static_cast<T*>(a.out) + n0 * ld + half * a.m + m0;
+  const int n_rows = a.n - n0, n_cols = a.m - m0;
+  if constexpr (PARTS == 1) {
+    write_tile<G>(smem, dst, ld, n_rows, n_cols,
+                  [&](int nb, int mb, int i) { return from_float<bf16>(acc.v[mb][nb][i]); });
+  } else {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
+#pragma unroll
+    for (int nb = 0; nb < G::kNB; ++nb) {
+      const int r = G::kWaveN * wn + 16 * nb + r16;
+      if (r >= n_rows) continue;
+#pragma unroll
+      for (int mb = 0; mb < G::kMB; ++mb) {
+        const int c = G::kWaveM * wm + 16 * mb + 4 * kq;
+        if (c < n_cols) store_row(dst + r * ld + c, n_cols - c, acc.v[mb][nb]);
+      }
+    }
+  }
+}
+
+// Sums over the splits of K, rounded: four columns a thread.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void splits_kernel(const ProductArgs a) {
+  const int quads = (a.m + 3) / 4;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t rh = t / quads;
+  if (rh >= static_cast<int64_t>(a.n) * a.halves) return;
+  const int64_t n = rh / a.halves;
+  const int h = static_cast<int>(rh - n * a.halves), c = static_cast<int>(t - rh * quads) * 4;
+  const float* src = a.acc + n * a.ldm + h * (a.ldm / a.halves) + c;
+  const int64_t stride = static_cast<int64_t>(a.np) * a.ldm;
+  f32x4 x = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < a.splits; s0 += 8) {  // (eight loads in flight)
+    f32x4 y[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      y[u] = *reinterpret_cast<const f32x4*>(src + min(s0 + u, a.splits - 1) * stride);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (s0 + u < a.splits) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] += y[u][i];
+      }
+  }
+  T* p = static_cast<T*>(a.out) + rh * a.m + c;
+  if (c + 4 <= a.m && is_aligned(p, 4 * sizeof(T))) {
+    store4<T>(p, x[0], x[1], x[2], x[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < a.m) p[i] = from_float<T>(x[i]);
+  }
+}
+
+// ------------------------------------------------------------------- host --
+
+// Tiles of a launch of m x n outputs without splits: as for the losses' logits.
+enum Tile { kBig, kSmall, kTiny };
+Tile tile_for(int64_t m, int64_t n, int64_t cols_of_tile_halved) {
+  auto tiles = [&](int64_t tile) { return ceil_div(m, tile / cols_of_tile_halved) * ceil_div(n, tile); };
+  if (big_tiles(tiles(BigTile::kTile), n)) return kBig;
+  return tiles(SmallTile::kTile) > 256 ? kSmall : kTiny;
+}
+template <class F>
+void with_tile(Tile t, F fn) {
+  if (t == kBig) fn(BigTile());
+  else if (t == kSmall) fn(SmallTile());
+  else fn(TinyTile());
+}
+
+// Tiles and splits of a product of m x n outputs over `steps` steps of K.
+struct Choice {
+  Tile tile;
+  int32_t splits;
+};
+Choice choose(int64_t m, int64_t n, int64_t steps, int combos) {
+  const Split s = choose_split(m, n, steps, combos, false);
+  return {s.big ? kBig : kSmall, s.splits};
+}
+
+struct Call {
+  int64_t N, d, f;
+  int32_t dtype, act;
+};
+
+int check_call_shape(const Call& c) {
+  if (c.N < 1 || c.N > (1ll << 22)) return fail(DPG_ERR_INVALID_ARG, "N must be in [1, 2^22]");
+  if (c.d < 1 || c.d > (1ll << 16)) return fail(DPG_ERR_INVALID_ARG, "d must be in [1, 2^16]");
+  if (c.f < 1 || c.f > (1ll << 16)) return fail(DPG_ERR_INVALID_ARG, "f must be in [1, 2^16]");
+  if (c.dtype != DPG_FP32 && c.dtype != DPG_BF16) return fail(DPG_ERR_INVALID_ARG, "unknown dtype");
+  return DPG_OK;
+}
+int check_call(const Call& c) {
+  if (const int st = check_call_shape(c)) return st;
+  if (c.act != DPG_ACT_SILU && c.act != DPG_ACT_GELU && c.act != DPG_ACT_GELU_TANH)
+    return fail(DPG_ERR_INVALID_ARG, "unknown activation");
+  return DPG_OK;
+}
+
+// Rows whose Z in fp32 is kept at a time where it is computed again.
+constexpr int64_t kZBytes = 256ll << 20;
+
+// Where everything lies in the workspace. Copies of the operands are planned whatever
+// their alignment, since a size depends on shapes alone.
+struct Plan {
+  int64_t parts, ldx, ldh, fq, ldz, np, fp, z_rows = 0;
+  Choice y{}, x{}, wi{}, wo{};
+  size_t off_x, off_wi, off_wo, off_dy, off_h, off_dz = 0, off_zf = 0, off_x8 = 0, off_acc, total;
+};
+
+size_t acc_bytes(const Choice& c, int64_t halves, int64_t m, int64_t n) {
+  return c.splits > 1 ? c.splits * round_up(n, kPad) * halves * round_up(m, 64) * 4 : 0;
+}
+
+Plan plan_gated(const Call& c, bool grad, bool again, bool weights) {
+  Plan p;
+  p.parts = c.dtype == DPG_BF16 ? 1 : 3;
+  p.ldx = round_up(c.d, kStepK);
+  p.ldh = round_up(c.f, kStepK);
+  p.fq = round_up(c.f, 8);
+  p.ldz = round_up(2 * p.fq, kStepK);
+  p.fp = round_up(c.f, kBlock8);
+  p.np = round_up(c.N, kPad);
+  const int combos = p.parts == 1 ? 1 : Combos<3>::n;
+  size_t off = 0, acc = 0;
+  auto take = [&](int64_t elems, int64_t size) {
+    const size_t at = off;
+    off += align_up(static_cast<size_t>(elems * size));
+    return at;
+  };
+  p.off_x = take(p.parts * c.N * p.ldx, 2);
+  p.off_wi = take(p.parts * c.d * p.ldz, 2);
+  p.off_wo = take(p.parts * c.f * p.ldx, 2);
+  p.off_dy = take(grad ? p.parts * c.N * p.ldx : 0, 2);
+  p.off_h = take(p.parts * p.np * p.ldh, 2);
+  if (!grad) {
+    p.y = choose(c.d, c.N, p.ldh / kStepK, combos);
+    acc = acc_bytes(p.y, 1, c.d, c.N);
+  } else {
+    p.off_dz = take(p.parts * p.np * p.ldz, 2);
+    if (again) {
+      p.z_rows = std::min(p.np, std::max<int64_t>(kPad, kZBytes / (p.ldh * 8) / kPad * kPad));
+      p.off_zf = take(p.z_rows * 2 * p.ldh, 4);
+    }
+    p.x = choose(c.d, c.N, p.ldz / kStepK, combos);
+    acc = acc_bytes(p.x, 1, c.d, c.N);
+    if (weights) {
+      p.wi = choose(2 * round_up(c.f, SmallTile::kTile), c.d, p.np / kStepK, combos);
+      p.wo = choose(c.d, c.f, p.np / kStepK, combos);
+      acc = std::max({acc, acc_bytes(p.wi, 2, c.f, c.d), acc_bytes(p.wo, 1, c.d, c.f)});
+      p.off_x8 = take(c.N * p.ldx, c.dtype == DPG_BF16 ? 2 : 4);
+    }
+  }
+  p.off_acc = take(static_cast<int64_t>(acc), 1);
+  p.total = off;
+  return p;
+}
+
+// The operands of one call: the caller's matrices where their rows can be copied 16
+// bytes at a time and K needs no padding, else copies in the workspace.
+struct Operands {
+  PackArgs pack{};
+  const Plan& p;
+  char* ws;
+  bool bf16_in;
+
+  Mat bring(const void* src, int64_t rows, int64_t cols, int64_t halves, int64_t half, int64_t ld,
+            size_t off, bool direct) {
+    if (direct)
+      return {static_cast<const bf16*>(src), halves * cols, 0, static_cast<int32_t>(rows),
+              static_cast<int32_t>(halves * cols)};
+    PackJob& j = pack.job[pack.n++];
+    j = {src, reinterpret_cast<bf16*>(ws + off), ld, rows * ld, static_cast<int32_t>(rows),
+         static_cast<int32_t>(cols), static_cast<int32_t>(halves), static_cast<int32_t>(half), pack.waves};
+    pack.waves += rows * halves;
+    return {j.dst, ld, j.part, static_cast<int32_t>(rows), static_cast<int32_t>(ld)};
+  }
+  void launch(hipStream_t s) {
+    if (!pack.n) return;
+    const dim3 grid(static_cast<unsigned>(ceil_div(pack.waves, 4)));
+    if (bf16_in) hipLaunchKernelGGL(pack_mat_kernel<bf16>, grid, dim3(kThreads), 0, s, pack);
+    else hipLaunchKernelGGL(pack_mat_kernel<float>, grid, dim3(kThreads), 0, s, pack);
+    pack.n = 0, pack.waves = 0;
+  }
+};
+
+GatedArgs make_args(const Call& c, const Plan& p) {
+  GatedArgs a{};
+  a.N = static_cast<int32_t>(c.N), a.d = static_cast<int32_t>(c.d), a.f = static_cast<int32_t>(c.f);
+  a.fq = static_cast<int32_t>(p.fq), a.act = c.act;
+  a.ldh = static_cast<int32_t>(p.ldh), a.fp = static_cast<int32_t>(p.fp);
+  return a;
+}
+
+template <typename T, int OUT>
+void launch_gate_up(const GatedArgs& a, hipStream_t s) {
+  with_tile(tile_for(a.ldh, a.N, 2), [&](auto g) {
+    typedef decltype(g) G;
+    hipLaunchKernelGGL((gate_up_kernel<G, kParts<T>, OUT>),
+                       tile_grid(ceil_div(a.ldh, G::kTile / 2), ceil_div(a.N, G::kTile)),
+                       dim3(G::kThreads), 0, s, a);
+  });
+}
+
+// out = B A^T in one of the three orders of the operands.
+template <typename T, bool KA, bool KB>
+void launch_product(const Choice& c, const Mat& ma, const Mat& mb, int64_t half, int64_t halves,
+                    int64_t m, int64_t n, int64_t k, void* out, float* acc, hipStream_t s) {
+  ProductArgs a{};
+  a.a = ma, a.b = mb;
+  a.half = static_cast<int32_t>(half), a.halves = static_cast<int32_t>(halves);
+  a.m = static_cast<int32_t>(m), a.n = static_cast<int32_t>(n);
+  a.steps = static_cast<int32_t>(ceil_div(k, kStepK));
+  a.splits = c.splits;
+  a.out = out, a.acc = acc;
+  a.np = static_cast<int32_t>(round_up(n, kPad));
+  a.ldm = static_cast<int32_t>(halves * round_up(m, 64));
+  with_tile(c.tile, [&](auto g) {
+    typedef decltype(g) G;
+    hipLaunchKernelGGL((product_kernel<G, T, KA, KB>),
+                       tile_grid(ceil_div(m, G::kTile) * halves, ceil_div(n, G::kTile) * c.splits),
+                       dim3(G::kThreads), 0, s, a);
+  });
+  if (c.splits > 1)
+    hipLaunchKernelGGL(splits_kernel<T>, dim3(blocks_of(n * halves * ceil_div(m, 4), kThreads)),
+                       dim3(kThreads), 0, s, a);
+}
+
+template <typename T>
+int run_forward(const Call& c, const Plan& p, const void* X, const void* W_in, const void* W_out,
+                void* Y, int8_t* codes, uint8_t* exps, char* ws, hipStream_t s) {
+  constexpr bool kHalf = sizeof(T) == 2;
+  GatedArgs a = make_args(c, p);
+  Operands o{{}, p, ws, kHalf};
+  a.x = o.bring(X, c.N, c.d, 1, 0, p.ldx, p.off_x, kHalf && c.d % kStepK == 0 && aligned(X, 16));
+  a.w_in = o.bring(W_in, c.d, c.f, 2, p.fq, p.ldz, p.off_wi, kHalf && c.f % 8 == 0 && aligned(W_in, 16));
+  a.w_out = o.bring(W_out, c.f, c.d, 1, 0, p.ldx, p.off_wo, kHalf && c.d % 8 == 0 && aligned(W_out, 16));
+  o.launch(s);
+  a.h = {reinterpret_cast<bf16*>(ws + p.off_h), p.ldh, p.np * p.ldh, a.N, a.ldh};
+  a.codes = codes, a.exps = exps;
+  if (codes) launch_gate_up<T, kHAndCodes>(a, s);
+  else launch_gate_up<T, kH>(a, s);
+  launch_product<T, true, false>(p.y, a.w_out, a.h, 0, 1, c.d, c.N, p.ldh, Y,
+                                 reinterpret_cast<float*>(ws + p.off_acc), s);
+  return check_launch("gated block");
+}
+
+struct Grads {
+  void *dX, *dW_in, *dW_out, *dZ, *H;
+};
+
+template <typename T>
+int run_backward(const Call& c, const Plan& p, const void* X, const int8_t* x_codes,
+                 const uint8_t* x_exps, const void* W_in, const void* W_out, const int8_t* z_codes,
+                 const uint8_t* z_exps, const void* dY, const Grads& g, char* ws, hipStream_t s) {
+  constexpr bool kHalf = sizeof(T) == 2;
+  GatedArgs a = make_args(c, p);
+  Operands o{{}, p, ws, kHalf};
+  const bool again = !z_codes;
+  if (x_codes && g.dW_in) {
+    if (launch_unpack8(x_codes, x_exps, c.N, c.d, ws + p.off_x8, kHalf, p.ldx, s) != hipSuccess)
+      return fail(DPG_ERR_HIP, "gated gradient: launch failed");
+    if (kHalf) {
+      a.x = {reinterpret_cast<bf16*>(ws + p.off_x8), p.ldx, 0, a.N, static_cast<int32_t>(p.ldx)};
+    } else {
+      a.x = o.bring(ws + p.off_x8, c.N, p.ldx, 1, 0, p.ldx, p.off_x, false);
+    }
+  } else if (again || g.dW_in) {
+    a.x = o.bring(X, c.N, c.d, 1, 0, p.ldx, p.off_x, kHalf && c.d % kStepK == 0 && aligned(X, 16));
+  }
+  if (again || g.dX)
+    a.w_in = o.bring(W_in, c.d, c.f, 2, p.fq, p.ldz, p.off_wi, kHalf && c.f % 8 == 0 && aligned(W_in, 16));
+  a.w_out = o.bring(W_out, c.f, c.d, 1, 0, p.ldx, p.off_wo, kHalf && c.d % 8 == 0 && aligned(W_out, 16));
+  a.dy = o.bring(dY, c.N, c.d, 1, 0, p.ldx, p.off_dy, kHalf && c.d % kStepK == 0 && aligned(dY, 16));
+  o.launch(s);
+  // dZ and H go straight to the caller where they need no padding
+  const bool whole = kHalf && c.N % kStepK == 0;
+  const bool own_z = whole && g.dZ && p.ldz == 2 * c.f && aligned(g.dZ, 16);
+  const bool own_h = whole && g.H && p.ldh == c.f && aligned(g.H, 16);
+  bf16* const dz = own_z ? static_cast<bf16*>(g.dZ) : reinterpret_cast<bf16*>(ws + p.off_dz);
+  bf16* const h = own_h ? static_cast<bf16*>(g.H) : reinterpret_cast<bf16*>(ws + p.off_h);
+  // (rows past N are written only where both have them)
+  a.np = static_cast<int32_t>(own_z || own_h ? c.N : p.np);
+  a.dz = {dz, p.ldz, p.np * p.ldz, a.np, static_cast<int32_t>(p.ldz)};
+  a.h = {h, p.ldh, p.np * p.ldh, a.np, static_cast<int32_t>(p.ldh)};
+  a.codes = const_cast<int8_t*>(z_codes), a.exps = const_cast<uint8_t*>(z_exps);
+  a.zf = reinterpret_cast<float*>(ws + p.off_zf);
+  a.dz_out = own_z ? nullptr : g.dZ;
+  a.h_out = own_h ? nullptr : g.H;
+  const int64_t run = again ? p.z_rows : c.N;
+  for (int64_t n0 = 0; n0 < c.N; n0 += run) {
+    GatedArgs b = a;
+    b.N = static_cast<int32_t>(std::min(run, c.N - n0));
+    b.np = static_cast<int32_t>(std::min<int64_t>(run, a.np - n0));
+    auto from = [&](Mat& m) { m.p += n0 * m.ld, m.rows -= static_cast<int32_t>(n0); };
+    if (again) from(b.x);
+    from(b.dy), from(b.dz), from(b.h);
+    if (!again) b.np = a.np;
+    if (b.dz_out) b.dz_out = static_cast<T*>(b.dz_out) + n0 * 2 * c.f;
+    if (b.h_out) b.h_out = static_cast<T*>(b.h_out) + n0 * c.f;
+    if (again) launch_gate_up<T, kZ>(b, s);
+    const int64_t cols = std::max<int64_t>(p.ldh, p.ldz - p.fq);
+    with_tile(tile_for(cols, b.np, 1), [&](auto t) {
+      typedef decltype(t) G;
+      const dim3 grid = tile_grid(ceil_div(cols, G::kTile), ceil_div(b.np, G::kTile)), bl(G::kThreads);
+      if (again) hipLaunchKernelGGL((gate_up_grad_kernel<G, kParts<T>, false>), grid, bl, 0, s, b);
+      else hipLaunchKernelGGL((gate_up_grad_kernel<G, kParts<T>, true>), grid, bl, 0, s, b);
+    });
+  }
+  float* acc = reinterpret_cast<float*>(ws + p.off_acc);
+  if (g.dX)
+    launch_product<T, false, false>(p.x, a.w_in, a.dz, 0, 1, c.d, c.N, p.ldz, g.dX, acc, s);
+  // (K runs over the rows that are written: whole steps, zero from N on)
+  const int64_t k = round_up(c.N, kStepK);
+  if (g.dW_in)
+    launch_product<T, true, true>(p.wi, a.dz, a.x, p.fq, 2, c.f, c.d, k, g.dW_in, acc, s);
+  if (g.dW_out)
+    launch_product<T, true, true>(p.wo, a.dy, a.h, 0, 1, c.d, c.f, k, g.dW_out, acc, s);
+  return check_launch("gated gradient");
+}
+
+}  // namespace
+}  // namespace dpg
+
+using namespace dpg;
+
+extern "C" {
+
+int dpg_gated_workspace_size(int64_t N, int64_t d, int64_t f, int32_t dtype, size_t* bytes) {
+  record_error(DPG_OK, "");
+  if (!bytes) return fail(DPG_ERR_INVALID_ARG, "bytes is NULL");
+  const Call c{N, d, f, dtype, DPG_ACT_SILU};
+  if (const int st = check_call_shape(c)) return st;
+  *bytes = plan_gated(c, false, false, false).total;
+  return DPG_OK;
+}
+
+int dpg_gated(const void* X, const void* W_in, const void* W_out, int64_t N, int64_t d, int64_t f,
+              int32_t dtype, int32_t act, void* Y, int8_t* z_codes, uint8_t* z_exps, void* workspace,
+              size_t workspace_bytes, void* stream) {
+  record_error(DPG_OK, "");
+  const Call c{N, d, f, dtype, act};
+  if (const int st = check_call(c)) return st;
+  if (!X || !W_in || !W_out || !Y) return fail(DPG_ERR_INVALID_ARG, "NULL data pointer");
+  if (!z_codes != !z_exps) return fail(DPG_ERR_INVALID_ARG, "z_codes and z_exps go together");
+  const Plan p = plan_gated(c, false, false, false);
+  if (const int st = check_ws(workspace, workspace_bytes, p.total)) return st;
+  char* ws = static_cast<char*>(workspace);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return dtype == DPG_BF16 ? run_forward<bf16>(c, p, X, W_in, W_out, Y, z_codes, z_exps, ws, s)
+                           : run_forward<float>(c, p, X, W_in, W_out, Y, z_codes, z_exps, ws, s);
+}
+
+int dpg_gated_grad_workspace_size(int64_t N, int64_t d, int64_t f, int32_t dtype, int32_t have_z,
+                                  int32_t weights, size_t* bytes) {
+  record_error(DPG_OK, "");
+  if (!bytes) return fail(DPG_ERR_INVALID_ARG, "bytes is NULL");
+  const Call c{N, d, f, dtype, DPG_ACT_SILU};
+  if (const int st = check_call_shape(c)) return st;
+  *bytes = plan_gated(c, true, !have_z, weights != 0).total;
+  return DPG_OK;
+}
+
+int dpg_gated_grad(const void* X, const int8_t* x_codes, const uint8_t* x_exps, const void* W_in,
+                   const void* W_out, const int8_t* z_codes, const uint8_t* z_exps, const void* dY,
+                   int64_t N, int64_t d, int64_t f, int32_t dtype, int32_t act, void* dX,
+                   void* dW_in, void* dW_out, void* dZ, void* H, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  record_error(DPG_OK, "");
+  const Call c{N, d, f, dtype, act};
+  if (const int st = check_call(c)) return st;
+  if (!W_in || !W_out || !dY) return fail(DPG_ERR_INVALID_ARG, "NULL data pointer");
+  if (!x_codes != !x_exps) return fail(DPG_ERR_INVALID_ARG, "x_codes and x_exps go together");
+  if (!z_codes != !z_exps) return fail(DPG_ERR_INVALID_ARG, "z_codes and z_exps go together");
+  if (X && x_codes) return fail(DPG_ERR_INVALID_ARG, "X and its 8-bit form are both given");
+  if (!z_codes && !X) return fail(DPG_ERR_INVALID_ARG, "the projections need X, or their 8-bit form");
+  if (dW_in && !X && !x_codes) return fail(DPG_ERR_INVALID_ARG, "dW_in needs X, or its 8-bit form");
+  if (!dX && !dW_in && !dW_out && !dZ && !H) return fail(DPG_ERR_INVALID_ARG, "no output is asked for");
+  const Plan p = plan_gated(c, true, !z_codes, dW_in || dW_out);
+  if (const int st = check_ws(workspace, workspace_bytes, p.total)) return st;
+  char* ws = static_cast<char*>(workspace);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const Grads g{dX, dW_in, dW_out, dZ, H};
+  return dtype == DPG_BF16
+             ? run_backward<bf16>(c, p, X, x_codes, x_exps, W_in, W_out, z_codes, z_exps, dY, g, ws, s)
+             : run_backward<float>(c, p, X, x_codes, x_exps, W_in, W_out, z_codes, z_exps, dY, g, ws, s);
+}
+
+}  // extern "C"

@@ -279,5 +279,11 @@ hipError_t launch_philox_normals(uint32_t k0, uint32_t k1, uint32_t layer_id,
                                  uint32_t step_word, uint32_t tag,
                                  uint32_t start, uint32_t n, float* z_out,
                                  uint32_t* words_out, hipStream_t s);
+// Activations in 8 bits (dpg_act8.hip): X [N][d] packed, and read back into rows of
+// ldo elements (>= d, zero from d on).
+hipError_t launch_pack8(const void* X, bool bf16_in, int64_t N, int64_t d, int8_t* codes,
+                        uint8_t* exps, hipStream_t s);
+hipError_t launch_unpack8(const int8_t* codes, const uint8_t* exps, int64_t N, int64_t d,
+                          void* X, bool bf16_out, int64_t ldo, hipStream_t s);
 
 }  // namespace dpg

@@ -198,11 +198,15 @@ typedef Geometry<128, 4, 4> SmallTile;
 // 22 and 20.5; 80 x 1024 x 50304, 393: 19 and 25).
 typedef Geometry<64, 4, 1> TinyTile;
 
-// Slot of 16-byte chunk c in row k of a k-major tile. Of the
+// Slot of 16-byte chunk c in row k of a k-major tile of CHUNKS chunks a row. Of the
 // transposing read, 16 lanes take 32 bytes from each of four rows, and the
 // next 16 the same eight rows further on: the slots of these eight pieces
-// differ in their 64 banks.
-__device__ __forceinline__ int kslot(int k, int c) { return c ^ (4 * (k & 3)) ^ (2 * ((k >> 3) & 1)); }
+// differ in their 64 banks (rows of 8 chunks fill half of them, so that two rows do).
+template <int CHUNKS>
+__device__ __forceinline__ int kslot(int k, int c) {
+  if constexpr (CHUNKS == 8) return c ^ (2 * ((k >> 1) & 1)) ^ (4 * ((k >> 3) & 1));
+  else return c ^ (4 * (k & 3)) ^ (2 * ((k >> 3) & 1));
+}
 
 struct Operand {
   const bf16* base;     // first row of the tile (rows) or of K (k-major)
@@ -210,6 +214,8 @@ struct Operand {
   int64_t part_stride;  // elements between the bf16 parts
   int rows;             // rows: rows there are from base; k-major: rows of K
   int cols;             // rows: elements of K in a row; k-major: columns from base
+  int64_t half = 0;     // k-major: where not 0, a wave's columns are half from base
+                        // on and half from base + half on (elements, a multiple of 8)
 };
 
 // The direct copies of one operand: G::kCopies of 1 KiB a wave and step.
@@ -239,11 +245,19 @@ struct Copier {
       if constexpr (!KMAJOR) off[q] = static_cast<uint32_t>(min(g * 8 + (lane >> 3), o.rows - 1)) * ldb;
       else off[q] = static_cast<uint32_t>(g * kRowsPerCopy + lane / kChunks);
     }
-    if constexpr (!KMAJOR)
+    if constexpr (!KMAJOR) {
       chunk = static_cast<uint32_t>((lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7)) * 16u;
-    else
-      chunk = static_cast<uint32_t>(
-          min(kslot(kRowsPerCopy * wave + lane / kChunks, lane % kChunks), o.cols / 8 - 1)) * 16u;
+    } else {
+      const int c = kslot<kChunks>(kRowsPerCopy * wave + lane / kChunks, lane % kChunks);
+      chunk = static_cast<uint32_t>(min(c, o.cols / 8 - 1)) * 16u;
+      if (o.half) {
+        // a wave's first chunks from one half, the others from the other
+        constexpr int kSpan = G::kWaveM / 8;
+        const int at = c / kSpan * (kSpan / 2) + c % (kSpan / 2);
+        chunk = static_cast<uint32_t>(min(at, o.cols / 8 - 1)) * 16u +
+                (c % kSpan < kSpan / 2 ? 0u : static_cast<uint32_t>(o.half) * 2u);
+      }
+    }
     last = KMAJOR ? static_cast<uint32_t>(o.rows - 1) : static_cast<uint32_t>(o.cols) * 2u - 16u;
   }
   // copies q0 .. q1 - 1 of the current K step (kStepK columns or rows)
@@ -285,7 +299,7 @@ __device__ __forceinline__ bf16x8 tile_frag(const char* tile, int kk, int c0, in
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int k = 32 * kk + 8 * kq + 4 * i + (q16 >> 2);
-      h[i] = lds_read_tr(tile + k * (2 * G::kTile) + kslot(k, n >> 3) * 16 + (n & 7) * 2);
+      h[i] = lds_read_tr(tile + k * (2 * G::kTile) + kslot<G::kTile / 8>(k, n >> 3) * 16 + (n & 7) * 2);
     }
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
   } else {
@@ -475,6 +489,35 @@ __device__ __forceinline__ void write_tile(char* smem, bf16* dst, int64_t ld, in
       store_row(dst + static_cast<int64_t>(r) * ld + c * 8, n_cols - c * 8, v);
   }
 }
+
+// 16 rows of a wave, kept in LDS as COLS bytes-pairs each, and written in whole rows: the
+// form of an epilogue that has several arrays to write and works through a tile one nb
+// at a time. Row q of a strip is the tile's row kWaveN (q / 16) + 16 nb + q % 16; 16-byte
+// chunk c of it sits in slot c ^ (q mod the chunks of a row).
+template <class G, int COLS>
+struct Strip {
+  static constexpr int kRows = 16 * G::kWavesN, kChunks = COLS / 8, kBytes = kRows * COLS * 2;
+  __device__ __forceinline__ static int row(int q, int nb) {
+    return G::kWaveN * (q >> 4) + 16 * nb + (q & 15);
+  }
+  // columns c .. c + 3 of row q
+  __device__ __forceinline__ static void put(char* s, int q, int c, Vec4<bf16>::type v) {
+    *reinterpret_cast<Vec4<bf16>::type*>(s + q * (2 * COLS) + ((c >> 3) ^ (q % kChunks)) * 16 +
+                                         (c & 4) * 2) = v;
+  }
+  // Rows below n_rows, columns below n_cols, of what dst is the tile's first row of.
+  __device__ __forceinline__ static void write(const char* s, bf16* dst, int64_t ld, int nb,
+                                               int n_rows, int n_cols) {
+#pragma unroll
+    for (int i = 0; i < (kRows * kChunks + G::kThreads - 1) / G::kThreads; ++i) {
+      const int at = i * G::kThreads + static_cast<int>(threadIdx.x);
+      const int q = at / kChunks, c = at % kChunks, r = row(q, nb);
+      if (at >= kRows * kChunks || r >= n_rows || c * 8 >= n_cols) continue;
+      const bf16x8 v = lds_read_b128(s + q * (2 * COLS) + (c ^ (q % kChunks)) * 16);
+      store_row(dst + static_cast<int64_t>(r) * ld + c * 8, n_cols - c * 8, v);
+    }
+  }
+};
 
 // Writes a tile to rows of ld floats, or adds it to them: an accumulator value's N
 // is its row, its M its column. Columns >= n_cols (a multiple of 16) stay.

@@ -77,6 +77,9 @@ class GrapeOptimizer:
     sum takes the clip factors (dpg_embed_grad) and noise sigma C Z from the
     stream of its own layer id, and the update is plain:
     table -= table_lr * (sum_i s_i g_i + sigma C Z) / B.
+    checkpoint: "int8" keeps every layer's input in 8 bits between its forward and its
+    backward pass (dpg_pack_act, 1.03 bytes an element); the per-sample gradients are then
+    those of the kept inputs, clip and noise as before.
     g is the lookup's gradient alone. The losses' [V, d] tables are not clipped here:
     keep them frozen, as a table that serves both ends is for its part in the loss."""
 
@@ -84,7 +87,9 @@ class GrapeOptimizer:
                  sigma: float, seed: int, lr: float, beta1: float = 0.9,
                  beta2: float = 0.999, eps: float = 1e-8, proj_period: int = 1,
                  keep_inputs: bool = False, embeddings: Sequence = (),
-                 table_lr: Optional[float] = None):
+                 table_lr: Optional[float] = None, checkpoint: Optional[str] = None):
+        if checkpoint not in (None, "int8"):
+            raise ValueError(f"checkpoint must be None or \"int8\", got {checkpoint!r}")
         self.layers: List[ProjectedLinear] = list(layers)
         self.embeddings = list(embeddings)
         self.table_lr = lr if table_lr is None else table_lr
@@ -98,6 +103,7 @@ class GrapeOptimizer:
         self.lr, self.beta1, self.beta2, self.eps = lr, beta1, beta2, eps
         self.proj_period = int(proj_period)
         self.keep_inputs = keep_inputs
+        self.checkpoint = checkpoint
         dev = self.layers[0].W.device
         self.m = [torch.zeros((self.r, l.d_out), device=dev) for l in self.layers]
         self.v = [torch.zeros((self.r, l.d_out), device=dev) for l in self.layers]
@@ -163,29 +169,31 @@ class GrapeOptimizer:
             G.add_(Z.view(V, d), alpha=self.sigma * self.clip_C)
         return G
 
+    def _begin_layer(self, x: torch.Tensor) -> None:
+        self._begin(int(x.shape[0]), x.device)
+        if self.dtype is None:
+            self.dtype = x.dtype
+
     def _capture(self, layer: ProjectedLinear, x: torch.Tensor, y: torch.Tensor):
         A = x.detach().contiguous()
-        B = int(A.shape[0])
-        self._begin(B, A.device)
-        if self.dtype is None:
-            self.dtype = A.dtype
+        self._begin_layer(A)
+        if self.checkpoint == "int8":
+            A = _b.dpg_pack_act(A)
+        y.register_hook(lambda g: self._project(layer, A, g.detach().contiguous()))
 
-        def on_grad(g: torch.Tensor):
-            if layer.layer_id in self._done:
-                raise RuntimeError(f"layer {layer.layer_id} ran twice in one step")
-            dY = g.detach().contiguous()
-            buf = self.G_hat.get(layer.layer_id)
-            if buf is not None and tuple(buf.shape) != (B, self.r, layer.d_out):
-                buf = None
-            self.G_hat[layer.layer_id] = _b.dpg_project_layer(
-                A, dY, self.r, self.seed, self.proj_step, layer.layer_id,
-                self.norm_sq, G_hat=buf)
-            self._done.add(layer.layer_id)
-            if self.keep_inputs:
-                self.inputs[layer.layer_id] = (A, dY)
-            return None
-
-        y.register_hook(on_grad)
+    def _project(self, layer: ProjectedLinear, A, dY: torch.Tensor) -> None:
+        if layer.layer_id in self._done:
+            raise RuntimeError(f"layer {layer.layer_id} ran twice in one step")
+        buf = self.G_hat.get(layer.layer_id)
+        if buf is not None and tuple(buf.shape) != (int(dY.shape[0]), self.r, layer.d_out):
+            buf = None
+        project = (_b.dpg_project_layer_packed if isinstance(A, _b.PackedActivations)
+                   else _b.dpg_project_layer)
+        self.G_hat[layer.layer_id] = project(A, dY, self.r, self.seed, self.proj_step,
+                                             layer.layer_id, self.norm_sq, G_hat=buf)
+        self._done.add(layer.layer_id)
+        if self.keep_inputs:
+            self.inputs[layer.layer_id] = (A, dY)
 
     def step(self) -> None:
         missing = [l.layer_id for l in self.layers + self.embeddings

@@ -450,6 +450,94 @@ int dpg_distill_loss_grad(const void* X, const void* E, const int64_t* top_ids,
                           double scale, double temperature, void* dX, void* dE,
                           void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * What a backward pass keeps: activations in 8 bits, and the projection of a layer's
+ * per-sample gradients from them.
+ */
+
+/*
+ * dpg_pack_act / dpg_unpack_act: rows X [N][d] in 8 bits and back. Blocks of 32
+ * consecutive channels of a row (the last one of a row may be short) share a power of
+ * two: with b = max(7, the exponent field that the block's largest magnitude has as
+ * fp32), a value becomes the integer
+ *     q = clamp(round(x 2^(133 - b)), -127, 127)      (ties to even)
+ * and stands for q 2^(b - 133): off by at most 2^-7 of the block's largest magnitude
+ * (half that, but for fp32 values within the last 2^-8 below a power of two). A block
+ * with an infinity or NaN gets b = 255 and reads as NaN. What a code stands for is
+ * exact in bf16 as in fp32.
+ *   codes  device [N][32 ceil(d / 32)] int8, zero from d on
+ *   exps   device [N][ceil(d / 32)] uint8, the b of every block
+ * dtype is X's type. Limits: N in [1, 2^30], d in [1, 2^20]. No workspace.
+ */
+int dpg_pack_act(const void* X, int64_t N, int64_t d, int32_t dtype, int8_t* codes,
+                 uint8_t* exps, void* stream);
+int dpg_unpack_act(const int8_t* codes, const uint8_t* exps, int64_t N, int64_t d,
+                   int32_t dtype, void* X, void* stream);
+
+/*
+ * dpg_project_layer_packed_workspace_size / dpg_project_layer_packed:
+ * dpg_project_layer with the layer's input A given in the form of dpg_pack_act, as
+ * [B T] rows of d_in: the result is that of dpg_project_layer on what the codes stand
+ * for. dtype is dY's type and the operands' precision; layer->A is not read.
+ */
+int dpg_project_layer_packed_workspace_size(const dpg_layer_grad* layer, int64_t B, int64_t T,
+                                            int32_t r, int32_t dtype, size_t* bytes);
+int dpg_project_layer_packed(const dpg_layer_grad* layer, const int8_t* codes,
+                             const uint8_t* exps, int64_t B, int64_t T, int32_t r, int32_t dtype,
+                             uint64_t seed, uint64_t proj_step, float* G_hat, float* norm_sq,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The gated feed-forward block, two linear layers of the private step: W_in =
+ * [W_gate | W_up] of shape [d][2f], and W_out [f][d],
+ *     Z = [G | U] = X W_in,  H = act(G) * U,  Y = H W_out.
+ */
+typedef enum {
+  DPG_ACT_SILU,      /* 0: x / (1 + e^-x) */
+  DPG_ACT_GELU,      /* 1: x Phi(x), Phi the normal distribution function */
+  DPG_ACT_GELU_TANH  /* 2: x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2 */
+} dpg_act;
+
+/*
+ * dpg_gated: Y [N][d] of rows X [N][d], everything in dtype. G and U are not stored
+ * unless their 8-bit form is asked for (both or neither of z_codes and z_exps), for
+ * dpg_gated_grad: rows (n, half) of f channels, as dpg_pack_act writes them,
+ *   z_codes  device out [N][2][32 ceil(f / 32)],  z_exps  [N][2][ceil(f / 32)].
+ * Products run on 16-bit operands and accumulate in fp32: with bf16, H is rounded once;
+ * with fp32, operands are split exactly into three bf16 parts, so that products keep
+ * fp32's accuracy. G and U are never rounded before the activation. An infinity in an
+ * operand can make NaN of all that it meets. Results do not vary from run to run.
+ *   workspace  dpg_gated_workspace_size(...) bytes, 256-byte aligned
+ * Limits: N in [1, 2^22], d and f in [1, 2^16].
+ */
+int dpg_gated_workspace_size(int64_t N, int64_t d, int64_t f, int32_t dtype, size_t* bytes);
+int dpg_gated(const void* X, const void* W_in, const void* W_out, int64_t N, int64_t d,
+              int64_t f, int32_t dtype, int32_t act, void* Y, int8_t* z_codes,
+              uint8_t* z_exps, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dpg_gated_grad: with dY [N][d] the gradient of Y,
+ *     dH = dY W_out^T,  dU = dH * act(G),  dG = dH * U * act'(G),  dZ = [dG | dU]
+ *     dX = dZ W_in^T [N][d],  dW_in = X^T dZ [d][2f],  dW_out = H^T dY [f][d]
+ * each output NULL where it is not needed (one at least is). For the private step, whose
+ * weights take no gradient of their own: dZ [N][2f] is the dY of the layer W_in, whose A
+ * is X, and H [N][f] the A of the layer W_out.
+ *   G and U   from z_codes and z_exps as dpg_gated wrote them; both NULL: they are
+ *             computed again from X, without a rounding
+ *   X         [N][d], for dW_in and for computing G and U again; or, for dW_in,
+ *             x_codes and x_exps, its form of dpg_pack_act (then X is NULL)
+ * With bf16, dZ and H are rounded once, before the products that they enter; dH is not.
+ *   workspace  dpg_gated_grad_workspace_size(...) bytes, 256-byte aligned; have_z:
+ *              z_codes is given, weights: dW_in or dW_out is asked for
+ */
+int dpg_gated_grad_workspace_size(int64_t N, int64_t d, int64_t f, int32_t dtype,
+                                  int32_t have_z, int32_t weights, size_t* bytes);
+int dpg_gated_grad(const void* X, const int8_t* x_codes, const uint8_t* x_exps,
+                   const void* W_in, const void* W_out, const int8_t* z_codes,
+                   const uint8_t* z_exps, const void* dY, int64_t N, int64_t d, int64_t f,
+                   int32_t dtype, int32_t act, void* dX, void* dW_in, void* dW_out, void* dZ,
+                   void* H, void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * dpg_philox_normals: the random stream both calls draw from, exposed so it
  * can be checked on its own. For e in [start, start + n):
