@@ -28,15 +28,16 @@ __device__ __forceinline__ float step8(uint32_t b) {
 __device__ __forceinline__ uint32_t magnitude_bits(float x) {
   return __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu;
 }
-// The codes of four values, the first in the lowest byte; zero where b = 255.
+// The codes of four values, the first in the lowest byte; zero where b = 255. Adding 1.5
+// 2^23 to x in steps rounds it to an integer, ties to even, whose low byte is the code.
 __device__ __forceinline__ uint32_t codes8(float x0, float x1, float x2, float x3, uint32_t b) {
-  const float s = to_steps8(b);
+  const float s = to_steps8(b), top = 127.0f * step8(b);
   auto code = [&](float x) {
-    const float q = __builtin_amdgcn_fmed3f(rintf(x * s), -127.0f, 127.0f);
-    return static_cast<uint32_t>(static_cast<int>(q)) & 0xFFu;
+    return __builtin_bit_cast(uint32_t, fmaf(__builtin_amdgcn_fmed3f(x, -top, top), s, 12582912.0f));
   };
-  if (b == 255u) return 0u;
-  return code(x0) | code(x1) << 8 | code(x2) << 16 | code(x3) << 24;
+  const uint32_t lo = __builtin_amdgcn_perm(code(x1), code(x0), 0x0c0c0400u),
+                 hi = __builtin_amdgcn_perm(code(x3), code(x2), 0x04000c0cu);
+  return b == 255u ? 0u : lo | hi;
 }
 // The value of byte i of `codes`.
 __device__ __forceinline__ float value8(uint32_t codes, int i, float step) {

@@ -140,6 +140,53 @@ __device__ __forceinline__ Operand kmajor_of(const Mat& m, int k0, int c0) {
   return rows_operand(m.p + static_cast<int64_t>(k0) * m.ld + c0, m.ld, m.part, m.rows - k0, m.cols - c0);
 }
 
+typedef uint32_t any_u32x4 __attribute__((ext_vector_type(4), aligned(1)));
+
+// The codes of a lane's eight values of a block of 32 columns, which four lanes share.
+__device__ __forceinline__ void codes_of_block(const f32x4& x, const f32x4& y, uint32_t& cx,
+                                               uint32_t& cy, uint32_t& b) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max(top, max(magnitude_bits(x[i]), magnitude_bits(y[i])));
+  uint32_t other = top;
+  swap16(top, other);
+  top = max(top, other);
+  other = top;
+  swap32(top, other);
+  b = exponent8(max(top, other));
+  cx = codes8(x[0], x[1], x[2], x[3], b);
+  cy = codes8(y[0], y[1], y[2], y[3], b);
+}
+
+// MB blocks of 16 columns of one row, rounded (or, of several parts, the next one taken
+// off x), to dst of n columns.
+template <int MB, int PARTS>
+__device__ __forceinline__ void store_strip(bf16* dst, f32x4 (&x)[MB], int kq, bool row, int n) {
+#pragma unroll
+  for (int p = 0; p < MB / 2; ++p) {
+    Vec4<bf16>::type v[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[m][i] = PARTS == 1 ? from_float<bf16>(x[2 * p + m][i]) : take_part(x[2 * p + m], i);
+    const bf16x8 w = pair_cols(v[0], v[1]);
+    const int c = 32 * p + pair_col(kq);
+    if (row && c < n) store_row(dst + c, n - c, w);
+  }
+}
+
+// fn(std::integral_constant<int, 0>) .. <N - 1>: unrolled whatever its size, so that the
+// accumulators it indexes stay in registers.
+template <class F, int... I>
+__device__ __forceinline__ void each_of(F fn, std::integer_sequence<int, I...>) {
+  (fn(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F fn) {
+  each_of(fn, std::make_integer_sequence<int, N>{});
+}
+
 // What the tile of both projections leaves: H for the next product, with or without the
 // 8-bit form of G and U, or G and U alone in fp32.
 enum { kH = 0, kHAndCodes = 1, kZ = 2 };
@@ -161,7 +208,7 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void gate_up_kernel(const 
   w.half = a.fq;
   typename G::Acc acc;
   tile_product<G, PARTS, true, false>(w, rows_of(a.x, r0, 0), (a.d + kStepK - 1) / kStepK, smem, acc);
-  const int cw = c0 + 16 * kHB * wm + 4 * kq;  // the lane's first column
+  const int cw = c0 + 16 * kHB * wm;  // the wave's first column of H
   if constexpr (OUT == kZ) {
 #pragma unroll
     for (int nb = 0; nb < G::kNB; ++nb) {
@@ -169,89 +216,63 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void gate_up_kernel(const 
       if (r >= a.N) continue;
 #pragma unroll
       for (int mb = 0; mb < G::kMB; ++mb) {
-        const int h = mb / kHB, c = cw + 16 * (mb % kHB);
+        const int h = mb / kHB, c = cw + 16 * (mb % kHB) + 4 * kq;
         if (c < a.ldh)
           *reinterpret_cast<f32x4*>(a.zf + (2 * static_cast<int64_t>(r) + h) * a.ldh + c) = acc.v[mb][nb];
       }
     }
-    return;
   } else {
-    typedef Strip<G, kCols> S;
-    constexpr int kCodeRow = 2 * kCols;  // bytes: the codes of G, then of U
-    static_assert(S::kBytes + S::kRows * kCodeRow <= G::kLds, "the strips fit");
-    char* const codes = smem + S::kBytes;
-    const int q = 16 * wn + r16;
-    bf16* const h_dst = const_cast<bf16*>(a.h.p) + static_cast<int64_t>(r0) * a.h.ld + c0;
-#pragma unroll
-    for (int nb = 0; nb < G::kNB; ++nb) {
-      __syncthreads();
-      const int r = r0 + G::kWaveN * wn + 16 * nb + r16;
-      if constexpr (OUT == kHAndCodes) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int p = 0; p < kHB / 2; ++p) {
-            f32x4 v[2];
-            uint32_t top = 0;
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float x = acc.v[kHB * h + 2 * p + m][nb][i];
-                v[m][i] = cw + 32 * p + 16 * m + i < a.f ? x : 0.0f;
-                top = max(top, magnitude_bits(v[m][i]));
-              }
-            top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16, 64)));
-            top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, 64)));
-            const uint32_t b = exponent8(top);
-            const int c = 16 * kHB * wm + 32 * p;  // of the block in the tile
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-              *reinterpret_cast<uint32_t*>(codes + q * kCodeRow + h * kCols + c + 16 * m + 4 * kq) =
-                  codes8(v[m][0], v[m][1], v[m][2], v[m][3], b);
-            if (kq == 0 && r < a.N && c0 + c < a.fp)
-              a.exps[(2 * static_cast<int64_t>(r) + h) * (a.fp / kBlock8) + (c0 + c) / kBlock8] =
-                  static_cast<uint8_t>(b);
-          }
-      }
-      f32x4 hv[kHB];
-      with_act(a.act, [&](auto act) {
+    with_edge(r0 + G::kTile > a.N || c0 + kCols > a.f, [&](auto edge) {
+      constexpr bool E = decltype(edge)::value;
+      each<G::kNB>([&](auto at) {
+        constexpr int nb = decltype(at)::value;
+        const int r = r0 + G::kWaveN * wn + 16 * nb + r16;
+        const bool row = !E || r < a.N;
+        f32x4 g[kHB], u[kHB];
 #pragma unroll
         for (int mb = 0; mb < kHB; ++mb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            hv[mb][i] = cw + 16 * mb + i < a.f
-                            ? act_of<decltype(act)::value>(acc.v[mb][nb][i]) * acc.v[kHB + mb][nb][i]
-                            : 0.0f;
+          for (int i = 0; i < 4; ++i) {
+            const bool there = !E || cw + 16 * mb + 4 * kq + i < a.f;
+            g[mb][i] = there ? acc.v[mb][nb][i] : 0.0f;
+            u[mb][i] = there ? acc.v[kHB + mb][nb][i] : 0.0f;
+          }
+        if constexpr (OUT == kHAndCodes) {
+          uint32_t code[2][kHB], e[2][kHB / 2];
+#pragma unroll
+          for (int p = 0; p < kHB / 2; ++p) {
+            codes_of_block(g[2 * p], g[2 * p + 1], code[0][2 * p], code[0][2 * p + 1], e[0][p]);
+            codes_of_block(u[2 * p], u[2 * p + 1], code[1][2 * p], code[1][2 * p + 1], e[1][p]);
+          }
+          const int64_t rz = 2 * static_cast<int64_t>(r);
+          // 64 bytes of a row by four lanes: of one half, or half of that of both
+#pragma unroll
+          for (int o = 0; o < kHB / 2; ++o) {
+            u32x4 x = kHB == 4 ? u32x4{code[o][0], code[o][1], code[o][2], code[o][3]}
+                               : u32x4{code[0][0], code[0][1], code[1][0], code[1][1]};
+            transpose4(x);
+            const int h = kHB == 4 ? o : kq >> 1, c = cw + 16 * (kHB == 4 ? kq : kq & 1);
+            if (row && (!E || c < a.fp)) *reinterpret_cast<any_u32x4*>(a.codes + (rz + h) * a.fp + c) = x;
+          }
+          // and the exponents of its blocks by as many lanes as there are
+          constexpr int kP = kHB / 2;
+          const int h = kq / kP, p = kq % kP, c = cw + 32 * p;
+          const uint32_t b = h == 0 ? (p == 0 ? e[0][0] : e[0][kP - 1]) : (p == 0 ? e[1][0] : e[1][kP - 1]);
+          if (h < 2 && row && (!E || c < a.fp))
+            a.exps[(rz + h) * (a.fp / kBlock8) + c / kBlock8] = static_cast<uint8_t>(b);
+        }
+        with_act(a.act, [&](auto act) {
+#pragma unroll
+          for (int mb = 0; mb < kHB; ++mb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g[mb][i] = act_of<decltype(act)::value>(g[mb][i]) * u[mb][i];
+        });
+        bf16* const dst = const_cast<bf16*>(a.h.p) + static_cast<int64_t>(r) * a.h.ld + cw;
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part)
+          store_strip<kHB, PARTS>(dst + part * a.h.part, g, kq, row, E ? a.ldh - cw : 16 * kHB);
       });
-#pragma unroll
-      for (int part = 0; part < PARTS; ++part) {
-        if (part) __syncthreads();
-#pragma unroll
-        for (int mb = 0; mb < kHB; ++mb) {
-          Vec4<bf16>::type v;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[i] = PARTS == 1 ? from_float<bf16>(hv[mb][i]) : take_part(hv[mb], i);
-          S::put(smem, q, 16 * kHB * wm + 16 * mb + 4 * kq, v);
-        }
-        __syncthreads();
-        S::write(smem, h_dst + part * a.h.part, a.h.ld, nb, a.N - r0, a.ldh - c0);
-      }
-      if constexpr (OUT == kHAndCodes) {
-        constexpr int kChunks = kCodeRow / 16, kAll = S::kRows * kChunks;
-        typedef uint32_t any_u32x4 __attribute__((ext_vector_type(4), aligned(1)));
-#pragma unroll
-        for (int i = 0; i < (kAll + G::kThreads - 1) / G::kThreads; ++i) {
-          const int at = i * G::kThreads + tid, row = at / kChunks, c = at % kChunks;
-          const int h = c / (kChunks / 2), cb = c % (kChunks / 2) * 16;
-          const int64_t r = r0 + S::row(row, nb);
-          if (at < kAll && r < a.N && c0 + cb < a.fp)
-            *reinterpret_cast<any_u32x4*>(a.codes + (2 * r + h) * a.fp + c0 + cb) =
-                *reinterpret_cast<const any_u32x4*>(codes + row * kCodeRow + c * 16);
-        }
-      }
-    }
+    });
   }
 }
 
@@ -273,114 +294,109 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void gate_up_grad_kernel(c
   tile_product<G, PARTS, false, false>(rows_of(a.w_out, min(c0, a.f - 1), 0),
                                        rows_of(a.dy, min(r0, a.N - 1), 0),
                                        (a.d + kStepK - 1) / kStepK, smem, acc);
-  typedef Strip<G, G::kTile> S;
-  static_assert(3 * S::kBytes <= G::kLds, "the strips fit");
-  const int q = 16 * wn + r16;
-  const int cw = c0 + G::kWaveM * wm + 4 * kq;  // the lane's first column
-  bf16* const dz = const_cast<bf16*>(a.dz.p) + static_cast<int64_t>(r0) * a.dz.ld + c0;
-  bf16* const h = const_cast<bf16*>(a.h.p) + static_cast<int64_t>(r0) * a.h.ld + c0;
+  const int cw = c0 + G::kWaveM * wm;  // the wave's first column
+  with_edge(r0 + G::kTile > a.N || c0 + G::kTile > a.f, [&](auto edge) {
+    constexpr bool E = decltype(edge)::value;
+    // 64 columns of the wave's 16 rows at a time, the next ones' codes in flight
+    constexpr int kO = G::kMB / 4;
+    u32x4 code[2][2];
+    uint32_t e[2][2][2];
+    auto load = [&](int nb, int o, int to) {
+      const int r = r0 + G::kWaveN * wn + 16 * nb + r16, c = cw + 64 * o;
+      const int64_t rz = 2 * static_cast<int64_t>(E ? min(r, a.N - 1) : r);
 #pragma unroll
-  for (int nb = 0; nb < G::kNB; ++nb) {
-    const int r = r0 + G::kWaveN * wn + 16 * nb + r16;
-    const int64_t rz = 2 * static_cast<int64_t>(min(r, a.N - 1));
-    f32x4 dg[G::kMB], du[G::kMB], hv[G::kMB];
-    // G into dg and U into du first
-    if constexpr (CODES) {
-      uint32_t code[2][G::kMB], e[2][G::kMB / 2];
+      for (int h = 0; h < 2; ++h) {
+        const int cc = c + 16 * kq;
+        code[to][h] = *reinterpret_cast<const any_u32x4*>(a.codes + (rz + h) * a.fp +
+                                                          (E ? min(cc, a.fp - 16) : cc));
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-        for (int mb = 0; mb < G::kMB; ++mb) {
-          const int c = min(cw + 16 * mb, a.fp - 4);
-          code[hf][mb] = *reinterpret_cast<const uint32_t*>(a.codes + (rz + hf) * a.fp + c);
-        }
-#pragma unroll
-        for (int p = 0; p < G::kMB / 2; ++p)
-          e[hf][p] = a.exps[(rz + hf) * (a.fp / kBlock8) + min(cw + 32 * p, a.fp - 4) / kBlock8];
+        for (int p = 0; p < 2; ++p)
+          e[to][h][p] = a.exps[(rz + h) * (a.fp / kBlock8) +
+                               (E ? min(c + 32 * p, a.fp - 32) : c + 32 * p) / kBlock8];
       }
+    };
+    if constexpr (CODES) load(0, 0, 0);
+    each<G::kNB * kO>([&](auto at) {
+      constexpr int t = decltype(at)::value, nb = t / kO, o = t % kO, cur = t & 1;
+      const int r = r0 + G::kWaveN * wn + 16 * nb + r16, co = cw + 64 * o;
+      const bool row = !E || r < a.N;
+      f32x4 dg[4], du[4], hv[4];
+      // G into dg and U into du first
+      if constexpr (CODES) {
+        if constexpr (t + 1 < G::kNB * kO) load((t + 1) / kO, (t + 1) % kO, cur ^ 1);
+        transpose4(code[cur][0]);
+        transpose4(code[cur][1]);
 #pragma unroll
-      for (int mb = 0; mb < G::kMB; ++mb) {
-        const float sg = step8(e[0][mb / 2]), su = step8(e[1][mb / 2]);
+        for (int mb = 0; mb < 4; ++mb) {
+          const float sg = step8(e[cur][0][mb / 2]), su = step8(e[cur][1][mb / 2]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dg[mb][i] = value8(code[0][mb], i, sg);
-          du[mb][i] = value8(code[1][mb], i, su);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int mb = 0; mb < G::kMB; ++mb) {
-        const int c = min(cw + 16 * mb, a.ldh - 4);
-        dg[mb] = *reinterpret_cast<const f32x4*>(a.zf + rz * a.ldh + c);
-        du[mb] = *reinterpret_cast<const f32x4*>(a.zf + (rz + 1) * a.ldh + c);
-      }
-    }
-    with_act(a.act, [&](auto act) {
-#pragma unroll
-      for (int mb = 0; mb < G::kMB; ++mb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool there = cw + 16 * mb + i < a.f && r < a.N;
-          const float dh = acc.v[mb][nb][i], u = du[mb][i];
-          float slope;
-          const float v = act_of<decltype(act)::value>(dg[mb][i], slope);
-          hv[mb][i] = there ? v * u : 0.0f;
-          du[mb][i] = there ? dh * v : 0.0f;
-          dg[mb][i] = there ? dh * u * slope : 0.0f;
-        }
-    });
-    if constexpr (PARTS == 3) {
-      // the caller's own, in fp32
-      if (r < a.N) {
-#pragma unroll
-        for (int mb = 0; mb < G::kMB; ++mb) {
-          const int c = cw + 16 * mb;
-          if (c >= a.f) continue;
-          float* z = static_cast<float*>(a.dz_out);
-          if (z) {
-            z += rz * a.f + c;
-            store_row(z, a.f - c, dg[mb]);
-            store_row(z + a.f, a.f - c, du[mb]);
+          for (int i = 0; i < 4; ++i) {
+            dg[mb][i] = value8(code[cur][0][mb], i, sg);
+            du[mb][i] = value8(code[cur][1][mb], i, su);
           }
-          if (a.h_out)
-            store_row(static_cast<float*>(a.h_out) + static_cast<int64_t>(r) * a.f + c, a.f - c, hv[mb]);
+        }
+      } else {
+        const int64_t rz = 2 * static_cast<int64_t>(E ? min(r, a.N - 1) : r);
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb) {
+          const int c = co + 16 * mb + 4 * kq;
+          const float* z = a.zf + rz * a.ldh + (E ? min(c, a.ldh - 4) : c);
+          dg[mb] = *reinterpret_cast<const f32x4*>(z);
+          du[mb] = *reinterpret_cast<const f32x4*>(z + a.ldh);
         }
       }
-    }
+      with_act(a.act, [&](auto act) {
 #pragma unroll
-    for (int part = 0; part < PARTS; ++part) {
-      __syncthreads();
-      auto stage = [&](char* s, f32x4 (&x)[G::kMB]) {
+        for (int mb = 0; mb < 4; ++mb)
 #pragma unroll
-        for (int mb = 0; mb < G::kMB; ++mb) {
-          Vec4<bf16>::type v;
+          for (int i = 0; i < 4; ++i) {
+            const bool there = !E || (row && co + 16 * mb + 4 * kq + i < a.f);
+            const float dh = acc.v[4 * o + mb][nb][i], u = du[mb][i];
+            float slope;
+            const float v = act_of<decltype(act)::value>(dg[mb][i], slope);
+            hv[mb][i] = there ? v * u : 0.0f;
+            du[mb][i] = there ? dh * v : 0.0f;
+            dg[mb][i] = there ? dh * u * slope : 0.0f;
+          }
+      });
+      // the caller's own arrays, rows of 2 f and of f
+      const int64_t own = static_cast<int64_t>(r) * a.f + co;
+      if constexpr (PARTS == 3) {
+        auto store = [&](float* p, const f32x4 (&x)[4]) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = PARTS == 1 ? from_float<bf16>(x[mb][i]) : take_part(x[mb], i);
-          S::put(s, q, G::kWaveM * wm + 16 * mb + 4 * kq, v);
+          for (int mb = 0; mb < 4; ++mb) {
+            const int c = 16 * mb + 4 * kq;
+            if (row && co + c < a.f) store_row(p + c, a.f - co - c, x[mb]);
+          }
+        };
+        float* const z = static_cast<float*>(a.dz_out);
+        if (z) store(z + own + static_cast<int64_t>(r) * a.f, dg), store(z + own + static_cast<int64_t>(r + 1) * a.f, du);
+        if (a.h_out) store(static_cast<float*>(a.h_out) + own, hv);
+      } else {
+        bf16* const z = static_cast<bf16*>(a.dz_out);
+        const int n = E ? a.f - co : 64;
+        if (z) {
+          store_strip<4, 1>(z + own + static_cast<int64_t>(r) * a.f, dg, kq, row, n);
+          store_strip<4, 1>(z + own + static_cast<int64_t>(r + 1) * a.f, du, kq, row, n);
         }
-      };
-      stage(smem, dg);
-      stage(smem + S::kBytes, du);
-      stage(smem + 2 * S::kBytes, hv);
-      __syncthreads();
-      const int64_t off = part * a.dz.part;
-      S::write(smem, dz + off, a.dz.ld, nb, a.np - r0, a.fq - c0);
-      S::write(smem + S::kBytes, dz + off + a.fq, a.dz.ld, nb, a.np - r0,
-               static_cast<int>(a.dz.ld) - a.fq - c0);
-      S::write(smem + 2 * S::kBytes, h + part * a.h.part, a.h.ld, nb, a.np - r0,
-               static_cast<int>(a.h.ld) - c0);
-      if constexpr (PARTS == 1) {
-        if (a.dz_out) {
-          bf16* z = static_cast<bf16*>(a.dz_out) + 2 * static_cast<int64_t>(r0) * a.f + c0;
-          S::write(smem, z, 2 * static_cast<int64_t>(a.f), nb, a.N - r0, a.f - c0);
-          S::write(smem + S::kBytes, z + a.f, 2 * static_cast<int64_t>(a.f), nb, a.N - r0, a.f - c0);
-        }
-        if (a.h_out)
-          S::write(smem + 2 * S::kBytes, static_cast<bf16*>(a.h_out) + static_cast<int64_t>(r0) * a.f + c0,
-                   a.f, nb, a.N - r0, a.f - c0);
+        if (a.h_out) store_strip<4, 1>(static_cast<bf16*>(a.h_out) + own, hv, kq, row, n);
       }
-    }
-  }
+      // (rows from N on are written up to np, columns up to the end of the padding)
+      const bool there = !E || r < a.np;
+      bf16* const dz = const_cast<bf16*>(a.dz.p) + static_cast<int64_t>(r) * a.dz.ld + co;
+      bf16* const h = const_cast<bf16*>(a.h.p) + static_cast<int64_t>(r) * a.h.ld + co;
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part) {
+        const int64_t off = part * a.dz.part;
+        store_strip<4, PARTS>(dz + off, dg, kq, there, E ? a.fq - co : 64);
+        store_strip<4, PARTS>(dz + off + a.fq, du, kq, there,
+                              E ? static_cast<int>(a.dz.ld) - a.fq - co : 64);
+        store_strip<4, PARTS>(h + part * a.h.part, hv, kq, there,
+                              E ? static_cast<int>(a.h.ld) - co : 64);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // (interleaved steps would need more registers)
+    });
+  });
 }
 
 // out[n][h m + c] = sum_k b[n][k] a[h][c][k] for the halves h of A (its columns or rows

@@ -490,34 +490,33 @@ __device__ __forceinline__ void write_tile(char* smem, bf16* dst, int64_t ld, in
   }
 }
 
-// 16 rows of a wave, kept in LDS as COLS bytes-pairs each, and written in whole rows: the
-// form of an epilogue that has several arrays to write and works through a tile one nb
-// at a time. Row q of a strip is the tile's row kWaveN (q / 16) + 16 nb + q % 16; 16-byte
-// chunk c of it sits in slot c ^ (q mod the chunks of a row).
-template <class G, int COLS>
-struct Strip {
-  static constexpr int kRows = 16 * G::kWavesN, kChunks = COLS / 8, kBytes = kRows * COLS * 2;
-  __device__ __forceinline__ static int row(int q, int nb) {
-    return G::kWaveN * (q >> 4) + 16 * nb + (q & 15);
-  }
-  // columns c .. c + 3 of row q
-  __device__ __forceinline__ static void put(char* s, int q, int c, Vec4<bf16>::type v) {
-    *reinterpret_cast<Vec4<bf16>::type*>(s + q * (2 * COLS) + ((c >> 3) ^ (q % kChunks)) * 16 +
-                                         (c & 4) * 2) = v;
-  }
-  // Rows below n_rows, columns below n_cols, of what dst is the tile's first row of.
-  __device__ __forceinline__ static void write(const char* s, bf16* dst, int64_t ld, int nb,
-                                               int n_rows, int n_cols) {
-#pragma unroll
-    for (int i = 0; i < (kRows * kChunks + G::kThreads - 1) / G::kThreads; ++i) {
-      const int at = i * G::kThreads + static_cast<int>(threadIdx.x);
-      const int q = at / kChunks, c = at % kChunks, r = row(q, nb);
-      if (at >= kRows * kChunks || r >= n_rows || c * 8 >= n_cols) continue;
-      const bf16x8 v = lds_read_b128(s + q * (2 * COLS) + (c ^ (q % kChunks)) * 16);
-      store_row(dst + static_cast<int64_t>(r) * ld + c * 8, n_cols - c * 8, v);
-    }
-  }
-};
+// Transposes the lane quarters (kq = lane / 16) of a wave against four registers: x[j]
+// of quarter kq and x[kq] of quarter j change places. What an accumulator holds as runs
+// of four columns then becomes 16 bytes of one row, without LDS.
+__device__ __forceinline__ void swap16(uint32_t& x, uint32_t& y) {
+  const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+  x = r[0], y = r[1];
+}
+__device__ __forceinline__ void swap32(uint32_t& x, uint32_t& y) {
+  const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+  x = r[0], y = r[1];
+}
+__device__ __forceinline__ void transpose4(u32x4& x) {
+  uint32_t r[4] = {x[0], x[1], x[2], x[3]};
+  swap16(r[0], r[1]), swap16(r[2], r[3]);
+  swap32(r[0], r[2]), swap32(r[1], r[3]);
+  x = u32x4{r[0], r[1], r[2], r[3]};
+}
+// Two neighbouring blocks of 16 columns of an accumulator's row in bf16 (the lane's four
+// columns of either), as the 8 columns from pair_col(kq) on of the 32.
+__device__ __forceinline__ int pair_col(int kq) { return 16 * (kq & 1) + 8 * (kq >> 1); }
+__device__ __forceinline__ bf16x8 pair_cols(Vec4<bf16>::type a, Vec4<bf16>::type b) {
+  typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+  u2 x = __builtin_bit_cast(u2, a), y = __builtin_bit_cast(u2, b);
+  uint32_t x0 = x[0], x1 = x[1], y0 = y[0], y1 = y[1];
+  swap16(x0, y0), swap16(x1, y1);
+  return __builtin_bit_cast(bf16x8, u32x4{x0, x1, y0, y1});
+}
 
 // Writes a tile to rows of ld floats, or adds it to them: an accumulator value's N
 // is its row, its M its column. Columns >= n_cols (a multiple of 16) stay.
