@@ -852,11 +852,16 @@ def dpg_distill_loss_grad(X: torch.Tensor, E: torch.Tensor, top_ids: torch.Tenso
     return dX, dE
 
 
+# The current device without torch.cuda's check that it is initialised, which the tensors
+# that a call was given settle (half a microsecond a call), where this torch has it.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _on_this_device(ref: torch.Tensor):
     """The library enqueues on the current device's stream."""
-    if ref.get_device() != torch.cuda.current_device():
+    if ref.get_device() != _current_device():
         raise ValueError(f"tensors on {ref.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+                         f"cuda:{_current_device()}")
 
 
 class PackedActivations(NamedTuple):
@@ -883,22 +888,26 @@ def _packed_like(rows, d, dtype, device):
                              d, dtype)
 
 
-def _require_packed(p: PackedActivations, name: str, shape=None):
+def _require_packed(p: PackedActivations, name: str, rows=None, d=None):
+    """rows, d: the shape it has to have, where it is given."""
     if not isinstance(p, PackedActivations):
         raise TypeError(f"{name} must be PackedActivations")
-    _require(p.codes, f"{name}.codes", torch.int8)
-    blocks = -(-p.d // 32)
-    if p.codes.dim() < 1 or int(p.codes.shape[-1]) != 32 * blocks:
+    codes, exps = p.codes, p.exps
+    _require(codes, f"{name}.codes", torch.int8)
+    lead, blocks = codes.shape[:-1], -(-p.d // 32)
+    if codes.dim() < 1 or int(codes.shape[-1]) != 32 * blocks:
         raise ValueError(f"{name}.codes must be [..., {32 * blocks}] for {p.d} channels")
-    _require(p.exps, f"{name}.exps", torch.uint8, (*p.codes.shape[:-1], blocks))
-    _same_device(p.codes, **{f"{name}.exps": p.exps})
-    if shape is not None and p.shape != torch.Size(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(p.shape)}")
+    _require(exps, f"{name}.exps", torch.uint8, (*lead, blocks))
+    if exps.get_device() != codes.get_device():
+        raise ValueError(f"{name}.exps must be on {codes.device}, got {exps.device}")
+    if d is not None and (p.d != d or lead != rows):
+        raise ValueError(f"{name} must have shape {(*rows, d)}, got {tuple(p.shape)}")
 
 
 def _rows_of(t: torch.Tensor) -> int:
     """Rows of [..., d] (a width of zero has them all the same)."""
-    return math.prod(t.shape[:-1])
+    d = t.shape[-1]
+    return t.numel() // d if d else math.prod(t.shape[:-1])
 
 
 @_on_stream
@@ -915,10 +924,11 @@ def dpg_pack_act(X: torch.Tensor, out: Optional[PackedActivations] = None,
     d, code = int(X.shape[-1]), _dtype_code(X.dtype)
     if out is None:
         out = _packed_like(X.shape[:-1], d, X.dtype, X.device)
-    _require_packed(out, "out", X.shape)
-    if out.dtype != X.dtype:
-        raise TypeError(f"out is of {out.dtype}, X of {X.dtype}")
-    _same_device(X, out=out.codes)
+    else:
+        _require_packed(out, "out", X.shape[:-1], d)
+        if out.dtype != X.dtype:
+            raise TypeError(f"out is of {out.dtype}, X of {X.dtype}")
+        _same_device(X, out=out.codes)
     N = _rows_of(X)
     if N:
         _check(lib, lib.dpg_pack_act(_ptr(X), N, d, code, _ptr(out.codes), _ptr(out.exps),
@@ -937,14 +947,25 @@ def dpg_unpack_act(packed: PackedActivations, dtype: Optional[torch.dtype] = Non
     dtype = dtype or (packed.dtype if X is None else X.dtype)
     code = _dtype_code(dtype)
     if X is None:
-        X = torch.empty(packed.shape, dtype=dtype, device=packed.codes.device)
-    _require(X, "X", dtype, packed.shape)
-    _same_device(X, packed=packed.codes)
+        X = torch.empty((*packed.codes.shape[:-1], packed.d), dtype=dtype,
+                        device=packed.codes.device)
+    else:
+        _require(X, "X", dtype, packed.shape)
+        _same_device(X, packed=packed.codes)
     N = _rows_of(X)
     if N:
         _check(lib, lib.dpg_unpack_act(_ptr(packed.codes), _ptr(packed.exps), N, packed.d, code,
                                        _ptr(X), _stream_handle(stream)))
     return X
+
+
+@functools.lru_cache(maxsize=1024)
+def _packed_workspace_size(B, T, d_in, d_out, r, code):
+    lib, need = load_library(), ctypes.c_size_t(0)
+    layer = LayerGrad(d_in, d_out, 0, 0, None, None, None)
+    _check(lib, lib.dpg_project_layer_packed_workspace_size(ctypes.byref(layer), B, T, r, code,
+                                                            ctypes.byref(need)))
+    return need.value
 
 
 @_on_stream
@@ -956,28 +977,26 @@ def dpg_project_layer_packed(A: PackedActivations, dY: torch.Tensor, r: int, see
     P A_i^T dY_i ([B, r, d_out] fp32) for what A's codes stand for, and norm_sq[i] +=
     ||G_hat[i]||^2. dY's type is the operands' precision. Returns G_hat."""
     lib = load_library()
-    _require_packed(A, "A")
     _require(dY, "dY")
-    if len(A.shape) != 3 or dY.dim() != 3 or tuple(A.shape[:2]) != tuple(dY.shape[:2]):
+    if dY.dim() != 3:
         raise ValueError("A and dY must be [B, T, d] with common B, T")
-    B, T = int(dY.shape[0]), int(dY.shape[1])
-    d_out, code = int(dY.shape[2]), _dtype_code(dY.dtype)
+    B, T, d_out = (int(n) for n in dY.shape)
+    _require_packed(A, "A", (B, T), A.d if isinstance(A, PackedActivations) else None)
+    code = _dtype_code(dY.dtype)
     _on_this_device(dY)
     if G_hat is None:
         G_hat = torch.empty((B, r, d_out), dtype=torch.float32, device=dY.device)
-    _require(G_hat, "G_hat", torch.float32, (B, r, d_out))
+    else:
+        _require(G_hat, "G_hat", torch.float32, (B, r, d_out))
     _require(norm_sq, "norm_sq", torch.float32, (B,))
     _same_device(dY, A=A.codes, G_hat=G_hat, norm_sq=norm_sq)
-    arr = (LayerGrad * 1)()
-    arr[0].d_in, arr[0].d_out, arr[0].layer_id = A.d, d_out, int(layer_id)
-    arr[0].dY = _ptr(dY)
-    need = ctypes.c_size_t(0)
-    _check(lib, lib.dpg_project_layer_packed_workspace_size(arr, B, T, int(r), code,
-                                                            ctypes.byref(need)))
-    ws, ws_bytes = _workspace(need.value, dY.device, workspace)
+    layer = LayerGrad(A.d, d_out, int(layer_id), 0, None, _ptr(dY), None)
+    ws, ws_bytes = _workspace(_packed_workspace_size(B, T, A.d, d_out, int(r), code), dY.device,
+                              workspace)
     _check(lib, lib.dpg_project_layer_packed(
-        arr, _ptr(A.codes), _ptr(A.exps), B, T, int(r), code, int(seed), int(proj_step),
-        _ptr(G_hat), _ptr(norm_sq), ws.data_ptr(), ws_bytes, _stream_handle(stream)))
+        ctypes.byref(layer), _ptr(A.codes), _ptr(A.exps), B, T, int(r), code, int(seed),
+        int(proj_step), _ptr(G_hat), _ptr(norm_sq), ws.data_ptr(), ws_bytes,
+        _stream_handle(stream)))
     return G_hat
 
 
@@ -1036,15 +1055,16 @@ def dpg_gated(X: torch.Tensor, W_in: torch.Tensor, W_out: torch.Tensor, act: str
     act_code = _act_code(act)
     if Y is None:
         Y = torch.empty_like(X)
-    _require(Y, "Y", X.dtype, X.shape)
-    if Z is not None and not keep:
-        raise ValueError("Z is given, but keep is not set")
-    if keep:
-        if Z is None:
-            Z = _packed_like((*X.shape[:-1], 2), f, X.dtype, X.device)
-        _require_packed(Z, "Z", (*X.shape[:-1], 2, f))
+    else:
+        _require(Y, "Y", X.dtype, X.shape)
+        _same_device(X, Y=Y)
+    if Z is not None:
+        if not keep:
+            raise ValueError("Z is given, but keep is not set")
+        _require_packed(Z, "Z", (*X.shape[:-1], 2), f)
         _same_device(X, Z=Z.codes)
-    _same_device(X, Y=Y)
+    elif keep:
+        Z = _packed_like((*X.shape[:-1], 2), f, X.dtype, X.device)
     if N == 0:
         return Y, Z
     ws, ws_bytes = _workspace(_gated_workspace_size(N, d, f, code), X.device, workspace)
@@ -1079,13 +1099,13 @@ def dpg_gated_grad(dY: torch.Tensor, X: Union[torch.Tensor, PackedActivations, N
     act_code = _act_code(act)
     w_in, w_out = need_dW if isinstance(need_dW, (tuple, list)) else (need_dW, need_dW)
     if Z is not None:
-        _require_packed(Z, "Z", (*dY.shape[:-1], 2, f))
+        _require_packed(Z, "Z", (*dY.shape[:-1], 2), f)
         _same_device(dY, Z=Z.codes)
     x = codes = exps = None
     if isinstance(X, PackedActivations):
         if Z is None:
             raise ValueError("Z is needed with X in 8 bits")
-        _require_packed(X, "X", dY.shape)
+        _require_packed(X, "X", dY.shape[:-1], d)
         _same_device(dY, X=X.codes)
         codes, exps = X.codes, X.exps
     elif X is not None:

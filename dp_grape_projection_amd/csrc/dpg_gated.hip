@@ -140,6 +140,7 @@ __device__ __forceinline__ Operand kmajor_of(const Mat& m, int k0, int c0) {
   return rows_operand(m.p + static_cast<int64_t>(k0) * m.ld + c0, m.ld, m.part, m.rows - k0, m.cols - c0);
 }
 
+typedef uint32_t any_u32 __attribute__((aligned(1)));
 typedef uint32_t any_u32x4 __attribute__((ext_vector_type(4), aligned(1)));
 
 // The codes of a lane's eight values of a block of 32 columns, which four lanes share.
@@ -156,6 +157,15 @@ __device__ __forceinline__ void codes_of_block(const f32x4& x, const f32x4& y, u
   b = exponent8(max(top, other));
   cx = codes8(x[0], x[1], x[2], x[3], b);
   cy = codes8(y[0], y[1], y[2], y[3], b);
+}
+
+// Four values, rounded, at any element's address.
+__device__ __forceinline__ void store_any4(bf16* p, const f32x4& x) {
+  typedef __bf16 any4 __attribute__((ext_vector_type(4), aligned(2)));
+  any4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = from_float<bf16>(x[i]);
+  *reinterpret_cast<any4*>(p) = v;
 }
 
 // MB blocks of 16 columns of one row, rounded (or, of several parts, the next one taken
@@ -495,15 +505,182 @@ __global__ __launch_bounds__(kThreads) void splits_kernel(const ProductArgs a) {
   }
 }
 
+// ---------------------------------------------------------------- few rows --
+//
+// At most 16 rows (tokens being answered): the weights' bytes are the time, and what
+// counts is how many of them are in flight. A block takes 64 columns (of the up and gate
+// projections 32 each), its four waves every fourth K step of 32, each on its own: a wave
+// copies a step's 32 rows of 128 bytes and 16 rows of X into its own LDS, five steps
+// ahead, and waits for nothing but its copies; no barrier until the waves' sums meet.
+// H stays in two bf16 parts (2^-17 of it), which costs a product but no bytes that count.
+
+constexpr int kFewRows = 16, kFewK = 32, kFewCols = 64, kFewStages = 6;
+
+struct FewArgs {
+  const bf16* w;       // [K][ldw], K-major
+  const bf16* x;       // [parts][16 or more][ldx]
+  int64_t ldw, ldx, part;
+  int32_t N, K, cols;  // rows, columns of a half
+  int32_t half;        // columns from a half to the other (gate and up)
+  int32_t tiles, splits;
+  int32_t act;
+  bf16* h;             // gate and up: [2][16][cols]
+  int8_t* codes;       // and [N][2][cols], or null
+  uint8_t* exps;
+  float* acc;          // [splits][16][ldm], or, with one split,
+  bf16* out;           // [N][cols]
+  int32_t ldm;
+};
+
+// Nothing in memory or on the matrix cores moves across.
+__device__ __forceinline__ void keep_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <bool GATED>
+__global__ __launch_bounds__(kThreads, 1) void few_rows_kernel(const FewArgs a) {
+  constexpr int kParts2 = GATED ? 1 : 2;         // parts of the rows
+  constexpr int kCopies = 4 + kParts2;           // a step's
+  constexpr int kStage = 4096 + 1024 * kParts2;  // 32 rows of 64 columns, 16 rows of 32 K
+  __shared__ __attribute__((aligned(1024))) char smem[4 * kFewStages * kStage];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, kq = lane >> 4;
+  const int total = a.tiles * a.splits, per = (total + 7) >> 3;
+  const int at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (static_cast<int>(blockIdx.x >> 3) >= per || at >= total) return;
+  const int split = at / a.tiles, tile = at - split * a.tiles;
+  const int c0 = tile * (GATED ? kFewCols / 2 : kFewCols);
+  const int all = a.K / kFewK, some = (all + a.splits - 1) / a.splits;
+  const int s0 = min(all, split * some) + wave, s1 = min(all, (split + 1) * some);
+  const int n = s0 < s1 ? (s1 - s0 + 3) / 4 : 0;  // this wave's steps: s0, s0 + 4, ...
+  char* const mine = smem + wave * kFewStages * kStage;
+  // a copy is 8 rows of 8 chunks; slots as in any k-major tile of 64 columns
+  uint32_t off_w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int k = 8 * q + (lane >> 3), c = kslot<8>(k, lane & 7);
+    const int col = GATED ? c0 + 8 * (c & 3) + (c >> 2) * a.half : min(c0 + 8 * c, a.cols - 8);
+    off_w[q] = static_cast<uint32_t>(k) * static_cast<uint32_t>(a.ldw) * 2u + static_cast<uint32_t>(col) * 2u;
+  }
+  // and 16 rows of 4 chunks, chunk c of row r in slot c ^ (r / 4 mod 4)
+  const int xr = lane >> 2, xc = (lane & 3) ^ ((xr >> 2) & 3);
+  const uint32_t off_x = static_cast<uint32_t>(min(xr, a.N - 1)) * static_cast<uint32_t>(a.ldx) * 2u +
+                         static_cast<uint32_t>(xc) * 16u;
+  auto issue = [&](int i) {  // the wave's step i
+    char* const to = mine + (i % kFewStages) * kStage;
+    const int64_t k = static_cast<int64_t>(s0 + 4 * i) * kFewK;
+    const __amdgpu_buffer_rsrc_t rw = tile_rsrc(a.w + k * a.ldw), rx = tile_rsrc(a.x + k);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) copy_to_lds(rw, off_w[q], 0, to + q * 1024);
+#pragma unroll
+    for (int q = 0; q < kParts2; ++q)
+      copy_to_lds(q ? tile_rsrc(a.x + a.part + k) : rx, off_x, 0, to + 4096 + q * 1024);
+  };
+  f32x4 acc[4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto use = [&](int i) {
+    const char* const from = mine + (i % kFewStages) * kStage;
+    bf16x8 fw[4], fx[kParts2];
+#pragma unroll
+    for (int q = 0; q < kParts2; ++q)
+      fx[q] = lds_read_b128(from + 4096 + q * 1024 + r16 * 64 + (kq ^ ((r16 >> 2) & 3)) * 16);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      v4i16 h[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int k = 8 * kq + 4 * j + (r16 >> 2), c = 16 * m + 4 * (r16 & 3);
+        h[j] = lds_read_tr(from + k * 128 + kslot<8>(k, c >> 3) * 16 + (c & 7) * 2);
+      }
+      fw[m] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+#pragma unroll
+    for (int q = kParts2 - 1; q >= 0; --q)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) acc[m] = mfma<1>(fw[m], fx[q], acc[m]);
+  };
+  // a step is used once at most the copies of the ones after it are in flight: loads
+  // return in order
+#pragma unroll
+  for (int i = 0; i < kFewStages - 1; ++i)
+    if (i < n) issue(i);
+  int i = 0;
+  for (; i + kFewStages - 1 < n; ++i) {
+    issue(i + kFewStages - 1);
+    wait_vm_all<kCopies * (kFewStages - 1)>();
+    keep_order();
+    use(i);
+    wait_lgkm0();  // the next step's copies go where this one's were
+    keep_order();
+  }
+  wait_vm_all<0>();
+  keep_order();
+  for (; i < n; ++i) use(i);
+  // the waves' sums, in their order
+  __syncthreads();
+  f32x4* const sums = reinterpret_cast<f32x4*>(smem);
+#pragma unroll
+  for (int m = 0; m < 4; ++m) sums[(wave * 4 + m) * 64 + lane] = acc[m];
+  __syncthreads();
+  // wave w's lanes hold columns 16 w + 4 kq .. + 3 of row r16
+  f32x4 x = sums[wave * 64 + lane];
+#pragma unroll
+  for (int w = 1; w < 4; ++w) {
+    const f32x4 y = sums[(w * 4 + wave) * 64 + lane];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] += y[j];
+  }
+  const int c = 16 * wave + 4 * kq;
+  if constexpr (GATED) {
+    __syncthreads();
+    sums[wave * 64 + lane] = x;
+    __syncthreads();
+    if (wave >= 2) {  // the 8-bit form of G and of U
+      if (!a.codes) return;
+      const int h = wave - 2;
+      uint32_t code[2], b;
+      codes_of_block(sums[2 * h * 64 + lane], sums[(2 * h + 1) * 64 + lane], code[0], code[1], b);
+      if (r16 >= a.N) return;
+      const int64_t rz = 2 * r16 + h;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        *reinterpret_cast<any_u32*>(a.codes + rz * a.cols + c0 + 16 * m + 4 * kq) = code[m];
+      if (kq == 0) a.exps[(rz * a.cols + c0) / kBlock8] = static_cast<uint8_t>(b);
+      return;
+    }
+    if (r16 >= a.N) return;
+    const f32x4 u = sums[(wave + 2) * 64 + lane];
+    f32x4 hv;
+    with_act(a.act, [&](auto act) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) hv[j] = act_of<decltype(act)::value>(x[j]) * u[j];
+    });
+    bf16* const dst = a.h + static_cast<int64_t>(r16) * a.cols + c0 + c;
+    f32x4 rest;
+    Vec4<bf16>::type v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = from_float<bf16>(hv[j]);
+      // (an infinity leaves nothing)
+      rest[j] = fabsf(hv[j]) < INFINITY ? hv[j] - static_cast<float>(v[j]) : 0.0f;
+    }
+    *reinterpret_cast<Vec4<bf16>::type*>(dst) = v;
+    store4<bf16>(dst + kFewRows * static_cast<int64_t>(a.cols), rest[0], rest[1], rest[2], rest[3]);
+  } else {
+    if (r16 >= a.N || c0 + c >= a.cols) return;
+    if (a.splits > 1)
+      *reinterpret_cast<f32x4*>(a.acc + (static_cast<int64_t>(split) * kFewRows + r16) * a.ldm + c0 + c) = x;
+    else
+      store_any4(a.out + static_cast<int64_t>(r16) * a.cols + c0 + c, x);
+  }
+}
+
 // ------------------------------------------------------------------- host --
 
-// Tiles of a launch of m x n outputs without splits: as for the losses' logits.
 enum Tile { kBig, kSmall, kTiny };
-Tile tile_for(int64_t m, int64_t n, int64_t cols_of_tile_halved) {
-  auto tiles = [&](int64_t tile) { return ceil_div(m, tile / cols_of_tile_halved) * ceil_div(n, tile); };
-  if (big_tiles(tiles(BigTile::kTile), n)) return kBig;
-  return tiles(SmallTile::kTile) > 256 ? kSmall : kTiny;
-}
 template <class F>
 void with_tile(Tile t, F fn) {
   if (t == kBig) fn(BigTile());
@@ -511,14 +688,45 @@ void with_tile(Tile t, F fn) {
   else fn(TinyTile());
 }
 
-// Tiles and splits of a product of m x n outputs over `steps` steps of K.
+// Tiles and splits of a product of m x n outputs over `steps` K steps of `combos`
+// products each; of G and U together, whose tiles have half their width of columns of
+// either and which needs all of K, as dH does (`whole`).
+// Modelled on 300 measurements: with c blocks on a CU, a K step takes 1.05 + 0.5 c us in a
+// big tile, 0.5 max(1, c) in a small one, 0.34 + 0.13 (c - 1) in a tiny one, a fifth more
+// where both operands are read transposed; outputs and partial sums are written at 5.6
+// TB/s, and adding those up is a launch of 2.5 us and 6.5 TB/s. (dW_out of 16384 x 768 x
+// 2048: 64 us in small tiles with 5 splits, 65 big with 10, 90 tiny with 2; of 128 x 64 x
+// 256: 3.6 tiny, 4.5 small, 7.9 big. dX of 2048 x 2048 x 4096: 67 us in small tiles, 73 big
+// with 4 splits, 99 tiny.)
 struct Choice {
   Tile tile;
   int32_t splits;
 };
-Choice choose(int64_t m, int64_t n, int64_t steps, int combos) {
-  const Split s = choose_split(m, n, steps, combos, false);
-  return {s.big ? kBig : kSmall, s.splits};
+enum Kind { kPlain, kBothTransposed, kGateUp, kWhole };
+Choice choose(int64_t m, int64_t n, int64_t steps, int combos, Kind kind) {
+  Choice best{kTiny, 1};
+  double best_us = 1e30;
+  const double mn = static_cast<double>(m) * static_cast<double>(n) / 1e6;
+  for (const Tile t : {kBig, kSmall, kTiny}) {
+    const int64_t tile = t == kBig ? BigTile::kTile : t == kSmall ? SmallTile::kTile : TinyTile::kTile;
+    const int64_t slots = t == kBig ? 256 : t == kSmall ? 512 : 1024;
+    const int64_t tiles = ceil_div(m, kind == kGateUp ? tile / 2 : tile) * ceil_div(n, tile);
+    const int64_t most = kind <= kBothTransposed ? std::max<int64_t>(1, std::min(slots / tiles, steps)) : 1;
+    // (every count up to 16, then steps of an eighth, and the most)
+    for (int64_t k = 1; k <= most; k = k < most ? std::min(k + std::max<int64_t>(1, k / 8), most) : k + 1) {
+      const int64_t blocks = tiles * k, rounds = ceil_div(blocks, slots);
+      const double c = static_cast<double>(std::min(blocks, slots)) / 256;
+      double step = t == kBig ? 1.05 + 0.5 * c : t == kSmall ? 0.5 * std::max(1.0, c)
+                                                             : 0.34 + 0.13 * std::max(0.0, c - 1.0);
+      if (kind == kBothTransposed) step *= 1.2;
+      const double around = t == kBig ? 5.0 : t == kSmall ? 3.5 : 3.0;
+      double us = static_cast<double>(rounds) * (static_cast<double>(ceil_div(steps, k) * combos) * step + around);
+      us += mn * (k > 1 ? 4.0 * static_cast<double>(k) : 2.0) / 5.6;
+      if (k > 1) us += 2.5 + mn * (4.0 * static_cast<double>(k) + 2.0) / 6.5;
+      if (us < best_us) best_us = us, best = {t, static_cast<int32_t>(k)};
+    }
+  }
+  return best;
 }
 
 struct Call {
@@ -548,8 +756,15 @@ constexpr int64_t kZBytes = 256ll << 20;
 struct Plan {
   int64_t parts, ldx, ldh, fq, ldz, np, fp, z_rows = 0;
   Choice y{}, x{}, wi{}, wo{};
+  int32_t few_splits = 0;  // few rows: parts of f in the second product
   size_t off_x, off_wi, off_wo, off_dy, off_h, off_dz = 0, off_zf = 0, off_x8 = 0, off_acc, total;
 };
+
+// Few rows of bf16 in whole K steps go their own way where the weights are 16-byte
+// aligned (4 rows x 2048 x 8192: FEWTIMES).
+bool few_rows(const Call& c) {
+  return c.dtype == DPG_BF16 && c.N <= kFewRows && c.d % kFewK == 0 && c.f % kFewK == 0;
+}
 
 size_t acc_bytes(const Choice& c, int64_t halves, int64_t m, int64_t n) {
   return c.splits > 1 ? c.splits * round_up(n, kPad) * halves * round_up(m, 64) * 4 : 0;
@@ -577,19 +792,26 @@ Plan plan_gated(const Call& c, bool grad, bool again, bool weights) {
   p.off_dy = take(grad ? p.parts * c.N * p.ldx : 0, 2);
   p.off_h = take(p.parts * p.np * p.ldh, 2);
   if (!grad) {
-    p.y = choose(c.d, c.N, p.ldh / kStepK, combos);
+    p.y = choose(c.d, c.N, p.ldh / kStepK, combos, kPlain);
     acc = acc_bytes(p.y, 1, c.d, c.N);
+    if (few_rows(c)) {
+      // about a block for every CU, each wave with four steps at least
+      const int64_t tiles = ceil_div(c.d, kFewCols);
+      p.few_splits = static_cast<int32_t>(
+          std::max<int64_t>(1, std::min(256 / tiles, c.f / (16 * kFewK))));
+      acc = std::max<size_t>(acc, p.few_splits * kFewRows * round_up(c.d, 64) * 4);
+    }
   } else {
     p.off_dz = take(p.parts * p.np * p.ldz, 2);
     if (again) {
       p.z_rows = std::min(p.np, std::max<int64_t>(kPad, kZBytes / (p.ldh * 8) / kPad * kPad));
       p.off_zf = take(p.z_rows * 2 * p.ldh, 4);
     }
-    p.x = choose(c.d, c.N, p.ldz / kStepK, combos);
+    p.x = choose(c.d, c.N, p.ldz / kStepK, combos, kPlain);
     acc = acc_bytes(p.x, 1, c.d, c.N);
     if (weights) {
-      p.wi = choose(2 * round_up(c.f, SmallTile::kTile), c.d, p.np / kStepK, combos);
-      p.wo = choose(c.d, c.f, p.np / kStepK, combos);
+      p.wi = choose(2 * c.f, c.d, ceil_div(c.N, kStepK), combos, kBothTransposed);
+      p.wo = choose(c.d, c.f, ceil_div(c.N, kStepK), combos, kBothTransposed);
       acc = std::max({acc, acc_bytes(p.wi, 2, c.f, c.d), acc_bytes(p.wo, 1, c.d, c.f)});
       p.off_x8 = take(c.N * p.ldx, c.dtype == DPG_BF16 ? 2 : 4);
     }
@@ -635,9 +857,15 @@ GatedArgs make_args(const Call& c, const Plan& p) {
   return a;
 }
 
+// The tiles of the kernels that need all of K: of G and U, of dH.
+template <typename T>
+Tile whole_tile(int64_t m, int64_t n, int64_t d, Kind kind) {
+  return choose(m, n, ceil_div(d, kStepK), Combos<kParts<T>>::n, kind).tile;
+}
+
 template <typename T, int OUT>
 void launch_gate_up(const GatedArgs& a, hipStream_t s) {
-  with_tile(tile_for(a.ldh, a.N, 2), [&](auto g) {
+  with_tile(whole_tile<T>(a.ldh, a.N, a.d, kGateUp), [&](auto g) {
     typedef decltype(g) G;
     hipLaunchKernelGGL((gate_up_kernel<G, kParts<T>, OUT>),
                        tile_grid(ceil_div(a.ldh, G::kTile / 2), ceil_div(a.N, G::kTile)),
@@ -685,6 +913,37 @@ int run_forward(const Call& c, const Plan& p, const void* X, const void* W_in, c
   else launch_gate_up<T, kH>(a, s);
   launch_product<T, true, false>(p.y, a.w_out, a.h, 0, 1, c.d, c.N, p.ldh, Y,
                                  reinterpret_cast<float*>(ws + p.off_acc), s);
+  return check_launch("gated block");
+}
+
+// The forward pass of few rows. The two parts of H are where the tiles' H would be.
+int run_few(const Call& c, const Plan& p, const void* X, const void* W_in, const void* W_out, void* Y,
+            int8_t* codes, uint8_t* exps, char* ws, hipStream_t s) {
+  FewArgs a{};
+  a.N = static_cast<int32_t>(c.N), a.act = c.act;
+  a.w = static_cast<const bf16*>(W_in), a.ldw = 2 * c.f;
+  a.x = static_cast<const bf16*>(X), a.ldx = c.d;
+  a.K = static_cast<int32_t>(c.d), a.cols = a.half = static_cast<int32_t>(c.f);
+  a.h = reinterpret_cast<bf16*>(ws + p.off_h);
+  a.codes = codes, a.exps = exps;
+  a.tiles = static_cast<int32_t>(ceil_div(c.f, kFewCols / 2)), a.splits = 1;
+  hipLaunchKernelGGL(few_rows_kernel<true>, tile_grid(a.tiles, 1), dim3(kThreads), 0, s, a);
+  FewArgs b{};
+  b.N = a.N;
+  b.w = static_cast<const bf16*>(W_out), b.ldw = c.d;
+  b.x = a.h, b.ldx = c.f, b.part = kFewRows * c.f;
+  b.K = static_cast<int32_t>(c.f), b.cols = static_cast<int32_t>(c.d);
+  b.tiles = static_cast<int32_t>(ceil_div(c.d, kFewCols)), b.splits = p.few_splits;
+  b.acc = reinterpret_cast<float*>(ws + p.off_acc), b.out = static_cast<bf16*>(Y);
+  b.ldm = static_cast<int32_t>(round_up(c.d, 64));
+  hipLaunchKernelGGL(few_rows_kernel<false>, tile_grid(b.tiles, b.splits), dim3(kThreads), 0, s, b);
+  if (b.splits > 1) {
+    ProductArgs q{};
+    q.m = b.cols, q.n = b.N, q.halves = 1, q.splits = b.splits;
+    q.acc = b.acc, q.out = Y, q.np = kFewRows, q.ldm = b.ldm;
+    hipLaunchKernelGGL(splits_kernel<bf16>, dim3(blocks_of(c.N * ceil_div(c.d, 4), kThreads)),
+                       dim3(kThreads), 0, s, q);
+  }
   return check_launch("gated block");
 }
 
@@ -743,7 +1002,7 @@ int run_backward(const Call& c, const Plan& p, const void* X, const int8_t* x_co
     if (b.h_out) b.h_out = static_cast<T*>(b.h_out) + n0 * c.f;
     if (again) launch_gate_up<T, kZ>(b, s);
     const int64_t cols = std::max<int64_t>(p.ldh, p.ldz - p.fq);
-    with_tile(tile_for(cols, b.np, 1), [&](auto t) {
+    with_tile(whole_tile<T>(cols, b.np, c.d, kWhole), [&](auto t) {
       typedef decltype(t) G;
       const dim3 grid = tile_grid(ceil_div(cols, G::kTile), ceil_div(b.np, G::kTile)), bl(G::kThreads);
       if (again) hipLaunchKernelGGL((gate_up_grad_kernel<G, kParts<T>, false>), grid, bl, 0, s, b);
@@ -790,6 +1049,8 @@ int dpg_gated(const void* X, const void* W_in, const void* W_out, int64_t N, int
   if (const int st = check_ws(workspace, workspace_bytes, p.total)) return st;
   char* ws = static_cast<char*>(workspace);
   hipStream_t s = static_cast<hipStream_t>(stream);
+  if (few_rows(c) && aligned(X, 16) && aligned(W_in, 16) && aligned(W_out, 16))
+    return run_few(c, p, X, W_in, W_out, Y, z_codes, z_exps, ws, s);
   return dtype == DPG_BF16 ? run_forward<bf16>(c, p, X, W_in, W_out, Y, z_codes, z_exps, ws, s)
                            : run_forward<float>(c, p, X, W_in, W_out, Y, z_codes, z_exps, ws, s);
 }

@@ -172,6 +172,12 @@ template <int N> __device__ __forceinline__ void wait_vm_n() {
   __builtin_amdgcn_s_waitcnt(0x0F70 | N);
 }
 
+// The same for any N < 64.
+template <int N> __device__ __forceinline__ void wait_vm_all() {
+  static_assert(N < 64, "six bits of the count");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+}
+
 constexpr int kStepK = 64;
 // A block's tile, and the blocks of 16 x 16 in a wave's part of it. In a
 // wave's accumulator, lane l, register i of block (mb, nb) holds M = 16 mb + 4
