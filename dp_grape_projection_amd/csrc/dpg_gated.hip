@@ -50,7 +50,8 @@ struct GatedArgs {
   int32_t np;           // rows of dz and h that are written (N, or whole tiles)
   int8_t* codes;        // [N][2][fp], or null
   uint8_t* exps;        // [N][2][fp / 32]
-  float* zf;            // [N][2][ldh] Z in fp32, where it is computed again
+  bool two;             // bf16: h and dz in two parts
+  f32x4* scratch;       // a tile of dH for every resident block, where Z is computed again
   void* dz_out;         // [N][2f] the caller's dZ where h and dz are not his own
   void* h_out;          // [N][f]
 };
@@ -94,7 +95,7 @@ __device__ __forceinline__ float act_of(float x, float& slope) {
   }
 }
 template <class F>
-__device__ __forceinline__ void with_act(int act, F fn) {
+__host__ __device__ __forceinline__ void with_act(int act, F fn) {
   if (act == DPG_ACT_SILU) fn(std::integral_constant<int, DPG_ACT_SILU>{});
   else if (act == DPG_ACT_GELU) fn(std::integral_constant<int, DPG_ACT_GELU>{});
   else fn(std::integral_constant<int, DPG_ACT_GELU_TANH>{});
@@ -132,6 +133,18 @@ __global__ __launch_bounds__(kThreads) void pack_mat_kernel(const PackArgs a) {
 }
 
 // --------------------------------------------------------------- products --
+
+// LDS of a kernel of tiles, and its blocks on a CU.
+template <class G, int PARTS> constexpr int kLdsOf = PARTS == 3 ? kPartsLds<G> : G::kLds;
+template <class G, int PARTS>
+constexpr int kBlocksOf = PARTS != 3 ? G::kBlocks : G::kTile == TinyTile::kTile ? 2 : 1;
+
+template <class G, int PARTS, bool KA, bool KB>
+__device__ __forceinline__ void product(const Operand& a, const Operand& b, int n_k, char* smem,
+                                        typename G::Acc& acc) {
+  if constexpr (PARTS == 3) parts_product<G, KA, KB>(a, b, n_k, smem, acc);
+  else tile_product<G, PARTS, KA, KB>(a, b, n_k, smem, acc);
+}
 
 __device__ __forceinline__ Operand rows_of(const Mat& m, int r0, int k0) {
   return rows_operand(m.p + static_cast<int64_t>(r0) * m.ld + k0, m.ld, m.part, m.rows - r0, m.cols - k0);
@@ -186,25 +199,25 @@ __device__ __forceinline__ void store_strip(bf16* dst, f32x4 (&x)[MB], int kq, b
   }
 }
 
-// fn(std::integral_constant<int, 0>) .. <N - 1>: unrolled whatever its size, so that the
-// accumulators it indexes stay in registers.
-template <class F, int... I>
-__device__ __forceinline__ void each_of(F fn, std::integer_sequence<int, I...>) {
-  (fn(std::integral_constant<int, I>{}), ...);
+// store_strip of values in bf16: once, and with `two` (TWO: it may be set) what that left
+// over to dst + part.
+template <int MB, bool TWO>
+__device__ __forceinline__ void store_strips(bf16* dst, int64_t part, bool two, f32x4 (&x)[MB], int kq,
+                                             bool row, int n) {
+  store_strip<MB, 1>(dst, x, kq, row, n);
+  if (!TWO || !two) return;
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // (an infinity leaves nothing)
+      x[mb][i] = fabsf(x[mb][i]) < INFINITY ? x[mb][i] - static_cast<float>(from_float<bf16>(x[mb][i])) : 0.0f;
+  store_strip<MB, 1>(dst + part, x, kq, row, n);
 }
-template <int N, class F>
-__device__ __forceinline__ void each(F fn) {
-  each_of(fn, std::make_integer_sequence<int, N>{});
-}
-
-// What the tile of both projections leaves: H for the next product, with or without the
-// 8-bit form of G and U, or G and U alone in fp32.
-enum { kH = 0, kHAndCodes = 1, kZ = 2 };
 
 // A tile of G and U: TILE / 2 columns of each by TILE rows.
-template <class G, int PARTS, int OUT>
-__global__ __launch_bounds__(G::kThreads, G::kBlocks) void gate_up_kernel(const GatedArgs a) {
-  __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
+template <class G, int PARTS, int ACT, bool CODES>
+__global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void gate_up_kernel(const GatedArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[kLdsOf<G, PARTS>];
   constexpr int kCols = G::kTile / 2, kHB = G::kMB / 2;  // columns of H; blocks of a half
   int mt, nt;
   if (!tile_of_block(blockIdx.x, (a.ldh + kCols - 1) / kCols, (a.N + G::kTile - 1) / G::kTile, mt, nt))
@@ -217,91 +230,150 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void gate_up_kernel(const 
   w.cols = a.fq - min(c0, a.fq - 8);
   w.half = a.fq;
   typename G::Acc acc;
-  tile_product<G, PARTS, true, false>(w, rows_of(a.x, r0, 0), (a.d + kStepK - 1) / kStepK, smem, acc);
+  product<G, PARTS, true, false>(w, rows_of(a.x, r0, 0), (a.d + kStepK - 1) / kStepK, smem, acc);
   const int cw = c0 + 16 * kHB * wm;  // the wave's first column of H
-  if constexpr (OUT == kZ) {
-#pragma unroll
-    for (int nb = 0; nb < G::kNB; ++nb) {
+  with_edge(r0 + G::kTile > a.N || c0 + kCols > a.f, [&](auto edge) {
+    constexpr bool E = decltype(edge)::value;
+    each<G::kNB>([&](auto at) {
+      constexpr int nb = decltype(at)::value;
       const int r = r0 + G::kWaveN * wn + 16 * nb + r16;
-      if (r >= a.N) continue;
+      const bool row = !E || r < a.N;
+      f32x4 g[kHB], u[kHB];
 #pragma unroll
-      for (int mb = 0; mb < G::kMB; ++mb) {
-        const int h = mb / kHB, c = cw + 16 * (mb % kHB) + 4 * kq;
-        if (c < a.ldh)
-          *reinterpret_cast<f32x4*>(a.zf + (2 * static_cast<int64_t>(r) + h) * a.ldh + c) = acc.v[mb][nb];
-      }
-    }
-  } else {
-    with_edge(r0 + G::kTile > a.N || c0 + kCols > a.f, [&](auto edge) {
-      constexpr bool E = decltype(edge)::value;
-      each<G::kNB>([&](auto at) {
-        constexpr int nb = decltype(at)::value;
-        const int r = r0 + G::kWaveN * wn + 16 * nb + r16;
-        const bool row = !E || r < a.N;
-        f32x4 g[kHB], u[kHB];
+      for (int mb = 0; mb < kHB; ++mb)
 #pragma unroll
-        for (int mb = 0; mb < kHB; ++mb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool there = !E || cw + 16 * mb + 4 * kq + i < a.f;
-            g[mb][i] = there ? acc.v[mb][nb][i] : 0.0f;
-            u[mb][i] = there ? acc.v[kHB + mb][nb][i] : 0.0f;
-          }
-        if constexpr (OUT == kHAndCodes) {
-          uint32_t code[2][kHB], e[2][kHB / 2];
-#pragma unroll
-          for (int p = 0; p < kHB / 2; ++p) {
-            codes_of_block(g[2 * p], g[2 * p + 1], code[0][2 * p], code[0][2 * p + 1], e[0][p]);
-            codes_of_block(u[2 * p], u[2 * p + 1], code[1][2 * p], code[1][2 * p + 1], e[1][p]);
-          }
-          const int64_t rz = 2 * static_cast<int64_t>(r);
-          // 64 bytes of a row by four lanes: of one half, or half of that of both
-#pragma unroll
-          for (int o = 0; o < kHB / 2; ++o) {
-            u32x4 x = kHB == 4 ? u32x4{code[o][0], code[o][1], code[o][2], code[o][3]}
-                               : u32x4{code[0][0], code[0][1], code[1][0], code[1][1]};
-            transpose4(x);
-            const int h = kHB == 4 ? o : kq >> 1, c = cw + 16 * (kHB == 4 ? kq : kq & 1);
-            if (row && (!E || c < a.fp)) *reinterpret_cast<any_u32x4*>(a.codes + (rz + h) * a.fp + c) = x;
-          }
-          // and the exponents of its blocks by as many lanes as there are
-          constexpr int kP = kHB / 2;
-          const int h = kq / kP, p = kq % kP, c = cw + 32 * p;
-          const uint32_t b = h == 0 ? (p == 0 ? e[0][0] : e[0][kP - 1]) : (p == 0 ? e[1][0] : e[1][kP - 1]);
-          if (h < 2 && row && (!E || c < a.fp))
-            a.exps[(rz + h) * (a.fp / kBlock8) + c / kBlock8] = static_cast<uint8_t>(b);
+        for (int i = 0; i < 4; ++i) {
+          const bool there = !E || cw + 16 * mb + 4 * kq + i < a.f;
+          g[mb][i] = there ? acc.v[mb][nb][i] : 0.0f;
+          u[mb][i] = there ? acc.v[kHB + mb][nb][i] : 0.0f;
         }
-        with_act(a.act, [&](auto act) {
+      if constexpr (CODES) {
+        uint32_t code[2][kHB], e[2][kHB / 2];
 #pragma unroll
-          for (int mb = 0; mb < kHB; ++mb)
+        for (int p = 0; p < kHB / 2; ++p) {
+          codes_of_block(g[2 * p], g[2 * p + 1], code[0][2 * p], code[0][2 * p + 1], e[0][p]);
+          codes_of_block(u[2 * p], u[2 * p + 1], code[1][2 * p], code[1][2 * p + 1], e[1][p]);
+        }
+        const int64_t rz = 2 * static_cast<int64_t>(r);
+        // 64 bytes of a row by four lanes: of one half, or half of that of both
 #pragma unroll
-            for (int i = 0; i < 4; ++i) g[mb][i] = act_of<decltype(act)::value>(g[mb][i]) * u[mb][i];
-        });
-        bf16* const dst = const_cast<bf16*>(a.h.p) + static_cast<int64_t>(r) * a.h.ld + cw;
+        for (int o = 0; o < kHB / 2; ++o) {
+          u32x4 x = kHB == 4 ? u32x4{code[o][0], code[o][1], code[o][2], code[o][3]}
+                             : u32x4{code[0][0], code[0][1], code[1][0], code[1][1]};
+          transpose4(x);
+          const int h = kHB == 4 ? o : kq >> 1, c = cw + 16 * (kHB == 4 ? kq : kq & 1);
+          if (row && (!E || c < a.fp)) *reinterpret_cast<any_u32x4*>(a.codes + (rz + h) * a.fp + c) = x;
+        }
+        // and the exponents of its blocks by as many lanes as there are
+        constexpr int kP = kHB / 2;
+        const int h = kq / kP, p = kq % kP, c = cw + 32 * p;
+        const uint32_t b = h == 0 ? (p == 0 ? e[0][0] : e[0][kP - 1]) : (p == 0 ? e[1][0] : e[1][kP - 1]);
+        if (h < 2 && row && (!E || c < a.fp))
+          a.exps[(rz + h) * (a.fp / kBlock8) + c / kBlock8] = static_cast<uint8_t>(b);
+      }
+#pragma unroll
+      for (int mb = 0; mb < kHB; ++mb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[mb][i] = act_of<ACT>(g[mb][i]) * u[mb][i];
+      bf16* const dst = const_cast<bf16*>(a.h.p) + static_cast<int64_t>(r) * a.h.ld + cw;
+      const int n = E ? a.ldh - cw : 16 * kHB;
+      if constexpr (PARTS == 1) {
+        store_strips<kHB, (G::kTile < BigTile::kTile)>(dst, a.h.part, a.two, g, kq, row, n);
+      } else {
 #pragma unroll
         for (int part = 0; part < PARTS; ++part)
-          store_strip<kHB, PARTS>(dst + part * a.h.part, g, kq, row, E ? a.ldh - cw : 16 * kHB);
-      });
+          store_strip<kHB, PARTS>(dst + part * a.h.part, g, kq, row, n);
+      }
     });
-  }
+  });
 }
 
-// A tile of dH, from which dG, dU and H follow; CODES: G and U are read from their 8-bit
-// form, else from zf.
-template <class G, int PARTS, bool CODES>
-__global__ __launch_bounds__(G::kThreads, G::kBlocks) void gate_up_grad_kernel(const GatedArgs a) {
-  __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
+// From G, U and dH of MB blocks of 16 columns of row r from column co on: dG, dU and H,
+// written. E: the tile has rows or columns that do not exist, which are zero.
+template <int MB, int PARTS, int ACT, bool TWO, bool E>
+__device__ __forceinline__ void grad_strip(const GatedArgs& a, int r, int co, int kq, f32x4 (&dg)[MB],
+                                           f32x4 (&du)[MB], const f32x4 (&dh)[MB]) {
+  constexpr int kAll = 16 * MB;
+  const bool row = !E || r < a.N;
+  f32x4 hv[MB];
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool there = !E || (row && co + 16 * mb + 4 * kq + i < a.f);
+      const float u = du[mb][i];
+      float slope;
+      const float v = act_of<ACT>(dg[mb][i], slope);
+      hv[mb][i] = there ? v * u : 0.0f;
+      du[mb][i] = there ? dh[mb][i] * v : 0.0f;
+      dg[mb][i] = there ? dh[mb][i] * u * slope : 0.0f;
+    }
+  // the caller's own arrays, rows of 2 f and of f
+  const int64_t own = static_cast<int64_t>(r) * a.f + co;
+  if (!a.dz_out && !a.h_out) {
+  } else if constexpr (PARTS == 3) {
+    auto store = [&](float* p, const f32x4 (&x)[MB]) {
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        const int c = 16 * mb + 4 * kq;
+        if (row && co + c < a.f) store_row(p + c, a.f - co - c, x[mb]);
+      }
+    };
+    if (float* const z = static_cast<float*>(a.dz_out)) {
+      store(z + own + static_cast<int64_t>(r) * a.f, dg);
+      store(z + own + static_cast<int64_t>(r + 1) * a.f, du);
+    }
+    if (a.h_out) store(static_cast<float*>(a.h_out) + own, hv);
+  } else {
+    const int n = E ? a.f - co : kAll;
+    if (bf16* const z = static_cast<bf16*>(a.dz_out)) {
+      store_strip<MB, 1>(z + own + static_cast<int64_t>(r) * a.f, dg, kq, row, n);
+      store_strip<MB, 1>(z + own + static_cast<int64_t>(r + 1) * a.f, du, kq, row, n);
+    }
+    if (a.h_out) store_strip<MB, 1>(static_cast<bf16*>(a.h_out) + own, hv, kq, row, n);
+  }
+  // (rows from N on are written up to np, columns up to the end of the padding)
+  const bool there = !E || r < a.np;
+  bf16* const dz = const_cast<bf16*>(a.dz.p) + static_cast<int64_t>(r) * a.dz.ld + co;
+  bf16* const h = const_cast<bf16*>(a.h.p) + static_cast<int64_t>(r) * a.h.ld + co;
+  const int ng = E ? a.fq - co : kAll, nu = E ? static_cast<int>(a.dz.ld) - a.fq - co : kAll,
+            nh = E ? static_cast<int>(a.h.ld) - co : kAll;
+  if constexpr (PARTS == 1) {
+    store_strips<MB, TWO>(dz, a.dz.part, a.two, dg, kq, there, ng);
+    store_strips<MB, TWO>(dz + a.fq, a.dz.part, a.two, du, kq, there, nu);
+    store_strips<MB, TWO>(h, a.h.part, a.two, hv, kq, there, nh);
+  } else {
+#pragma unroll
+    for (int part = 0; part < PARTS; ++part) {
+      store_strip<MB, PARTS>(dz + part * a.dz.part, dg, kq, there, ng);
+      store_strip<MB, PARTS>(dz + part * a.dz.part + a.fq, du, kq, there, nu);
+      store_strip<MB, PARTS>(h + part * a.h.part, hv, kq, there, nh);
+    }
+  }
+  __builtin_amdgcn_sched_barrier(0);  // (interleaved strips would need more registers)
+}
+
+// Columns that the gradient's tiles cover: up to the end of the padding of H and of dZ's
+// second half.
+__host__ __device__ __forceinline__ int grad_cols(const GatedArgs& a) {
+  const int u = static_cast<int>(a.dz.ld) - a.fq;
+  return a.ldh > u ? a.ldh : u;
+}
+
+// A tile of dH, from which with G and U in their 8-bit form dG, dU and H follow.
+template <class G, int PARTS, int ACT>
+__global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void gate_up_grad_kernel(const GatedArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[kLdsOf<G, PARTS>];
   int mt, nt;
-  // columns up to the end of the padding of H and of dZ's second half
-  const int cols = max(a.ldh, static_cast<int>(a.dz.ld) - a.fq);
-  if (!tile_of_block(blockIdx.x, (cols + G::kTile - 1) / G::kTile, (a.np + G::kTile - 1) / G::kTile, mt, nt))
+  if (!tile_of_block(blockIdx.x, (grad_cols(a) + G::kTile - 1) / G::kTile,
+                     (a.np + G::kTile - 1) / G::kTile, mt, nt))
     return;
   const int c0 = mt * G::kTile, r0 = nt * G::kTile;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
   typename G::Acc acc;
   // (rows and columns past the last compute the last ones again, and are written as zero)
-  tile_product<G, PARTS, false, false>(rows_of(a.w_out, min(c0, a.f - 1), 0),
+  product<G, PARTS, false, false>(rows_of(a.w_out, min(c0, a.f - 1), 0),
                                        rows_of(a.dy, min(r0, a.N - 1), 0),
                                        (a.d + kStepK - 1) / kStepK, smem, acc);
   const int cw = c0 + G::kWaveM * wm;  // the wave's first column
@@ -325,88 +397,83 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void gate_up_grad_kernel(c
                                (E ? min(c + 32 * p, a.fp - 32) : c + 32 * p) / kBlock8];
       }
     };
-    if constexpr (CODES) load(0, 0, 0);
+    load(0, 0, 0);
     each<G::kNB * kO>([&](auto at) {
       constexpr int t = decltype(at)::value, nb = t / kO, o = t % kO, cur = t & 1;
-      const int r = r0 + G::kWaveN * wn + 16 * nb + r16, co = cw + 64 * o;
-      const bool row = !E || r < a.N;
-      f32x4 dg[4], du[4], hv[4];
-      // G into dg and U into du first
-      if constexpr (CODES) {
-        if constexpr (t + 1 < G::kNB * kO) load((t + 1) / kO, (t + 1) % kO, cur ^ 1);
-        transpose4(code[cur][0]);
-        transpose4(code[cur][1]);
+      if constexpr (t + 1 < G::kNB * kO) load((t + 1) / kO, (t + 1) % kO, cur ^ 1);
+      transpose4(code[cur][0]);
+      transpose4(code[cur][1]);
+      f32x4 g[4], u[4], dh[4];
 #pragma unroll
-        for (int mb = 0; mb < 4; ++mb) {
-          const float sg = step8(e[cur][0][mb / 2]), su = step8(e[cur][1][mb / 2]);
+      for (int mb = 0; mb < 4; ++mb) {
+        const float sg = step8(e[cur][0][mb / 2]), su = step8(e[cur][1][mb / 2]);
+        dh[mb] = acc.v[4 * o + mb][nb];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            dg[mb][i] = value8(code[cur][0][mb], i, sg);
-            du[mb][i] = value8(code[cur][1][mb], i, su);
-          }
-        }
-      } else {
-        const int64_t rz = 2 * static_cast<int64_t>(E ? min(r, a.N - 1) : r);
-#pragma unroll
-        for (int mb = 0; mb < 4; ++mb) {
-          const int c = co + 16 * mb + 4 * kq;
-          const float* z = a.zf + rz * a.ldh + (E ? min(c, a.ldh - 4) : c);
-          dg[mb] = *reinterpret_cast<const f32x4*>(z);
-          du[mb] = *reinterpret_cast<const f32x4*>(z + a.ldh);
+        for (int i = 0; i < 4; ++i) {
+          g[mb][i] = value8(code[cur][0][mb], i, sg);
+          u[mb][i] = value8(code[cur][1][mb], i, su);
         }
       }
-      with_act(a.act, [&](auto act) {
-#pragma unroll
-        for (int mb = 0; mb < 4; ++mb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool there = !E || (row && co + 16 * mb + 4 * kq + i < a.f);
-            const float dh = acc.v[4 * o + mb][nb][i], u = du[mb][i];
-            float slope;
-            const float v = act_of<decltype(act)::value>(dg[mb][i], slope);
-            hv[mb][i] = there ? v * u : 0.0f;
-            du[mb][i] = there ? dh * v : 0.0f;
-            dg[mb][i] = there ? dh * u * slope : 0.0f;
-          }
-      });
-      // the caller's own arrays, rows of 2 f and of f
-      const int64_t own = static_cast<int64_t>(r) * a.f + co;
-      if constexpr (PARTS == 3) {
-        auto store = [&](float* p, const f32x4 (&x)[4]) {
-#pragma unroll
-          for (int mb = 0; mb < 4; ++mb) {
-            const int c = 16 * mb + 4 * kq;
-            if (row && co + c < a.f) store_row(p + c, a.f - co - c, x[mb]);
-          }
-        };
-        float* const z = static_cast<float*>(a.dz_out);
-        if (z) store(z + own + static_cast<int64_t>(r) * a.f, dg), store(z + own + static_cast<int64_t>(r + 1) * a.f, du);
-        if (a.h_out) store(static_cast<float*>(a.h_out) + own, hv);
-      } else {
-        bf16* const z = static_cast<bf16*>(a.dz_out);
-        const int n = E ? a.f - co : 64;
-        if (z) {
-          store_strip<4, 1>(z + own + static_cast<int64_t>(r) * a.f, dg, kq, row, n);
-          store_strip<4, 1>(z + own + static_cast<int64_t>(r + 1) * a.f, du, kq, row, n);
-        }
-        if (a.h_out) store_strip<4, 1>(static_cast<bf16*>(a.h_out) + own, hv, kq, row, n);
-      }
-      // (rows from N on are written up to np, columns up to the end of the padding)
-      const bool there = !E || r < a.np;
-      bf16* const dz = const_cast<bf16*>(a.dz.p) + static_cast<int64_t>(r) * a.dz.ld + co;
-      bf16* const h = const_cast<bf16*>(a.h.p) + static_cast<int64_t>(r) * a.h.ld + co;
-#pragma unroll
-      for (int part = 0; part < PARTS; ++part) {
-        const int64_t off = part * a.dz.part;
-        store_strip<4, PARTS>(dz + off, dg, kq, there, E ? a.fq - co : 64);
-        store_strip<4, PARTS>(dz + off + a.fq, du, kq, there,
-                              E ? static_cast<int>(a.dz.ld) - a.fq - co : 64);
-        store_strip<4, PARTS>(h + part * a.h.part, hv, kq, there,
-                              E ? static_cast<int>(a.h.ld) - co : 64);
-      }
-      __builtin_amdgcn_sched_barrier(0);  // (interleaved steps would need more registers)
+      grad_strip<4, PARTS, ACT, (G::kTile < BigTile::kTile), E>(a, r0 + G::kWaveN * wn + 16 * nb + r16, cw + 64 * o, kq, g, u, dh);
     });
   });
+}
+
+// The same with G and U computed again: a block takes tiles in turn, computes dH, puts it
+// where only it reads, and then both projections of the same columns, half of a wave's at
+// a time, in the places where the wave had dH. Two products with fp32 results between them
+// would write and read 12 bytes for every element of dH (TIMES).
+template <class G, int PARTS, int ACT>
+__global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void gate_up_again_kernel(const GatedArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[kLdsOf<G, PARTS>];
+  constexpr int kHB = G::kMB / 2;
+  const int mts = (grad_cols(a) + G::kTile - 1) / G::kTile, nts = (a.np + G::kTile - 1) / G::kTile;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
+  const int steps = (a.d + kStepK - 1) / kStepK, all = (mts * nts + 7) / 8 * 8;
+  f32x4* const mine = a.scratch + static_cast<int64_t>(blockIdx.x) * (G::kMB * G::kNB * G::kThreads) + tid;
+  for (int block = blockIdx.x; block < all; block += gridDim.x) {
+    int mt, nt;
+    if (!tile_of_block(block, mts, nts, mt, nt)) continue;
+    const int c0 = mt * G::kTile, r0 = nt * G::kTile;
+    typename G::Acc acc;
+    __syncthreads();  // the last tile's fragments have been read
+    product<G, PARTS, false, false>(rows_of(a.w_out, min(c0, a.f - 1), 0),
+                                         rows_of(a.dy, min(r0, a.N - 1), 0), steps, smem, acc);
+#pragma unroll
+    for (int mb = 0; mb < G::kMB; ++mb)
+#pragma unroll
+      for (int nb = 0; nb < G::kNB; ++nb) mine[(mb * G::kNB + nb) * G::kThreads] = acc.v[mb][nb];
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      const int ch = c0 + half * (G::kWaveM / 2), cb = min(ch, a.fq - 8);
+      Operand w = kmajor_of(a.w_in, 0, cb);
+      w.cols = a.fq - cb;
+      w.half = a.fq;
+      w.apart = true;
+      __syncthreads();
+      product<G, PARTS, true, false>(w, rows_of(a.x, min(r0, a.N - 1), 0), steps, smem, acc);
+      const int cw = ch + G::kWaveM * wm;  // the wave's first column of this half
+      const f32x4* const dhs = mine + half * (kHB * G::kNB * G::kThreads);
+      with_edge(r0 + G::kTile > a.N || c0 + G::kTile > a.f, [&](auto edge) {
+        constexpr bool E = decltype(edge)::value;
+        f32x4 dh[2][kHB];
+        auto load = [&](int nb, int to) {
+#pragma unroll
+          for (int mb = 0; mb < kHB; ++mb) dh[to][mb] = dhs[(mb * G::kNB + nb) * G::kThreads];
+        };
+        load(0, 0);
+        each<G::kNB>([&](auto at) {
+          constexpr int nb = decltype(at)::value;
+          if constexpr (nb + 1 < G::kNB) load(nb + 1, (nb + 1) & 1);
+          f32x4 g[kHB], u[kHB];
+#pragma unroll
+          for (int mb = 0; mb < kHB; ++mb) g[mb] = acc.v[mb][nb], u[mb] = acc.v[kHB + mb][nb];
+          grad_strip<kHB, PARTS, ACT, (G::kTile < BigTile::kTile), E>(a, r0 + G::kWaveN * wn + 16 * nb + r16, cw, kq, g, u, dh[nb & 1]);
+        });
+      });
+    }
+  }
 }
 
 // out[n][h m + c] = sum_k b[n][k] a[h][c][k] for the halves h of A (its columns or rows
@@ -422,10 +489,9 @@ struct ProductArgs {
   int32_t np, ldm;     // rows, and halves times m rounded up to 64
 };
 
-template <class G, typename T, bool KA, bool KB>
-__global__ __launch_bounds__(G::kThreads, G::kBlocks) void product_kernel(const ProductArgs a) {
-  constexpr int PARTS = kParts<T>;
-  __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
+template <class G, typename T, int PARTS, bool KA, bool KB>
+__global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void product_kernel(const ProductArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[kLdsOf<G, PARTS>];
   const int mh = (a.m + G::kTile - 1) / G::kTile, nh = (a.n + G::kTile - 1) / G::kTile;
   int mt, nt;
   if (!tile_of_block(blockIdx.x, mh * a.halves, nh * a.splits, mt, nt)) return;
@@ -442,7 +508,7 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void product_kernel(const 
   if constexpr (KB) ob = kmajor_of(a.b, kk, n0);
   else ob = rows_of(a.b, n0, kk);
   typename G::Acc acc;
-  tile_product<G, PARTS, KA, KB>(oa, ob, k1 - k0, smem, acc);
+  product<G, PARTS, KA, KB>(oa, ob, k1 - k0, smem, acc);
   if (a.splits > 1) {
     const int c = half * (a.ldm / a.halves) + m0;
     add_tile<G>(a.acc + (static_cast<int64_t>(split) * a.np + n0) * a.ldm + c, a.ldm,
@@ -452,7 +518,7 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void product_kernel(const 
   const int64_t ld = static_cast<int64_t>(a.halves) * a.m;
   T* dst = static_cast<T*>(a.out) + n0 * ld + half * a.m + m0;
   const int n_rows = a.n - n0, n_cols = a.m - m0;
-  if constexpr (PARTS == 1) {
+  if constexpr (sizeof(T) == 2) {
     write_tile<G>(smem, dst, ld, n_rows, n_cols,
                   [&](int nb, int mb, int i) { return from_float<bf16>(acc.v[mb][nb][i]); });
   } else {
@@ -681,35 +747,45 @@ __global__ __launch_bounds__(kThreads, 1) void few_rows_kernel(const FewArgs a) 
 // ------------------------------------------------------------------- host --
 
 enum Tile { kBig, kSmall, kTiny };
-template <class F>
+// (three parts have no big tiles: their six tiles of a K step would not fit LDS)
+template <int PARTS, class F>
 void with_tile(Tile t, F fn) {
-  if (t == kBig) fn(BigTile());
-  else if (t == kSmall) fn(SmallTile());
-  else fn(TinyTile());
+  if constexpr (PARTS != 3) {
+    if (t == kBig) return fn(BigTile());
+  }
+  if (t == kTiny) fn(TinyTile());
+  else fn(SmallTile());
 }
 
-// Tiles and splits of a product of m x n outputs over `steps` K steps of `combos`
-// products each; of G and U together, whose tiles have half their width of columns of
-// either and which needs all of K, as dH does (`whole`).
+// Blocks that the chip holds.
+int64_t resident(Tile t, int parts) {
+  if (parts == 3) return t == kTiny ? 512 : 256;
+  return t == kBig ? 256 : t == kSmall ? 512 : 1024;
+}
+
+// Tiles and splits of a product of m x n outputs over `steps` K steps, of operands in
+// `parts`; of G and U together, whose tiles have half their width of columns of either
+// and which needs all of K, as dH does (kWhole) and the three products of kAgain.
 // Modelled on 300 measurements: with c blocks on a CU, a K step takes 1.05 + 0.5 c us in a
 // big tile, 0.5 max(1, c) in a small one, 0.34 + 0.13 (c - 1) in a tiny one, a fifth more
-// where both operands are read transposed; outputs and partial sums are written at 5.6
-// TB/s, and adding those up is a launch of 2.5 us and 6.5 TB/s. (dW_out of 16384 x 768 x
-// 2048: 64 us in small tiles with 5 splits, 65 big with 10, 90 tiny with 2; of 128 x 64 x
-// 256: 3.6 tiny, 4.5 small, 7.9 big. dX of 2048 x 2048 x 4096: 67 us in small tiles, 73 big
-// with 4 splits, 99 tiny.)
+// where both operands are read transposed; in three parts PARTSTIMES; outputs and partial
+// sums are written at 5.6 TB/s, and adding those up is a launch of 2.5 us and 6.5 TB/s.
+// (dW_out of 16384 x 768 x 2048: 64 us in small tiles with 5 splits, 65 big with 10, 90
+// tiny with 2; of 128 x 64 x 256: 3.6 tiny, 4.5 small, 7.9 big. dX of 2048 x 2048 x 4096:
+// 67 us in small tiles, 73 big with 4 splits, 99 tiny.)
 struct Choice {
   Tile tile;
   int32_t splits;
 };
-enum Kind { kPlain, kBothTransposed, kGateUp, kWhole };
-Choice choose(int64_t m, int64_t n, int64_t steps, int combos, Kind kind) {
+enum Kind { kPlain, kBothTransposed, kGateUp, kWhole, kAgain };
+Choice choose(int64_t m, int64_t n, int64_t steps, int parts, Kind kind) {
   Choice best{kTiny, 1};
   double best_us = 1e30;
   const double mn = static_cast<double>(m) * static_cast<double>(n) / 1e6;
   for (const Tile t : {kBig, kSmall, kTiny}) {
+    if (parts == 3 && t == kBig) continue;
     const int64_t tile = t == kBig ? BigTile::kTile : t == kSmall ? SmallTile::kTile : TinyTile::kTile;
-    const int64_t slots = t == kBig ? 256 : t == kSmall ? 512 : 1024;
+    const int64_t slots = resident(t, parts);
     const int64_t tiles = ceil_div(m, kind == kGateUp ? tile / 2 : tile) * ceil_div(n, tile);
     const int64_t most = kind <= kBothTransposed ? std::max<int64_t>(1, std::min(slots / tiles, steps)) : 1;
     // (every count up to 16, then steps of an eighth, and the most)
@@ -719,8 +795,11 @@ Choice choose(int64_t m, int64_t n, int64_t steps, int combos, Kind kind) {
       double step = t == kBig ? 1.05 + 0.5 * c : t == kSmall ? 0.5 * std::max(1.0, c)
                                                              : 0.34 + 0.13 * std::max(0.0, c - 1.0);
       if (kind == kBothTransposed) step *= 1.2;
+      if (parts == kTwo) step *= 2;
+      if (parts == 3) step = (t == kSmall ? 2.5 : 1.05 * std::max(1.0, c)) * (kind == kBothTransposed ? 1.15 : 1.0);
       const double around = t == kBig ? 5.0 : t == kSmall ? 3.5 : 3.0;
-      double us = static_cast<double>(rounds) * (static_cast<double>(ceil_div(steps, k) * combos) * step + around);
+      double us = static_cast<double>(rounds) *
+                  (static_cast<double>(ceil_div(steps, k) * (kind == kAgain ? 3 : 1)) * step + around);
       us += mn * (k > 1 ? 4.0 * static_cast<double>(k) : 2.0) / 5.6;
       if (k > 1) us += 2.5 + mn * (4.0 * static_cast<double>(k) + 2.0) / 6.5;
       if (us < best_us) best_us = us, best = {t, static_cast<int32_t>(k)};
@@ -748,16 +827,19 @@ int check_call(const Call& c) {
   return DPG_OK;
 }
 
-// Rows whose Z in fp32 is kept at a time where it is computed again.
-constexpr int64_t kZBytes = 256ll << 20;
+// With few rows of bf16, H and dZ stay in two parts: the products they enter cost twice
+// as much, but an output of few values then has one rounding and not two (TWOTIMES).
+constexpr int64_t kTwoRows = 64;
 
 // Where everything lies in the workspace. Copies of the operands are planned whatever
 // their alignment, since a size depends on shapes alone.
 struct Plan {
-  int64_t parts, ldx, ldh, fq, ldz, np, fp, z_rows = 0;
-  Choice y{}, x{}, wi{}, wo{};
+  int64_t parts, ldx, ldh, fq, ldz, np, fp;
+  bool two;  // H and dZ in two parts
+  Choice y{}, x{}, wi{}, wo{}, again{};
+  int64_t again_blocks = 0;
   int32_t few_splits = 0;  // few rows: parts of f in the second product
-  size_t off_x, off_wi, off_wo, off_dy, off_h, off_dz = 0, off_zf = 0, off_x8 = 0, off_acc, total;
+  size_t off_x, off_wi, off_wo, off_dy, off_h, off_dz = 0, off_scratch = 0, off_x8 = 0, off_acc, total;
 };
 
 // Few rows of bf16 in whole K steps go their own way where the weights are 16-byte
@@ -779,7 +861,7 @@ Plan plan_gated(const Call& c, bool grad, bool again, bool weights) {
   p.ldz = round_up(2 * p.fq, kStepK);
   p.fp = round_up(c.f, kBlock8);
   p.np = round_up(c.N, kPad);
-  const int combos = p.parts == 1 ? 1 : Combos<3>::n;
+  const int parts = static_cast<int>(p.parts), later = c.dtype == DPG_BF16 && c.N <= kTwoRows ? kTwo : parts;
   size_t off = 0, acc = 0;
   auto take = [&](int64_t elems, int64_t size) {
     const size_t at = off;
@@ -790,9 +872,11 @@ Plan plan_gated(const Call& c, bool grad, bool again, bool weights) {
   p.off_wi = take(p.parts * c.d * p.ldz, 2);
   p.off_wo = take(p.parts * c.f * p.ldx, 2);
   p.off_dy = take(grad ? p.parts * c.N * p.ldx : 0, 2);
-  p.off_h = take(p.parts * p.np * p.ldh, 2);
+  p.two = c.dtype == DPG_BF16 && c.N <= kTwoRows;
+  const int64_t made = p.two ? 2 : p.parts;  // parts of what the kernels make
+  p.off_h = take(made * p.np * p.ldh, 2);
   if (!grad) {
-    p.y = choose(c.d, c.N, p.ldh / kStepK, combos, kPlain);
+    p.y = choose(c.d, c.N, p.ldh / kStepK, later, kPlain);
     acc = acc_bytes(p.y, 1, c.d, c.N);
     if (few_rows(c)) {
       // about a block for every CU, each wave with four steps at least
@@ -802,16 +886,25 @@ Plan plan_gated(const Call& c, bool grad, bool again, bool weights) {
       acc = std::max<size_t>(acc, p.few_splits * kFewRows * round_up(c.d, 64) * 4);
     }
   } else {
-    p.off_dz = take(p.parts * p.np * p.ldz, 2);
+    p.off_dz = take(made * p.np * p.ldz, 2);
     if (again) {
-      p.z_rows = std::min(p.np, std::max<int64_t>(kPad, kZBytes / (p.ldh * 8) / kPad * kPad));
-      p.off_zf = take(p.z_rows * 2 * p.ldh, 4);
+      // three products in one kernel, whose blocks are as many as the chip holds at most
+      const int64_t cols = std::max(p.ldh, p.ldz - p.fq);
+      p.again = choose(cols, c.N, ceil_div(c.d, kStepK), parts, kAgain);
+      auto blocks = [&](auto g) {
+        typedef decltype(g) G;
+        const int64_t tiles = round_up(ceil_div(cols, G::kTile) * ceil_div(p.np, G::kTile), 8);
+        p.again_blocks = std::min(tiles, resident(p.again.tile, parts));
+        p.off_scratch = take(p.again_blocks * G::kTile * G::kTile, 4);
+      };
+      if (p.parts == 3) with_tile<3>(p.again.tile, blocks);
+      else with_tile<1>(p.again.tile, blocks);
     }
-    p.x = choose(c.d, c.N, p.ldz / kStepK, combos, kPlain);
+    p.x = choose(c.d, c.N, p.ldz / kStepK, later, kPlain);
     acc = acc_bytes(p.x, 1, c.d, c.N);
     if (weights) {
-      p.wi = choose(2 * c.f, c.d, ceil_div(c.N, kStepK), combos, kBothTransposed);
-      p.wo = choose(c.d, c.f, ceil_div(c.N, kStepK), combos, kBothTransposed);
+      p.wi = choose(2 * c.f, c.d, ceil_div(c.N, kStepK), later, kBothTransposed);
+      p.wo = choose(c.d, c.f, ceil_div(c.N, kStepK), later, kBothTransposed);
       acc = std::max({acc, acc_bytes(p.wi, 2, c.f, c.d), acc_bytes(p.wo, 1, c.d, c.f)});
       p.off_x8 = take(c.N * p.ldx, c.dtype == DPG_BF16 ? 2 : 4);
     }
@@ -838,7 +931,8 @@ struct Operands {
     j = {src, reinterpret_cast<bf16*>(ws + off), ld, rows * ld, static_cast<int32_t>(rows),
          static_cast<int32_t>(cols), static_cast<int32_t>(halves), static_cast<int32_t>(half), pack.waves};
     pack.waves += rows * halves;
-    return {j.dst, ld, j.part, static_cast<int32_t>(rows), static_cast<int32_t>(ld)};
+    // (one part has no other: 0 apart, for the products whose other operand has two)
+    return {j.dst, ld, bf16_in ? 0 : j.part, static_cast<int32_t>(rows), static_cast<int32_t>(ld)};
   }
   void launch(hipStream_t s) {
     if (!pack.n) return;
@@ -854,28 +948,31 @@ GatedArgs make_args(const Call& c, const Plan& p) {
   a.N = static_cast<int32_t>(c.N), a.d = static_cast<int32_t>(c.d), a.f = static_cast<int32_t>(c.f);
   a.fq = static_cast<int32_t>(p.fq), a.act = c.act;
   a.ldh = static_cast<int32_t>(p.ldh), a.fp = static_cast<int32_t>(p.fp);
+  a.two = p.two;
   return a;
 }
 
 // The tiles of the kernels that need all of K: of G and U, of dH.
 template <typename T>
 Tile whole_tile(int64_t m, int64_t n, int64_t d, Kind kind) {
-  return choose(m, n, ceil_div(d, kStepK), Combos<kParts<T>>::n, kind).tile;
+  return choose(m, n, ceil_div(d, kStepK), kParts<T>, kind).tile;
 }
 
-template <typename T, int OUT>
+template <typename T, bool CODES>
 void launch_gate_up(const GatedArgs& a, hipStream_t s) {
-  with_tile(whole_tile<T>(a.ldh, a.N, a.d, kGateUp), [&](auto g) {
+  with_tile<kParts<T>>(whole_tile<T>(a.ldh, a.N, a.d, kGateUp), [&](auto g) {
     typedef decltype(g) G;
-    hipLaunchKernelGGL((gate_up_kernel<G, kParts<T>, OUT>),
-                       tile_grid(ceil_div(a.ldh, G::kTile / 2), ceil_div(a.N, G::kTile)),
-                       dim3(G::kThreads), 0, s, a);
+    with_act(a.act, [&](auto act) {
+      hipLaunchKernelGGL((gate_up_kernel<G, kParts<T>, decltype(act)::value, CODES>),
+                         tile_grid(ceil_div(a.ldh, G::kTile / 2), ceil_div(a.N, G::kTile)),
+                         dim3(G::kThreads), 0, s, a);
+    });
   });
 }
 
 // out = B A^T in one of the three orders of the operands.
 template <typename T, bool KA, bool KB>
-void launch_product(const Choice& c, const Mat& ma, const Mat& mb, int64_t half, int64_t halves,
+void launch_product(const Choice& c, bool two, const Mat& ma, const Mat& mb, int64_t half, int64_t halves,
                     int64_t m, int64_t n, int64_t k, void* out, float* acc, hipStream_t s) {
   ProductArgs a{};
   a.a = ma, a.b = mb;
@@ -886,11 +983,16 @@ void launch_product(const Choice& c, const Mat& ma, const Mat& mb, int64_t half,
   a.out = out, a.acc = acc;
   a.np = static_cast<int32_t>(round_up(n, kPad));
   a.ldm = static_cast<int32_t>(halves * round_up(m, 64));
-  with_tile(c.tile, [&](auto g) {
+  with_tile<kParts<T>>(c.tile, [&](auto g) {
     typedef decltype(g) G;
-    hipLaunchKernelGGL((product_kernel<G, T, KA, KB>),
-                       tile_grid(ceil_div(m, G::kTile) * halves, ceil_div(n, G::kTile) * c.splits),
-                       dim3(G::kThreads), 0, s, a);
+    const dim3 grid = tile_grid(ceil_div(m, G::kTile) * halves, ceil_div(n, G::kTile) * c.splits);
+    if constexpr (sizeof(T) == 2) {
+      if (two) {
+        hipLaunchKernelGGL((product_kernel<G, T, kTwo, KA, KB>), grid, dim3(G::kThreads), 0, s, a);
+        return;
+      }
+    }
+    hipLaunchKernelGGL((product_kernel<G, T, kParts<T>, KA, KB>), grid, dim3(G::kThreads), 0, s, a);
   });
   if (c.splits > 1)
     hipLaunchKernelGGL(splits_kernel<T>, dim3(blocks_of(n * halves * ceil_div(m, 4), kThreads)),
@@ -909,9 +1011,9 @@ int run_forward(const Call& c, const Plan& p, const void* X, const void* W_in, c
   o.launch(s);
   a.h = {reinterpret_cast<bf16*>(ws + p.off_h), p.ldh, p.np * p.ldh, a.N, a.ldh};
   a.codes = codes, a.exps = exps;
-  if (codes) launch_gate_up<T, kHAndCodes>(a, s);
-  else launch_gate_up<T, kH>(a, s);
-  launch_product<T, true, false>(p.y, a.w_out, a.h, 0, 1, c.d, c.N, p.ldh, Y,
+  if (codes) launch_gate_up<T, true>(a, s);
+  else launch_gate_up<T, false>(a, s);
+  launch_product<T, true, false>(p.y, p.two, a.w_out, a.h, 0, 1, c.d, c.N, p.ldh, Y,
                                  reinterpret_cast<float*>(ws + p.off_acc), s);
   return check_launch("gated block");
 }
@@ -976,7 +1078,7 @@ int run_backward(const Call& c, const Plan& p, const void* X, const int8_t* x_co
   a.dy = o.bring(dY, c.N, c.d, 1, 0, p.ldx, p.off_dy, kHalf && c.d % kStepK == 0 && aligned(dY, 16));
   o.launch(s);
   // dZ and H go straight to the caller where they need no padding
-  const bool whole = kHalf && c.N % kStepK == 0;
+  const bool whole = kHalf && !p.two && c.N % kStepK == 0;
   const bool own_z = whole && g.dZ && p.ldz == 2 * c.f && aligned(g.dZ, 16);
   const bool own_h = whole && g.H && p.ldh == c.f && aligned(g.H, 16);
   bf16* const dz = own_z ? static_cast<bf16*>(g.dZ) : reinterpret_cast<bf16*>(ws + p.off_dz);
@@ -986,38 +1088,37 @@ int run_backward(const Call& c, const Plan& p, const void* X, const int8_t* x_co
   a.dz = {dz, p.ldz, p.np * p.ldz, a.np, static_cast<int32_t>(p.ldz)};
   a.h = {h, p.ldh, p.np * p.ldh, a.np, static_cast<int32_t>(p.ldh)};
   a.codes = const_cast<int8_t*>(z_codes), a.exps = const_cast<uint8_t*>(z_exps);
-  a.zf = reinterpret_cast<float*>(ws + p.off_zf);
+  a.scratch = reinterpret_cast<f32x4*>(ws + p.off_scratch);
   a.dz_out = own_z ? nullptr : g.dZ;
   a.h_out = own_h ? nullptr : g.H;
-  const int64_t run = again ? p.z_rows : c.N;
-  for (int64_t n0 = 0; n0 < c.N; n0 += run) {
-    GatedArgs b = a;
-    b.N = static_cast<int32_t>(std::min(run, c.N - n0));
-    b.np = static_cast<int32_t>(std::min<int64_t>(run, a.np - n0));
-    auto from = [&](Mat& m) { m.p += n0 * m.ld, m.rows -= static_cast<int32_t>(n0); };
-    if (again) from(b.x);
-    from(b.dy), from(b.dz), from(b.h);
-    if (!again) b.np = a.np;
-    if (b.dz_out) b.dz_out = static_cast<T*>(b.dz_out) + n0 * 2 * c.f;
-    if (b.h_out) b.h_out = static_cast<T*>(b.h_out) + n0 * c.f;
-    if (again) launch_gate_up<T, kZ>(b, s);
-    const int64_t cols = std::max<int64_t>(p.ldh, p.ldz - p.fq);
-    with_tile(whole_tile<T>(cols, b.np, c.d, kWhole), [&](auto t) {
+  if (again) {
+    with_tile<kParts<T>>(p.again.tile, [&](auto t) {
       typedef decltype(t) G;
-      const dim3 grid = tile_grid(ceil_div(cols, G::kTile), ceil_div(b.np, G::kTile)), bl(G::kThreads);
-      if (again) hipLaunchKernelGGL((gate_up_grad_kernel<G, kParts<T>, false>), grid, bl, 0, s, b);
-      else hipLaunchKernelGGL((gate_up_grad_kernel<G, kParts<T>, true>), grid, bl, 0, s, b);
+      with_act(c.act, [&](auto act) {
+        hipLaunchKernelGGL((gate_up_again_kernel<G, kParts<T>, decltype(act)::value>),
+                           dim3(static_cast<unsigned>(p.again_blocks)), dim3(G::kThreads), 0, s, a);
+      });
+    });
+  } else {
+    const int64_t cols = grad_cols(a);
+    with_tile<kParts<T>>(whole_tile<T>(cols, c.N, c.d, kWhole), [&](auto t) {
+      typedef decltype(t) G;
+      with_act(c.act, [&](auto act) {
+        hipLaunchKernelGGL((gate_up_grad_kernel<G, kParts<T>, decltype(act)::value>),
+                           tile_grid(ceil_div(cols, G::kTile), ceil_div(a.np, G::kTile)),
+                           dim3(G::kThreads), 0, s, a);
+      });
     });
   }
   float* acc = reinterpret_cast<float*>(ws + p.off_acc);
   if (g.dX)
-    launch_product<T, false, false>(p.x, a.w_in, a.dz, 0, 1, c.d, c.N, p.ldz, g.dX, acc, s);
+    launch_product<T, false, false>(p.x, p.two, a.w_in, a.dz, 0, 1, c.d, c.N, p.ldz, g.dX, acc, s);
   // (K runs over the rows that are written: whole steps, zero from N on)
   const int64_t k = round_up(c.N, kStepK);
   if (g.dW_in)
-    launch_product<T, true, true>(p.wi, a.dz, a.x, p.fq, 2, c.f, c.d, k, g.dW_in, acc, s);
+    launch_product<T, true, true>(p.wi, p.two, a.dz, a.x, p.fq, 2, c.f, c.d, k, g.dW_in, acc, s);
   if (g.dW_out)
-    launch_product<T, true, true>(p.wo, a.dy, a.h, 0, 1, c.d, c.f, k, g.dW_out, acc, s);
+    launch_product<T, true, true>(p.wo, p.two, a.dy, a.h, 0, 1, c.d, c.f, k, g.dW_out, acc, s);
   return check_launch("gated gradient");
 }
 

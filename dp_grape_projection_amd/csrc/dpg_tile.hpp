@@ -48,6 +48,13 @@ template <> struct Combos<3> {
   __device__ __forceinline__ static int a(int c) { return (0x001102 >> (4 * c)) & 15; }
   __device__ __forceinline__ static int b(int c) { return (0x010120 >> (4 * c)) & 15; }
 };
+// One operand in two bf16 parts, the other in one, with its parts 0 elements apart.
+constexpr int kTwo = 4;
+template <> struct Combos<kTwo> {
+  static constexpr int n = 2;
+  __device__ __forceinline__ static int a(int c) { return c == 0 ? 1 : 0; }
+  __device__ __forceinline__ static int b(int c) { return c == 0 ? 1 : 0; }
+};
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
@@ -204,6 +211,17 @@ typedef Geometry<128, 4, 4> SmallTile;
 // 22 and 20.5; 80 x 1024 x 50304, 393: 19 and 25).
 typedef Geometry<64, 4, 1> TinyTile;
 
+// fn(std::integral_constant<int, 0>) .. <N - 1>: unrolled whatever its size, so that the
+// accumulators it indexes stay in registers.
+template <class F, int... I>
+__device__ __forceinline__ void each_of(F fn, std::integer_sequence<int, I...>) {
+  (fn(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F fn) {
+  each_of(fn, std::make_integer_sequence<int, N>{});
+}
+
 // Slot of 16-byte chunk c in row k of a k-major tile of CHUNKS chunks a row. Of the
 // transposing read, 16 lanes take 32 bytes from each of four rows, and the
 // next 16 the same eight rows further on: the slots of these eight pieces
@@ -222,7 +240,20 @@ struct Operand {
   int cols;             // rows: elements of K in a row; k-major: columns from base
   int64_t half = 0;     // k-major: where not 0, a wave's columns are half from base
                         // on and half from base + half on (elements, a multiple of 8)
+  bool apart = false;   // and the next wave's a whole wave's columns further, not half
 };
+
+// Byte offset in a row of a k-major operand of what the tile has as its chunk c of eight
+// columns.
+template <class G>
+__device__ __forceinline__ uint32_t column_chunk(const Operand& o, int c) {
+  if (!o.half) return static_cast<uint32_t>(min(c, o.cols / 8 - 1)) * 16u;
+  // a wave's first chunks from one half, the others from the other
+  constexpr int kSpan = G::kWaveM / 8;
+  const int at = c / kSpan * (o.apart ? kSpan : kSpan / 2) + c % (kSpan / 2);
+  return static_cast<uint32_t>(min(at, o.cols / 8 - 1)) * 16u +
+         (c % kSpan < kSpan / 2 ? 0u : static_cast<uint32_t>(o.half) * 2u);
+}
 
 // The direct copies of one operand: G::kCopies of 1 KiB a wave and step.
 template <class G, bool KMAJOR>
@@ -254,15 +285,7 @@ struct Copier {
     if constexpr (!KMAJOR) {
       chunk = static_cast<uint32_t>((lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7)) * 16u;
     } else {
-      const int c = kslot<kChunks>(kRowsPerCopy * wave + lane / kChunks, lane % kChunks);
-      chunk = static_cast<uint32_t>(min(c, o.cols / 8 - 1)) * 16u;
-      if (o.half) {
-        // a wave's first chunks from one half, the others from the other
-        constexpr int kSpan = G::kWaveM / 8;
-        const int at = c / kSpan * (kSpan / 2) + c % (kSpan / 2);
-        chunk = static_cast<uint32_t>(min(at, o.cols / 8 - 1)) * 16u +
-                (c % kSpan < kSpan / 2 ? 0u : static_cast<uint32_t>(o.half) * 2u);
-      }
+      chunk = column_chunk<G>(o, kslot<kChunks>(kRowsPerCopy * wave + lane / kChunks, lane % kChunks));
     }
     last = KMAJOR ? static_cast<uint32_t>(o.rows - 1) : static_cast<uint32_t>(o.cols) * 2u - 16u;
   }
@@ -427,6 +450,170 @@ __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& o
   for (; s + 2 < n_steps; ++s) step(std::true_type{}, true);
 #pragma unroll 1
   for (; s < n_steps; ++s) step(std::false_type{}, s + 1 < n_steps);
+}
+
+// The same for operands in three bf16 parts, all of a K step's parts at once: a step of 32
+// is six tiles in LDS (A's parts, then B's), read once for the six products, where a pass
+// over K for every product would copy and read twelve (TIMESPARTS). Three stages, the
+// copies two steps ahead; a step's fragments are read while the products of the one before
+// it run, which takes most of the 512 registers that four waves on a CU have. An
+// operand whose K runs along its rows lies in rows of 64 bytes, chunk c of row R in slot
+// c ^ (R / 4 mod 4), so that the 16 rows that a read touches lie in different banks.
+constexpr int kPartsK = 32;
+template <class G> constexpr int kPartsTile = G::kTile * kPartsK * 2;
+template <class G> constexpr int kPartsLds = 3 * 6 * kPartsTile<G>;
+
+template <class G, bool KMAJOR>
+struct PartsCopier {
+  static constexpr int kPer = kPartsTile<G> / 1024 / G::kWaves;  // copies of a wave, step and part
+  static constexpr int kChunks = KMAJOR ? G::kTile / 8 : 4, kRowsPerCopy = 64 / kChunks;
+  const char* at;       // the step to copy, first part
+  int64_t part_bytes;
+  uint32_t ldb;         // row stride, bytes
+  uint32_t kb;          // rows: byte offset of the step in a row; k-major: its K row
+  uint32_t last;        // rows: last chunk of a row; k-major: last K row
+  uint32_t row[kPer];   // rows: row offset; k-major: K row of the lane
+  uint32_t chunk[kPer]; // byte offset of the lane's 16 bytes in the row
+
+  __device__ __forceinline__ void init(const Operand& o, int lane, int wave) {
+    at = reinterpret_cast<const char*>(o.base);
+    part_bytes = o.part_stride * 2;
+    ldb = static_cast<uint32_t>(o.ld) * 2u;
+    kb = 0;
+    last = KMAJOR ? static_cast<uint32_t>(o.rows - 1) : static_cast<uint32_t>(o.cols) * 2u - 16u;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int r = (q * G::kWaves + wave) * kRowsPerCopy + lane / kChunks, slot = lane % kChunks;
+      if constexpr (KMAJOR) {
+        row[q] = static_cast<uint32_t>(r);
+        chunk[q] = column_chunk<G>(o, kslot<kChunks>(r, slot));
+      } else {
+        row[q] = static_cast<uint32_t>(min(r, o.rows - 1)) * ldb;
+        chunk[q] = static_cast<uint32_t>(slot ^ ((r >> 2) & 3)) * 16u;
+      }
+    }
+  }
+  // copy j of the 3 kPer of a step
+  __device__ __forceinline__ void issue(char* tiles, int wave, int j) const {
+    const int p = j / kPer, q = j % kPer;
+    copy_to_lds(tile_rsrc(at + p * part_bytes),
+                KMAJOR ? min(row[q], last - kb) * ldb + chunk[q] : row[q] + min(kb + chunk[q], last), 0,
+                tiles + p * kPartsTile<G> + (q * G::kWaves + wave) * 1024);
+  }
+  __device__ __forceinline__ void next_step() {
+    if constexpr (KMAJOR) {
+      // (past the last row of K, in the second half of a last step, the same again)
+      if (kb + kPartsK > last) return;
+      at += static_cast<uint64_t>(ldb) * kPartsK;
+      kb += kPartsK;
+    } else {
+      kb += kPartsK * 2;
+    }
+  }
+};
+
+template <class G, bool KMAJOR>
+__device__ __forceinline__ bf16x8 parts_frag(const char* tile, int c0, int lane) {
+  if constexpr (KMAJOR) return tile_frag<G, true>(tile, 0, c0, lane);
+  const int r = c0 + (lane & 15);
+  return lds_read_b128(tile + r * (2 * kPartsK) + ((lane >> 4) ^ ((r >> 2) & 3)) * 16);
+}
+
+// acc = A B^T over n_k steps of kStepK.
+template <class G, bool KA, bool KB>
+__device__ __forceinline__ void parts_product(const Operand& oa, const Operand& ob, int n_k, char* smem,
+                                              typename G::Acc& acc) {
+  typedef Combos<3> C;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave % G::kWavesM, wn = wave / G::kWavesM;
+  PartsCopier<G, KA> ca;
+  PartsCopier<G, KB> cb;
+  ca.init(oa, lane, wave);
+  cb.init(ob, lane, wave);
+  constexpr int kCopies = 3 * (PartsCopier<G, KA>::kPer + PartsCopier<G, KB>::kPer);
+  constexpr int kStage = 6 * kPartsTile<G>;
+#pragma unroll
+  for (int m = 0; m < G::kMB; ++m)
+#pragma unroll
+    for (int n = 0; n < G::kNB; ++n) acc.v[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int n_steps = n_k * (kStepK / kPartsK);
+  if (n_steps <= 0) return;
+  auto issue = [&](int s, int j) {  // copy j of step s
+    char* const to = smem + s % 3 * kStage;
+    constexpr int kA = 3 * PartsCopier<G, KA>::kPer;
+    if (j < kA) ca.issue(to, wave, j);
+    else cb.issue(to + 3 * kPartsTile<G>, wave, j - kA);
+    if (j + 1 == kCopies) ca.next_step(), cb.next_step();
+  };
+  auto issue_all = [&](int s) {
+#pragma unroll
+    for (int j = 0; j < kCopies; ++j) issue(s, j);
+  };
+  bf16x8 fa[2][3][G::kMB], fb[2][3][G::kNB];
+  constexpr int kFrags = 3 * (G::kMB + G::kNB);
+  auto read = [&](int s, int to, int j) {  // fragment j of step s
+    const char* const from = smem + s % 3 * kStage;
+    if (j < 3 * G::kMB) {
+      const int p = j / G::kMB, m = j % G::kMB;
+      fa[to][p][m] = parts_frag<G, KA>(from + p * kPartsTile<G>, G::kWaveM * wm + 16 * m, lane);
+    } else {
+      const int p = (j - 3 * G::kMB) / G::kNB, n = (j - 3 * G::kMB) % G::kNB;
+      fb[to][p][n] = parts_frag<G, KB>(from + (3 + p) * kPartsTile<G>, G::kWaveN * wn + 16 * n, lane);
+    }
+  };
+  // Step s: the copies of s + 1 are complete once at most those of s + 2 are in flight,
+  // and once every wave has read step s, s + 3 takes its place. Reads and copies go
+  // between the products, a row of blocks at a time: issued at once they would leave the
+  // matrix cores idle for as long as the products take. LEFT: the steps there are after
+  // it, 3 for more; no test inside a step, on whose joining paths the compiler would have
+  // the products wait for the newest fragments.
+  issue_all(0);
+  issue_all(1);
+  wait_vm_all<kCopies>();
+  lds_barrier();
+  if (n_steps > 2) issue_all(2);  // (n_steps is even)
+#pragma unroll
+  for (int j = 0; j < kFrags; ++j) read(0, 0, j);
+  auto step = [&](int s, auto at, auto left) {
+    constexpr int cur = decltype(at)::value, LEFT = decltype(left)::value;
+    constexpr int kGroups = C::n * G::kMB;
+    if constexpr (LEFT >= 1) {
+      wait_lgkm0();
+      wait_vm_all<LEFT >= 2 ? kCopies : 0>();
+      lds_barrier();
+    }
+    each<kGroups>([&](auto group) {
+      constexpr int g = decltype(group)::value, c = g / G::kMB, m = g % G::kMB;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int n = 0; n < G::kNB; ++n)
+        acc.v[m][n] = mfma<3>(fa[cur][C::a(c)][m], fb[cur][C::b(c)][n], acc.v[m][n]);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (LEFT >= 1) {
+#pragma unroll
+        for (int j = g * kFrags / kGroups; j < (g + 1) * kFrags / kGroups; ++j) read(s + 1, cur ^ 1, j);
+      }
+      if constexpr (LEFT >= 3) {
+#pragma unroll
+        for (int j = g * kCopies / kGroups; j < (g + 1) * kCopies / kGroups; ++j) issue(s + 3, j);
+      }
+    });
+  };
+  constexpr std::integral_constant<int, 0> even;
+  constexpr std::integral_constant<int, 1> odd;
+  constexpr std::integral_constant<int, 3> more;
+  if (n_steps > 2) {
+#pragma unroll 1
+    for (int s = 0; s < n_steps - 4; s += 2) {
+      step(s, even, more);
+      step(s + 1, odd, more);
+    }
+    step(n_steps - 4, even, more);
+    step(n_steps - 3, odd, std::integral_constant<int, 2>{});
+  }
+  step(n_steps - 2, even, odd);
+  step(n_steps - 1, odd, even);
 }
 
 // The tile (m, n) of a block among mt x nt: each XCD takes a
