@@ -139,11 +139,11 @@ template <class G, int PARTS> constexpr int kLdsOf = PARTS == 3 ? kPartsLds<G> :
 template <class G, int PARTS>
 constexpr int kBlocksOf = PARTS != 3 ? G::kBlocks : G::kTile == TinyTile::kTile ? 2 : 1;
 
-template <class G, int PARTS, bool KA, bool KB>
+template <class G, int PARTS, bool KA, bool KB, bool AGAIN = false>
 __device__ __forceinline__ void product(const Operand& a, const Operand& b, int n_k, char* smem,
                                         typename G::Acc& acc) {
   if constexpr (PARTS == 3) parts_product<G, KA, KB>(a, b, n_k, smem, acc);
-  else tile_product<G, PARTS, KA, KB>(a, b, n_k, smem, acc);
+  else tile_product<G, PARTS, KA, KB, AGAIN>(a, b, n_k, smem, acc);
 }
 
 __device__ __forceinline__ Operand rows_of(const Mat& m, int r0, int k0) {
@@ -428,22 +428,30 @@ __global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void gate_up_ag
   __shared__ __attribute__((aligned(1024))) char smem[kLdsOf<G, PARTS>];
   constexpr int kHB = G::kMB / 2;
   const int mts = (grad_cols(a) + G::kTile - 1) / G::kTile, nts = (a.np + G::kTile - 1) / G::kTile;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
   const int steps = (a.d + kStepK - 1) / kStepK, all = (mts * nts + 7) / 8 * 8;
-  f32x4* const mine = a.scratch + static_cast<int64_t>(blockIdx.x) * (G::kMB * G::kNB * G::kThreads) + tid;
+  // the block's dH: 16 bytes a thread for every 16 x 16 block of its wave (through a
+  // buffer resource, whose offsets cost no registers)
+  const __amdgpu_buffer_rsrc_t mine =
+      tile_rsrc(a.scratch + static_cast<int64_t>(blockIdx.x) * (G::kMB * G::kNB * G::kThreads));
+  constexpr int kEach = G::kThreads * 16;
   for (int block = blockIdx.x; block < all; block += gridDim.x) {
     int mt, nt;
     if (!tile_of_block(block, mts, nts, mt, nt)) continue;
     const int c0 = mt * G::kTile, r0 = nt * G::kTile;
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));  // (nothing of it is kept from tile to tile)
+    const int lane = tid & 63, wave = tid >> 6;
+    const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
     typename G::Acc acc;
     __syncthreads();  // the last tile's fragments have been read
-    product<G, PARTS, false, false>(rows_of(a.w_out, min(c0, a.f - 1), 0),
+    product<G, PARTS, false, false, true>(rows_of(a.w_out, min(c0, a.f - 1), 0),
                                          rows_of(a.dy, min(r0, a.N - 1), 0), steps, smem, acc);
 #pragma unroll
     for (int mb = 0; mb < G::kMB; ++mb)
 #pragma unroll
-      for (int nb = 0; nb < G::kNB; ++nb) mine[(mb * G::kNB + nb) * G::kThreads] = acc.v[mb][nb];
+      for (int nb = 0; nb < G::kNB; ++nb)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc.v[mb][nb]), mine, tid * 16,
+                                               (mb * G::kNB + nb) * kEach, 0);
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
       const int ch = c0 + half * (G::kWaveM / 2), cb = min(ch, a.fq - 8);
@@ -452,15 +460,17 @@ __global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void gate_up_ag
       w.half = a.fq;
       w.apart = true;
       __syncthreads();
-      product<G, PARTS, true, false>(w, rows_of(a.x, min(r0, a.N - 1), 0), steps, smem, acc);
+      product<G, PARTS, true, false, true>(w, rows_of(a.x, min(r0, a.N - 1), 0), steps, smem, acc);
       const int cw = ch + G::kWaveM * wm;  // the wave's first column of this half
-      const f32x4* const dhs = mine + half * (kHB * G::kNB * G::kThreads);
       with_edge(r0 + G::kTile > a.N || c0 + G::kTile > a.f, [&](auto edge) {
         constexpr bool E = decltype(edge)::value;
         f32x4 dh[2][kHB];
         auto load = [&](int nb, int to) {
 #pragma unroll
-          for (int mb = 0; mb < kHB; ++mb) dh[to][mb] = dhs[(mb * G::kNB + nb) * G::kThreads];
+          for (int mb = 0; mb < kHB; ++mb)
+            dh[to][mb] = __builtin_bit_cast(
+                f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                           mine, tid * 16, ((half * kHB + mb) * G::kNB + nb) * kEach, 0));
         };
         load(0, 0);
         each<G::kNB>([&](auto at) {

@@ -337,13 +337,17 @@ __device__ __forceinline__ bf16x8 tile_frag(const char* tile, int kk, int c0, in
   }
 }
 
-// acc = A B^T over K steps [0, n_k) of every combination of parts.
-template <class G, int PARTS, bool KA, bool KB>
+// acc = A B^T over K steps [0, n_k) of every combination of parts. AGAIN: the kernel has
+// other products or runs this one in a loop; what is computed from the thread's number is
+// then computed here and not kept in registers from before.
+template <class G, int PARTS, bool KA, bool KB, bool AGAIN = false>
 __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& ob, int n_k,
                                              char* smem, typename G::Acc& acc) {
   typedef Combos<PARTS> C;
   constexpr int KK = kStepK / 32;
-  const int tid = threadIdx.x, lane = tid & 63;
+  int tid = threadIdx.x;
+  if constexpr (AGAIN) asm volatile("" : "+v"(tid));
+  const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % G::kWavesM, wn = wave / G::kWavesM;
   Copier<G, KA> ca;
