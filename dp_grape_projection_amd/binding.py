@@ -881,11 +881,10 @@ class PackedActivations(NamedTuple):
         return self.codes.numel() + self.exps.numel()
 
 
-def _packed_like(rows, d, dtype, device):
+def _packed_like(X, rows, d):
     blocks = -(-d // 32)
-    return PackedActivations(torch.empty((*rows, 32 * blocks), dtype=torch.int8, device=device),
-                             torch.empty((*rows, blocks), dtype=torch.uint8, device=device),
-                             d, dtype)
+    return PackedActivations(X.new_empty((*rows, 32 * blocks), dtype=torch.int8),
+                             X.new_empty((*rows, blocks), dtype=torch.uint8), d, X.dtype)
 
 
 def _require_packed(p: PackedActivations, name: str, rows=None, d=None):
@@ -923,7 +922,7 @@ def dpg_pack_act(X: torch.Tensor, out: Optional[PackedActivations] = None,
     _on_this_device(X)
     d, code = int(X.shape[-1]), _dtype_code(X.dtype)
     if out is None:
-        out = _packed_like(X.shape[:-1], d, X.dtype, X.device)
+        out = _packed_like(X, X.shape[:-1], d)
     else:
         _require_packed(out, "out", X.shape[:-1], d)
         if out.dtype != X.dtype:
@@ -1064,7 +1063,7 @@ def dpg_gated(X: torch.Tensor, W_in: torch.Tensor, W_out: torch.Tensor, act: str
         _require_packed(Z, "Z", (*X.shape[:-1], 2), f)
         _same_device(X, Z=Z.codes)
     elif keep:
-        Z = _packed_like((*X.shape[:-1], 2), f, X.dtype, X.device)
+        Z = _packed_like(X, (*X.shape[:-1], 2), f)
     if N == 0:
         return Y, Z
     ws, ws_bytes = _workspace(_gated_workspace_size(N, d, f, code), X.device, workspace)

@@ -719,6 +719,15 @@ int check_clip_sigma(double clip_C, double sigma) {
 // noise 1).
 constexpr uint32_t kTagProbe = 3;
 
+// One layer's input in 8 bits, and the bytes of its workspace that it is read back to.
+struct PackedA {
+  const int8_t* codes;
+  const uint8_t* exps;
+};
+size_t packed_a_bytes(const dpg_layer_grad& layer, int64_t B, int64_t T, int32_t dtype) {
+  return align_up(static_cast<size_t>(B * T * layer.d_in) * elem_size(dtype));
+}
+
 // The projection call. With ghat == nullptr: the whole batch step (norms,
 // clip, sum, noise into each layer's G_priv). With ghat: the streaming form
 // for one layer (its product tiles into ghat, its squared norms added into
@@ -736,13 +745,22 @@ int project_impl(const dpg_layer_grad* layers, int32_t n_layers, int64_t B,
                  uint64_t proj_step, float* sample_norms, void* workspace,
                  size_t workspace_bytes, void* stream, float* ghat,
                  float* norm_sq, const StepUpdate* upd = nullptr,
-                 float* rc_scales = nullptr) {
+                 float* rc_scales = nullptr, const PackedA* packed = nullptr) {
   const bool layer_mode = ghat != nullptr;
   const bool rc = rc_scales != nullptr;
   int st = validate_proj_shapes(layers, n_layers, B, T, r, dtype);
   if (st) return st;
+  dpg_layer_grad own;
+  size_t a_bytes = 0;
+  if (packed) {  // the one layer's A: read back at the workspace's start
+    if (!packed->codes || !packed->exps) return fail(DPG_ERR_INVALID_ARG, "NULL data pointer");
+    a_bytes = packed_a_bytes(layers[0], B, T, dtype);
+    own = layers[0];
+    own.A = workspace;
+    layers = &own;
+  }
   for (int i = 0; i < n_layers; ++i)
-    if (!layers[i].A || !layers[i].dY || (!layer_mode && !rc && !layers[i].G_priv))
+    if ((!layers[i].A && !packed) || !layers[i].dY || (!layer_mode && !rc && !layers[i].G_priv))
       return fail(DPG_ERR_INVALID_ARG,
                   "NULL data pointer in layer index " + std::to_string(i));
   if (layer_mode && !norm_sq) return fail(DPG_ERR_INVALID_ARG, "norm_sq is NULL");
@@ -751,11 +769,14 @@ int project_impl(const dpg_layer_grad* layers, int32_t n_layers, int64_t B,
   const ProjPlan p = plan_proj(layers, n_layers, B, T, r, dtype);
   std::vector<size_t> off_U;
   const size_t u_bytes = upd ? step_u_bytes(layers, n_layers, r, dtype, p.total, &off_U) : 0;
-  if ((st = check_workspace(workspace, workspace_bytes, p.total + u_bytes))) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, a_bytes + p.total + u_bytes))) return st;
 
   hipStream_t s = static_cast<hipStream_t>(stream);
-  char* ws = static_cast<char*>(workspace);
+  char* ws = static_cast<char*>(workspace) + a_bytes;
   const bool bf16 = dtype == DPG_BF16;
+  if (packed &&
+      launch_unpack8(packed->codes, packed->exps, B * T, own.d_in, workspace, bf16, own.d_in, s) != hipSuccess)
+    return fail(DPG_ERR_HIP, "unpack: launch failed");
   const int vec_elems = static_cast<int>(16 / elem_size(dtype));
   float* norm_part = reinterpret_cast<float*>(ws + p.off_norm);
   float* scales = reinterpret_cast<float*>(ws + p.off_scales);
@@ -1192,32 +1213,19 @@ int dpg_project_layer(const dpg_layer_grad* layer, int64_t B, int64_t T,
 int dpg_project_layer_packed_workspace_size(const dpg_layer_grad* layer, int64_t B, int64_t T,
                                             int32_t r, int32_t dtype, size_t* bytes) {
   if (const int st = dpg_project_workspace_size(layer, 1, B, T, r, dtype, bytes)) return st;
-  *bytes = align_up(*bytes) + align_up(static_cast<size_t>(B * T * layer->d_in) * elem_size(dtype));
+  *bytes += packed_a_bytes(*layer, B, T, dtype);
   return DPG_OK;
 }
 
-// A is read back at the workspace's end, where the projection takes it from.
 int dpg_project_layer_packed(const dpg_layer_grad* layer, const int8_t* codes,
                              const uint8_t* exps, int64_t B, int64_t T, int32_t r, int32_t dtype,
                              uint64_t seed, uint64_t proj_step, float* G_hat, float* norm_sq,
                              void* workspace, size_t workspace_bytes, void* stream) {
   g_last_error.clear();
-  size_t need = 0;
-  if (const int st = dpg_project_layer_packed_workspace_size(layer, B, T, r, dtype, &need)) return st;
   if (!G_hat) return fail(DPG_ERR_INVALID_ARG, "G_hat is NULL");
-  if (!norm_sq) return fail(DPG_ERR_INVALID_ARG, "norm_sq is NULL");
-  if (!codes || !exps || !layer->dY) return fail(DPG_ERR_INVALID_ARG, "NULL data pointer");
-  if (const int st = check_seed_steps(1, proj_step)) return st;
-  if (const int st = check_workspace(workspace, workspace_bytes, need)) return st;
-  const size_t a_bytes = align_up(static_cast<size_t>(B * T * layer->d_in) * elem_size(dtype));
-  dpg_layer_grad L = *layer;
-  char* const A = static_cast<char*>(workspace) + (need - a_bytes);
-  L.A = A;
-  if (launch_unpack8(codes, exps, B * T, L.d_in, A, dtype == DPG_BF16, L.d_in,
-                     static_cast<hipStream_t>(stream)) != hipSuccess)
-    return fail(DPG_ERR_HIP, "unpack: launch failed");
-  return project_impl(&L, 1, B, T, r, dtype, 1.0, 0.0, seed, 1, proj_step, nullptr, workspace,
-                      need - a_bytes, stream, G_hat, norm_sq);
+  const PackedA packed{codes, exps};
+  return project_impl(layer, 1, B, T, r, dtype, 1.0, 0.0, seed, 1, proj_step, nullptr, workspace,
+                      workspace_bytes, stream, G_hat, norm_sq, nullptr, nullptr, &packed);
 }
 
 int dpg_clip_workspace_size(int64_t B, size_t* bytes) {

@@ -500,11 +500,10 @@ struct ProductArgs {
 };
 
 template <class G, typename T, int PARTS, bool KA, bool KB>
-__global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void product_kernel(const ProductArgs a) {
-  __shared__ __attribute__((aligned(1024))) char smem[kLdsOf<G, PARTS>];
+__device__ __forceinline__ void product_tile(const ProductArgs& a, int block, char* smem) {
   const int mh = (a.m + G::kTile - 1) / G::kTile, nh = (a.n + G::kTile - 1) / G::kTile;
   int mt, nt;
-  if (!tile_of_block(blockIdx.x, mh * a.halves, nh * a.splits, mt, nt)) return;
+  if (!tile_of_block(block, mh * a.halves, nh * a.splits, mt, nt)) return;
   const int split = nt / nh, half = mt / mh;
   const int m0 = (mt - half * mh) * G::kTile, n0 = (nt - split * nh) * G::kTile;
   const int per = (a.steps + a.splits - 1) / a.splits;
@@ -545,6 +544,25 @@ __global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void product_ke
       }
     }
   }
+}
+
+template <class G, typename T, int PARTS, bool KA, bool KB>
+__global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void product_kernel(const ProductArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[kLdsOf<G, PARTS>];
+  product_tile<G, T, PARTS, KA, KB>(a, blockIdx.x, smem);
+}
+
+// The three products of the gradients in one launch, where none of them takes big tiles:
+// each alone leaves CUs idle, and a launch is 3 us of host time (128 x 64 x 256, fp32:
+// THREETIMES).
+template <class G, typename T, int PARTS>
+__global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void three_products_kernel(
+    const ProductArgs dx, const ProductArgs dw_in, const ProductArgs dw_out, int first_in, int first_out) {
+  __shared__ __attribute__((aligned(1024))) char smem[kLdsOf<G, PARTS>];
+  const int block = blockIdx.x;
+  if (block < first_in) product_tile<G, T, PARTS, false, false>(dx, block, smem);
+  else if (block < first_out) product_tile<G, T, PARTS, true, true>(dw_in, block - first_in, smem);
+  else product_tile<G, T, PARTS, true, true>(dw_out, block - first_out, smem);
 }
 
 // Sums over the splits of K, rounded: four columns a thread.
@@ -768,7 +786,7 @@ void with_tile(Tile t, F fn) {
 }
 
 // Blocks that the chip holds.
-int64_t resident(Tile t, int parts) {
+int32_t resident(Tile t, int parts) {
   if (parts == 3) return t == kTiny ? 512 : 256;
   return t == kBig ? 256 : t == kSmall ? 512 : 1024;
 }
@@ -794,13 +812,13 @@ Choice choose(int64_t m, int64_t n, int64_t steps, int parts, Kind kind) {
   const double mn = static_cast<double>(m) * static_cast<double>(n) / 1e6;
   for (const Tile t : {kBig, kSmall, kTiny}) {
     if (parts == 3 && t == kBig) continue;
-    const int64_t tile = t == kBig ? BigTile::kTile : t == kSmall ? SmallTile::kTile : TinyTile::kTile;
-    const int64_t slots = resident(t, parts);
-    const int64_t tiles = ceil_div(m, kind == kGateUp ? tile / 2 : tile) * ceil_div(n, tile);
-    const int64_t most = kind <= kBothTransposed ? std::max<int64_t>(1, std::min(slots / tiles, steps)) : 1;
-    // (every count up to 16, then steps of an eighth, and the most)
-    for (int64_t k = 1; k <= most; k = k < most ? std::min(k + std::max<int64_t>(1, k / 8), most) : k + 1) {
-      const int64_t blocks = tiles * k, rounds = ceil_div(blocks, slots);
+    const uint32_t tile = t == kBig ? BigTile::kTile : t == kSmall ? SmallTile::kTile : TinyTile::kTile;
+    const uint32_t slots = resident(t, parts), all_steps = static_cast<uint32_t>(steps);
+    const uint32_t tiles = static_cast<uint32_t>(ceil_div(m, kind == kGateUp ? tile / 2 : tile) * ceil_div(n, tile));
+    const uint32_t most = kind <= kBothTransposed ? std::max(1u, std::min(slots / tiles, all_steps)) : 1;
+    // (a call searches every time: counts a quarter apart, from 4 on)
+    for (uint32_t k = 1; k <= most; k += std::max(1u, k / 4)) {
+      const uint32_t blocks = tiles * k, rounds = (blocks + slots - 1) / slots;
       const double c = static_cast<double>(std::min(blocks, slots)) / 256;
       double step = t == kBig ? 1.05 + 0.5 * c : t == kSmall ? 0.5 * std::max(1.0, c)
                                                              : 0.34 + 0.13 * std::max(0.0, c - 1.0);
@@ -809,7 +827,7 @@ Choice choose(int64_t m, int64_t n, int64_t steps, int parts, Kind kind) {
       if (parts == 3) step = (t == kSmall ? 2.5 : 1.05 * std::max(1.0, c)) * (kind == kBothTransposed ? 1.15 : 1.0);
       const double around = t == kBig ? 5.0 : t == kSmall ? 3.5 : 3.0;
       double us = static_cast<double>(rounds) *
-                  (static_cast<double>(ceil_div(steps, k) * (kind == kAgain ? 3 : 1)) * step + around);
+                  (static_cast<double>((all_steps + k - 1) / k * (kind == kAgain ? 3 : 1)) * step + around);
       us += mn * (k > 1 ? 4.0 * static_cast<double>(k) : 2.0) / 5.6;
       if (k > 1) us += 2.5 + mn * (4.0 * static_cast<double>(k) + 2.0) / 6.5;
       if (us < best_us) best_us = us, best = {t, static_cast<int32_t>(k)};
@@ -849,7 +867,8 @@ struct Plan {
   Choice y{}, x{}, wi{}, wo{}, again{};
   int64_t again_blocks = 0;
   int32_t few_splits = 0;  // few rows: parts of f in the second product
-  size_t off_x, off_wi, off_wo, off_dy, off_h, off_dz = 0, off_scratch = 0, off_x8 = 0, off_acc, total;
+  size_t off_x, off_wi, off_wo, off_dy, off_h, off_dz = 0, off_scratch = 0, off_x8 = 0, off_acc = 0,
+                                                  off_acc_wi = 0, off_acc_wo = 0, total;
 };
 
 // Few rows of bf16 in whole K steps go their own way where the weights are 16-byte
@@ -872,7 +891,7 @@ Plan plan_gated(const Call& c, bool grad, bool again, bool weights) {
   p.fp = round_up(c.f, kBlock8);
   p.np = round_up(c.N, kPad);
   const int parts = static_cast<int>(p.parts), later = c.dtype == DPG_BF16 && c.N <= kTwoRows ? kTwo : parts;
-  size_t off = 0, acc = 0;
+  size_t off = 0;
   auto take = [&](int64_t elems, int64_t size) {
     const size_t at = off;
     off += align_up(static_cast<size_t>(elems * size));
@@ -887,7 +906,7 @@ Plan plan_gated(const Call& c, bool grad, bool again, bool weights) {
   p.off_h = take(made * p.np * p.ldh, 2);
   if (!grad) {
     p.y = choose(c.d, c.N, p.ldh / kStepK, later, kPlain);
-    acc = acc_bytes(p.y, 1, c.d, c.N);
+    size_t acc = acc_bytes(p.y, 1, c.d, c.N);
     if (few_rows(c)) {
       // about a block for every CU, each wave with four steps at least
       const int64_t tiles = ceil_div(c.d, kFewCols);
@@ -895,6 +914,7 @@ Plan plan_gated(const Call& c, bool grad, bool again, bool weights) {
           std::max<int64_t>(1, std::min(256 / tiles, c.f / (16 * kFewK))));
       acc = std::max<size_t>(acc, p.few_splits * kFewRows * round_up(c.d, 64) * 4);
     }
+    p.off_acc = take(static_cast<int64_t>(acc), 1);
   } else {
     p.off_dz = take(made * p.np * p.ldz, 2);
     if (again) {
@@ -904,22 +924,22 @@ Plan plan_gated(const Call& c, bool grad, bool again, bool weights) {
       auto blocks = [&](auto g) {
         typedef decltype(g) G;
         const int64_t tiles = round_up(ceil_div(cols, G::kTile) * ceil_div(p.np, G::kTile), 8);
-        p.again_blocks = std::min(tiles, resident(p.again.tile, parts));
+        p.again_blocks = std::min<int64_t>(tiles, resident(p.again.tile, parts));
         p.off_scratch = take(p.again_blocks * G::kTile * G::kTile, 4);
       };
       if (p.parts == 3) with_tile<3>(p.again.tile, blocks);
       else with_tile<1>(p.again.tile, blocks);
     }
     p.x = choose(c.d, c.N, p.ldz / kStepK, later, kPlain);
-    acc = acc_bytes(p.x, 1, c.d, c.N);
+    p.off_acc = take(static_cast<int64_t>(acc_bytes(p.x, 1, c.d, c.N)), 1);
     if (weights) {
       p.wi = choose(2 * c.f, c.d, ceil_div(c.N, kStepK), later, kBothTransposed);
       p.wo = choose(c.d, c.f, ceil_div(c.N, kStepK), later, kBothTransposed);
-      acc = std::max({acc, acc_bytes(p.wi, 2, c.f, c.d), acc_bytes(p.wo, 1, c.d, c.f)});
+      p.off_acc_wi = take(static_cast<int64_t>(acc_bytes(p.wi, 2, c.f, c.d)), 1);
+      p.off_acc_wo = take(static_cast<int64_t>(acc_bytes(p.wo, 1, c.d, c.f)), 1);
       p.off_x8 = take(c.N * p.ldx, c.dtype == DPG_BF16 ? 2 : 4);
     }
   }
-  p.off_acc = take(static_cast<int64_t>(acc), 1);
   p.total = off;
   return p;
 }
@@ -980,33 +1000,55 @@ void launch_gate_up(const GatedArgs& a, hipStream_t s) {
   });
 }
 
-// out = B A^T in one of the three orders of the operands.
-template <typename T, bool KA, bool KB>
-void launch_product(const Choice& c, bool two, const Mat& ma, const Mat& mb, int64_t half, int64_t halves,
-                    int64_t m, int64_t n, int64_t k, void* out, float* acc, hipStream_t s) {
+template <class F>
+void with_small(Tile t, F fn) {
+  if (t == kTiny) fn(TinyTile());
+  else fn(SmallTile());
+}
+
+// out = B A^T.
+ProductArgs product_args(const Choice& c, const Mat& ma, const Mat& mb, int64_t half, int64_t halves,
+                         int64_t m, int64_t n, int64_t k, void* out, char* acc) {
   ProductArgs a{};
   a.a = ma, a.b = mb;
   a.half = static_cast<int32_t>(half), a.halves = static_cast<int32_t>(halves);
   a.m = static_cast<int32_t>(m), a.n = static_cast<int32_t>(n);
   a.steps = static_cast<int32_t>(ceil_div(k, kStepK));
   a.splits = c.splits;
-  a.out = out, a.acc = acc;
+  a.out = out, a.acc = reinterpret_cast<float*>(acc);
   a.np = static_cast<int32_t>(round_up(n, kPad));
   a.ldm = static_cast<int32_t>(halves * round_up(m, 64));
-  with_tile<kParts<T>>(c.tile, [&](auto g) {
-    typedef decltype(g) G;
-    const dim3 grid = tile_grid(ceil_div(m, G::kTile) * halves, ceil_div(n, G::kTile) * c.splits);
-    if constexpr (sizeof(T) == 2) {
-      if (two) {
-        hipLaunchKernelGGL((product_kernel<G, T, kTwo, KA, KB>), grid, dim3(G::kThreads), 0, s, a);
-        return;
-      }
-    }
-    hipLaunchKernelGGL((product_kernel<G, T, kParts<T>, KA, KB>), grid, dim3(G::kThreads), 0, s, a);
-  });
-  if (c.splits > 1)
-    hipLaunchKernelGGL(splits_kernel<T>, dim3(blocks_of(n * halves * ceil_div(m, 4), kThreads)),
+  return a;
+}
+dim3 product_grid(const ProductArgs& a, int64_t tile) {
+  return tile_grid(ceil_div(a.m, tile) * a.halves, ceil_div(a.n, tile) * a.splits);
+}
+template <typename T>
+void launch_splits(const ProductArgs& a, hipStream_t s) {
+  if (a.splits > 1)
+    hipLaunchKernelGGL(splits_kernel<T>, dim3(blocks_of(static_cast<int64_t>(a.n) * a.halves * ((a.m + 3) / 4), kThreads)),
                        dim3(kThreads), 0, s, a);
+}
+// fn with the parts of the operands of a product, one of which the kernels made.
+template <typename T, class F>
+void with_parts(bool two, F fn) {
+  if constexpr (sizeof(T) == 2) {
+    if (two) return fn(std::integral_constant<int, kTwo>{});
+  }
+  fn(std::integral_constant<int, kParts<T>>{});
+}
+
+// One product in one of the three orders of its operands.
+template <typename T, bool KA, bool KB>
+void launch_product(Tile tile, bool two, const ProductArgs& a, hipStream_t s) {
+  with_tile<kParts<T>>(tile, [&](auto g) {
+    typedef decltype(g) G;
+    with_parts<T>(two, [&](auto parts) {
+      hipLaunchKernelGGL((product_kernel<G, T, decltype(parts)::value, KA, KB>), product_grid(a, G::kTile),
+                         dim3(G::kThreads), 0, s, a);
+    });
+  });
+  launch_splits<T>(a, s);
 }
 
 template <typename T>
@@ -1023,8 +1065,8 @@ int run_forward(const Call& c, const Plan& p, const void* X, const void* W_in, c
   a.codes = codes, a.exps = exps;
   if (codes) launch_gate_up<T, true>(a, s);
   else launch_gate_up<T, false>(a, s);
-  launch_product<T, true, false>(p.y, p.two, a.w_out, a.h, 0, 1, c.d, c.N, p.ldh, Y,
-                                 reinterpret_cast<float*>(ws + p.off_acc), s);
+  launch_product<T, true, false>(
+      p.y.tile, p.two, product_args(p.y, a.w_out, a.h, 0, 1, c.d, c.N, p.ldh, Y, ws + p.off_acc), s);
   return check_launch("gated block");
 }
 
@@ -1120,15 +1162,32 @@ int run_backward(const Call& c, const Plan& p, const void* X, const int8_t* x_co
       });
     });
   }
-  float* acc = reinterpret_cast<float*>(ws + p.off_acc);
-  if (g.dX)
-    launch_product<T, false, false>(p.x, p.two, a.w_in, a.dz, 0, 1, c.d, c.N, p.ldz, g.dX, acc, s);
   // (K runs over the rows that are written: whole steps, zero from N on)
   const int64_t k = round_up(c.N, kStepK);
-  if (g.dW_in)
-    launch_product<T, true, true>(p.wi, p.two, a.dz, a.x, p.fq, 2, c.f, c.d, k, g.dW_in, acc, s);
-  if (g.dW_out)
-    launch_product<T, true, true>(p.wo, p.two, a.dy, a.h, 0, 1, c.d, c.f, k, g.dW_out, acc, s);
+  const ProductArgs x = product_args(p.x, a.w_in, a.dz, 0, 1, c.d, c.N, p.ldz, g.dX, ws + p.off_acc);
+  if (!g.dW_in && !g.dW_out) {
+    if (g.dX) launch_product<T, false, false>(p.x.tile, p.two, x, s);
+    return check_launch("gated gradient");
+  }
+  const ProductArgs wi = product_args(p.wi, a.dz, a.x, p.fq, 2, c.f, c.d, k, g.dW_in, ws + p.off_acc_wi);
+  const ProductArgs wo = product_args(p.wo, a.dy, a.h, 0, 1, c.d, c.f, k, g.dW_out, ws + p.off_acc_wo);
+  if (g.dX && g.dW_in && g.dW_out && p.x.tile != kBig && p.x.tile == p.wi.tile && p.x.tile == p.wo.tile) {
+    with_small(p.x.tile, [&](auto t) {
+      typedef decltype(t) G;
+      const unsigned first_in = product_grid(x, G::kTile).x,
+                     first_out = first_in + product_grid(wi, G::kTile).x;
+      with_parts<T>(p.two, [&](auto parts) {
+        hipLaunchKernelGGL((three_products_kernel<G, T, decltype(parts)::value>),
+                           dim3(first_out + product_grid(wo, G::kTile).x), dim3(G::kThreads), 0, s, x, wi,
+                           wo, static_cast<int>(first_in), static_cast<int>(first_out));
+      });
+    });
+    launch_splits<T>(x, s), launch_splits<T>(wi, s), launch_splits<T>(wo, s);
+    return check_launch("gated gradient");
+  }
+  if (g.dX) launch_product<T, false, false>(p.x.tile, p.two, x, s);
+  if (g.dW_in) launch_product<T, true, true>(p.wi.tile, p.two, wi, s);
+  if (g.dW_out) launch_product<T, true, true>(p.wo.tile, p.two, wo, s);
   return check_launch("gated gradient");
 }
 
