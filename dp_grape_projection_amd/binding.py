@@ -148,9 +148,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         ctypes.POINTER(LayerGrad), i64, i64, i32, i32, psz]
     lib.dpg_project_layer_packed.argtypes = [
         ctypes.POINTER(LayerGrad), vp, vp, i64, i64, i32, i32, u64, u64, vp, vp, vp, sz, vp]
-    lib.dpg_gated_workspace_size.argtypes = [i64, i64, i64, i32, psz]
+    lib.dpg_gated_workspace_size.argtypes = [i64, i64, i64, i32, i32, psz]
     lib.dpg_gated.argtypes = [vp, vp, vp, i64, i64, i64, i32, i32, vp, vp, vp, vp, sz, vp]
-    lib.dpg_gated_grad_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32, psz]
+    lib.dpg_gated_grad_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32, i32, i32, psz]
     lib.dpg_gated_grad.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp,
                                    vp, vp, vp, vp, vp, sz, vp]
     for name in EXPORTED:
@@ -1025,18 +1025,26 @@ def _gated_args(rows: torch.Tensor, name: str, W_in, W_out):
 
 
 @functools.lru_cache(maxsize=1024)
-def _gated_workspace_size(N, d, f, code):
+def _gated_workspace_size(N, d, f, code, unaligned=0):
     lib, need = load_library(), ctypes.c_size_t(0)
-    _check(lib, lib.dpg_gated_workspace_size(N, d, f, code, ctypes.byref(need)))
+    _check(lib, lib.dpg_gated_workspace_size(N, d, f, code, unaligned, ctypes.byref(need)))
     return need.value
 
 
 @functools.lru_cache(maxsize=1024)
-def _gated_grad_workspace_size(N, d, f, code, have_z, weights):
+def _gated_grad_workspace_size(N, d, f, code, have_z, weights, layers=0, unaligned=0):
     lib, need = load_library(), ctypes.c_size_t(0)
-    _check(lib, lib.dpg_gated_grad_workspace_size(N, d, f, code, have_z, weights,
+    _check(lib, lib.dpg_gated_grad_workspace_size(N, d, f, code, have_z, weights, layers, unaligned,
                                                   ctypes.byref(need)))
     return need.value
+
+
+def _unaligned(*pointers) -> int:
+    """Whether one of the addresses (or None) is not a multiple of 16."""
+    at = 0
+    for p in pointers:
+        at |= p or 0
+    return int(at & 15 != 0)
 
 
 @_on_stream
@@ -1066,8 +1074,10 @@ def dpg_gated(X: torch.Tensor, W_in: torch.Tensor, W_out: torch.Tensor, act: str
         Z = _packed_like(X, (*X.shape[:-1], 2), f)
     if N == 0:
         return Y, Z
-    ws, ws_bytes = _workspace(_gated_workspace_size(N, d, f, code), X.device, workspace)
-    _check(lib, lib.dpg_gated(_ptr(X), _ptr(W_in), _ptr(W_out), N, d, f, code, act_code, _ptr(Y),
+    x, wi, wo = _ptr(X), _ptr(W_in), _ptr(W_out)
+    ws, ws_bytes = _workspace(_gated_workspace_size(N, d, f, code, _unaligned(x, wi, wo)), X.device,
+                              workspace)
+    _check(lib, lib.dpg_gated(x, wi, wo, N, d, f, code, act_code, _ptr(Y),
                               _ptr(Z.codes) if keep else None, _ptr(Z.exps) if keep else None,
                               ws.data_ptr(), ws_bytes, _stream_handle(stream)))
     return Y, Z
@@ -1127,13 +1137,14 @@ def dpg_gated_grad(dY: torch.Tensor, X: Union[torch.Tensor, PackedActivations, N
             if dW is not None:
                 dW.zero_()
         return out
-    need = _gated_grad_workspace_size(N, d, f, code, int(Z is not None), int(w_in or w_out))
+    xp, wi, wo, dy, dz, h = (_ptr(t) for t in (x, W_in, W_out, dY, out.dZ, out.H))
+    need = _gated_grad_workspace_size(N, d, f, code, int(Z is not None), int(w_in or w_out),
+                                      int(need_layers), _unaligned(xp, wi, wo, dy, dz, h))
     ws, ws_bytes = _workspace(need, dY.device, workspace)
     _check(lib, lib.dpg_gated_grad(
-        _ptr(x), _ptr(codes), _ptr(exps), _ptr(W_in), _ptr(W_out),
-        None if Z is None else _ptr(Z.codes), None if Z is None else _ptr(Z.exps), _ptr(dY), N, d,
-        f, code, act_code, _ptr(out.dX), _ptr(out.dW_in), _ptr(out.dW_out), _ptr(out.dZ),
-        _ptr(out.H), ws.data_ptr(), ws_bytes, _stream_handle(stream)))
+        xp, _ptr(codes), _ptr(exps), wi, wo, None if Z is None else _ptr(Z.codes),
+        None if Z is None else _ptr(Z.exps), dy, N, d, f, code, act_code, _ptr(out.dX),
+        _ptr(out.dW_in), _ptr(out.dW_out), dz, h, ws.data_ptr(), ws_bytes, _stream_handle(stream)))
     return out
 
 

@@ -7,6 +7,7 @@ dp_grape_projection_amd/libdpg.so. No GPU is needed to build.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import shutil
@@ -47,14 +48,14 @@ def sources():
 def build(verbose: bool = False) -> str:
     """Compile all sources and link libdpg.so; returns its path."""
     cc = hipcc()
-    objs = []
     with tempfile.TemporaryDirectory(prefix="dpg_build_") as tmp:
-        for src in sources():
+        def compile_one(src):
             obj = os.path.join(tmp, os.path.basename(src) + ".o")
-            cmd = [cc, *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", src,
-                   "-o", obj]
-            _run(cmd, verbose)
-            objs.append(obj)
+            _run([cc, *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj], verbose)
+            return obj
+
+        with concurrent.futures.ThreadPoolExecutor(max_workers=4) as pool:
+            objs = list(pool.map(compile_one, sources()))
         out_tmp = LIB + ".tmp"
         _run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs,
               "-o", out_tmp], verbose)

@@ -3,7 +3,10 @@
 //
 // Both kernels are bound by memory: a row of d bf16 values is 2 d bytes against 1.03 d
 // of codes and exponents. A lane takes 8 channels (16 or 32 bytes of X, 8 bytes of
-// codes); the four lanes of a block find its largest magnitude between them.
+// codes), four such pieces in flight; the four lanes of a block find its largest magnitude
+// between them. 8192 x 8192 bf16: written in 47 us (4.3 TB/s), read back in 31 (6.6 TB/s,
+// part of it from the memory-side cache), where a large copy moves 5.2 TB/s; 16384 x 11008:
+// 119 and 86 us.
 #include <cmath>
 #include <string>
 

@@ -11,8 +11,14 @@
 // up projection, so that a lane holds G and U of the same places and H leaves the tile
 // without either being stored. What the backward pass keeps of them is the caller's
 // choice: their 8-bit form (dpg_act8.hpp), written by the same epilogue, or nothing, in
-// which case they are computed again, in fp32, a run of rows at a time. dH never leaves
-// its tile either: the epilogue of its product reads G and U and writes dG, dU and H.
+// which case they are computed again, without a rounding, by the blocks that need them.
+// dH is not stored as a matrix either: what computes it has G and U of the same places
+// and writes dG, dU and H.
+//
+// Epilogues keep to registers: quarters of a wave change places with four registers
+// (dpg_tile.hpp), so that a lane stores 16 bytes of one row where it held four columns of
+// four blocks, without LDS, barriers or the copies' space (forward and backward of 8192 x
+// 2048 x 8192, 8-bit projections: 2.28 ms staged in LDS, 2.13 so).
 //
 // Inside, Z = [G | U] and dZ have their halves fq columns apart, f rounded up to 8, so
 // that both halves' rows can be copied 16 bytes at a time; what lies between and after
@@ -20,6 +26,7 @@
 // gradients sum over.
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <string>
 
 #include "dpg.h"
@@ -209,12 +216,17 @@ __device__ __forceinline__ void store_strips(bf16* dst, int64_t part, bool two, 
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)  // (an infinity leaves nothing)
-      x[mb][i] = fabsf(x[mb][i]) < INFINITY ? x[mb][i] - static_cast<float>(from_float<bf16>(x[mb][i])) : 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      const float v = static_cast<float>(from_float<bf16>(x[mb][i]));
+      x[mb][i] = fabsf(v) < INFINITY ? x[mb][i] - v : 0.0f;  // (an infinity leaves nothing)
+    }
   store_strip<MB, 1>(dst + part, x, kq, row, n);
 }
 
-// A tile of G and U: TILE / 2 columns of each by TILE rows.
+// A tile of G and U: TILE / 2 columns of each by TILE rows. Bound by the products: 16384 x
+// 4096 x 11008 in 2.13 to 2.20 ms, 1390 to 1340 TFLOP/s; with the 8-bit form written,
+// 8192 x 2048 x 8192 in 484 us, 1140 TFLOP/s (the epilogue rounds and packs 128 values a
+// lane, 10 us of a tile's 60).
 template <class G, int PARTS, int ACT, bool CODES>
 __global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void gate_up_kernel(const GatedArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[kLdsOf<G, PARTS>];
@@ -360,7 +372,11 @@ __host__ __device__ __forceinline__ int grad_cols(const GatedArgs& a) {
   return a.ldh > u ? a.ldh : u;
 }
 
-// A tile of dH, from which with G and U in their 8-bit form dG, dU and H follow.
+// A tile of dH, from which with G and U in their 8-bit form dG, dU and H follow. 8192 x
+// 2048 x 8192: 328 us, of which the product is 215; the rest is the epilogues' 540 MB,
+// which all CUs read and write at the same time, and 20 vector instructions a value. (564
+// us with strips staged in LDS and registers spilled; 354 with the activation chosen
+// inside the kernel.)
 template <class G, int PARTS, int ACT>
 __global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void gate_up_grad_kernel(const GatedArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[kLdsOf<G, PARTS>];
@@ -420,9 +436,12 @@ __global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void gate_up_gr
 }
 
 // The same with G and U computed again: a block takes tiles in turn, computes dH, puts it
-// where only it reads, and then both projections of the same columns, half of a wave's at
-// a time, in the places where the wave had dH. Two products with fp32 results between them
-// would write and read 12 bytes for every element of dH (TIMES).
+// where only it reads, and then both projections of the same columns, half of a wave's
+// at a time, in the places where the wave had dH. Two kernels with G and U in fp32 between
+// them write and read 16 bytes for every element of dH (16384 x 768 x 2048: 274 us so, 213
+// in one; 16384 x 4096 x 11008: 4.15 and 3.59 ms). What bounds it is the products, at 1230
+// TFLOP/s of the 1250 to 1340 that a large one of the library reaches, and for short K the
+// epilogues between them, which nothing overlaps in a block that has all of LDS.
 template <class G, int PARTS, int ACT>
 __global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void gate_up_again_kernel(const GatedArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[kLdsOf<G, PARTS>];
@@ -553,8 +572,8 @@ __global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void product_ke
 }
 
 // The three products of the gradients in one launch, where none of them takes big tiles:
-// each alone leaves CUs idle, and a launch is 3 us of host time (128 x 64 x 256, fp32:
-// THREETIMES).
+// each alone leaves CUs idle, and a launch is 3 us of host time (forward and backward of
+// 128 x 64 x 256, fp32: 40 us, 45 with three launches).
 template <class G, typename T, int PARTS>
 __global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void three_products_kernel(
     const ProductArgs dx, const ProductArgs dw_in, const ProductArgs dw_out, int first_in, int first_out) {
@@ -759,7 +778,7 @@ __global__ __launch_bounds__(kThreads, 1) void few_rows_kernel(const FewArgs a) 
     for (int j = 0; j < 4; ++j) {
       v[j] = from_float<bf16>(hv[j]);
       // (an infinity leaves nothing)
-      rest[j] = fabsf(hv[j]) < INFINITY ? hv[j] - static_cast<float>(v[j]) : 0.0f;
+      rest[j] = fabsf(static_cast<float>(v[j])) < INFINITY ? hv[j] - static_cast<float>(v[j]) : 0.0f;
     }
     *reinterpret_cast<Vec4<bf16>::type*>(dst) = v;
     store4<bf16>(dst + kFewRows * static_cast<int64_t>(a.cols), rest[0], rest[1], rest[2], rest[3]);
@@ -796,8 +815,8 @@ int32_t resident(Tile t, int parts) {
 // and which needs all of K, as dH does (kWhole) and the three products of kAgain.
 // Modelled on 300 measurements: with c blocks on a CU, a K step takes 1.05 + 0.5 c us in a
 // big tile, 0.5 max(1, c) in a small one, 0.34 + 0.13 (c - 1) in a tiny one, a fifth more
-// where both operands are read transposed; in three parts PARTSTIMES; outputs and partial
-// sums are written at 5.6 TB/s, and adding those up is a launch of 2.5 us and 6.5 TB/s.
+// where both operands are read transposed; in three parts 2.5 us in a small tile, 1.05 max(1,
+// c) in a tiny one; outputs and partial sums are written at 5.6 TB/s, and adding those up is a launch of 2.5 us and 6.5 TB/s.
 // (dW_out of 16384 x 768 x 2048: 64 us in small tiles with 5 splits, 65 big with 10, 90
 // tiny with 2; of 128 x 64 x 256: 3.6 tiny, 4.5 small, 7.9 big. dX of 2048 x 2048 x 4096:
 // 67 us in small tiles, 73 big with 4 splits, 99 tiny.)
@@ -856,14 +875,18 @@ int check_call(const Call& c) {
 }
 
 // With few rows of bf16, H and dZ stay in two parts: the products they enter cost twice
-// as much, but an output of few values then has one rounding and not two (TWOTIMES).
+// as much, but an output of few values, whose two roundings do not average out, then has
+// one (64 rows x 2048 x 8192: forward 41 us, 34 with one part, backward 128 and 108; 32 x
+// 768 x 2048: 16 and 17, 35 and 30; errors over those of one rounding, 47 outputs of 1 to 64
+// rows: all 1.00, with one part 1.41 in the middle and up to 1.47).
 constexpr int64_t kTwoRows = 64;
 
 // Where everything lies in the workspace. Copies of the operands are planned whatever
 // their alignment, since a size depends on shapes alone.
 struct Plan {
   int64_t parts, ldx, ldh, fq, ldz, np, fp;
-  bool two;  // H and dZ in two parts
+  bool two;    // H and dZ in two parts
+  bool whole;  // no rows of dZ and H need padding
   Choice y{}, x{}, wi{}, wo{}, again{};
   int64_t again_blocks = 0;
   int32_t few_splits = 0;  // few rows: parts of f in the second product
@@ -872,7 +895,8 @@ struct Plan {
 };
 
 // Few rows of bf16 in whole K steps go their own way where the weights are 16-byte
-// aligned (4 rows x 2048 x 8192: FEWTIMES).
+// aligned (4 rows x 2048 x 8192: 30 us, 42 in tiles; 16 rows x 4096 x 11008: 78, where 17
+// rows take 88 in tiles; the weights alone are 19 and 52 us of a large copy).
 bool few_rows(const Call& c) {
   return c.dtype == DPG_BF16 && c.N <= kFewRows && c.d % kFewK == 0 && c.f % kFewK == 0;
 }
@@ -881,7 +905,13 @@ size_t acc_bytes(const Choice& c, int64_t halves, int64_t m, int64_t n) {
   return c.splits > 1 ? c.splits * round_up(n, kPad) * halves * round_up(m, 64) * 4 : 0;
 }
 
-Plan plan_gated(const Call& c, bool grad, bool again, bool weights) {
+// What a call needs of the workspace beside its shape.
+struct Needs {
+  bool grad, again, weights;
+  bool layers;     // dZ and H are the caller's, both of them
+  bool unaligned;  // some operand or output is not 16-byte aligned
+};
+Plan plan_gated(const Call& c, const Needs& w) {
   Plan p;
   p.parts = c.dtype == DPG_BF16 ? 1 : 3;
   p.ldx = round_up(c.d, kStepK);
@@ -897,14 +927,19 @@ Plan plan_gated(const Call& c, bool grad, bool again, bool weights) {
     off += align_up(static_cast<size_t>(elems * size));
     return at;
   };
-  p.off_x = take(p.parts * c.N * p.ldx, 2);
-  p.off_wi = take(p.parts * c.d * p.ldz, 2);
-  p.off_wo = take(p.parts * c.f * p.ldx, 2);
-  p.off_dy = take(grad ? p.parts * c.N * p.ldx : 0, 2);
+  // operands are copied where they are split, where their rows are no whole 16 bytes or
+  // K steps, and where they do not start on 16 bytes
+  const bool copy = p.parts == 3 || w.unaligned, copy_rows = copy || c.d % kStepK;
+  p.off_x = take(copy_rows ? p.parts * c.N * p.ldx : 0, 2);
+  p.off_wi = take(copy || c.f % 8 ? p.parts * c.d * p.ldz : 0, 2);
+  p.off_wo = take(copy || c.d % 8 ? p.parts * c.f * p.ldx : 0, 2);
+  p.off_dy = take(w.grad && copy_rows ? p.parts * c.N * p.ldx : 0, 2);
   p.two = c.dtype == DPG_BF16 && c.N <= kTwoRows;
   const int64_t made = p.two ? 2 : p.parts;  // parts of what the kernels make
-  p.off_h = take(made * p.np * p.ldh, 2);
-  if (!grad) {
+  // dZ and H go straight to the caller where they need no padding
+  p.whole = c.dtype == DPG_BF16 && !p.two && !w.unaligned && c.N % kStepK == 0;
+  p.off_h = take(w.layers && p.whole && p.ldh == c.f ? 0 : made * p.np * p.ldh, 2);
+  if (!w.grad) {
     p.y = choose(c.d, c.N, p.ldh / kStepK, later, kPlain);
     size_t acc = acc_bytes(p.y, 1, c.d, c.N);
     if (few_rows(c)) {
@@ -916,8 +951,8 @@ Plan plan_gated(const Call& c, bool grad, bool again, bool weights) {
     }
     p.off_acc = take(static_cast<int64_t>(acc), 1);
   } else {
-    p.off_dz = take(made * p.np * p.ldz, 2);
-    if (again) {
+    p.off_dz = take(w.layers && p.whole && p.ldz == 2 * c.f ? 0 : made * p.np * p.ldz, 2);
+    if (w.again) {
       // three products in one kernel, whose blocks are as many as the chip holds at most
       const int64_t cols = std::max(p.ldh, p.ldz - p.fq);
       p.again = choose(cols, c.N, ceil_div(c.d, kStepK), parts, kAgain);
@@ -932,7 +967,7 @@ Plan plan_gated(const Call& c, bool grad, bool again, bool weights) {
     }
     p.x = choose(c.d, c.N, p.ldz / kStepK, later, kPlain);
     p.off_acc = take(static_cast<int64_t>(acc_bytes(p.x, 1, c.d, c.N)), 1);
-    if (weights) {
+    if (w.weights) {
       p.wi = choose(2 * c.f, c.d, ceil_div(c.N, kStepK), later, kBothTransposed);
       p.wo = choose(c.d, c.f, ceil_div(c.N, kStepK), later, kBothTransposed);
       p.off_acc_wi = take(static_cast<int64_t>(acc_bytes(p.wi, 2, c.f, c.d)), 1);
@@ -1101,6 +1136,10 @@ int run_few(const Call& c, const Plan& p, const void* X, const void* W_in, const
   return check_launch("gated block");
 }
 
+bool unaligned(std::initializer_list<const void*> pointers) {
+  return std::any_of(pointers.begin(), pointers.end(), [](const void* p) { return !aligned(p, 16); });
+}
+
 struct Grads {
   void *dX, *dW_in, *dW_out, *dZ, *H;
 };
@@ -1129,10 +1168,7 @@ int run_backward(const Call& c, const Plan& p, const void* X, const int8_t* x_co
   a.w_out = o.bring(W_out, c.f, c.d, 1, 0, p.ldx, p.off_wo, kHalf && c.d % 8 == 0 && aligned(W_out, 16));
   a.dy = o.bring(dY, c.N, c.d, 1, 0, p.ldx, p.off_dy, kHalf && c.d % kStepK == 0 && aligned(dY, 16));
   o.launch(s);
-  // dZ and H go straight to the caller where they need no padding
-  const bool whole = kHalf && !p.two && c.N % kStepK == 0;
-  const bool own_z = whole && g.dZ && p.ldz == 2 * c.f && aligned(g.dZ, 16);
-  const bool own_h = whole && g.H && p.ldh == c.f && aligned(g.H, 16);
+  const bool own_z = p.whole && g.dZ && p.ldz == 2 * c.f, own_h = p.whole && g.H && p.ldh == c.f;
   bf16* const dz = own_z ? static_cast<bf16*>(g.dZ) : reinterpret_cast<bf16*>(ws + p.off_dz);
   bf16* const h = own_h ? static_cast<bf16*>(g.H) : reinterpret_cast<bf16*>(ws + p.off_h);
   // (rows past N are written only where both have them)
@@ -1198,12 +1234,13 @@ using namespace dpg;
 
 extern "C" {
 
-int dpg_gated_workspace_size(int64_t N, int64_t d, int64_t f, int32_t dtype, size_t* bytes) {
+int dpg_gated_workspace_size(int64_t N, int64_t d, int64_t f, int32_t dtype, int32_t unaligned,
+                             size_t* bytes) {
   record_error(DPG_OK, "");
   if (!bytes) return fail(DPG_ERR_INVALID_ARG, "bytes is NULL");
   const Call c{N, d, f, dtype, DPG_ACT_SILU};
   if (const int st = check_call_shape(c)) return st;
-  *bytes = plan_gated(c, false, false, false).total;
+  *bytes = plan_gated(c, {false, false, false, false, unaligned != 0}).total;
   return DPG_OK;
 }
 
@@ -1215,23 +1252,24 @@ int dpg_gated(const void* X, const void* W_in, const void* W_out, int64_t N, int
   if (const int st = check_call(c)) return st;
   if (!X || !W_in || !W_out || !Y) return fail(DPG_ERR_INVALID_ARG, "NULL data pointer");
   if (!z_codes != !z_exps) return fail(DPG_ERR_INVALID_ARG, "z_codes and z_exps go together");
-  const Plan p = plan_gated(c, false, false, false);
+  const bool off = unaligned({X, W_in, W_out});
+  const Plan p = plan_gated(c, {false, false, false, false, off});
   if (const int st = check_ws(workspace, workspace_bytes, p.total)) return st;
   char* ws = static_cast<char*>(workspace);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (few_rows(c) && aligned(X, 16) && aligned(W_in, 16) && aligned(W_out, 16))
+  if (few_rows(c) && !off)
     return run_few(c, p, X, W_in, W_out, Y, z_codes, z_exps, ws, s);
   return dtype == DPG_BF16 ? run_forward<bf16>(c, p, X, W_in, W_out, Y, z_codes, z_exps, ws, s)
                            : run_forward<float>(c, p, X, W_in, W_out, Y, z_codes, z_exps, ws, s);
 }
 
 int dpg_gated_grad_workspace_size(int64_t N, int64_t d, int64_t f, int32_t dtype, int32_t have_z,
-                                  int32_t weights, size_t* bytes) {
+                                  int32_t weights, int32_t layers, int32_t unaligned, size_t* bytes) {
   record_error(DPG_OK, "");
   if (!bytes) return fail(DPG_ERR_INVALID_ARG, "bytes is NULL");
   const Call c{N, d, f, dtype, DPG_ACT_SILU};
   if (const int st = check_call_shape(c)) return st;
-  *bytes = plan_gated(c, true, !have_z, weights != 0).total;
+  *bytes = plan_gated(c, {true, !have_z, weights != 0, layers != 0, unaligned != 0}).total;
   return DPG_OK;
 }
 
@@ -1250,7 +1288,8 @@ int dpg_gated_grad(const void* X, const int8_t* x_codes, const uint8_t* x_exps, 
   if (!z_codes && !X) return fail(DPG_ERR_INVALID_ARG, "the projections need X, or their 8-bit form");
   if (dW_in && !X && !x_codes) return fail(DPG_ERR_INVALID_ARG, "dW_in needs X, or its 8-bit form");
   if (!dX && !dW_in && !dW_out && !dZ && !H) return fail(DPG_ERR_INVALID_ARG, "no output is asked for");
-  const Plan p = plan_gated(c, true, !z_codes, dW_in || dW_out);
+  const Plan p = plan_gated(c, {true, !z_codes, dW_in || dW_out, dZ && H,
+                                unaligned({X, W_in, W_out, dY, dZ, H})});
   if (const int st = check_ws(workspace, workspace_bytes, p.total)) return st;
   char* ws = static_cast<char*>(workspace);
   hipStream_t s = static_cast<hipStream_t>(stream);

@@ -146,10 +146,10 @@ __device__ __forceinline__ void pack_row(const T* src, bf16* dst, int d, int ldx
 
 // --------------------------------------------------------------- products --
 //
-// One device function computes the three products in tiles of 256 x 256 (8
+// One device function computes products A B^T in tiles of 256 x 256 (8
 // waves of 128 x 64, one block per CU) or, where those would not fill the 256
 // CUs, 128 x 128 (4 waves of 64 x 64, two blocks per CU), with 16x16x32 matrix
-// instructions:
+// instructions; those of the losses, for instance:
 //   logits   M = vocabulary rows (E), N = packed rows (Xp), K = d
 //   dX       M = columns (E), N = packed rows (D), K = the vocabulary piece
 //   dE       M = columns (Xp), N = vocabulary rows (D), K = packed rows
@@ -458,7 +458,8 @@ __device__ __forceinline__ void tile_product(const Operand& oa, const Operand& o
 
 // The same for operands in three bf16 parts, all of a K step's parts at once: a step of 32
 // is six tiles in LDS (A's parts, then B's), read once for the six products, where a pass
-// over K for every product would copy and read twelve (TIMESPARTS). Three stages, the
+// over K for every product would copy and read twelve (dX of 999 x 768 x 2050: 38 us so,
+// 47 in passes; the weights' gradients 80 and 108). Three stages, the
 // copies two steps ahead; a step's fragments are read while the products of the one before
 // it run, which takes most of the 512 registers that four waves on a CU have. An
 // operand whose K runs along its rows lies in rows of 64 bytes, chunk c of row R in slot

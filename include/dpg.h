@@ -503,14 +503,17 @@ typedef enum {
  * unless their 8-bit form is asked for (both or neither of z_codes and z_exps), for
  * dpg_gated_grad: rows (n, half) of f channels, as dpg_pack_act writes them,
  *   z_codes  device out [N][2][32 ceil(f / 32)],  z_exps  [N][2][ceil(f / 32)].
- * Products run on 16-bit operands and accumulate in fp32: with bf16, H is rounded once;
+ * Products run on 16-bit operands and accumulate in fp32: with bf16, H is rounded once
+ * (to 16 bits for up to 64 rows, whose few outputs would not average the rounding out);
  * with fp32, operands are split exactly into three bf16 parts, so that products keep
  * fp32's accuracy. G and U are never rounded before the activation. An infinity in an
  * operand can make NaN of all that it meets. Results do not vary from run to run.
- *   workspace  dpg_gated_workspace_size(...) bytes, 256-byte aligned
+ *   workspace  dpg_gated_workspace_size(...) bytes, 256-byte aligned; unaligned: X, W_in
+ *              or W_out does not start on 16 bytes (room for copies of them)
  * Limits: N in [1, 2^22], d and f in [1, 2^16].
  */
-int dpg_gated_workspace_size(int64_t N, int64_t d, int64_t f, int32_t dtype, size_t* bytes);
+int dpg_gated_workspace_size(int64_t N, int64_t d, int64_t f, int32_t dtype, int32_t unaligned,
+                             size_t* bytes);
 int dpg_gated(const void* X, const void* W_in, const void* W_out, int64_t N, int64_t d,
               int64_t f, int32_t dtype, int32_t act, void* Y, int8_t* z_codes,
               uint8_t* z_exps, void* workspace, size_t workspace_bytes, void* stream);
@@ -526,12 +529,15 @@ int dpg_gated(const void* X, const void* W_in, const void* W_out, int64_t N, int
  *             computed again from X, without a rounding
  *   X         [N][d], for dW_in and for computing G and U again; or, for dW_in,
  *             x_codes and x_exps, its form of dpg_pack_act (then X is NULL)
- * With bf16, dZ and H are rounded once, before the products that they enter; dH is not.
+ * With bf16, dZ and H are rounded once, before the products that they enter (up to 64
+ * rows: to 16 bits); dH is not.
  *   workspace  dpg_gated_grad_workspace_size(...) bytes, 256-byte aligned; have_z:
- *              z_codes is given, weights: dW_in or dW_out is asked for
+ *              z_codes is given, weights: dW_in or dW_out is asked for, layers: dZ and H
+ *              are, unaligned: X, W_in, W_out, dY, dZ or H does not start on 16 bytes
  */
 int dpg_gated_grad_workspace_size(int64_t N, int64_t d, int64_t f, int32_t dtype,
-                                  int32_t have_z, int32_t weights, size_t* bytes);
+                                  int32_t have_z, int32_t weights, int32_t layers,
+                                  int32_t unaligned, size_t* bytes);
 int dpg_gated_grad(const void* X, const int8_t* x_codes, const uint8_t* x_exps,
                    const void* W_in, const void* W_out, const int8_t* z_codes,
                    const uint8_t* z_exps, const void* dY, int64_t N, int64_t d, int64_t f,

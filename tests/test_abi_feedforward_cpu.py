@@ -62,10 +62,10 @@ def test_block_gradient_refuses(lib, kw):
 
 def test_block_workspace(lib):
     a, b, c, e = (ctypes.c_size_t(0) for _ in range(4))
-    assert lib.dpg_gated_workspace_size(4, 8, 16, 1, ctypes.byref(a)) == 0
-    assert lib.dpg_gated_grad_workspace_size(4, 8, 16, 1, 1, 0, ctypes.byref(b)) == 0
-    assert lib.dpg_gated_grad_workspace_size(4, 8, 16, 1, 1, 1, ctypes.byref(c)) == 0
-    assert lib.dpg_gated_grad_workspace_size(4, 8, 16, 1, 0, 1, ctypes.byref(e)) == 0
+    assert lib.dpg_gated_workspace_size(4, 8, 16, 1, 0, ctypes.byref(a)) == 0
+    assert lib.dpg_gated_grad_workspace_size(4, 8, 16, 1, 1, 0, 1, 0, ctypes.byref(b)) == 0
+    assert lib.dpg_gated_grad_workspace_size(4, 8, 16, 1, 1, 1, 1, 0, ctypes.byref(c)) == 0
+    assert lib.dpg_gated_grad_workspace_size(4, 8, 16, 1, 0, 1, 1, 0, ctypes.byref(e)) == 0
     assert 0 < a.value and b.value < c.value < e.value
     assert all(x.value % 256 == 0 for x in (a, b, c, e))
     for kw in (dict(n=a.value - 1), dict(ws=None), dict(ws=P + 16)):
@@ -73,16 +73,36 @@ def test_block_workspace(lib):
     for kw in (dict(n=c.value - 1), dict(zc=None, ze=None, n=e.value - 1), dict(ws=P + 16),
                dict(dW_in=None, dW_out=None, n=b.value - 1)):
         assert _call(lib.dpg_gated_grad, GRAD, BLOCK, kw) == WORKSPACE
-    assert lib.dpg_gated_workspace_size(4, 8, 16, 1, None) == INVALID
-    assert lib.dpg_gated_workspace_size(4, 8, 16, 7, ctypes.byref(a)) == INVALID
-    assert lib.dpg_gated_grad_workspace_size(4, 8, 16, 1, 1, 1, None) == INVALID
+    assert lib.dpg_gated_workspace_size(4, 8, 16, 1, 0, None) == INVALID
+    assert lib.dpg_gated_workspace_size(4, 8, 16, 7, 0, ctypes.byref(a)) == INVALID
+    assert lib.dpg_gated_grad_workspace_size(4, 8, 16, 1, 1, 1, 0, 0, None) == INVALID
+
+
+def test_workspace_holds_copies_only_where_they_are_needed(lib):
+    """Aligned bf16 operands of whole K steps are read where they are, and the private
+    step's dZ and H are written where the caller has them."""
+    def size(name, *args):
+        need = ctypes.c_size_t(0)
+        assert getattr(lib, name)(*args, ctypes.byref(need)) == 0
+        return need.value
+    N, d, f = 4096, 1024, 4096
+    operands = 2 * (N * d + 3 * d * f)
+    forward = size("dpg_gated_workspace_size", N, d, f, 1, 0)
+    assert 2 * N * f <= forward < 2 * N * f + (1 << 20)
+    assert size("dpg_gated_workspace_size", N, d, f, 1, 1) >= forward + operands
+    assert size("dpg_gated_workspace_size", N, d, f, 0, 0) >= 3 * operands
+    args = (N, d, f, 1, 1, 0)
+    made = size("dpg_gated_grad_workspace_size", *args, 0, 0)
+    assert made >= 6 * N * f
+    assert size("dpg_gated_grad_workspace_size", *args, 1, 0) <= made - 6 * N * f
+    assert size("dpg_gated_grad_workspace_size", *args, 1, 1) >= made + operands
 
 
 def test_projections_computed_again_take_a_bounded_workspace(lib):
     """G and U in fp32 would be 2^20 x 2 x 4096 x 4 bytes, 34 GB, at once."""
     a, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
-    assert lib.dpg_gated_grad_workspace_size(2 ** 20, 64, 4096, 1, 1, 0, ctypes.byref(a)) == 0
-    assert lib.dpg_gated_grad_workspace_size(2 ** 20, 64, 4096, 1, 0, 0, ctypes.byref(b)) == 0
+    assert lib.dpg_gated_grad_workspace_size(2 ** 20, 64, 4096, 1, 1, 0, 0, 0, ctypes.byref(a)) == 0
+    assert lib.dpg_gated_grad_workspace_size(2 ** 20, 64, 4096, 1, 0, 0, 0, 0, ctypes.byref(b)) == 0
     assert b.value - a.value <= 1 << 30
 
 

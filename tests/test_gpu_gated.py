@@ -87,7 +87,7 @@ def _run(N, d, f, dtype, act, offset=0):
     X, W_in, W_out, dY = _case(N, d, f, dtype, 1, offset)
     x, wi, wo, dy = (_host(t) for t in (X, W_in, W_out, dY))
     code = b._dtype_code(X.dtype)
-    ws = _poisoned(b._gated_workspace_size(N, d, f, code))
+    ws = _poisoned(b._gated_workspace_size(N, d, f, code, int(offset > 0)))
     want, G, Uv = of.gated(x, wi, wo, act)
     H = of.activation(G, act)[0] * Uv
     Y, none = dpg.dpg_gated(X, W_in, W_out, act=act, workspace=ws)
@@ -106,7 +106,8 @@ def _run(N, d, f, dtype, act, offset=0):
     assert (np.abs(kept - exact) <= half + noise).all()
     # the backward pass: from the codes, and with both projections computed again
     for name, Zp, Xp, g, u in (("codes", Z, X, kept[:, 0], kept[:, 1]), ("again", None, X, G, Uv)):
-        ws = _poisoned(b._gated_grad_workspace_size(N, d, f, code, int(Zp is not None), 1))
+        ws = _poisoned(b._gated_grad_workspace_size(N, d, f, code, int(Zp is not None), 1, 1,
+                                                    int(offset > 0)))
         out = dpg.dpg_gated_grad(dY, Xp, W_in, W_out, act=act, Z=Zp, need_layers=True, workspace=ws)
         dX, dWi, dWo, dZ, Hk = of.gated_grad(dy, x, g, u, wi, wo, act)
         _check(out.dZ, dZ, name + " dZ", dtype)
@@ -134,7 +135,9 @@ def _run(N, d, f, dtype, act, offset=0):
 
 
 SIZES = [(1, 8, 8), (1, 1, 1), (3, 5, 7), (2, 64, 31), (4, 64, 128), (128, 64, 256), (65, 128, 96),
-         (130, 100, 70), (257, 72, 264), (300, 130, 33), (64, 320, 64), (513, 65, 161)]
+         (130, 100, 70), (257, 72, 264), (300, 130, 33), (64, 320, 64), (513, 65, 161),
+         # few rows: one and sixteen of them, columns and K that end inside a block's
+         (1, 32, 32), (16, 96, 160), (5, 2080, 1056), (16, 64, 8224), (17, 96, 160)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -154,6 +157,7 @@ def test_activations(act):
 def test_unaligned_operands(dtype):
     """Rows that could be copied as they are, from an address that cannot."""
     _run(130, 64, 64, dtype, "silu", offset=1)
+    _run(9, 64, 64, dtype, "gelu", offset=1)
 
 
 # the tiles of 128 and of 256 rows: enough of them for the rule to take each
@@ -186,6 +190,37 @@ def test_runs_of_rows():
     want = _host(X).T @ _host(whole.dZ)
     assert rel_fro(_host(whole.dW_in), want) <= U      # (dZ as it was rounded)
     assert rel_fro(_host(whole.dW_out), _host(whole.H).T @ _host(dY)) <= U
+
+
+def test_private_layers_alone_need_no_copies_of_them():
+    """dZ and H written straight to the caller, their products reading them there."""
+    import torch
+    import dp_grape_projection_amd as dpg
+    X, W_in, W_out, dY = _case(192, 64, 128, "bf16", 11)
+    _, Z = dpg.dpg_gated(X, W_in, W_out, keep=True)
+    for z in (None, Z):
+        own = dpg.dpg_gated_grad(dY, X, W_in, W_out, Z=z, need_layers=True)
+        part = dpg.dpg_gated_grad(dY, X, W_in, W_out, Z=z)
+        for a, b in zip(own[:3], part[:3]):
+            assert torch.equal(a, b)
+
+
+def test_at_once_on_two_streams():
+    """Two calls in flight at once, each with its own workspace and outputs."""
+    import torch
+    import dp_grape_projection_amd as dpg
+    ins = [_case(1500, 256, 512, "bf16", 20 + k) for k in range(2)]
+    want = [dpg.dpg_gated_grad(t[3], *t[:3], need_layers=True) for t in ins]
+    streams = [torch.cuda.Stream() for _ in ins]
+    torch.cuda.synchronize()
+    got = [[] for _ in ins]
+    for _ in range(5):
+        for k, (t, s) in enumerate(zip(ins, streams)):
+            got[k].append(dpg.dpg_gated_grad(t[3], *t[:3], need_layers=True, stream=s))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for g in got[k]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[k]))
 
 
 def test_wide_values():
