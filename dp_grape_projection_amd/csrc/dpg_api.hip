@@ -719,13 +719,20 @@ int check_clip_sigma(double clip_C, double sigma) {
 // noise 1).
 constexpr uint32_t kTagProbe = 3;
 
-// One layer's input in 8 bits, and the bytes of its workspace that it is read back to.
+// One layer's input in 8 bits. In fp32 it goes its own way to Xt (16-bit products of exact
+// parts) unless the rows are more than one launch reads back; otherwise it is read back
+// and taken as any other.
 struct PackedA {
   const int8_t* codes;
   const uint8_t* exps;
 };
-size_t packed_a_bytes(const dpg_layer_grad& layer, int64_t B, int64_t T, int32_t dtype) {
-  return align_up(static_cast<size_t>(B * T * layer.d_in) * elem_size(dtype));
+bool packed_product(const dpg_layer_grad& layer, int64_t B, int64_t T, int32_t dtype) {
+  return dtype == DPG_FP32 && B * T * (layer.d_in / 8 + 9) < (1ll << 30);
+}
+size_t packed_a_bytes(const dpg_layer_grad& layer, int64_t B, int64_t T, int32_t r, int32_t dtype) {
+  return packed_product(layer, B, T, dtype)
+             ? plan_packed(B * T, layer.d_in, r).total
+             : align_up(static_cast<size_t>(B * T * layer.d_in) * elem_size(dtype));
 }
 
 // The projection call. With ghat == nullptr: the whole batch step (norms,
@@ -754,7 +761,7 @@ int project_impl(const dpg_layer_grad* layers, int32_t n_layers, int64_t B,
   size_t a_bytes = 0;
   if (packed) {  // the one layer's A: read back at the workspace's start
     if (!packed->codes || !packed->exps) return fail(DPG_ERR_INVALID_ARG, "NULL data pointer");
-    a_bytes = packed_a_bytes(layers[0], B, T, dtype);
+    a_bytes = packed_a_bytes(layers[0], B, T, r, dtype);
     own = layers[0];
     own.A = workspace;
     layers = &own;
@@ -774,16 +781,40 @@ int project_impl(const dpg_layer_grad* layers, int32_t n_layers, int64_t B,
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* ws = static_cast<char*>(workspace) + a_bytes;
   const bool bf16 = dtype == DPG_BF16;
-  if (packed &&
-      launch_unpack8(packed->codes, packed->exps, B * T, own.d_in, workspace, bf16, own.d_in, s) != hipSuccess)
+  const bool exact_a = packed && packed_product(own, B, T, dtype);
+  if (exact_a) {
+    const PackedPlan q = plan_packed(B * T, own.d_in, r);
+    char* const area = static_cast<char*>(workspace);
+    float* const Xt = reinterpret_cast<float*>(ws + p.off_Xt[0]);
+    float* const part = reinterpret_cast<float*>(area + q.off_part);
+    if ((st = timed(K_GEN_P, s, [&] {
+           return launch_packed_prep(q, packed->codes, packed->exps, B * T, own.d_in, r, own.layer_id, seed,
+                                     static_cast<uint32_t>(proj_step),
+                                     static_cast<float>(1.0 / std::sqrt(static_cast<double>(r))), area, s);
+         })))
+      return st;
+    if ((st = timed(K_PROJ, s, [&] { return launch_packed_product(q, B, T, r, p.ldt, area, Xt, part, s); })))
+      return st;
+    if (q.splits > 1) {
+      XsumArgs x;
+      std::memset(&x, 0, sizeof(x));
+      x.B = static_cast<int32_t>(B), x.T = static_cast<int32_t>(T), x.r = r;
+      x.ldt = static_cast<int32_t>(p.ldt), x.n_layers = 1;
+      x.L[0] = {part, Xt, q.splits, 0};
+      const int xblocks = static_cast<int>(ceil_div(ceil_div(B * T, 4) * r, kThreads));
+      if ((st = timed(K_XSUM, s, [&] { return launch_xsum(x, xblocks, false, s); }))) return st;
+    }
+  } else if (packed && launch_unpack8(packed->codes, packed->exps, B * T, own.d_in, workspace, bf16,
+                                      own.d_in, s) != hipSuccess) {
     return fail(DPG_ERR_HIP, "unpack: launch failed");
+  }
   const int vec_elems = static_cast<int>(16 / elem_size(dtype));
   float* norm_part = reinterpret_cast<float*>(ws + p.off_norm);
   float* scales = reinterpret_cast<float*>(ws + p.off_scales);
   const uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
   const int64_t BT = B * T;
 
-  for (int l0 = 0; l0 < n_layers; l0 += kMaxLayers) {
+  for (int l0 = 0; l0 < n_layers && !exact_a; l0 += kMaxLayers) {
     const int l1 = std::min(n_layers, l0 + kMaxLayers);
     // 1. P_l, row-major [r][ldp], regenerated from the seed
     {
@@ -1213,7 +1244,7 @@ int dpg_project_layer(const dpg_layer_grad* layer, int64_t B, int64_t T,
 int dpg_project_layer_packed_workspace_size(const dpg_layer_grad* layer, int64_t B, int64_t T,
                                             int32_t r, int32_t dtype, size_t* bytes) {
   if (const int st = dpg_project_workspace_size(layer, 1, B, T, r, dtype, bytes)) return st;
-  *bytes += packed_a_bytes(*layer, B, T, dtype);
+  *bytes += packed_a_bytes(*layer, B, T, r, dtype);
   return DPG_OK;
 }
 

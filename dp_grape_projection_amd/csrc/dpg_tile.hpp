@@ -55,6 +55,13 @@ template <> struct Combos<kTwo> {
   __device__ __forceinline__ static int a(int c) { return c == 0 ? 1 : 0; }
   __device__ __forceinline__ static int b(int c) { return c == 0 ? 1 : 0; }
 };
+// The same with three parts.
+constexpr int kThree = 5;
+template <> struct Combos<kThree> {
+  static constexpr int n = 3;
+  __device__ __forceinline__ static int a(int c) { return (0x012 >> (4 * c)) & 15; }
+  __device__ __forceinline__ static int b(int c) { return (0x012 >> (4 * c)) & 15; }
+};
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
