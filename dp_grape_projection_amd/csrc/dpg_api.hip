@@ -720,17 +720,18 @@ int check_clip_sigma(double clip_C, double sigma) {
 constexpr uint32_t kTagProbe = 3;
 
 // One layer's input in 8 bits. In fp32 it goes its own way to Xt (16-bit products of exact
-// parts) unless the rows are more than one launch reads back; otherwise it is read back
-// and taken as any other.
+// parts) unless A or P's padded rows are more than one launch's 32-bit indexes reach;
+// otherwise it is read back and taken as any other.
 struct PackedA {
   const int8_t* codes;
   const uint8_t* exps;
 };
-bool packed_product(const dpg_layer_grad& layer, int64_t B, int64_t T, int32_t dtype) {
-  return dtype == DPG_FP32 && B * T * (layer.d_in / 8 + 9) < (1ll << 30);
+bool packed_product(const dpg_layer_grad& layer, int64_t B, int64_t T, int32_t r, int32_t dtype) {
+  return dtype == DPG_FP32 && B * T * (layer.d_in / 8 + 9) < (1ll << 30) &&
+         r * round_up(layer.d_in, 64) < (1ll << 31);
 }
 size_t packed_a_bytes(const dpg_layer_grad& layer, int64_t B, int64_t T, int32_t r, int32_t dtype) {
-  return packed_product(layer, B, T, dtype)
+  return packed_product(layer, B, T, r, dtype)
              ? plan_packed(B * T, layer.d_in, r).total
              : align_up(static_cast<size_t>(B * T * layer.d_in) * elem_size(dtype));
 }
@@ -781,7 +782,7 @@ int project_impl(const dpg_layer_grad* layers, int32_t n_layers, int64_t B,
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* ws = static_cast<char*>(workspace) + a_bytes;
   const bool bf16 = dtype == DPG_BF16;
-  const bool exact_a = packed && packed_product(own, B, T, dtype);
+  const bool exact_a = packed && packed_product(own, B, T, r, dtype);
   if (exact_a) {
     const PackedPlan q = plan_packed(B * T, own.d_in, r);
     char* const area = static_cast<char*>(workspace);

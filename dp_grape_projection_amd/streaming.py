@@ -79,7 +79,8 @@ class GrapeOptimizer:
     table -= table_lr * (sum_i s_i g_i + sigma C Z) / B.
     checkpoint: "int8" keeps every layer's input in 8 bits between its forward and its
     backward pass (dpg_pack_act, 1.03 bytes an element); the per-sample gradients are then
-    those of the kept inputs, clip and noise as before.
+    those of the kept inputs, clip and noise as before. A gated block keeps what its own
+    checkpoint says.
     g is the lookup's gradient alone. The losses' [V, d] tables are not clipped here:
     keep them frozen, as a table that serves both ends is for its part in the loss."""
 

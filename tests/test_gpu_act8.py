@@ -203,6 +203,49 @@ def test_projection_from_8_bits(B, T, d_in, d_out, r, dtype):
     assert torch.equal(norm_sq, again)
 
 
+# more tokens than tiny tiles are for; a d_in that is split, at an odd count of tokens
+MORE_LAYERS = [(16, 1024, 100, 33, 321), (3, 37, 1000, 65, 33), (1, 1, 2000, 40, 16), (7, 3, 400, 9, 70)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,T,d_in,d_out,r", MORE_LAYERS)
+def test_projection_in_a_used_workspace(B, T, d_in, d_out, r, dtype):
+    """Whatever the workspace held, in a graph that is replayed, on another stream: the
+    projection of what the codes stand for, within each type's bar (see above)."""
+    import torch
+    import dp_grape_projection_amd as dpg
+    from _helpers import TOL, rel_err
+    print(f"[project] {B} {T} {d_in} {d_out} {r} {dtype}", flush=True)
+    rng = np.random.default_rng([B, T, d_in, d_out, r, 1])
+    A = _dev(rng.standard_normal((B, T, d_in)), dtype)
+    dY = _dev(rng.standard_normal((B, T, d_out)) / np.sqrt(T * d_out), dtype)
+    p = dpg.dpg_pack_act(A)
+    ws = torch.full((1 << 26,), 0xFF, dtype=torch.uint8, device="cuda")     # all NaN
+    norm_sq = torch.zeros(B, device="cuda")
+    G = dpg.dpg_project_layer_packed(p, dY, r, 5, 2, 3, norm_sq, workspace=ws)
+    P = oracle.projection_matrix(5, 3, 2, r, d_in)
+    kept = dpg.dpg_unpack_act(p, dtype=torch.float32).double().cpu().numpy()
+    want = np.stack([(P @ kept[i].T) @ dY[i].double().cpu().numpy() for i in range(B)])
+    assert rel_err(G.double().cpu().numpy(), want) <= TOL[dtype]
+    assert rel_err(norm_sq.double().cpu().numpy(), np.sum(want ** 2, axis=(1, 2))) <= TOL[dtype]
+    s = torch.cuda.Stream()
+    got, n = torch.empty_like(G), torch.zeros_like(norm_sq)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        dpg.dpg_project_layer_packed(p, dY, r, 5, 2, 3, n, G_hat=got, workspace=ws)
+    for _ in range(3):
+        ws.fill_(0xFF), got.fill_(float("nan")), n.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, G) and torch.equal(n, norm_sq)
+    n.zero_()
+    torch.cuda.synchronize()
+    other = dpg.dpg_project_layer_packed(p, dY, r, 5, 2, 3, n, stream=s)
+    s.synchronize()
+    assert torch.equal(other, G) and torch.equal(n, norm_sq)
+
+
 def test_packed_projection_refuses():
     import torch
     import dp_grape_projection_amd as dpg

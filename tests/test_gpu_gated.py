@@ -173,8 +173,8 @@ def test_larger_tiles_fp32():
 
 
 def test_runs_of_rows():
-    """Projections computed again a run of rows at a time: 256 MiB of them are 8192 rows
-    of 4096 channels; the rows past the first run, and a last run of a few rows."""
+    """More tiles than the chip holds at once, their projections computed again: rows from
+    the beginning, the middle and the end against calls of those rows alone."""
     import torch
     import dp_grape_projection_amd as dpg
     N, d, f = 8192 + 256 + 7, 64, 4096
