@@ -732,7 +732,7 @@ bool packed_product(const dpg_layer_grad& layer, int64_t B, int64_t T, int32_t r
 }
 size_t packed_a_bytes(const dpg_layer_grad& layer, int64_t B, int64_t T, int32_t r, int32_t dtype) {
   return packed_product(layer, B, T, r, dtype)
-             ? plan_packed(B * T, layer.d_in, r).total
+             ? plan_packed(B, T, layer.d_in, layer.d_out, r).total
              : align_up(static_cast<size_t>(B * T * layer.d_in) * elem_size(dtype));
 }
 
@@ -783,8 +783,9 @@ int project_impl(const dpg_layer_grad* layers, int32_t n_layers, int64_t B,
   char* ws = static_cast<char*>(workspace) + a_bytes;
   const bool bf16 = dtype == DPG_BF16;
   const bool exact_a = packed && packed_product(own, B, T, r, dtype);
+  PackedPlan q{};
   if (exact_a) {
-    const PackedPlan q = plan_packed(B * T, own.d_in, r);
+    q = plan_packed(B, T, own.d_in, own.d_out, r);
     char* const area = static_cast<char*>(workspace);
     float* const Xt = reinterpret_cast<float*>(ws + p.off_Xt[0]);
     float* const part = reinterpret_cast<float*>(area + q.off_part);
@@ -977,6 +978,16 @@ int project_impl(const dpg_layer_grad* layers, int32_t n_layers, int64_t B,
     for (int l = l0; l < l1; ++l)
       if (layers[l].d_out % kTileN != 0) a.full = 0;
   };
+  if (q.parts > 1) {  // (from 8 bits) T in parts
+    char* const area = static_cast<char*>(workspace);
+    if ((st = timed(K_NORM, s, [&] {
+           return launch_packed_hat(q, B, T, r, p.ldt, own.d_out, reinterpret_cast<const float*>(ws + p.off_Xt[0]),
+                                    static_cast<const float*>(own.dY), area, ghat, s);
+         })))
+      return st;
+    const NormAccArgs a{reinterpret_cast<const float*>(area + q.off_slots), q.slots, static_cast<int32_t>(B), norm_sq};
+    return timed(K_CLIP, s, [&] { return launch_norm_acc(a, s); });
+  }
   // 3. squared-norm partials of every (sample, layer, tile), and with
   //    hat_sum every sample's product
   for (int l0 = 0; l0 < n_layers; l0 += kMaxLayers) {

@@ -286,20 +286,25 @@ hipError_t launch_pack8(const void* X, bool bf16_in, int64_t N, int64_t d, int8_
 hipError_t launch_unpack8(const int8_t* codes, const uint8_t* exps, int64_t N, int64_t d,
                           void* X, bool bf16_out, int64_t ldo, hipStream_t s);
 
-// Xt of one fp32 layer from its input in 8 bits (dpg_packed.hip): its workspace, the codes
-// read back with P generated, and the product, to Xt or, with splits, to `part` as the
-// xsum kernel takes it.
+// One fp32 layer from its input in 8 bits (dpg_packed.hip): its workspace; the codes read
+// back with P generated; the product, to Xt or, with splits, to `part` as the xsum kernel
+// takes it; and, where parts > 1, G_hat from Xt in that many parts of T, with the squared
+// norms' partials.
 struct PackedPlan {
   int64_t ld;       // d_in rounded up to whole K steps
   int32_t splits;
   bool small;       // 128 x 128 tiles
-  size_t off_P, off_part, total;
+  int32_t parts, per;  // parts of T, tokens of each
+  int32_t chunk, slots;  // elements of G_hat that a block joins; partials of a sample
+  size_t off_P, off_part, off_hat, off_slots, total;
 };
-PackedPlan plan_packed(int64_t BT, int64_t d_in, int32_t r);
+PackedPlan plan_packed(int64_t B, int64_t T, int64_t d_in, int64_t d_out, int32_t r);
 hipError_t launch_packed_prep(const PackedPlan& p, const int8_t* codes, const uint8_t* exps, int64_t BT,
                               int64_t d_in, int32_t r, uint32_t layer_id, uint64_t seed, uint32_t proj_step,
                               float scale, char* ws, hipStream_t s);
 hipError_t launch_packed_product(const PackedPlan& p, int64_t B, int64_t T, int32_t r, int64_t ldt,
                                  const char* ws, float* Xt, float* part, hipStream_t s);
+hipError_t launch_packed_hat(const PackedPlan& p, int64_t B, int64_t T, int32_t r, int64_t ldt, int64_t d_out,
+                             const float* Xt, const float* dY, char* ws, float* ghat, hipStream_t s);
 
 }  // namespace dpg

@@ -522,37 +522,6 @@ __global__ __launch_bounds__(kThreads) void xsum_kernel(const XsumArgs a) {
   }
 }
 
-// Stores a tile accumulator with waves 4 x 1 (each lane NB = 4 or 2
-// consecutive columns of 16 rows) into dst = [r][d_out], rows j0 ..,
-// columns n0 ..; rows >= r and columns >= d_out are skipped.
-template <class Tl>
-__device__ __forceinline__ void store_tile(float* dst, const Acc<Tl::MB, Tl::NB>& acc,
-                                           int r, int d_out, int j0, int n0,
-                                           int wave, int lane) {
-  constexpr int NB = Tl::NB;
-  static_assert(Tl::MB == 1 && (NB == 4 || NB == 2) && Tl::WGN == 1, "4 x 1 waves");
-  const int wm = Tl::wave_m(wave);
-  const int nq = n0 + Tl::acc_col(0, 0, lane);  // this lane's NB columns
-  const bool vec = (d_out % NB) == 0 && nq + NB - 1 < d_out && is_aligned(dst, NB * 4);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int j = j0 + Tl::acc_row(wm, 0, i, lane);
-    if (j >= r || nq >= d_out) continue;
-    float* p = dst + static_cast<int64_t>(j) * d_out + nq;
-    if (vec) {
-      if constexpr (NB == 4)
-        *reinterpret_cast<f32x4*>(p) =
-            f32x4{acc.v[0][0][i], acc.v[0][1][i], acc.v[0][2][i], acc.v[0][3][i]};
-      else
-        *reinterpret_cast<f32x2*>(p) = f32x2{acc.v[0][0][i], acc.v[0][1][i]};
-    } else {
-#pragma unroll
-      for (int q = 0; q < NB; ++q)
-        if (nq + q < d_out) p[q] = acc.v[0][q][i];
-    }
-  }
-}
-
 // ---------------------------------------------------------- norm and sum --
 
 // Norm mode: squared-norm partials of Xt_i dY_i per (sample, tile, wave).

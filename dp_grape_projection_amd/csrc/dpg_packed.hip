@@ -1,5 +1,6 @@
-// The first half of a layer's projection from its input in 8 bits, for fp32 operands:
-// Xt[b][j][t] = sum_k P[j][k] A[b][t][k].
+// A layer's projection from its input in 8 bits, for fp32 operands:
+// Xt[b][j][t] = sum_k P[j][k] A[b][t][k], and where the step's own kernels would leave
+// most CUs idle over a long T, G_hat[b][j][n] = sum_t Xt[b][j][t] dY[b][t][n] as well.
 //
 // What a code stands for is a bf16 number, so that A is exact as it is on the 16-bit matrix
 // instructions, which are 16 times as fast as the fp32 ones; P, in fp32, is split exactly
@@ -8,6 +9,7 @@
 // share a long d_in, that is split and the sums added by another. (4096 tokens
 // x 768, r 128: 18 us in all, 30 with A read back to fp32 and the fp32 instructions.)
 #include <algorithm>
+#include <type_traits>
 
 #include "dpg_act8.hpp"
 #include "dpg_device.hpp"
@@ -117,11 +119,108 @@ __global__ __launch_bounds__(G::kThreads, G::kBlocks) void packed_product_kernel
   }
 }
 
+struct PackedHatArgs {
+  const float *Xt, *dY;
+  float* hat;       // [B][parts][r][d_out]
+  int64_t ldt, d_out;
+  int32_t B, T, r, parts, per, off32;
+  int32_t m_tiles, n_tiles;
+};
+
+// One part of T of a tile of one sample's product, both operands in fp32.
+typedef Tile<float, kTileM, kTileN, kStepF32, 4, 1> HatTile;
+__global__ __launch_bounds__(kThreads, 2) void packed_hat_kernel(const PackedHatArgs a) {
+  typedef HatTile Tl;
+  __shared__ __attribute__((aligned(16))) float smem[Tl::kLdsElems];
+  const int block = xcd_logical_block(), tiles = a.m_tiles * a.n_tiles;
+  const int run = block / tiles, at = block - run * tiles;  // a sample's part
+  if (run >= a.B * a.parts) return;
+  const int i = run / a.parts, t0 = (run - i * a.parts) * a.per;
+  const int j0 = at % a.m_tiles * Tl::BM, n0 = at / a.m_tiles * Tl::BN;
+  const int K = min(a.per, a.T - t0);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  RowsLoader<float, Tl::BM, Tl::BK, true, IdentityRows> la{a.ldt, a.r - j0, K, {}};
+  ColsLoader<float, Tl::BN, Tl::BK, true, BOperandRows<Tl>> lb{a.d_out, static_cast<int>(a.d_out) - n0, K, {}};
+  const float* const Xt = a.Xt + (static_cast<int64_t>(i) * a.r + j0) * a.ldt + t0;
+  const float* const dY = a.dY + (static_cast<int64_t>(i) * a.T + t0) * a.d_out + n0;
+  Acc<Tl::MB, Tl::NB> acc;
+  acc.zero();
+  run_steps<float, Tl>(
+      la, lb, smem, acc, (K + Tl::BK - 1) / Tl::BK, tid,
+      [&](int s) {
+        la.load(Xt, s * Tl::BK, tid, a.off32);
+        lb.load(dY, s * Tl::BK, tid, a.off32);
+      },
+      [](int) {});
+  store_tile<Tl>(a.hat + static_cast<int64_t>(run) * a.r * a.d_out, acc, a.r, static_cast<int>(a.d_out), j0, n0,
+                 wave, lane);
+}
+
+// G_hat from its parts, added in their order, and the squared norm of each block's share.
+__global__ __launch_bounds__(kThreads) void packed_join_kernel(const float* hat, float* ghat, float* norm_part,
+                                                               int32_t parts, int64_t size, int32_t chunk,
+                                                               int32_t slots) {
+  __shared__ float sums[kThreads / 64];
+  const int i = blockIdx.x / slots, slot = blockIdx.x - i * slots;
+  const int64_t first = static_cast<int64_t>(slot) * chunk, end = min(size, first + chunk);
+  hat += static_cast<int64_t>(i) * parts * size;
+  float sq = 0.0f;
+  for (int64_t e = first + threadIdx.x; e < end; e += kThreads) {
+    float g = 0.0f;
+    int p = 0;
+    auto add = [&](auto n) {  // (n loads in flight)
+      float x[decltype(n)::value];
+#pragma unroll
+      for (int u = 0; u < decltype(n)::value; ++u) x[u] = hat[(p + u) * size + e];
+#pragma unroll
+      for (int u = 0; u < decltype(n)::value; ++u) g += x[u];
+      p += decltype(n)::value;
+    };
+    while (p + 8 <= parts) add(std::integral_constant<int, 8>{});
+    if (parts & 4) add(std::integral_constant<int, 4>{});
+    if (parts & 2) add(std::integral_constant<int, 2>{});
+    if (parts & 1) add(std::integral_constant<int, 1>{});
+    ghat[static_cast<int64_t>(i) * size + e] = g;
+    sq = fmaf(g, g, sq);
+  }
+  sq = wave_sum(sq);
+  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = sq;
+  __syncthreads();
+  if (threadIdx.x == 0) norm_part[blockIdx.x] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+}
+static_assert(kThreads == 256, "the join adds four waves' sums");
+
 }  // namespace
+
+// Parts of T. Modelled on measurements: a step of a block alone on its CU takes 3.2 us, of
+// two together 5.8 (the fp32 matrix instructions bound both), a launch 4.5, the join 2.5,
+// 0.12 for every part of an element and its bytes. fp32 sums over T one after the other
+// also lose bits: at most kMostT tokens, as long as all parts take 512 MiB at most. The
+// whole call with the step's kernel, which keeps a sample's T in one block, and so: 1 x 5906
+// x 1600 x 384, r 8: 657 us, error 1.4e-6, and 49 us, 2.5e-7; 1 x 8192 x 2048 x 2048, r 256:
+// 863 and 171 us; 8 x 1000 x 768 x 768, r 128: 136 and 59. Twice as many parts as fill the
+// CUs: 32 x 256 x 768 x 768, r 128: 65 us, 54 in one part.
+constexpr int64_t kMostT = 2048;
+int64_t parts_of(int64_t B, int64_t T, int64_t d_out, int64_t r) {
+  const int64_t blocks = B * ceil_div(r, kTileM) * ceil_div(d_out, kTileN), all = ceil_div(T, kStepF32);
+  const double elems = static_cast<double>(B * r) * static_cast<double>(d_out) / 1e6;
+  int64_t best = 1;
+  double best_us = 1e30;
+  for (int64_t k = 1; k <= std::max<int64_t>(1, std::min(512 / blocks, all)); k += std::max<int64_t>(1, k / 4)) {
+    const double step = blocks * k <= 256 ? 3.2 : 5.8 * static_cast<double>(ceil_div(blocks * k, 512));
+    double us = static_cast<double>(ceil_div(all, k)) * step + 4.5;
+    const double n = static_cast<double>(k), each = static_cast<double>(ceil_div(r * d_out, 256 * kThreads));
+    if (k > 1) us += 2.5 + 0.12 * n * each + elems * (8.0 * n + 4.0) / 5.0;
+    if (us < best_us) best_us = us, best = k;
+  }
+  const int64_t room = (int64_t{1} << 29) / (B * r * d_out * 4);
+  return std::max<int64_t>(1, std::min(room, std::max(ceil_div(T, kMostT), best)));
+}
 
 // Tiny tiles where the others would leave most CUs idle; d_in split where even those do
 // and it is long.
-PackedPlan plan_packed(int64_t BT, int64_t d_in, int32_t r) {
+PackedPlan plan_packed(int64_t B, int64_t T, int64_t d_in, int64_t d_out, int32_t r) {
+  const int64_t BT = B * T;
   PackedPlan p;
   p.ld = round_up(d_in, kStepK);
   const int64_t tiny = ceil_div(BT, TinyTile::kTile) * ceil_div(r, TinyTile::kTile), steps = p.ld / kStepK;
@@ -139,6 +238,12 @@ PackedPlan plan_packed(int64_t BT, int64_t d_in, int32_t r) {
   take(BT * p.ld * 2);
   p.off_P = take(3 * static_cast<int64_t>(r) * p.ld * 2);
   p.off_part = take(p.splits > 1 ? p.splits * r * BT * 4 : 0);
+  p.per = static_cast<int32_t>(ceil_div(ceil_div(T, kStepF32), parts_of(B, T, d_out, r)) * kStepF32);
+  p.parts = static_cast<int32_t>(ceil_div(T, p.per));
+  p.chunk = static_cast<int32_t>(ceil_div(r * d_out, 256 * kThreads) * kThreads);
+  p.slots = static_cast<int32_t>(ceil_div(r * d_out, p.chunk));
+  p.off_hat = take(p.parts > 1 ? B * p.parts * r * d_out * 4 : 0);
+  p.off_slots = take(p.parts > 1 ? B * p.slots * 4 : 0);
   p.total = off;
   return p;
 }
@@ -176,6 +281,22 @@ hipError_t launch_packed_product(const PackedPlan& p, int64_t B, int64_t T, int3
   };
   if (p.small) run(SmallTile());
   else run(TinyTile());
+  return hipGetLastError();
+}
+
+hipError_t launch_packed_hat(const PackedPlan& p, int64_t B, int64_t T, int32_t r, int64_t ldt, int64_t d_out,
+                             const float* Xt, const float* dY, char* ws, float* ghat, hipStream_t s) {
+  PackedHatArgs a{};
+  a.Xt = Xt, a.dY = dY, a.hat = reinterpret_cast<float*>(ws + p.off_hat);
+  a.ldt = ldt, a.d_out = d_out;
+  a.B = static_cast<int32_t>(B), a.T = static_cast<int32_t>(T), a.r = r;
+  a.parts = p.parts, a.per = p.per;
+  a.off32 = kTileM * ldt * 4 < (1ll << 31) && p.per * d_out * 4 < (1ll << 31);
+  a.m_tiles = static_cast<int32_t>(ceil_div(r, kTileM)), a.n_tiles = static_cast<int32_t>(ceil_div(d_out, kTileN));
+  hipLaunchKernelGGL(packed_hat_kernel, dim3(static_cast<unsigned>(round_up(B * p.parts * a.m_tiles * a.n_tiles, 8))),
+                     dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL(packed_join_kernel, dim3(static_cast<unsigned>(B * p.slots)), dim3(kThreads), 0, s, a.hat, ghat,
+                     reinterpret_cast<float*>(ws + p.off_slots), p.parts, r * d_out, p.chunk, p.slots);
   return hipGetLastError();
 }
 

@@ -1,6 +1,6 @@
 """A small language model trained privately end to end: token embedding,
-projected linear layers (or gated feed-forward blocks), and a loss that mixes cross entropy with distillation
-from a teacher's top logits, against a frozen [V, d] head.
+projected linear layers (or gated feed-forward blocks), and a loss that mixes cross
+entropy with distillation from a teacher's top logits, against a frozen [V, d] head.
 
     python examples/private_lm.py [steps] [--gated]
 

@@ -203,8 +203,10 @@ def test_projection_from_8_bits(B, T, d_in, d_out, r, dtype):
     assert torch.equal(norm_sq, again)
 
 
-# more tokens than tiny tiles are for; a d_in that is split, at an odd count of tokens
-MORE_LAYERS = [(16, 1024, 100, 33, 321), (3, 37, 1000, 65, 33), (1, 1, 2000, 40, 16), (7, 3, 400, 9, 70)]
+# more tokens than tiny tiles are for; a d_in that is split, at an odd count of tokens; long
+# samples, whose tokens are summed in parts
+MORE_LAYERS = [(16, 1024, 100, 33, 321), (3, 37, 1000, 65, 33), (1, 1, 2000, 40, 16), (7, 3, 400, 9, 70),
+               (1, 5003, 40, 130, 5), (2, 2501, 64, 7, 3), (5, 65, 33, 257, 129), (1, 2049, 8, 300, 300)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
