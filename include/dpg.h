@@ -478,7 +478,9 @@ int dpg_unpack_act(const int8_t* codes, const uint8_t* exps, int64_t N, int64_t 
  * dpg_project_layer_packed_workspace_size / dpg_project_layer_packed:
  * dpg_project_layer with the layer's input A given in the form of dpg_pack_act, as
  * [B T] rows of d_in: the result is that of dpg_project_layer on what the codes stand
- * for. dtype is dY's type and the operands' precision; layer->A is not read.
+ * for, in fp32 with sums in another order (T in parts where it is long). Results do not
+ * vary from run to run. dtype is dY's type and the operands' precision; layer->A is not
+ * read.
  */
 int dpg_project_layer_packed_workspace_size(const dpg_layer_grad* layer, int64_t B, int64_t T,
                                             int32_t r, int32_t dtype, size_t* bytes);
