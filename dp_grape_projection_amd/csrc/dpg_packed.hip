@@ -195,11 +195,12 @@ static_assert(kThreads == 256, "the join adds four waves' sums");
 // Parts of T. Modelled on measurements: a step of a block alone on its CU takes 3.2 us, of
 // two together 5.8 (the fp32 matrix instructions bound both), a launch 4.5, the join 2.5,
 // 0.12 for every part of an element and its bytes. fp32 sums over T one after the other
-// also lose bits: at most kMostT tokens, as long as all parts take 512 MiB at most. The
-// whole call with the step's kernel, which keeps a sample's T in one block, and so: 1 x 5906
-// x 1600 x 384, r 8: 657 us, error 1.4e-6, and 49 us, 2.5e-7; 1 x 8192 x 2048 x 2048, r 256:
-// 863 and 171 us; 8 x 1000 x 768 x 768, r 128: 136 and 59. Twice as many parts as fill the
-// CUs: 32 x 256 x 768 x 768, r 128: 65 us, 54 in one part.
+// also lose bits: at most kMostT tokens, as long as all parts take 512 MiB at most (1 x 5906
+// x 1600 x 384, r 8: error 1.4e-6 in one part, 2.5e-7 so). A whole call of
+// dpg_project_layer, which keeps a sample's T in one block, and of this one: 1 x 5906 x 1600 x
+// 384, r 8: 657 and 49 us; 1 x 8192 x 2048 x 2048, r 256: 863 and 171; 8 x 1000 x 768 x 768,
+// r 128: 136 and 59. Parts where one fills the CUs: 32 x 256 x 768 x 768, r 128: 65 us in
+// two, 54 in one.
 constexpr int64_t kMostT = 2048;
 int64_t parts_of(int64_t B, int64_t T, int64_t d_out, int64_t r) {
   const int64_t blocks = B * ceil_div(r, kTileM) * ceil_div(d_out, kTileN), all = ceil_div(T, kStepF32);
