@@ -7,6 +7,7 @@ from __future__ import annotations
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from . import binding as _b
 from .streaming import ProjectedLinear
@@ -61,6 +62,9 @@ def _gated_block(X, W_in, W_out, act, checkpoint, driver):
     X, W_in, W_out = X.contiguous(), W_in.contiguous(), W_out.contiguous()
     if torch.is_grad_enabled() and any(t.requires_grad for t in (X, W_in, W_out)):
         return _GatedBlock.apply(X, W_in, W_out, act, checkpoint, driver)
+    # (the library's call would lose a tangent, which reads as a derivative of zero)
+    if any(unpack_dual(t).tangent is not None for t in (X, W_in, W_out)):
+        raise NotImplementedError("the gated block has no forward mode")
     return _b.dpg_gated(X, W_in, W_out, act=act)[0]
 
 
@@ -68,10 +72,10 @@ def gated_feed_forward(X: torch.Tensor, W_in: torch.Tensor, W_out: torch.Tensor,
                        act: str = "silu", checkpoint: Optional[str] = None) -> torch.Tensor:
     """(act(X W_gate) * (X W_up)) W_out of X [..., d], W_in = [W_gate | W_up] [d, 2 f] and
     W_out [f, d] in one type (bf16 or fp32); act "silu", "gelu" or "gelu_tanh".
-    Differentiable once in all three; a backward pass that builds a graph of its own is
-    refused. What is kept until then: with checkpoint None X alone, from which both
-    projections are computed again; with "int8" both projections and (for W_in's
-    gradient) X in 8 bits, whose gradients are those at the kept values."""
+    Differentiable once in all three, backwards; a backward pass that builds a graph of its
+    own is refused, and so is forward mode. What is kept until then: with checkpoint None X
+    alone, from which both projections are computed again; with "int8" both projections and
+    (for W_in's gradient) X in 8 bits, whose gradients are those at the kept values."""
     _check_checkpoint(checkpoint)
     return _gated_block(X, W_in, W_out, act, checkpoint, None)
 
