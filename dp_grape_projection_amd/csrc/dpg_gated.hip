@@ -114,8 +114,9 @@ __device__ __forceinline__ float act_of(float x, float& slope) {
     slope = c + x * (0.3989422804f * e);
     return x * c;
   } else {
-    // beyond 20 the sigmoid is 0 or 1 and the slope's second term nothing
-    const float y = __builtin_amdgcn_fmed3f(x, -20.0f, 20.0f);
+    // beyond 20 the sigmoid is 0 or 1 and the slope's second term nothing (the median of a
+    // NaN would be -20, and its slope 0)
+    const float y = x != x ? x : __builtin_amdgcn_fmed3f(x, -20.0f, 20.0f);
     const float s = sigmoid(1.5957691216f * (y + 0.044715f * y * y * y));
     slope = s + y * s * (1.0f - s) * (1.5957691216f * (1.0f + 0.134145f * y * y));
     return x * s;

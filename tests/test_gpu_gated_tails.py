@@ -99,3 +99,24 @@ def test_every_value_to_its_own_precision(act, dtype, N):
         _close(g.H, value, off, dtype, name + " H")
         _close(g.dZ[:, D:], value, off, dtype, name + " dU")
         _close(g.dZ[:, :D], slope, off_slope, dtype, name + " dG")
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_a_gate_that_is_no_number(act, dtype):
+    """What was kept of G reads as NaN in some blocks of 32 columns, U does not: H, dU and
+    dG are NaN there, and nowhere else."""
+    import torch
+    import dp_grape_projection_amd as dpg
+    for N in (40, 200):
+        X, W_in, W_out, dY = _operands(np.linspace(-2, 2, N).astype(np.float32), dtype)
+        _, Z = dpg.dpg_gated(X, W_in, W_out, act=act, keep=True)
+        bad = torch.zeros(N, dtype=torch.bool, device="cuda")
+        bad[3], bad[N - 1] = True, True
+        Z.exps[bad, 0] = 255
+        g = dpg.dpg_gated_grad(dY, X, W_in, W_out, act=act, Z=Z, need_layers=True)
+        for t in (g.H, g.dZ[:, :D], g.dZ[:, D:]):
+            assert torch.equal(t.isnan(), bad[:, None].expand(N, D))
+        # (row 0 of W_in is the gates': a sum over all rows of what is NaN in some)
+        assert g.dX[bad].isnan().all() and not g.dX[~bad].isnan().any()
+        assert g.dW_in.isnan().all() and g.dW_out.isnan().all()
