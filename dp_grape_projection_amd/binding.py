@@ -1069,6 +1069,8 @@ def dpg_gated(X: torch.Tensor, W_in: torch.Tensor, W_out: torch.Tensor, act: str
         if not keep:
             raise ValueError("Z is given, but keep is not set")
         _require_packed(Z, "Z", (*X.shape[:-1], 2), f)
+        if Z.dtype != X.dtype:
+            raise TypeError(f"Z is of {Z.dtype}, X of {X.dtype}")
         _same_device(X, Z=Z.codes)
     elif keep:
         Z = _packed_like(X, (*X.shape[:-1], 2), f)
