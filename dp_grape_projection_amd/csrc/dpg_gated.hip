@@ -22,7 +22,7 @@
 //
 // Inside, Z = [G | U] and dZ have their halves fq columns apart, f rounded up to 8, so
 // that both halves' rows can be copied 16 bytes at a time; what lies between and after
-// is zero, and so are dZ's and H's rows from N up to whole tiles, which the weights'
+// is zero, and so are dZ's and H's rows from N up to whole K steps, which the weights'
 // gradients sum over.
 #include <algorithm>
 #include <cmath>
@@ -38,7 +38,7 @@
 namespace dpg {
 namespace {
 
-constexpr int kPad = 256;  // rows of dZ and H are padded to whole tiles
+constexpr int kPad = 256;  // rows of a product's partial sums are padded to whole tiles
 constexpr float kLog2e = 1.4426950408889634f;
 
 // A matrix as operands of 16 bits see it: rows of ld elements, in one or three parts.
@@ -54,7 +54,7 @@ struct GatedArgs {
   int32_t N, d, f, fq, act;
   int32_t ldh;          // f rounded up to 64
   int32_t fp;           // f rounded up to 32: the codes of one half of a row of Z
-  int32_t np;           // rows of dz and h that are written (N, or whole tiles)
+  int32_t np;           // rows of dz and h that are written: N up to whole K steps
   int8_t* codes;        // [N][2][fp], or null
   uint8_t* exps;        // [N][2][fp / 32]
   bool two;             // bf16: h and dz in two parts
@@ -409,10 +409,9 @@ __global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void gate_up_gr
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
   typename G::Acc acc;
-  // (rows and columns past the last compute the last ones again, and are written as zero)
-  product<G, PARTS, false, false>(rows_of(a.w_out, min(c0, a.f - 1), 0),
-                                       rows_of(a.dy, min(r0, a.N - 1), 0),
-                                       (a.d + kStepK - 1) / kStepK, smem, acc);
+  // (columns past the last compute the last ones again, and are written as zero)
+  product<G, PARTS, false, false>(rows_of(a.w_out, min(c0, a.f - 1), 0), rows_of(a.dy, r0, 0),
+                                  (a.d + kStepK - 1) / kStepK, smem, acc);
   const int cw = c0 + G::kWaveM * wm;  // the wave's first column
   with_edge(r0 + G::kTile > a.N || c0 + G::kTile > a.f, [&](auto edge) {
     constexpr bool E = decltype(edge)::value;
@@ -484,8 +483,8 @@ __global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void gate_up_ag
     const int wm = wave % G::kWavesM, wn = wave / G::kWavesM, r16 = lane & 15, kq = lane >> 4;
     typename G::Acc acc;
     __syncthreads();  // the last tile's fragments have been read
-    product<G, PARTS, false, false, true>(rows_of(a.w_out, min(c0, a.f - 1), 0),
-                                         rows_of(a.dy, min(r0, a.N - 1), 0), steps, smem, acc);
+    product<G, PARTS, false, false, true>(rows_of(a.w_out, min(c0, a.f - 1), 0), rows_of(a.dy, r0, 0),
+                                         steps, smem, acc);
 #pragma unroll
     for (int mb = 0; mb < G::kMB; ++mb)
 #pragma unroll
@@ -500,7 +499,7 @@ __global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void gate_up_ag
       w.half = a.fq;
       w.apart = true;
       __syncthreads();
-      product<G, PARTS, true, false, true>(w, rows_of(a.x, min(r0, a.N - 1), 0), steps, smem, acc);
+      product<G, PARTS, true, false, true>(w, rows_of(a.x, r0, 0), steps, smem, acc);
       const int cw = ch + G::kWaveM * wm;  // the wave's first column of this half
       with_edge(r0 + G::kTile > a.N || c0 + G::kTile > a.f, [&](auto edge) {
         constexpr bool E = decltype(edge)::value;
@@ -940,7 +939,10 @@ Plan plan_gated(const Call& c, const Needs& w) {
   p.fq = round_up(c.f, 8);
   p.ldz = round_up(2 * p.fq, kStepK);
   p.fp = round_up(c.f, kBlock8);
-  p.np = round_up(c.N, kPad);
+  // (no more: a tile of rows that do not exist takes as long as any; 1 row x 2048 x 8192, dX
+  // with G and U computed again: 84 us with rows padded to 256, 75 so; 64 rows: 81 and 78)
+  p.np = round_up(c.N, kStepK);
+  static_assert(TinyTile::kTile % kStepK == 0, "every tile has a row of the block");
   const int parts = static_cast<int>(p.parts), later = c.dtype == DPG_BF16 && c.N <= kTwoRows ? kTwo : parts;
   size_t off = 0;
   auto take = [&](int64_t elems, int64_t size) {
@@ -1192,8 +1194,7 @@ int run_backward(const Call& c, const Plan& p, const void* X, const int8_t* x_co
   const bool own_z = p.whole && g.dZ && p.ldz == 2 * c.f, own_h = p.whole && g.H && p.ldh == c.f;
   bf16* const dz = own_z ? static_cast<bf16*>(g.dZ) : reinterpret_cast<bf16*>(ws + p.off_dz);
   bf16* const h = own_h ? static_cast<bf16*>(g.H) : reinterpret_cast<bf16*>(ws + p.off_h);
-  // (rows past N are written only where both have them)
-  a.np = static_cast<int32_t>(own_z || own_h ? c.N : p.np);
+  a.np = static_cast<int32_t>(p.np);
   a.dz = {dz, p.ldz, p.np * p.ldz, a.np, static_cast<int32_t>(p.ldz)};
   a.h = {h, p.ldh, p.np * p.ldh, a.np, static_cast<int32_t>(p.ldh)};
   a.codes = const_cast<int8_t*>(z_codes), a.exps = const_cast<uint8_t*>(z_exps);

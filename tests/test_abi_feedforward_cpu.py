@@ -98,6 +98,18 @@ def test_workspace_holds_copies_only_where_they_are_needed(lib):
     assert size("dpg_gated_grad_workspace_size", *args, 1, 1) >= made + operands
 
 
+@pytest.mark.parametrize("N", [128, 192, 320])
+def test_rows_are_padded_to_whole_steps_alone(lib, N):
+    """dZ and H of the workspace, which the caller's own take the place of: tiles of rows
+    beyond them would be computed like any other."""
+    d, f, need = 64, 8192, []
+    for layers in (0, 1):
+        n = ctypes.c_size_t(0)
+        assert lib.dpg_gated_grad_workspace_size(N, d, f, 1, 1, 0, layers, 0, ctypes.byref(n)) == 0
+        need.append(n.value)
+    assert need[0] - need[1] == 2 * N * 3 * f
+
+
 def test_projections_computed_again_take_a_bounded_workspace(lib):
     """G and U in fp32 would be 2^20 x 2 x 4096 x 4 bytes, 34 GB, at once."""
     a, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
