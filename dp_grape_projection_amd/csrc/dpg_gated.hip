@@ -995,7 +995,9 @@ Plan plan_gated(const Call& c, const Needs& w) {
       p.wo = choose(c.d, c.f, ceil_div(c.N, kStepK), later, kBothTransposed);
       p.off_acc_wi = take(static_cast<int64_t>(acc_bytes(p.wi, 2, c.f, c.d)), 1);
       p.off_acc_wo = take(static_cast<int64_t>(acc_bytes(p.wo, 1, c.d, c.f)), 1);
-      p.off_x8 = take(c.N * p.ldx, c.dtype == DPG_BF16 ? 2 : 4);
+      // X read back from 8 bits, whether the call has it so or as it is (a size is asked for
+      // without X); never where G and U are computed again, from X as it is
+      p.off_x8 = take(w.again ? 0 : c.N * p.ldx, c.dtype == DPG_BF16 ? 2 : 4);
     }
   }
   p.total = off;

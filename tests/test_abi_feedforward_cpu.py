@@ -110,6 +110,19 @@ def test_rows_are_padded_to_whole_steps_alone(lib, N):
     assert need[0] - need[1] == 2 * N * 3 * f
 
 
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_no_room_for_8_bits_of_what_cannot_be_in_8_bits(lib, dtype):
+    """Projections computed again need X as it is: nothing of it is read back, and with
+    tiles enough not to split a sum the weights' gradients need no workspace."""
+    need = []
+    for weights in (0, 1):
+        n = ctypes.c_size_t(0)
+        assert lib.dpg_gated_grad_workspace_size(16384, 4096, 11008, dtype, 0, weights, 0, 0,
+                                                 ctypes.byref(n)) == 0
+        need.append(n.value)
+    assert need[0] == need[1]
+
+
 def test_projections_computed_again_take_a_bounded_workspace(lib):
     """G and U in fp32 would be 2^20 x 2 x 4096 x 4 bytes, 34 GB, at once."""
     a, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
