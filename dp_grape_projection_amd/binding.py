@@ -913,8 +913,9 @@ def _rows_of(t: torch.Tensor) -> int:
 def dpg_pack_act(X: torch.Tensor, out: Optional[PackedActivations] = None,
                  stream=None) -> PackedActivations:
     """X [..., d] (bf16 or fp32) in 8 bits (libdpg): blocks of 32 channels share a power
-    of two, a value is off by at most 2^-7 of its block's largest. A block with an
-    infinity or NaN reads as NaN. out: an earlier result of the same shape to overwrite."""
+    of two, a value is off by at most 2^-7 of its block's largest, or by 2^-127 where that is
+    more. A block with an infinity or NaN reads as NaN. out: an earlier result of the same
+    shape to overwrite."""
     lib = load_library()
     _require(X, "X")
     if X.dim() < 1:

@@ -5,8 +5,9 @@
 // even, and b as one byte; it stands for q 2^(b - 133). The largest magnitude lies in
 // [64, 128) steps, so a value is off by at most half a step, 2^-7 of the block's
 // largest (fp32 values in a block's last half step by up to one). b >= 7 keeps both
-// factors normal numbers; a block with an infinity or NaN gets b = 255 and reads as
-// NaN. Every value q 2^(b - 133) is a bf16 number: reading it back, or feeding it to
+// factors normal numbers, at steps of 2^-126: a block whose largest is below 2^-120 is
+// off by up to 2^-127, whatever part of it that is. A block with an infinity or NaN gets
+// b = 255 and reads as NaN. Every value q 2^(b - 133) is a bf16 number: reading it back, or feeding it to
 // the bf16 matrix instructions, rounds nothing.
 #pragma once
 

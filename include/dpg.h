@@ -463,8 +463,9 @@ int dpg_distill_loss_grad(const void* X, const void* E, const int64_t* top_ids,
  *     q = clamp(round(x 2^(133 - b)), -127, 127)      (ties to even)
  * and stands for q 2^(b - 133): off by at most half a step, which is at most 2^-7 of the
  * block's largest magnitude (fp32 values above 127 steps by up to one step, less than
- * 2^-7 of themselves). A block with an infinity or NaN gets b = 255 and reads as NaN.
- * What a code stands for is exact in bf16 as in fp32.
+ * 2^-7 of themselves), or 2^-127 where that magnitude is below 2^-120. A block with an
+ * infinity or NaN gets b = 255 and reads as NaN. What a code stands for is exact in bf16
+ * as in fp32.
  *   codes  device [N][32 ceil(d / 32)] int8, zero from d on
  *   exps   device [N][ceil(d / 32)] uint8, the b of every block
  * dtype is X's type. Limits: N in [1, 2^30], d in [1, 2^20]. No workspace.

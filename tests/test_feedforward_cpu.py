@@ -1,10 +1,12 @@
 """What the gated block's torch function does around the library's calls, with those
 calls replaced by elementary torch on the CPU."""
+import numpy as np
 import pytest
 import torch
 
 import dp_grape_projection_amd as dpg
 from dp_grape_projection_amd import feedforward as ff
+from oracle import feedforward as of
 
 
 @pytest.fixture
@@ -85,3 +87,16 @@ def test_function_transforms_are_refused(calls):
         torch.func.jvp(dpg.gated_feed_forward, tuple(args), tuple(tangents))
     with pytest.raises((NotImplementedError, RuntimeError)):
         torch.func.grad(lambda x: dpg.gated_feed_forward(x, *args[1:]).sum())(args[0])
+
+
+def test_how_far_8_bits_are_off():
+    """By 2^-7 of a block's largest magnitude or by 2^-127, whichever is more; either bound
+    is met within a few percent, the second where the first would promise more."""
+    r = np.random.default_rng(2)
+    x = (r.uniform(-1, 1, (4000, 32)) * 2.0 ** r.integers(-140, 120, (4000, 1))).astype(np.float32)
+    off = np.abs(of.unpack8(*of.pack8(x), 32) - x.astype(np.float64)).max(1)
+    top = np.abs(x.astype(np.float64)).max(1)
+    assert (off <= np.maximum(2.0 ** -7 * top, 2.0 ** -127)).all()
+    large, small = top >= 2.0 ** -120, (top > 2.0 ** -127) & (top < 2.0 ** -121)
+    assert (off[large] / top[large]).max() > 0.95 * 2.0 ** -7
+    assert (off[small] / top[small]).max() > 2.0 ** -2 and off[small].max() > 0.95 * 2.0 ** -127

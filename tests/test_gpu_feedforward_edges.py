@@ -28,3 +28,35 @@ def test_projections_of_another_type_are_not_overwritten():
     assert torch.equal(Z.codes, codes)
     _, again = dpg.dpg_gated(X, W_in, W_out, keep=True, Z=Z)
     assert again is Z and torch.equal(Z.codes, codes)
+
+
+def test_projection_of_more_rows_than_the_16_bit_products_index():
+    """fp32, 107 million tokens: A is read back and taken as dpg_project_layer takes it.
+    Every sample against the formula; products and sums in fp32, the step's fp32 bar."""
+    import torch
+    import oracle
+    import dp_grape_projection_amd as dpg
+    from _helpers import TOL, rel_err
+    if torch.cuda.get_device_properties(0).total_memory < 100 << 30:
+        pytest.skip("needs 100 GiB")
+    B, T, d = 105000, 1024, 8
+    assert B * T * (d // 8 + 9) >= 1 << 30     # (below, the other path)
+    print(f"[edges] {B} x {T} x {d}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    codes = torch.randint(-127, 128, (B, T, 32), generator=g, device="cuda", dtype=torch.int8)
+    exps = torch.randint(125, 129, (B, T, 1), generator=g, device="cuda", dtype=torch.uint8)
+    dY = torch.randn(B, T, 1, generator=g, device="cuda") / T ** 0.5
+    p = dpg.PackedActivations(codes, exps, d, torch.float32)
+    n = torch.ones(B, device="cuda")
+    G = dpg.dpg_project_layer_packed(p, dY, 1, 8, 2, 3, n)
+    P = torch.from_numpy(oracle.projection_matrix(8, 3, 2, 1, d)).cuda()[0]
+    want = torch.empty(B, dtype=torch.float64, device="cuda")
+    scale = torch.empty_like(want)
+    for i in range(0, B, 5000):
+        s = slice(i, i + 5000)
+        A = codes[s, :, :d].double() * torch.exp2(exps[s].double() - 133)
+        terms = (A @ P) * dY[s, :, 0].double()
+        want[s], scale[s] = terms.sum(1), terms.square().sum(1).sqrt()
+    # (a sample's one sum may cancel: its error is that of its terms)
+    assert float(((G[:, 0, 0].double() - want).abs() / scale).max()) <= TOL["fp32"]
+    assert rel_err(n.double().cpu().numpy(), (1 + want.square()).cpu().numpy()) <= TOL["fp32"]
