@@ -461,7 +461,9 @@ __global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void gate_up_gr
 // them write and read 16 bytes for every element of dH (16384 x 768 x 2048: 274 us so, 213
 // in one; 16384 x 4096 x 11008: 4.15 and 3.59 ms). What bounds it is the products, at 1230
 // TFLOP/s of the 1250 to 1340 that a large one of the library reaches, and for short K the
-// epilogues between them, which nothing overlaps in a block that has all of LDS.
+// epilogues between them, which nothing overlaps in a block that has all of LDS. In tiles of
+// 256 x 256 it spills 54 to 70 registers (220 to 284 bytes a thread), stored and loaded in
+// the epilogues and between the products, none of it in a K loop.
 template <class G, int PARTS, int ACT>
 __global__ __launch_bounds__(G::kThreads, (kBlocksOf<G, PARTS>)) void gate_up_again_kernel(const GatedArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[kLdsOf<G, PARTS>];
@@ -833,7 +835,7 @@ int32_t resident(Tile t, int parts) {
 // Tiles and splits of a product of m x n outputs over `steps` K steps, of operands in
 // `parts`; of G and U together, whose tiles have half their width of columns of either
 // and which needs all of K, as dH does (kWhole) and the three products of kAgain.
-// Modelled on 300 measurements: with c blocks on a CU, a K step takes 1.05 + 0.5 c us in a
+// Modelled on 400 measurements: with c blocks on a CU, a K step takes 1.05 + 0.5 c us in a
 // big tile, 0.5 max(1, c) in a small one, 0.34 + 0.13 (c - 1) in a tiny one, a fifth more
 // where both operands are read transposed; in three parts 2.5 us in a small tile, 1.05 max(1,
 // c) in a tiny one; outputs and partial sums are written at 5.6 TB/s, and adding those up is a launch of 2.5 us and 6.5 TB/s.
@@ -894,11 +896,14 @@ int check_call(const Call& c) {
   return DPG_OK;
 }
 
-// With few rows of bf16, H and dZ stay in two parts: the products they enter cost twice
-// as much, but an output of few values, whose two roundings do not average out, then has
-// one (64 rows x 2048 x 8192: forward 41 us, 34 with one part, backward 128 and 108; 32 x
-// 768 x 2048: 16 and 17, 35 and 30; errors over those of one rounding, 47 outputs of 1 to 64
-// rows: all 1.00, with one part 1.41 in the middle and up to 1.47).
+// bf16: H and dZ are rounded once where they enter their products, which with the rounding
+// of the output makes its error 1.41 times that of one rounding, at any size (Y of 17 to 8192
+// rows). In two parts it is 1.00 times, for products that cost twice as much. Up to a row of
+// tiles of 64 the weights' bytes hide a part of that and the two parts are kept: 64 rows x
+// 2048 x 8192: forward 40.4 us, 33.3 with one part, gradients 83 and 68; 32 x 768 x 2048: 16
+// and 16, 26 and 23. Beyond they are not: 128 rows x 2048 x 8192: 43 and 37, 103 and 75; 256:
+// 54 and 43, 129 and 91. A row's result so depends, by that rounding, on whether the call has
+// more than 64 rows.
 constexpr int64_t kTwoRows = 64;
 
 // Where everything lies in the workspace. Copies of the operands are planned whatever
@@ -1008,7 +1013,6 @@ Plan plan_gated(const Call& c, const Needs& w) {
 // bytes at a time and K needs no padding, else copies in the workspace.
 struct Operands {
   PackArgs pack{};
-  const Plan& p;
   char* ws;
   bool bf16_in;
 
@@ -1116,7 +1120,7 @@ int run_forward(const Call& c, const Plan& p, const void* X, const void* W_in, c
                 void* Y, int8_t* codes, uint8_t* exps, char* ws, hipStream_t s) {
   constexpr bool kHalf = sizeof(T) == 2;
   GatedArgs a = make_args(c, p);
-  Operands o{{}, p, ws, kHalf};
+  Operands o{{}, ws, kHalf};
   a.x = o.bring(X, c.N, c.d, 1, 0, p.ldx, p.off_x, kHalf && c.d % kStepK == 0 && aligned(X, 16));
   a.w_in = o.bring(W_in, c.d, c.f, 2, p.fq, p.ldz, p.off_wi, kHalf && c.f % 8 == 0 && aligned(W_in, 16));
   a.w_out = o.bring(W_out, c.f, c.d, 1, 0, p.ldx, p.off_wo, kHalf && c.d % 8 == 0 && aligned(W_out, 16));
@@ -1175,7 +1179,7 @@ int run_backward(const Call& c, const Plan& p, const void* X, const int8_t* x_co
                  const uint8_t* z_exps, const void* dY, const Grads& g, char* ws, hipStream_t s) {
   constexpr bool kHalf = sizeof(T) == 2;
   GatedArgs a = make_args(c, p);
-  Operands o{{}, p, ws, kHalf};
+  Operands o{{}, ws, kHalf};
   const bool again = !z_codes;
   if (x_codes && g.dW_in) {
     if (launch_unpack8(x_codes, x_exps, c.N, c.d, ws + p.off_x8, kHalf, p.ldx, s) != hipSuccess)

@@ -506,9 +506,9 @@ typedef enum {
  * unless their 8-bit form is asked for (both or neither of z_codes and z_exps), for
  * dpg_gated_grad: rows (n, half) of f channels, as dpg_pack_act writes them,
  *   z_codes  device out [N][2][32 ceil(f / 32)],  z_exps  [N][2][ceil(f / 32)].
- * Products run on 16-bit operands and accumulate in fp32: with bf16, H is rounded once
- * (to 16 bits for up to 64 rows, whose few outputs would not average the rounding out);
- * with fp32, operands are split exactly into three bf16 parts, so that products keep
+ * Products run on 16-bit operands and accumulate in fp32: with bf16, H is rounded once to
+ * bf16, or up to 64 rows, where that costs little, to 16 bits (a row's result differs by
+ * that rounding between a call of 64 rows and one of more); with fp32, operands are split exactly into three bf16 parts, so that products keep
  * fp32's accuracy. G and U are never rounded before the activation. An infinity in an
  * operand can make NaN of all that it meets. Results do not vary from run to run.
  *   workspace  dpg_gated_workspace_size(...) bytes, 256-byte aligned; unaligned: X, W_in
@@ -532,8 +532,8 @@ int dpg_gated(const void* X, const void* W_in, const void* W_out, int64_t N, int
  *             computed again from X, without a rounding
  *   X         [N][d], for dW_in and for computing G and U again; or, for dW_in,
  *             x_codes and x_exps, its form of dpg_pack_act (then X is NULL)
- * With bf16, dZ and H are rounded once, before the products that they enter (up to 64
- * rows: to 16 bits); dH is not.
+ * With bf16, dZ and H are rounded once to bf16 before the products that they enter (up to
+ * 64 rows: to 16 bits); dH is not.
  *   workspace  dpg_gated_grad_workspace_size(...) bytes, 256-byte aligned; have_z:
  *              z_codes is given, weights: dW_in or dW_out is asked for, layers: dZ and H
  *              are, unaligned: X, W_in, W_out, dY, dZ or H does not start on 16 bytes
