@@ -763,7 +763,7 @@ inline bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintpt
 inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
 inline int check_ws(const void* ws, size_t have, size_t need) {
-  if (!ws) return fail(DPG_ERR_WORKSPACE, "workspace is NULL");
+  if (need > 0 && !ws) return fail(DPG_ERR_WORKSPACE, "workspace is NULL");
   if (!aligned(ws, 256)) return fail(DPG_ERR_WORKSPACE, "workspace must be 256-byte aligned");
   if (have < need)
     return fail(DPG_ERR_WORKSPACE, "workspace of " + std::to_string(have) + " bytes, " +

@@ -60,3 +60,28 @@ def test_projection_of_more_rows_than_the_16_bit_products_index():
     # (a sample's one sum may cancel: its error is that of its terms)
     assert float(((G[:, 0, 0].double() - want).abs() / scale).max()) <= TOL["fp32"]
     assert rel_err(n.double().cpu().numpy(), (1 + want.square()).cpu().numpy()) <= TOL["fp32"]
+
+
+def test_a_gradient_that_needs_no_workspace_takes_none():
+    """dZ, H and dX where no operand is copied and no sum is split: the query says 0 bytes,
+    and the call takes a null pointer for them."""
+    import ctypes
+    import torch
+    import dp_grape_projection_amd as dpg
+    from dp_grape_projection_amd import binding as b
+    N, d, f = 16384, 64, 512
+    X, W_in, W_out, dY = (torch.randn(s, device="cuda").bfloat16()
+                          for s in ((N, d), (d, 2 * f), (f, d), (N, d)))
+    assert b._gated_grad_workspace_size(N, d, f, b.DPG_BF16, 1, 0, 1) == 0
+    _, Z = dpg.dpg_gated(X, W_in, W_out, keep=True)
+    want = dpg.dpg_gated_grad(dY, None, W_in, W_out, Z=Z, need_dW=False, need_layers=True)
+    dX, dZ, H = (torch.full_like(t, float("nan")) for t in (want.dX, want.dZ, want.H))
+    lib = dpg.load_library()
+    status = lib.dpg_gated_grad(
+        None, None, None, W_in.data_ptr(), W_out.data_ptr(), Z.codes.data_ptr(),
+        Z.exps.data_ptr(), dY.data_ptr(), N, d, f, b.DPG_BF16, 0, dX.data_ptr(), None, None,
+        dZ.data_ptr(), H.data_ptr(), None, 0, torch.cuda.current_stream().cuda_stream)
+    assert status == b.DPG_OK, lib.dpg_last_error()
+    torch.cuda.synchronize()
+    for got, ref in zip((dX, dZ, H), (want.dX, want.dZ, want.H)):
+        assert torch.equal(got, ref)
