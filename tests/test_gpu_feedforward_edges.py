@@ -85,3 +85,58 @@ def test_a_gradient_that_needs_no_workspace_takes_none():
     torch.cuda.synchronize()
     for got, ref in zip((dX, dZ, H), (want.dX, want.dZ, want.H)):
         assert torch.equal(got, ref)
+
+
+def _products(a, b, rows=1 << 18):
+    """a^T b in 64 bits, by pieces of their rows."""
+    import torch
+    out = torch.zeros(a.shape[1], b.shape[1], dtype=torch.float64, device="cuda")
+    for i in range(0, a.shape[0], rows):
+        out += a[i:i + rows].double().t().contiguous() @ b[i:i + rows].double()
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("N,d,f", [(1 << 22, 64, 40), (20, 1 << 16, 64), (20, 64, 1 << 16),
+                                   (3, 1 << 16, 96), (3, 96, 1 << 16)])
+def test_block_at_its_limits(N, d, f, dtype):
+    """The most rows, and the widest rows. bf16: two roundings of 2^-8 at most, independent, at
+    most 0.82 of 2^-8 in the mean square. fp32: the fp32 bar, or what K terms of random
+    signs summed one after the other may lose: six additions for every 32 of them, each off
+    by one last place, 2^-23, of a partial sum, which is 2 / 3 sqrt(K) terms in the mean where
+    the whole is sqrt(K): K / 8 2^-23. In S parts, should all be off the same way, each part's
+    K / S terms lose (K / 8 S) 2^-23 sqrt(K / S), S of them together K / 8 2^-23 / sqrt(S) of
+    the whole; the 2^22 rows are summed in 200 parts and more."""
+    import torch
+    import dp_grape_projection_amd as dpg
+    dt = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
+    parts = 200 if N > 1 << 20 else 1
+    bar = {"bf16": 2.0 ** -8, "fp32": max(1e-5, max(N, d, f) / 8 * 2.0 ** -23 / parts ** 0.5)}[dtype]
+    print(f"[edges] block {N} x {d} x {f} {dtype}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    X, W_in, W_out, dY = (torch.randn(s, generator=g, device="cuda").div_(n ** 0.5).to(dt)
+                          for s, n in (((N, d), 1), ((d, 2 * f), d), ((f, d), f), ((N, d), d)))
+    Y, none = dpg.dpg_gated(X, W_in, W_out)
+    out = dpg.dpg_gated_grad(dY, X, W_in, W_out, need_layers=True)
+    wi, wo = W_in.double(), W_out.double()
+    worst = {}
+
+    def check(name, got, want):
+        off = float((got.double() - want).norm() / want.norm())
+        worst[name] = max(worst.get(name, 0.0), off)
+
+    H, dZ = torch.empty(N, f, device="cuda"), torch.empty(N, 2 * f, device="cuda")
+    for i in range(0, N, 1 << 18):
+        r = slice(i, i + (1 << 18))
+        G, U = (X[r].double() @ wi).chunk(2, 1)
+        s = torch.sigmoid(G)
+        h, dh = G * s * U, dY[r].double() @ wo.t().contiguous()
+        dz = torch.cat([dh * U * s * (1 + G * (1 - s)), dh * G * s], 1)
+        check("Y", Y[r], h @ wo)
+        check("H", out.H[r], h)
+        check("dZ", out.dZ[r], dz)
+        check("dX", out.dX[r], dz @ wi.t().contiguous())
+        H[r], dZ[r] = h.float(), dz.float()
+    check("dW_in", out.dW_in, _products(X, dZ))
+    check("dW_out", out.dW_out, _products(H, dY))
+    assert max(worst.values()) <= bar, worst
