@@ -59,7 +59,7 @@ struct GatedArgs {
   uint8_t* exps;        // [N][2][fp / 32]
   bool two;             // bf16: h and dz in two parts
   f32x4* scratch;       // a tile of dH for every resident block, where Z is computed again
-  void* dz_out;         // [N][2f] the caller's dZ where h and dz are not his own
+  void* dz_out;         // [N][2f] the caller's dZ where dz is in the workspace, h_out likewise
   void* h_out;          // [N][f]
 };
 

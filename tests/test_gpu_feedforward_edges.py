@@ -140,3 +140,42 @@ def test_block_at_its_limits(N, d, f, dtype):
     check("dW_in", out.dW_in, _products(X, dZ))
     check("dW_out", out.dW_out, _products(H, dY))
     assert max(worst.values()) <= bar, worst
+
+
+@pytest.mark.parametrize("checkpoint", [None, "int8"])
+def test_autograd_on_another_stream_and_captured(checkpoint):
+    """Forward and backward pass of the torch function on a stream of their own, and in a
+    graph that is replayed on new data between eager work. (Captured while no eager graph
+    of the same leaves lives, as torch needs it.)"""
+    import torch
+    import dp_grape_projection_amd as dpg
+    g = torch.Generator(device="cuda").manual_seed(12)
+    X, W_in, W_out, dY = (torch.randn(s, generator=g, device="cuda").div_(8).bfloat16()
+                          for s in ((5, 20, 64), (64, 192), (96, 64), (5, 20, 64)))
+    leaves = [t.requires_grad_() for t in (X, W_in, W_out)]
+
+    def step():
+        Y = dpg.gated_feed_forward(*leaves, act="gelu", checkpoint=checkpoint)
+        return [Y.detach(), *torch.autograd.grad(Y, leaves, dY)]
+
+    want = step()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        other = step()
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(other, want))
+    del other
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        out = step()
+    data = torch.randn(3, *X.shape, generator=g, device="cuda").bfloat16()
+    for k in (0, 1, 2, 0):
+        with torch.no_grad():
+            X.copy_(data[k])
+        for t in out:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, step()):
+            assert torch.equal(a, b), k
